@@ -366,10 +366,141 @@ kvq_status kv_attn_prefill(kvq_format fmt, const kvq_mla_layout* layout,
                            uint8_t* codes, float* scales, float sm_scale, float* out,
                            void* workspace, size_t workspace_bytes, kvq_path path, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Paged pools: pages, the append with rotary positions, attention          */
+/* ------------------------------------------------------------------------ */
+
+/* A paged pool is a row pool (codes, scales as above) cut into n_pages pages of
+ * page_rows rows; row `slot` of the pool lies in page slot / page_rows.  The
+ * rows of a sequence lie in the pages that its row of the block table lists:
+ * row t in page block_table[s][t / page_rows] at place t % page_rows.  A step of
+ * a serving loop is
+ *   kv_pages_reserve   pages, slots and positions for the step's new rows
+ *   kv_rope_append     queries rotated; new rows rotated, quantized, stored
+ *   kv_attn_paged      every new token over its sequence's rows
+ * (and kv_pages_trim for rows that are given back: a finished request, rejected
+ * speculative tokens), all on the device: no length is read back, so a step can
+ * be captured into a CUDA graph and replayed.
+ *
+ * page_rows is a power of two (pages: 1 .. 65536, attention: 16 .. 65536), and
+ * n_pages * page_rows at most 2^31 - 1.  Rows are of the formats KVQ_KV8 and
+ * KVQ_TQ4.  block_table is int32 [n_seq][table_stride].  Sequences appear once
+ * in a batch. */
+
+/* Bytes of workspace kv_pages_reserve and kv_pages_trim need: the error word
+ * and a counter, zero before the first call (each call leaves it so). */
+size_t kv_pages_workspace_size(void);
+
+/* Takes pages for new_lens[s] new rows of every sequence from the top of a
+ * stack of free pages (free_pages[n_free - 1] first), in sequence order, and
+ * works out where the rows go.
+ *   kv_lens      [n_seq] int64: rows each sequence holds
+ *   new_lens     [n_seq] int64: rows to add (0 allowed)
+ *   block_table  the entries of the new pages are written, the others kept
+ *   free_pages   int32 [n_pages], n_free int32 [1]: the stack; n_free is lowered
+ *   lens_out     [n_seq] int64: kv_lens + new_lens (may be kv_lens itself)
+ *   cu_new       [n_seq + 1] int64: offsets of each sequence's new rows
+ *   slot_map     [max_new] int64: pool row of each new row, in sequence order;
+ *                -1 past the batch's rows
+ *   positions    NULL, or [max_new] int64: each new row's index in its
+ *                sequence; 0 past the batch's rows
+ * All or nothing: with too few free pages (device word KVQ_ERR_WORKSPACE), or
+ * a negative length, a row of the table too short, more than max_new rows or a
+ * free count outside [0, n_pages] (KVQ_ERR_ARG), no page is taken: cu_new is 0,
+ * slot_map -1 and lens_out = kv_lens, so that the calls after it do nothing.
+ * A listed page outside [0, n_pages) gives slot -1 and KVQ_ERR_ARG.  n_seq up
+ * to 65535.  kv_lens, new_lens and lens_out may not overlap otherwise. */
+kvq_status kv_pages_reserve(int32_t n_seq, int32_t page_rows, const int64_t* kv_lens, const int64_t* new_lens,
+                            int32_t* block_table, int32_t table_stride, int32_t* free_pages, int32_t* n_free,
+                            int32_t n_pages, int64_t* lens_out, int64_t* cu_new, int64_t* slot_map,
+                            int64_t* positions, int64_t max_new, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* Cuts every sequence back to keep_lens[s] rows (a negative or larger value
+ * keeps it; 0 ends it) and puts the pages that hold none of its rows any more
+ * back on the stack, in the order that undoes a reservation.
+ *   kv_lens      [n_seq] int64, updated
+ *   keep_lens    [n_seq] int64 (not kv_lens itself)
+ * Block-table entries are left as they are.  More pages than the stack has
+ * room for, or an invalid length, changes nothing and sets KVQ_ERR_ARG. */
+kvq_status kv_pages_trim(int32_t n_seq, int32_t page_rows, int64_t* kv_lens, const int64_t* keep_lens,
+                         int32_t* block_table, int32_t table_stride, int32_t* free_pages, int32_t* n_free,
+                         int32_t n_pages, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Rotary positions of the last `dim` dims of a row (dim even, 2 .. 128).  Pair i
+ * (dims i and i + dim/2, or 2i and 2i + 1 if `adjacent`) turns by
+ * positions[axis[i]][token] * inv_freq[i]: one axis for text, several (time,
+ * height, width) for images and video, in whatever assignment of pairs to axes
+ * (consecutive sections, interleaved) and with whatever frequency scaling the
+ * model uses.  Angles are right to f32 for positions up to 2^28 in size. */
+typedef struct kvq_rope {
+    int32_t dim;
+    int32_t n_axes;          /* 1 .. 4 */
+    int32_t adjacent;
+    uint8_t axis[64];
+    double inv_freq[64];     /* finite, radians per position */
+} kvq_rope;
+
+/* One step's producer over a paged pool, one launch: rotates the queries'
+ * rotary dims, and rotates the new rows' last dims, encodes the rows exactly as
+ * kv8_encode / tq4_encode would the rotated f32 rows and stores them in their
+ * slots.  Products and the one sum of a rotation are rounded to f32 each; a
+ * bf16 result is rounded once more.
+ *   x_new        [n][D] f32 or bf16, row stride x_stride elements; NULL: no rows
+ *   positions    [n_axes][n] int64, axis stride pos_stride
+ *   slot_map     [n] int64: pool row of row i; a negative one is skipped (a
+ *                padded row), one past pool_rows is skipped and sets KVQ_ERR_ARG
+ *   q_in         the queries' rotary dims [n][n_heads][dim], f32 or bf16, strides
+ *                q_in_token and q_in_head (elements)
+ *   q_out        where they go, same type, strides q_out_token and q_out_head;
+ *                q_in itself (same strides) rotates in place.  n_heads = 0: none
+ *   codes, scales  the pool [pool_rows][*], rows slot_map[i] written
+ *   err_word     NULL, or a device int32 error word (KVQ_ERR_NONFINITE for a row
+ *                with a NaN or an infinity, as the encoders)
+ * Any alignment of element size; 16-byte aligned queries with strides and dims
+ * of whole 16 bytes move fastest.  D up to 1024.  The same slot twice leaves one of
+ * the rows' bytes or a mixture. */
+kvq_status kv_rope_append(kvq_format fmt, const kvq_mla_layout* layout, const kvq_rope* rope,
+                          const void* x_new, kvq_dtype x_dtype, int64_t x_stride, int64_t n,
+                          const int64_t* positions, int64_t pos_stride, const int64_t* slot_map,
+                          const void* q_in, kvq_dtype q_dtype, int64_t q_in_token, int64_t q_in_head,
+                          void* q_out, int64_t q_out_token, int64_t q_out_head, int32_t n_heads,
+                          uint8_t* codes, float* scales, int64_t pool_rows, int32_t* err_word, void* stream);
+
+/* Bytes of workspace kv_attn_paged needs: one size for every length, page size
+ * and batch (two partial tiles per SM).  0 for invalid or unsupported
+ * arguments. */
+size_t kv_attn_paged_workspace_size(kvq_format fmt, const kvq_mla_layout* layout, kvq_dtype q_dtype, int32_t n_seq,
+                                    int32_t n_heads, int64_t n_tokens, kvq_path path);
+
+/* Causal attention of new tokens over paged quantized rows, the rows of the new
+ * tokens included: a decode step (one token a sequence), a prompt's chunk, a
+ * window of speculative tokens, or any mixture of them.  Token i of sequence b
+ * (i < n = cu_q[b+1] - cu_q[b]) attends rows [0, kv_lens[b] - n + i]:
+ *   z_t = sm_scale * (q . x_hat_t),  out = sum_t softmax(z)_t x_hat_t[0:v_dim]
+ * A token that sees no row (kv_lens[b] < n) yields zeros.
+ *   q            [n_tokens][n_heads][576] in q_dtype, any n_heads
+ *   cu_q         [n_seq + 1] int64, non-decreasing, cu_q[n_seq] <= n_tokens; the
+ *                rows of out behind cu_q[n_seq] are left as they are
+ *   codes, scales  the pool, [n_pages * page_rows] rows
+ *   kv_lens      [n_seq] int64: rows of each sequence, at most
+ *                table_stride * page_rows
+ *   out          [n_tokens][n_heads][512] in q_dtype
+ * Layouts as kv_attn_decode.  Runs in f32 (KVQ_PATH_SIMT, and AUTO), within 1e-5
+ * before the rounding to q_dtype.  Invalid lengths or offsets and pages outside
+ * [0, n_pages) set KVQ_ERR_ARG in the workspace's device word; nothing outside
+ * the pool is read. */
+kvq_status kv_attn_paged(kvq_format fmt, const kvq_mla_layout* layout, const void* q, kvq_dtype q_dtype,
+                         int64_t n_tokens, int32_t n_heads, int32_t n_seq, const int64_t* cu_q,
+                         const uint8_t* codes, const float* scales, const int32_t* block_table,
+                         int32_t table_stride, const int64_t* kv_lens, int32_t page_rows, int32_t n_pages,
+                         float sm_scale, void* out, void* workspace, size_t workspace_bytes, kvq_path path,
+                         void* stream);
+
 /* Opt-in launch timing, for kernel-level rooflines (instrumentation, not part
  * of the pages' method).  With capacity > 0, every kv_attn_decode,
- * kv_attn_decode_append, kv_attn_decode_gather, kv_attn_prefill and
- * kv_attn_decode_k2v4 call records three CUDA events on its stream -- before
+ * kv_attn_decode_append, kv_attn_decode_gather, kv_attn_prefill, kv_attn_paged
+ * and kv_attn_decode_k2v4 call records three CUDA events on its stream -- before
  * its partial kernel, before its merge, after its merge -- into the next of
  * `capacity` slots (a ring: older calls are overwritten); capacity 0 turns it
  * off and frees the events.  The record between the two kernels ends the

@@ -426,6 +426,135 @@ kvq_status kv_attn_prefill(kvq_format fmt, const kvq_mla_layout* layout, const f
                                         n_past, pl, sm_scale, out, workspace, st));
 }
 
+// Pages of a paged pool: a power of two of rows, row indices within int32.
+static kvq_status check_pages(int32_t n_seq, int32_t page_rows, int32_t table_stride, int32_t n_pages, int32_t least) {
+    if (n_seq < 0 || page_rows <= 0 || table_stride < 0 || n_pages < 0) return KVQ_ERR_ARG;
+    if (page_rows & (page_rows - 1)) return KVQ_ERR_UNSUPPORTED;
+    if (n_seq > 65535 || page_rows < least || page_rows > 65536) return KVQ_ERR_UNSUPPORTED;
+    if ((int64_t)n_pages * page_rows > 0x7fffffff) return KVQ_ERR_UNSUPPORTED;
+    return KVQ_OK;
+}
+
+size_t kv_pages_workspace_size(void) { return kWsHeader; }
+
+kvq_status kv_pages_reserve(int32_t n_seq, int32_t page_rows, const int64_t* kv_lens, const int64_t* new_lens,
+                            int32_t* block_table, int32_t table_stride, int32_t* free_pages, int32_t* n_free,
+                            int32_t n_pages, int64_t* lens_out, int64_t* cu_new, int64_t* slot_map,
+                            int64_t* positions, int64_t max_new, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+    kvq_status s = check_pages(n_seq, page_rows, table_stride, n_pages, 1);
+    if (s != KVQ_OK) return s;
+    if (max_new < 0) return KVQ_ERR_ARG;
+    if (max_new > 0x7fffffff) return KVQ_ERR_UNSUPPORTED;
+    if (!cu_new || !n_free || (max_new > 0 && !slot_map)) return KVQ_ERR_ARG;
+    if (n_seq > 0 && (!kv_lens || !new_lens || !lens_out)) return KVQ_ERR_ARG;
+    if (n_seq > 0 && n_pages > 0 && (!block_table || !free_pages)) return KVQ_ERR_ARG;
+    if (lens_out && lens_out == new_lens) return KVQ_ERR_ARG;
+    if (!aligned(kv_lens, 8) || !aligned(new_lens, 8) || !aligned(lens_out, 8) || !aligned(cu_new, 8) ||
+        !aligned(slot_map, 8) || !aligned(positions, 8) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
+        !aligned(n_free, 4) || !aligned(workspace, 16))
+        return KVQ_ERR_ARG;
+    if (!workspace || workspace_bytes < kWsHeader) return KVQ_ERR_WORKSPACE;
+    return cuda_status(launch_pages_reserve(n_seq, page_rows, kv_lens, new_lens, block_table, table_stride, free_pages,
+                                            n_free, n_pages, lens_out, cu_new, slot_map, positions, max_new, workspace,
+                                            (cudaStream_t)stream));
+}
+
+kvq_status kv_pages_trim(int32_t n_seq, int32_t page_rows, int64_t* kv_lens, const int64_t* keep_lens,
+                         int32_t* block_table, int32_t table_stride, int32_t* free_pages, int32_t* n_free,
+                         int32_t n_pages, void* workspace, size_t workspace_bytes, void* stream) {
+    kvq_status s = check_pages(n_seq, page_rows, table_stride, n_pages, 1);
+    if (s != KVQ_OK) return s;
+    if (n_seq == 0) return KVQ_OK;
+    if (!kv_lens || !keep_lens || !n_free || kv_lens == keep_lens) return KVQ_ERR_ARG;
+    if (n_pages > 0 && (!block_table || !free_pages)) return KVQ_ERR_ARG;
+    if (!aligned(kv_lens, 8) || !aligned(keep_lens, 8) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
+        !aligned(n_free, 4) || !aligned(workspace, 16))
+        return KVQ_ERR_ARG;
+    if (!workspace || workspace_bytes < kWsHeader) return KVQ_ERR_WORKSPACE;
+    return cuda_status(launch_pages_trim(n_seq, page_rows, kv_lens, keep_lens, block_table, table_stride, free_pages,
+                                         n_free, n_pages, workspace, (cudaStream_t)stream));
+}
+
+kvq_status kv_rope_append(kvq_format fmt, const kvq_mla_layout* layout, const kvq_rope* rope, const void* x_new,
+                          kvq_dtype x_dtype, int64_t x_stride, int64_t n, const int64_t* positions,
+                          int64_t pos_stride, const int64_t* slot_map, const void* q_in, kvq_dtype q_dtype,
+                          int64_t q_in_token, int64_t q_in_head, void* q_out, int64_t q_out_token,
+                          int64_t q_out_head, int32_t n_heads, uint8_t* codes, float* scales, int64_t pool_rows,
+                          int32_t* err_word, void* stream) {
+    if (fmt != KVQ_KV8 && !is_tq(fmt)) return KVQ_ERR_ARG;
+    if (is_pq(fmt)) return KVQ_ERR_UNSUPPORTED;
+    kvq_status s = fmt == KVQ_TQ4 ? check_tq4_layout(layout) : check_layout(layout);
+    if (s != KVQ_OK) return s;
+    const int D = row_dim(layout);
+    if (!rope || rope->dim <= 0 || rope->dim % 2 != 0 || rope->n_axes < 1) return KVQ_ERR_ARG;
+    if (D > 1024 || rope->dim > 128 || rope->n_axes > 4) return KVQ_ERR_UNSUPPORTED;
+    if (rope->dim > D) return KVQ_ERR_ARG;
+    for (int i = 0; i < rope->dim / 2; ++i)
+        if (rope->axis[i] >= rope->n_axes || !isfinite(rope->inv_freq[i])) return KVQ_ERR_ARG;
+    if ((x_dtype != KVQ_F32 && x_dtype != KVQ_BF16) || (q_dtype != KVQ_F32 && q_dtype != KVQ_BF16)) return KVQ_ERR_ARG;
+    if (n < 0 || n_heads < 0 || pool_rows < 0) return KVQ_ERR_ARG;
+    if (n > 0x7fffffff || n_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+    if (n == 0) return KVQ_OK;
+    if (!positions || (rope->n_axes > 1 && pos_stride < n)) return KVQ_ERR_ARG;
+    if (x_new && (!slot_map || x_stride < D || (pool_rows > 0 && (!codes || !scales)))) return KVQ_ERR_ARG;
+    if (n_heads > 0 && (!q_in || !q_out)) return KVQ_ERR_ARG;
+    const uintptr_t xs = x_dtype == KVQ_BF16 ? 2 : 4, qs = q_dtype == KVQ_BF16 ? 2 : 4;
+    if (!aligned(x_new, xs) || !aligned(q_in, qs) || !aligned(q_out, qs) || !aligned(positions, 8) ||
+        !aligned(slot_map, 8) || !aligned(scales, 4) || !aligned(err_word, 4))
+        return KVQ_ERR_ARG;
+    if (n_heads > 0 && q_in == q_out && (q_in_token != q_out_token || q_in_head != q_out_head)) return KVQ_ERR_ARG;
+    return cuda_status(launch_rope_append(fmt, *layout, *rope, x_new, x_dtype, x_stride, n, positions, pos_stride,
+                                          slot_map, q_in, q_dtype, q_in_token, q_in_head, q_out, q_out_token,
+                                          q_out_head, n_heads, codes, scales, pool_rows, err_word,
+                                          (cudaStream_t)stream));
+}
+
+// Paged attention: the exact kernel takes both query types.
+static kvq_status resolve_paged(kvq_format fmt, const kvq_mla_layout* L, kvq_dtype dt, kvq_path path, bool* tensor) {
+    if (is_pq(fmt)) return KVQ_ERR_UNSUPPORTED;
+    kvq_status s = check_attn_layout(fmt, L);
+    if (s != KVQ_OK) return s;
+    if ((s = check_path(path)) != KVQ_OK) return s;
+    if (dt != KVQ_F32 && dt != KVQ_BF16) return KVQ_ERR_ARG;
+    if (path == KVQ_PATH_TENSOR) return KVQ_ERR_UNSUPPORTED;
+    *tensor = false;
+    return KVQ_OK;
+}
+
+size_t kv_attn_paged_workspace_size(kvq_format fmt, const kvq_mla_layout* layout, kvq_dtype q_dtype, int32_t n_seq,
+                                    int32_t n_heads, int64_t n_tokens, kvq_path path) {
+    bool tensor;
+    if (n_seq < 0 || n_heads < 0 || n_tokens < 0) return 0;
+    if (resolve_paged(fmt, layout, q_dtype, path, &tensor) != KVQ_OK) return 0;
+    return paged_workspace_bytes(tensor);
+}
+
+kvq_status kv_attn_paged(kvq_format fmt, const kvq_mla_layout* layout, const void* q, kvq_dtype q_dtype,
+                         int64_t n_tokens, int32_t n_heads, int32_t n_seq, const int64_t* cu_q, const uint8_t* codes,
+                         const float* scales, const int32_t* block_table, int32_t table_stride,
+                         const int64_t* kv_lens, int32_t page_rows, int32_t n_pages, float sm_scale, void* out,
+                         void* workspace, size_t workspace_bytes, kvq_path path, void* stream) {
+    bool tensor;
+    kvq_status s = resolve_paged(fmt, layout, q_dtype, path, &tensor);
+    if (s != KVQ_OK) return s;
+    if ((s = check_pages(n_seq, page_rows, table_stride, n_pages, 16)) != KVQ_OK) return s;
+    if (n_heads < 0 || n_tokens < 0) return KVQ_ERR_ARG;
+    if (n_heads > 65535 || n_tokens > 0x7fffffff) return KVQ_ERR_UNSUPPORTED;
+    if (!isfinite(sm_scale)) return KVQ_ERR_ARG;
+    if (n_heads == 0 || n_tokens == 0 || n_seq == 0) return KVQ_OK;
+    if (!q || !out || !cu_q || !kv_lens) return KVQ_ERR_ARG;
+    if (n_pages > 0 && table_stride > 0 && (!codes || !scales || !block_table)) return KVQ_ERR_ARG;
+    if (n_pages == 0) table_stride = 0;   // nothing to read: every length but 0 is invalid
+    if (!attn_pointers_aligned(q, codes, scales, cu_q, static_cast<const float*>(out)) || !aligned(kv_lens, 8) ||
+        !aligned(block_table, 4) || !aligned(workspace, 16))
+        return KVQ_ERR_ARG;
+    if (!workspace || workspace_bytes < paged_workspace_bytes(tensor)) return KVQ_ERR_WORKSPACE;
+    return cuda_status(launch_attn_paged(fmt, *layout, tensor, q, q_dtype, n_tokens, n_heads, n_seq, cu_q, codes,
+                                         scales, block_table, table_stride, kv_lens, page_rows, n_pages, sm_scale, out,
+                                         workspace, (cudaStream_t)stream));
+}
+
 int32_t kvq_read_device_error(void* workspace, int32_t clear, void* stream) {
     if (!workspace) return KVQ_ERR_ARG;
     cudaStream_t st = (cudaStream_t)stream;

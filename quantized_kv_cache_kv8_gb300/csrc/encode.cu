@@ -6,7 +6,7 @@
 // FWHT of a 512-block is 5 shuffle stages plus 4 in-register stages.  All
 // arithmetic is IEEE f32 with explicit _rn intrinsics, so nvcc cannot fuse or
 // reorder it: the codes and scales are bit-identical to the plain definition.
-#include "kvq_internal.cuh"
+#include "encode_common.cuh"
 
 #include <math.h>
 
@@ -83,47 +83,6 @@ cudaError_t launch_kv8_encode(const float* x, int64_t n_rows, const kvq_mla_layo
 // ---------------------------------------------------------------------------
 // TQ4: rotate, radius, nearest codebook level, nibble pack
 // ---------------------------------------------------------------------------
-struct Tq4Params {
-    int32_t D, n_blocks, bd[2];
-    float kn[2];      // (float)(1/sqrt(n)) per block
-    float sqrtn[2];   // sqrtf((float)n) per block
-    SignWords signs;
-    Codebook16 cb;
-};
-
-template <int N>
-__device__ __forceinline__ void tq4_encode_block(const float* __restrict__ xb, int lane, const Tq4Params& p, int blk,
-                                                 const float* th, uint8_t* __restrict__ out, float* scale_out,
-                                                 int32_t* err) {
-    constexpr int K = N >= 32 ? N / 32 : 1;
-    const bool active = (N >= 32) || (lane < N);
-    float x[K], v[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int i = lane + 32 * k;
-        x[k] = active ? __ldg(xb + i) : 0.0f;
-        v[k] = (active && sign_neg(p.signs, blk, i)) ? -x[k] : x[k];
-    }
-    // sum of squares: per-lane fma chain over ascending elements, then halving
-    float ss = 0.0f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) ss = __fmaf_rn(x[k], x[k], ss);
-    ss = warp_sum(ss);
-    // a NaN or infinite input, or a radius past the f32 range: no code exists
-    if (!(ss <= 3.402823466e38f) && lane == 0 && err) atomicCAS(err, 0, (int32_t)KVQ_ERR_NONFINITE);
-    const float s = __fdiv_rn(__fsqrt_rn(ss), p.sqrtn[blk]);
-    warp_fwht<N>(v, lane);
-    const float kn = p.kn[blk];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        int c = 0;
-        if (s != 0.0f) c = code16(__fdiv_rn(__fmul_rn(v[k], kn), s), th);
-        const int hi = __shfl_down_sync(kFull, c, 1);
-        if (active && (lane & 1) == 0) out[(lane + 32 * k) >> 1] = (uint8_t)(c | (hi << 4));
-    }
-    if (lane == 0) *scale_out = s;
-}
-
 template <int N>
 __device__ __forceinline__ void tq4_rotate_block(float* v, int lane, const Tq4Params& p, int blk, bool inverse) {
     constexpr int K = N >= 32 ? N / 32 : 1;
@@ -140,9 +99,6 @@ __device__ __forceinline__ void tq4_rotate_block(float* v, int lane, const Tq4Pa
         if (inverse && active && sign_neg(p.signs, blk, lane + 32 * k)) v[k] = -v[k];
     }
 }
-
-#define KVQ_POW2_CASES(MACRO) \
-    MACRO(2) MACRO(4) MACRO(8) MACRO(16) MACRO(32) MACRO(64) MACRO(128) MACRO(256) MACRO(512) MACRO(1024)
 
 __global__ void __launch_bounds__(256) tq4_encode_kernel(const float* __restrict__ x, int64_t n_rows, Tq4Params p,
                                                          const int64_t* __restrict__ dst_rows,
@@ -162,7 +118,7 @@ __global__ void __launch_bounds__(256) tq4_encode_kernel(const float* __restrict
         float* so = scales + row * p.n_blocks + b;
         switch (p.bd[b]) {
 #define KVQ_CASE(n) \
-    case n: tq4_encode_block<n>(xb, lane, p, b, th, ob, so, err); break;
+    case n: tq4_encode_block<n>([xb](int i) { return __ldg(xb + i); }, lane, p, b, th, ob, so, err); break;
             KVQ_POW2_CASES(KVQ_CASE)
 #undef KVQ_CASE
             default: break;
@@ -215,7 +171,7 @@ __global__ void __launch_bounds__(256) tq4_rotate_kernel(const T* __restrict__ i
     }
 }
 
-static Tq4Params make_tq4_params(const kvq_mla_layout& L) {
+Tq4Params make_tq4_params(const kvq_mla_layout& L) {
     Tq4Params p{};
     p.n_blocks = L.n_blocks;
     p.bd[0] = L.block_dim[0];

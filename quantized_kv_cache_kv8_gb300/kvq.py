@@ -33,6 +33,11 @@ class MLALayout(C.Structure):
                 ("seed", C.c_uint64)]
 
 
+class Rope(C.Structure):
+    _fields_ = [("dim", C.c_int32), ("n_axes", C.c_int32), ("adjacent", C.c_int32), ("axis", C.c_uint8 * 64),
+                ("inv_freq", C.c_double * 64)]
+
+
 class K2V4Layout(C.Structure):
     _fields_ = [("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("group", C.c_int32),
                 ("k_gain", C.c_float), ("n_sink", C.c_int32), ("n_window", C.c_int32), ("n_slack", C.c_int32)]
@@ -45,6 +50,20 @@ def mla_layout(block_dims=(512, 64), v_dim=512, seed=0) -> MLALayout:
 
 def k2v4_layout(n_kv_heads=2, head_dim=256, k_gain=1.10, n_sink=8, n_window=256, n_slack=16) -> K2V4Layout:
     return K2V4Layout(n_kv_heads, head_dim, 32, k_gain, n_sink, n_window, n_slack)
+
+
+def rope_layout(inv_freq, axis=None, n_axes: int | None = None, adjacent: bool = False) -> Rope:
+    """Rotary positions of the last 2 * len(inv_freq) dims: pair i turns by
+    positions[axis[i]] * inv_freq[i] (axis None: one axis for every pair); pairs
+    are (i, i + n) or, if adjacent, (2 i, 2 i + 1)."""
+    n = len(inv_freq)
+    if not 1 <= n <= 64:
+        raise ValueError("rope_layout takes 1..64 pairs")
+    axis = [0] * n if axis is None else [int(a) for a in axis]
+    if len(axis) != n or min(axis) < 0 or max(axis) > 255:
+        raise ValueError("one axis index per pair")
+    return Rope(2 * n, max(axis) + 1 if n_axes is None else n_axes, int(adjacent), (C.c_uint8 * 64)(*axis),
+                (C.c_double * 64)(*[float(w) for w in inv_freq]))
 
 
 _lock = threading.Lock()
@@ -113,6 +132,20 @@ def _declare(L):
     L.kv_attn_prefill_workspace_size.argtypes = [C.c_int, pl, I32, I64, I64, C.c_int]
     L.kv_attn_prefill.restype = C.c_int
     L.kv_attn_prefill.argtypes = [C.c_int, pl, P, P, C.c_int, I64, I64, I32, P, P, C.c_float, P, P, S, C.c_int, P]
+    L.kv_pages_workspace_size.restype = S
+    L.kv_pages_workspace_size.argtypes = []
+    L.kv_pages_reserve.restype = C.c_int
+    L.kv_pages_reserve.argtypes = [I32, I32, P, P, P, I32, P, P, I32, P, P, P, P, I64, P, S, P]
+    L.kv_pages_trim.restype = C.c_int
+    L.kv_pages_trim.argtypes = [I32, I32, P, P, P, I32, P, P, I32, P, S, P]
+    L.kv_rope_append.restype = C.c_int
+    L.kv_rope_append.argtypes = [C.c_int, pl, C.POINTER(Rope), P, C.c_int, I64, I64, P, I64, P, P, C.c_int, I64, I64, P,
+                                 I64, I64, I32, P, P, I64, P, P]
+    L.kv_attn_paged_workspace_size.restype = S
+    L.kv_attn_paged_workspace_size.argtypes = [C.c_int, pl, C.c_int, I32, I32, I64, C.c_int]
+    L.kv_attn_paged.restype = C.c_int
+    L.kv_attn_paged.argtypes = [C.c_int, pl, P, C.c_int, I64, I32, I32, P, P, P, P, I32, P, I32, I32, C.c_float, P, P, S,
+                                C.c_int, P]
     L.kvq_read_device_error.restype = I32
     L.kvq_read_device_error.argtypes = [P, I32, P]
     L.kvq_read_exact_rescales.restype = I64
@@ -359,6 +392,128 @@ def kv_attn_prefill(fmt: int, x_new, q, codes, scales, n_past: int, out, workspa
                               _ptr(scales, torch.float32, "scales"), float(sm_scale), _ptr(out, torch.float32, "out"),
                               _ptr(workspace, torch.uint8, "workspace"), workspace.numel(), path, _stream(stream)),
         "kv_attn_prefill")
+
+
+# -- paged pools ---------------------------------------------------------------
+
+def _dev(t, dtype, name, shape=None):
+    """Pointer of a contiguous CUDA tensor on the current device, its type and shape checked."""
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return _ptr(t, dtype, name)
+
+
+def kv_pages_workspace_size() -> int:
+    return lib().kv_pages_workspace_size()
+
+
+def _pages(block_table, free_pages, n_free, n_seq):
+    if block_table.dim() != 2 or block_table.shape[0] != n_seq:
+        raise ValueError("block_table must be [n_seq][table_stride]")
+    return (_dev(block_table, torch.int32, "block_table"), block_table.shape[1],
+            _dev(free_pages, torch.int32, "free_pages", (free_pages.numel(),)), _dev(n_free, torch.int32, "n_free", (1,)),
+            free_pages.numel())
+
+
+def kv_pages_reserve(kv_lens, new_lens, block_table, free_pages, n_free, page_rows: int, lens_out, cu_new, slot_map,
+                     positions, workspace, stream=None):
+    """Pages, slots and positions for new_lens[s] new rows of every sequence (free_pages is the stack of all
+    pages, n_free its height).  lens_out may be kv_lens, positions None."""
+    n = kv_lens.numel()
+    m = slot_map.numel()
+    table, stride, stack, height, n_pages = _pages(block_table, free_pages, n_free, n)
+    _ok(lib().kv_pages_reserve(n, page_rows, _dev(kv_lens, torch.int64, "kv_lens", (n,)),
+                               _dev(new_lens, torch.int64, "new_lens", (n,)), table, stride, stack, height, n_pages,
+                               _dev(lens_out, torch.int64, "lens_out", (n,)),
+                               _dev(cu_new, torch.int64, "cu_new", (n + 1,)),
+                               _dev(slot_map, torch.int64, "slot_map", (m,)),
+                               None if positions is None else _dev(positions, torch.int64, "positions", (m,)), m,
+                               _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)),
+        "kv_pages_reserve")
+
+
+def kv_pages_trim(kv_lens, keep_lens, block_table, free_pages, n_free, page_rows: int, workspace, stream=None):
+    """Cuts every sequence back to keep_lens[s] rows (negative: keeps it, 0: ends it); its pages return to the stack."""
+    n = kv_lens.numel()
+    table, stride, stack, height, n_pages = _pages(block_table, free_pages, n_free, n)
+    _ok(lib().kv_pages_trim(n, page_rows, _dev(kv_lens, torch.int64, "kv_lens", (n,)),
+                            _dev(keep_lens, torch.int64, "keep_lens", (n,)), table, stride, stack, height, n_pages,
+                            _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)),
+        "kv_pages_trim")
+
+
+def _strided(t, dims, name):
+    """A CUDA tensor whose last dimension is contiguous, on the current device."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must have {dims} dimensions, the last one contiguous")
+    return C.c_void_p(t.data_ptr())
+
+
+def kv_rope_append(fmt: int, rope: Rope, x_new, positions, slot_map, q_in, q_out, codes, scales,
+                   layout: MLALayout | None = None, err_word=None, stream=None):
+    """One step's producer: q_in [n][n_heads][dim] rotated into q_out (the same shape, or whole queries
+    [n][n_heads][D] whose last dims it fills; q_in itself rotates in place), x_new [n][D] rotated, encoded and
+    stored in the pool rows slot_map (negative: skipped).  positions int64 [n_axes][n] (or [n] for one axis).
+    x_new None: only queries; q_in None: only rows."""
+    layout = layout or mla_layout()
+    D = layout.block_dim[0] + (layout.block_dim[1] if layout.n_blocks > 1 else 0)
+    n = x_new.shape[0] if x_new is not None else q_in.shape[0]
+    shape = (n,) if positions.dim() == 1 and rope.n_axes == 1 else (rope.n_axes, n)
+    pos = _dev(positions, torch.int64, "positions", shape)
+    xp = sp = cp = fp = None
+    xd, xs, rows = KVQ_F32, 0, 0
+    if x_new is not None:
+        xp, xd, xs = _strided(x_new, 2, "x_new"), _qdtype(x_new), x_new.stride(0)
+        if x_new.shape[1] != D:
+            raise ValueError(f"x_new must have {D} columns")
+        rows = codes.shape[0]
+        sp = _dev(slot_map, torch.int64, "slot_map", (n,))
+        cp = _dev(codes, torch.uint8, "codes", (rows, row_bytes(fmt, layout)))
+        fp = _dev(scales, torch.float32, "scales", (rows, layout.n_blocks))
+    qi = qo = None
+    qd, heads, si, so = KVQ_F32, 0, (0, 0), (0, 0)
+    if q_in is not None:
+        qi, qd, heads, si = _strided(q_in, 3, "q_in"), _qdtype(q_in), q_in.shape[1], q_in.stride()
+        if q_out.shape[-1] == D and D != rope.dim:
+            q_out = q_out[..., D - rope.dim:]
+        if tuple(q_in.shape) != (n, heads, rope.dim) or q_out.shape != q_in.shape or q_out.dtype != q_in.dtype:
+            raise ValueError(f"q_in must be [{n}][n_heads][{rope.dim}] and q_out match it")
+        qo, so = _strided(q_out, 3, "q_out"), q_out.stride()
+    _ok(lib().kv_rope_append(fmt, C.byref(layout), C.byref(rope), xp, xd, xs, n, pos, n, sp, qi, qd, si[0], si[1], qo,
+                             so[0], so[1], heads, cp, fp, rows, _err_ptr(err_word), _stream(stream)), "kv_rope_append")
+
+
+def kv_attn_paged_workspace_size(fmt: int, n_seq: int, n_heads: int, n_tokens: int, layout: MLALayout | None = None,
+                                 bf16: bool = True, path: int = PATH_AUTO) -> int:
+    layout = layout or mla_layout()
+    return lib().kv_attn_paged_workspace_size(fmt, C.byref(layout), KVQ_BF16 if bf16 else KVQ_F32, n_seq, n_heads,
+                                              n_tokens, path)
+
+
+def kv_attn_paged(fmt: int, q, cu_q, codes, scales, block_table, kv_lens, page_rows: int, out, workspace,
+                  sm_scale: float = SM_SCALE_MLA, layout: MLALayout | None = None, path: int = PATH_AUTO, stream=None):
+    """Causal attention of the new tokens q [n_tokens][n_heads][576] (sequence b: q[cu_q[b]:cu_q[b+1]], the last
+    of its kv_lens[b] rows) over paged rows; out [n_tokens][n_heads][512] in q's type."""
+    layout = layout or mla_layout()
+    n, H, B = q.shape[0], q.shape[1], kv_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [n_seq][table_stride]")
+    rows = codes.shape[0]
+    if rows % page_rows != 0:
+        raise ValueError("the pool must hold whole pages")
+    _ok(lib().kv_attn_paged(fmt, C.byref(layout), _dev(q, None, "q", (n, H, 576)), _qdtype(q), n, H, B,
+                            _dev(cu_q, torch.int64, "cu_q", (B + 1,)),
+                            _dev(codes, torch.uint8, "codes", (rows, row_bytes(fmt, layout))),
+                            _dev(scales, torch.float32, "scales", (rows, layout.n_blocks)),
+                            _dev(block_table, torch.int32, "block_table"), block_table.shape[1],
+                            _dev(kv_lens, torch.int64, "kv_lens", (B,)), page_rows, rows // page_rows,
+                            float(sm_scale), _dev(out, q.dtype, "out", (n, H, 512)),
+                            _dev(workspace, torch.uint8, "workspace"), workspace.numel(), path, _stream(stream)),
+        "kv_attn_paged")
 
 
 def read_device_error(workspace, clear: bool = True, stream=None) -> int:
