@@ -486,8 +486,12 @@ size_t kv_attn_paged_workspace_size(kvq_format fmt, const kvq_mla_layout* layout
  *   kv_lens      [n_seq] int64: rows of each sequence, at most
  *                table_stride * page_rows
  *   out          [n_tokens][n_heads][512] in q_dtype
- * Layouts as kv_attn_decode.  Runs in f32 (KVQ_PATH_SIMT, and AUTO), within 1e-5
- * before the rounding to q_dtype.  Invalid lengths or offsets and pages outside
+ * Layouts as kv_attn_decode.  KVQ_PATH_TENSOR (AUTO with bf16 queries): f16
+ * operands with f32 accumulation, bf16 queries only, within 2e-3 of exact before
+ * the rounding to bf16.  With TQ4 the rotated query is rounded to f16 once,
+ * which moves a score by about 2^-12 sm_scale |q'| |x'| / 24 more (4e-4 of the
+ * outputs in the 2-norm on channel-outlier rows; the rounding to bf16 is 1.7e-3).  KVQ_PATH_SIMT (AUTO with f32 queries): f32, within 1e-5 before the
+ * rounding to q_dtype.  Invalid lengths or offsets and pages outside
  * [0, n_pages) set KVQ_ERR_ARG in the workspace's device word; nothing outside
  * the pool is read. */
 kvq_status kv_attn_paged(kvq_format fmt, const kvq_mla_layout* layout, const void* q, kvq_dtype q_dtype,

@@ -510,15 +510,16 @@ kvq_status kv_rope_append(kvq_format fmt, const kvq_mla_layout* layout, const kv
                                           (cudaStream_t)stream));
 }
 
-// Paged attention: the exact kernel takes both query types.
+// Paged attention: the tensor-core kernel takes bf16 queries (AUTO prefers it),
+// the exact kernel both types.
 static kvq_status resolve_paged(kvq_format fmt, const kvq_mla_layout* L, kvq_dtype dt, kvq_path path, bool* tensor) {
     if (is_pq(fmt)) return KVQ_ERR_UNSUPPORTED;
     kvq_status s = check_attn_layout(fmt, L);
     if (s != KVQ_OK) return s;
     if ((s = check_path(path)) != KVQ_OK) return s;
     if (dt != KVQ_F32 && dt != KVQ_BF16) return KVQ_ERR_ARG;
-    if (path == KVQ_PATH_TENSOR) return KVQ_ERR_UNSUPPORTED;
-    *tensor = false;
+    if (path == KVQ_PATH_TENSOR && dt != KVQ_BF16) return KVQ_ERR_UNSUPPORTED;
+    *tensor = path != KVQ_PATH_SIMT && dt == KVQ_BF16;
     return KVQ_OK;
 }
 

@@ -437,11 +437,13 @@ cudaError_t launch_attn_paged(kvq_format fmt, const kvq_mla_layout& L, bool tens
     const bool tq4 = fmt == KVQ_TQ4, bf16 = dt == KVQ_BF16;
     timing_mark(stream, 0);
     cudaError_t e;
-    if (tq4) e = bf16 ? launch_exact<true, true>(p, stream) : launch_exact<true, false>(p, stream);
+    if (tensor) e = launch_paged_tensor(fmt, p, stream);
+    else if (tq4) e = bf16 ? launch_exact<true, true>(p, stream) : launch_exact<true, false>(p, stream);
     else e = bf16 ? launch_exact<false, true>(p, stream) : launch_exact<false, false>(p, stream);
     if (e != cudaSuccess) return e;
     timing_mark(stream, 1);
-    if (tq4) e = bf16 ? launch_merge<true, true, PagedSimt::kM>(p, stream) : launch_merge<true, false, PagedSimt::kM>(p, stream);
+    if (tensor) e = tq4 ? launch_merge<true, true, PagedTensor::kM>(p, stream) : launch_merge<false, true, PagedTensor::kM>(p, stream);
+    else if (tq4) e = bf16 ? launch_merge<true, true, PagedSimt::kM>(p, stream) : launch_merge<true, false, PagedSimt::kM>(p, stream);
     else e = bf16 ? launch_merge<false, true, PagedSimt::kM>(p, stream) : launch_merge<false, false, PagedSimt::kM>(p, stream);
     timing_mark(stream, 2);
     return e;

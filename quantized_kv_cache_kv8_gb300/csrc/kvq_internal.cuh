@@ -257,7 +257,7 @@ cudaError_t launch_attn_tc(kvq_format fmt, const kvq_mla_layout& L, const void* 
                            cudaStream_t stream, const int64_t* sel = nullptr, int64_t pool_rows = 0);
 
 // Paged pools: page bookkeeping (pages.cu), rotary append (rope.cu), attention
-// (attn_paged.cu)
+// (attn_paged.cu, attn_tc_paged.cu)
 cudaError_t launch_pages_reserve(int32_t n_seq, int32_t page_rows, const int64_t* lens, const int64_t* new_lens,
                                  int32_t* table, int32_t table_stride, int32_t* free_pages, int32_t* n_free,
                                  int32_t n_pages, int64_t* lens_out, int64_t* cu_new, int64_t* slots,

@@ -74,7 +74,8 @@ struct PagedSched {
         if (b >= p.n_seq) return s;
         const int64_t a = p.cu_q[b], e = p.cu_q[b + 1];
         int64_t kv = p.kv_lens[b];
-        const int64_t cap = (int64_t)p.table_stride << p.shift;
+        // a table row, and the pool, hold so many rows; row indices stay within int32
+        const int64_t cap = min((int64_t)min(p.table_stride, p.n_pages) << p.shift, (int64_t)0x7fffffff - 1024);
         if (a < 0 || e < a || e > p.max_tok || kv < 0 || kv > cap) set_err(p.err, KVQ_ERR_ARG);
         if (a < 0 || e <= a || e > p.max_tok) return s;
         kv = min(max(kv, (int64_t)0), cap);
@@ -257,5 +258,7 @@ __device__ __forceinline__ int32_t paged_row(const PagedParams& p, int32_t b, in
 using PagedSimt = SchedOf<32, 32, 4>;
 using PagedTensor = SchedOf<64, 128, 2>;
 constexpr int kPagedCtas = 152;
+
+cudaError_t launch_paged_tensor(kvq_format fmt, const PagedParams& p, cudaStream_t stream);
 
 }  // namespace kvq
