@@ -18,12 +18,11 @@
 //
 // Step t: 16 worker warps store the step's codes chunk group by chunk group
 // (dims 0-255, 256-511, rope) as the context products of step t-1 release the
-// chunks; one thread of a 17th warp issues score products group by group behind
+// chunks; a 17th warp issues score products group by group behind
 // them, and the context products once the weights are written.  The next step's
 // codes are on their way to registers before the softmax.  16 warps, because a
 // step is a chain (store, score, softmax, context) and its links are as long as
-// a warp's share of them; their registers come from the issuing warpgroup
-// (setmaxnreg).
+// a warp's share of them.
 //
 // Softmax, per query vector, in log2 units: m is a lagged running maximum of the
 // scores, p = 2^(z - m) enters the row sum in f32, and the context takes the f16
@@ -48,9 +47,7 @@ constexpr int kRows = PagedTensor::kN;      // rows a step
 constexpr int kCols = PagedTensor::kM;      // query vectors
 constexpr int kWarps = 16;                  // worker warps
 constexpr int kWorkers = 32 * kWarps;
-constexpr int kThreads = kWorkers + 128;
-constexpr int kRegsLaunch = 96, kRegsWorker = 112, kRegsMma = 32;
-static_assert(kWorkers * kRegsWorker + 128 * kRegsMma <= kThreads * kRegsLaunch, "register split");
+constexpr int kThreads = kWorkers + 64;     // ... and the issuing and the walking warp: 112 registers a thread
 constexpr int kChunks = 9, kRope = 8;       // the rope chunk's slot holds P^T after the score
 constexpr uint32_t kSlotBytes = kRows * 128, kQChunkBytes = kCols * 128;
 constexpr uint32_t kOffQ = 0;
@@ -195,6 +192,27 @@ __device__ __forceinline__ void store_group(unsigned char* sSlot, const uint4 (&
         if (TQ4) store_tq4(sSlot + (4 * g + (byte >> 5)) * kSlotBytes, v[i], row, 4 * (byte & 31), t);
         else store_kv8(sSlot + (4 * g + (byte >> 6)) * kSlotBytes, v[i], row, 2 * (byte & 63));
     }
+}
+
+// One MMA, or one commit, of a whole warp in step: the warp computes the
+// descriptors together (in uniform registers) and one elected lane, always the
+// same, issues.  A lone lane in a branch of its own spends about 115 cycles an
+// MMA on moving its operands; this way N = 64 runs at the 48 cycles that its 6 KB
+// of operands take to read.
+__device__ __forceinline__ void umma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
+    return __all_sync(kFull, mbar_wait(bar, parity, abort_flag, limit));
 }
 
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
@@ -385,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tensor_kernel(const __grid_
     int64_t* sPart = reinterpret_cast<int64_t*>(sm + kOffPart);
     Work* sWork = reinterpret_cast<Work*>(sm + kOffWork);
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
     const int64_t cta = blockIdx.x;
     const int64_t wl = p.wait_limit;
     if (tid < 4) p.ws_desc[cta * 4 + tid] = 0;
@@ -428,7 +446,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tensor_kernel(const __grid_
     const uint32_t tmem = *sTmem;
 
     if (warp >= kWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
         // ================= the walk: announces segments one ahead =================
         if (warp == kWarps + 1 && lane == 0) {
             bool more = true;
@@ -453,60 +470,57 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tensor_kernel(const __grid_
                 mbar_arrive(&bars[kBarWork0 + (n & 1)]);
             }
         }
-        // ================= the issuing thread =================
-        if (warp == kWarps && lane == 0) {
+        // ================= the issuing warp =================
+        if (warp == kWarps) {
             const uint64_t dq0 = umma_desc(smem_u32(sQ), 16, 1024);
             const uint64_t dslot0 = umma_desc(smem_u32(sSlot), 16, 1024);
             const uint64_t dpair0 = umma_desc(smem_u32(sSlot), kSlotBytes, 1024);
             const uint64_t dp = umma_desc(smem_u32(sP), kSlotBytes, 1024);
             constexpr uint64_t kQStep = kQChunkBytes >> 4, kSlotStep = kSlotBytes >> 4;
             bool ok = true;
-            if (p.stall_polls > 0) ok = mbar_wait(&bars[kBarNever], 0u, sAbort, p.stall_polls);
+            if (p.stall_polls > 0) ok = warp_wait(&bars[kBarNever], 0u, sAbort, p.stall_polls);
             uint32_t it = 0;
             for (int n = 0; ok; ++n) {
-                ok = mbar_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl);
+                ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl);
                 if (!ok) break;
-                const int steps = sWork[n & 1].steps;
+                const int steps = __shfl_sync(kFull, sWork[n & 1].steps, 0);
                 if (steps == 0) break;
-                mbar_arrive(&bars[kBarWorkFree0 + (n & 1)]);
+                warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
                 for (int t = 0; t < steps && ok; ++t, ++it) {
                     const uint32_t par = it & 1u;
-#pragma unroll 1
-                    for (int kc = 0; kc < kChunks && ok; ++kc) {
-                        if ((kc & 3) == 0) {
-                            ok = mbar_wait(&bars[kBarFull0 + (kc >> 2)], par, sAbort, wl);
-                            tc_after();
-                        }
-                        const uint32_t d = tmem + (kc < kRope ? kColSL : kColSR);
-                        const uint64_t a = dslot0 + kc * kSlotStep, bq = dq0 + kc * kQStep;
-                        const bool fresh = kc == 0 || kc == kRope;
-                        if (ok) {
+#pragma unroll
+                    for (int gr = 0; gr < 3; ++gr) {
+                        ok = ok && warp_wait(&bars[kBarFull0 + gr], par, sAbort, wl);
+                        if (!ok) break;
+                        tc_after();
+#pragma unroll
+                        for (int kc = 4 * gr; kc < (gr < 2 ? 4 * gr + 4 : kChunks); ++kc)
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                umma_f16(d, a + 2 * ks, bq + 2 * ks, kIdescScore, (fresh && ks == 0) ? 0u : 1u);
-                        }
+                                umma_one(tmem + (kc < kRope ? kColSL : kColSR), dslot0 + kc * kSlotStep + 2 * ks,
+                                         dq0 + kc * kQStep + 2 * ks, kIdescScore,
+                                         ((kc == 0 || kc == kRope) && ks == 0) ? 0u : 1u);
                     }
-                    umma_commit(&bars[kBarScore]);
-                    ok = ok && mbar_wait(&bars[kBarP], par, sAbort, wl);
+                    commit_one(&bars[kBarScore]);
+                    ok = ok && warp_wait(&bars[kBarP], par, sAbort, wl);
+                    if (!ok) break;
                     tc_after();
-#pragma unroll 1
-                    for (int db = 0; db < 4 && ok; ++db) {
-                        const uint32_t d = tmem + kColO + 64 * db;
-                        const uint64_t a = dpair0 + 2 * db * kSlotStep;
+#pragma unroll
+                    for (int db = 0; db < 4; ++db) {
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            umma_f16(d, a + 128 * ks, dp + 128 * ks, kIdescCtx, (t > 0 || ks > 0) ? 1u : 0u);
-                        umma_commit(&bars[kBarFree0 + db]);
+                            umma_one(tmem + kColO + 64 * db, dpair0 + 2 * db * kSlotStep + 128 * ks, dp + 128 * ks,
+                                     kIdescCtx, (t > 0 || ks > 0) ? 1u : 0u);
+                        commit_one(&bars[kBarFree0 + db]);
                     }
                 }
             }
-            umma_commit(&bars[kBarDone]);
+            commit_one(&bars[kBarDone]);
         }
         return;
     }
 
     // ================= workers =================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWorker));
     const int srow = 32 * (warp & 3) + lane;   // softmax: this thread's row (TMEM lane)
     const int hq = warp >> 2;                   // ... and vectors 16 hq .. 16 hq + 15
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
@@ -523,15 +537,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tensor_kernel(const __grid_
         if (steps == 0) break;
         // ---- prologue: state, limits, queries, the first step's rows ----
         const int32_t first = g.first, end = g.end;
-        // pool rows of step t (tid < kRows); rows past the end get row 0, never read
-        auto row_of = [&](int t) -> int32_t {
+        // a row of step t (tid < kRows): its page is asked for early, and turned
+        // into a pool row where it is stored; rows past the end get row 0, never read
+        const int32_t* table = p.table + (int64_t)g.b * p.table_stride;
+        auto page_of = [&](int t) -> int32_t {
             const int32_t r = first + t * kRows + tid;
-            return (tid < kRows && r < end) ? paged_row(p, g.b, r) : 0;
+            return (tid < kRows && t < steps && r < end) ? __ldg(table + (r >> p.shift)) : 0;
+        };
+        auto set_row = [&](int t, int32_t id) {
+            if (tid >= kRows) return;
+            if (id < 0 || id >= p.n_pages) {
+                set_err(p.err, KVQ_ERR_ARG);
+                id = 0;
+            }
+            const int32_t r = first + t * kRows + tid;
+            sRow[(t & 1) * kRows + tid] = (id << p.shift) + (r & ((1 << p.shift) - 1));
         };
         auto rows_in = [&](int t) { return max(0, min(kRows, end - first - t * kRows)); };
-        if (tid < kRows) {
-            sRow[tid] = row_of(0);
-            sRow[kRows + tid] = row_of(1);
+        {
+            const int32_t id0 = page_of(0), id1 = page_of(1);
+            set_row(0, id0);
+            set_row(1, id1);
         }
         if (tid < kCols) {
             sM[tid] = -INFINITY;
@@ -565,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tensor_kernel(const __grid_
         int t = 0;
         for (; t < steps; ++t, ++it) {
             const uint32_t par = it & 1u, prev = par ^ 1u;
-            const int32_t row2 = t + 2 < steps ? row_of(t + 2) : 0;
+            const int32_t page2 = page_of(t + 2);
             const RowView view{tmem + lane_base + 16 * hq, sl_next, sr_next, first + t * kRows + srow,
                                srow < rows_in(t), first + (t + 1) * kRows > g.seen0};
             // ---- decode: dims 0-255, 256-511, rope ----
@@ -596,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tensor_kernel(const __grid_
             if (warp == 1) mbar_wait(&bars[kBarScore], par, sAbort, wl);
             worker_sync<kWorkers>();
             tc_after();
-            if (tid < kRows) sRow[(t & 1) * kRows + tid] = row2;   // step t's rows are no longer needed
+            set_row(t + 2, page2);   // step t's rows are no longer needed
             float z[16];
             load_scores(view, sCz + 16 * hq, sM + 16 * hq, sLim + 16 * hq, z);
             float dmax = z[0];
@@ -723,13 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tensor_kernel(const __grid_
 
 template <bool TQ4>
 cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
-    // the workers' setmaxnreg.inc waits for registers the other warpgroup
-    // released: launch only if the split adds up against the launch's own count
-    cudaFuncAttributes fa{};
-    cudaError_t e = cudaFuncGetAttributes(&fa, paged_tensor_kernel<TQ4>);
-    if (e != cudaSuccess) return e;
-    if (kWorkers * kRegsWorker + 128 * kRegsMma > kThreads * fa.numRegs) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(paged_tensor_kernel<TQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemUsed);
+    cudaError_t e = cudaFuncSetAttribute(paged_tensor_kernel<TQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemUsed);
     if (e != cudaSuccess) return e;
     paged_tensor_kernel<TQ4><<<kPagedCtas, kThreads, kSmemUsed, stream>>>(p);
     return cudaGetLastError();
