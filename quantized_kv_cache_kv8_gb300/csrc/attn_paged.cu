@@ -378,7 +378,7 @@ cudaError_t launch_exact(const PagedParams& p, cudaStream_t stream) {
 template <bool TQ4, bool BF16, int M>
 cudaError_t launch_merge(const PagedParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(M, kPagedCtas);
+    cfg.gridDim = dim3(M, M == PagedTensor::kM ? kPagedPairs : kPagedCtas);
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -389,13 +389,15 @@ cudaError_t launch_merge(const PagedParams& p, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, paged_merge_kernel<TQ4, BF16, M>, p);
 }
 
-constexpr int64_t slots_of(int64_t m) { return 2 * kPagedCtas * m; }
+// query vectors of partial state: two tiles a walker
+constexpr int64_t state_rows(bool tensor) {
+    return tensor ? 2 * kPagedPairs * PagedTensor::kM : 2 * kPagedCtas * PagedSimt::kM;
+}
 
 }  // namespace
 
 size_t paged_workspace_bytes(bool tensor) {
-    const int64_t rows = slots_of(tensor ? PagedTensor::kM : PagedSimt::kM);
-    return kWsHeader + (size_t)kPagedCtas * 4 * sizeof(int64_t) + (size_t)rows * (kMlaDV + 2) * sizeof(float);
+    return kWsHeader + (size_t)kPagedCtas * 4 * sizeof(int64_t) + (size_t)state_rows(tensor) * (kMlaDV + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn_paged(kvq_format fmt, const kvq_mla_layout& L, bool tensor, const void* q, kvq_dtype dt,
@@ -426,7 +428,7 @@ cudaError_t launch_attn_paged(kvq_format fmt, const kvq_mla_layout& L, bool tens
     p.wait_limit = p.stall_polls > 0 ? p.stall_polls : kWaitLimit;
     p.ws_desc = reinterpret_cast<int64_t*>(ws + kWsHeader);
     p.ws_o = reinterpret_cast<float*>(ws + kWsHeader + (size_t)kPagedCtas * 4 * sizeof(int64_t));
-    p.ws_ml = p.ws_o + slots_of(tensor ? PagedTensor::kM : PagedSimt::kM) * kMlaDV;
+    p.ws_ml = p.ws_o + state_rows(tensor) * kMlaDV;
     if (fmt == KVQ_TQ4) {
         p.signs = tq4_sign_words(L);
         p.kn[0] = (float)(1.0 / sqrt((double)L.block_dim[0]));

@@ -1,38 +1,48 @@
 // attn_tc_paged.cu -- tensor-core attention of new tokens over paged KV8 or TQ4
-// rows, bf16 queries.
+// rows, bf16 queries, on pairs of CTAs.
 //
-// A CTA walks over segments (paged_common.cuh): 64 query vectors -- consecutive
-// (token, head) pairs of one sequence, whatever the head count -- against a run
-// of 128-row steps.  Both products are transposed, rows (or dims) on M = 128 and
-// the 64 vectors on N:
-//   S^T = C Q^T   (A = codes, K-major; the latent and the rope dims into an
-//                  accumulator each, as each has its own row scale)
-//   O^T += C^T P^T (A = the same codes read MN-major, 4 blocks of 128 dims)
-// because 64 x 512 f32 of context is half of tensor memory and M = 64 forms run
-// at half rate.  A step's rows are decoded once to f16 (e4m3 codes exactly, the
-// 16 levels of TQ4 times kGamma within 9.3e-5) into nine 64-dim chunks of
-// swizzled shared memory (144 KB), next to the queries (72 KB).
+// A pair (a cluster of two CTAs on neighbouring SMs) walks over segments
+// (paged_common.cuh): 128 query vectors -- consecutive (token, head) pairs of
+// one sequence, whatever the head count, 64 to a CTA -- against a run of 128-row
+// steps.  Both products run as cta_group::2 MMAs with M = 128, issued by the
+// first CTA:
+//   S = Q C^T   N = 128 rows, K = 576 dims; latent and rope dims into an
+//               accumulator each, as each has its own row scale
+//   O += P C    N = 256 dims, twice, K = 128 rows
+// The pair shares the B operands: a CTA supplies 64 of the step's rows (all
+// dims) to the scores and 256 of the latent dims (all rows) to the context.
+// That decides the layout.  One CTA alone, with rows on M and 64 vectors on N,
+// reads 6 KB of operands for each 32 cycles of products, where shared memory
+// delivers 128 B a cycle (48 cycles; 575 KB a step with the decoded stores, 4.5k
+// cycles); here the scores read 4 KB in 32 cycles and the context 6 KB in 64
+// (400 KB, 3.1k).  More vectors a CTA do not fit: 64 x 512 f32 of context are
+// half of a CTA's tensor memory.
 //
-// A bf16 query vector times a power of two of its own is exact in f16 (down to
-// 2^-24 of 2^14); the rotated query of TQ4 is rounded once, 2^-12 relative.
+// Codes become f16 operands in shared memory (e4m3 exactly, the 16 levels of
+// TQ4 times kGamma within 9.3e-5).  A bf16 query vector times a power of two of
+// its own is exact in f16 (down to 2^-24 of 2^14); the rotated query of TQ4 is
+// rounded once, 2^-12 relative.
 //
-// Step t: 16 worker warps store the step's codes chunk group by chunk group
-// (dims 0-255, 256-511, rope) as the context products of step t-1 release the
-// chunks; a 17th warp issues score products group by group behind
-// them, and the context products once the weights are written.  The next step's
-// codes are on their way to registers before the softmax.  16 warps, because a
-// step is a chain (store, score, softmax, context) and its links are as long as
-// a warp's share of them.
+// Roles (a CTA): 8 decode warps, 4 softmax warps, one issuing warp (in the first
+// CTA), one that announces segments.  The decode warps store the score rows of
+// step t+1 once the scores of step t are complete and the context rows of step t
+// once the context of step t-1 is; the scores of t+1 are issued before the
+// context of t.  So the tensor pipe alternates between the two while the other
+// operand is being stored and while the softmax of the step runs:
+//   tensor   S(t)   O(t-1)    S(t+1)    O(t)
+//   decode          K(t+1)    V(t)      K(t+2)  ...
+//   softmax         ---- P(t) ----      -- P(t+1) --
+// Accumulators: O 256 columns, S two buffers of 64 + 64.
 //
-// Softmax, per query vector, in log2 units: m is a lagged running maximum of the
-// scores, p = 2^(z - m) enters the row sum in f32, and the context takes the f16
-// weight w = p s_L E, E = 2^(m - R - 3) with R the largest z + log2 s_L of the
-// steps that set the references, so that weights are relative to the largest
-// p s_L and rows of small latent scale keep f16 precision where they matter.  A
-// score that passes m by more than 2^14, or a latent scale past 3.5 / max E,
-// sends the step down the exact path: column maxima, new m, R and E, O^T
-// rescaled in tensor memory.  Both limits keep w under the f16 maximum.
-// Rows that a vector does not see (causal end, vectors of shorter limits) get
+// Softmax, per query vector (a thread has one and half of the rows), in log2
+// units: m is a lagged running maximum of the scores, p = 2^(z - m) enters the
+// row sum in f32, and the context takes the f16 weight w = p s_L E,
+// E = 2^(m - R - 3) with R the largest z + log2 s_L of the steps that set the
+// references, so that weights are relative to the largest p s_L and rows of
+// small latent scale keep f16 precision where they matter.  A score that passes
+// m by more than 2^14, or a latent scale past 3.5 / E, sends the step down the
+// exact path: row maxima, new m, R and E, O rescaled in tensor memory.  Both
+// limits keep w under the f16 maximum.  Rows that a vector does not see get
 // z = -inf; a vector that has seen no row has m = -inf and E = 0.
 #include "tc_common.cuh"
 #include "paged_common.cuh"
@@ -43,133 +53,160 @@ namespace kvq {
 namespace {
 using namespace tc;
 
-constexpr int kRows = PagedTensor::kN;      // rows a step
-constexpr int kCols = PagedTensor::kM;      // query vectors
-constexpr int kWarps = 16;                  // worker warps
-constexpr int kWorkers = 32 * kWarps;
-constexpr int kThreads = kWorkers + 64;     // ... and the issuing and the walking warp: 112 registers a thread
-constexpr int kChunks = 9, kRope = 8;       // the rope chunk's slot holds P^T after the score
-constexpr uint32_t kSlotBytes = kRows * 128, kQChunkBytes = kCols * 128;
+constexpr int kRows = PagedTensor::kN;       // rows a step
+constexpr int kVecs = PagedTensor::kM;       // query vectors of the pair
+constexpr int kHalf = 64;                    // query vectors, and score rows, of a CTA
+static_assert(kRows == 2 * kHalf && kVecs == 2 * kHalf, "pair layout");
+constexpr int kSoftWarps = 4, kDecWarps = 8;
+constexpr int kSoft = 32 * kSoftWarps;
+constexpr int kIssueWarp = kSoftWarps + kDecWarps, kWalkWarp = kIssueWarp + 1;
+constexpr int kThreads = 32 * (kWalkWarp + 1);
+constexpr int kChunks = 9, kRope = 8;        // 64-dim chunks of a row: 8 latent, 1 rope
+constexpr uint32_t kChunkBytes = kHalf * 128;   // 64 rows (or vectors) x 64 f16
+constexpr uint32_t kVChunkBytes = kRows * 128;  // 128 rows x 64 f16
 constexpr uint32_t kOffQ = 0;
-constexpr uint32_t kOffSlot = kOffQ + kChunks * kQChunkBytes;
-constexpr uint32_t kOffM = kOffSlot + kChunks * kSlotBytes;
-constexpr uint32_t kOffR = kOffM + kCols * 4;
-constexpr uint32_t kOffE = kOffR + kCols * 4;
-constexpr uint32_t kOffF = kOffE + kCols * 4;          // 1 / E
-constexpr uint32_t kOffCz = kOffF + kCols * 4;         // score scale of a vector (sm log2 e / its query scale)
-constexpr uint32_t kOffAlpha = kOffCz + kCols * 4;     // O^T rescale; row sums and output factors at the end
-constexpr uint32_t kOffAlphaM = kOffAlpha + kCols * 4; // row-sum rescale
-constexpr uint32_t kOffLim = kOffAlphaM + kCols * 4;   // rows each vector sees
-constexpr uint32_t kOffRow = kOffLim + kCols * 4;      // pool rows of two steps
-constexpr uint32_t kOffRed = kOffRow + 2 * kRows * 4;  // 2 x 4 quadrants x 64 vectors
-constexpr uint32_t kOffBar = kOffRed + 2 * 4 * kCols * 4;
-constexpr uint32_t kOffLevels = kOffBar + 16 * 8;      // f16 levels as byte planes
-constexpr uint32_t kOffEmax = kOffLevels + 32;
-constexpr uint32_t kOffMisc = kOffEmax + 16;           // abort flag, TMEM base
-constexpr uint32_t kOffPart = kOffMisc + 16;           // scan of the work split
-constexpr uint32_t kOffWork = kOffPart + (kThreads / 32 + 2) * 8;   // two segments, announced one ahead
-constexpr uint32_t kSmemUsed = kOffWork + 2 * 64;
-static_assert(kOffSlot % 1024 == 0 && kOffPart % 8 == 0, "alignment");
+constexpr uint32_t kOffK = kOffQ + kChunks * kChunkBytes;
+constexpr uint32_t kOffV = kOffK + kChunks * kChunkBytes;   // 4 chunks: dims 256 j + 128 rank + 64 i
+constexpr uint32_t kOffP = kOffV + 4 * kVChunkBytes;        // weights: 2 chunks of 64 rows
+constexpr uint32_t kOffScale = kOffP + 2 * kChunkBytes;     // (s_L, s_R) of two steps' rows
+constexpr uint32_t kScaleBytes = kRows * 8;
+constexpr uint32_t kOffCz = kOffScale + 2 * kScaleBytes;    // score scale of a vector, two segments
+constexpr uint32_t kOffBar = kOffCz + 2 * kHalf * 4;
+constexpr uint32_t kOffMax = kOffBar + 20 * 8;              // largest s_L of two steps by warp
+constexpr uint32_t kOffLevels = kOffMax + 2 * kSoftWarps * 4;
+constexpr uint32_t kOffMisc = kOffLevels + 32;              // abort flag, TMEM base
+constexpr uint32_t kOffWork = kOffMisc + 16;                // two segments, announced one ahead
+constexpr uint32_t kSmemUsed = kOffWork + 2 * 72;
+constexpr uint32_t kOffPart = kOffScale;                    // scan of the work split, before the steps
+static_assert((kThreads / 32 + 2) * 8 <= 2 * kScaleBytes, "scan scratch");
+static_assert(kOffK % 1024 == 0 && kOffV % 1024 == 0 && kOffP % 1024 == 0 && kOffWork % 8 == 0, "alignment");
 static_assert(kSmemUsed <= 232448, "shared memory budget");
-constexpr int kStageStride = 516;           // floats between staged output vectors
-static_assert(kCols * kStageStride * 4 <= kChunks * kSlotBytes, "output stage");
+static_assert(32 * kMlaDV * 4 <= 4 * kVChunkBytes, "output stage");
 
-constexpr uint32_t kColO = 0, kColSL = 256, kColSR = 320, kTmemCols = 512;
+constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 
-// mbarriers: chunk group stored (16 warps), chunk pair released by the context
-// products, scores complete, weights written (16 warps), all products complete,
-// one that nothing arrives on (the testing hook's stall), segment announced,
-// segment done with (16 warps and the issuing thread)
+// mbarriers.  In the first CTA, arrivals from both: score rows stored (chunks
+// 0-3, 4-7, rope), context rows stored (rows 0-63, 64-127), weights written.  In
+// each CTA: scores complete (by buffer; commits reach both CTAs), context complete
+// (by row half), segment announced, segment done with, queries stored, output written,
+// every product complete, and one that nothing arrives on (the testing hook).
 enum {
-    kBarFull0 = 0, kBarFree0 = 3, kBarScore = 7, kBarP = 8, kBarDone = 9, kBarNever = 10, kBarWork0 = 11,
-    kBarWorkFree0 = 13, kNumBars = 15
+    kBarK0 = 0, kBarV0 = 3, kBarP = 5, kBarScore0 = 6, kBarCtx0 = 8, kBarWork0 = 10, kBarWorkFree0 = 12, kBarQ0 = 14,
+    kBarOut = 16, kBarDone = 17, kBarNever = 18, kNumBars = 19
 };
-
-// A segment as the workers use it; steps = 0 ends the walk.
-struct Work {
-    int32_t steps, b, rows;
-    int32_t first, end, seen0;   // first row; rows that some vector sees; rows that the first one sees
-    int64_t row0, tok0, base, slot, parts;
-};
-static_assert(sizeof(Work) <= 64, "segment record");
+// Scores, announcements and queries have two barriers each, used in turn: their
+// next but one event waits for whoever waits for this one, the next does not.
 
 constexpr float kLagLog2 = 14.0f, kScaleLim = 3.5f, kHeadroom = 3.0f, kLogEmax = 120.0f;
 // levels times this round to f16 within 9.3e-5 (unscaled: 3.2e-4); divided out in f32
 constexpr float kGamma = 1.3338516f;
-constexpr uint32_t kIdescScore = idesc_f16(128, kCols, false, false);
-constexpr uint32_t kIdescCtx = idesc_f16(128, kCols, true, true);
+constexpr uint32_t kIdescScore = idesc_f16(kVecs, kRows, false, false);
+constexpr uint32_t kIdescCtx = idesc_f16(kVecs, 256, false, true);
 
-// ---- a worker's raw share of a step -------------------------------------------
-// KV8, groups of 256 bytes a row: 4 pieces of 16 bytes, piece i at row
-// 2 (warp + 16 i) + (lane / 4) % 2, bytes 64 (lane / 8) + 16 (lane % 4): a warp
-// reads two whole runs of 256 bytes, and the 8 lanes that a shared store serves
-// at a time write one chunk of two adjacent rows, 8 different 16-byte units.
-// Rope: one piece, row tid / 4, bytes 16 (tid % 4).
-// TQ4, groups of 128 bytes a row: 2 pieces, piece i at row 8 warp + lane % 8,
-// bytes 64 i + 16 (lane / 8): 8 lanes store one unit of 8 rows, whose swizzle
-// phases differ.  Rope (32 bytes): warps 0-7, row 16 warp + lane % 8 +
-// 8 (lane / 16), bytes 16 ((lane / 8) % 2).
+// A segment as the roles use it; steps = 0 ends the walk.
+struct Work {
+    int32_t steps, b, rows;
+    int32_t first, end, seen0;   // first row; rows that some vector sees; rows that the first one sees
+    int64_t row0, tok0, base, slot;
+    int32_t parts, pad;
+};
+static_assert(sizeof(Work) <= 72, "segment record");
+
+// ---- pair-wide barriers and MMAs ----------------------------------------------
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Bounded wait, as mbar_wait, that also sees what the other CTA's arrivals release.
+__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
+    if (*abort_flag) return false;
+    const uint32_t a = smem_u32(bar);
+    for (long long i = 0; i < limit; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(a), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((i & 63) == 63 && *abort_flag) return false;
+    }
+    *abort_flag = 1;
+    return false;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
+    return __all_sync(kFull, pair_wait(bar, parity, abort_flag, limit));
+}
+// One arrival of a warp on a barrier of its own CTA, or of the first CTA.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ void warp_arrive_first(uint64_t* bar, int lane) {
+    __syncwarp();
+    if (lane == 0) {
+        uint32_t a;
+        asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
+    }
+}
+// One MMA, or one commit, of a whole warp in step: the warp computes the
+// descriptors together (in uniform registers) and one elected lane, always the
+// same, issues.  A lone lane in a branch of its own spends about 115 cycles an
+// MMA on moving its operands, more than the MMA takes.
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n .reg .b16 m;\n mov.b16 m, 3;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}\n" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+
+// ---- decode -------------------------------------------------------------------
+// 16 codes: a quarter of a row's 64-dim chunk.  Four lanes read a chunk (64 or 32
+// contiguous bytes) and store its 128 bytes; the 8 lanes that a shared store
+// serves at a time cover two rows whose swizzle phases differ in the low bit,
+// 8 different 16-byte units.
 template <bool TQ4>
-struct Raw {
-    static constexpr int kPer = TQ4 ? 2 : 4;
-    uint4 a[kPer], b[kPer], c;
+struct PieceOf {
+    using type = uint4;
+};
+template <>
+struct PieceOf<true> {
+    using type = uint2;
 };
 template <bool TQ4>
-__device__ __forceinline__ int piece_row(int i, int warp, int lane) {
-    return TQ4 ? 8 * warp + (lane & 7) : 2 * (warp + 16 * i) + ((lane >> 2) & 1);
-}
-template <bool TQ4>
-__device__ __forceinline__ int piece_byte(int i, int lane) {
-    return TQ4 ? 64 * i + 16 * (lane >> 3) : 64 * (lane >> 3) + 16 * (lane & 3);
-}
-template <bool TQ4>
-__device__ __forceinline__ int rope_row(int tid, int warp, int lane) {
-    return TQ4 ? 16 * warp + (lane & 7) + 8 * (lane >> 4) : tid >> 2;
-}
-template <bool TQ4>
-__device__ __forceinline__ int rope_byte(int tid, int lane) {
-    return TQ4 ? 16 * ((lane >> 3) & 1) : 16 * (tid & 3);
-}
-template <bool TQ4>
-__device__ __forceinline__ void load_raw(Raw<TQ4>& r, const uint8_t* __restrict__ codes, const int32_t* prow, int nt,
-                                         int tid, int warp, int lane) {
-    constexpr int kRow = TQ4 ? kMlaD / 2 : kMlaD, kGroup = TQ4 ? 128 : 256;
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-    for (int i = 0; i < Raw<TQ4>::kPer; ++i) {
-        const int row = piece_row<TQ4>(i, warp, lane);
-        const uint8_t* src = codes + (int64_t)prow[row] * kRow + piece_byte<TQ4>(i, lane);
-        r.a[i] = row < nt ? __ldg(reinterpret_cast<const uint4*>(src)) : z;
-        r.b[i] = row < nt ? __ldg(reinterpret_cast<const uint4*>(src + kGroup)) : z;
-    }
-    r.c = z;
-    if (!TQ4 || warp < 8) {
-        const int row = rope_row<TQ4>(tid, warp, lane);
-        if (row < nt)
-            r.c = __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)prow[row] * kRow + 2 * kGroup +
-                                                       rope_byte<TQ4>(tid, lane)));
-    }
-}
+using Piece = typename PieceOf<TQ4>::type;
 
-// 16 e4m3 codes -> 16 f16 at byte offset b of swizzled row `row`.
-__device__ __forceinline__ void store_kv8(unsigned char* slot, const uint4& c, int row, int b) {
+// f16 levels as byte planes, four levels a word
+struct Planes {
+    uint32_t lo[4], hi[4];
+};
+__device__ __forceinline__ void store_piece(unsigned char* chunk, const uint4& c, int row, int q, const Planes&) {
     const uint32_t in[4] = {c.x, c.y, c.z, c.w};
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) e4m3x4_to_half2x2(in[i], w[2 * i], w[2 * i + 1]);
-    *reinterpret_cast<uint4*>(slot + sw128(row, b)) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4*>(slot + sw128(row, b + 16)) = make_uint4(w[4], w[5], w[6], w[7]);
+    *reinterpret_cast<uint4*>(chunk + sw128(row, 32 * q)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(chunk + sw128(row, 32 * q + 16)) = make_uint4(w[4], w[5], w[6], w[7]);
 }
-// 32 nibble codes -> 32 f16 levels (64 bytes) by byte permutes over the low and
-// the high bytes of the levels: the low 3 bits of a code pick among levels 0-7
-// and 8-15, bit 3 between the two.
-struct Planes {
-    uint32_t lo[4], hi[4];
-};
-__device__ __forceinline__ void store_tq4(unsigned char* slot, const uint4& c, int row, int b, const Planes& t) {
-    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+// Nibble codes by byte permutes over the low and the high bytes of the levels:
+// the low 3 bits of a code pick among levels 0-7 and 8-15, bit 3 between the two.
+__device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c, int row, int q, const Planes& t) {
+    const uint32_t in[2] = {c.x, c.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         const uint32_t sel = in[i] & 0x77777777u, pick = ((in[i] >> 1) & 0x44444444u) | 0x32103210u;
         uint32_t w[4];
 #pragma unroll
@@ -180,62 +217,27 @@ __device__ __forceinline__ void store_tq4(unsigned char* slot, const uint4& c, i
             w[2 * h] = __byte_perm(lo, hi, 0x5140u);
             w[2 * h + 1] = __byte_perm(lo, hi, 0x7362u);
         }
-        *reinterpret_cast<uint4*>(slot + sw128(row, b + 16 * i)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(chunk + sw128(row, 32 * q + 16 * i)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-}
-template <bool TQ4>
-__device__ __forceinline__ void store_group(unsigned char* sSlot, const uint4 (&v)[Raw<TQ4>::kPer], int g, int warp,
-                                            int lane, const Planes& t) {
-#pragma unroll
-    for (int i = 0; i < Raw<TQ4>::kPer; ++i) {
-        const int row = piece_row<TQ4>(i, warp, lane), byte = piece_byte<TQ4>(i, lane);
-        if (TQ4) store_tq4(sSlot + (4 * g + (byte >> 5)) * kSlotBytes, v[i], row, 4 * (byte & 31), t);
-        else store_kv8(sSlot + (4 * g + (byte >> 6)) * kSlotBytes, v[i], row, 2 * (byte & 63));
-    }
-}
-
-// One MMA, or one commit, of a whole warp in step: the warp computes the
-// descriptors together (in uniform registers) and one elected lane, always the
-// same, issues.  A lone lane in a branch of its own spends about 115 cycles an
-// MMA on moving its operands; this way N = 64 runs at the 48 cycles that its 6 KB
-// of operands take to read.
-__device__ __forceinline__ void umma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc));
-}
-__device__ __forceinline__ void commit_one(uint64_t* bar) {
-    asm volatile(
-        "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
-    return __all_sync(kFull, mbar_wait(bar, parity, abort_flag, limit));
-}
-
-__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
 }
 
 // ---- queries ------------------------------------------------------------------
-// Four vectors a warp: to f16 under a power of two that puts the largest element
-// in [2^13, 2^14); sCz gets what undoes it in the score.
+// This CTA's 64 vectors, 8 a decode warp: to f16 under a power of two that puts
+// the largest element in [2^13, 2^14); sCz gets what undoes it in the score.
 template <bool TQ4>
-__device__ __forceinline__ void load_queries(const PagedParams& p, const Work& g, unsigned char* sQ, float* sCz,
-                                             int warp, int lane) {
+__device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0, int rows, unsigned char* sQ,
+                                             float* sCz, int warp, int lane) {
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
-#pragma unroll 1
-    for (int k = 0; k < kCols / kWarps; ++k) {
-        const int r = (kCols / kWarps) * warp + k;
+    constexpr int kPer = kHalf / kDecWarps;
+#pragma unroll 2
+    for (int k = 0; k < kPer; ++k) {
+        const int r = kPer * warp + k;
         float v[18];
-        const int64_t at = (g.row0 + r) * kMlaD;
+        const int64_t at = (row0 + r) * kMlaD;
         if (TQ4) {
             // element lane + 32 i
 #pragma unroll
-            for (int i = 0; i < 18; ++i) v[i] = r < g.rows ? __bfloat162float(q[at + lane + 32 * i]) : 0.0f;
+            for (int i = 0; i < 18; ++i) v[i] = r < rows ? __bfloat162float(q[at + lane + 32 * i]) : 0.0f;
             float rot[16], rope[2];
 #pragma unroll
             for (int i = 0; i < 16; ++i) rot[i] = sign_neg(p.signs, 0, lane + 32 * i) ? -v[i] : v[i];
@@ -252,7 +254,7 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, const Work& g
             const uint32_t* qw = reinterpret_cast<const uint32_t*>(q + at);
 #pragma unroll
             for (int i = 0; i < 9; ++i) {
-                const uint32_t w = r < g.rows ? __ldg(qw + lane + 32 * i) : 0u;
+                const uint32_t w = r < rows ? __ldg(qw + lane + 32 * i) : 0u;
                 v[2 * i] = __uint_as_float(w << 16);
                 v[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
             }
@@ -270,164 +272,62 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, const Work& g
 #pragma unroll
             for (int i = 0; i < 18; ++i) {
                 const int d = lane + 32 * i;
-                *reinterpret_cast<__half*>(sQ + (d >> 6) * kQChunkBytes + sw128(r, (d & 63) * 2)) =
+                *reinterpret_cast<__half*>(sQ + (d >> 6) * kChunkBytes + sw128(r, (d & 63) * 2)) =
                     __float2half_rn(v[i] * scale);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 9; ++i)
-                *reinterpret_cast<__half2*>(sQ + i * kQChunkBytes + sw128(r, lane * 4)) =
+                *reinterpret_cast<__half2*>(sQ + i * kChunkBytes + sw128(r, lane * 4)) =
                     __floats2half2_rn(v[2 * i] * scale, v[2 * i + 1] * scale);
         }
     }
 }
 
-// One thread's row of scores: 16 vectors, d = z - m (sub = their m) or z itself.
-struct RowView {
-    uint32_t tmem;     // lane base + first column of the 16
-    float sl, sr;      // row scales
-    int32_t t;         // row within the sequence
-    bool ok, mask;     // row within the step; some vector of the tile does not see the step's end
+// A query vector's softmax state.
+struct RowState {
+    float m, R, E, logE, l;
+    bool none;   // rows seen, but none with a latent scale yet
 };
-__device__ __forceinline__ void load_scores(const RowView& v, const float* cz, const float* sub, const int32_t* lim,
-                                            float (&z)[16]) {
-    uint32_t l[16], r[16];
-    tmem_ld16(v.tmem + kColSR, r);
-    tmem_ld16(v.tmem + kColSL, l);
-    tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 c = *reinterpret_cast<const float4*>(cz + 4 * i);
-        const float4 m = sub ? *reinterpret_cast<const float4*>(sub + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float cv[4] = {c.x, c.y, c.z, c.w}, mv[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int j = 4 * i + k;
-            const float s = fmaf(__uint_as_float(l[j]), v.sl, __uint_as_float(r[j]) * v.sr);
-            z[j] = v.ok ? fmaf(s, cv[k], -mv[k]) : -INFINITY;
-        }
-    }
-    if (v.mask) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (v.t >= lim[j]) z[j] = -INFINITY;
-    }
-}
-
-// The exact path of a step, by every worker (out of line: rare).
-__device__ __noinline__ void exact_path(unsigned char* sm, uint32_t tmem, RowView view, int hq, int lane, int warp,
-                                        int tid, bool first, uint32_t* exact_count) {
-    float* sM = reinterpret_cast<float*>(sm + kOffM);
-    float* sR = reinterpret_cast<float*>(sm + kOffR);
-    float* sAlpha = reinterpret_cast<float*>(sm + kOffAlpha);
-    float* sRed = reinterpret_cast<float*>(sm + kOffRed);
-    const float* cz = reinterpret_cast<const float*>(sm + kOffCz) + 16 * hq;
-    const int32_t* lim = reinterpret_cast<const int32_t*>(sm + kOffLim) + 16 * hq;
-    {
-        float z[16];
-        const int at = (warp & 3) * kCols + 16 * hq + (lane & 15);
-        load_scores(view, cz, nullptr, lim, z);
-        float top = warp_columns16<true>(z, lane);
-        if (lane < 16) sRed[at] = top;
-        load_scores(view, cz, nullptr, lim, z);
-        const float add = view.sl > 0.0f ? __log2f(view.sl) : -INFINITY;   // -inf: an inert latent block
-#pragma unroll
-        for (int j = 0; j < 16; ++j) z[j] += add;
-        top = warp_columns16<true>(z, lane);
-        if (lane < 16) sRed[4 * kCols + at] = top;
-    }
-    worker_sync<kWorkers>();
-    if (tid < kCols) {
-        const float* ry = sRed + 4 * kCols;
-        const float c4 = fmaxf(fmaxf(sRed[tid], sRed[kCols + tid]), fmaxf(sRed[2 * kCols + tid], sRed[3 * kCols + tid]));
-        const float y4 = fmaxf(fmaxf(ry[tid], ry[kCols + tid]), fmaxf(ry[2 * kCols + tid], ry[3 * kCols + tid]));
-        const float mo = sM[tid], mn = fmaxf(mo, c4);
-        const float ro = sR[tid], rn = fmaxf(ro, y4);
-        const float dn = fminf(mn - rn - kHeadroom, kLogEmax), d_old = fminf(mo - ro - kHeadroom, kLogEmax);
-        reinterpret_cast<float*>(sm + kOffAlphaM)[tid] = mo == -INFINITY ? 0.0f : ex2(mo - mn);
-        // O^T holds sum p s_L E c: rescaled by (E_new / E_old) 2^(m_old - m_new)
-        sAlpha[tid] = ro == -INFINITY ? 0.0f : ex2(dn - d_old + (mo - mn));
-        sM[tid] = mn;
-        sR[tid] = rn;
-        // no latent scale met yet: E = 0, and the next one takes this path (max E
-        // infinite); no row seen at all: the first score takes it by m = -inf
-        const bool none = rn == -INFINITY;
-        const float e = none ? 0.0f : ex2(dn);
-        reinterpret_cast<float*>(sm + kOffE)[tid] = e;
-        reinterpret_cast<float*>(sm + kOffF)[tid] = none ? 0.0f : ex2(-dn);
-        const float em = warp_max(mn == -INFINITY ? 0.0f : none ? INFINITY : e);
-        if (lane == 0) reinterpret_cast<float*>(sm + kOffEmax)[tid >> 5] = em;
-        if (!first && tid == 0) atomicAdd(exact_count, 1u);
-    }
-    worker_sync<kWorkers>();
-    if (!first) {
-        // every context product so far is complete: the score commit of this
-        // step follows them
-        const uint32_t ta = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColO + 64 * hq;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-            uint32_t o[16];
-            tmem_ld16(ta + 16 * c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sAlpha[16 * c + j]);
-            tmem_st16(ta + 16 * c, o);
-        }
-        tmem_wait_st();
-    }
-}
 
 template <bool TQ4>
-__global__ void __launch_bounds__(kThreads, 1) paged_tensor_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    paged_tensor_kernel(const __grid_constant__ PagedParams p) {
     launch_dependents();
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char* sm = smem_raw;
-    unsigned char* sQ = sm + kOffQ;
-    unsigned char* sSlot = sm + kOffSlot;
-    unsigned char* sP = sSlot + kRope * kSlotBytes;
-    float* sM = reinterpret_cast<float*>(sm + kOffM);
-    float* sR = reinterpret_cast<float*>(sm + kOffR);
-    float* sE = reinterpret_cast<float*>(sm + kOffE);
-    float* sF = reinterpret_cast<float*>(sm + kOffF);
-    float* sCz = reinterpret_cast<float*>(sm + kOffCz);
-    float* sAlpha = reinterpret_cast<float*>(sm + kOffAlpha);
-    float* sAlphaM = reinterpret_cast<float*>(sm + kOffAlphaM);
-    int32_t* sLim = reinterpret_cast<int32_t*>(sm + kOffLim);
-    int32_t* sRow = reinterpret_cast<int32_t*>(sm + kOffRow);
-    float* sRed = reinterpret_cast<float*>(sm + kOffRed);
+    extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
-    unsigned char* sLevels = sm + kOffLevels;
-    float* sEmax = reinterpret_cast<float*>(sm + kOffEmax);
     volatile int* sAbort = reinterpret_cast<volatile int*>(sm + kOffMisc);
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + kOffMisc + 4);
-    int64_t* sPart = reinterpret_cast<int64_t*>(sm + kOffPart);
     Work* sWork = reinterpret_cast<Work*>(sm + kOffWork);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
-    const int64_t cta = blockIdx.x;
+    const int rank = (int)cta_rank();
+    const int64_t pair = blockIdx.x >> 1;
     const int64_t wl = p.wait_limit;
-    if (tid < 4) p.ws_desc[cta * 4 + tid] = 0;
+    if (rank == 0 && tid < 4) p.ws_desc[pair * 4 + tid] = 0;
     PagedWalk<PagedTensor> walk;
-    if (!walk.template start<kThreads>(p, cta, gridDim.x, sPart)) return;
-    if (smem_u32(smem_raw) & 1023u) {   // the swizzled operands would be misread
-        if (tid == 0) set_err(p.err, KVQ_ERR_DEVICE);
-        return;
-    }
+    // the same answer in both CTAs
+    if (!walk.template start<kThreads>(p, pair, gridDim.x >> 1, reinterpret_cast<int64_t*>(sm + kOffPart))) return;
+    const bool aligned = (smem_u32(sm) & 1023u) == 0;   // else the swizzled operands would be misread
 
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sTmem)),
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sTmem)),
                      "r"(kTmemCols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     if (tid == 64) {
         for (int i = 0; i < kNumBars; ++i) {
-            const uint32_t count = (i < kBarFree0 || i == kBarP) ? (uint32_t)kWarps
-                                   : i >= kBarWorkFree0          ? (uint32_t)kWarps + 1u
-                                                                 : 1u;
+            const uint32_t count = i < kBarP          ? 2u * kDecWarps
+                                   : i == kBarP       ? 2u * kSoftWarps
+                                   : (i == kBarQ0 || i == kBarQ0 + 1) ? (uint32_t)kDecWarps
+                                   : i == kBarOut     ? (uint32_t)kSoftWarps
+                                   : (i == kBarWorkFree0 || i == kBarWorkFree0 + 1)
+                                       ? (uint32_t)(kSoftWarps + kDecWarps + (rank == 0 ? 1 : 0))
+                                       : 1u;
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&bars[i])), "r"(count));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        *sAbort = 0;
+        *sAbort = aligned ? 0 : 1;
     }
     if (TQ4 && tid == 0) {
         uint32_t lo[4] = {0u, 0u, 0u, 0u}, hi[4] = {0u, 0u, 0u, 0u};
@@ -437,24 +337,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tensor_kernel(const __grid_
             lo[k >> 2] |= (h & 0xffu) << (8 * (k & 3));
             hi[k >> 2] |= (h >> 8) << (8 * (k & 3));
         }
-        *reinterpret_cast<uint4*>(sLevels) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<uint4*>(sLevels + 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(sm + kOffLevels) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(sm + kOffLevels + 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     }
     tc_before();
     __syncthreads();
+    cluster_sync();   // the other CTA's barriers are there, its tensor memory is allocated
     tc_after();
     const uint32_t tmem = *sTmem;
 
-    if (warp >= kWarps) {
+    if (warp == kWalkWarp) {
         // ================= the walk: announces segments one ahead =================
-        if (warp == kWarps + 1 && lane == 0) {
+        if (lane == 0) {
             bool more = true;
             for (int n = 0; more; ++n, walk.next(p)) {
-                if (n >= 2 && !mbar_wait(&bars[kBarWorkFree0 + (n & 1)], (uint32_t)(n / 2 - 1) & 1u, sAbort, wl)) break;
+                if (n >= 2 && !pair_wait(&bars[kBarWorkFree0 + (n & 1)], (uint32_t)(n / 2 - 1) & 1u, sAbort, wl)) break;
                 Segment g;
                 Work w{};
                 more = walk.get(p, g);
                 if (more) {
+                    int64_t parts;
                     w.steps = (int32_t)(g.u1 - g.u0);
                     w.b = g.b;
                     w.rows = g.rows;
@@ -464,294 +366,462 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tensor_kernel(const __grid_
                     w.row0 = g.row0;
                     w.tok0 = g.tok0;
                     w.base = g.base;
-                    w.slot = walk.slot(g, cta, &w.parts);
+                    w.slot = walk.slot(g, pair, &parts);
+                    w.parts = (int32_t)parts;
                 }
                 sWork[n & 1] = w;
                 mbar_arrive(&bars[kBarWork0 + (n & 1)]);
             }
         }
-        // ================= the issuing warp =================
-        if (warp == kWarps) {
-            const uint64_t dq0 = umma_desc(smem_u32(sQ), 16, 1024);
-            const uint64_t dslot0 = umma_desc(smem_u32(sSlot), 16, 1024);
-            const uint64_t dpair0 = umma_desc(smem_u32(sSlot), kSlotBytes, 1024);
-            const uint64_t dp = umma_desc(smem_u32(sP), kSlotBytes, 1024);
-            constexpr uint64_t kQStep = kQChunkBytes >> 4, kSlotStep = kSlotBytes >> 4;
+    } else if (warp == kIssueWarp) {
+        // ================= products (first CTA) =================
+        if (rank == 0) {
+            const uint64_t dq = umma_desc(smem_u32(sm + kOffQ), 16, 1024);
+            const uint64_t dk = umma_desc(smem_u32(sm + kOffK), 16, 1024);
+            const uint64_t dv = umma_desc(smem_u32(sm + kOffV), kVChunkBytes, 1024);
+            const uint64_t dp = umma_desc(smem_u32(sm + kOffP), 16, 1024);
+            constexpr uint64_t kStep = kChunkBytes >> 4, kVStep = kVChunkBytes >> 4;
             bool ok = true;
             if (p.stall_polls > 0) ok = warp_wait(&bars[kBarNever], 0u, sAbort, p.stall_polls);
-            uint32_t it = 0;
+            auto scores = [&](uint32_t it) {
+                const uint32_t d = tmem + kColS + 128 * (it & 1u);
+#pragma unroll
+                for (int gr = 0; gr < 3; ++gr) {
+                    if (!warp_wait(&bars[kBarK0 + gr], it & 1u, sAbort, wl)) return false;
+                    tc_after();
+#pragma unroll
+                    for (int kc = 4 * gr; kc < (gr < 2 ? 4 * gr + 4 : kChunks); ++kc)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            pair_mma(d + (kc < kRope ? 0 : 64), dq + kc * kStep + 2 * ks, dk + kc * kStep + 2 * ks,
+                                     kIdescScore, ((kc == 0 || kc == kRope) && ks == 0) ? 0u : 1u);
+                }
+                pair_commit(&bars[kBarScore0 + (it & 1u)]);
+                return true;
+            };
+            uint32_t it = 0;   // step of the whole walk
             for (int n = 0; ok; ++n) {
                 ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl);
                 if (!ok) break;
                 const int steps = __shfl_sync(kFull, sWork[n & 1].steps, 0);
-                if (steps == 0) break;
                 warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
+                if (steps == 0) break;
+                ok = scores(it);
                 for (int t = 0; t < steps && ok; ++t, ++it) {
-                    const uint32_t par = it & 1u;
+                    // the other score buffer is free: its weights were written before the last context
+                    if (t + 1 < steps && !(ok = scores(it + 1))) break;
+                    ok = warp_wait(&bars[kBarP], it & 1u, sAbort, wl);
+                    if (!ok) break;
 #pragma unroll
-                    for (int gr = 0; gr < 3; ++gr) {
-                        ok = ok && warp_wait(&bars[kBarFull0 + gr], par, sAbort, wl);
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && warp_wait(&bars[kBarV0 + h], it & 1u, sAbort, wl);
                         if (!ok) break;
                         tc_after();
 #pragma unroll
-                        for (int kc = 4 * gr; kc < (gr < 2 ? 4 * gr + 4 : kChunks); ++kc)
+                        for (int j = 0; j < 2; ++j)
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                umma_one(tmem + (kc < kRope ? kColSL : kColSR), dslot0 + kc * kSlotStep + 2 * ks,
-                                         dq0 + kc * kQStep + 2 * ks, kIdescScore,
-                                         ((kc == 0 || kc == kRope) && ks == 0) ? 0u : 1u);
-                    }
-                    commit_one(&bars[kBarScore]);
-                    ok = ok && warp_wait(&bars[kBarP], par, sAbort, wl);
-                    if (!ok) break;
-                    tc_after();
-#pragma unroll
-                    for (int db = 0; db < 4; ++db) {
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            umma_one(tmem + kColO + 64 * db, dpair0 + 2 * db * kSlotStep + 128 * ks, dp + 128 * ks,
-                                     kIdescCtx, (t > 0 || ks > 0) ? 1u : 0u);
-                        commit_one(&bars[kBarFree0 + db]);
+                                pair_mma(tmem + kColO + 128 * j, dp + h * kStep + 2 * ks,
+                                         dv + 2 * j * kVStep + (4 * h + ks) * 128, kIdescCtx,
+                                         (t > 0 || h > 0 || ks > 0) ? 1u : 0u);
+                        pair_commit(&bars[kBarCtx0 + h]);
                     }
                 }
             }
-            commit_one(&bars[kBarDone]);
+            __syncwarp();
+            pair_commit(&bars[kBarDone]);
         }
-        return;
-    }
-
-    // ================= workers =================
-    const int srow = 32 * (warp & 3) + lane;   // softmax: this thread's row (TMEM lane)
-    const int hq = warp >> 2;                   // ... and vectors 16 hq .. 16 hq + 15
-    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    uint32_t it = 0;
-    bool aborted = false;
-    for (int n = 0;; ++n) {
-        if (!mbar_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl)) aborted = true;
-        if (worker_any<kWorkers>(aborted)) {
-            aborted = true;
-            break;
+    } else if (warp >= kSoftWarps) {
+        // ================= decode warps =================
+        using P = Piece<TQ4>;
+        constexpr int kRowBytes = TQ4 ? kMlaD / 2 : kMlaD, kQuarter = sizeof(P);
+        const int dw = warp - kSoftWarps, dt = tid - kSoft, drow = dt >> 2, dq4 = dt & 3;
+        Planes pl{};
+        if (TQ4) {
+            const uint4 a = *reinterpret_cast<const uint4*>(sm + kOffLevels);
+            const uint4 b = *reinterpret_cast<const uint4*>(sm + kOffLevels + 16);
+            pl = Planes{{a.x, a.y, a.z, a.w}, {b.x, b.y, b.z, b.w}};
         }
-        const Work& g = sWork[n & 1];
-        const int steps = g.steps;
-        if (steps == 0) break;
-        // ---- prologue: state, limits, queries, the first step's rows ----
-        const int32_t first = g.first, end = g.end;
-        // a row of step t (tid < kRows): its page is asked for early, and turned
-        // into a pool row where it is stored; rows past the end get row 0, never read
-        const int32_t* table = p.table + (int64_t)g.b * p.table_stride;
-        auto page_of = [&](int t) -> int32_t {
-            const int32_t r = first + t * kRows + tid;
-            return (tid < kRows && t < steps && r < end) ? __ldg(table + (r >> p.shift)) : 0;
-        };
-        auto set_row = [&](int t, int32_t id) {
-            if (tid >= kRows) return;
-            if (id < 0 || id >= p.n_pages) {
-                set_err(p.err, KVQ_ERR_ARG);
-                id = 0;
-            }
-            const int32_t r = first + t * kRows + tid;
-            sRow[(t & 1) * kRows + tid] = (id << p.shift) + (r & ((1 << p.shift) - 1));
-        };
-        auto rows_in = [&](int t) { return max(0, min(kRows, end - first - t * kRows)); };
-        {
-            const int32_t id0 = page_of(0), id1 = page_of(1);
-            set_row(0, id0);
-            set_row(1, id1);
-        }
-        if (tid < kCols) {
-            sM[tid] = -INFINITY;
-            sR[tid] = -INFINITY;
-            sE[tid] = 0.0f;
-            sF[tid] = 0.0f;
-            // vectors past the tile's last repeat its limit: they score 0 and are dropped
-            sLim[tid] = (int32_t)max((int64_t)0, g.base + 1 + (g.tok0 + min(tid, g.rows - 1)) / p.n_heads);
-            if (tid < kCols / 32) sEmax[tid] = 0.0f;
-        }
-        load_queries<TQ4>(p, g, sQ, sCz, warp, lane);
-        fence_async_smem();
-        worker_sync<kWorkers>();
-        float lsum[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) lsum[j] = 0.0f;
-        Raw<TQ4> raw;
-        float sl_next = 0.0f, sr_next = 0.0f;
-        auto request = [&](int t) {   // codes and scales of step t
-            const int32_t* rows = sRow + (t & 1) * kRows;
-            const int nt = rows_in(t);
-            load_raw<TQ4>(raw, p.codes, rows, nt, tid, warp, lane);
-            sl_next = sr_next = 0.0f;
-            if (srow < nt) {
-                const float* s = p.scales + (int64_t)rows[srow] * p.n_blocks;
-                sl_next = s[0];
-                sr_next = s[p.n_blocks - 1];
-            }
-        };
-        request(0);
-        int t = 0;
-        for (; t < steps; ++t, ++it) {
-            const uint32_t par = it & 1u, prev = par ^ 1u;
-            const int32_t page2 = page_of(t + 2);
-            const RowView view{tmem + lane_base + 16 * hq, sl_next, sr_next, first + t * kRows + srow,
-                               srow < rows_in(t), first + (t + 1) * kRows > g.seen0};
-            // ---- decode: dims 0-255, 256-511, rope ----
-            {
-                Planes pl;
-                if (TQ4) {
-                    const uint4 a = *reinterpret_cast<const uint4*>(sLevels), b = *reinterpret_cast<const uint4*>(sLevels + 16);
-                    pl = Planes{{a.x, a.y, a.z, a.w}, {b.x, b.y, b.z, b.w}};
+        uint32_t it = 0;
+        bool ok = true;
+        auto score_done = [&](uint32_t s) { return warp_wait(&bars[kBarScore0 + (s & 1u)], (s >> 1) & 1u, sAbort, wl); };
+        for (int n = 0; ok; ++n) {
+            if (!(ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl))) break;
+            const Work w = sWork[n & 1];
+            warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
+            if (w.steps == 0) break;
+            const int32_t* table = p.table + (int64_t)w.b * p.table_stride;
+            // this thread's two rows of a step: the one it supplies to the
+            // scores, and the other CTA's at the same place.  Pages are asked
+            // for a step before the codes, the codes a step before their use.
+            const int32_t own0 = w.first + kHalf * rank + drow, peer0 = w.first + kHalf * (1 - rank) + drow;
+            int32_t id_own = 0, id_peer = 0;
+            auto ask = [&](int t) {
+                const int32_t a = own0 + t * kRows, b = peer0 + t * kRows;
+                id_own = t < w.steps && a < w.end ? __ldg(table + (a >> p.shift)) : 0;
+                id_peer = t < w.steps && b < w.end ? __ldg(table + (b >> p.shift)) : 0;
+            };
+            auto code_row = [&](int32_t r, int32_t id) -> const uint8_t* {
+                if (r >= w.end) return nullptr;
+                if (id < 0 || id >= p.n_pages) {
+                    set_err(p.err, KVQ_ERR_ARG);
+                    id = 0;
                 }
+                const int64_t row = ((int64_t)id << p.shift) + (r & ((1 << p.shift) - 1));
+                return p.codes + row * kRowBytes + kQuarter * dq4;
+            };
+            P raw[kChunks], next[4], v_own[4], v_peer[4];
+            auto request = [&](int t) {
+                const uint8_t* a = code_row(own0 + t * kRows, id_own);
+                const uint8_t* b = code_row(peer0 + t * kRows, id_peer);
 #pragma unroll
-                for (int gr = 0; gr < 2; ++gr) {
-                    if (it > 0) {
-                        mbar_wait(&bars[kBarFree0 + 2 * gr], prev, sAbort, wl);
-                        mbar_wait(&bars[kBarFree0 + 2 * gr + 1], prev, sAbort, wl);
-                    }
-                    store_group<TQ4>(sSlot, gr == 0 ? raw.a : raw.b, gr, warp, lane, pl);
+                for (int c = 0; c < kChunks; ++c)
+                    raw[c] = a ? __ldg(reinterpret_cast<const P*>(a + 4 * kQuarter * c)) : P{};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    next[i] = b ? __ldg(reinterpret_cast<const P*>(b + 4 * kQuarter * (4 * (i >> 1) + 2 * rank + (i & 1)))) : P{};
+                ask(t + 1);
+            };
+            auto store_v = [&](uint32_t s) {   // the context rows of step s (whole walk), from v_own and v_peer
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (s > 0 && !warp_wait(&bars[kBarCtx0 + h], (s - 1) & 1u, sAbort, wl)) return false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        store_piece(sm + kOffV + i * kVChunkBytes, h == rank ? v_own[i] : v_peer[i], kHalf * h + drow, dq4, pl);
                     fence_async_smem();
-                    warp_arrive(&bars[kBarFull0 + gr], lane);
+                    warp_arrive_first(&bars[kBarV0 + h], lane);
                 }
-                if (!TQ4) store_kv8(sP, raw.c, rope_row<TQ4>(tid, warp, lane), 2 * rope_byte<TQ4>(tid, lane));
-                else if (warp < 8) store_tq4(sP, raw.c, rope_row<TQ4>(tid, warp, lane), 4 * rope_byte<TQ4>(tid, lane), pl);
-                fence_async_smem();
-                warp_arrive(&bars[kBarFull0 + 2], lane);
-            }
-            if (t + 1 < steps) request(t + 1);
-
-            // ---- softmax: one warp polls, the others wait on the named barrier ----
-            if (warp == 1) mbar_wait(&bars[kBarScore], par, sAbort, wl);
-            worker_sync<kWorkers>();
-            tc_after();
-            set_row(t + 2, page2);   // step t's rows are no longer needed
-            float z[16];
-            load_scores(view, sCz + 16 * hq, sM + 16 * hq, sLim + 16 * hq, z);
-            float dmax = z[0];
+                return true;
+            };
+            ask(0);
+            request(0);
+            if (it > 0 && !(ok = score_done(it - 1))) break;
+            load_queries<TQ4>(p, w.row0 + kHalf * rank, w.rows - kHalf * rank, sm + kOffQ,
+                              reinterpret_cast<float*>(sm + kOffCz) + (n & 1) * kHalf, dw, lane);
+            fence_async_smem();
+            warp_arrive(&bars[kBarQ0 + (n & 1)], lane);
+            for (int t = 0; t < w.steps; ++t, ++it) {
+                if (t > 0 && !(ok = score_done(it - 1))) break;
 #pragma unroll
-            for (int j = 1; j < 16; ++j) dmax = fmaxf(dmax, z[j]);
-            const float emax = fmaxf(sEmax[0], sEmax[1]);
-            const bool flag = (*sAbort != 0) | (view.sl * emax > kScaleLim) | (dmax > kLagLog2);
-            if (worker_any<kWorkers>(flag)) {
-                if (worker_any<kWorkers>(*sAbort != 0)) {
-                    aborted = true;
-                    break;
+                for (int gr = 0; gr < 3; ++gr) {
+#pragma unroll
+                    for (int c = 4 * gr; c < (gr < 2 ? 4 * gr + 4 : kChunks); ++c)
+                        store_piece(sm + kOffK + c * kChunkBytes, raw[c], drow, dq4, pl);
+                    fence_async_smem();
+                    warp_arrive_first(&bars[kBarK0 + gr], lane);
                 }
-                exact_path(sm, tmem, view, hq, lane, warp, tid, t == 0, p.exact_count);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) lsum[j] *= sAlphaM[16 * hq + j];
-                load_scores(view, sCz + 16 * hq, sM + 16 * hq, sLim + 16 * hq, z);
-            }
-            {
-                uint32_t pk[8];
+                if (t > 0 && !(ok = store_v(it - 1))) break;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float4 e = *reinterpret_cast<const float4*>(sE + 16 * hq + 4 * i);
-                    const float ev[4] = {e.x * view.sl, e.y * view.sl, e.z * view.sl, e.w * view.sl};
+                    // this CTA's dims of the own row: chunks 4 (i / 2) + 2 rank + i % 2
+                    v_own[i] = rank ? raw[4 * (i >> 1) + 2 + (i & 1)] : raw[4 * (i >> 1) + (i & 1)];
+                    v_peer[i] = next[i];
+                }
+                // the context buffer may stage the last segment's output
+                if (t == 0 && n > 0 && !(ok = warp_wait(&bars[kBarOut], (uint32_t)(n - 1) & 1u, sAbort, wl))) break;
+                if (t + 1 < w.steps) request(t + 1);
+            }
+            if (ok) ok = store_v(it - 1);
+        }
+    } else {
+        // ================= softmax warps =================
+        const int r = tid & (kHalf - 1), half = tid >> 6;   // vector (of this CTA); rows 64 half .. + 63 of a step
+        const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
+        unsigned char* sP = sm + kOffP + half * kChunkBytes;
+        uint32_t it = 0;
+        bool aborted = false;
+        for (int n = 0;; ++n) {
+            if (!warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl)) aborted = true;
+            if (worker_any<kSoft>(aborted)) {
+                aborted = true;
+                break;
+            }
+            const Work& w = sWork[n & 1];
+            const int steps = w.steps;
+            if (steps == 0) break;
+            const int32_t first = w.first, seen0 = w.seen0;
+            // vectors past the tile's last repeat its limit: they score 0 and are dropped
+            const int vec = kHalf * rank + r;
+            const int32_t lim = (int32_t)max((int64_t)0, w.base + 1 + (w.tok0 + min(vec, w.rows - 1)) / p.n_heads);
+            // this thread's row of a step, for its scales: page, then scales, a step ahead of their use
+            const int32_t* table = p.table + (int64_t)w.b * p.table_stride;
+            const int32_t end = w.end;
+            int32_t id_next = 0;
+            float2 scale_next = make_float2(0.f, 0.f);
+            auto ask = [&](int t) {
+                const int32_t x = first + t * kRows + tid;
+                id_next = t < steps && x < end ? __ldg(table + (x >> p.shift)) : 0;
+            };
+            auto request = [&](int t) {
+                const int32_t x = first + t * kRows + tid;
+                scale_next = make_float2(0.f, 0.f);
+                if (t < steps && x < end) {
+                    const int32_t id = id_next < 0 || id_next >= p.n_pages ? 0 : id_next;   // the decode warps report it
+                    const float* s = p.scales + (((int64_t)id << p.shift) + (x & ((1 << p.shift) - 1))) * p.n_blocks;
+                    scale_next = make_float2(__ldg(s), __ldg(s + p.n_blocks - 1));
+                }
+                ask(t + 1);
+            };
+            ask(0);
+            request(0);
+            RowState st{-INFINITY, -INFINITY, 0.0f, 0.0f, 0.0f, false};
+            if (!warp_wait(&bars[kBarQ0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl)) aborted = true;
+            const float cz = reinterpret_cast<const float*>(sm + kOffCz)[(n & 1) * kHalf + r];
+
+            for (int t = 0; t < steps; ++t, ++it) {
+                float2* sScale = reinterpret_cast<float2*>(sm + kOffScale + (it & 1u) * kScaleBytes);
+                float* sMax = reinterpret_cast<float*>(sm + kOffMax) + (it & 1u) * kSoftWarps;
+                sScale[tid] = scale_next;
+                {
+                    const float top = warp_max(scale_next.x);
+                    if (lane == 0) sMax[warp] = top;
+                }
+                request(t + 1);
+                worker_sync<kSoft>();
+                warp_wait(&bars[kBarScore0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl);
+                tc_after();
+                const float4* sc4 = reinterpret_cast<const float4*>(sScale + kHalf * half);   // (s_L, s_R) of two rows
+                const uint32_t ts = tmem + lane_base + kColS + 128 * (it & 1u);
+                const int32_t t0 = first + t * kRows + kHalf * half;
+                const bool masked = first + (t + 1) * kRows > seen0;
+                float z[kHalf];
+                auto scores = [&](float sub) {   // z - sub of this vector's 64 rows
 #pragma unroll
-                    for (int k = 0; k < 4; k += 2) {
-                        const int j = 4 * i + k;
-                        z[j] = ex2(z[j]);
-                        z[j + 1] = ex2(z[j + 1]);
-                        const __half2 h2 = __floats2half2_rn(z[j] * ev[k], z[j + 1] * ev[k + 1]);
-                        pk[j / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t a[16], b[16];
+                        tmem_ld16(ts + 16 * c, a);
+                        tmem_ld16(ts + 64 + 16 * c, b);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float4 s = sc4[8 * c + j / 2];
+                            z[16 * c + j] = fmaf(fmaf(__uint_as_float(a[j]), s.x, __uint_as_float(b[j]) * s.y), cz, -sub);
+                            z[16 * c + j + 1] =
+                                fmaf(fmaf(__uint_as_float(a[j + 1]), s.z, __uint_as_float(b[j + 1]) * s.w), cz, -sub);
+                        }
                     }
+                    if (masked) {
+#pragma unroll
+                        for (int j = 0; j < kHalf; ++j)
+                            if (t0 + j >= lim) z[j] = -INFINITY;
+                    }
+                };
+                scores(st.m);
+                float top[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+                for (int j = 4; j < kHalf; ++j) top[j & 3] = fmaxf(top[j & 3], z[j]);
+                const float dmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                const float smax = fmaxf(fmaxf(sMax[0], sMax[1]), fmaxf(sMax[2], sMax[3]));
+                const bool flag = aborted | (*sAbort != 0) | (smax * (st.none ? INFINITY : st.E) > kScaleLim) | (dmax > kLagLog2);
+                if (worker_any<kSoft>(flag)) {
+                    // ---- exact path: row maxima, new references, O rescaled ----
+                    if (it > 0 && (!warp_wait(&bars[kBarCtx0], (it - 1) & 1u, sAbort, wl) ||
+                                   !warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)))
+                        aborted = true;
+                    if (worker_any<kSoft>(aborted | (*sAbort != 0))) {
+                        aborted = true;
+                        break;
+                    }
+                    tc_after();
+                    // the next step's scales are still in registers: their buffer
+                    // takes the exchange between the two halves of a vector
+                    float* sX = reinterpret_cast<float*>(sm + kOffScale + ((it & 1u) ^ 1u) * kScaleBytes);
+                    scores(0.0f);
+                    float zt = -INFINITY, yt = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < kHalf; ++j) {
+                        const float s = sScale[kHalf * half + j].x;
+                        zt = fmaxf(zt, z[j]);
+                        yt = fmaxf(yt, z[j] + (s > 0.0f ? __log2f(s) : -INFINITY));   // -inf: an inert latent block
+                    }
+                    sX[tid] = zt;
+                    sX[kSoft + tid] = yt;
+                    worker_sync<kSoft>();
+                    zt = fmaxf(zt, sX[tid ^ kHalf]);
+                    yt = fmaxf(yt, sX[kSoft + (tid ^ kHalf)]);
+                    worker_sync<kSoft>();
+                    const float mn = fmaxf(st.m, zt), rn = fmaxf(st.R, yt);
+                    const bool inert = rn == -INFINITY;
+                    const float le = fminf(mn - rn - kHeadroom, kLogEmax);
+                    const float al = st.m == -INFINITY ? 0.0f : ex2(st.m - mn);
+                    // O holds sum p s_L E c: rescaled by (E_new / E_old) 2^(m_old - m_new)
+                    const float ao = st.R == -INFINITY ? 0.0f : ex2(le - st.logE + (st.m - mn));
+                    st.l *= al;
+                    st.m = mn;
+                    st.R = rn;
+                    st.logE = le;
+                    st.E = inert ? 0.0f : ex2(le);
+                    // rows seen without a latent scale: the next one comes here again;
+                    // no row seen: the first score does, by m = -inf
+                    st.none = inert && mn > -INFINITY;
+                    if (t > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(tmem + lane_base + kColO + 16 * c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * ao);
+                            tmem_st16(tmem + lane_base + kColO + 16 * c, o);
+                        }
+                        tmem_wait_st();
+                        if (tid == 0 && rank == 0) atomicAdd(p.exact_count, 1u);
+                    }
+                    scores(st.m);
+                }
+                uint32_t pk[kHalf / 2];
+                float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < kHalf; j += 2) {
+                    const float4 s = sc4[j / 2];
+                    const float a = ex2(z[j]), b = ex2(z[j + 1]);
+                    sum[0] += a;
+                    sum[1] += b;
+                    const __half2 h2 = __floats2half2_rn(a * (st.E * s.x), b * (st.E * s.z));
+                    pk[j / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+                }
+                st.l += sum[0] + sum[1];
+                // the weights of the step before have been read
+                if (it > 0) {
+                    warp_wait(&bars[kBarCtx0], (it - 1) & 1u, sAbort, wl);
+                    warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl);
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    *reinterpret_cast<uint4*>(sP + sw128(srow, 32 * hq + 16 * i)) =
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4*>(sP + sw128(r, 16 * i)) =
                         make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                fence_async_smem();
+                tc_before();
+                warp_arrive_first(&bars[kBarP], lane);
             }
-            fence_async_smem();
-            tc_before();
-            warp_arrive(&bars[kBarP], lane);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) lsum[j] += z[j];
-        }
-        if (aborted) break;
-
-        // ---- epilogue: the last context products, row sums, O^T out ----
-        if (!mbar_wait(&bars[kBarFree0 + 3], (it - 1) & 1u, sAbort, wl)) aborted = true;
-        tc_after();
-        if (worker_any<kWorkers>(aborted)) {
-            aborted = true;
-            break;
-        }
-        {
-            const float s = warp_columns16<false>(lsum, lane);
-            if (lane < 16) sRed[(warp & 3) * kCols + 16 * hq + lane] = s;
-        }
-        worker_sync<kWorkers>();
-        const int64_t slot = g.slot;
-        if (tid < kCols) {
-            const float l = (sRed[tid] + sRed[kCols + tid]) + (sRed[2 * kCols + tid] + sRed[3 * kCols + tid]);
-            const float f = TQ4 ? sF[tid] / kGamma : sF[tid];
-            sAlpha[tid] = slot >= 0 ? f : (l == 0.0f ? 0.0f : f / l);   // no visible row: zeros
-            if (slot >= 0) {
-                float* ml = p.ws_ml + (slot * kCols + tid) * 2;
-                ml[0] = sM[tid] * kLn2;
+            // ---- output ----
+            if (!aborted && !(warp_wait(&bars[kBarCtx0], (it - 1) & 1u, sAbort, wl) &&
+                              warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)))
+                aborted = true;
+            if (worker_any<kSoft>(aborted)) {
+                aborted = true;
+                break;
+            }
+            tc_after();
+            float* sX = reinterpret_cast<float*>(sm + kOffScale + (it & 1u) * kScaleBytes);
+            sX[tid] = st.l;
+            worker_sync<kSoft>();
+            const float l = sX[r] + sX[kHalf + r];   // the same order in both halves
+            worker_sync<kSoft>();
+            const int64_t slot = w.slot;
+            float f = st.R == -INFINITY ? 0.0f : ex2(-st.logE);
+            if (TQ4) f *= 1.0f / kGamma;
+            if (slot < 0) f = l == 0.0f ? 0.0f : f / l;   // no visible row: zeros
+            if (slot >= 0 && half == 0) {
+                float* ml = p.ws_ml + (slot * kVecs + vec) * 2;
+                ml[0] = st.m * kLn2;
                 ml[1] = l;
             }
-        }
-        if (g.parts > 0 && tid == 0) {
-            p.ws_desc[cta * 4] = g.parts;
-            p.ws_desc[cta * 4 + 1] = g.row0;
-            p.ws_desc[cta * 4 + 2] = g.rows;
-        }
-        worker_sync<kWorkers>();
-        const int dim = 128 * hq + 32 * (warp & 3) + lane;   // block hq of the context
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-        float* stage = reinterpret_cast<float*>(sSlot);
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-            uint32_t v[16];
-            tmem_ld16(tmem + lane_base + kColO + 64 * hq + 16 * c, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int r = 16 * c + j;
-                const float x = __uint_as_float(v[j]) * sAlpha[r];
-                if (slot >= 0) p.ws_o[(slot * kCols + r) * kMlaDV + dim] = x;
-                else if (TQ4) stage[r * kStageStride + dim] = x;
-                else if (r < g.rows) out[(g.row0 + r) * kMlaDV + dim] = __float2bfloat16_rn(x);
+            if (rank == 0 && tid == 0 && w.parts > 0) {
+                p.ws_desc[pair * 4] = w.parts;
+                p.ws_desc[pair * 4 + 1] = w.row0;
+                p.ws_desc[pair * 4 + 2] = w.rows;
             }
-        }
-        if (TQ4 && slot < 0) {
-            worker_sync<kWorkers>();
-            for (int r = warp; r < g.rows; r += kWarps) {
-                float v[16];
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + w.row0 * kMlaDV;
+            const int rows = w.rows;
+            // 16 dims of this vector: block c / 8 of 256, 128 half + 16 (c % 8)
+            auto context = [&](int c, float (&o)[16]) {
+                uint32_t u[16];
+                tmem_ld16(tmem + lane_base + kColO + 16 * c, u);
+                tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = stage[r * kStageStride + lane + 32 * k];
-                warp_fwht<512>(v, lane);
+                for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(u[j]) * f;
+                return 256 * (c >> 3) + 128 * half + 16 * (c & 7);
+            };
+            if (slot >= 0) {
+#pragma unroll 2
+                for (int c = 0; c < 16; ++c) {
+                    float o[16];
+                    const int d = context(c, o);
+                    float4* dst = reinterpret_cast<float4*>(p.ws_o + (slot * kVecs + vec) * kMlaDV + d);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int i = lane + 32 * k;
-                    const float y = v[k] * p.kn[0];
-                    out[(g.row0 + r) * kMlaDV + i] = __float2bfloat16_rn(sign_neg(p.signs, 0, i) ? -y : y);
+                    for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+            } else if (!TQ4) {
+#pragma unroll 2
+                for (int c = 0; c < 16; ++c) {
+                    float o[16];
+                    const int d = context(c, o);
+                    uint32_t h[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+                        h[i] = *reinterpret_cast<const uint32_t*>(&b2);
+                    }
+                    if (vec < rows) {
+                        uint4* dst = reinterpret_cast<uint4*>(out + (int64_t)vec * kMlaDV + d);
+                        dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+                        dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+                    }
+                }
+            } else {
+                // unrotate: 32 vectors at a time through the context buffer (free
+                // until the next segment's rows), 16-byte units swizzled by vector
+                float* stage = reinterpret_cast<float*>(sm + kOffV);
+#pragma unroll 1
+                for (int rr = 0; rr < 2; ++rr) {
+                    if ((r >> 5) == rr) {
+#pragma unroll 2
+                        for (int c = 0; c < 16; ++c) {
+                            float o[16];
+                            const int d = context(c, o);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                *reinterpret_cast<float4*>(stage + lane * kMlaDV + 4 * ((d / 4 + i) ^ (lane & 7))) =
+                                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        }
+                    }
+                    worker_sync<kSoft>();
+                    for (int k = warp; k < 32; k += kSoftWarps) {
+                        const int ov = kHalf * rank + 32 * rr + k;
+                        if (ov >= rows) break;
+                        float v[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int e = lane + 32 * i;
+                            v[i] = stage[k * kMlaDV + 4 * ((e >> 2) ^ (k & 7)) + (e & 3)];
+                        }
+                        warp_fwht<512>(v, lane);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int e = lane + 32 * i;
+                            const float y = v[i] * p.kn[0];
+                            out[(int64_t)ov * kMlaDV + e] = __float2bfloat16_rn(sign_neg(p.signs, 0, e) ? -y : y);
+                        }
+                    }
+                    worker_sync<kSoft>();
                 }
             }
+            tc_before();
+            warp_arrive(&bars[kBarOut], lane);
+            warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
         }
-        warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
-        tc_before();
-        worker_sync<kWorkers>();   // O^T, the stage and the state are free for the next segment
-        tc_after();
-    }
-    {
-        // bounded, and not cut short by the abort flag: TMEM is released only
-        // after the products in flight have completed
+        // bounded, and not cut short by the abort flag: tensor memory is
+        // released only after the products in flight have completed
         volatile int never = 0;
-        if (!mbar_wait(&bars[kBarDone], 0u, &never)) aborted = true;
+        if (!pair_wait(&bars[kBarDone], 0u, &never, kWaitLimit)) aborted = true;
+        if ((aborted || *sAbort != 0) && tid == 0) set_err(p.err, aligned ? KVQ_ERR_TIMEOUT : KVQ_ERR_DEVICE);
     }
-    if (aborted && tid == 0) set_err(p.err, KVQ_ERR_TIMEOUT);
+    __syncwarp();
     tc_before();
-    worker_sync<kWorkers>();
+    __syncthreads();
+    cluster_sync();   // nothing of either CTA is in flight towards the other
     tc_after();
-    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
 }
 
 template <bool TQ4>
 cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(paged_tensor_kernel<TQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemUsed);
+    cudaError_t e =
+        cudaFuncSetAttribute(paged_tensor_kernel<TQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemUsed);
     if (e != cudaSuccess) return e;
-    paged_tensor_kernel<TQ4><<<kPagedCtas, kThreads, kSmemUsed, stream>>>(p);
+    paged_tensor_kernel<TQ4><<<2 * kPagedPairs, kThreads, kSmemUsed, stream>>>(p);
     return cudaGetLastError();
 }
 

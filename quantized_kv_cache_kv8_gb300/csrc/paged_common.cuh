@@ -254,10 +254,10 @@ __device__ __forceinline__ int32_t paged_row(const PagedParams& p, int32_t b, in
 }
 
 // The exact (fp32) kernel and the tensor-core kernel: query vectors a tile,
-// rows a step, prologue allowance in steps, CTAs.
+// rows a step, prologue allowance in steps; CTAs, and pairs of CTAs, that walk.
 using PagedSimt = SchedOf<32, 32, 4>;
-using PagedTensor = SchedOf<64, 128, 2>;
-constexpr int kPagedCtas = 152;
+using PagedTensor = SchedOf<128, 128, 2>;
+constexpr int kPagedCtas = 152, kPagedPairs = 76;
 
 cudaError_t launch_paged_tensor(kvq_format fmt, const PagedParams& p, cudaStream_t stream);
 
