@@ -23,8 +23,9 @@
 // its own is exact in f16 (down to 2^-24 of 2^14); the rotated query of TQ4 is
 // rounded once, 2^-12 relative.
 //
-// Roles (a CTA): 8 decode warps, 4 softmax warps, one issuing warp (in the first
-// CTA), one that announces segments.  The decode warps store the score rows of
+// Roles (a CTA): 8 softmax warps, 8 decode warps, one issuing warp (in the first
+// CTA), one that announces segments, one that fetches row scales; registers move
+// to the decode warps, which hold a step's codes (setmaxnreg).  The decode warps store the score rows of
 // step t+1 once the scores of step t are complete and the context rows of step t
 // once the context of step t-1 is; the scores of t+1 are issued before the
 // context of t.  So the tensor pipe alternates between the two while the other
@@ -34,7 +35,7 @@
 //   softmax         ---- P(t) ----      -- P(t+1) --
 // Accumulators: O 256 columns, S two buffers of 64 + 64.
 //
-// Softmax, per query vector (a thread has one and half of the rows), in log2
+// Softmax, per query vector (a thread has one and a quarter of the rows), in log2
 // units: m is a lagged running maximum of the scores, p = 2^(z - m) enters the
 // row sum in f32, and the context takes the f16 weight w = p s_L E,
 // E = 2^(m - R - 3) with R the largest z + log2 s_L of the steps that set the
@@ -57,10 +58,13 @@ constexpr int kRows = PagedTensor::kN;       // rows a step
 constexpr int kVecs = PagedTensor::kM;       // query vectors of the pair
 constexpr int kHalf = 64;                    // query vectors, and score rows, of a CTA
 static_assert(kRows == 2 * kHalf && kVecs == 2 * kHalf, "pair layout");
-constexpr int kSoftWarps = 4, kDecWarps = 8;
-constexpr int kSoft = 32 * kSoftWarps;
-constexpr int kIssueWarp = kSoftWarps + kDecWarps, kWalkWarp = kIssueWarp + 1;
-constexpr int kThreads = 32 * (kWalkWarp + 1);
+constexpr int kSoftWarps = 8, kDecWarps = 8;
+constexpr int kSoft = 32 * kSoftWarps, kDec = 32 * kDecWarps;
+constexpr int kIssueWarp = kSoftWarps + kDecWarps, kWalkWarp = kIssueWarp + 1, kScaleWarp = kIssueWarp + 2;
+constexpr int kThreads = kSoft + kDec + 128;   // five warpgroups; one warp of the last is idle
+constexpr int kRegsLaunch = 96, kRegsSoft = 88, kRegsDec = 120, kRegsRest = 64;
+static_assert(kSoft * kRegsSoft + kDec * kRegsDec + 128 * kRegsRest <= kThreads * kRegsLaunch, "register split");
+constexpr int kCols = 32;                    // rows of a step that a softmax thread has
 constexpr int kChunks = 9, kRope = 8;        // 64-dim chunks of a row: 8 latent, 1 rope
 constexpr uint32_t kChunkBytes = kHalf * 128;   // 64 rows (or vectors) x 64 f16
 constexpr uint32_t kVChunkBytes = kRows * 128;  // 128 rows x 64 f16
@@ -72,8 +76,8 @@ constexpr uint32_t kOffScale = kOffP + 2 * kChunkBytes;     // (s_L, s_R) of two
 constexpr uint32_t kScaleBytes = kRows * 8;
 constexpr uint32_t kOffCz = kOffScale + 2 * kScaleBytes;    // score scale of a vector, two segments
 constexpr uint32_t kOffBar = kOffCz + 2 * kHalf * 4;
-constexpr uint32_t kOffMax = kOffBar + 20 * 8;              // largest s_L of two steps by warp
-constexpr uint32_t kOffLevels = kOffMax + 2 * kSoftWarps * 4;
+constexpr uint32_t kOffMax = kOffBar + 24 * 8;              // largest s_L of two steps
+constexpr uint32_t kOffLevels = kOffMax + 16;
 constexpr uint32_t kOffMisc = kOffLevels + 32;              // abort flag, TMEM base
 constexpr uint32_t kOffWork = kOffMisc + 16;                // two segments, announced one ahead
 constexpr uint32_t kSmemUsed = kOffWork + 2 * 72;
@@ -85,17 +89,18 @@ static_assert(32 * kMlaDV * 4 <= 4 * kVChunkBytes, "output stage");
 
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 
-// mbarriers.  In the first CTA, arrivals from both: score rows stored (chunks
-// 0-3, 4-7, rope), context rows stored (rows 0-63, 64-127), weights written.  In
+// mbarriers.  In the first CTA, arrivals from both: score rows stored (latent,
+// rope), context rows stored (rows 0-63, 64-127), weights written.  In
 // each CTA: scores complete (by buffer; commits reach both CTAs), context complete
-// (by row half), segment announced, segment done with, queries stored, output written,
+// (by row half), segment announced, segment done with, queries stored, output
+// written, row scales stored and read,
 // every product complete, and one that nothing arrives on (the testing hook).
 enum {
-    kBarK0 = 0, kBarV0 = 3, kBarP = 5, kBarScore0 = 6, kBarCtx0 = 8, kBarWork0 = 10, kBarWorkFree0 = 12, kBarQ0 = 14,
-    kBarOut = 16, kBarDone = 17, kBarNever = 18, kNumBars = 19
+    kBarK0 = 0, kBarV0 = 2, kBarP = 4, kBarScore0 = 5, kBarCtx0 = 7, kBarWork0 = 9, kBarWorkFree0 = 11, kBarQ0 = 13, kBarOut = 15,
+    kBarDone = 16, kBarNever = 17, kBarScale0 = 18, kBarScaleFree0 = 20, kNumBars = 22
 };
-// Scores, announcements and queries have two barriers each, used in turn: their
-// next but one event waits for whoever waits for this one, the next does not.
+// Scores, announcements, queries and scales have two barriers each, used in turn:
+// their next but one event waits for whoever waits for this one, the next does not.
 
 constexpr float kLagLog2 = 14.0f, kScaleLim = 3.5f, kHeadroom = 3.0f, kLogEmax = 120.0f;
 // levels times this round to f16 within 9.3e-5 (unscaled: 3.2e-4); divided out in f32
@@ -120,6 +125,22 @@ __device__ __forceinline__ uint32_t cta_rank() {
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same for waits that last for many steps: half a microsecond between polls.
+__device__ __forceinline__ bool idle_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
+    for (long long i = 0; i < limit; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (*abort_flag) return false;
+        __nanosleep(500);
+    }
+    *abort_flag = 1;
+    return false;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
     return __all_sync(kFull, mbar_wait(bar, parity, abort_flag, limit));
@@ -160,10 +181,10 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
 }
 
 // ---- decode -------------------------------------------------------------------
-// 16 codes: a quarter of a row's 64-dim chunk.  Four lanes read a chunk (64 or 32
-// contiguous bytes) and store its 128 bytes; the 8 lanes that a shared store
-// serves at a time cover two rows whose swizzle phases differ in the low bit,
-// 8 different 16-byte units.
+// 16 codes: a quarter of a row's 64-dim chunk.  32 lanes read a row's 512 latent
+// dims (or two rows' 256) in one run and store 32 bytes each in two 16-byte
+// stores; lanes of odd chunks store their upper half first, so that the 8 lanes a
+// store serves at a time (one row, two chunks) cover 8 different 16-byte units.
 template <bool TQ4>
 struct PieceOf {
     using type = uint4;
@@ -179,18 +200,20 @@ using Piece = typename PieceOf<TQ4>::type;
 struct Planes {
     uint32_t lo[4], hi[4];
 };
-__device__ __forceinline__ void store_piece(unsigned char* chunk, const uint4& c, int row, int q, const Planes&) {
+// `flip`: 16 for the lanes that store their upper half first, else 0.
+__device__ __forceinline__ void store_piece(unsigned char* chunk, const uint4& c, int row, int q, int flip, const Planes&) {
     const uint32_t in[4] = {c.x, c.y, c.z, c.w};
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) e4m3x4_to_half2x2(in[i], w[2 * i], w[2 * i + 1]);
-    *reinterpret_cast<uint4*>(chunk + sw128(row, 32 * q)) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4*>(chunk + sw128(row, 32 * q + 16)) = make_uint4(w[4], w[5], w[6], w[7]);
+    const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
+    *reinterpret_cast<uint4*>(chunk + sw128(row, (32 * q) ^ flip)) = flip ? hi : lo;
+    *reinterpret_cast<uint4*>(chunk + sw128(row, (32 * q + 16) ^ flip)) = flip ? lo : hi;
 }
 // Nibble codes by byte permutes over the low and the high bytes of the levels:
 // the low 3 bits of a code pick among levels 0-7 and 8-15, bit 3 between the two.
-__device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c, int row, int q, const Planes& t) {
-    const uint32_t in[2] = {c.x, c.y};
+__device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c, int row, int q, int flip, const Planes& t) {
+    const uint32_t in[2] = {flip ? c.y : c.x, flip ? c.x : c.y};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint32_t sel = in[i] & 0x77777777u, pick = ((in[i] >> 1) & 0x44444444u) | 0x32103210u;
@@ -203,7 +226,7 @@ __device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c
             w[2 * h] = __byte_perm(lo, hi, 0x5140u);
             w[2 * h + 1] = __byte_perm(lo, hi, 0x7362u);
         }
-        *reinterpret_cast<uint4*>(chunk + sw128(row, 32 * q + 16 * i)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(chunk + sw128(row, (32 * q + 16 * i) ^ flip)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -308,8 +331,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                    : (i == kBarQ0 || i == kBarQ0 + 1) ? (uint32_t)kDecWarps
                                    : i == kBarOut     ? (uint32_t)kSoftWarps
                                    : (i == kBarWorkFree0 || i == kBarWorkFree0 + 1)
-                                       ? (uint32_t)(kSoftWarps + kDecWarps + (rank == 0 ? 1 : 0))
-                                       : 1u;
+                                       ? (uint32_t)(kSoftWarps + kDecWarps + 1 + (rank == 0 ? 1 : 0))
+                                   : (i == kBarScaleFree0 || i == kBarScaleFree0 + 1) ? (uint32_t)kSoftWarps
+                                                                                      : 1u;
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&bars[i])), "r"(count));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -332,12 +356,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_after();
     const uint32_t tmem = *sTmem;
 
+    if (warp >= kIssueWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kWalkWarp) {
         // ================= the walk: announces segments one ahead =================
         if (lane == 0) {
             bool more = true;
             for (int n = 0; more; ++n, walk.next(p)) {
-                if (n >= 2 && !mbar_wait(&bars[kBarWorkFree0 + (n & 1)], (uint32_t)(n / 2 - 1) & 1u, sAbort, wl)) break;
+                if (n >= 2 && !idle_wait(&bars[kBarWorkFree0 + (n & 1)], (uint32_t)(n / 2 - 1) & 1u, sAbort, wl)) break;
                 Segment g;
                 Work w{};
                 more = walk.get(p, g);
@@ -372,11 +398,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             auto scores = [&](uint32_t it) {
                 const uint32_t d = tmem + kColS + 128 * (it & 1u);
 #pragma unroll
-                for (int gr = 0; gr < 3; ++gr) {
+                for (int gr = 0; gr < 2; ++gr) {
                     if (!warp_wait(&bars[kBarK0 + gr], it & 1u, sAbort, wl)) return false;
                     tc_after();
 #pragma unroll
-                    for (int kc = 4 * gr; kc < (gr < 2 ? 4 * gr + 4 : kChunks); ++kc)
+                    for (int kc = gr ? kRope : 0; kc < (gr ? kChunks : kRope); ++kc)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             pair_mma(d + (kc < kRope ? 0 : 64), dq + kc * kStep + 2 * ks, dk + kc * kStep + 2 * ks,
@@ -417,17 +443,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             pair_commit(&bars[kBarDone]);
         }
+    } else if (warp == kScaleWarp) {
+        // ================= row scales, two steps ahead =================
+        // 4 consecutive rows a lane: in one page, as pages hold whole multiples of 16
+        uint32_t it = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            if (!(ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl))) break;
+            const Work w = sWork[n & 1];
+            warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
+            if (w.steps == 0) break;
+            const int32_t* table = p.table + (int64_t)w.b * p.table_stride;
+            auto page = [&](int t) {
+                const int32_t x = w.first + t * kRows + 4 * lane;
+                return t < w.steps && x < w.end ? __ldg(table + (x >> p.shift)) : 0;
+            };
+            int32_t id = page(0);
+            for (int t = 0; t < w.steps; ++t, ++it) {
+                const int32_t x = w.first + t * kRows + 4 * lane;
+                if (id < 0 || id >= p.n_pages) id = 0;   // the decode warps report it
+                const float* s = p.scales + (((int64_t)id << p.shift) + (x & ((1 << p.shift) - 1))) * p.n_blocks;
+                float2 v[4];
+                float top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = make_float2(0.f, 0.f);
+                    if (x + i < w.end) v[i] = make_float2(__ldg(s + i * p.n_blocks), __ldg(s + (i + 1) * p.n_blocks - 1));
+                }
+                id = page(t + 1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, v[i].x);
+                top = warp_max(top);
+                if (it >= 2 && !(ok = warp_wait(&bars[kBarScaleFree0 + (it & 1u)], (it / 2 - 1) & 1u, sAbort, wl))) break;
+                float4* dst = reinterpret_cast<float4*>(sm + kOffScale + (it & 1u) * kScaleBytes) + 2 * lane;
+                dst[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+                dst[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+                if (lane == 0) reinterpret_cast<float*>(sm + kOffMax)[it & 1u] = top;
+                warp_arrive(&bars[kBarScale0 + (it & 1u)], lane);
+            }
+        }
+    }
     } else if (warp >= kSoftWarps) {
         // ================= decode warps =================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsDec));
         using P = Piece<TQ4>;
-        constexpr int kRowBytes = TQ4 ? kMlaD / 2 : kMlaD, kQuarter = sizeof(P);
-        const int dw = warp - kSoftWarps, dt = tid - kSoft, drow = dt >> 2, dq4 = dt & 3;
+        constexpr int kRowBytes = TQ4 ? kMlaD / 2 : kMlaD, kQ = sizeof(P);
+        const int dw = warp - kSoftWarps;
         Planes pl{};
         if (TQ4) {
             const uint4 a = *reinterpret_cast<const uint4*>(sm + kOffLevels);
             const uint4 b = *reinterpret_cast<const uint4*>(sm + kOffLevels + 16);
             pl = Planes{{a.x, a.y, a.z, a.w}, {b.x, b.y, b.z, b.w}};
         }
+        // A warp has 8 consecutive rows of each half of a step (8 rows lie in one
+        // page): of the CTA's own half for the scores, of both for the context.
+        //   score row i: lane has chunk lane / 4, quarter lane % 4; rope: row lane / 4
+        //   context rows 2 i, 2 i + 1: lane / 16 picks the row, m = lane % 16 the
+        //     quarter: chunk m / 4, quarter m % 4
+        // The two are loaded apart, each straight into the registers it is stored
+        // from once the load of the step before has left them: codes of the own
+        // half come twice (L2 has room, 10% busy), but no loaded register is
+        // moved, and so waited for, before its step.
+        const int oc = lane >> 2, q4 = lane & 3, m16 = lane & 15;
+        const int flip_k = (oc & 1) * 16, flip_v = ((m16 >> 2) & 1) * 16;
+        unsigned char* k_chunk = sm + kOffK + oc * kChunkBytes;
+        unsigned char* v_chunk = sm + kOffV + (m16 >> 2) * kVChunkBytes;
+        const int v_code = 256 * (m16 >> 3) + 128 * rank + 16 * (m16 & 7);   // first dim of the quarter
         uint32_t it = 0;
         bool ok = true;
         auto score_done = [&](uint32_t s) { return warp_wait(&bars[kBarScore0 + (s & 1u)], (s >> 1) & 1u, sAbort, wl); };
@@ -437,51 +518,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
             if (w.steps == 0) break;
             const int32_t* table = p.table + (int64_t)w.b * p.table_stride;
-            // this thread's two rows of a step: the one it supplies to the
-            // scores, and the other CTA's at the same place.  Pages are asked
-            // for a step before the codes, the codes a step before their use.
-            const int32_t own0 = w.first + kHalf * rank + drow, peer0 = w.first + kHalf * (1 - rank) + drow;
-            int32_t id_own = 0, id_peer = 0;
-            auto ask = [&](int t) {
-                const int32_t a = own0 + t * kRows, b = peer0 + t * kRows;
-                id_own = t < w.steps && a < w.end ? __ldg(table + (a >> p.shift)) : 0;
-                id_peer = t < w.steps && b < w.end ? __ldg(table + (b >> p.shift)) : 0;
-            };
-            auto code_row = [&](int32_t r, int32_t id) -> const uint8_t* {
-                if (r >= w.end) return nullptr;
+            const int32_t row_k = w.first + kHalf * rank + 8 * dw, row_v = w.first + 8 * dw;
+            // pages are asked for a step before the codes, the codes a step before their use
+            auto page = [&](int32_t r) { return r < w.end ? __ldg(table + (r >> p.shift)) : 0; };
+            auto code_rows = [&](int32_t r, int32_t id) {
                 if (id < 0 || id >= p.n_pages) {
-                    set_err(p.err, KVQ_ERR_ARG);
+                    if (lane == 0) set_err(p.err, KVQ_ERR_ARG);
                     id = 0;
                 }
-                const int64_t row = ((int64_t)id << p.shift) + (r & ((1 << p.shift) - 1));
-                return p.codes + row * kRowBytes + kQuarter * dq4;
+                return p.codes + (((int64_t)id << p.shift) + (r & ((1 << p.shift) - 1))) * kRowBytes;
             };
-            P raw[kChunks], next[4], v_own[4], v_peer[4];
-            auto request = [&](int t) {
-                const uint8_t* a = code_row(own0 + t * kRows, id_own);
-                const uint8_t* b = code_row(peer0 + t * kRows, id_peer);
+            int32_t id_k = page(row_k), id_v[2] = {page(row_v), page(row_v + kHalf)};
+            P raw[8], rope, ctx[2][4];
+            auto request_k = [&](int t) {
+                const int32_t r0 = row_k + t * kRows;
+                const uint8_t* a = code_rows(r0, id_k) + kQ * lane;
+                const uint8_t* b = a + oc * kRowBytes + kQ * (32 + q4 - lane);
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c)
-                    raw[c] = a ? __ldg(reinterpret_cast<const P*>(a + 4 * kQuarter * c)) : P{};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    next[i] = b ? __ldg(reinterpret_cast<const P*>(b + 4 * kQuarter * (4 * (i >> 1) + 2 * rank + (i & 1)))) : P{};
-                ask(t + 1);
+                for (int i = 0; i < 8; ++i)
+                    raw[i] = r0 + i < w.end ? __ldg(reinterpret_cast<const P*>(a + i * kRowBytes)) : P{};
+                rope = r0 + oc < w.end ? __ldg(reinterpret_cast<const P*>(b)) : P{};
+                if (t + 1 < w.steps) id_k = page(r0 + kRows);
             };
-            auto store_v = [&](uint32_t s) {   // the context rows of step s (whole walk), from v_own and v_peer
+            auto request_v = [&](int t) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int32_t r0 = row_v + t * kRows + kHalf * h;
+                    const uint8_t* a = code_rows(r0, id_v[h]) + (lane >> 4) * kRowBytes + v_code * kQ / 16;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        ctx[h][i] = r0 + 2 * i + (lane >> 4) < w.end ? __ldg(reinterpret_cast<const P*>(a + 2 * i * kRowBytes)) : P{};
+                    if (t + 1 < w.steps) id_v[h] = page(r0 + kRows);
+                }
+            };
+            auto store_v = [&](uint32_t s) {   // the context rows of step s (of the whole walk)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (s > 0 && !warp_wait(&bars[kBarCtx0 + h], (s - 1) & 1u, sAbort, wl)) return false;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        store_piece(sm + kOffV + i * kVChunkBytes, h == rank ? v_own[i] : v_peer[i], kHalf * h + drow, dq4, pl);
+                        store_piece(v_chunk, ctx[h][i], kHalf * h + 8 * dw + 2 * i + (lane >> 4), q4, flip_v, pl);
                     fence_async_smem();
                     warp_arrive_first(&bars[kBarV0 + h], lane);
                 }
                 return true;
             };
-            ask(0);
-            request(0);
+            request_k(0);
+            request_v(0);
             if (it > 0 && !(ok = score_done(it - 1))) break;
             load_queries<TQ4>(p, w.row0 + kHalf * rank, w.rows - kHalf * rank, sm + kOffQ,
                               reinterpret_cast<float*>(sm + kOffCz) + (n & 1) * kHalf, dw, lane);
@@ -490,31 +573,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int t = 0; t < w.steps; ++t, ++it) {
                 if (t > 0 && !(ok = score_done(it - 1))) break;
 #pragma unroll
-                for (int gr = 0; gr < 3; ++gr) {
-#pragma unroll
-                    for (int c = 4 * gr; c < (gr < 2 ? 4 * gr + 4 : kChunks); ++c)
-                        store_piece(sm + kOffK + c * kChunkBytes, raw[c], drow, dq4, pl);
-                    fence_async_smem();
-                    warp_arrive_first(&bars[kBarK0 + gr], lane);
+                for (int i = 0; i < 8; ++i) store_piece(k_chunk, raw[i], 8 * dw + i, q4, flip_k, pl);
+                fence_async_smem();
+                warp_arrive_first(&bars[kBarK0], lane);
+                store_piece(sm + kOffK + kRope * kChunkBytes, rope, 8 * dw + oc, q4, 0, pl);   // two rows: phases differ
+                fence_async_smem();
+                warp_arrive_first(&bars[kBarK0 + 1], lane);
+                if (t + 1 < w.steps) request_k(t + 1);
+                if (t > 0) {
+                    if (!(ok = store_v(it - 1))) break;
+                    request_v(t);
+                } else if (n > 0 && !(ok = warp_wait(&bars[kBarOut], (uint32_t)(n - 1) & 1u, sAbort, wl))) {
+                    break;   // (the context buffer staged the last segment's output)
                 }
-                if (t > 0 && !(ok = store_v(it - 1))) break;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // this CTA's dims of the own row: chunks 4 (i / 2) + 2 rank + i % 2
-                    v_own[i] = rank ? raw[4 * (i >> 1) + 2 + (i & 1)] : raw[4 * (i >> 1) + (i & 1)];
-                    v_peer[i] = next[i];
-                }
-                // the context buffer may stage the last segment's output
-                if (t == 0 && n > 0 && !(ok = warp_wait(&bars[kBarOut], (uint32_t)(n - 1) & 1u, sAbort, wl))) break;
-                if (t + 1 < w.steps) request(t + 1);
             }
             if (ok) ok = store_v(it - 1);
         }
     } else {
         // ================= softmax warps =================
-        const int r = tid & (kHalf - 1), half = tid >> 6;   // vector (of this CTA); rows 64 half .. + 63 of a step
-        const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        // vector (of this CTA); rows 64 half + 32 sub .. + 31 of a step
+        const int r = tid & (kHalf - 1), half = (tid >> 6) & 1, sub = tid >> 7;
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         unsigned char* sP = sm + kOffP + half * kChunkBytes;
+        // between the four threads of a vector: the weights' buffer, while no step's weights are in it
+        float* sX = reinterpret_cast<float*>(sm + kOffP);
         uint32_t it = 0;
         bool aborted = false;
         for (int n = 0;; ++n) {
@@ -530,103 +613,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // vectors past the tile's last repeat its limit: they score 0 and are dropped
             const int vec = kHalf * rank + r;
             const int32_t lim = (int32_t)max((int64_t)0, w.base + 1 + (w.tok0 + min(vec, w.rows - 1)) / p.n_heads);
-            // this thread's row of a step, for its scales: page, then scales, a step ahead of their use
-            const int32_t* table = p.table + (int64_t)w.b * p.table_stride;
-            const int32_t end = w.end;
-            int32_t id_next = 0;
-            float2 scale_next = make_float2(0.f, 0.f);
-            auto ask = [&](int t) {
-                const int32_t x = first + t * kRows + tid;
-                id_next = t < steps && x < end ? __ldg(table + (x >> p.shift)) : 0;
-            };
-            auto request = [&](int t) {
-                const int32_t x = first + t * kRows + tid;
-                scale_next = make_float2(0.f, 0.f);
-                if (t < steps && x < end) {
-                    const int32_t id = id_next < 0 || id_next >= p.n_pages ? 0 : id_next;   // the decode warps report it
-                    const float* s = p.scales + (((int64_t)id << p.shift) + (x & ((1 << p.shift) - 1))) * p.n_blocks;
-                    scale_next = make_float2(__ldg(s), __ldg(s + p.n_blocks - 1));
-                }
-                ask(t + 1);
-            };
-            ask(0);
-            request(0);
             RowState st{-INFINITY, -INFINITY, 0.0f, 0.0f, 0.0f, false};
             if (!warp_wait(&bars[kBarQ0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl)) aborted = true;
             const float cz = reinterpret_cast<const float*>(sm + kOffCz)[(n & 1) * kHalf + r];
 
             for (int t = 0; t < steps; ++t, ++it) {
-                float2* sScale = reinterpret_cast<float2*>(sm + kOffScale + (it & 1u) * kScaleBytes);
-                float* sMax = reinterpret_cast<float*>(sm + kOffMax) + (it & 1u) * kSoftWarps;
-                sScale[tid] = scale_next;
-                {
-                    const float top = warp_max(scale_next.x);
-                    if (lane == 0) sMax[warp] = top;
-                }
-                request(t + 1);
-                worker_sync<kSoft>();
+                warp_wait(&bars[kBarScale0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl);
                 warp_wait(&bars[kBarScore0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl);
                 tc_after();
-                const float4* sc4 = reinterpret_cast<const float4*>(sScale + kHalf * half);   // (s_L, s_R) of two rows
-                const uint32_t ts = tmem + lane_base + kColS + 128 * (it & 1u);
-                const int32_t t0 = first + t * kRows + kHalf * half;
+                const float2* sScale = reinterpret_cast<const float2*>(sm + kOffScale + (it & 1u) * kScaleBytes) +
+                                       kHalf * half + kCols * sub;
+                const float4* sc4 = reinterpret_cast<const float4*>(sScale);   // (s_L, s_R) of two rows
+                const float smax = reinterpret_cast<const float*>(sm + kOffMax)[it & 1u];
+                const uint32_t ts = tmem + lane_base + kColS + 128 * (it & 1u) + kCols * sub;
+                const int32_t t0 = first + t * kRows + kHalf * half + kCols * sub;
                 const bool masked = first + (t + 1) * kRows > seen0;
-                float z[kHalf];
-                auto scores = [&](float sub) {   // z - sub of this vector's 64 rows
+                float z[kCols];
+                auto scores = [&](float ref) {   // z - ref of this thread's rows
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < kCols; c += 16) {
                         uint32_t a[16], b[16];
-                        tmem_ld16(ts + 16 * c, a);
-                        tmem_ld16(ts + 64 + 16 * c, b);
+                        tmem_ld16(ts + c, a);
+                        tmem_ld16(ts + 64 + c, b);
                         tmem_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
-                            const float4 s = sc4[8 * c + j / 2];
-                            z[16 * c + j] = fmaf(fmaf(__uint_as_float(a[j]), s.x, __uint_as_float(b[j]) * s.y), cz, -sub);
-                            z[16 * c + j + 1] =
-                                fmaf(fmaf(__uint_as_float(a[j + 1]), s.z, __uint_as_float(b[j + 1]) * s.w), cz, -sub);
+                            const float4 s = sc4[(c + j) / 2];
+                            z[c + j] = fmaf(fmaf(__uint_as_float(a[j]), s.x, __uint_as_float(b[j]) * s.y), cz, -ref);
+                            z[c + j + 1] =
+                                fmaf(fmaf(__uint_as_float(a[j + 1]), s.z, __uint_as_float(b[j + 1]) * s.w), cz, -ref);
                         }
                     }
                     if (masked) {
 #pragma unroll
-                        for (int j = 0; j < kHalf; ++j)
+                        for (int j = 0; j < kCols; ++j)
                             if (t0 + j >= lim) z[j] = -INFINITY;
                     }
                 };
                 scores(st.m);
                 float top[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
-                for (int j = 4; j < kHalf; ++j) top[j & 3] = fmaxf(top[j & 3], z[j]);
+                for (int j = 4; j < kCols; ++j) top[j & 3] = fmaxf(top[j & 3], z[j]);
                 const float dmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                const float smax = fmaxf(fmaxf(sMax[0], sMax[1]), fmaxf(sMax[2], sMax[3]));
                 const bool flag = aborted | (*sAbort != 0) | (smax * (st.none ? INFINITY : st.E) > kScaleLim) | (dmax > kLagLog2);
                 if (worker_any<kSoft>(flag)) {
                     // ---- exact path: row maxima, new references, O rescaled ----
-                    if (it > 0 && (!warp_wait(&bars[kBarCtx0], (it - 1) & 1u, sAbort, wl) ||
-                                   !warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)))
-                        aborted = true;
+                    if (it > 0 && !warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)) aborted = true;
                     if (worker_any<kSoft>(aborted | (*sAbort != 0))) {
                         aborted = true;
                         break;
                     }
                     tc_after();
-                    // the next step's scales are still in registers: their buffer
-                    // takes the exchange between the two halves of a vector
-                    float* sX = reinterpret_cast<float*>(sm + kOffScale + ((it & 1u) ^ 1u) * kScaleBytes);
                     scores(0.0f);
                     float zt = -INFINITY, yt = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < kHalf; ++j) {
-                        const float s = sScale[kHalf * half + j].x;
+                    for (int j = 0; j < kCols; ++j) {
+                        const float s = sScale[j].x;
                         zt = fmaxf(zt, z[j]);
                         yt = fmaxf(yt, z[j] + (s > 0.0f ? __log2f(s) : -INFINITY));   // -inf: an inert latent block
                     }
                     sX[tid] = zt;
                     sX[kSoft + tid] = yt;
                     worker_sync<kSoft>();
-                    zt = fmaxf(zt, sX[tid ^ kHalf]);
-                    yt = fmaxf(yt, sX[kSoft + (tid ^ kHalf)]);
-                    worker_sync<kSoft>();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        zt = fmaxf(zt, sX[kHalf * k + r]);
+                        yt = fmaxf(yt, sX[kSoft + kHalf * k + r]);
+                    }
+                    worker_sync<kSoft>();   // read before any thread's weights go there
                     const float mn = fmaxf(st.m, zt), rn = fmaxf(st.R, yt);
                     const bool inert = rn == -INFINITY;
                     const float le = fminf(mn - rn - kHeadroom, kLogEmax);
@@ -643,7 +697,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     st.none = inert && mn > -INFINITY;
                     if (t > 0) {
 #pragma unroll 1
-                        for (int c = 0; c < 16; ++c) {
+                        for (int c = 8 * sub; c < 8 * sub + 8; ++c) {   // 128 of the columns a thread
                             uint32_t o[16];
                             tmem_ld16(tmem + lane_base + kColO + 16 * c, o);
                             tmem_wait_ld();
@@ -656,10 +710,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     scores(st.m);
                 }
-                uint32_t pk[kHalf / 2];
+                uint32_t pk[kCols / 2];
                 float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int j = 0; j < kHalf; j += 2) {
+                for (int j = 0; j < kCols; j += 2) {
                     const float4 s = sc4[j / 2];
                     const float a = ex2(z[j]), b = ex2(z[j + 1]);
                     sum[0] += a;
@@ -668,38 +722,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     pk[j / 2] = *reinterpret_cast<const uint32_t*>(&h2);
                 }
                 st.l += sum[0] + sum[1];
+                warp_arrive(&bars[kBarScaleFree0 + (it & 1u)], lane);
                 // the weights of the step before have been read
-                if (it > 0) {
-                    warp_wait(&bars[kBarCtx0], (it - 1) & 1u, sAbort, wl);
-                    warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl);
-                }
+                if (it > 0) warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<uint4*>(sP + sw128(r, 16 * i)) =
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4*>(sP + sw128(r, 64 * sub + 16 * i)) =
                         make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
                 fence_async_smem();
                 tc_before();
                 warp_arrive_first(&bars[kBarP], lane);
             }
             // ---- output ----
-            if (!aborted && !(warp_wait(&bars[kBarCtx0], (it - 1) & 1u, sAbort, wl) &&
-                              warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)))
-                aborted = true;
+            if (!aborted && !warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)) aborted = true;
             if (worker_any<kSoft>(aborted)) {
                 aborted = true;
                 break;
             }
             tc_after();
-            float* sX = reinterpret_cast<float*>(sm + kOffScale + (it & 1u) * kScaleBytes);
             sX[tid] = st.l;
             worker_sync<kSoft>();
-            const float l = sX[r] + sX[kHalf + r];   // the same order in both halves
+            const float l = (sX[r] + sX[kHalf + r]) + (sX[2 * kHalf + r] + sX[3 * kHalf + r]);   // the same in all four
             worker_sync<kSoft>();
             const int64_t slot = w.slot;
             float f = st.R == -INFINITY ? 0.0f : ex2(-st.logE);
             if (TQ4) f *= 1.0f / kGamma;
             if (slot < 0) f = l == 0.0f ? 0.0f : f / l;   // no visible row: zeros
-            if (slot >= 0 && half == 0) {
+            if (slot >= 0 && tid < kHalf) {
                 float* ml = p.ws_ml + (slot * kVecs + vec) * 2;
                 ml[0] = st.m * kLn2;
                 ml[1] = l;
@@ -711,29 +760,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + w.row0 * kMlaDV;
             const int rows = w.rows;
-            // 16 dims of this vector: block c / 8 of 256, 128 half + 16 (c % 8)
+            // dims d0 + 16 c .. + 15 of this vector, c < 8
+            const int d0 = 256 * sub + 128 * half;
             auto context = [&](int c, float (&o)[16]) {
                 uint32_t u[16];
-                tmem_ld16(tmem + lane_base + kColO + 16 * c, u);
+                tmem_ld16(tmem + lane_base + kColO + 128 * sub + 16 * c, u);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(u[j]) * f;
-                return 256 * (c >> 3) + 128 * half + 16 * (c & 7);
             };
             if (slot >= 0) {
 #pragma unroll 2
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < 8; ++c) {
                     float o[16];
-                    const int d = context(c, o);
-                    float4* dst = reinterpret_cast<float4*>(p.ws_o + (slot * kVecs + vec) * kMlaDV + d);
+                    context(c, o);
+                    float4* dst = reinterpret_cast<float4*>(p.ws_o + (slot * kVecs + vec) * kMlaDV + d0 + 16 * c);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
             } else if (!TQ4) {
 #pragma unroll 2
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < 8; ++c) {
                     float o[16];
-                    const int d = context(c, o);
+                    context(c, o);
                     uint32_t h[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -741,7 +790,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         h[i] = *reinterpret_cast<const uint32_t*>(&b2);
                     }
                     if (vec < rows) {
-                        uint4* dst = reinterpret_cast<uint4*>(out + (int64_t)vec * kMlaDV + d);
+                        uint4* dst = reinterpret_cast<uint4*>(out + (int64_t)vec * kMlaDV + d0 + 16 * c);
                         dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
                         dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
                     }
@@ -754,12 +803,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int rr = 0; rr < 2; ++rr) {
                     if ((r >> 5) == rr) {
 #pragma unroll 2
-                        for (int c = 0; c < 16; ++c) {
+                        for (int c = 0; c < 8; ++c) {
                             float o[16];
-                            const int d = context(c, o);
+                            context(c, o);
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                *reinterpret_cast<float4*>(stage + lane * kMlaDV + 4 * ((d / 4 + i) ^ (lane & 7))) =
+                                *reinterpret_cast<float4*>(stage + lane * kMlaDV + 4 * (((d0 + 16 * c) / 4 + i) ^ (lane & 7))) =
                                     make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                         }
                     }
@@ -804,8 +853,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 template <bool TQ4>
 cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
-    cudaError_t e =
-        cudaFuncSetAttribute(paged_tensor_kernel<TQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemUsed);
+    // the decode warps' setmaxnreg.inc waits for registers the others released:
+    // launch only if the split adds up against the launch's own count
+    cudaFuncAttributes fa{};
+    cudaError_t e = cudaFuncGetAttributes(&fa, paged_tensor_kernel<TQ4>);
+    if (e != cudaSuccess) return e;
+    if (kSoft * kRegsSoft + kDec * kRegsDec + 128 * kRegsRest > kThreads * fa.numRegs) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(paged_tensor_kernel<TQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemUsed);
     if (e != cudaSuccess) return e;
     paged_tensor_kernel<TQ4><<<2 * kPagedPairs, kThreads, kSmemUsed, stream>>>(p);
     return cudaGetLastError();
