@@ -72,7 +72,7 @@ constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kOffQ + kChunks * kChunkBytes;
 constexpr uint32_t kOffV = kOffK + kChunks * kChunkBytes;   // 4 chunks: dims 256 j + 128 rank + 64 i
 constexpr uint32_t kOffP = kOffV + 4 * kVChunkBytes;        // weights: 2 chunks of 64 rows
-constexpr uint32_t kOffScale = kOffP + 2 * kChunkBytes;     // (s_L, s_R) of two steps' rows
+constexpr uint32_t kOffScale = kOffP + 2 * kChunkBytes;     // s_L, then s_R, of two steps' rows
 constexpr uint32_t kScaleBytes = kRows * 8;
 constexpr uint32_t kOffCz = kOffScale + 2 * kScaleBytes;    // score scale of a vector, two segments
 constexpr uint32_t kOffBar = kOffCz + 2 * kHalf * 4;
@@ -91,13 +91,13 @@ constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 
 // mbarriers.  In the first CTA, arrivals from both: score rows stored (latent,
 // rope), context rows stored (rows 0-63, 64-127), weights written.  In
-// each CTA: scores complete (by buffer; commits reach both CTAs), context complete
-// (by row half), segment announced, segment done with, queries stored, output
-// written, row scales stored and read,
+// each CTA: scores complete and their row scales stored (by buffer; commits reach
+// both CTAs), context complete (by row half), segment announced, segment done
+// with, queries stored, output written, row scales read,
 // every product complete, and one that nothing arrives on (the testing hook).
 enum {
     kBarK0 = 0, kBarV0 = 2, kBarP = 4, kBarScore0 = 5, kBarCtx0 = 7, kBarWork0 = 9, kBarWorkFree0 = 11, kBarQ0 = 13, kBarOut = 15,
-    kBarDone = 16, kBarNever = 17, kBarScale0 = 18, kBarScaleFree0 = 20, kNumBars = 22
+    kBarDone = 16, kBarNever = 17, kBarScaleFree0 = 18, kNumBars = 20
 };
 // Scores, announcements, queries and scales have two barriers each, used in turn:
 // their next but one event waits for whoever waits for this one, the next does not.
@@ -142,9 +142,23 @@ __device__ __forceinline__ bool idle_wait(uint64_t* bar, uint32_t parity, volati
     *abort_flag = 1;
     return false;
 }
+// A warp's bounded wait.  The abort flag is read between polls only: a shared
+// load takes some 200 cycles next to the operand reads of the products.
+__device__ __forceinline__ bool try_once(uint32_t a, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
+    const uint32_t a = smem_u32(bar);
+    if (__all_sync(kFull, try_once(a, parity))) return true;
     return __all_sync(kFull, mbar_wait(bar, parity, abort_flag, limit));
 }
+
 // One arrival of a warp on a barrier of its own CTA, or of the first CTA.  What
 // an arrival announces is this CTA's shared memory, read by this SM's tensor
 // core: the async-proxy fence before it has put the stores there, so the arrival
@@ -332,6 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                    : i == kBarOut     ? (uint32_t)kSoftWarps
                                    : (i == kBarWorkFree0 || i == kBarWorkFree0 + 1)
                                        ? (uint32_t)(kSoftWarps + kDecWarps + 1 + (rank == 0 ? 1 : 0))
+                                   : (i == kBarScore0 || i == kBarScore0 + 1) ? 2u
                                    : (i == kBarScaleFree0 || i == kBarScaleFree0 + 1) ? (uint32_t)kSoftWarps
                                                                                       : 1u;
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&bars[i])), "r"(count));
@@ -475,11 +490,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 4; ++i) top = fmaxf(top, v[i].x);
                 top = warp_max(top);
                 if (it >= 2 && !(ok = warp_wait(&bars[kBarScaleFree0 + (it & 1u)], (it / 2 - 1) & 1u, sAbort, wl))) break;
-                float4* dst = reinterpret_cast<float4*>(sm + kOffScale + (it & 1u) * kScaleBytes) + 2 * lane;
-                dst[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-                dst[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+                float4* dst = reinterpret_cast<float4*>(sm + kOffScale + (it & 1u) * kScaleBytes) + lane;
+                dst[0] = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
+                dst[kRows / 4] = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
                 if (lane == 0) reinterpret_cast<float*>(sm + kOffMax)[it & 1u] = top;
-                warp_arrive(&bars[kBarScale0 + (it & 1u)], lane);
+                warp_arrive(&bars[kBarScore0 + (it & 1u)], lane);
             }
         }
     }
@@ -618,12 +633,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float cz = reinterpret_cast<const float*>(sm + kOffCz)[(n & 1) * kHalf + r];
 
             for (int t = 0; t < steps; ++t, ++it) {
-                warp_wait(&bars[kBarScale0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl);
                 warp_wait(&bars[kBarScore0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl);
                 tc_after();
-                const float2* sScale = reinterpret_cast<const float2*>(sm + kOffScale + (it & 1u) * kScaleBytes) +
-                                       kHalf * half + kCols * sub;
-                const float4* sc4 = reinterpret_cast<const float4*>(sScale);   // (s_L, s_R) of two rows
+                const float* s_l = reinterpret_cast<const float*>(sm + kOffScale + (it & 1u) * kScaleBytes) + kHalf * half +
+                                   kCols * sub;
+                const int stop = *sAbort;   // read ahead of its use
                 const float smax = reinterpret_cast<const float*>(sm + kOffMax)[it & 1u];
                 const uint32_t ts = tmem + lane_base + kColS + 128 * (it & 1u) + kCols * sub;
                 const int32_t t0 = first + t * kRows + kHalf * half + kCols * sub;
@@ -637,11 +651,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tmem_ld16(ts + 64 + c, b);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const float4 s = sc4[(c + j) / 2];
-                            z[c + j] = fmaf(fmaf(__uint_as_float(a[j]), s.x, __uint_as_float(b[j]) * s.y), cz, -ref);
-                            z[c + j + 1] =
-                                fmaf(fmaf(__uint_as_float(a[j + 1]), s.z, __uint_as_float(b[j + 1]) * s.w), cz, -ref);
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 sl = *reinterpret_cast<const float4*>(s_l + c + j);
+                            const float4 sr = *reinterpret_cast<const float4*>(s_l + kRows + c + j);
+                            const float lv[4] = {sl.x, sl.y, sl.z, sl.w}, rv[4] = {sr.x, sr.y, sr.z, sr.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                z[c + j + k] = fmaf(fmaf(__uint_as_float(a[j + k]), lv[k], __uint_as_float(b[j + k]) * rv[k]),
+                                                    cz, -ref);
                         }
                     }
                     if (masked) {
@@ -655,7 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 4; j < kCols; ++j) top[j & 3] = fmaxf(top[j & 3], z[j]);
                 const float dmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                const bool flag = aborted | (*sAbort != 0) | (smax * (st.none ? INFINITY : st.E) > kScaleLim) | (dmax > kLagLog2);
+                const bool flag = aborted | (stop != 0) | (smax * (st.none ? INFINITY : st.E) > kScaleLim) | (dmax > kLagLog2);
                 if (worker_any<kSoft>(flag)) {
                     // ---- exact path: row maxima, new references, O rescaled ----
                     if (it > 0 && !warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)) aborted = true;
@@ -668,7 +685,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     float zt = -INFINITY, yt = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < kCols; ++j) {
-                        const float s = sScale[j].x;
+                        const float s = s_l[j];
                         zt = fmaxf(zt, z[j]);
                         yt = fmaxf(yt, z[j] + (s > 0.0f ? __log2f(s) : -INFINITY));   // -inf: an inert latent block
                     }
@@ -710,21 +727,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     scores(st.m);
                 }
+                // asked before the weights are computed, used after: has the context
+                // of the step before read its weights?
+                const bool free_p = it == 0 || try_once(smem_u32(&bars[kBarCtx0 + 1]), (it - 1) & 1u);
                 uint32_t pk[kCols / 2];
                 float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int j = 0; j < kCols; j += 2) {
-                    const float4 s = sc4[j / 2];
-                    const float a = ex2(z[j]), b = ex2(z[j + 1]);
-                    sum[0] += a;
-                    sum[1] += b;
-                    const __half2 h2 = __floats2half2_rn(a * (st.E * s.x), b * (st.E * s.z));
-                    pk[j / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+                for (int j = 0; j < kCols; j += 4) {
+                    const float4 sl = *reinterpret_cast<const float4*>(s_l + j);
+                    const float e[4] = {ex2(z[j]), ex2(z[j + 1]), ex2(z[j + 2]), ex2(z[j + 3])};
+                    sum[0] += e[0] + e[1];
+                    sum[1] += e[2] + e[3];
+                    const __half2 h0 = __floats2half2_rn(e[0] * (st.E * sl.x), e[1] * (st.E * sl.y));
+                    const __half2 h1 = __floats2half2_rn(e[2] * (st.E * sl.z), e[3] * (st.E * sl.w));
+                    pk[j / 2] = *reinterpret_cast<const uint32_t*>(&h0);
+                    pk[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
                 }
                 st.l += sum[0] + sum[1];
                 warp_arrive(&bars[kBarScaleFree0 + (it & 1u)], lane);
-                // the weights of the step before have been read
-                if (it > 0) warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl);
+                if (!__all_sync(kFull, free_p)) warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     *reinterpret_cast<uint4*>(sP + sw128(r, 64 * sub + 16 * i)) =
