@@ -89,15 +89,16 @@ static_assert(32 * kMlaDV * 4 <= 4 * kVChunkBytes, "output stage");
 
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 
-// mbarriers.  In the first CTA, arrivals from both: score rows stored (latent,
-// rope), context rows stored (rows 0-63, 64-127), weights written.  In
+// mbarriers.  In the first CTA, arrivals from both: score rows stored (dims 0-255,
+// the rest), context rows stored (rows 0-63, 64-127), weights written.  In
 // each CTA: scores complete and their row scales stored (by buffer; commits reach
 // both CTAs), context complete (by row half), segment announced, segment done
-// with, queries stored, output written, row scales read,
+// with, queries stored, output written, row scales read, dims 0-255 of the score
+// rows read,
 // every product complete, and one that nothing arrives on (the testing hook).
 enum {
     kBarK0 = 0, kBarV0 = 2, kBarP = 4, kBarScore0 = 5, kBarCtx0 = 7, kBarWork0 = 9, kBarWorkFree0 = 11, kBarQ0 = 13, kBarOut = 15,
-    kBarDone = 16, kBarNever = 17, kBarScaleFree0 = 18, kNumBars = 20
+    kBarDone = 16, kBarNever = 17, kBarScaleFree0 = 18, kBarKFree = 20, kNumBars = 21
 };
 // Scores, announcements, queries and scales have two barriers each, used in turn:
 // their next but one event waits for whoever waits for this one, the next does not.
@@ -156,7 +157,17 @@ __device__ __forceinline__ bool try_once(uint32_t a, uint32_t parity) {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
     const uint32_t a = smem_u32(bar);
     if (__all_sync(kFull, try_once(a, parity))) return true;
-    return __all_sync(kFull, mbar_wait(bar, parity, abort_flag, limit));
+    bool ok = false;
+    for (long long i = 0; i < limit; ++i) {
+        __nanosleep(20);   // leave the issue slots to the warps at work
+        if (__all_sync(kFull, try_once(a, parity))) {
+            ok = true;
+            break;
+        }
+        if ((i & 63) == 63 && __any_sync(kFull, *abort_flag != 0)) break;
+    }
+    if (!ok) *abort_flag = 1;
+    return ok;
 }
 
 // One arrival of a warp on a barrier of its own CTA, or of the first CTA.  What
@@ -195,10 +206,10 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
 }
 
 // ---- decode -------------------------------------------------------------------
-// 16 codes: a quarter of a row's 64-dim chunk.  32 lanes read a row's 512 latent
-// dims (or two rows' 256) in one run and store 32 bytes each in two 16-byte
-// stores; lanes of odd chunks store their upper half first, so that the 8 lanes a
-// store serves at a time (one row, two chunks) cover 8 different 16-byte units.
+// 16 codes: a quarter of a row's 64-dim chunk, 32 bytes of f16 in two 16-byte
+// stores.  A warp reads 256 dims of two rows; the 8 lanes that a store serves at
+// a time have one chunk of both rows, whose swizzle phases differ in the low bit:
+// 8 different 16-byte units.
 template <bool TQ4>
 struct PieceOf {
     using type = uint4;
@@ -214,20 +225,18 @@ using Piece = typename PieceOf<TQ4>::type;
 struct Planes {
     uint32_t lo[4], hi[4];
 };
-// `flip`: 16 for the lanes that store their upper half first, else 0.
-__device__ __forceinline__ void store_piece(unsigned char* chunk, const uint4& c, int row, int q, int flip, const Planes&) {
+__device__ __forceinline__ void store_piece(unsigned char* chunk, const uint4& c, int row, int q, const Planes&) {
     const uint32_t in[4] = {c.x, c.y, c.z, c.w};
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) e4m3x4_to_half2x2(in[i], w[2 * i], w[2 * i + 1]);
-    const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
-    *reinterpret_cast<uint4*>(chunk + sw128(row, (32 * q) ^ flip)) = flip ? hi : lo;
-    *reinterpret_cast<uint4*>(chunk + sw128(row, (32 * q + 16) ^ flip)) = flip ? lo : hi;
+    *reinterpret_cast<uint4*>(chunk + sw128(row, 32 * q)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(chunk + sw128(row, 32 * q + 16)) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 // Nibble codes by byte permutes over the low and the high bytes of the levels:
 // the low 3 bits of a code pick among levels 0-7 and 8-15, bit 3 between the two.
-__device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c, int row, int q, int flip, const Planes& t) {
-    const uint32_t in[2] = {flip ? c.y : c.x, flip ? c.x : c.y};
+__device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c, int row, int q, const Planes& t) {
+    const uint32_t in[2] = {c.x, c.y};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint32_t sel = in[i] & 0x77777777u, pick = ((in[i] >> 1) & 0x44444444u) | 0x32103210u;
@@ -240,7 +249,7 @@ __device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c
             w[2 * h] = __byte_perm(lo, hi, 0x5140u);
             w[2 * h + 1] = __byte_perm(lo, hi, 0x7362u);
         }
-        *reinterpret_cast<uint4*>(chunk + sw128(row, (32 * q + 16 * i) ^ flip)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(chunk + sw128(row, 32 * q + 16 * i)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -305,6 +314,37 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0,
                     __floats2half2_rn(v[2 * i] * scale, v[2 * i + 1] * scale);
         }
     }
+}
+
+// Two f32 operations in one instruction.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2(uint32_t a, uint32_t b) { return f2(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ float2 unpack(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
 }
 
 // A query vector's softmax state.
@@ -417,11 +457,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (!warp_wait(&bars[kBarK0 + gr], it & 1u, sAbort, wl)) return false;
                     tc_after();
 #pragma unroll
-                    for (int kc = gr ? kRope : 0; kc < (gr ? kChunks : kRope); ++kc)
+                    for (int kc = 4 * gr; kc < (gr ? kChunks : 4); ++kc)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             pair_mma(d + (kc < kRope ? 0 : 64), dq + kc * kStep + 2 * ks, dk + kc * kStep + 2 * ks,
                                      kIdescScore, ((kc == 0 || kc == kRope) && ks == 0) ? 0u : 1u);
+                    if (gr == 0) pair_commit(&bars[kBarKFree]);
                 }
                 pair_commit(&bars[kBarScore0 + (it & 1u)]);
                 return true;
@@ -512,18 +553,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // A warp has 8 consecutive rows of each half of a step (8 rows lie in one
         // page): of the CTA's own half for the scores, of both for the context.
-        //   score row i: lane has chunk lane / 4, quarter lane % 4; rope: row lane / 4
-        //   context rows 2 i, 2 i + 1: lane / 16 picks the row, m = lane % 16 the
-        //     quarter: chunk m / 4, quarter m % 4
+        //   rows 2 i, 2 i + 1: bit 2 of the lane picks the row, c = lane / 8 the chunk
+        //     (score chunk 4 g + c, g = 0, 1; context chunk c), lane % 4 the quarter
+        //   rope: row lane / 4, quarter lane % 4
         // The two are loaded apart, each straight into the registers it is stored
         // from once the load of the step before has left them: codes of the own
         // half come twice (L2 has room, 10% busy), but no loaded register is
         // moved, and so waited for, before its step.
-        const int oc = lane >> 2, q4 = lane & 3, m16 = lane & 15;
-        const int flip_k = (oc & 1) * 16, flip_v = ((m16 >> 2) & 1) * 16;
-        unsigned char* k_chunk = sm + kOffK + oc * kChunkBytes;
-        unsigned char* v_chunk = sm + kOffV + (m16 >> 2) * kVChunkBytes;
-        const int v_code = 256 * (m16 >> 3) + 128 * rank + 16 * (m16 & 7);   // first dim of the quarter
+        const int q4 = lane & 3, up = (lane >> 2) & 1, c4 = lane >> 3;
+        unsigned char* k_chunk = sm + kOffK + c4 * kChunkBytes;
+        unsigned char* v_chunk = sm + kOffV + c4 * kVChunkBytes;
+        const int k_piece = 4 * c4 + q4;                                            // 16-code piece of the row's 36
+        const int v_piece = 16 * (c4 >> 1) + 8 * rank + 4 * (c4 & 1) + q4;
         uint32_t it = 0;
         bool ok = true;
         auto score_done = [&](uint32_t s) { return warp_wait(&bars[kBarScore0 + (s & 1u)], (s >> 1) & 1u, sAbort, wl); };
@@ -544,25 +585,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 return p.codes + (((int64_t)id << p.shift) + (r & ((1 << p.shift) - 1))) * kRowBytes;
             };
             int32_t id_k = page(row_k), id_v[2] = {page(row_v), page(row_v + kHalf)};
-            P raw[8], rope, ctx[2][4];
+            P raw[2][4], rope, ctx[2][4];
             auto request_k = [&](int t) {
                 const int32_t r0 = row_k + t * kRows;
-                const uint8_t* a = code_rows(r0, id_k) + kQ * lane;
-                const uint8_t* b = a + oc * kRowBytes + kQ * (32 + q4 - lane);
+                const uint8_t* a = code_rows(r0, id_k);
+                const uint8_t* b = a + up * kRowBytes + kQ * k_piece;
+                const int last = w.end - r0 - up;   // rows 2 i up to here exist
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    raw[i] = r0 + i < w.end ? __ldg(reinterpret_cast<const P*>(a + i * kRowBytes)) : P{};
-                rope = r0 + oc < w.end ? __ldg(reinterpret_cast<const P*>(b)) : P{};
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        raw[g][i] = 2 * i < last ? __ldg(reinterpret_cast<const P*>(b + 2 * i * kRowBytes + 16 * kQ * g)) : P{};
+                rope = r0 + (lane >> 2) < w.end
+                           ? __ldg(reinterpret_cast<const P*>(a + (lane >> 2) * kRowBytes + kQ * (32 + q4)))
+                           : P{};
                 if (t + 1 < w.steps) id_k = page(r0 + kRows);
             };
             auto request_v = [&](int t) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int32_t r0 = row_v + t * kRows + kHalf * h;
-                    const uint8_t* a = code_rows(r0, id_v[h]) + (lane >> 4) * kRowBytes + v_code * kQ / 16;
+                    const uint8_t* a = code_rows(r0, id_v[h]) + up * kRowBytes + kQ * v_piece;
+                    const int last = w.end - r0 - up;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        ctx[h][i] = r0 + 2 * i + (lane >> 4) < w.end ? __ldg(reinterpret_cast<const P*>(a + 2 * i * kRowBytes)) : P{};
+                        ctx[h][i] = 2 * i < last ? __ldg(reinterpret_cast<const P*>(a + 2 * i * kRowBytes)) : P{};
                     if (t + 1 < w.steps) id_v[h] = page(r0 + kRows);
                 }
             };
@@ -572,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (s > 0 && !warp_wait(&bars[kBarCtx0 + h], (s - 1) & 1u, sAbort, wl)) return false;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        store_piece(v_chunk, ctx[h][i], kHalf * h + 8 * dw + 2 * i + (lane >> 4), q4, flip_v, pl);
+                        store_piece(v_chunk, ctx[h][i], kHalf * h + 8 * dw + 2 * i + up, q4, pl);
                     fence_async_smem();
                     warp_arrive_first(&bars[kBarV0 + h], lane);
                 }
@@ -586,12 +633,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             fence_async_smem();
             warp_arrive(&bars[kBarQ0 + (n & 1)], lane);
             for (int t = 0; t < w.steps; ++t, ++it) {
-                if (t > 0 && !(ok = score_done(it - 1))) break;
+                if (t > 0 && !(ok = warp_wait(&bars[kBarKFree], (it - 1) & 1u, sAbort, wl))) break;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) store_piece(k_chunk, raw[i], 8 * dw + i, q4, flip_k, pl);
+                for (int i = 0; i < 4; ++i) store_piece(k_chunk, raw[0][i], 8 * dw + 2 * i + up, q4, pl);
                 fence_async_smem();
                 warp_arrive_first(&bars[kBarK0], lane);
-                store_piece(sm + kOffK + kRope * kChunkBytes, rope, 8 * dw + oc, q4, 0, pl);   // two rows: phases differ
+                if (t > 0 && !(ok = score_done(it - 1))) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    store_piece(k_chunk + 4 * kChunkBytes, raw[1][i], 8 * dw + 2 * i + up, q4, pl);
+                store_piece(sm + kOffK + kRope * kChunkBytes, rope, 8 * dw + (lane >> 2), q4, pl);
                 fence_async_smem();
                 warp_arrive_first(&bars[kBarK0 + 1], lane);
                 if (t + 1 < w.steps) request_k(t + 1);
@@ -644,6 +695,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const bool masked = first + (t + 1) * kRows > seen0;
                 float z[kCols];
                 auto scores = [&](float ref) {   // z - ref of this thread's rows
+                    const F2 cz2 = f2(cz, cz), ref2 = f2(-ref, -ref);
 #pragma unroll
                     for (int c = 0; c < kCols; c += 16) {
                         uint32_t a[16], b[16];
@@ -654,11 +706,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         for (int j = 0; j < 16; j += 4) {
                             const float4 sl = *reinterpret_cast<const float4*>(s_l + c + j);
                             const float4 sr = *reinterpret_cast<const float4*>(s_l + kRows + c + j);
-                            const float lv[4] = {sl.x, sl.y, sl.z, sl.w}, rv[4] = {sr.x, sr.y, sr.z, sr.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                z[c + j + k] = fmaf(fmaf(__uint_as_float(a[j + k]), lv[k], __uint_as_float(b[j + k]) * rv[k]),
-                                                    cz, -ref);
+                            const F2 z0 = fma2(fma2(f2(a[j], a[j + 1]), f2(sl.x, sl.y), mul2(f2(b[j], b[j + 1]), f2(sr.x, sr.y))),
+                                               cz2, ref2);
+                            const F2 z1 = fma2(
+                                fma2(f2(a[j + 2], a[j + 3]), f2(sl.z, sl.w), mul2(f2(b[j + 2], b[j + 3]), f2(sr.z, sr.w))), cz2,
+                                ref2);
+                            const float2 u0 = unpack(z0), u1 = unpack(z1);
+                            z[c + j] = u0.x;
+                            z[c + j + 1] = u0.y;
+                            z[c + j + 2] = u1.x;
+                            z[c + j + 3] = u1.y;
                         }
                     }
                     if (masked) {
@@ -731,19 +788,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // of the step before read its weights?
                 const bool free_p = it == 0 || try_once(smem_u32(&bars[kBarCtx0 + 1]), (it - 1) & 1u);
                 uint32_t pk[kCols / 2];
-                float sum[2] = {0.0f, 0.0f};
+                F2 sum2 = f2(0.0f, 0.0f);
+                const F2 e2 = f2(st.E, st.E);
 #pragma unroll
                 for (int j = 0; j < kCols; j += 4) {
                     const float4 sl = *reinterpret_cast<const float4*>(s_l + j);
                     const float e[4] = {ex2(z[j]), ex2(z[j + 1]), ex2(z[j + 2]), ex2(z[j + 3])};
-                    sum[0] += e[0] + e[1];
-                    sum[1] += e[2] + e[3];
-                    const __half2 h0 = __floats2half2_rn(e[0] * (st.E * sl.x), e[1] * (st.E * sl.y));
-                    const __half2 h1 = __floats2half2_rn(e[2] * (st.E * sl.z), e[3] * (st.E * sl.w));
+                    const F2 p0 = f2(e[0], e[1]), p1 = f2(e[2], e[3]);
+                    sum2 = add2(sum2, add2(p0, p1));
+                    const float2 w0 = unpack(mul2(p0, mul2(e2, f2(sl.x, sl.y))));
+                    const float2 w1 = unpack(mul2(p1, mul2(e2, f2(sl.z, sl.w))));
+                    const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
                     pk[j / 2] = *reinterpret_cast<const uint32_t*>(&h0);
                     pk[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
                 }
-                st.l += sum[0] + sum[1];
+                const float2 sum = unpack(sum2);
+                st.l += sum.x + sum.y;
                 warp_arrive(&bars[kBarScaleFree0 + (it & 1u)], lane);
                 if (!__all_sync(kFull, free_p)) warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl);
 #pragma unroll
