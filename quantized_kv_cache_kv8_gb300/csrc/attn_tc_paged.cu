@@ -18,14 +18,23 @@
 // (400 KB, 3.1k).  More vectors a CTA do not fit: 64 x 512 f32 of context are
 // half of a CTA's tensor memory.
 //
-// Codes become f16 operands in shared memory (e4m3 exactly, the 16 levels of
-// TQ4 times kGamma within 9.3e-5).  A bf16 query vector times a power of two of
-// its own is exact in f16 (down to 2^-24 of 2^14); the rotated query of TQ4 is
-// rounded once, 2^-12 relative.
+// Operands.  KV8: the scores run as fp8 MMAs on the codes themselves: TMA puts
+// them into swizzled shared memory page by page, no warp touches them, and they
+// take half the space of f16 (so a step's latent dims are loaded while the step
+// before is in use).  A bf16 query vector times a power of two of its own is
+// q1 + q2 in e4m3, the upper and the lower 4 of its 8 significant bits (exact for
+// elements over 2^-9 of the largest, off by at most 2^-17 of the largest below),
+// so each K step runs twice, with q1 and q2, in the time of one f16 step.  The
+// context needs weights with more range than fp8 has: its rows are decoded to f16
+// (e4m3 codes exactly).
+// TQ4: levels are no fp8 values; both operands are decoded to f16 (the 16 levels
+// times kGamma within 9.3e-5), and the rotated query is rounded to f16 once, 2^-12
+// relative.
 //
 // Roles (a CTA): 8 softmax warps, 8 decode warps, one issuing warp (in the first
-// CTA), one that announces segments, one that fetches row scales; registers move
-// to the decode warps, which hold a step's codes (setmaxnreg).  The decode warps store the score rows of
+// CTA; the second's passes on that its codes have arrived), one that announces
+// segments, one that fetches row scales, one that loads codes by TMA; registers
+// move to the decode warps, which hold a step's codes (setmaxnreg).  The decode warps store the score rows of
 // step t+1 once the scores of step t are complete and the context rows of step t
 // once the context of step t-1 is; the scores of t+1 are issued before the
 // context of t.  So the tensor pipe alternates between the two while the other
@@ -48,6 +57,7 @@
 #include "tc_common.cuh"
 #include "paged_common.cuh"
 
+#include <cuda.h>
 #include <math.h>
 
 namespace kvq {
@@ -60,14 +70,18 @@ constexpr int kHalf = 64;                    // query vectors, and score rows, o
 static_assert(kRows == 2 * kHalf && kVecs == 2 * kHalf, "pair layout");
 constexpr int kSoftWarps = 8, kDecWarps = 8;
 constexpr int kSoft = 32 * kSoftWarps, kDec = 32 * kDecWarps;
-constexpr int kIssueWarp = kSoftWarps + kDecWarps, kWalkWarp = kIssueWarp + 1, kScaleWarp = kIssueWarp + 2;
-constexpr int kThreads = kSoft + kDec + 128;   // five warpgroups; one warp of the last is idle
+constexpr int kIssueWarp = kSoftWarps + kDecWarps, kWalkWarp = kIssueWarp + 1, kScaleWarp = kIssueWarp + 2,
+              kLoadWarp = kIssueWarp + 3;
+constexpr int kThreads = kSoft + kDec + 128;   // five warpgroups
 constexpr int kRegsLaunch = 96, kRegsSoft = 88, kRegsDec = 120, kRegsRest = 64;
 static_assert(kSoft * kRegsSoft + kDec * kRegsDec + 128 * kRegsRest <= kThreads * kRegsLaunch, "register split");
 constexpr int kCols = 32;                    // rows of a step that a softmax thread has
-constexpr int kChunks = 9, kRope = 8;        // 64-dim chunks of a row: 8 latent, 1 rope
+constexpr int kChunks = 9, kRope = 8;        // TQ4: 64-dim f16 chunks of a row, 8 latent, 1 rope
 constexpr uint32_t kChunkBytes = kHalf * 128;   // 64 rows (or vectors) x 64 f16
 constexpr uint32_t kVChunkBytes = kRows * 128;  // 128 rows x 64 f16
+// KV8, the same nine places of 8 KB: queries q1 of 4 x 128 dims, q2 likewise, rope
+// (q1 in the lower 64 bytes of a row, q2 in the upper); codes of 4 x 128 dims of two
+// steps, and the row's last 128 bytes (the rope dims are the upper 64).
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kOffQ + kChunks * kChunkBytes;
 constexpr uint32_t kOffV = kOffK + kChunks * kChunkBytes;   // 4 chunks: dims 256 j + 128 rank + 64 i
@@ -76,7 +90,7 @@ constexpr uint32_t kOffScale = kOffP + 2 * kChunkBytes;     // s_L, then s_R, of
 constexpr uint32_t kScaleBytes = kRows * 8;
 constexpr uint32_t kOffCz = kOffScale + 2 * kScaleBytes;    // score scale of a vector, two segments
 constexpr uint32_t kOffBar = kOffCz + 2 * kHalf * 4;
-constexpr uint32_t kOffMax = kOffBar + 24 * 8;              // largest s_L of two steps
+constexpr uint32_t kOffMax = kOffBar + 26 * 8;              // largest s_L of two steps
 constexpr uint32_t kOffLevels = kOffMax + 16;
 constexpr uint32_t kOffMisc = kOffLevels + 32;              // abort flag, TMEM base
 constexpr uint32_t kOffWork = kOffMisc + 16;                // two segments, announced one ahead
@@ -93,12 +107,15 @@ constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 // the rest), context rows stored (rows 0-63, 64-127), weights written.  In
 // each CTA: scores complete and their row scales stored (by buffer; commits reach
 // both CTAs), context complete (by row half), segment announced, segment done
-// with, queries stored, output written, row scales read, dims 0-255 of the score
-// rows read,
+// with, queries stored, output written, row scales read,
 // every product complete, and one that nothing arrives on (the testing hook).
 enum {
     kBarK0 = 0, kBarV0 = 2, kBarP = 4, kBarScore0 = 5, kBarCtx0 = 7, kBarWork0 = 9, kBarWorkFree0 = 11, kBarQ0 = 13, kBarOut = 15,
-    kBarDone = 16, kBarNever = 17, kBarScaleFree0 = 18, kBarKFree = 20, kNumBars = 21
+    kBarDone = 16, kBarNever = 17, kBarScaleFree0 = 18,
+    // KV8: latent codes of a step (two buffers) and its rope codes have arrived
+    // here; in the first CTA, that they have arrived in the second
+    kBarLat0 = 20, kBarRope = 22, kBarPeerLat0 = 23, kBarPeerRope = 25, kNumBars = 26,
+    kBarQFirst = kBarK0   // KV8, in the first CTA: queries stored in both
 };
 // Scores, announcements, queries and scales have two barriers each, used in turn:
 // their next but one event waits for whoever waits for this one, the next does not.
@@ -106,7 +123,7 @@ enum {
 constexpr float kLagLog2 = 14.0f, kScaleLim = 3.5f, kHeadroom = 3.0f, kLogEmax = 120.0f;
 // levels times this round to f16 within 9.3e-5 (unscaled: 3.2e-4); divided out in f32
 constexpr float kGamma = 1.3338516f;
-constexpr uint32_t kIdescScore = idesc_f16(kVecs, kRows, false, false);
+constexpr uint32_t kIdescScore = idesc_f16(kVecs, kRows, false, false);   // e4m3 x e4m3 has the same bits
 constexpr uint32_t kIdescCtx = idesc_f16(kVecs, 256, false, true);
 
 // A segment as the roles use it; steps = 0 ends the walk.
@@ -159,7 +176,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     if (__all_sync(kFull, try_once(a, parity))) return true;
     bool ok = false;
     for (long long i = 0; i < limit; ++i) {
-        __nanosleep(20);   // leave the issue slots to the warps at work
         if (__all_sync(kFull, try_once(a, parity))) {
             ok = true;
             break;
@@ -197,11 +213,30 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uin
         " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(acc));
 }
+__device__ __forceinline__ void pair_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
 __device__ __forceinline__ void pair_commit(uint64_t* bar) {
     asm volatile(
         "{\n .reg .pred q;\n .reg .b16 m;\n mov.b16 m, 3;\n elect.sync _|q, 0xffffffff;\n"
         " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}\n" ::"r"(
             smem_u32(bar))
+        : "memory");
+}
+
+// ---- loads (KV8) --------------------------------------------------------------
+__device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+// A box of pool rows [y, y + box) x bytes [x, x + 128), x a multiple of 16.
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int32_t x, int32_t y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
         : "memory");
 }
 
@@ -254,8 +289,9 @@ __device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c
 }
 
 // ---- queries ------------------------------------------------------------------
-// This CTA's 64 vectors, 8 a decode warp: to f16 under a power of two that puts
-// the largest element in [2^13, 2^14); sCz gets what undoes it in the score.
+// This CTA's 64 vectors, 8 a decode warp: to f16 (TQ4, rotated) or to a sum of two
+// e4m3 values, under a power of two of their own; sCz gets what undoes it in the
+// score.
 template <bool TQ4>
 __device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0, int rows, unsigned char* sQ,
                                              float* sCz, int warp, int lane) {
@@ -295,11 +331,13 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0,
 #pragma unroll
         for (int i = 0; i < 18; ++i) top = fmaxf(top, fabsf(v[i]));
         top = warp_max(top);
-        int e = 14;
+        // the power of two: largest element in [2^13, 2^14), for e4m3 in [128, 256)
+        constexpr int kTop = TQ4 ? 14 : 8;
+        int e = kTop;
         if (top > 0.0f && top <= 3.402823466e38f) frexpf(top, &e);
-        e = max(e, -100);   // 2^(14 - e) stays finite
-        const float scale = ldexpf(1.0f, 14 - e);
-        if (lane == 0) sCz[r] = p.sm_scale * kLog2e * ldexpf(1.0f, e - 14) * (TQ4 ? 1.0f / kGamma : 1.0f);
+        e = max(e, -100);   // 2^(kTop - e) stays finite
+        const float scale = ldexpf(1.0f, kTop - e);
+        if (lane == 0) sCz[r] = p.sm_scale * kLog2e * ldexpf(1.0f, e - kTop) * (TQ4 ? 1.0f / kGamma : 1.0f);
         if (TQ4) {
 #pragma unroll
             for (int i = 0; i < 18; ++i) {
@@ -309,9 +347,23 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0,
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 9; ++i)
-                *reinterpret_cast<__half2*>(sQ + i * kChunkBytes + sw128(r, lane * 4)) =
-                    __floats2half2_rn(v[2 * i] * scale, v[2 * i + 1] * scale);
+            for (int i = 0; i < 9; ++i) {
+                // q1 and what it leaves; an infinity becomes a NaN (the conversion would saturate it)
+                float2 x = make_float2(v[2 * i] * scale, v[2 * i + 1] * scale);
+                if (!(fabsf(x.x) <= 3.402823466e38f)) x.x = __int_as_float(0x7fffffff);
+                if (!(fabsf(x.y) <= 3.402823466e38f)) x.y = __int_as_float(0x7fffffff);
+                const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3);
+                const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+                const __nv_fp8x2_storage_t lo =
+                    __nv_cvt_float2_to_fp8x2(make_float2(x.x - h.x, x.y - h.y), __NV_SATFINITE, __NV_E4M3);
+                const int d = 2 * (lane + 32 * i);   // latent: chunk d / 128; rope: dims 512 + 2 lane
+                unsigned char* c = sQ + (i < 8 ? (d >> 7) * kChunkBytes : kRope * kChunkBytes);
+                unsigned char* at1 = c + sw128(r, i < 8 ? d & 127 : d - 512);
+                unsigned char* at2 = i < 8 ? c + 4 * kChunkBytes + sw128(r, d & 127) : c + sw128(r, 64 + d - 512);
+                *reinterpret_cast<__nv_fp8x2_storage_t*>(at1) = hi;
+                *reinterpret_cast<__nv_fp8x2_storage_t*>(at2) = lo;
+            }
         }
     }
 }
@@ -355,7 +407,7 @@ struct RowState {
 
 template <bool TQ4>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    paged_tensor_kernel(const __grid_constant__ PagedParams p) {
+    paged_tensor_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap map) {
     launch_dependents();
     extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
@@ -385,7 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                    : (i == kBarQ0 || i == kBarQ0 + 1) ? (uint32_t)kDecWarps
                                    : i == kBarOut     ? (uint32_t)kSoftWarps
                                    : (i == kBarWorkFree0 || i == kBarWorkFree0 + 1)
-                                       ? (uint32_t)(kSoftWarps + kDecWarps + 1 + (rank == 0 ? 1 : 0))
+                                       ? (uint32_t)(kSoftWarps + kDecWarps + 1 + (TQ4 ? (rank == 0 ? 1 : 0) : 2))
                                    : (i == kBarScore0 || i == kBarScore0 + 1) ? 2u
                                    : (i == kBarScaleFree0 || i == kBarScaleFree0 + 1) ? (uint32_t)kSoftWarps
                                                                                       : 1u;
@@ -452,17 +504,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (p.stall_polls > 0) ok = warp_wait(&bars[kBarNever], 0u, sAbort, p.stall_polls);
             auto scores = [&](uint32_t it) {
                 const uint32_t d = tmem + kColS + 128 * (it & 1u);
+                if (TQ4) {
 #pragma unroll
-                for (int gr = 0; gr < 2; ++gr) {
-                    if (!warp_wait(&bars[kBarK0 + gr], it & 1u, sAbort, wl)) return false;
+                    for (int gr = 0; gr < 2; ++gr) {
+                        if (!warp_wait(&bars[kBarK0 + gr], it & 1u, sAbort, wl)) return false;
+                        tc_after();
+#pragma unroll
+                        for (int kc = 4 * gr; kc < (gr ? kChunks : 4); ++kc)
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                pair_mma(d + (kc < kRope ? 0 : 64), dq + kc * kStep + 2 * ks, dk + kc * kStep + 2 * ks,
+                                         kIdescScore, ((kc == 0 || kc == kRope) && ks == 0) ? 0u : 1u);
+                    }
+                } else {
+                    if (!warp_wait(&bars[kBarLat0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl)) return false;
+                    if (!warp_wait(&bars[kBarPeerLat0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl)) return false;
                     tc_after();
+                    const uint64_t dl = dk + (it & 1u) * 4 * kStep;
 #pragma unroll
-                    for (int kc = 4 * gr; kc < (gr ? kChunks : 4); ++kc)
+                    for (int kc = 0; kc < 4; ++kc)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            pair_mma(d + (kc < kRope ? 0 : 64), dq + kc * kStep + 2 * ks, dk + kc * kStep + 2 * ks,
-                                     kIdescScore, ((kc == 0 || kc == kRope) && ks == 0) ? 0u : 1u);
-                    if (gr == 0) pair_commit(&bars[kBarKFree]);
+#pragma unroll
+                            for (int part = 0; part < 2; ++part)
+                                pair_mma_f8(d, dq + (4 * part + kc) * kStep + 2 * ks, dl + kc * kStep + 2 * ks, kIdescScore,
+                                            (kc > 0 || ks > 0 || part > 0) ? 1u : 0u);
+                    if (!warp_wait(&bars[kBarRope], it & 1u, sAbort, wl)) return false;
+                    if (!warp_wait(&bars[kBarPeerRope], it & 1u, sAbort, wl)) return false;
+                    tc_after();
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+                            pair_mma_f8(d + 64, dq + kRope * kStep + 4 * part + 2 * ks, dk + kRope * kStep + 4 + 2 * ks,
+                                        kIdescScore, (ks > 0 || part > 0) ? 1u : 0u);
                 }
                 pair_commit(&bars[kBarScore0 + (it & 1u)]);
                 return true;
@@ -474,6 +549,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int steps = __shfl_sync(kFull, sWork[n & 1].steps, 0);
                 warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
                 if (steps == 0) break;
+                if (!TQ4) {   // TQ4: the score rows come after the queries of the same warps
+                    ok = warp_wait(&bars[kBarQFirst], (uint32_t)n & 1u, sAbort, wl);
+                    if (!ok) break;
+                }
                 ok = scores(it);
                 for (int t = 0; t < steps && ok; ++t, ++it) {
                     // the other score buffer is free: its weights were written before the last context
@@ -498,6 +577,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             pair_commit(&bars[kBarDone]);
+        } else if (!TQ4) {
+            // ================= this CTA's codes are there: tell the first =================
+            uint32_t it = 0;
+            bool ok = true;
+            for (int n = 0; ok; ++n) {
+                if (!(ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl))) break;
+                const int steps = __shfl_sync(kFull, sWork[n & 1].steps, 0);
+                warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
+                if (steps == 0) break;
+                for (int t = 0; t < steps && ok; ++t, ++it) {
+                    if (!(ok = warp_wait(&bars[kBarLat0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl))) break;
+                    warp_arrive_first(&bars[kBarPeerLat0 + (it & 1u)], lane);
+                    if (!(ok = warp_wait(&bars[kBarRope], it & 1u, sAbort, wl))) break;
+                    warp_arrive_first(&bars[kBarPeerRope], lane);
+                }
+            }
+        }
+    } else if (warp == kLoadWarp) {
+        if (!TQ4) {
+            // ================= codes of the score rows, by TMA =================
+            // this CTA's 64 rows of a step in boxes of whole pages (64 rows at
+            // most): lanes 0-15 a box and 128 latent dims each, lanes 16-19 a box's
+            // last 128 bytes.  Boxes past the sequence's end are left as they are:
+            // the softmax drops their scores.
+            const int box = min(1 << p.shift, kHalf);
+            const int j = lane < 16 ? lane >> 2 : lane - 16, c = lane < 16 ? lane & 3 : 0;
+            const bool mine = lane < 20 && j * box < kHalf;
+            uint32_t it = 0;
+            bool ok = true;
+            for (int n = 0; ok; ++n) {
+                if (!(ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl))) break;
+                const Work w = sWork[n & 1];
+                warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
+                if (w.steps == 0) break;
+                const int32_t* table = p.table + (int64_t)w.b * p.table_stride;
+                const int32_t row0 = w.first + kHalf * rank + j * box;
+                auto page = [&](int t) {
+                    const int32_t r = row0 + t * kRows;
+                    return mine && t < w.steps && r < w.end ? __ldg(table + (r >> p.shift)) : 0;
+                };
+                int32_t id = page(0);
+                for (int t = 0; t < w.steps; ++t, ++it) {
+                    const int32_t r = row0 + t * kRows;
+                    const bool live = mine && r < w.end;
+                    if (id < 0 || id >= p.n_pages) id = 0;   // the decode warps report it
+                    const int32_t y = (id << p.shift) + (r & ((1 << p.shift) - 1));
+                    const uint32_t boxes = __popc(__ballot_sync(kFull, live && lane >= 16));
+                    id = page(t + 1);
+                    if (it >= 2 && !(ok = warp_wait(&bars[kBarScore0 + (it & 1u)], (it / 2 - 1) & 1u, sAbort, wl))) break;
+                    if (lane == 0) expect_bytes(&bars[kBarLat0 + (it & 1u)], boxes * box * 512);
+                    __syncwarp();
+                    if (live && lane < 16)
+                        load_box(sm + kOffK + (4 * (it & 1u) + c) * kChunkBytes + j * box * 128, &map, 128 * c, y,
+                                 &bars[kBarLat0 + (it & 1u)]);
+                    if (it >= 1 && !(ok = warp_wait(&bars[kBarScore0 + ((it - 1) & 1u)], ((it - 1) >> 1) & 1u, sAbort, wl))) break;
+                    if (lane == 0) expect_bytes(&bars[kBarRope], boxes * box * 128);
+                    __syncwarp();
+                    if (live && lane >= 16)
+                        load_box(sm + kOffK + kRope * kChunkBytes + j * box * 128, &map, kMlaD - 128, y, &bars[kBarRope]);
+                }
+            }
         }
     } else if (warp == kScaleWarp) {
         // ================= row scales, two steps ahead =================
@@ -625,27 +765,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 return true;
             };
-            request_k(0);
+            if (TQ4) request_k(0);
             request_v(0);
             if (it > 0 && !(ok = score_done(it - 1))) break;
             load_queries<TQ4>(p, w.row0 + kHalf * rank, w.rows - kHalf * rank, sm + kOffQ,
                               reinterpret_cast<float*>(sm + kOffCz) + (n & 1) * kHalf, dw, lane);
             fence_async_smem();
             warp_arrive(&bars[kBarQ0 + (n & 1)], lane);
+            if (!TQ4) warp_arrive_first(&bars[kBarQFirst], lane);
             for (int t = 0; t < w.steps; ++t, ++it) {
-                if (t > 0 && !(ok = warp_wait(&bars[kBarKFree], (it - 1) & 1u, sAbort, wl))) break;
+                if (TQ4) {
+                    if (t > 0 && !(ok = score_done(it - 1))) break;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) store_piece(k_chunk, raw[0][i], 8 * dw + 2 * i + up, q4, pl);
-                fence_async_smem();
-                warp_arrive_first(&bars[kBarK0], lane);
-                if (t > 0 && !(ok = score_done(it - 1))) break;
+                    for (int i = 0; i < 4; ++i) store_piece(k_chunk, raw[0][i], 8 * dw + 2 * i + up, q4, pl);
+                    fence_async_smem();
+                    warp_arrive_first(&bars[kBarK0], lane);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    store_piece(k_chunk + 4 * kChunkBytes, raw[1][i], 8 * dw + 2 * i + up, q4, pl);
-                store_piece(sm + kOffK + kRope * kChunkBytes, rope, 8 * dw + (lane >> 2), q4, pl);
-                fence_async_smem();
-                warp_arrive_first(&bars[kBarK0 + 1], lane);
-                if (t + 1 < w.steps) request_k(t + 1);
+                    for (int i = 0; i < 4; ++i)
+                        store_piece(k_chunk + 4 * kChunkBytes, raw[1][i], 8 * dw + 2 * i + up, q4, pl);
+                    store_piece(sm + kOffK + kRope * kChunkBytes, rope, 8 * dw + (lane >> 2), q4, pl);   // two rows: phases differ
+                    fence_async_smem();
+                    warp_arrive_first(&bars[kBarK0 + 1], lane);
+                    if (t + 1 < w.steps) request_k(t + 1);
+                }
                 if (t > 0) {
                     if (!(ok = store_v(it - 1))) break;
                     request_v(t);
@@ -932,6 +1074,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
 }
 
+// The pool as a matrix of bytes, read in boxes of 128 bytes x `box` rows in the
+// 128-byte swizzle.
+cudaError_t pool_map(const PagedParams& p, CUtensorMap* map) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)kMlaD, (cuuint64_t)p.n_pages << p.shift};
+    const cuuint64_t strides[1] = {(cuuint64_t)kMlaD};
+    const cuuint32_t box[2] = {128, (cuuint32_t)(1 << p.shift < kHalf ? 1 << p.shift : kHalf)}, step[2] = {1, 1};
+    const CUresult r = reinterpret_cast<Encode>(fn)(
+        map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p.codes), dims, strides, box, step,
+        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <bool TQ4>
 cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
     // the decode warps' setmaxnreg.inc waits for registers the others released:
@@ -940,9 +1104,11 @@ cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
     cudaError_t e = cudaFuncGetAttributes(&fa, paged_tensor_kernel<TQ4>);
     if (e != cudaSuccess) return e;
     if (kSoft * kRegsSoft + kDec * kRegsDec + 128 * kRegsRest > kThreads * fa.numRegs) return cudaErrorInvalidConfiguration;
+    CUtensorMap map{};
+    if (!TQ4 && p.n_pages > 0 && (e = pool_map(p, &map)) != cudaSuccess) return e;
     e = cudaFuncSetAttribute(paged_tensor_kernel<TQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemUsed);
     if (e != cudaSuccess) return e;
-    paged_tensor_kernel<TQ4><<<2 * kPagedPairs, kThreads, kSmemUsed, stream>>>(p);
+    paged_tensor_kernel<TQ4><<<2 * kPagedPairs, kThreads, kSmemUsed, stream>>>(p, map);
     return cudaGetLastError();
 }
 
