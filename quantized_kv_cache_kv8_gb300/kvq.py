@@ -395,62 +395,81 @@ def kv_attn_prefill(fmt: int, x_new, q, codes, scales, n_past: int, out, workspa
 
 
 # -- paged pools ---------------------------------------------------------------
+# A serving loop makes these calls every step, on a few KB, so what they cost the
+# host is what they cost: each argument is checked once, in a few attribute reads,
+# and passed as a plain address.
 
-def _dev(t, dtype, name, shape=None):
-    """Pointer of a contiguous CUDA tensor on the current device, its type and shape checked."""
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return _ptr(t, dtype, name)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _here(stream):
+    """(current device index, stream handle)."""
+    dev = torch.cuda.current_device()
+    if stream is not None:
+        return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return dev, _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _at(t, dtype, dev, name, shape):
+    """Address of a contiguous tensor on the current device; its type and shape are checked."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, not on the current device")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def kv_pages_workspace_size() -> int:
     return lib().kv_pages_workspace_size()
 
 
-def _pages(block_table, free_pages, n_free, n_seq):
-    if block_table.dim() != 2 or block_table.shape[0] != n_seq:
-        raise ValueError("block_table must be [n_seq][table_stride]")
-    return (_dev(block_table, torch.int32, "block_table"), block_table.shape[1],
-            _dev(free_pages, torch.int32, "free_pages", (free_pages.numel(),)), _dev(n_free, torch.int32, "n_free", (1,)),
-            free_pages.numel())
+def _flat(t, name):
+    if t.dim() != 1:
+        raise ValueError(f"{name} must have one dimension")
+    return t.shape[0]
 
 
 def kv_pages_reserve(kv_lens, new_lens, block_table, free_pages, n_free, page_rows: int, lens_out, cu_new, slot_map,
                      positions, workspace, stream=None):
     """Pages, slots and positions for new_lens[s] new rows of every sequence (free_pages is the stack of all
     pages, n_free its height).  lens_out may be kv_lens, positions None."""
-    n = kv_lens.numel()
-    m = slot_map.numel()
-    table, stride, stack, height, n_pages = _pages(block_table, free_pages, n_free, n)
-    _ok(lib().kv_pages_reserve(n, page_rows, _dev(kv_lens, torch.int64, "kv_lens", (n,)),
-                               _dev(new_lens, torch.int64, "new_lens", (n,)), table, stride, stack, height, n_pages,
-                               _dev(lens_out, torch.int64, "lens_out", (n,)),
-                               _dev(cu_new, torch.int64, "cu_new", (n + 1,)),
-                               _dev(slot_map, torch.int64, "slot_map", (m,)),
-                               None if positions is None else _dev(positions, torch.int64, "positions", (m,)), m,
-                               _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)),
-        "kv_pages_reserve")
+    dev, st = _here(stream)
+    n, m, n_pages, stride = _flat(kv_lens, "kv_lens"), _flat(slot_map, "slot_map"), free_pages.numel(), block_table.shape[-1]
+    _ok((_lib or lib()).kv_pages_reserve(
+        n, page_rows, _at(kv_lens, torch.int64, dev, "kv_lens", (n,)), _at(new_lens, torch.int64, dev, "new_lens", (n,)),
+        _at(block_table, torch.int32, dev, "block_table", (n, stride)), stride,
+        _at(free_pages, torch.int32, dev, "free_pages", (n_pages,)), _at(n_free, torch.int32, dev, "n_free", (1,)), n_pages,
+        _at(lens_out, torch.int64, dev, "lens_out", (n,)), _at(cu_new, torch.int64, dev, "cu_new", (n + 1,)),
+        _at(slot_map, torch.int64, dev, "slot_map", (m,)),
+        None if positions is None else _at(positions, torch.int64, dev, "positions", (m,)), m,
+        _at(workspace, torch.uint8, dev, "workspace", workspace.shape), workspace.numel(), st), "kv_pages_reserve")
 
 
 def kv_pages_trim(kv_lens, keep_lens, block_table, free_pages, n_free, page_rows: int, workspace, stream=None):
     """Cuts every sequence back to keep_lens[s] rows (negative: keeps it, 0: ends it); its pages return to the stack."""
-    n = kv_lens.numel()
-    table, stride, stack, height, n_pages = _pages(block_table, free_pages, n_free, n)
-    _ok(lib().kv_pages_trim(n, page_rows, _dev(kv_lens, torch.int64, "kv_lens", (n,)),
-                            _dev(keep_lens, torch.int64, "keep_lens", (n,)), table, stride, stack, height, n_pages,
-                            _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)),
-        "kv_pages_trim")
+    dev, st = _here(stream)
+    n, n_pages, stride = _flat(kv_lens, "kv_lens"), free_pages.numel(), block_table.shape[-1]
+    _ok((_lib or lib()).kv_pages_trim(
+        n, page_rows, _at(kv_lens, torch.int64, dev, "kv_lens", (n,)), _at(keep_lens, torch.int64, dev, "keep_lens", (n,)),
+        _at(block_table, torch.int32, dev, "block_table", (n, stride)), stride,
+        _at(free_pages, torch.int32, dev, "free_pages", (n_pages,)), _at(n_free, torch.int32, dev, "n_free", (1,)), n_pages,
+        _at(workspace, torch.uint8, dev, "workspace", workspace.shape), workspace.numel(), st), "kv_pages_trim")
 
 
-def _strided(t, dims, name):
-    """A CUDA tensor whose last dimension is contiguous, on the current device."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+def _strided(t, dims, dev, name):
+    """Address and strides of a tensor on the current device whose last dimension is contiguous."""
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    st = t.stride()
+    if len(st) != dims or (st[-1] != 1 and t.shape[-1] > 1):
         raise ValueError(f"{name} must have {dims} dimensions, the last one contiguous")
-    return C.c_void_p(t.data_ptr())
+    return t.data_ptr(), st
 
 
 def kv_rope_append(fmt: int, rope: Rope, x_new, positions, slot_map, q_in, q_out, codes, scales,
@@ -460,31 +479,36 @@ def kv_rope_append(fmt: int, rope: Rope, x_new, positions, slot_map, q_in, q_out
     stored in the pool rows slot_map (negative: skipped).  positions int64 [n_axes][n] (or [n] for one axis).
     x_new None: only queries; q_in None: only rows."""
     layout = layout or mla_layout()
+    dev, st = _here(stream)
     D = layout.block_dim[0] + (layout.block_dim[1] if layout.n_blocks > 1 else 0)
+    dim, axes = rope.dim, rope.n_axes
     n = x_new.shape[0] if x_new is not None else q_in.shape[0]
-    shape = (n,) if positions.dim() == 1 and rope.n_axes == 1 else (rope.n_axes, n)
-    pos = _dev(positions, torch.int64, "positions", shape)
+    pos = _at(positions, torch.int64, dev, "positions", (n,) if axes == 1 and positions.dim() == 1 else (axes, n))
     xp = sp = cp = fp = None
     xd, xs, rows = KVQ_F32, 0, 0
     if x_new is not None:
-        xp, xd, xs = _strided(x_new, 2, "x_new"), _qdtype(x_new), x_new.stride(0)
+        xp, xs = _strided(x_new, 2, dev, "x_new")
+        xd, xs = _qdtype(x_new), xs[0]
         if x_new.shape[1] != D:
             raise ValueError(f"x_new must have {D} columns")
         rows = codes.shape[0]
-        sp = _dev(slot_map, torch.int64, "slot_map", (n,))
-        cp = _dev(codes, torch.uint8, "codes", (rows, row_bytes(fmt, layout)))
-        fp = _dev(scales, torch.float32, "scales", (rows, layout.n_blocks))
+        sp = _at(slot_map, torch.int64, dev, "slot_map", (n,))
+        cp = _at(codes, torch.uint8, dev, "codes", (rows, row_bytes(fmt, layout)))
+        fp = _at(scales, torch.float32, dev, "scales", (rows, layout.n_blocks))
     qi = qo = None
     qd, heads, si, so = KVQ_F32, 0, (0, 0), (0, 0)
     if q_in is not None:
-        qi, qd, heads, si = _strided(q_in, 3, "q_in"), _qdtype(q_in), q_in.shape[1], q_in.stride()
-        if q_out.shape[-1] == D and D != rope.dim:
-            q_out = q_out[..., D - rope.dim:]
-        if tuple(q_in.shape) != (n, heads, rope.dim) or q_out.shape != q_in.shape or q_out.dtype != q_in.dtype:
-            raise ValueError(f"q_in must be [{n}][n_heads][{rope.dim}] and q_out match it")
-        qo, so = _strided(q_out, 3, "q_out"), q_out.stride()
-    _ok(lib().kv_rope_append(fmt, C.byref(layout), C.byref(rope), xp, xd, xs, n, pos, n, sp, qi, qd, si[0], si[1], qo,
-                             so[0], so[1], heads, cp, fp, rows, _err_ptr(err_word), _stream(stream)), "kv_rope_append")
+        qi, si = _strided(q_in, 3, dev, "q_in")
+        qo, so = _strided(q_out, 3, dev, "q_out")
+        qd, heads = _qdtype(q_in), q_in.shape[1]
+        width = q_out.shape[2]
+        if q_in.shape != (n, heads, dim) or q_out.shape != (n, heads, width) or width not in (dim, D) or \
+                q_out.dtype is not q_in.dtype:
+            raise ValueError(f"q_in must be [{n}][n_heads][{dim}] and q_out match it")
+        qo += (width - dim) * q_out.element_size()
+    err = None if err_word is None else _err_ptr(err_word)
+    _ok((_lib or lib()).kv_rope_append(fmt, C.byref(layout), C.byref(rope), xp, xd, xs, n, pos, n, sp, qi, qd, si[0], si[1],
+                                       qo, so[0], so[1], heads, cp, fp, rows, err, st), "kv_rope_append")
 
 
 def kv_attn_paged_workspace_size(fmt: int, n_seq: int, n_heads: int, n_tokens: int, layout: MLALayout | None = None,
@@ -499,21 +523,19 @@ def kv_attn_paged(fmt: int, q, cu_q, codes, scales, block_table, kv_lens, page_r
     """Causal attention of the new tokens q [n_tokens][n_heads][576] (sequence b: q[cu_q[b]:cu_q[b+1]], the last
     of its kv_lens[b] rows) over paged rows; out [n_tokens][n_heads][512] in q's type."""
     layout = layout or mla_layout()
-    n, H, B = q.shape[0], q.shape[1], kv_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [n_seq][table_stride]")
-    rows = codes.shape[0]
+    dev, st = _here(stream)
+    n, H, B, rows, stride = q.shape[0], q.shape[1], _flat(kv_lens, "kv_lens"), codes.shape[0], block_table.shape[-1]
     if rows % page_rows != 0:
         raise ValueError("the pool must hold whole pages")
-    _ok(lib().kv_attn_paged(fmt, C.byref(layout), _dev(q, None, "q", (n, H, 576)), _qdtype(q), n, H, B,
-                            _dev(cu_q, torch.int64, "cu_q", (B + 1,)),
-                            _dev(codes, torch.uint8, "codes", (rows, row_bytes(fmt, layout))),
-                            _dev(scales, torch.float32, "scales", (rows, layout.n_blocks)),
-                            _dev(block_table, torch.int32, "block_table"), block_table.shape[1],
-                            _dev(kv_lens, torch.int64, "kv_lens", (B,)), page_rows, rows // page_rows,
-                            float(sm_scale), _dev(out, q.dtype, "out", (n, H, 512)),
-                            _dev(workspace, torch.uint8, "workspace"), workspace.numel(), path, _stream(stream)),
-        "kv_attn_paged")
+    qd = _qdtype(q)
+    _ok((_lib or lib()).kv_attn_paged(
+        fmt, C.byref(layout), _at(q, q.dtype, dev, "q", (n, H, 576)), qd, n, H, B,
+        _at(cu_q, torch.int64, dev, "cu_q", (B + 1,)), _at(codes, torch.uint8, dev, "codes", (rows, row_bytes(fmt, layout))),
+        _at(scales, torch.float32, dev, "scales", (rows, layout.n_blocks)),
+        _at(block_table, torch.int32, dev, "block_table", (B, stride)), stride,
+        _at(kv_lens, torch.int64, dev, "kv_lens", (B,)), page_rows, rows // page_rows, float(sm_scale),
+        _at(out, q.dtype, dev, "out", (n, H, 512)), _at(workspace, torch.uint8, dev, "workspace", workspace.shape),
+        workspace.numel(), path, st), "kv_attn_paged")
 
 
 def read_device_error(workspace, clear: bool = True, stream=None) -> int:
