@@ -299,21 +299,26 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
     }
 }
 
-// Joins the parts of the tile that CTA blockIdx.y began: vector blockIdx.x of
-// it, 128 threads with 4 dims each, by log-sum-exp.
+constexpr int kMergeRows = 4, kMergeNT = 128 * kMergeRows;
+
+// Joins the parts of the tile that walker blockIdx.y began, 4 vectors a CTA, 128
+// threads with 4 dims each to a vector, by log-sum-exp.  The grid covers every
+// walker; where none left a cut tile its CTAs return at once.
 template <bool TQ4, bool BF16, int M>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(kMergeNT) paged_merge_kernel(const __grid_constant__ PagedParams p) {
     using OT = typename std::conditional<BF16, __nv_bfloat16, float>::type;
-    __shared__ float ov[kMlaDV];
+    __shared__ float ov[kMergeRows][kMlaDV];
     const int64_t cta = blockIdx.y;
-    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+    const int sub = threadIdx.x >> 7, tid = threadIdx.x & 127, lane = tid & 31;
+    const int r = kMergeRows * blockIdx.x + sub;
     grid_dependency_wait();
     const int64_t parts = p.ws_desc[cta * 4], row0 = p.ws_desc[cta * 4 + 1];
-    if (parts == 0 || r >= p.ws_desc[cta * 4 + 2]) return;
+    const bool live = r < p.ws_desc[cta * 4 + 2];
+    if (parts == 0) return;
     float Mx = -INFINITY, L = 0.0f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int kBatch = 8;
-    for (int64_t c0 = 0; c0 < parts; c0 += kBatch) {
+    for (int64_t c0 = 0; live && c0 < parts; c0 += kBatch) {
         float mv[kBatch], lw[kBatch];
         float4 v[kBatch];
 #pragma unroll
@@ -353,15 +358,15 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
     OT* out = static_cast<OT*>(p.out);
     const int64_t at = (row0 + r) * kMlaDV;
     if (!TQ4) {
-        store_out(out, at + 4 * tid, acc);
+        if (live) store_out(out, at + 4 * tid, acc);
         return;
     }
-    *reinterpret_cast<float4*>(ov + 4 * tid) = acc;
+    *reinterpret_cast<float4*>(ov[sub] + 4 * tid) = acc;
     __syncthreads();
-    if (tid < 32) {
+    if (live && tid < 32) {
         float v[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = ov[lane + 32 * k];
+        for (int k = 0; k < 16; ++k) v[k] = ov[sub][lane + 32 * k];
         unrotate_out(p, v, out, at, lane);
     }
 }
@@ -378,8 +383,8 @@ cudaError_t launch_exact(const PagedParams& p, cudaStream_t stream) {
 template <bool TQ4, bool BF16, int M>
 cudaError_t launch_merge(const PagedParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(M, M == PagedTensor::kM ? kPagedPairs : kPagedCtas);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(M / kMergeRows, M == PagedTensor::kM ? kPagedPairs : kPagedCtas);
+    cfg.blockDim = dim3(kMergeNT);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

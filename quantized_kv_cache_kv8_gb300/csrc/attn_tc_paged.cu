@@ -289,80 +289,151 @@ __device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c
 }
 
 // ---- queries ------------------------------------------------------------------
+// Prologue and epilogue code runs once a segment and is fetched anew each time:
+// unrolled over their vectors these loops took 4 to 12 us in instruction fetches
+// alone, so they are kept rolled, with the next vector's loads in flight.
+
+// The 512-point transform of a row that a warp holds with element
+// 128 i + 4 lane + k in v[i][k] (unscaled): in registers over k and i, by shuffles
+// over the lanes.
+__device__ __forceinline__ void butterfly(float& a, float& b) {
+    const float s = a + b, d = a - b;
+    a = s;
+    b = d;
+}
+__device__ __forceinline__ void transform4(float (&v)[4]) {
+    butterfly(v[0], v[1]);
+    butterfly(v[2], v[3]);
+    butterfly(v[0], v[2]);
+    butterfly(v[1], v[3]);
+}
+template <int N>
+__device__ __forceinline__ void transform_lanes(float (&v)[N][4], int lanes, int lane) {
+#pragma unroll 1
+    for (int h = 1; h < lanes; h <<= 1) {
+        const float sign = (lane & h) ? -1.0f : 1.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[i][k] = fmaf(sign, v[i][k], __shfl_xor_sync(kFull, v[i][k], h));
+    }
+}
+__device__ __forceinline__ void transform512(float (&v)[4][4], int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) transform4(v[i]);
+    transform_lanes<4>(v, 32, lane);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        butterfly(v[0][k], v[1][k]);
+        butterfly(v[2][k], v[3][k]);
+        butterfly(v[0][k], v[2][k]);
+        butterfly(v[1][k], v[3][k]);
+    }
+}
+// The signs of elements 4 at .. 4 at + 3 of block b, one a bit.
+__device__ __forceinline__ uint32_t signs4(const SignWords& s, int b, int at) {
+    return (uint32_t)(s.w[s.block_word[b] + (at >> 4)] >> (4 * (at & 15))) & 15u;
+}
+__device__ __forceinline__ void apply_signs(float (&v)[4], uint32_t bits) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __int_as_float(__float_as_int(v[k]) ^ (int)((bits >> k) << 31));
+}
+
 // This CTA's 64 vectors, 8 a decode warp: to f16 (TQ4, rotated) or to a sum of two
 // e4m3 values, under a power of two of their own; sCz gets what undoes it in the
-// score.
+// score.  A lane has dims 128 i + 4 lane .. + 3 of a vector, the lower 16 lanes also
+// its rope dims 4 lane .. + 3.
 template <bool TQ4>
 __device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0, int rows, unsigned char* sQ,
                                              float* sCz, int warp, int lane) {
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
     constexpr int kPer = kHalf / kDecWarps;
-#pragma unroll 2
+    const uint2* src = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                      (row0 + kPer * warp) * kMlaD) + lane;
+    uint2 raw[5], next[5];
+    auto fetch = [&](int k, uint2 (&x)[5]) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+            x[i] = kPer * warp + k < rows && (i < 4 || lane < 16) ? __ldg(src + k * (kMlaD / 4) + 32 * i) : make_uint2(0u, 0u);
+    };
+    fetch(0, raw);
+#pragma unroll 1
     for (int k = 0; k < kPer; ++k) {
+        if (k + 1 < kPer) fetch(k + 1, next);
         const int r = kPer * warp + k;
-        float v[18];
-        const int64_t at = (row0 + r) * kMlaD;
+        float v[5][4];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            v[i][0] = __uint_as_float(raw[i].x << 16);
+            v[i][1] = __uint_as_float(raw[i].x & 0xffff0000u);
+            v[i][2] = __uint_as_float(raw[i].y << 16);
+            v[i][3] = __uint_as_float(raw[i].y & 0xffff0000u);
+            raw[i] = next[i];
+        }
         if (TQ4) {
-            // element lane + 32 i
+            float lat[4][4], rope[1][4];
 #pragma unroll
-            for (int i = 0; i < 18; ++i) v[i] = r < rows ? __bfloat162float(q[at + lane + 32 * i]) : 0.0f;
-            float rot[16], rope[2];
+            for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) rot[i] = sign_neg(p.signs, 0, lane + 32 * i) ? -v[i] : v[i];
-            warp_fwht<512>(rot, lane);
+                for (int e = 0; e < 4; ++e) lat[i][e] = v[i][e];
+                apply_signs(lat[i], signs4(p.signs, 0, 32 * i + lane));
+            }
+            transform512(lat, lane);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = rot[i] * p.kn[0];
+            for (int e = 0; e < 4; ++e) rope[0][e] = v[4][e];
+            apply_signs(rope[0], signs4(p.signs, 1, lane & 15));
+            transform4(rope[0]);
+            transform_lanes<1>(rope, 16, lane);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) rope[i] = sign_neg(p.signs, 1, lane + 32 * i) ? -v[16 + i] : v[16 + i];
-            warp_fwht<64>(rope, lane);
+            for (int e = 0; e < 4; ++e) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) v[16 + i] = rope[i] * p.kn[1];
-        } else {
-            // elements 2 (lane + 32 i), + 1
-            const uint32_t* qw = reinterpret_cast<const uint32_t*>(q + at);
-#pragma unroll
-            for (int i = 0; i < 9; ++i) {
-                const uint32_t w = r < rows ? __ldg(qw + lane + 32 * i) : 0u;
-                v[2 * i] = __uint_as_float(w << 16);
-                v[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+                for (int i = 0; i < 4; ++i) v[i][e] = lat[i][e] * p.kn[0];
+                v[4][e] = rope[0][e] * p.kn[1];
             }
         }
         float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 18; ++i) top = fmaxf(top, fabsf(v[i]));
+        for (int i = 0; i < 5; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(v[i][e]));
         top = warp_max(top);
-        // the power of two: largest element in [2^13, 2^14), for e4m3 in [128, 256)
+        // 2^shift puts the largest element into [2^13, 2^14), for e4m3 into [128, 256);
+        // |shift| <= 114 keeps it and its inverse normal numbers
         constexpr int kTop = TQ4 ? 14 : 8;
-        int e = kTop;
-        if (top > 0.0f && top <= 3.402823466e38f) frexpf(top, &e);
-        e = max(e, -100);   // 2^(kTop - e) stays finite
-        const float scale = ldexpf(1.0f, kTop - e);
-        if (lane == 0) sCz[r] = p.sm_scale * kLog2e * ldexpf(1.0f, e - kTop) * (TQ4 ? 1.0f / kGamma : 1.0f);
-        if (TQ4) {
+        int shift = 0;
+        if (top > 0.0f && top <= 3.402823466e38f)
+            shift = min(114, kTop + 126 - max((int)(__float_as_uint(top) >> 23), 1));
+        const float scale = __uint_as_float((uint32_t)(127 + shift) << 23);
+        if (lane == 0)
+            sCz[r] = p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 - shift) << 23) * (TQ4 ? 1.0f / kGamma : 1.0f);
 #pragma unroll
-            for (int i = 0; i < 18; ++i) {
-                const int d = lane + 32 * i;
-                *reinterpret_cast<__half*>(sQ + (d >> 6) * kChunkBytes + sw128(r, (d & 63) * 2)) =
-                    __float2half_rn(v[i] * scale);
-            }
-        } else {
+        for (int i = 0; i < 5; ++i) {
+            if (i == 4 && lane >= 16) break;
+            if (TQ4) {
+                const __half2 a = __floats2half2_rn(v[i][0] * scale, v[i][1] * scale);
+                const __half2 b = __floats2half2_rn(v[i][2] * scale, v[i][3] * scale);
+                unsigned char* c = sQ + (i < 4 ? 2 * i + (lane >> 4) : kRope) * kChunkBytes;
+                *reinterpret_cast<uint2*>(c + sw128(r, 8 * (lane & 15))) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+            } else {
+                uint32_t hi = 0u, lo = 0u;
 #pragma unroll
-            for (int i = 0; i < 9; ++i) {
-                // q1 and what it leaves; an infinity becomes a NaN (the conversion would saturate it)
-                float2 x = make_float2(v[2 * i] * scale, v[2 * i + 1] * scale);
-                if (!(fabsf(x.x) <= 3.402823466e38f)) x.x = __int_as_float(0x7fffffff);
-                if (!(fabsf(x.y) <= 3.402823466e38f)) x.y = __int_as_float(0x7fffffff);
-                const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
-                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3);
-                const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-                const __nv_fp8x2_storage_t lo =
-                    __nv_cvt_float2_to_fp8x2(make_float2(x.x - h.x, x.y - h.y), __NV_SATFINITE, __NV_E4M3);
-                const int d = 2 * (lane + 32 * i);   // latent: chunk d / 128; rope: dims 512 + 2 lane
-                unsigned char* c = sQ + (i < 8 ? (d >> 7) * kChunkBytes : kRope * kChunkBytes);
-                unsigned char* at1 = c + sw128(r, i < 8 ? d & 127 : d - 512);
-                unsigned char* at2 = i < 8 ? c + 4 * kChunkBytes + sw128(r, d & 127) : c + sw128(r, 64 + d - 512);
-                *reinterpret_cast<__nv_fp8x2_storage_t*>(at1) = hi;
-                *reinterpret_cast<__nv_fp8x2_storage_t*>(at2) = lo;
+                for (int h = 0; h < 2; ++h) {
+                    // q1 and what it leaves; an infinity becomes a NaN (the conversion would saturate it)
+                    float2 x = make_float2(v[i][2 * h] * scale, v[i][2 * h + 1] * scale);
+                    if (!(fabsf(x.x) <= 3.402823466e38f)) x.x = __int_as_float(0x7fffffff);
+                    if (!(fabsf(x.y) <= 3.402823466e38f)) x.y = __int_as_float(0x7fffffff);
+                    const __nv_fp8x2_storage_t c1 = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+                    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(c1, __NV_E4M3);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+                    const __nv_fp8x2_storage_t c2 =
+                        __nv_cvt_float2_to_fp8x2(make_float2(x.x - f.x, x.y - f.y), __NV_SATFINITE, __NV_E4M3);
+                    hi |= (uint32_t)c1 << (16 * h);
+                    lo |= (uint32_t)c2 << (16 * h);
+                }
+                unsigned char* c = sQ + (i < 4 ? i : kRope) * kChunkBytes;
+                *reinterpret_cast<uint32_t*>(c + sw128(r, 4 * lane)) = hi;
+                if (i < 4) *reinterpret_cast<uint32_t*>(c + 4 * kChunkBytes + sw128(r, 4 * lane)) = lo;
+                else *reinterpret_cast<uint32_t*>(c + sw128(r, 64 + 4 * lane)) = lo;
             }
         }
     }
@@ -397,6 +468,19 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     F2 r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
+}
+
+// 32 bytes: one store where the address is a multiple of 32 (`wide`), which fills
+// a sector at once, else two.
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        static_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        static_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
 }
 
 // A query vector's softmax state.
@@ -553,15 +637,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = warp_wait(&bars[kBarQFirst], (uint32_t)n & 1u, sAbort, wl);
                     if (!ok) break;
                 }
-                ok = scores(it);
-                for (int t = 0; t < steps && ok; ++t, ++it) {
-                    // the other score buffer is free: its weights were written before the last context
-                    if (t + 1 < steps && !(ok = scores(it + 1))) break;
-                    ok = warp_wait(&bars[kBarP], it & 1u, sAbort, wl);
+                // scores of step t, then the context of step t - 1; the other score
+                // buffer is free by then, as its weights came before the last context
+                for (int t = 0; t <= steps && ok; ++t) {
+                    if (t < steps && !(ok = scores(it + t))) break;
+                    if (t == 0) continue;
+                    const uint32_t s = it + t - 1;   // step of the context
+                    ok = warp_wait(&bars[kBarP], s & 1u, sAbort, wl);
                     if (!ok) break;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        ok = ok && warp_wait(&bars[kBarV0 + h], it & 1u, sAbort, wl);
+                        ok = ok && warp_wait(&bars[kBarV0 + h], s & 1u, sAbort, wl);
                         if (!ok) break;
                         tc_after();
 #pragma unroll
@@ -570,10 +656,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             for (int ks = 0; ks < 4; ++ks)
                                 pair_mma(tmem + kColO + 128 * j, dp + h * kStep + 2 * ks,
                                          dv + 2 * j * kVStep + (4 * h + ks) * 128, kIdescCtx,
-                                         (t > 0 || h > 0 || ks > 0) ? 1u : 0u);
+                                         (t > 1 || h > 0 || ks > 0) ? 1u : 0u);
                         pair_commit(&bars[kBarCtx0 + h]);
                     }
                 }
+                it += steps;
             }
             __syncwarp();
             pair_commit(&bars[kBarDone]);
@@ -765,17 +852,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 return true;
             };
-            if (TQ4) request_k(0);
-            request_v(0);
             if (it > 0 && !(ok = score_done(it - 1))) break;
             load_queries<TQ4>(p, w.row0 + kHalf * rank, w.rows - kHalf * rank, sm + kOffQ,
                               reinterpret_cast<float*>(sm + kOffCz) + (n & 1) * kHalf, dw, lane);
             fence_async_smem();
             warp_arrive(&bars[kBarQ0 + (n & 1)], lane);
             if (!TQ4) warp_arrive_first(&bars[kBarQFirst], lane);
-            for (int t = 0; t < w.steps; ++t, ++it) {
-                if (TQ4) {
-                    if (t > 0 && !(ok = score_done(it - 1))) break;
+            if (TQ4) request_k(0);
+            request_v(0);
+            // score rows of step t, then context rows of step t - 1
+            for (int t = 0; t <= w.steps; ++t) {
+                if (TQ4 && t < w.steps) {
+                    if (t > 0 && !(ok = score_done(it + t - 1))) break;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) store_piece(k_chunk, raw[0][i], 8 * dw + 2 * i + up, q4, pl);
                     fence_async_smem();
@@ -788,14 +876,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     warp_arrive_first(&bars[kBarK0 + 1], lane);
                     if (t + 1 < w.steps) request_k(t + 1);
                 }
-                if (t > 0) {
-                    if (!(ok = store_v(it - 1))) break;
-                    request_v(t);
-                } else if (n > 0 && !(ok = warp_wait(&bars[kBarOut], (uint32_t)(n - 1) & 1u, sAbort, wl))) {
-                    break;   // (the context buffer staged the last segment's output)
+                if (t == 0) {
+                    // (the context buffer staged the last segment's output)
+                    if (n > 0 && !(ok = warp_wait(&bars[kBarOut], (uint32_t)(n - 1) & 1u, sAbort, wl))) break;
+                    continue;
                 }
+                if (!(ok = store_v(it + t - 1))) break;
+                if (t < w.steps) request_v(t);
             }
-            if (ok) ok = store_v(it - 1);
+            it += w.steps;
         }
     } else {
         // ================= softmax warps =================
@@ -830,7 +919,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_after();
                 const float* s_l = reinterpret_cast<const float*>(sm + kOffScale + (it & 1u) * kScaleBytes) + kHalf * half +
                                    kCols * sub;
-                const int stop = *sAbort;   // read ahead of its use
+                const int seen_abort = *sAbort;   // read ahead of its use
                 const float smax = reinterpret_cast<const float*>(sm + kOffMax)[it & 1u];
                 const uint32_t ts = tmem + lane_base + kColS + 128 * (it & 1u) + kCols * sub;
                 const int32_t t0 = first + t * kRows + kHalf * half + kCols * sub;
@@ -866,21 +955,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             if (t0 + j >= lim) z[j] = -INFINITY;
                     }
                 };
-                scores(st.m);
-                float top[4] = {z[0], z[1], z[2], z[3]};
+                // The first step has no reference yet and goes to the exact path with
+                // plain scores; a later one comes back for them if a vote sends it there.
+                bool exact = t == 0, stop = false;
+                for (;;) {
+                    scores(exact ? 0.0f : st.m);
+                    if (!exact) {
+                        float top[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
-                for (int j = 4; j < kCols; ++j) top[j & 3] = fmaxf(top[j & 3], z[j]);
-                const float dmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                const bool flag = aborted | (stop != 0) | (smax * (st.none ? INFINITY : st.E) > kScaleLim) | (dmax > kLagLog2);
-                if (worker_any<kSoft>(flag)) {
+                        for (int j = 4; j < kCols; ++j) top[j & 3] = fmaxf(top[j & 3], z[j]);
+                        const float dmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                        const bool flag = aborted | (seen_abort != 0) | (smax * (st.none ? INFINITY : st.E) > kScaleLim) |
+                                          (dmax > kLagLog2);
+                        if (!worker_any<kSoft>(flag)) break;
+                        exact = true;
+                        continue;
+                    }
                     // ---- exact path: row maxima, new references, O rescaled ----
                     if (it > 0 && !warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)) aborted = true;
                     if (worker_any<kSoft>(aborted | (*sAbort != 0))) {
-                        aborted = true;
+                        stop = true;
                         break;
                     }
                     tc_after();
-                    scores(0.0f);
                     float zt = -INFINITY, yt = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < kCols; ++j) {
@@ -924,7 +1021,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tmem_wait_st();
                         if (tid == 0 && rank == 0) atomicAdd(p.exact_count, 1u);
                     }
-                    scores(st.m);
+                    // a vector that has seen no row keeps z = -inf
+                    const float ref = mn == -INFINITY ? 0.0f : mn;
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) z[j] -= ref;
+                    break;
+                }
+                if (stop) {
+                    aborted = true;
+                    break;
                 }
                 // asked before the weights are computed, used after: has the context
                 // of the step before read its weights?
@@ -983,6 +1088,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + w.row0 * kMlaDV;
             const int rows = w.rows;
+            const bool wide = (((uintptr_t)p.out | (uintptr_t)p.ws_o) & 31) == 0;
             // dims d0 + 16 c .. + 15 of this vector, c < 8
             const int d0 = 256 * sub + 128 * half;
             auto context = [&](int c, float (&o)[16]) {
@@ -993,16 +1099,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(u[j]) * f;
             };
             if (slot >= 0) {
-#pragma unroll 2
+#pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
                     float o[16];
                     context(c, o);
-                    float4* dst = reinterpret_cast<float4*>(p.ws_o + (slot * kVecs + vec) * kMlaDV + d0 + 16 * c);
+                    float* dst = p.ws_o + (slot * kVecs + vec) * kMlaDV + d0 + 16 * c;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t u[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(o[8 * h + i]);
+                        store32(dst + 8 * h, u, wide);
+                    }
                 }
             } else if (!TQ4) {
-#pragma unroll 2
+#pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
                     float o[16];
                     context(c, o);
@@ -1012,11 +1123,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
                         h[i] = *reinterpret_cast<const uint32_t*>(&b2);
                     }
-                    if (vec < rows) {
-                        uint4* dst = reinterpret_cast<uint4*>(out + (int64_t)vec * kMlaDV + d0 + 16 * c);
-                        dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
-                        dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
-                    }
+                    if (vec < rows) store32(out + (int64_t)vec * kMlaDV + d0 + 16 * c, h, wide);
                 }
             } else {
                 // unrotate: 32 vectors at a time through the context buffer (free
@@ -1025,7 +1132,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int rr = 0; rr < 2; ++rr) {
                     if ((r >> 5) == rr) {
-#pragma unroll 2
+#pragma unroll 1
                         for (int c = 0; c < 8; ++c) {
                             float o[16];
                             context(c, o);
@@ -1036,21 +1143,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     }
                     worker_sync<kSoft>();
+#pragma unroll 1
                     for (int k = warp; k < 32; k += kSoftWarps) {
                         const int ov = kHalf * rank + 32 * rr + k;
                         if (ov >= rows) break;
-                        float v[16];
+                        float v[4][4];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int e = lane + 32 * i;
-                            v[i] = stage[k * kMlaDV + 4 * ((e >> 2) ^ (k & 7)) + (e & 3)];
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 x = *reinterpret_cast<const float4*>(stage + k * kMlaDV + 4 * ((32 * i + lane) ^ (k & 7)));
+                            v[i][0] = x.x;
+                            v[i][1] = x.y;
+                            v[i][2] = x.z;
+                            v[i][3] = x.w;
                         }
-                        warp_fwht<512>(v, lane);
+                        transform512(v, lane);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int e = lane + 32 * i;
-                            const float y = v[i] * p.kn[0];
-                            out[(int64_t)ov * kMlaDV + e] = __float2bfloat16_rn(sign_neg(p.signs, 0, e) ? -y : y);
+                        for (int i = 0; i < 4; ++i) {
+                            apply_signs(v[i], signs4(p.signs, 0, 32 * i + lane));
+                            const __nv_bfloat162 a = __floats2bfloat162_rn(v[i][0] * p.kn[0], v[i][1] * p.kn[0]);
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(v[i][2] * p.kn[0], v[i][3] * p.kn[0]);
+                            *reinterpret_cast<uint2*>(out + (int64_t)ov * kMlaDV + 128 * i + 4 * lane) =
+                                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
                         }
                     }
                     worker_sync<kSoft>();

@@ -51,6 +51,13 @@ struct PagedParams {
     float lv[16];
 };
 
+// Quotient of non-negative integers: a 64-bit division takes some hundred
+// instructions, and nearly every one of these fits 32 bits.
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+    if (((uint64_t)a | (uint64_t)b) >> 32) return a / b;
+    return (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 struct SeqShape {
     int64_t q0, n_new, base, tiles, j0, D;
 };
@@ -68,6 +75,8 @@ template <int M, int N, int OV>
 struct PagedSched {
     static constexpr int kM = M, kN = N;
     static constexpr int64_t kRatio = N / M;
+    static constexpr int kLogM = M == 32 ? 5 : 7, kLogN = N == 32 ? 5 : 7;
+    static_assert((1 << kLogM) == M && (1 << kLogN) == N, "tile sizes");
 
     __device__ static SeqShape shape(const PagedParams& p, int b) {
         SeqShape s{0, 0, 0, 0, 0, 0};
@@ -83,18 +92,18 @@ struct PagedSched {
         s.q0 = a;
         s.n_new = e - a;
         s.base = kv - s.n_new;
-        s.tiles = (s.n_new * H + M - 1) / M;
-        s.j0 = s.base >= 0 ? 0 : (-s.base * H) / M;   // first tile with limit >= 1
+        s.tiles = (s.n_new * H + M - 1) >> kLogM;
+        s.j0 = s.base >= 0 ? 0 : (-s.base * H) >> kLogM;   // first tile with limit >= 1
         const int64_t C = H * (s.base + N) + M - 1;
-        s.D = C >= 0 ? C / M : -((-C + M - 1) / M);
+        s.D = C >> kLogM;   // floor, also below zero
         return s;
     }
     __device__ static int64_t units(const SeqShape& s, int64_t H, int64_t j) {
-        const int64_t tok = min(s.n_new - 1, (M * j + M - 1) / H);
-        return max((int64_t)1, (s.base + tok + 1 + N - 1) / N);
+        const int64_t tok = min(s.n_new - 1, quot(M * j + M - 1, H));
+        return max((int64_t)1, (s.base + tok + N) >> kLogN);
     }
     __device__ static int64_t floor_sum(int64_t n, int64_t d) {   // sum_{k<n} floor(k / d)
-        const int64_t q = n / d, r = n - q * d;
+        const int64_t q = quot(n, d), r = n - q * d;
         return d * (q * (q - 1) / 2) + q * r;
     }
     // numbers before tile j (j < tiles)
@@ -141,19 +150,18 @@ struct PagedWalk {
     SeqShape s;
     int64_t u0;
 
-    __device__ __forceinline__ int64_t start_of(int64_t c) const { return total * c / ctas; }
+    __device__ __forceinline__ int64_t start_of(int64_t c) const { return quot(total * c, ctas); }
 
     // False when this CTA has nothing to do.
     template <int NT>
     __device__ __forceinline__ bool start(const PagedParams& p, int64_t c, int64_t n_cta, int64_t* part) {
         const int tid = threadIdx.x;
         const int64_t H = p.n_heads;
-        int64_t mine = 0, sum;
-        for (int k = tid; k < p.n_seq; k += NT) {
-            const SeqShape x = S::shape(p, k);
-            mine += S::total(x, H);
-        }
-        block_scan<NT>(mine, part, &sum);
+        // batches of at most NT sequences: one thread each, read once
+        SeqShape x = S::shape(p, tid);
+        int64_t n = S::total(x, H), mine = n, sum;
+        for (int k = tid + NT; k < p.n_seq; k += NT) mine += S::total(S::shape(p, k), H);
+        int64_t incl = block_scan<NT>(mine, part, &sum);
         total = sum;
         ctas = min(n_cta, total);
         if (c >= ctas) return false;   // every thread alike
@@ -161,9 +169,11 @@ struct PagedWalk {
         v_end = start_of(c + 1);
         int64_t base = 0;
         for (int k0 = 0; k0 < p.n_seq; k0 += NT) {
-            const SeqShape x = S::shape(p, k0 + tid);
-            const int64_t n = S::total(x, H);
-            const int64_t incl = base + block_scan<NT>(n, part, &sum);
+            if (p.n_seq > NT) {
+                x = S::shape(p, k0 + tid);
+                n = S::total(x, H);
+                incl = base + block_scan<NT>(n, part, &sum);
+            }
             if (v0 >= incl - n && v0 < incl) {
                 part[NT / 32] = k0 + tid;
                 part[NT / 32 + 1] = incl - n;
@@ -215,7 +225,7 @@ struct PagedWalk {
     }
     // CTA of number v
     __device__ __forceinline__ int64_t cta_of(int64_t v) const {
-        int64_t c = v * ctas / total;
+        int64_t c = quot(v * ctas, total);
         while (start_of(c + 1) <= v) ++c;
         while (start_of(c) > v) --c;
         return c;
@@ -239,7 +249,7 @@ struct SchedOf : PagedSched<M, N, OV> {
 
 // Rows query vector r of a segment sees (r counts within the tile).
 __device__ __forceinline__ int64_t row_limit(const Segment& g, int r, int n_heads) {
-    return max((int64_t)0, g.base + 1 + (g.tok0 + r) / n_heads);
+    return max((int64_t)0, g.base + 1 + quot(g.tok0 + r, n_heads));
 }
 
 // Pool row of row t of sequence b; a table entry outside the pool sets the
