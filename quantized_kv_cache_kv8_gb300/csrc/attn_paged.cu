@@ -23,7 +23,7 @@ constexpr int kXS = 580;             // row stride in floats (4 banks apart)
 constexpr int kPS = kM + 4;          // weights: [row][vector]
 constexpr int kFlush = 1024 / kN;    // steps per block sum
 constexpr size_t kSmemFloats = (size_t)(kM + kN) * kXS + kN * 2 + (size_t)kN * kPS + kM + 16;
-constexpr size_t kSmem = kSmemFloats * 4 + kN * 4 + kM * 8 + (kNT / 32 + 2) * 8 + 16;
+constexpr size_t kSmem = kSmemFloats * 4 + kN * 4 + kM * 8 + kWalkScratch<kNT> * 8 + 16;
 
 __device__ __forceinline__ void store_out(float* o, int64_t i, float4 v) { *reinterpret_cast<float4*>(o + i) = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* o, int64_t i, float4 v) {
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
             const int r = i / kMlaD, d = i - r * kMlaD;
             qs[r * kXS + d] = r < g.rows ? load_q<BF16>(p.q, (g.row0 + r) * kMlaD + d) : 0.0f;
         }
-        if (tid < kM) lim[tid] = tid < g.rows ? row_limit(g, tid, p.n_heads) : 0;
+        if (tid < kM) lim[tid] = tid < g.rows ? row_limit(p, g, tid) : 0;
         __syncthreads();
         if (TQ4) {
             for (int r = warp; r < kM; r += kNT / 32) {
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[i][k] = o_tot[i][k] = 0.0f;
-        const int64_t end = row_limit(g, g.rows - 1, p.n_heads);   // rows any vector of the tile sees
+        const int64_t end = row_limit(p, g, g.rows - 1);   // rows any vector of the tile sees
         int steps = 0;
         for (int64_t u = g.u0; u < g.u1; ++u) {
             const int64_t t0 = u * kN;
@@ -413,6 +413,7 @@ cudaError_t launch_attn_paged(kvq_format fmt, const kvq_mla_layout& L, bool tens
     PagedParams p{};
     p.n_seq = n_seq;
     p.n_heads = n_heads;
+    p.h_inv = ~0ull / (uint64_t)n_heads;
     p.q = q;
     p.out = out;
     p.codes = codes;

@@ -96,7 +96,7 @@ constexpr uint32_t kOffMisc = kOffLevels + 32;              // abort flag, TMEM 
 constexpr uint32_t kOffWork = kOffMisc + 16;                // two segments, announced one ahead
 constexpr uint32_t kSmemUsed = kOffWork + 2 * 72;
 constexpr uint32_t kOffPart = kOffScale;                    // scan of the work split, before the steps
-static_assert((kThreads / 32 + 2) * 8 <= 2 * kScaleBytes, "scan scratch");
+static_assert(kWalkScratch<kThreads> * 8 <= 2 * kScaleBytes, "scan scratch");
 static_assert(kOffK % 1024 == 0 && kOffV % 1024 == 0 && kOffP % 1024 == 0 && kOffWork % 8 == 0, "alignment");
 static_assert(kSmemUsed <= 232448, "shared memory budget");
 static_assert(32 * kMlaDV * 4 <= 4 * kVChunkBytes, "output stage");
@@ -564,8 +564,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     w.b = g.b;
                     w.rows = g.rows;
                     w.first = (int32_t)(g.u0 * kRows);
-                    w.end = (int32_t)row_limit(g, g.rows - 1, p.n_heads);
-                    w.seen0 = (int32_t)row_limit(g, 0, p.n_heads);
+                    w.end = (int32_t)row_limit(p, g, g.rows - 1);
+                    w.seen0 = (int32_t)row_limit(p, g, 0);
                     w.row0 = g.row0;
                     w.tok0 = g.tok0;
                     w.base = g.base;
@@ -909,7 +909,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int32_t first = w.first, seen0 = w.seen0;
             // vectors past the tile's last repeat its limit: they score 0 and are dropped
             const int vec = kHalf * rank + r;
-            const int32_t lim = (int32_t)max((int64_t)0, w.base + 1 + (w.tok0 + min(vec, w.rows - 1)) / p.n_heads);
+            const int32_t lim = (int32_t)max((int64_t)0, w.base + 1 + over_heads(p, w.tok0 + min(vec, w.rows - 1)));
             RowState st{-INFINITY, -INFINITY, 0.0f, 0.0f, 0.0f, false};
             if (!warp_wait(&bars[kBarQ0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl)) aborted = true;
             const float cz = reinterpret_cast<const float*>(sm + kOffCz)[(n & 1) * kHalf + r];

@@ -7,7 +7,7 @@
 // base = kv_lens[b] - n.  Its n * H query vectors (token-major, as they lie in
 // memory) are cut into tiles of M; tile j needs
 //   units(j) = max(1, ceil(limit(j) / N)),  limit(j) = base + 1 + token of its last vector
-// steps of N rows (N a multiple of M).  All steps of the batch, with kOverhead
+// steps of N rows (N = M).  All steps of the batch, with kOverhead
 // more in front of each tile for its prologue, are numbered through, and CTA c
 // of C takes the numbers [V c / C, V (c+1) / C): every CTA gets the same work
 // whatever the lengths, a long sequence is spread over many CTAs, and nothing
@@ -20,7 +20,7 @@
 // is not the last tile,
 //   units(j) = floor((base + N + floor((M j + M - 1) / H)) / N)
 //            = floor((H (base + N) + M j + M - 1) / (N H))
-//            = floor((j + D) / (k H)),  D = floor((H (base + N) + M - 1) / M), k = N / M
+//            = floor((j + D) / H),  D = floor((H (base + N) + M - 1) / M), as M = N
 // (floors of quotients nest), a sum of floors over consecutive integers.
 #pragma once
 
@@ -30,6 +30,7 @@ namespace kvq {
 
 struct PagedParams {
     int32_t n_seq, n_heads;
+    uint64_t h_inv;            // floor((2^64 - 1) / n_heads)
     const void* q;             // [tokens][n_heads][576]
     void* out;                 // [tokens][n_heads][512], the query's type
     const uint8_t* codes;
@@ -51,15 +52,23 @@ struct PagedParams {
     float lv[16];
 };
 
-// Quotient of non-negative integers: a 64-bit division takes some hundred
-// instructions, and nearly every one of these fits 32 bits.
-__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+// Quotients of non-negative integers.  By the head count: a multiplication with
+// h_inv = floor((2^64 - 1) / n_heads), at most 1 short, then a correction (inlined
+// 64-bit divisions made the walk 80 KB of code, fetched anew by every launch).  By
+// anything else, out of line.
+__device__ __forceinline__ int64_t over_heads(const PagedParams& p, int64_t n) {
+    int64_t q = (int64_t)__umul64hi((uint64_t)n, p.h_inv);
+    if (n - q * p.n_heads >= p.n_heads) ++q;
+    return q;
+}
+static __device__ __noinline__ int64_t quot(int64_t a, int64_t b) {
     if (((uint64_t)a | (uint64_t)b) >> 32) return a / b;
     return (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
 struct SeqShape {
     int64_t q0, n_new, base, tiles, j0, D;
+    int64_t before;    // sum_{k < j0 + D} floor(k / H)
 };
 struct Segment {
     int32_t b;
@@ -74,12 +83,12 @@ struct Segment {
 template <int M, int N, int OV>
 struct PagedSched {
     static constexpr int kM = M, kN = N;
-    static constexpr int64_t kRatio = N / M;
+    static_assert(M == N, "the closed form below is for steps of as many rows as a tile has vectors");
     static constexpr int kLogM = M == 32 ? 5 : 7, kLogN = N == 32 ? 5 : 7;
     static_assert((1 << kLogM) == M && (1 << kLogN) == N, "tile sizes");
 
     __device__ static SeqShape shape(const PagedParams& p, int b) {
-        SeqShape s{0, 0, 0, 0, 0, 0};
+        SeqShape s{0, 0, 0, 0, 0, 0, 0};
         if (b >= p.n_seq) return s;
         const int64_t a = p.cu_q[b], e = p.cu_q[b + 1];
         int64_t kv = p.kv_lens[b];
@@ -96,24 +105,25 @@ struct PagedSched {
         s.j0 = s.base >= 0 ? 0 : (-s.base * H) >> kLogM;   // first tile with limit >= 1
         const int64_t C = H * (s.base + N) + M - 1;
         s.D = C >> kLogM;   // floor, also below zero
+        s.before = floor_sum(p, s.j0 + s.D);
         return s;
     }
-    __device__ static int64_t units(const SeqShape& s, int64_t H, int64_t j) {
-        const int64_t tok = min(s.n_new - 1, quot(M * j + M - 1, H));
+    __device__ static int64_t units(const PagedParams& p, const SeqShape& s, int64_t j) {
+        const int64_t tok = min(s.n_new - 1, over_heads(p, M * j + M - 1));
         return max((int64_t)1, (s.base + tok + N) >> kLogN);
     }
-    __device__ static int64_t floor_sum(int64_t n, int64_t d) {   // sum_{k<n} floor(k / d)
-        const int64_t q = quot(n, d), r = n - q * d;
-        return d * (q * (q - 1) / 2) + q * r;
+    __device__ static int64_t floor_sum(const PagedParams& p, int64_t n) {   // sum_{k<n} floor(k / H)
+        const int64_t H = p.n_heads, q = over_heads(p, n), r = n - q * H;
+        return H * (q * (q - 1) / 2) + q * r;
     }
     // numbers before tile j (j < tiles)
-    __device__ static int64_t prefix(const SeqShape& s, int64_t H, int64_t j) {
-        const int64_t v = OV * j + min(j, s.j0), d = kRatio * H;
-        return j <= s.j0 ? v : v + floor_sum(j + s.D, d) - floor_sum(s.j0 + s.D, d);
+    __device__ static int64_t prefix(const PagedParams& p, const SeqShape& s, int64_t j) {
+        const int64_t v = OV * j + min(j, s.j0);
+        return j <= s.j0 ? v : v + floor_sum(p, j + s.D) - s.before;
     }
-    __device__ static int64_t total(const SeqShape& s, int64_t H) {
+    __device__ static int64_t total(const PagedParams& p, const SeqShape& s) {
         if (s.tiles == 0) return 0;
-        return prefix(s, H, s.tiles - 1) + OV + units(s, H, s.tiles - 1);
+        return prefix(p, s, s.tiles - 1) + OV + units(p, s, s.tiles - 1);
     }
 };
 
@@ -129,16 +139,20 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t*
     __syncthreads();
     if (lane == 31) part[warp] = v;
     __syncthreads();
-    int64_t before = 0, all = 0;
+    int64_t w = lane < NT / 32 ? part[lane] : 0;   // every warp scans the warps' sums
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-        const int64_t x = part[w];
-        before += w < warp ? x : 0;
-        all += x;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(kFull, w, o);
+        if (lane >= o) w += t;
     }
-    *sum = all;
-    return v + before;
+    *sum = __shfl_sync(kFull, w, NT / 32 - 1);
+    const int64_t before = __shfl_sync(kFull, w, max(warp - 1, 0));
+    return warp > 0 ? v + before : v;
 }
+
+// Scratch of start() in int64s: the warps' sums, the found sequence.
+template <int NT>
+constexpr int kWalkScratch = NT / 32 + 9;
 
 // A CTA's walk over its segments.  start() is called by all NT threads of the
 // CTA; the rest by any thread on its own (every thread holds the same walk).
@@ -156,43 +170,59 @@ struct PagedWalk {
     template <int NT>
     __device__ __forceinline__ bool start(const PagedParams& p, int64_t c, int64_t n_cta, int64_t* part) {
         const int tid = threadIdx.x;
-        const int64_t H = p.n_heads;
-        // batches of at most NT sequences: one thread each, read once
-        SeqShape x = S::shape(p, tid);
-        int64_t n = S::total(x, H), mine = n, sum;
-        for (int k = tid + NT; k < p.n_seq; k += NT) mine += S::total(S::shape(p, k), H);
-        int64_t incl = block_scan<NT>(mine, part, &sum);
-        total = sum;
-        ctas = min(n_cta, total);
-        if (c >= ctas) return false;   // every thread alike
-        const int64_t v0 = start_of(c);
-        v_end = start_of(c + 1);
-        int64_t base = 0;
-        for (int k0 = 0; k0 < p.n_seq; k0 += NT) {
-            if (p.n_seq > NT) {
-                x = S::shape(p, k0 + tid);
-                n = S::total(x, H);
-                incl = base + block_scan<NT>(n, part, &sum);
+        SeqShape x;
+        int64_t n = 0, incl = 0, sum = 0, v0 = 0, base = 0;
+        total = 0;
+        // pass 0 adds up the numbers, pass 1 finds this CTA's first; a batch of at
+        // most NT sequences, a thread each, is read once
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+            for (int k0 = 0; k0 < p.n_seq; k0 += NT) {
+                if (pass == 0 || p.n_seq > NT) {
+                    x = S::shape(p, k0 + tid);
+                    n = S::total(p, x);
+                    incl = block_scan<NT>(n, part, &sum);
+                }
+                if (pass == 0) {
+                    total += sum;
+                    continue;
+                }
+                if (v0 >= base + incl - n && v0 < base + incl) {
+                    int64_t* own = part + NT / 32;
+                    own[0] = k0 + tid;
+                    own[1] = base + incl - n;
+                    own[2] = x.q0;
+                    own[3] = x.n_new;
+                    own[4] = x.base;
+                    own[5] = x.tiles;
+                    own[6] = x.j0;
+                    own[7] = x.D;
+                    own[8] = x.before;
+                }
+                base += sum;
+                if (v0 < base) break;
             }
-            if (v0 >= incl - n && v0 < incl) {
-                part[NT / 32] = k0 + tid;
-                part[NT / 32 + 1] = incl - n;
+            if (pass == 0) {
+                ctas = min(n_cta, total);
+                if (c >= ctas) return false;   // every thread alike
+                v0 = start_of(c);
+                v_end = start_of(c + 1);
             }
-            base += sum;
-            if (v0 < base) break;
         }
         __syncthreads();
-        b = (int32_t)part[NT / 32];
-        seq_v = part[NT / 32 + 1];
-        s = S::shape(p, b);
+        const int64_t* own = part + NT / 32;
+        b = (int32_t)own[0];
+        seq_v = own[1];
+        s = SeqShape{own[2], own[3], own[4], own[5], own[6], own[7], own[8]};
         int64_t lo = 0, hi = s.tiles;
         while (hi - lo > 1) {
             const int64_t mid = (lo + hi) / 2;
-            if (S::prefix(s, H, mid) <= v0 - seq_v) lo = mid;
+            if (S::prefix(p, s, mid) <= v0 - seq_v) lo = mid;
             else hi = mid;
         }
         j = lo;
-        u0 = max((int64_t)0, v0 - seq_v - S::prefix(s, H, j) - (int64_t)overhead());
+        u0 = max((int64_t)0, v0 - seq_v - S::prefix(p, s, j) - (int64_t)overhead());
         return true;
     }
     __device__ static constexpr int overhead() { return S::kOverhead; }
@@ -202,8 +232,8 @@ struct PagedWalk {
         if (b >= p.n_seq) return false;
         const int64_t H = p.n_heads;
         g.b = b;
-        g.tile_v = seq_v + S::prefix(s, H, j);
-        g.units = S::units(s, H, j);
+        g.tile_v = seq_v + S::prefix(p, s, j);
+        g.units = S::units(p, s, j);
         g.u0 = u0;
         g.u1 = min(g.units, v_end - g.tile_v - overhead());
         if (g.u1 <= g.u0) return false;
@@ -217,7 +247,7 @@ struct PagedWalk {
     __device__ __forceinline__ void next(const PagedParams& p) {
         u0 = 0;
         if (++j < s.tiles) return;
-        seq_v += S::total(s, p.n_heads);
+        seq_v += S::total(p, s);
         j = 0;
         do {
             s = S::shape(p, ++b);
@@ -248,8 +278,8 @@ struct SchedOf : PagedSched<M, N, OV> {
 };
 
 // Rows query vector r of a segment sees (r counts within the tile).
-__device__ __forceinline__ int64_t row_limit(const Segment& g, int r, int n_heads) {
-    return max((int64_t)0, g.base + 1 + quot(g.tok0 + r, n_heads));
+__device__ __forceinline__ int64_t row_limit(const PagedParams& p, const Segment& g, int r) {
+    return max((int64_t)0, g.base + 1 + over_heads(p, g.tok0 + r));
 }
 
 // Pool row of row t of sequence b; a table entry outside the pool sets the
