@@ -289,28 +289,36 @@ __device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c
 }
 
 // ---- queries ------------------------------------------------------------------
-// Prologue and epilogue code runs once a segment and is fetched anew each time:
-// unrolled over their vectors these loops took 4 to 12 us in instruction fetches
-// alone, so they are kept rolled, with the next vector's loads in flight.
+// Prologue and epilogue run once a segment, with few warps: what counts is the
+// chain of each warp, so a warp takes four vectors at once, 8 lanes each.  Lane
+// l = lane % 8 of a vector has its units l + 8 i of four elements.
 
-// The 512-point transform of a row that a warp holds with element
-// 128 i + 4 lane + k in v[i][k] (unscaled): in registers over k and i, by shuffles
-// over the lanes.
+// The unscaled 512-point transform of four vectors, element 4 (l + 8 i) + k in
+// v[i][k]: in registers over k and i, by shuffles over the 8 lanes (a vector over a
+// whole warp would shuffle five times instead of three, and take twice as long).
 __device__ __forceinline__ void butterfly(float& a, float& b) {
     const float s = a + b, d = a - b;
     a = s;
     b = d;
 }
-__device__ __forceinline__ void transform4(float (&v)[4]) {
-    butterfly(v[0], v[1]);
-    butterfly(v[2], v[3]);
-    butterfly(v[0], v[2]);
-    butterfly(v[1], v[3]);
-}
 template <int N>
-__device__ __forceinline__ void transform_lanes(float (&v)[N][4], int lanes, int lane) {
+__device__ __forceinline__ void transform(float (&v)[N][4], int lane) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        butterfly(v[i][0], v[i][1]);
+        butterfly(v[i][2], v[i][3]);
+        butterfly(v[i][0], v[i][2]);
+        butterfly(v[i][1], v[i][3]);
+    }
+#pragma unroll
+    for (int h = 1; h < N; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if ((i & h) == 0)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) butterfly(v[i][k], v[i + h][k]);
 #pragma unroll 1
-    for (int h = 1; h < lanes; h <<= 1) {
+    for (int h = 1; h < 8; h <<= 1) {
         const float sign = (lane & h) ? -1.0f : 1.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -318,124 +326,118 @@ __device__ __forceinline__ void transform_lanes(float (&v)[N][4], int lanes, int
             for (int k = 0; k < 4; ++k) v[i][k] = fmaf(sign, v[i][k], __shfl_xor_sync(kFull, v[i][k], h));
     }
 }
-__device__ __forceinline__ void transform512(float (&v)[4][4], int lane) {
+// Flips the elements of v whose sign bit is set in words w of a block.
+template <int N>
+__device__ __forceinline__ void apply_signs(float (&v)[N][4], const uint64_t* w, int l) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) transform4(v[i]);
-    transform_lanes<4>(v, 32, lane);
+    for (int i = 0; i < N; ++i) {
+        const uint32_t half = (uint32_t)(w[i >> 1] >> (32 * (i & 1)));   // 32 signs: units 8 i .. 8 i + 7
+        const uint32_t bits = half >> (4 * l);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        butterfly(v[0][k], v[1][k]);
-        butterfly(v[2][k], v[3][k]);
-        butterfly(v[0][k], v[2][k]);
-        butterfly(v[1][k], v[3][k]);
+        for (int k = 0; k < 4; ++k) v[i][k] = __int_as_float(__float_as_int(v[i][k]) ^ (int)((bits >> k) << 31));
     }
-}
-// The signs of elements 4 at .. 4 at + 3 of block b, one a bit.
-__device__ __forceinline__ uint32_t signs4(const SignWords& s, int b, int at) {
-    return (uint32_t)(s.w[s.block_word[b] + (at >> 4)] >> (4 * (at & 15))) & 15u;
-}
-__device__ __forceinline__ void apply_signs(float (&v)[4], uint32_t bits) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = __int_as_float(__float_as_int(v[k]) ^ (int)((bits >> k) << 31));
 }
 
 // This CTA's 64 vectors, 8 a decode warp: to f16 (TQ4, rotated) or to a sum of two
 // e4m3 values, under a power of two of their own; sCz gets what undoes it in the
-// score.  A lane has dims 128 i + 4 lane .. + 3 of a vector, the lower 16 lanes also
-// its rope dims 4 lane .. + 3.
+// score.
 template <bool TQ4>
 __device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0, int rows, unsigned char* sQ,
                                              float* sCz, int warp, int lane) {
-    constexpr int kPer = kHalf / kDecWarps;
-    const uint2* src = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                      (row0 + kPer * warp) * kMlaD) + lane;
-    uint2 raw[5], next[5];
-    auto fetch = [&](int k, uint2 (&x)[5]) {
+    constexpr int kUnits = 18;   // units of a lane: 16 latent, 2 rope
+    const int l = lane & 7;
+    const int r0 = (kHalf / kDecWarps) * warp + (lane >> 3);
+    const uint2* src = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q) + (row0 + r0) * kMlaD) + l;
+    uint2 raw[kUnits];
+    auto fetch = [&](int g) {
+        const bool ok = r0 + 4 * g < rows;
 #pragma unroll
-        for (int i = 0; i < 5; ++i)
-            x[i] = kPer * warp + k < rows && (i < 4 || lane < 16) ? __ldg(src + k * (kMlaD / 4) + 32 * i) : make_uint2(0u, 0u);
+        for (int i = 0; i < kUnits; ++i)
+            raw[i] = ok ? __ldg(src + g * kMlaD + 8 * i) : make_uint2(0u, 0u);   // 4 vectors on: 4 * 144 units
     };
-    fetch(0, raw);
+    fetch(0);
 #pragma unroll 1
-    for (int k = 0; k < kPer; ++k) {
-        if (k + 1 < kPer) fetch(k + 1, next);
-        const int r = kPer * warp + k;
-        float v[5][4];
-#pragma unroll
-        for (int i = 0; i < 5; ++i) {
-            v[i][0] = __uint_as_float(raw[i].x << 16);
-            v[i][1] = __uint_as_float(raw[i].x & 0xffff0000u);
-            v[i][2] = __uint_as_float(raw[i].y << 16);
-            v[i][3] = __uint_as_float(raw[i].y & 0xffff0000u);
-            raw[i] = next[i];
-        }
+    for (int g = 0; g < 2; ++g) {
+        const int r = r0 + 4 * g;
+        // the largest magnitude, as bits: a NaN counts above an infinity
+        uint32_t top = 0u;
+        float v[16][4], rope[2][4];
         if (TQ4) {
-            float lat[4][4], rope[1][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) lat[i][e] = v[i][e];
-                apply_signs(lat[i], signs4(p.signs, 0, 32 * i + lane));
+            for (int i = 0; i < kUnits; ++i) {
+                float (&x)[4] = i < 16 ? v[i < 16 ? i : 0] : rope[i < 16 ? 0 : i - 16];
+                x[0] = __uint_as_float(raw[i].x << 16);
+                x[1] = __uint_as_float(raw[i].x & 0xffff0000u);
+                x[2] = __uint_as_float(raw[i].y << 16);
+                x[3] = __uint_as_float(raw[i].y & 0xffff0000u);
             }
-            transform512(lat, lane);
+            if (g == 0) fetch(1);
+            apply_signs(v, p.signs.w, l);
+            transform(v, lane);
+            apply_signs(rope, p.signs.w + 8, l);   // the rope block's words follow the latent block's 8
+            transform(rope, lane);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) rope[0][e] = v[4][e];
-            apply_signs(rope[0], signs4(p.signs, 1, lane & 15));
-            transform4(rope[0]);
-            transform_lanes<1>(rope, 16, lane);
+            for (int k = 0; k < 4; ++k) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+                for (int i = 0; i < 16; ++i) {
+                    v[i][k] *= p.kn[0];
+                    top = max(top, __float_as_uint(v[i][k]) & 0x7fffffffu);
+                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i][e] = lat[i][e] * p.kn[0];
-                v[4][e] = rope[0][e] * p.kn[1];
+                for (int i = 0; i < 2; ++i) {
+                    rope[i][k] *= p.kn[1];
+                    top = max(top, __float_as_uint(rope[i][k]) & 0x7fffffffu);
+                }
             }
+        } else {
+            uint32_t both = 0u;
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i)
+                both = __vmaxu2(both, __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu));
+            top = max(both << 16, both & 0xffff0000u);
         }
-        float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 5; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(v[i][e]));
-        top = warp_max(top);
+        for (int h = 1; h < 8; h <<= 1) top = max(top, __shfl_xor_sync(kFull, top, h));
         // 2^shift puts the largest element into [2^13, 2^14), for e4m3 into [128, 256);
-        // |shift| <= 114 keeps it and its inverse normal numbers
+        // |shift| <= 114 keeps it and its inverse normal numbers.  A vector with a NaN
+        // or an infinity becomes NaN throughout (e4m3 would saturate the infinity).
         constexpr int kTop = TQ4 ? 14 : 8;
-        int shift = 0;
-        if (top > 0.0f && top <= 3.402823466e38f)
-            shift = min(114, kTop + 126 - max((int)(__float_as_uint(top) >> 23), 1));
-        const float scale = __uint_as_float((uint32_t)(127 + shift) << 23);
-        if (lane == 0)
+        const bool finite = top < 0x7f800000u;
+        const int shift = top == 0u || !finite ? 0 : min(114, kTop + 126 - max((int)(top >> 23), 1));
+        const float scale = finite ? __uint_as_float((uint32_t)(127 + shift) << 23) : __uint_as_float(0x7fffffffu);
+        if (l == 0)
             sCz[r] = p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 - shift) << 23) * (TQ4 ? 1.0f / kGamma : 1.0f);
 #pragma unroll
-        for (int i = 0; i < 5; ++i) {
-            if (i == 4 && lane >= 16) break;
+        for (int i = 0; i < kUnits; ++i) {
+            const int u = l + 8 * (i < 16 ? i : i - 16);   // unit of the latent or of the rope dims
             if (TQ4) {
-                const __half2 a = __floats2half2_rn(v[i][0] * scale, v[i][1] * scale);
-                const __half2 b = __floats2half2_rn(v[i][2] * scale, v[i][3] * scale);
-                unsigned char* c = sQ + (i < 4 ? 2 * i + (lane >> 4) : kRope) * kChunkBytes;
-                *reinterpret_cast<uint2*>(c + sw128(r, 8 * (lane & 15))) =
+                const float (&x)[4] = i < 16 ? v[i < 16 ? i : 0] : rope[i < 16 ? 0 : i - 16];
+                const __half2 a = __floats2half2_rn(x[0] * scale, x[1] * scale);
+                const __half2 b = __floats2half2_rn(x[2] * scale, x[3] * scale);
+                unsigned char* c = sQ + (i < 16 ? i >> 1 : kRope) * kChunkBytes;
+                *reinterpret_cast<uint2*>(c + sw128(r, 8 * (u & 15))) =
                     make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
             } else {
-                uint32_t hi = 0u, lo = 0u;
+                // 8 significant bits under 256: exact in f16, as is what q1 leaves
+                uint32_t c1[2], c2[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    // q1 and what it leaves; an infinity becomes a NaN (the conversion would saturate it)
-                    float2 x = make_float2(v[i][2 * h] * scale, v[i][2 * h + 1] * scale);
-                    if (!(fabsf(x.x) <= 3.402823466e38f)) x.x = __int_as_float(0x7fffffff);
-                    if (!(fabsf(x.y) <= 3.402823466e38f)) x.y = __int_as_float(0x7fffffff);
-                    const __nv_fp8x2_storage_t c1 = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
-                    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(c1, __NV_E4M3);
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-                    const __nv_fp8x2_storage_t c2 =
-                        __nv_cvt_float2_to_fp8x2(make_float2(x.x - f.x, x.y - f.y), __NV_SATFINITE, __NV_E4M3);
-                    hi |= (uint32_t)c1 << (16 * h);
-                    lo |= (uint32_t)c2 << (16 * h);
+                    const uint32_t w = h ? raw[i].y : raw[i].x;
+                    const __half2 x = __floats2half2_rn(__uint_as_float(w << 16) * scale, __uint_as_float(w & 0xffff0000u) * scale);
+                    const __nv_fp8x2_storage_t f1 =
+                        __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+                    const __half2 rest = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2(f1, __NV_E4M3)));
+                    c1[h] = f1;
+                    c2[h] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
                 }
-                unsigned char* c = sQ + (i < 4 ? i : kRope) * kChunkBytes;
-                *reinterpret_cast<uint32_t*>(c + sw128(r, 4 * lane)) = hi;
-                if (i < 4) *reinterpret_cast<uint32_t*>(c + 4 * kChunkBytes + sw128(r, 4 * lane)) = lo;
-                else *reinterpret_cast<uint32_t*>(c + sw128(r, 64 + 4 * lane)) = lo;
+                unsigned char* c = sQ + (i < 16 ? i >> 2 : kRope) * kChunkBytes;
+                const int byte = i < 16 ? 4 * (u & 31) : 4 * u;
+                *reinterpret_cast<uint32_t*>(c + sw128(r, byte)) = c1[0] | c1[1] << 16;
+                *reinterpret_cast<uint32_t*>(i < 16 ? c + 4 * kChunkBytes + sw128(r, byte) : c + sw128(r, 64 + byte)) =
+                    c2[0] | c2[1] << 16;
             }
         }
+        if (!TQ4 && g == 0) fetch(1);
     }
 }
 
@@ -489,6 +491,29 @@ struct RowState {
     bool none;   // rows seen, but none with a latent scale yet
 };
 
+// The walk's current segment as a record; false at its end.
+__device__ __forceinline__ bool announce(const PagedParams& p, const PagedWalk<PagedTensor>& walk, int64_t pair, Work* to) {
+    Segment g;
+    Work w{};
+    const bool more = walk.get(p, g);
+    if (more) {
+        int64_t parts;
+        w.steps = (int32_t)(g.u1 - g.u0);
+        w.b = g.b;
+        w.rows = g.rows;
+        w.first = (int32_t)(g.u0 * kRows);
+        w.end = (int32_t)row_limit(p, g, g.rows - 1);
+        w.seen0 = (int32_t)row_limit(p, g, 0);
+        w.row0 = g.row0;
+        w.tok0 = g.tok0;
+        w.base = g.base;
+        w.slot = walk.slot(g, pair, &parts);
+        w.parts = (int32_t)parts;
+    }
+    *to = w;
+    return more;
+}
+
 template <bool TQ4>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     paged_tensor_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap map) {
@@ -541,6 +566,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint4*>(sm + kOffLevels) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         *reinterpret_cast<uint4*>(sm + kOffLevels + 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     }
+    bool more = true;
+    if (warp == kWalkWarp && lane == 0) more = announce(p, walk, pair, &sWork[0]);
     tc_before();
     __syncthreads();
     cluster_sync();   // the other CTA's barriers are there, its tensor memory is allocated
@@ -552,27 +579,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == kWalkWarp) {
         // ================= the walk: announces segments one ahead =================
         if (lane == 0) {
-            bool more = true;
-            for (int n = 0; more; ++n, walk.next(p)) {
+            mbar_arrive(&bars[kBarWork0]);   // the first lies there
+            for (int n = 1; more; ++n) {
+                walk.next(p);
                 if (n >= 2 && !idle_wait(&bars[kBarWorkFree0 + (n & 1)], (uint32_t)(n / 2 - 1) & 1u, sAbort, wl)) break;
-                Segment g;
-                Work w{};
-                more = walk.get(p, g);
-                if (more) {
-                    int64_t parts;
-                    w.steps = (int32_t)(g.u1 - g.u0);
-                    w.b = g.b;
-                    w.rows = g.rows;
-                    w.first = (int32_t)(g.u0 * kRows);
-                    w.end = (int32_t)row_limit(p, g, g.rows - 1);
-                    w.seen0 = (int32_t)row_limit(p, g, 0);
-                    w.row0 = g.row0;
-                    w.tok0 = g.tok0;
-                    w.base = g.base;
-                    w.slot = walk.slot(g, pair, &parts);
-                    w.parts = (int32_t)parts;
-                }
-                sWork[n & 1] = w;
+                more = announce(p, walk, pair, &sWork[n & 1]);
                 mbar_arrive(&bars[kBarWork0 + (n & 1)]);
             }
         }
@@ -1143,27 +1154,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     }
                     worker_sync<kSoft>();
-#pragma unroll 1
-                    for (int k = warp; k < 32; k += kSoftWarps) {
+                    {
+                        const int k = 4 * warp + (lane >> 3), l = lane & 7;
                         const int ov = kHalf * rank + 32 * rr + k;
-                        if (ov >= rows) break;
-                        float v[4][4];
+                        float v[16][4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 x = *reinterpret_cast<const float4*>(stage + k * kMlaDV + 4 * ((32 * i + lane) ^ (k & 7)));
+                        for (int i = 0; i < 16; ++i) {
+                            const float4 x = *reinterpret_cast<const float4*>(stage + k * kMlaDV + 4 * ((l + 8 * i) ^ (k & 7)));
                             v[i][0] = x.x;
                             v[i][1] = x.y;
                             v[i][2] = x.z;
                             v[i][3] = x.w;
                         }
-                        transform512(v, lane);
+                        transform(v, lane);
+                        apply_signs(v, p.signs.w, l);
+                        if (ov < rows) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            apply_signs(v[i], signs4(p.signs, 0, 32 * i + lane));
-                            const __nv_bfloat162 a = __floats2bfloat162_rn(v[i][0] * p.kn[0], v[i][1] * p.kn[0]);
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(v[i][2] * p.kn[0], v[i][3] * p.kn[0]);
-                            *reinterpret_cast<uint2*>(out + (int64_t)ov * kMlaDV + 128 * i + 4 * lane) =
-                                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+                            for (int i = 0; i < 16; ++i) {
+                                const __nv_bfloat162 a = __floats2bfloat162_rn(v[i][0] * p.kn[0], v[i][1] * p.kn[0]);
+                                const __nv_bfloat162 b = __floats2bfloat162_rn(v[i][2] * p.kn[0], v[i][3] * p.kn[0]);
+                                *reinterpret_cast<uint2*>(out + (int64_t)ov * kMlaDV + 4 * (l + 8 * i)) =
+                                    make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+                            }
                         }
                     }
                     worker_sync<kSoft>();
