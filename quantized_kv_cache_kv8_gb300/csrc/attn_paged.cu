@@ -299,75 +299,96 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
     }
 }
 
-constexpr int kMergeRows = 4, kMergeNT = 128 * kMergeRows;
+constexpr int kMergeRows = 4, kMergeNT = 128 * kMergeRows, kMergeCtas = 304;
 
-// Joins the parts of the tile that walker blockIdx.y began, 4 vectors a CTA, 128
-// threads with 4 dims each to a vector, by log-sum-exp.  The grid covers every
-// walker; where none left a cut tile its CTAs return at once.
+// Joins the parts of cut tiles by log-sum-exp: 4 vectors at a time, 128 threads
+// with 4 dims each to a vector.  Each CTA lists the walkers that began a cut tile
+// and takes its share of their vectors (a CTA for every walker and group of vectors
+// would be 2,400, most of them with nothing to do).
 template <bool TQ4, bool BF16, int M>
 __global__ void __launch_bounds__(kMergeNT) paged_merge_kernel(const __grid_constant__ PagedParams p) {
     using OT = typename std::conditional<BF16, __nv_bfloat16, float>::type;
+    constexpr int kWalkers = M == PagedTensor::kM ? kPagedPairs : kPagedCtas;
+    static_assert(kWalkers <= kMergeNT, "a thread a walker");
     __shared__ float ov[kMergeRows][kMlaDV];
-    const int64_t cta = blockIdx.y;
-    const int sub = threadIdx.x >> 7, tid = threadIdx.x & 127, lane = tid & 31;
-    const int r = kMergeRows * blockIdx.x + sub;
+    constexpr int kListWarps = (kWalkers + 31) / 32;
+    __shared__ int32_t cut[kWalkers], in_warp[kListWarps];
+    const int sub = threadIdx.x >> 7, tid = threadIdx.x & 127, lane = tid & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
-    const int64_t parts = p.ws_desc[cta * 4], row0 = p.ws_desc[cta * 4 + 1];
-    const bool live = r < p.ws_desc[cta * 4 + 2];
-    if (parts == 0) return;
-    float Mx = -INFINITY, L = 0.0f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kBatch = 8;
-    for (int64_t c0 = 0; live && c0 < parts; c0 += kBatch) {
-        float mv[kBatch], lw[kBatch];
-        float4 v[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            mv[k] = -INFINITY;
-            lw[k] = 0.0f;
-            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c0 + k < parts) {
-                // the beginning lies in this CTA's second slot, the rest in the first slots of the CTAs after it
-                const int64_t row = (c0 + k == 0 ? 2 * cta + 1 : 2 * (cta + c0 + k)) * M + r;
-                const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + row * 2);
-                mv[k] = ml.x;
-                lw[k] = ml.y;
-                v[k] = *reinterpret_cast<const float4*>(p.ws_o + row * kMlaDV + 4 * tid);
-            }
-        }
-        float mb = Mx;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) mb = fmaxf(mb, mv[k]);
-        const float ref = mb == -INFINITY ? 0.0f : mb;   // parts without a visible row weigh 0
-        const float keep = expf(Mx - ref);
-        L *= keep;
-        acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const float w = expf(mv[k] - ref);
-            L = fmaf(w, lw[k], L);
-            acc.x = fmaf(w, v[k].x, acc.x);
-            acc.y = fmaf(w, v[k].y, acc.y);
-            acc.z = fmaf(w, v[k].z, acc.z);
-            acc.w = fmaf(w, v[k].w, acc.w);
-        }
-        Mx = mb;
-    }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // no visible row: zeros
-    acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    OT* out = static_cast<OT*>(p.out);
-    const int64_t at = (row0 + r) * kMlaDV;
-    if (!TQ4) {
-        if (live) store_out(out, at + 4 * tid, acc);
-        return;
-    }
-    *reinterpret_cast<float4*>(ov[sub] + 4 * tid) = acc;
+    // the walkers with a cut tile, in order: every CTA has the same list
+    const bool mine = threadIdx.x < kWalkers && p.ws_desc[threadIdx.x * 4] > 0;
+    const unsigned mask = __ballot_sync(kFull, mine);
+    if (lane == 0 && warp < kListWarps) in_warp[warp] = __popc(mask);
     __syncthreads();
-    if (live && tid < 32) {
-        float v[16];
+    int before = 0, n_cut = 0;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = ov[sub][lane + 32 * k];
-        unrotate_out(p, v, out, at, lane);
+    for (int w = 0; w < kListWarps; ++w) {
+        before += w < warp ? in_warp[w] : 0;
+        n_cut += in_warp[w];
+    }
+    if (mine) cut[before + __popc(mask & ((1u << lane) - 1u))] = threadIdx.x;
+    __syncthreads();
+    constexpr int kGroups = M / kMergeRows;
+    for (int item = blockIdx.x; item < n_cut * kGroups; item += gridDim.x) {
+        const int64_t cta = cut[item / kGroups];
+        const int r = kMergeRows * (item % kGroups) + sub;
+        const int64_t parts = p.ws_desc[cta * 4], row0 = p.ws_desc[cta * 4 + 1];
+        const bool live = r < p.ws_desc[cta * 4 + 2];
+        float Mx = -INFINITY, L = 0.0f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kBatch = 8;
+        for (int64_t c0 = 0; live && c0 < parts; c0 += kBatch) {
+            float mv[kBatch], lw[kBatch];
+            float4 v[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                mv[k] = -INFINITY;
+                lw[k] = 0.0f;
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c0 + k < parts) {
+                    // the beginning lies in this CTA's second slot, the rest in the first slots of the CTAs after it
+                    const int64_t row = (c0 + k == 0 ? 2 * cta + 1 : 2 * (cta + c0 + k)) * M + r;
+                    const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + row * 2);
+                    mv[k] = ml.x;
+                    lw[k] = ml.y;
+                    v[k] = *reinterpret_cast<const float4*>(p.ws_o + row * kMlaDV + 4 * tid);
+                }
+            }
+            float mb = Mx;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) mb = fmaxf(mb, mv[k]);
+            const float ref = mb == -INFINITY ? 0.0f : mb;   // parts without a visible row weigh 0
+            const float keep = expf(Mx - ref);
+            L *= keep;
+            acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const float w = expf(mv[k] - ref);
+                L = fmaf(w, lw[k], L);
+                acc.x = fmaf(w, v[k].x, acc.x);
+                acc.y = fmaf(w, v[k].y, acc.y);
+                acc.z = fmaf(w, v[k].z, acc.z);
+                acc.w = fmaf(w, v[k].w, acc.w);
+            }
+            Mx = mb;
+        }
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // no visible row: zeros
+        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        OT* out = static_cast<OT*>(p.out);
+        const int64_t at = (row0 + r) * kMlaDV;
+        if (!TQ4) {
+            if (live) store_out(out, at + 4 * tid, acc);
+            continue;
+        }
+        *reinterpret_cast<float4*>(ov[sub] + 4 * tid) = acc;
+        __syncthreads();
+        if (live && tid < 32) {
+            float v[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = ov[sub][lane + 32 * k];
+            unrotate_out(p, v, out, at, lane);
+        }
+        __syncthreads();   // ov is read before the next item's values
     }
 }
 
@@ -383,7 +404,7 @@ cudaError_t launch_exact(const PagedParams& p, cudaStream_t stream) {
 template <bool TQ4, bool BF16, int M>
 cudaError_t launch_merge(const PagedParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(M / kMergeRows, M == PagedTensor::kM ? kPagedPairs : kPagedCtas);
+    cfg.gridDim = dim3(kMergeCtas);
     cfg.blockDim = dim3(kMergeNT);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

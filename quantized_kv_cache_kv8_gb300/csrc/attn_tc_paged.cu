@@ -348,14 +348,15 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0,
     const int l = lane & 7;
     const int r0 = (kHalf / kDecWarps) * warp + (lane >> 3);
     const uint2* src = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q) + (row0 + r0) * kMlaD) + l;
-    uint2 raw[kUnits];
-    auto fetch = [&](int g) {
+    uint2 raw[kUnits], ahead[kUnits];
+    auto fetch = [&](int g, uint2 (&raw)[kUnits]) {
         const bool ok = r0 + 4 * g < rows;
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
             raw[i] = ok ? __ldg(src + g * kMlaD + 8 * i) : make_uint2(0u, 0u);   // 4 vectors on: 4 * 144 units
     };
-    fetch(0);
+    fetch(0, raw);
+    if (!TQ4) fetch(1, ahead);
 #pragma unroll 1
     for (int g = 0; g < 2; ++g) {
         const int r = r0 + 4 * g;
@@ -371,7 +372,7 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0,
                 x[2] = __uint_as_float(raw[i].y << 16);
                 x[3] = __uint_as_float(raw[i].y & 0xffff0000u);
             }
-            if (g == 0) fetch(1);
+            if (g == 0) fetch(1, raw);
             apply_signs(v, p.signs.w, l);
             transform(v, lane);
             apply_signs(rope, p.signs.w + 8, l);   // the rope block's words follow the latent block's 8
@@ -437,7 +438,10 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0,
                     c2[0] | c2[1] << 16;
             }
         }
-        if (!TQ4 && g == 0) fetch(1);
+        if (!TQ4) {
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) raw[i] = ahead[i];
+        }
     }
 }
 

@@ -14,8 +14,8 @@
 //
 // What bounds it: a decode step moves a few KB, so the call is one launch and
 // one chain of dependent reads (lengths, the scan, the table entry or the free
-// list, the slot).  Every CTA therefore scans all the lengths itself, 512 at a
-// time, instead of waiting for another launch's prefix sums; it then writes its
+// list, the slot).  Every CTA therefore scans all the lengths itself, up to 1024 at
+// a time, instead of waiting for another launch's prefix sums; it then writes its
 // share of the rows (a binary search over the scanned offsets in shared
 // memory) and of the new table entries.  The counters that are both read and
 // written (n_free, and the lengths where the caller updates them in place) are
@@ -27,7 +27,7 @@
 namespace kvq {
 namespace {
 
-constexpr int kNT = 512;   // threads of a CTA = sequences scanned at once
+constexpr int kSmall = 256, kLarge = 1024;   // threads of a CTA = sequences scanned at once
 constexpr int64_t kMaxLen = 1ll << 40;
 
 struct PagesParams {
@@ -51,6 +51,7 @@ __device__ __forceinline__ int64_t pages_of(int64_t rows, int shift) {
 }
 
 // Inclusive scan of two values over the CTA (kNT threads); totals in tot[2].
+template <int kNT>
 __device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b, int64_t (*part)[2], int64_t* tot) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -132,7 +133,7 @@ __device__ __forceinline__ int find_last(const int32_t* off, int n, int32_t x) {
     return lo;
 }
 
-template <bool TRIM>
+template <bool TRIM, int kNT>
 __global__ void __launch_bounds__(kNT) pages_kernel(PagesParams p) {
     __shared__ int64_t part[kNT / 32][2], tot[2];
     __shared__ int64_t s_len[kNT];
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(kNT) pages_kernel(PagesParams p) {
     }
     bad = __syncthreads_or(bad);
     int64_t row_incl = rows, page_incl = pages;
-    block_scan2(row_incl, page_incl, part, tot);
+    block_scan2<kNT>(row_incl, page_incl, part, tot);
     const int64_t row_total = tot[0], page_total = tot[1];
     int status = KVQ_OK;
     if (bad || n_free < 0 || n_free > p.n_pages || row_total > p.max_new) status = KVQ_ERR_ARG;
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kNT) pages_kernel(PagesParams p) {
         const int s = k * kNT + tid;
         if (n_chunks > 1) one = seq_need<TRIM>(p, s);
         int64_t ri = TRIM ? 0 : one.rows, pi = one.p1 - one.p0;
-        block_scan2(ri, pi, part, tot);
+        block_scan2<kNT>(ri, pi, part, tot);
         const int64_t chunk_rows = tot[0], chunk_pages = tot[1];
         s_len[tid] = one.len;
         s_row[tid] = (int32_t)(ri - (TRIM ? 0 : one.rows));
@@ -289,8 +290,12 @@ cudaError_t launch_pages_reserve(int32_t n_seq, int32_t page_rows, const int64_t
     p.positions = positions;
     p.max_new = max_new;
     // about two rows a thread: one CTA (no ticket) for a decode step's rows
-    const int64_t grid = std::min<int64_t>(152, std::max<int64_t>(1, (max_new + 2 * kNT - 1) / (2 * kNT)));
-    pages_kernel<false><<<(unsigned)grid, kNT, 0, stream>>>(p);
+    if (n_seq <= kSmall && max_new <= 2 * kSmall) {
+        pages_kernel<false, kSmall><<<1, kSmall, 0, stream>>>(p);
+    } else {
+        const int64_t grid = std::min<int64_t>(152, std::max<int64_t>(1, (max_new + 2 * kLarge - 1) / (2 * kLarge)));
+        pages_kernel<false, kLarge><<<(unsigned)grid, kLarge, 0, stream>>>(p);
+    }
     return cudaGetLastError();
 }
 
@@ -300,7 +305,8 @@ cudaError_t launch_pages_trim(int32_t n_seq, int32_t page_rows, int64_t* lens, c
     PagesParams p =
         base_params(n_seq, page_rows, lens, keep, table, table_stride, free_pages, n_free, n_pages, workspace);
     p.lens_out = lens;
-    pages_kernel<true><<<(unsigned)std::max(1, std::min(8, n_seq / 256)), kNT, 0, stream>>>(p);
+    if (n_seq <= kSmall) pages_kernel<true, kSmall><<<1, kSmall, 0, stream>>>(p);
+    else pages_kernel<true, kLarge><<<(unsigned)std::min(8, (n_seq + kLarge - 1) / kLarge), kLarge, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

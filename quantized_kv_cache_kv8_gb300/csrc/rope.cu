@@ -236,9 +236,9 @@ cudaError_t launch_rope_append(kvq_format fmt, const kvq_mla_layout& L, const kv
     p.pairs = rope.dim / 2;
     for (int i = 0; i < p.pairs; ++i) {
         // turns per position as a 64-bit fraction; whole turns drop out
-        const double turns = rope.inv_freq[i] / (2.0 * M_PI);
-        const double f = turns - floor(turns);
-        p.inc[i] = f >= 1.0 ? 0 : (uint64_t)ldexp(f, 63) << 1 | (uint64_t)(fmod(ldexp(f, 64), 2.0) >= 1.0);
+        double f = rope.inv_freq[i] / (2.0 * M_PI);
+        if (!(f >= 0.0 && f < 1.0)) f -= floor(f);
+        p.inc[i] = f < 1.0 ? (uint64_t)(f * 0x1p64) : 0;
         p.axis[i] = rope.axis[i];
     }
     p.pos = pos;

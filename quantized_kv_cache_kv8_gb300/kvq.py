@@ -425,6 +425,12 @@ def _at(t, dtype, dev, name, shape):
     return t.data_ptr()
 
 
+def _widths(fmt, layout):
+    """(row dims, code bytes of a row) of a paged pool's format."""
+    D = layout.block_dim[0] + (layout.block_dim[1] if layout.n_blocks > 1 else 0)
+    return D, D if fmt == KVQ_KV8 else D // 2
+
+
 def kv_pages_workspace_size() -> int:
     return lib().kv_pages_workspace_size()
 
@@ -480,7 +486,7 @@ def kv_rope_append(fmt: int, rope: Rope, x_new, positions, slot_map, q_in, q_out
     x_new None: only queries; q_in None: only rows."""
     layout = layout or mla_layout()
     dev, st = _here(stream)
-    D = layout.block_dim[0] + (layout.block_dim[1] if layout.n_blocks > 1 else 0)
+    D, row = _widths(fmt, layout)
     dim, axes = rope.dim, rope.n_axes
     n = x_new.shape[0] if x_new is not None else q_in.shape[0]
     pos = _at(positions, torch.int64, dev, "positions", (n,) if axes == 1 and positions.dim() == 1 else (axes, n))
@@ -493,7 +499,7 @@ def kv_rope_append(fmt: int, rope: Rope, x_new, positions, slot_map, q_in, q_out
             raise ValueError(f"x_new must have {D} columns")
         rows = codes.shape[0]
         sp = _at(slot_map, torch.int64, dev, "slot_map", (n,))
-        cp = _at(codes, torch.uint8, dev, "codes", (rows, row_bytes(fmt, layout)))
+        cp = _at(codes, torch.uint8, dev, "codes", (rows, row))
         fp = _at(scales, torch.float32, dev, "scales", (rows, layout.n_blocks))
     qi = qo = None
     qd, heads, si, so = KVQ_F32, 0, (0, 0), (0, 0)
@@ -530,7 +536,7 @@ def kv_attn_paged(fmt: int, q, cu_q, codes, scales, block_table, kv_lens, page_r
     qd = _qdtype(q)
     _ok((_lib or lib()).kv_attn_paged(
         fmt, C.byref(layout), _at(q, q.dtype, dev, "q", (n, H, 576)), qd, n, H, B,
-        _at(cu_q, torch.int64, dev, "cu_q", (B + 1,)), _at(codes, torch.uint8, dev, "codes", (rows, row_bytes(fmt, layout))),
+        _at(cu_q, torch.int64, dev, "cu_q", (B + 1,)), _at(codes, torch.uint8, dev, "codes", (rows, _widths(fmt, layout)[1])),
         _at(scales, torch.float32, dev, "scales", (rows, layout.n_blocks)),
         _at(block_table, torch.int32, dev, "block_table", (B, stride)), stride,
         _at(kv_lens, torch.int64, dev, "kv_lens", (B,)), page_rows, rows // page_rows, float(sm_scale),
