@@ -288,6 +288,37 @@ __device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c
     }
 }
 
+// Two f32 operations in one instruction.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2(uint32_t a, uint32_t b) { return f2(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ float2 unpack(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
 // ---- queries ------------------------------------------------------------------
 // Prologue and epilogue run once a segment, with few warps: what counts is the
 // chain of each warp, so a warp takes four vectors at once, 8 lanes each.  Lane
@@ -296,35 +327,48 @@ __device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c
 // The unscaled 512-point transform of four vectors, element 4 (l + 8 i) + k in
 // v[i][k]: in registers over k and i, by shuffles over the 8 lanes (a vector over a
 // whole warp would shuffle five times instead of three, and take twice as long).
-__device__ __forceinline__ void butterfly(float& a, float& b) {
-    const float s = a + b, d = a - b;
+__device__ __forceinline__ void butterfly(F2& a, F2& b) {
+    const F2 s = add2(a, b);
+    b = fma2(b, f2(-1.0f, -1.0f), a);
     a = s;
-    b = d;
 }
 template <int N>
 __device__ __forceinline__ void transform(float (&v)[N][4], int lane) {
+    F2 x[N][2];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        butterfly(v[i][0], v[i][1]);
-        butterfly(v[i][2], v[i][3]);
-        butterfly(v[i][0], v[i][2]);
-        butterfly(v[i][1], v[i][3]);
+        x[i][0] = f2(v[i][0] + v[i][1], v[i][0] - v[i][1]);
+        x[i][1] = f2(v[i][2] + v[i][3], v[i][2] - v[i][3]);
+        butterfly(x[i][0], x[i][1]);
     }
 #pragma unroll
     for (int h = 1; h < N; h <<= 1)
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if ((i & h) == 0)
+            if ((i & h) == 0) {
+                butterfly(x[i][0], x[i + h][0]);
+                butterfly(x[i][1], x[i + h][1]);
+            }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) butterfly(v[i][k], v[i + h][k]);
-#pragma unroll 1
     for (int h = 1; h < 8; h <<= 1) {
         const float sign = (lane & h) ? -1.0f : 1.0f;
+        const F2 s2 = f2(sign, sign);
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[i][k] = fmaf(sign, v[i][k], __shfl_xor_sync(kFull, v[i][k], h));
+            for (int k = 0; k < 2; ++k) {
+                const float2 e = unpack(x[i][k]);
+                x[i][k] = fma2(s2, x[i][k], f2(__shfl_xor_sync(kFull, e.x, h), __shfl_xor_sync(kFull, e.y, h)));
+            }
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float2 e = unpack(x[i][k]);
+            v[i][2 * k] = e.x;
+            v[i][2 * k + 1] = e.y;
+        }
 }
 // Flips the elements of v whose sign bit is set in words w of a block.
 template <int N>
@@ -443,37 +487,6 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0,
             for (int i = 0; i < kUnits; ++i) raw[i] = ahead[i];
         }
     }
-}
-
-// Two f32 operations in one instruction.
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ F2 f2(uint32_t a, uint32_t b) { return f2(__uint_as_float(a), __uint_as_float(b)); }
-__device__ __forceinline__ float2 unpack(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
 }
 
 // 32 bytes: one store where the address is a multiple of 32 (`wide`), which fills
