@@ -384,8 +384,11 @@ kvq_status kv_attn_prefill(kvq_format fmt, const kvq_mla_layout* layout,
  *
  * page_rows is a power of two (pages: 1 .. 65536, attention: 16 .. 65536), and
  * n_pages * page_rows at most 2^31 - 1.  Rows are of the formats KVQ_KV8 and
- * KVQ_TQ4.  block_table is int32 [n_seq][table_stride].  Sequences appear once
- * in a batch. */
+ * KVQ_TQ4.  block_table is int32 [n_seq][table_stride].  A sequence appears once
+ * in a batch.  Attention only reads, so sequences may list the same page there (a
+ * shared prefix); the stack of free pages knows no counts, so such a page is given
+ * back by one of them alone, and no new row goes into it.  A workspace serves one
+ * call at a time. */
 
 /* Bytes of workspace kv_pages_reserve and kv_pages_trim need: the error word
  * and a counter, zero before the first call (each call leaves it so). */
@@ -432,7 +435,8 @@ kvq_status kv_pages_trim(int32_t n_seq, int32_t page_rows, int64_t* kv_lens, con
  * positions[axis[i]][token] * inv_freq[i]: one axis for text, several (time,
  * height, width) for images and video, in whatever assignment of pairs to axes
  * (consecutive sections, interleaved) and with whatever frequency scaling the
- * model uses.  Angles are right to f32 for positions up to 2^28 in size. */
+ * model uses.  Angles are right to f32 for positions up to 2^28 in size and
+ * frequencies up to 1 (beyond: to 2^-53 positions * inv_freq radians). */
 typedef struct kvq_rope {
     int32_t dim;
     int32_t n_axes;          /* 1 .. 4 */
@@ -453,7 +457,8 @@ typedef struct kvq_rope {
  *   q_in         the queries' rotary dims [n][n_heads][dim], f32 or bf16, strides
  *                q_in_token and q_in_head (elements)
  *   q_out        where they go, same type, strides q_out_token and q_out_head;
- *                q_in itself (same strides) rotates in place.  n_heads = 0: none
+ *                q_in itself (same strides) rotates in place, no other overlap;
+ *                no stride 0 over several.  n_heads = 0: none
  *   codes, scales  the pool [pool_rows][*], rows slot_map[i] written
  *   err_word     NULL, or a device int32 error word (KVQ_ERR_NONFINITE for a row
  *                with a NaN or an infinity, as the encoders)
@@ -484,16 +489,20 @@ size_t kv_attn_paged_workspace_size(kvq_format fmt, const kvq_mla_layout* layout
  *                rows of out behind cu_q[n_seq] are left as they are
  *   codes, scales  the pool, [n_pages * page_rows] rows
  *   kv_lens      [n_seq] int64: rows of each sequence, at most
- *                table_stride * page_rows
+ *                min(table_stride, n_pages) * page_rows
  *   out          [n_tokens][n_heads][512] in q_dtype
- * Layouts as kv_attn_decode.  KVQ_PATH_TENSOR (AUTO with bf16 queries): f16
- * operands with f32 accumulation, bf16 queries only, within 2e-3 of exact before
- * the rounding to bf16.  With TQ4 the rotated query is rounded to f16 once,
- * which moves a score by about 2^-12 sm_scale |q'| |x'| / 24 more (4e-4 of the
- * outputs in the 2-norm on channel-outlier rows; the rounding to bf16 is 1.7e-3).  KVQ_PATH_SIMT (AUTO with f32 queries): f32, within 1e-5 before the
- * rounding to q_dtype.  Invalid lengths or offsets and pages outside
- * [0, n_pages) set KVQ_ERR_ARG in the workspace's device word; nothing outside
- * the pool is read. */
+ * Layouts as kv_attn_decode.  KVQ_PATH_SIMT (AUTO with f32 queries): f32, within
+ * 1e-5 before the rounding to q_dtype.  KVQ_PATH_TENSOR (AUTO with bf16 queries):
+ * bf16 queries only, f32 accumulation, within 2e-3 of exact before the rounding to
+ * bf16, but for what the query's own rounding adds.  KV8: query elements keep their 8
+ * bits down to 2^-9 of the vector's largest; smaller ones are off by at most 2^-17 of
+ * it.  TQ4: the rotated query is rounded to f16 once, which moves a score by about
+ * 2^-12 sm_scale |q'| |x'| / 24 (4e-4 of the outputs in the 2-norm on channel-outlier
+ * rows; the rounding to bf16 is 1.7e-3).
+ * A row with a NaN code, or a scale that is no finite number, makes NaN the tokens
+ * that see it and leaves the others as they are.  Invalid lengths or offsets and
+ * pages outside [0, n_pages) set KVQ_ERR_ARG in the workspace's device word; nothing
+ * outside the pool is read. */
 kvq_status kv_attn_paged(kvq_format fmt, const kvq_mla_layout* layout, const void* q, kvq_dtype q_dtype,
                          int64_t n_tokens, int32_t n_heads, int32_t n_seq, const int64_t* cu_q,
                          const uint8_t* codes, const float* scales, const int32_t* block_table,
@@ -538,7 +547,7 @@ int32_t kvq_read_device_error(void* workspace, int32_t clear, void* stream);
 int64_t kvq_read_exact_rescales(void* workspace, int32_t clear, void* stream);
 
 /* Testing hook for the timeout path of the tensor-core attention kernels (the
- * KV8, KV8 f32-query and TQ4 decode/prefill kernels).  Process-wide, not
+ * KV8, KV8 f32-query and TQ4 decode/prefill kernels, and the paged kernel).  Process-wide, not
  * thread-safe, off by default.  With polls > 0, every later launch of those
  * kernels first waits, for at most `polls` polls, on a barrier that nothing
  * arrives on, and its other tile-loop waits give up after `polls` polls too:

@@ -504,6 +504,7 @@ kvq_status kv_rope_append(kvq_format fmt, const kvq_mla_layout* layout, const kv
         !aligned(slot_map, 8) || !aligned(scales, 4) || !aligned(err_word, 4))
         return KVQ_ERR_ARG;
     if (n_heads > 0 && q_in == q_out && (q_in_token != q_out_token || q_in_head != q_out_head)) return KVQ_ERR_ARG;
+    if ((n_heads > 1 && q_out_head == 0) || (n_heads > 0 && n > 1 && q_out_token == 0)) return KVQ_ERR_ARG;
     return cuda_status(launch_rope_append(fmt, *layout, *rope, x_new, x_dtype, x_stride, n, positions, pos_stride,
                                           slot_map, q_in, q_dtype, q_in_token, q_in_head, q_out, q_out_token,
                                           q_out_head, n_heads, codes, scales, pool_rows, err_word,

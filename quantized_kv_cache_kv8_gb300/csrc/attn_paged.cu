@@ -130,8 +130,9 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
             }
             if (tid < kN) {
                 const float* s = p.scales + (int64_t)prow[tid] * p.n_blocks;
-                sc[2 * tid] = tid < nt ? s[0] : 0.0f;
-                sc[2 * tid + 1] = tid < nt ? s[p.n_blocks - 1] : 0.0f;
+                const float2 v = tid < nt ? row_scales(s[0], s[p.n_blocks - 1]) : make_float2(0.0f, 0.0f);
+                sc[2 * tid] = v.x;
+                sc[2 * tid + 1] = v.y;
             }
             __syncthreads();
             {
@@ -215,7 +216,11 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
                     const float4 pa = *reinterpret_cast<const float4*>(P + t * kPS + 8 * cq);
                     const float4 pb = *reinterpret_cast<const float4*>(P + t * kPS + 8 * cq + 4);
                     const float w[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
-                    const float x[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+                    float x[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+                    // a NaN code (finite here) reaches the vectors that see its row by their weights
+                    if (!TQ4)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) x[k] = fmaxf(x[k], -448.0f);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
 #pragma unroll

@@ -260,11 +260,16 @@ using Piece = typename PieceOf<TQ4>::type;
 struct Planes {
     uint32_t lo[4], hi[4];
 };
+// e4m3: a NaN code becomes the lowest value, for a row counts, weight 0, in the
+// context of the vectors that do not see it too; those that do get their NaN from
+// its score.
 __device__ __forceinline__ void store_piece(unsigned char* chunk, const uint4& c, int row, int q, const Planes&) {
     const uint32_t in[4] = {c.x, c.y, c.z, c.w};
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) e4m3x4_to_half2x2(in[i], w[2 * i], w[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("max.f16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(0xdf00df00u));   // -448
     *reinterpret_cast<uint4*>(chunk + sw128(row, 32 * q)) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4*>(chunk + sw128(row, 32 * q + 16)) = make_uint4(w[4], w[5], w[6], w[7]);
 }
@@ -595,14 +600,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kWalkWarp) {
         // ================= the walk: announces segments one ahead =================
-        if (lane == 0) {
-            mbar_arrive(&bars[kBarWork0]);   // the first lies there
-            for (int n = 1; more; ++n) {
-                walk.next(p);
-                if (n >= 2 && !idle_wait(&bars[kBarWorkFree0 + (n & 1)], (uint32_t)(n / 2 - 1) & 1u, sAbort, wl)) break;
-                more = announce(p, walk, pair, &sWork[n & 1]);
-                mbar_arrive(&bars[kBarWork0 + (n & 1)]);
+        if (lane == 0) mbar_arrive(&bars[kBarWork0]);   // the first lies there
+        more = __shfl_sync(kFull, (int)more, 0) != 0;
+        for (int n = 1; more; ++n) {
+            walk.next(p);
+            if (lane == 0) {
+                // a wait of a segment's length, up to millions of steps
+                more = n < 2 || idle_wait(&bars[kBarWorkFree0 + (n & 1)], (uint32_t)(n / 2 - 1) & 1u, sAbort, 8 * wl);
+                if (more) {
+                    more = announce(p, walk, pair, &sWork[n & 1]);
+                    mbar_arrive(&bars[kBarWork0 + (n & 1)]);
+                }
             }
+            more = __shfl_sync(kFull, (int)more, 0) != 0;
         }
     } else if (warp == kIssueWarp) {
         // ================= products (first CTA) =================
@@ -719,7 +729,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int box = min(1 << p.shift, kHalf);
             const int j = lane < 16 ? lane >> 2 : lane - 16, c = lane < 16 ? lane & 3 : 0;
             const bool mine = lane < 20 && j * box < kHalf;
-            uint32_t it = 0;
+            uint32_t it = 0, lat = 0, rope = 0;   // steps; steps whose latent, whose rope codes were asked for
             bool ok = true;
             for (int n = 0; ok; ++n) {
                 if (!(ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl))) break;
@@ -742,17 +752,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     id = page(t + 1);
                     if (it >= 2 && !(ok = warp_wait(&bars[kBarScore0 + (it & 1u)], (it / 2 - 1) & 1u, sAbort, wl))) break;
                     if (lane == 0) expect_bytes(&bars[kBarLat0 + (it & 1u)], boxes * box * 512);
+                    ++lat;
                     __syncwarp();
                     if (live && lane < 16)
                         load_box(sm + kOffK + (4 * (it & 1u) + c) * kChunkBytes + j * box * 128, &map, 128 * c, y,
                                  &bars[kBarLat0 + (it & 1u)]);
                     if (it >= 1 && !(ok = warp_wait(&bars[kBarScore0 + ((it - 1) & 1u)], ((it - 1) >> 1) & 1u, sAbort, wl))) break;
                     if (lane == 0) expect_bytes(&bars[kBarRope], boxes * box * 128);
+                    ++rope;
                     __syncwarp();
                     if (live && lane >= 16)
                         load_box(sm + kOffK + kRope * kChunkBytes + j * box * 128, &map, kMlaD - 128, y, &bars[kBarRope]);
                 }
             }
+            // after an abort too, no copy outlives the CTA's shared memory
+            volatile int never = 0;
+            for (uint32_t k = lat > 2 ? lat - 2 : 0; k < lat; ++k)
+                mbar_wait(&bars[kBarLat0 + (k & 1u)], (k >> 1) & 1u, &never, kWaitLimit);
+            if (rope > 0) mbar_wait(&bars[kBarRope], (rope - 1) & 1u, &never, kWaitLimit);
         }
     } else if (warp == kScaleWarp) {
         // ================= row scales, two steps ahead =================
@@ -781,6 +798,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     v[i] = make_float2(0.f, 0.f);
                     if (x + i < w.end) v[i] = make_float2(__ldg(s + i * p.n_blocks), __ldg(s + (i + 1) * p.n_blocks - 1));
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = row_scales(v[i].x, v[i].y);
                 id = page(t + 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) top = fmaxf(top, v[i].x);
@@ -834,7 +853,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             auto page = [&](int32_t r) { return r < w.end ? __ldg(table + (r >> p.shift)) : 0; };
             auto code_rows = [&](int32_t r, int32_t id) {
                 if (id < 0 || id >= p.n_pages) {
-                    if (lane == 0) set_err(p.err, KVQ_ERR_ARG);
+                    if (lane == 0 && r < w.end) set_err(p.err, KVQ_ERR_ARG);
                     id = 0;
                 }
                 return p.codes + (((int64_t)id << p.shift) + (r & ((1 << p.shift) - 1))) * kRowBytes;

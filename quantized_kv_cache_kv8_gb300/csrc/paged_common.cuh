@@ -87,6 +87,12 @@ struct PagedSched {
     static constexpr int kLogM = M == 32 ? 5 : 7, kLogN = N == 32 ? 5 : 7;
     static_assert((1 << kLogM) == M && (1 << kLogN) == N, "tile sizes");
 
+    // does sequence b have new tokens (and valid offsets)?
+    __device__ static bool some(const PagedParams& p, int b) {
+        if (b >= p.n_seq) return false;
+        const int64_t a = p.cu_q[b], e = p.cu_q[b + 1];
+        return a >= 0 && e > a && e <= p.max_tok;
+    }
     __device__ static SeqShape shape(const PagedParams& p, int b) {
         SeqShape s{0, 0, 0, 0, 0, 0, 0};
         if (b >= p.n_seq) return s;
@@ -155,7 +161,8 @@ template <int NT>
 constexpr int kWalkScratch = NT / 32 + 9;
 
 // A CTA's walk over its segments.  start() is called by all NT threads of the
-// CTA; the rest by any thread on its own (every thread holds the same walk).
+// CTA, next() by whole warps; the rest by any thread on its own (every thread holds
+// the same walk).
 template <class S>
 struct PagedWalk {
     int64_t v_end, total, ctas;   // the CTA's last number + 1; numbers in all; CTAs that hold any
@@ -244,14 +251,22 @@ struct PagedWalk {
         g.n_new = s.n_new;
         return true;
     }
+    // On to the next, by a whole warp: past sequences without new tokens (a padded
+    // batch has long runs of them) 32 at a time.
     __device__ __forceinline__ void next(const PagedParams& p) {
         u0 = 0;
         if (++j < s.tiles) return;
         seq_v += S::total(p, s);
         j = 0;
-        do {
-            s = S::shape(p, ++b);
-        } while (b < p.n_seq && s.tiles == 0);
+        ++b;
+        if (seq_v >= v_end) b = p.n_seq;   // the rest is for the walkers after this one
+        for (; b < p.n_seq; b += 32) {
+            const unsigned hit = __ballot_sync(kFull, S::some(p, b + (int)(threadIdx.x & 31)));
+            if (hit == 0u) continue;
+            b += __ffs(hit) - 1;
+            s = S::shape(p, b);
+            return;
+        }
     }
     // CTA of number v
     __device__ __forceinline__ int64_t cta_of(int64_t v) const {
@@ -291,6 +306,14 @@ __device__ __forceinline__ int32_t paged_row(const PagedParams& p, int32_t b, in
         id = 0;
     }
     return (id << p.shift) + (int32_t)(t & ((1ll << p.shift) - 1));
+}
+
+// A row's scales as the kernels use them.  One that is no finite number makes the
+// row's score NaN, and counts through it alone, where the mask can drop it: as a
+// weight's factor it would be 0 x NaN for the tokens that do not see the row.
+__device__ __forceinline__ float2 row_scales(float latent, float rope) {
+    const bool ok = fmaxf(fabsf(latent), fabsf(rope)) <= 3.402823466e38f && latent == latent && rope == rope;
+    return ok ? make_float2(latent, rope) : make_float2(0.0f, __uint_as_float(0x7fffffffu));
 }
 
 // The exact (fp32) kernel and the tensor-core kernel: query vectors a tile,

@@ -494,7 +494,7 @@ def kv_rope_append(fmt: int, rope: Rope, x_new, positions, slot_map, q_in, q_out
     xd, xs, rows = KVQ_F32, 0, 0
     if x_new is not None:
         xp, xs = _strided(x_new, 2, dev, "x_new")
-        xd, xs = _qdtype(x_new), xs[0]
+        xd, xs = _qdtype(x_new), xs[0] if n > 1 else D
         if x_new.shape[1] != D:
             raise ValueError(f"x_new must have {D} columns")
         rows = codes.shape[0]
@@ -507,6 +507,8 @@ def kv_rope_append(fmt: int, rope: Rope, x_new, positions, slot_map, q_in, q_out
         qi, si = _strided(q_in, 3, dev, "q_in")
         qo, so = _strided(q_out, 3, dev, "q_out")
         qd, heads = _qdtype(q_in), q_in.shape[1]
+        # the stride of a dimension of size one says nothing
+        si, so = ((s[0] if n > 1 else 0, s[1] if heads > 1 else 0) for s in (si, so))
         width = q_out.shape[2]
         if q_in.shape != (n, heads, dim) or q_out.shape != (n, heads, width) or width not in (dim, D) or \
                 q_out.dtype is not q_in.dtype:
@@ -531,7 +533,7 @@ def kv_attn_paged(fmt: int, q, cu_q, codes, scales, block_table, kv_lens, page_r
     layout = layout or mla_layout()
     dev, st = _here(stream)
     n, H, B, rows, stride = q.shape[0], q.shape[1], _flat(kv_lens, "kv_lens"), codes.shape[0], block_table.shape[-1]
-    if rows % page_rows != 0:
+    if page_rows <= 0 or rows % page_rows != 0:
         raise ValueError("the pool must hold whole pages")
     qd = _qdtype(q)
     _ok((_lib or lib()).kv_attn_paged(

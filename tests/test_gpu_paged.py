@@ -298,6 +298,21 @@ def test_rope_append_reports_bad_rows(kvq):
         kvq.kv_rope_append(1, rope, None, pos, None, q.transpose(1, 2), q, None, None)
 
 
+def test_rope_one_token_one_head_any_stride(kvq):
+    """Dimensions of size one have strides that say nothing."""
+    rope = kvq.rope_layout(freqs(64))
+    pos = torch.tensor([5], device="cuda")
+    q = torch.randn(64, device="cuda")
+    x = torch.randn(576, device="cuda")
+    out = torch.zeros(2, 1, 1, 64, device="cuda")
+    codes, scales = torch.zeros(2, 576, dtype=torch.uint8, device="cuda"), torch.zeros(2, 2, device="cuda")
+    for i, (qs, xs) in enumerate([((64, 64, 1), (576, 1)), ((0, 3, 1), (0, 1))]):
+        kvq.kv_rope_append(1, rope, x.as_strided((1, 576), xs), pos, torch.tensor([i], device="cuda"),
+                           q.as_strided((1, 1, 64), qs), out[i].as_strided((1, 1, 64), qs), codes, scales)
+    assert torch.equal(out[0], out[1]) and bool((out[0] != 0).any())
+    assert torch.equal(codes[0], codes[1]) and torch.equal(scales[0], scales[1]) and bool((scales > 0).all())
+
+
 # -- attention --------------------------------------------------------------------
 
 class Paged:
@@ -532,6 +547,159 @@ def test_attn_paged_on_its_own_stream_and_twice_at_once(kvq, oracle):
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("path,bf16", PATHS)
+@pytest.mark.parametrize("fmt", [1, 2])
+def test_attn_paged_rows_that_are_no_numbers(kvq, oracle, fmt, path, bf16):
+    """NaN codes and NaN or infinite scales in a late row: tokens before it do not notice, those that see it are NaN."""
+    p = Paged(kvq, oracle, fmt, [100, 30], [40, 3], 32, seed=14)
+    q = query(43, 16, 4, bf16)
+    want = p.run(q, path)
+    for what in ("code", "nan", "inf", "rope"):
+        if what == "code" and fmt == 2:
+            continue
+        r = p.table[0, 110 // 32] * 32 + 110 % 32           # row 110: tokens 10 .. 39 of sequence 0 see it
+        keep = p.codes[r].clone(), p.scales[r].clone()
+        if what == "code":
+            p.codes[r, 7] = 0xFF
+        else:
+            p.scales[r, 1 if what == "rope" else 0] = float("inf") if what == "inf" else float("nan")
+        out = p.run(q, path)
+        p.codes[r], p.scales[r] = keep
+        assert bool(torch.isnan(out[10:40]).all()), what
+        rest = torch.cat([out[:10], want[10:40], out[40:]])
+        p.check(q, rest, tolerance(fmt, path, bf16), q_rounded=fmt == 2 and path == 2)
+
+
+@pytest.mark.parametrize("path,bf16", PATHS)
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("n_seq,H,every", [(700, 4, 7), (1400, 2, 200), (300, 128, 1)])
+def test_attn_paged_padded_batches(kvq, oracle, fmt, path, bf16, n_seq, H, every):
+    """Many sequences, most of them without tokens; many short tiles to a walker."""
+    rng = np.random.default_rng(n_seq)
+    new = [int(rng.integers(1, 3)) if s % every == every - 1 else 0 for s in range(n_seq)]
+    past = [int(rng.integers(0, 40)) for _ in range(n_seq)]
+    p = Paged(kvq, oracle, fmt, past, new, 16, seed=2)
+    q = query(sum(new), H, 4, bf16)
+    out = p.run(q, path)
+    assert p.err == 0
+    p.check(q, out, tolerance(fmt, path, bf16), q_rounded=fmt == 2 and path == 2)
+
+
+@pytest.mark.parametrize("path,bf16", PATHS)
+@pytest.mark.parametrize("page", [16, 4096, 65536])
+def test_attn_paged_page_sizes(kvq, oracle, path, bf16, page):
+    p = Paged(kvq, oracle, 1, [4090, 5], [20, 2], page, seed=2, spare=1)
+    q = query(22, 8, 4, bf16)
+    out = p.run(q, path)
+    assert p.err == 0
+    p.check(q, out, tolerance(1, path, bf16))
+
+
+@pytest.mark.parametrize("path,bf16", PATHS)
+@pytest.mark.parametrize("fmt", [1, 2])
+def test_attn_paged_offset_buffers(kvq, oracle, fmt, path, bf16):
+    """Queries, output and workspace that start on 16 bytes and no more."""
+    p = Paged(kvq, oracle, fmt, [300, 5], [9, 2], 32, seed=2)
+    q = query(11, 24, 4, bf16)
+    want = p.run(q, path)
+    pad = 16 // q.element_size()
+    q2 = torch.empty(q.numel() + pad, dtype=q.dtype, device="cuda")[pad:].view(q.shape).copy_(q)
+    o2 = torch.zeros(want.numel() + pad, dtype=q.dtype, device="cuda")[pad:].view(want.shape)
+    size = kvq.kv_attn_paged_workspace_size(fmt, 2, 24, 11, p.layout, bf16, path)
+    ws = torch.zeros(size + 16, dtype=torch.uint8, device="cuda")[16:]
+    kvq.kv_attn_paged(fmt, q2, to_dev(p.cu), p.codes, p.scales, to_dev(p.table), to_dev(p.lens), 32, o2, ws, SM, p.layout, path)
+    assert torch.equal(o2, want) and kvq.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("path,bf16", PATHS)
+def test_attn_paged_shared_prefix(kvq, oracle, path, bf16):
+    """Three sequences over the same first pages."""
+    p = Paged(kvq, oracle, 1, [128, 128, 128], [5, 1, 40], 32, seed=2)
+    p.table[1, :4] = p.table[2, :4] = p.table[0, :4]
+    for b in (1, 2):
+        p.xh[b][:128] = p.xh[0][:128]
+    q = query(46, 20, 4, bf16)
+    p.check(q, p.run(q, path), tolerance(1, path, bf16))
+
+
+@pytest.mark.parametrize("path,bf16", PATHS)
+def test_attn_paged_empty_pool(kvq, path, bf16):
+    layout = kvq.mla_layout()
+    q = query(3, 4, 1, bf16)
+    out = torch.full((3, 4, 512), 7.0, dtype=q.dtype, device="cuda")
+    ws = torch.zeros(kvq.kv_attn_paged_workspace_size(1, 2, 4, 3, layout, bf16, path), dtype=torch.uint8, device="cuda")
+    for stride in (0, 2):
+        kvq.kv_attn_paged(1, q, to_dev(np.array([0, 1, 3])), torch.zeros(0, 576, dtype=torch.uint8, device="cuda"),
+                          torch.zeros(0, 2, device="cuda"), torch.zeros(2, stride, dtype=torch.int32, device="cuda"),
+                          to_dev(np.zeros(2, np.int64)), 16, out, ws, SM, layout, path)
+        assert bool((out == 0).all()) and kvq.read_device_error(ws) == 0
+
+
+def test_attn_paged_query_outliers(kvq, oracle):
+    """One query element 2^12 times the others, against rows that are small there.  The others keep an absolute error of
+    2^-17 of the largest (uniform, so 2^-17 / sqrt(3) in the root mean square): a score is off by
+    sigma = sm 2^-17 / sqrt(3) max|q| |x|, the output by at most 8 sigma_t w_t |x_t - out| summed over the rows."""
+    T, H = 600, 8
+    x = synth.mla_rows(7, T)
+    x[:, 33] = 0.0
+    p = Paged(kvq, oracle, 1, [T - 2], [2], 32, seed=2, x=x)
+    q = query(2, H, 4, True)
+    q[:, :4, 33] = 4096.0
+    out = p.run(q, 0).double().cpu().numpy()
+    qv = q.double().cpu().numpy()
+    for i in range(2):
+        K = p.xh[0][:T - 1 + i]
+        z = qv[i] @ K.T * SM
+        w = np.exp(z - z.max(1, keepdims=True))
+        w /= w.sum(1, keepdims=True)
+        ref = w @ K[:, :512]
+        for h in range(H):
+            sigma = SM * 2.0 ** -17 / math.sqrt(3.0) * np.abs(qv[i, h]).max() * np.linalg.norm(K, axis=1)
+            allowed = tolerance(1, 2, True) * np.abs(ref[h]).max() + np.max((8 * sigma * w[h]) @ np.abs(K[:, :512] - ref[h]))
+            assert np.max(np.abs(out[i, h] - ref[h])) <= allowed, (i, h)
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+def test_attn_paged_wait_that_runs_out(kvq, oracle, fmt):
+    """The products held back until their wait gives up: an error word, and the next call runs."""
+    p = Paged(kvq, oracle, fmt, [900, 60], [4, 2], 32, seed=4)
+    q = query(6, 64, 4, True)
+    try:
+        kvq.test_stall_waits(2000)
+        p.run(q, 0)
+        assert p.err == 10
+    finally:
+        kvq.test_stall_waits(0)
+    out = p.run(q, 0)
+    assert p.err == 0
+    p.check(q, out, tolerance(fmt, 2, True), q_rounded=fmt == 2)
+
+
+def test_attn_paged_two_graphs_share_a_workspace(kvq, oracle):
+    a = Paged(kvq, oracle, 1, [900, 60], [4, 2], 32, seed=4)
+    b = Paged(kvq, oracle, 2, [10, 700, 3], [1, 1, 9], 64, seed=5)
+    qs = [query(6, 64, 4, True), query(11, 16, 5, True)]
+    want = [p.run(q, 0) for p, q in zip((a, b), qs)]
+    size = max(kvq.kv_attn_paged_workspace_size(p.fmt, len(p.new), q.shape[1], q.shape[0], p.layout) for p, q in zip((a, b), qs))
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for p, q, w in zip((a, b), qs, want):
+        args = (p.fmt, q, to_dev(p.cu), p.codes, p.scales, to_dev(p.table), to_dev(p.lens), p.page)
+        outs.append((torch.zeros_like(w), args))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kvq.kv_attn_paged(*args, outs[-1][0], ws, SM, p.layout)
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for (o, _), w in zip(outs, want):
+        assert torch.equal(o, w)
+    assert kvq.read_device_error(ws) == 0
 
 
 # -- a serving loop -----------------------------------------------------------------

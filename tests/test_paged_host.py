@@ -122,3 +122,7 @@ def test_attn_paged_workspace_is_independent_of_lengths(kvq):
     assert size(14, 1, 16, 1) == 0
     assert size(1, 1, 16, 1, bf16=False, path=kvq.PATH_TENSOR) == 0
     assert kvq.kv_pages_workspace_size() >= 8
+
+
+def test_rope_append_refuses_outputs_that_overlap(kvq):
+    assert rope_call(kvq, qoh=0) == 1 and rope_call(kvq, qot=0) == 1
