@@ -155,8 +155,11 @@ __device__ __forceinline__ uint32_t cta_rank() {
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 // The same for waits that last for many steps: half a microsecond between polls.
 __device__ __forceinline__ bool idle_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
@@ -566,9 +569,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int64_t pair = blockIdx.x >> 1;
     const int64_t wl = p.wait_limit;
     if (rank == 0 && tid < 4) p.ws_desc[pair * 4 + tid] = 0;
-    PagedWalk<PagedTensor> walk;
-    // the same answer in both CTAs
-    if (!walk.template start<kThreads>(p, pair, gridDim.x >> 1, reinterpret_cast<int64_t*>(sm + kOffPart))) return;
     const bool aligned = (smem_u32(sm) & 1023u) == 0;   // else the swizzled operands would be misread
 
     if (warp == 1) {
@@ -603,13 +603,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint4*>(sm + kOffLevels) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         *reinterpret_cast<uint4*>(sm + kOffLevels + 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     }
+    __syncwarp();
+    cluster_arrive();
+    PagedWalk<PagedTensor> walk;
+    // the same answer in both CTAs
+    const bool any = walk.template start<kThreads>(p, pair, gridDim.x >> 1, reinterpret_cast<int64_t*>(sm + kOffPart));
     bool more = true;
-    if (warp == kWalkWarp && lane == 0) more = announce(p, walk, pair, &sWork[0]);
+    if (any && warp == kWalkWarp && lane == 0) more = announce(p, walk, pair, &sWork[0]);
     tc_before();
     __syncthreads();
-    cluster_sync();   // the other CTA's barriers are there, its tensor memory is allocated
+    cluster_wait();   // the other CTA's barriers are there, its tensor memory is allocated
     tc_after();
     const uint32_t tmem = *sTmem;
+    if (!any) {
+        if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+        return;
+    }
 
     if (warp >= kIssueWarp) {
         set_registers<R::kRest, R::kLaunch>();
