@@ -343,54 +343,52 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 
 // ---- queries ------------------------------------------------------------------
 // Prologue and epilogue run once a segment, with few warps: what counts is the
-// chain of each warp, so a warp takes four vectors at once, 8 lanes each.  Lane
-// l = lane % 8 of a vector has its units l + 8 i of four elements.
+// chain of each warp, so a warp takes four vectors at once, 8 lanes each (l = lane % 8),
+// and no transform crosses lanes where shared memory can turn the data instead.
 
-// The unscaled 512-point transform of four vectors, element 4 (l + 8 i) + k in
-// v[i][k]: in registers over k and i, by shuffles over the 8 lanes (a vector over a
-// whole warp would shuffle five times instead of three, and take twice as long).
+// The unscaled transform, stage by stage.
 __device__ __forceinline__ void butterfly(F2& a, F2& b) {
     const F2 s = add2(a, b);
     b = fma2(b, f2(-1.0f, -1.0f), a);
     a = s;
 }
+// Within the units, over the first index of x.
 template <int N>
-__device__ __forceinline__ void transform(float (&v)[N][4], int lane) {
-    F2 x[N][2];
+__device__ __forceinline__ void transform_in(F2 (&x)[N][2]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        x[i][0] = f2(v[i][0] + v[i][1], v[i][0] - v[i][1]);
-        x[i][1] = f2(v[i][2] + v[i][3], v[i][2] - v[i][3]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float2 e = unpack(x[i][k]);
+            x[i][k] = f2(e.x + e.y, e.x - e.y);
+        }
         butterfly(x[i][0], x[i][1]);
     }
+}
+template <int N, int K>
+__device__ __forceinline__ void transform_over(F2 (&x)[N][K]) {
 #pragma unroll
     for (int h = 1; h < N; h <<= 1)
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if ((i & h) == 0) {
-                butterfly(x[i][0], x[i + h][0]);
-                butterfly(x[i][1], x[i + h][1]);
-            }
+            if ((i & h) == 0)
+#pragma unroll
+                for (int k = 0; k < K; ++k) butterfly(x[i][k], x[i + h][k]);
+}
+// Over the 8 lanes of a vector.
+template <int N>
+__device__ __forceinline__ void transform_lanes(F2 (&x)[N][2], int lane) {
 #pragma unroll
     for (int h = 1; h < 8; h <<= 1) {
         const float sign = (lane & h) ? -1.0f : 1.0f;
-        const F2 s2 = f2(sign, sign);
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const float2 e = unpack(x[i][k]);
-                x[i][k] = fma2(s2, x[i][k], f2(__shfl_xor_sync(kFull, e.x, h), __shfl_xor_sync(kFull, e.y, h)));
+                x[i][k] = fma2(f2(sign, sign), x[i][k], f2(__shfl_xor_sync(kFull, e.x, h), __shfl_xor_sync(kFull, e.y, h)));
             }
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float2 e = unpack(x[i][k]);
-            v[i][2 * k] = e.x;
-            v[i][2 * k + 1] = e.y;
-        }
 }
 // Flips the elements of v whose sign bit is set in words w of a block.
 template <int N>
@@ -404,10 +402,22 @@ __device__ __forceinline__ void apply_signs(float (&v)[N][4], const uint64_t* w,
     }
 }
 
-// This CTA's 64 vectors, 8 a decode warp: to f16 (TQ4, rotated) or to a sum of two
-// e4m3 values, under a power of two of their own; sCz gets what undoes it in the
-// score.
-template <bool TQ4>
+// What both loaders do with a vector's largest magnitude (as bits: a NaN counts above
+// an infinity): 2^shift puts it into [2^(TOP-1), 2^TOP); |shift| <= 114 keeps that and
+// its inverse normal numbers.  A vector with a NaN or an infinity becomes NaN
+// throughout (e4m3 would saturate the infinity).  Returns 2^shift; *undo gets 2^-shift.
+template <int TOP>
+__device__ __forceinline__ float vector_scale(uint32_t top, float* undo) {
+#pragma unroll
+    for (int h = 1; h < 8; h <<= 1) top = max(top, __shfl_xor_sync(kFull, top, h));
+    const bool finite = top < 0x7f800000u;
+    const int shift = top == 0u || !finite ? 0 : min(114, TOP + 126 - max((int)(top >> 23), 1));
+    *undo = __uint_as_float((uint32_t)(127 - shift) << 23);
+    return finite ? __uint_as_float((uint32_t)(127 + shift) << 23) : __uint_as_float(0x7fffffffu);
+}
+
+// This CTA's 64 vectors, 8 a decode warp, under a power of two of their own; sCz gets
+// what undoes it in the score.  KV8: to a sum of two e4m3 values.
 __device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0, int rows, unsigned char* sQ,
                                              float* sCz, int warp, int lane) {
     constexpr int kUnits = 18;   // units of a lane: 16 latent, 2 rope
@@ -422,92 +432,131 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0,
             raw[i] = ok ? __ldg(src + g * kMlaD + 8 * i) : make_uint2(0u, 0u);   // 4 vectors on: 4 * 144 units
     };
     fetch(0, raw);
-    if (!TQ4) fetch(1, ahead);
+    fetch(1, ahead);
 #pragma unroll 1
     for (int g = 0; g < 2; ++g) {
         const int r = r0 + 4 * g;
-        // the largest magnitude, as bits: a NaN counts above an infinity
-        uint32_t top = 0u;
-        float v[16][4], rope[2][4];
-        if (TQ4) {
+        uint32_t both = 0u;
 #pragma unroll
-            for (int i = 0; i < kUnits; ++i) {
-                float (&x)[4] = i < 16 ? v[i < 16 ? i : 0] : rope[i < 16 ? 0 : i - 16];
-                x[0] = __uint_as_float(raw[i].x << 16);
-                x[1] = __uint_as_float(raw[i].x & 0xffff0000u);
-                x[2] = __uint_as_float(raw[i].y << 16);
-                x[3] = __uint_as_float(raw[i].y & 0xffff0000u);
-            }
-            if (g == 0) fetch(1, raw);
-            apply_signs(v, p.signs.w, l);
-            transform(v, lane);
-            apply_signs(rope, p.signs.w + 8, l);   // the rope block's words follow the latent block's 8
-            transform(rope, lane);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    v[i][k] *= p.kn[0];
-                    top = max(top, __float_as_uint(v[i][k]) & 0x7fffffffu);
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    rope[i][k] *= p.kn[1];
-                    top = max(top, __float_as_uint(rope[i][k]) & 0x7fffffffu);
-                }
-            }
-        } else {
-            uint32_t both = 0u;
-#pragma unroll
-            for (int i = 0; i < kUnits; ++i)
-                both = __vmaxu2(both, __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu));
-            top = max(both << 16, both & 0xffff0000u);
-        }
-#pragma unroll
-        for (int h = 1; h < 8; h <<= 1) top = max(top, __shfl_xor_sync(kFull, top, h));
-        // 2^shift puts the largest element into [2^13, 2^14), for e4m3 into [128, 256);
-        // |shift| <= 114 keeps it and its inverse normal numbers.  A vector with a NaN
-        // or an infinity becomes NaN throughout (e4m3 would saturate the infinity).
-        constexpr int kTop = TQ4 ? 14 : 8;
-        const bool finite = top < 0x7f800000u;
-        const int shift = top == 0u || !finite ? 0 : min(114, kTop + 126 - max((int)(top >> 23), 1));
-        const float scale = finite ? __uint_as_float((uint32_t)(127 + shift) << 23) : __uint_as_float(0x7fffffffu);
-        if (l == 0)
-            sCz[r] = p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 - shift) << 23) * (TQ4 ? 1.0f / kGamma : 1.0f);
+        for (int i = 0; i < kUnits; ++i)
+            both = __vmaxu2(both, __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu));
+        float undo;
+        const float scale = vector_scale<8>(max(both << 16, both & 0xffff0000u), &undo);
+        if (l == 0) sCz[r] = p.sm_scale * kLog2e * undo;
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
             const int u = l + 8 * (i < 16 ? i : i - 16);   // unit of the latent or of the rope dims
-            if (TQ4) {
-                const float (&x)[4] = i < 16 ? v[i < 16 ? i : 0] : rope[i < 16 ? 0 : i - 16];
-                const __half2 a = __floats2half2_rn(x[0] * scale, x[1] * scale);
-                const __half2 b = __floats2half2_rn(x[2] * scale, x[3] * scale);
-                unsigned char* c = sQ + (i < 16 ? i >> 1 : kRope) * kChunkBytes;
-                *reinterpret_cast<uint2*>(c + sw128(r, 8 * (u & 15))) =
-                    make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-            } else {
-                // 8 significant bits under 256: exact in f16, as is what q1 leaves
-                uint32_t c1[2], c2[2];
+            // 8 significant bits under 256: exact in f16, as is what q1 leaves
+            uint32_t c1[2], c2[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t w = h ? raw[i].y : raw[i].x;
-                    const __half2 x = __floats2half2_rn(__uint_as_float(w << 16) * scale, __uint_as_float(w & 0xffff0000u) * scale);
-                    const __nv_fp8x2_storage_t f1 =
-                        __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
-                    const __half2 rest = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2(f1, __NV_E4M3)));
-                    c1[h] = f1;
-                    c2[h] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
-                }
-                unsigned char* c = sQ + (i < 16 ? i >> 2 : kRope) * kChunkBytes;
-                const int byte = i < 16 ? 4 * (u & 31) : 4 * u;
-                *reinterpret_cast<uint32_t*>(c + sw128(r, byte)) = c1[0] | c1[1] << 16;
-                *reinterpret_cast<uint32_t*>(i < 16 ? c + 4 * kChunkBytes + sw128(r, byte) : c + sw128(r, 64 + byte)) =
-                    c2[0] | c2[1] << 16;
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t w = h ? raw[i].y : raw[i].x;
+                const __half2 x = __floats2half2_rn(__uint_as_float(w << 16) * scale, __uint_as_float(w & 0xffff0000u) * scale);
+                const __nv_fp8x2_storage_t f1 = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+                const __half2 rest = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2(f1, __NV_E4M3)));
+                c1[h] = f1;
+                c2[h] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
             }
+            unsigned char* c = sQ + (i < 16 ? i >> 2 : kRope) * kChunkBytes;
+            const int byte = i < 16 ? 4 * (u & 31) : 4 * u;
+            *reinterpret_cast<uint32_t*>(c + sw128(r, byte)) = c1[0] | c1[1] << 16;
+            *reinterpret_cast<uint32_t*>(i < 16 ? c + 4 * kChunkBytes + sw128(r, byte) : c + sw128(r, 64 + byte)) =
+                c2[0] | c2[1] << 16;
         }
-        if (!TQ4) {
 #pragma unroll
-            for (int i = 0; i < kUnits; ++i) raw[i] = ahead[i];
+        for (int i = 0; i < kUnits; ++i) raw[i] = ahead[i];
+    }
+}
+
+// TQ4: rotated, to f16.  A lane begins with dims 8 (l + 8 j) .. + 7 of its vector, six
+// of the nine stages in its registers; the warp's 8 KB of stage turn that into the 64
+// dims of chunk l for the other three (shuffles for them take longer than the rest of
+// the transform).
+__device__ __forceinline__ uint32_t to_half2(F2 x) {
+    const float2 e = unpack(x);
+    const __half2 h = __floats2half2_rn(e.x, e.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void rotate_queries(const PagedParams& p, int64_t row0, int rows, unsigned char* sQ,
+                                               unsigned char* stage, float* sCz, int warp, int lane) {
+    const int l = lane & 7;
+    const int r0 = (kHalf / kDecWarps) * warp + (lane >> 3);
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (row0 + r0) * kMlaD) + l;
+    float4* own = reinterpret_cast<float4*>(stage) + 128 * (lane >> 3);
+    // place of unit u (four dims): 8 lanes, 2 or 16 units apart, on different banks
+    auto at = [](int u) { return u ^ ((u >> 3) & 7) ^ ((u >> 6) & 1); };
+    uint4 raw[9];
+    auto fetch = [&](int g) {
+        const bool ok = r0 + 4 * g < rows;
+#pragma unroll
+        for (int j = 0; j < 9; ++j) raw[j] = ok ? __ldg(src + g * 4 * (kMlaD / 8) + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    // two elements with their signs (the lowest two bits) applied
+    auto pair = [](uint32_t w, uint32_t bits) {
+        w ^= (bits & 1u) << 15 | (bits & 2u) << 30;
+        return f2(w << 16, w & 0xffff0000u);
+    };
+    fetch(0);
+#pragma unroll 1
+    for (int g = 0; g < 2; ++g) {
+        const int r = r0 + 4 * g;
+        F2 x[16][2], rope[2][2];
+#pragma unroll
+        for (int j = 0; j < 9; ++j) {   // the rope block's word follows the latent block's 8
+            const uint32_t bits = (uint32_t)(p.signs.w[j] >> (8 * l));
+            F2 (&a)[2] = j < 8 ? x[j < 8 ? 2 * j : 0] : rope[0], (&b)[2] = j < 8 ? x[j < 8 ? 2 * j + 1 : 0] : rope[1];
+            a[0] = pair(raw[j].x, bits);
+            a[1] = pair(raw[j].y, bits >> 2);
+            b[0] = pair(raw[j].z, bits >> 4);
+            b[1] = pair(raw[j].w, bits >> 6);
         }
+        if (g == 0) fetch(1);
+        transform_in(x);
+        transform_over(x);
+        transform_in(rope);
+        transform_over(rope);
+        transform_lanes(rope, lane);
+        __syncwarp();   // the group before has been read
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 a = unpack(x[i][0]), b = unpack(x[i][1]);
+            own[at(2 * (l + 8 * (i >> 1)) + (i & 1))] = make_float4(a.x, a.y, b.x, b.y);
+        }
+        __syncwarp();
+        F2 y[8][4];   // dims 64 l + 8 m + 2 k, + 1
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 v = own[at(2 * (m + 8 * l) + h)];
+                y[m][2 * h] = f2(v.x, v.y);
+                y[m][2 * h + 1] = f2(v.z, v.w);
+            }
+        transform_over(y);
+        uint32_t top = 0u;
+        auto scaled = [&](F2 v, float kn) {
+            v = mul2(v, f2(kn, kn));
+            const float2 e = unpack(v);
+            top = max(top, max(__float_as_uint(e.x) & 0x7fffffffu, __float_as_uint(e.y) & 0x7fffffffu));
+            return v;
+        };
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int m = 0; m < 8; ++m) y[m][k] = scaled(y[m][k], p.kn[0]);
+            rope[k >> 1][k & 1] = scaled(rope[k >> 1][k & 1], p.kn[1]);
+        }
+        float undo;
+        const float scale = vector_scale<14>(top, &undo);
+        if (l == 0) sCz[r] = p.sm_scale * kLog2e * undo * (1.0f / kGamma);
+        const F2 s2 = f2(scale, scale);
+        auto store = [&](int chunk, int byte, F2 a, F2 b, F2 c, F2 d) {
+            *reinterpret_cast<uint4*>(sQ + chunk * kChunkBytes + sw128(r, byte)) =
+                make_uint4(to_half2(mul2(a, s2)), to_half2(mul2(b, s2)), to_half2(mul2(c, s2)), to_half2(mul2(d, s2)));
+        };
+#pragma unroll
+        for (int m = 0; m < 8; ++m) store(l, 16 * m, y[m][0], y[m][1], y[m][2], y[m][3]);
+        store(kRope, 16 * l, rope[0][0], rope[0][1], rope[1][0], rope[1][1]);
     }
 }
 
@@ -622,138 +671,184 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp >= kIssueWarp) {
         set_registers<R::kRest, R::kLaunch>();
-    if (warp == kWalkWarp) {
-        // ================= the walk: announces segments one ahead =================
-        if (lane == 0) mbar_arrive(&bars[kBarWork0]);   // the first lies there
-        more = __shfl_sync(kFull, (int)more, 0) != 0;
-        for (int n = 1; more; ++n) {
-            walk.next(p);
-            if (lane == 0) {
-                // a wait of a segment's length, up to millions of steps
-                more = n < 2 || idle_wait(&bars[kBarWorkFree0 + (n & 1)], (uint32_t)(n / 2 - 1) & 1u, sAbort, 8 * wl);
-                if (more) {
-                    more = announce(p, walk, pair, &sWork[n & 1]);
-                    mbar_arrive(&bars[kBarWork0 + (n & 1)]);
-                }
-            }
+        if (warp == kWalkWarp) {
+            // ================= the walk: announces segments one ahead =================
+            if (lane == 0) mbar_arrive(&bars[kBarWork0]);   // the first lies there
             more = __shfl_sync(kFull, (int)more, 0) != 0;
-        }
-    } else if (warp == kIssueWarp) {
-        // ================= products (first CTA) =================
-        if (rank == 0) {
-            const uint64_t dq = umma_desc(smem_u32(sm + kOffQ), 16, 1024);
-            const uint64_t dk = umma_desc(smem_u32(sm + kOffK), 16, 1024);
-            const uint64_t dv = umma_desc(smem_u32(sm + kOffV), kVChunkBytes, 1024);
-            const uint64_t dp = umma_desc(smem_u32(sm + kOffP), 16, 1024);
-            constexpr uint64_t kStep = kChunkBytes >> 4, kVStep = kVChunkBytes >> 4;
-            bool ok = true;
-            if (p.stall_polls > 0) ok = warp_wait(&bars[kBarNever], 0u, sAbort, p.stall_polls);
-            auto scores = [&](uint32_t it) {
-                const uint32_t d = tmem + kColS + 128 * (it & 1u);
-                if (TQ4) {
+            for (int n = 1; more; ++n) {
+                walk.next(p);
+                if (lane == 0) {
+                    // a wait of a segment's length, up to millions of steps
+                    more = n < 2 || idle_wait(&bars[kBarWorkFree0 + (n & 1)], (uint32_t)(n / 2 - 1) & 1u, sAbort, 8 * wl);
+                    if (more) {
+                        more = announce(p, walk, pair, &sWork[n & 1]);
+                        mbar_arrive(&bars[kBarWork0 + (n & 1)]);
+                    }
+                }
+                more = __shfl_sync(kFull, (int)more, 0) != 0;
+            }
+        } else if (warp == kIssueWarp) {
+            // ================= products (first CTA) =================
+            if (rank == 0) {
+                const uint64_t dq = umma_desc(smem_u32(sm + kOffQ), 16, 1024);
+                const uint64_t dk = umma_desc(smem_u32(sm + kOffK), 16, 1024);
+                const uint64_t dv = umma_desc(smem_u32(sm + kOffV), kVChunkBytes, 1024);
+                const uint64_t dp = umma_desc(smem_u32(sm + kOffP), 16, 1024);
+                constexpr uint64_t kStep = kChunkBytes >> 4, kVStep = kVChunkBytes >> 4;
+                bool ok = true;
+                if (p.stall_polls > 0) ok = warp_wait(&bars[kBarNever], 0u, sAbort, p.stall_polls);
+                auto scores = [&](uint32_t it) {
+                    const uint32_t d = tmem + kColS + 128 * (it & 1u);
+                    if (TQ4) {
 #pragma unroll
-                    for (int gr = 0; gr < 2; ++gr) {
-                        if (!warp_wait(&bars[kBarK0 + gr], it & 1u, sAbort, wl)) return false;
+                        for (int gr = 0; gr < 2; ++gr) {
+                            if (!warp_wait(&bars[kBarK0 + gr], it & 1u, sAbort, wl)) return false;
+                            tc_after();
+#pragma unroll
+                            for (int kc = 4 * gr; kc < (gr ? kChunks : 4); ++kc)
+#pragma unroll
+                                for (int ks = 0; ks < 4; ++ks)
+                                    pair_mma(d + (kc < kRope ? 0 : 64), dq + kc * kStep + 2 * ks, dk + kc * kStep + 2 * ks,
+                                             kIdescScore, ((kc == 0 || kc == kRope) && ks == 0) ? 0u : 1u);
+                        }
+                    } else {
+                        if (!warp_wait(&bars[kBarLat0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl)) return false;
+                        if (!warp_wait(&bars[kBarPeerLat0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl)) return false;
                         tc_after();
+                        const uint64_t dl = dk + (it & 1u) * 4 * kStep;
 #pragma unroll
-                        for (int kc = 4 * gr; kc < (gr ? kChunks : 4); ++kc)
+                        for (int kc = 0; kc < 4; ++kc)
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                pair_mma(d + (kc < kRope ? 0 : 64), dq + kc * kStep + 2 * ks, dk + kc * kStep + 2 * ks,
-                                         kIdescScore, ((kc == 0 || kc == kRope) && ks == 0) ? 0u : 1u);
-                    }
-                } else {
-                    if (!warp_wait(&bars[kBarLat0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl)) return false;
-                    if (!warp_wait(&bars[kBarPeerLat0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl)) return false;
-                    tc_after();
-                    const uint64_t dl = dk + (it & 1u) * 4 * kStep;
 #pragma unroll
-                    for (int kc = 0; kc < 4; ++kc)
+                                for (int part = 0; part < 2; ++part)
+                                    pair_mma_f8(d, dq + (4 * part + kc) * kStep + 2 * ks, dl + kc * kStep + 2 * ks, kIdescScore,
+                                                (kc > 0 || ks > 0 || part > 0) ? 1u : 0u);
+                        if (!warp_wait(&bars[kBarRope], it & 1u, sAbort, wl)) return false;
+                        if (!warp_wait(&bars[kBarPeerRope], it & 1u, sAbort, wl)) return false;
+                        tc_after();
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
+                        for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                             for (int part = 0; part < 2; ++part)
-                                pair_mma_f8(d, dq + (4 * part + kc) * kStep + 2 * ks, dl + kc * kStep + 2 * ks, kIdescScore,
-                                            (kc > 0 || ks > 0 || part > 0) ? 1u : 0u);
-                    if (!warp_wait(&bars[kBarRope], it & 1u, sAbort, wl)) return false;
-                    if (!warp_wait(&bars[kBarPeerRope], it & 1u, sAbort, wl)) return false;
-                    tc_after();
-#pragma unroll
-                    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-                        for (int part = 0; part < 2; ++part)
-                            pair_mma_f8(d + 64, dq + kRope * kStep + 4 * part + 2 * ks, dk + kRope * kStep + 4 + 2 * ks,
-                                        kIdescScore, (ks > 0 || part > 0) ? 1u : 0u);
-                }
-                pair_commit(&bars[kBarScore0 + (it & 1u)]);
-                return true;
-            };
-            uint32_t it = 0;   // step of the whole walk
-            for (int n = 0; ok; ++n) {
-                ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl);
-                if (!ok) break;
-                const int steps = __shfl_sync(kFull, sWork[n & 1].steps, 0);
-                warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
-                if (steps == 0) break;
-                if (!TQ4) {   // TQ4: the score rows come after the queries of the same warps
-                    ok = warp_wait(&bars[kBarQFirst], (uint32_t)n & 1u, sAbort, wl);
+                                pair_mma_f8(d + 64, dq + kRope * kStep + 4 * part + 2 * ks, dk + kRope * kStep + 4 + 2 * ks,
+                                            kIdescScore, (ks > 0 || part > 0) ? 1u : 0u);
+                    }
+                    pair_commit(&bars[kBarScore0 + (it & 1u)]);
+                    return true;
+                };
+                uint32_t it = 0;   // step of the whole walk
+                for (int n = 0; ok; ++n) {
+                    ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl);
                     if (!ok) break;
-                }
-                // scores of step t, then the context of step t - 1; the other score
-                // buffer is free by then, as its weights came before the last context
-                for (int t = 0; t <= steps && ok; ++t) {
-                    if (t < steps && !(ok = scores(it + t))) break;
-                    if (t == 0) continue;
-                    const uint32_t s = it + t - 1;   // step of the context
-                    ok = warp_wait(&bars[kBarP], s & 1u, sAbort, wl);
-                    if (!ok) break;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && warp_wait(&bars[kBarV0 + h], s & 1u, sAbort, wl);
+                    const int steps = __shfl_sync(kFull, sWork[n & 1].steps, 0);
+                    warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
+                    if (steps == 0) break;
+                    if (!TQ4) {   // TQ4: the score rows come after the queries of the same warps
+                        ok = warp_wait(&bars[kBarQFirst], (uint32_t)n & 1u, sAbort, wl);
                         if (!ok) break;
-                        tc_after();
+                    }
+                    // scores of step t, then the context of step t - 1; the other score
+                    // buffer is free by then, as its weights came before the last context
+                    for (int t = 0; t <= steps && ok; ++t) {
+                        if (t < steps && !(ok = scores(it + t))) break;
+                        if (t == 0) continue;
+                        const uint32_t s = it + t - 1;   // step of the context
+                        ok = warp_wait(&bars[kBarP], s & 1u, sAbort, wl);
+                        if (!ok) break;
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
+                        for (int h = 0; h < 2; ++h) {
+                            ok = ok && warp_wait(&bars[kBarV0 + h], s & 1u, sAbort, wl);
+                            if (!ok) break;
+                            tc_after();
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                pair_mma(tmem + kColO + 128 * j, dp + h * kStep + 2 * ks,
-                                         dv + 2 * j * kVStep + (4 * h + ks) * 128, kIdescCtx,
-                                         (t > 1 || h > 0 || ks > 0) ? 1u : 0u);
-                        pair_commit(&bars[kBarCtx0 + h]);
+                            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                for (int ks = 0; ks < 4; ++ks)
+                                    pair_mma(tmem + kColO + 128 * j, dp + h * kStep + 2 * ks,
+                                             dv + 2 * j * kVStep + (4 * h + ks) * 128, kIdescCtx,
+                                             (t > 1 || h > 0 || ks > 0) ? 1u : 0u);
+                            pair_commit(&bars[kBarCtx0 + h]);
+                        }
+                    }
+                    it += steps;
+                }
+                __syncwarp();
+                pair_commit(&bars[kBarDone]);
+            } else if (!TQ4) {
+                // ================= this CTA's codes are there: tell the first =================
+                uint32_t it = 0;
+                bool ok = true;
+                for (int n = 0; ok; ++n) {
+                    if (!(ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl))) break;
+                    const int steps = __shfl_sync(kFull, sWork[n & 1].steps, 0);
+                    warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
+                    if (steps == 0) break;
+                    for (int t = 0; t < steps && ok; ++t, ++it) {
+                        if (!(ok = warp_wait(&bars[kBarLat0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl))) break;
+                        warp_arrive_first(&bars[kBarPeerLat0 + (it & 1u)], lane);
+                        if (!(ok = warp_wait(&bars[kBarRope], it & 1u, sAbort, wl))) break;
+                        warp_arrive_first(&bars[kBarPeerRope], lane);
                     }
                 }
-                it += steps;
             }
-            __syncwarp();
-            pair_commit(&bars[kBarDone]);
-        } else if (!TQ4) {
-            // ================= this CTA's codes are there: tell the first =================
-            uint32_t it = 0;
-            bool ok = true;
-            for (int n = 0; ok; ++n) {
-                if (!(ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl))) break;
-                const int steps = __shfl_sync(kFull, sWork[n & 1].steps, 0);
-                warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
-                if (steps == 0) break;
-                for (int t = 0; t < steps && ok; ++t, ++it) {
-                    if (!(ok = warp_wait(&bars[kBarLat0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl))) break;
-                    warp_arrive_first(&bars[kBarPeerLat0 + (it & 1u)], lane);
-                    if (!(ok = warp_wait(&bars[kBarRope], it & 1u, sAbort, wl))) break;
-                    warp_arrive_first(&bars[kBarPeerRope], lane);
+        } else if (warp == kLoadWarp) {
+            if (!TQ4) {
+                // ================= codes of the score rows, by TMA =================
+                // this CTA's 64 rows of a step in boxes of whole pages (64 rows at
+                // most): lanes 0-15 a box and 128 latent dims each, lanes 16-19 a box's
+                // last 128 bytes.  Boxes past the sequence's end are left as they are:
+                // the softmax drops their scores.
+                const int box = min(1 << p.shift, kHalf);
+                const int j = lane < 16 ? lane >> 2 : lane - 16, c = lane < 16 ? lane & 3 : 0;
+                const bool mine = lane < 20 && j * box < kHalf;
+                uint32_t it = 0, lat = 0, rope = 0;   // steps; steps whose latent, whose rope codes were asked for
+                bool ok = true;
+                for (int n = 0; ok; ++n) {
+                    if (!(ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl))) break;
+                    const Work w = sWork[n & 1];
+                    warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
+                    if (w.steps == 0) break;
+                    const int32_t* table = p.table + (int64_t)w.b * p.table_stride;
+                    const int32_t row0 = w.first + kHalf * rank + j * box;
+                    auto page = [&](int t) {
+                        const int32_t r = row0 + t * kRows;
+                        return mine && t < w.steps && r < w.end ? __ldg(table + (r >> p.shift)) : 0;
+                    };
+                    int32_t id = page(0);
+                    for (int t = 0; t < w.steps; ++t, ++it) {
+                        const int32_t r = row0 + t * kRows;
+                        const bool live = mine && r < w.end;
+                        if (id < 0 || id >= p.n_pages) id = 0;   // the decode warps report it
+                        const int32_t y = (id << p.shift) + (r & ((1 << p.shift) - 1));
+                        const uint32_t boxes = __popc(__ballot_sync(kFull, live && lane >= 16));
+                        id = page(t + 1);
+                        if (it >= 2 && !(ok = warp_wait(&bars[kBarScore0 + (it & 1u)], (it / 2 - 1) & 1u, sAbort, wl))) break;
+                        if (lane == 0) expect_bytes(&bars[kBarLat0 + (it & 1u)], boxes * box * 512);
+                        ++lat;
+                        __syncwarp();
+                        if (live && lane < 16)
+                            load_box(sm + kOffK + (4 * (it & 1u) + c) * kChunkBytes + j * box * 128, &map, 128 * c, y,
+                                     &bars[kBarLat0 + (it & 1u)]);
+                        if (it >= 1 && !(ok = warp_wait(&bars[kBarScore0 + ((it - 1) & 1u)], ((it - 1) >> 1) & 1u, sAbort, wl)))
+                            break;
+                        if (lane == 0) expect_bytes(&bars[kBarRope], boxes * box * 128);
+                        ++rope;
+                        __syncwarp();
+                        if (live && lane >= 16)
+                            load_box(sm + kOffK + kRope * kChunkBytes + j * box * 128, &map, kMlaD - 128, y, &bars[kBarRope]);
+                    }
                 }
+                // after an abort too, no copy outlives the CTA's shared memory
+                volatile int never = 0;
+                for (uint32_t k = lat > 2 ? lat - 2 : 0; k < lat; ++k)
+                    mbar_wait(&bars[kBarLat0 + (k & 1u)], (k >> 1) & 1u, &never, kWaitLimit);
+                if (rope > 0) mbar_wait(&bars[kBarRope], (rope - 1) & 1u, &never, kWaitLimit);
             }
-        }
-    } else if (warp == kLoadWarp) {
-        if (!TQ4) {
-            // ================= codes of the score rows, by TMA =================
-            // this CTA's 64 rows of a step in boxes of whole pages (64 rows at
-            // most): lanes 0-15 a box and 128 latent dims each, lanes 16-19 a box's
-            // last 128 bytes.  Boxes past the sequence's end are left as they are:
-            // the softmax drops their scores.
-            const int box = min(1 << p.shift, kHalf);
-            const int j = lane < 16 ? lane >> 2 : lane - 16, c = lane < 16 ? lane & 3 : 0;
-            const bool mine = lane < 20 && j * box < kHalf;
-            uint32_t it = 0, lat = 0, rope = 0;   // steps; steps whose latent, whose rope codes were asked for
+        } else if (warp == kScaleWarp) {
+            // ================= row scales, two steps ahead =================
+            // 4 consecutive rows a lane: in one page, as pages hold whole multiples of 16
+            uint32_t it = 0;
             bool ok = true;
             for (int n = 0; ok; ++n) {
                 if (!(ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl))) break;
@@ -761,82 +856,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
                 if (w.steps == 0) break;
                 const int32_t* table = p.table + (int64_t)w.b * p.table_stride;
-                const int32_t row0 = w.first + kHalf * rank + j * box;
                 auto page = [&](int t) {
-                    const int32_t r = row0 + t * kRows;
-                    return mine && t < w.steps && r < w.end ? __ldg(table + (r >> p.shift)) : 0;
+                    const int32_t x = w.first + t * kRows + 4 * lane;
+                    return t < w.steps && x < w.end ? __ldg(table + (x >> p.shift)) : 0;
                 };
                 int32_t id = page(0);
                 for (int t = 0; t < w.steps; ++t, ++it) {
-                    const int32_t r = row0 + t * kRows;
-                    const bool live = mine && r < w.end;
+                    const int32_t x = w.first + t * kRows + 4 * lane;
                     if (id < 0 || id >= p.n_pages) id = 0;   // the decode warps report it
-                    const int32_t y = (id << p.shift) + (r & ((1 << p.shift) - 1));
-                    const uint32_t boxes = __popc(__ballot_sync(kFull, live && lane >= 16));
+                    const float* s = p.scales + (((int64_t)id << p.shift) + (x & ((1 << p.shift) - 1))) * p.n_blocks;
+                    float2 v[4];
+                    float top = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[i] = make_float2(0.f, 0.f);
+                        if (x + i < w.end) v[i] = make_float2(__ldg(s + i * p.n_blocks), __ldg(s + (i + 1) * p.n_blocks - 1));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = row_scales(v[i].x, v[i].y);
                     id = page(t + 1);
-                    if (it >= 2 && !(ok = warp_wait(&bars[kBarScore0 + (it & 1u)], (it / 2 - 1) & 1u, sAbort, wl))) break;
-                    if (lane == 0) expect_bytes(&bars[kBarLat0 + (it & 1u)], boxes * box * 512);
-                    ++lat;
-                    __syncwarp();
-                    if (live && lane < 16)
-                        load_box(sm + kOffK + (4 * (it & 1u) + c) * kChunkBytes + j * box * 128, &map, 128 * c, y,
-                                 &bars[kBarLat0 + (it & 1u)]);
-                    if (it >= 1 && !(ok = warp_wait(&bars[kBarScore0 + ((it - 1) & 1u)], ((it - 1) >> 1) & 1u, sAbort, wl))) break;
-                    if (lane == 0) expect_bytes(&bars[kBarRope], boxes * box * 128);
-                    ++rope;
-                    __syncwarp();
-                    if (live && lane >= 16)
-                        load_box(sm + kOffK + kRope * kChunkBytes + j * box * 128, &map, kMlaD - 128, y, &bars[kBarRope]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = fmaxf(top, v[i].x);
+                    top = warp_max(top);
+                    if (it >= 2 && !(ok = warp_wait(&bars[kBarScaleFree0 + (it & 1u)], (it / 2 - 1) & 1u, sAbort, wl))) break;
+                    float4* dst = reinterpret_cast<float4*>(sm + kOffScale + (it & 1u) * kScaleBytes) + lane;
+                    dst[0] = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
+                    dst[kRows / 4] = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
+                    if (lane == 0) reinterpret_cast<float*>(sm + kOffMax)[it & 1u] = top;
+                    warp_arrive(&bars[kBarScore0 + (it & 1u)], lane);
                 }
             }
-            // after an abort too, no copy outlives the CTA's shared memory
-            volatile int never = 0;
-            for (uint32_t k = lat > 2 ? lat - 2 : 0; k < lat; ++k)
-                mbar_wait(&bars[kBarLat0 + (k & 1u)], (k >> 1) & 1u, &never, kWaitLimit);
-            if (rope > 0) mbar_wait(&bars[kBarRope], (rope - 1) & 1u, &never, kWaitLimit);
         }
-    } else if (warp == kScaleWarp) {
-        // ================= row scales, two steps ahead =================
-        // 4 consecutive rows a lane: in one page, as pages hold whole multiples of 16
-        uint32_t it = 0;
-        bool ok = true;
-        for (int n = 0; ok; ++n) {
-            if (!(ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl))) break;
-            const Work w = sWork[n & 1];
-            warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
-            if (w.steps == 0) break;
-            const int32_t* table = p.table + (int64_t)w.b * p.table_stride;
-            auto page = [&](int t) {
-                const int32_t x = w.first + t * kRows + 4 * lane;
-                return t < w.steps && x < w.end ? __ldg(table + (x >> p.shift)) : 0;
-            };
-            int32_t id = page(0);
-            for (int t = 0; t < w.steps; ++t, ++it) {
-                const int32_t x = w.first + t * kRows + 4 * lane;
-                if (id < 0 || id >= p.n_pages) id = 0;   // the decode warps report it
-                const float* s = p.scales + (((int64_t)id << p.shift) + (x & ((1 << p.shift) - 1))) * p.n_blocks;
-                float2 v[4];
-                float top = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[i] = make_float2(0.f, 0.f);
-                    if (x + i < w.end) v[i] = make_float2(__ldg(s + i * p.n_blocks), __ldg(s + (i + 1) * p.n_blocks - 1));
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = row_scales(v[i].x, v[i].y);
-                id = page(t + 1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, v[i].x);
-                top = warp_max(top);
-                if (it >= 2 && !(ok = warp_wait(&bars[kBarScaleFree0 + (it & 1u)], (it / 2 - 1) & 1u, sAbort, wl))) break;
-                float4* dst = reinterpret_cast<float4*>(sm + kOffScale + (it & 1u) * kScaleBytes) + lane;
-                dst[0] = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
-                dst[kRows / 4] = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
-                if (lane == 0) reinterpret_cast<float*>(sm + kOffMax)[it & 1u] = top;
-                warp_arrive(&bars[kBarScore0 + (it & 1u)], lane);
-            }
-        }
-    }
     } else if (warp >= kSoftWarps) {
         // ================= decode warps =================
         set_registers<R::kDecode, R::kLaunch>();
@@ -924,13 +974,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 return true;
             };
             if (it > 0 && !(ok = score_done(it - 1))) break;
-            load_queries<TQ4>(p, w.row0 + kHalf * rank, w.rows - kHalf * rank, sm + kOffQ,
-                              reinterpret_cast<float*>(sm + kOffCz) + (n & 1) * kHalf, dw, lane);
+            float* cz = reinterpret_cast<float*>(sm + kOffCz) + (n & 1) * kHalf;
+            if (TQ4)   // (the score rows' buffer is free between segments)
+                rotate_queries(p, w.row0 + kHalf * rank, w.rows - kHalf * rank, sm + kOffQ, sm + kOffK + dw * kChunkBytes, cz,
+                               dw, lane);
+            else
+                load_queries(p, w.row0 + kHalf * rank, w.rows - kHalf * rank, sm + kOffQ, cz, dw, lane);
             fence_async_smem();
             warp_arrive(&bars[kBarQ0 + (n & 1)], lane);
             if (!TQ4) warp_arrive_first(&bars[kBarQFirst], lane);
             if (TQ4) request_k(0);
             request_v(0);
+            // no score rows before every warp is through with its part of their buffer
+            if (TQ4 && !(ok = warp_wait(&bars[kBarQ0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl))) break;
             // score rows of step t, then context rows of step t - 1
             for (int t = 0; t <= w.steps; ++t) {
                 if (TQ4 && t < w.steps) {
@@ -1204,35 +1260,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             } else {
                 // unrotate: 32 vectors at a time through the context buffer (free
-                // until the next segment's rows), 16-byte units swizzled by vector
+                // until the next segment's rows), 16-byte units swizzled by vector.
+                // The 5 stages within 32 dims in the vector's own threads, the 4 over
+                // them by 8 lanes a vector.
                 float* stage = reinterpret_cast<float*>(sm + kOffV);
 #pragma unroll 1
                 for (int rr = 0; rr < 2; ++rr) {
                     if ((r >> 5) == rr) {
 #pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {
-                            float o[16];
-                            context(c, o);
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t u[32];
+                            F2 x[8][2];
+                            tmem_ld32(tmem + lane_base + kColO + 128 * sub + 32 * c, u);
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                *reinterpret_cast<float4*>(stage + lane * kMlaDV + 4 * (((d0 + 16 * c) / 4 + i) ^ (lane & 7))) =
-                                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            for (int i = 0; i < 8; ++i) {
+                                x[i][0] = mul2(f2(u[4 * i], u[4 * i + 1]), f2(f, f));
+                                x[i][1] = mul2(f2(u[4 * i + 2], u[4 * i + 3]), f2(f, f));
+                            }
+                            transform_in(x);
+                            transform_over(x);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float2 a = unpack(x[i][0]), b = unpack(x[i][1]);
+                                *reinterpret_cast<float4*>(stage + lane * kMlaDV + 4 * ((d0 / 4 + 8 * c + i) ^ (lane & 7))) =
+                                    make_float4(a.x, a.y, b.x, b.y);
+                            }
                         }
                     }
                     worker_sync<kSoft>();
                     {
                         const int k = 4 * warp + (lane >> 3), l = lane & 7;
                         const int ov = kHalf * rank + 32 * rr + k;
+                        F2 x[16][2];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float4 y = *reinterpret_cast<const float4*>(stage + k * kMlaDV + 4 * ((l + 8 * i) ^ (k & 7)));
+                            x[i][0] = f2(y.x, y.y);
+                            x[i][1] = f2(y.z, y.w);
+                        }
+                        transform_over(x);
                         float v[16][4];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float4 x = *reinterpret_cast<const float4*>(stage + k * kMlaDV + 4 * ((l + 8 * i) ^ (k & 7)));
-                            v[i][0] = x.x;
-                            v[i][1] = x.y;
-                            v[i][2] = x.z;
-                            v[i][3] = x.w;
+                            const float2 a = unpack(x[i][0]), b = unpack(x[i][1]);
+                            v[i][0] = a.x;
+                            v[i][1] = a.y;
+                            v[i][2] = b.x;
+                            v[i][3] = b.y;
                         }
-                        transform(v, lane);
                         apply_signs(v, p.signs.w, l);
                         if (ov < rows) {
 #pragma unroll
