@@ -1113,10 +1113,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tc_after();
                     float zt = -INFINITY, yt = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < kCols; ++j) {
-                        const float s = s_l[j];
-                        zt = fmaxf(zt, z[j]);
-                        yt = fmaxf(yt, z[j] + (s > 0.0f ? __log2f(s) : -INFINITY));   // -inf: an inert latent block
+                    for (int j = 0; j < kCols; j += 4) {
+                        const float4 sl = TQ4 ? *reinterpret_cast<const float4*>(s_l + j) : s_lat[j / 4];
+                        const float s[4] = {sl.x, sl.y, sl.z, sl.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            zt = fmaxf(zt, z[j + k]);
+                            yt = fmaxf(yt, z[j + k] + (s[k] > 0.0f ? __log2f(s[k]) : -INFINITY));   // -inf: an inert latent block
+                        }
                     }
                     sX[tid] = zt;
                     sX[kSoft + tid] = yt;
