@@ -106,7 +106,7 @@ constexpr uint32_t kOffCz = kOffScale + 2 * kScaleBytes;    // score scale of a 
 constexpr uint32_t kOffBar = kOffCz + 2 * kHalf * 4;
 constexpr uint32_t kOffMax = kOffBar + 26 * 8;              // largest s_L of two steps
 constexpr uint32_t kOffLevels = kOffMax + 16;
-constexpr uint32_t kOffMisc = kOffLevels + 32;              // abort flag, TMEM base
+constexpr uint32_t kOffMisc = kOffLevels + 16;              // abort flag, TMEM base
 constexpr uint32_t kOffWork = kOffMisc + 16;                // two segments, announced one ahead
 constexpr uint32_t kSmemUsed = kOffWork + 2 * 72;
 constexpr uint32_t kOffPart = kOffScale;                    // scan of the work split, before the steps
@@ -273,10 +273,17 @@ struct PieceOf<true> {
 template <bool TQ4>
 using Piece = typename PieceOf<TQ4>::type;
 
-// f16 levels as byte planes, four levels a word
+// The f16 levels of codes 8-15 as byte planes, four levels a word; those of codes
+// 7-0 are their negatives.
 struct Planes {
-    uint32_t lo[4], hi[4];
+    uint32_t lo[2], hi[2];
 };
+constexpr bool levels_mirror() {
+    for (int k = 0; k < 8; ++k)
+        if (kTq4LevelBits[7 - k] != (kTq4LevelBits[8 + k] ^ 0x80000000u)) return false;
+    return true;
+}
+static_assert(levels_mirror(), "decode takes the lower levels from the upper ones");
 // e4m3: a NaN code becomes the lowest value, for a row counts, weight 0, in the
 // context of the vectors that do not see it too; those that do get their NaN from
 // its score.
@@ -290,19 +297,20 @@ __device__ __forceinline__ void store_piece(unsigned char* chunk, const uint4& c
     *reinterpret_cast<uint4*>(chunk + sw128(row, 32 * q)) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4*>(chunk + sw128(row, 32 * q + 16)) = make_uint4(w[4], w[5], w[6], w[7]);
 }
-// Nibble codes by byte permutes over the low and the high bytes of the levels:
-// the low 3 bits of a code pick among levels 0-7 and 8-15, bit 3 between the two.
+// Nibble codes by byte permutes over the low and the high bytes of the levels: the
+// low 3 bits of a code (their complement below 8) pick the level, bit 3 its sign.
 __device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c, int row, int q, const Planes& t) {
     const uint32_t in[2] = {c.x, c.y};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint32_t sel = in[i] & 0x77777777u, pick = ((in[i] >> 1) & 0x44444444u) | 0x32103210u;
+        const uint32_t neg = ~in[i] & 0x88888888u, even = neg << 4;   // signs in bit 7 of a byte: odd codes, even codes
+        const uint32_t sel = (in[i] & 0x77777777u) ^ (neg - (neg >> 3));
         uint32_t w[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t s = h ? sel >> 16 : sel, k = h ? pick >> 16 : pick;
-            const uint32_t lo = __byte_perm(__byte_perm(t.lo[0], t.lo[1], s), __byte_perm(t.lo[2], t.lo[3], s), k);
-            const uint32_t hi = __byte_perm(__byte_perm(t.hi[0], t.hi[1], s), __byte_perm(t.hi[2], t.hi[3], s), k);
+            const uint32_t s = h ? sel >> 16 : sel;
+            const uint32_t lo = __byte_perm(t.lo[0], t.lo[1], s);
+            const uint32_t hi = __byte_perm(t.hi[0], t.hi[1], s) | (__byte_perm(even, neg, h ? 0x7362u : 0x5140u) & 0x80808080u);
             w[2 * h] = __byte_perm(lo, hi, 0x5140u);
             w[2 * h + 1] = __byte_perm(lo, hi, 0x7362u);
         }
@@ -642,15 +650,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         *sAbort = aligned ? 0 : 1;
     }
     if (TQ4 && tid == 0) {
-        uint32_t lo[4] = {0u, 0u, 0u, 0u}, hi[4] = {0u, 0u, 0u, 0u};
+        uint32_t lo[2] = {0u, 0u}, hi[2] = {0u, 0u};
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const uint32_t h = __half_as_ushort(__float2half_rn(__fmul_rn(p.lv[k], kGamma)));
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t h = __half_as_ushort(__float2half_rn(__fmul_rn(p.lv[8 + k], kGamma)));
             lo[k >> 2] |= (h & 0xffu) << (8 * (k & 3));
             hi[k >> 2] |= (h >> 8) << (8 * (k & 3));
         }
-        *reinterpret_cast<uint4*>(sm + kOffLevels) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<uint4*>(sm + kOffLevels + 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(sm + kOffLevels) = make_uint4(lo[0], lo[1], hi[0], hi[1]);
     }
     __syncwarp();
     cluster_arrive();
@@ -896,8 +903,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Planes pl{};
         if (TQ4) {
             const uint4 a = *reinterpret_cast<const uint4*>(sm + kOffLevels);
-            const uint4 b = *reinterpret_cast<const uint4*>(sm + kOffLevels + 16);
-            pl = Planes{{a.x, a.y, a.z, a.w}, {b.x, b.y, b.z, b.w}};
+            pl = Planes{{a.x, a.y}, {a.z, a.w}};
         }
         // A warp has 8 consecutive rows of each half of a step (8 rows lie in one
         // page): of the CTA's own half for the scores, of both for the context.
