@@ -4,6 +4,7 @@
 // failed check returns a status and launches nothing.  No call allocates or
 // frees device memory.
 #include "kvq_internal.cuh"
+#include "paged.cuh"
 #include "pq_common.cuh"
 
 #include <algorithm>

@@ -1,10 +1,37 @@
-// encode_common.cuh -- the TQ4 block encoder shared by the row encoder and the
-// paged append, which feeds it rotated rows from shared memory.
+// encode_common.cuh -- the row encoders that the paged append shares with the row
+// encoder kernels, fed from rotated rows in shared memory: TQ4 blocks (both use this
+// one) and KV8 rows (kv8_encode_row_warp for any source).
 #pragma once
 
 #include "kvq_internal.cuh"
 
 namespace kvq {
+
+// kv8_encode_row_warp with load(i) for element i of the row: the same bytes, the same
+// error for a NaN or an infinity.
+template <class Load>
+__device__ __forceinline__ void kv8_encode_row_from(Load load, int n_blocks, int bd0, int bd1, uint8_t* cr, float* sr,
+                                                    int lane, int32_t* err) {
+    int off = 0;
+    bool bad = false;
+    for (int b = 0; b < n_blocks; ++b) {
+        const int n = b == 0 ? bd0 : bd1;
+        float amax = 0.0f;
+        for (int i = lane; i < n; i += 32) {
+            const float a = fabsf(load(off + i));
+            bad |= !(a <= 3.402823466e38f);
+            amax = fmaxf(amax, a);
+        }
+        amax = warp_max(amax);
+        const float s = __fdiv_rn(amax, 448.0f);
+        if (lane == 0) sr[b] = s;
+        for (int i = lane; i < n; i += 32)
+            cr[off + i] =
+                s == 0.0f ? 0 : (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(load(off + i), s), __NV_SATFINITE, __NV_E4M3);
+        off += n;
+    }
+    if (__any_sync(kFull, bad) && lane == 0 && err) atomicCAS(err, 0, (int32_t)KVQ_ERR_NONFINITE);
+}
 
 struct Tq4Params {
     int32_t D, n_blocks, bd[2];

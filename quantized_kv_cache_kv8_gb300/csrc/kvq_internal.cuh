@@ -86,17 +86,16 @@ __device__ __forceinline__ float warp_max(float v) {
 // the decode kernel that appends rows both call this, so their bytes agree.
 // With CHECK, a NaN or an infinity in the row sets *err (if given and still
 // 0) to KVQ_ERR_NONFINITE; the pages define no code for such values.
-// load(i) gives element i of the row.
-template <bool CHECK, class Load>
-__device__ __forceinline__ void kv8_encode_row_from(Load load, int n_blocks, int bd0, int bd1, uint8_t* cr, float* sr,
-                                                    int lane, int32_t* err) {
+template <bool CHECK = true>
+__device__ __forceinline__ void kv8_encode_row_warp(const float* __restrict__ xr, int n_blocks, int bd0, int bd1,
+                                                    uint8_t* cr, float* sr, int lane, int32_t* err) {
     int off = 0;
     bool bad = false;
     for (int b = 0; b < n_blocks; ++b) {
         const int n = b == 0 ? bd0 : bd1;
         float amax = 0.0f;
         for (int i = lane; i < n; i += 32) {
-            const float a = fabsf(load(off + i));
+            const float a = fabsf(__ldg(xr + off + i));
             if (CHECK) bad |= !(a <= 3.402823466e38f);
             amax = fmaxf(amax, a);
         }
@@ -106,18 +105,12 @@ __device__ __forceinline__ void kv8_encode_row_from(Load load, int n_blocks, int
         for (int i = lane; i < n; i += 32) {
             uint8_t c = 0;
             if (s != 0.0f)
-                c = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(load(off + i), s), __NV_SATFINITE, __NV_E4M3);
+                c = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(__ldg(xr + off + i), s), __NV_SATFINITE, __NV_E4M3);
             cr[off + i] = c;
         }
         off += n;
     }
     if (CHECK && __any_sync(kFull, bad) && lane == 0 && err) atomicCAS(err, 0, (int32_t)KVQ_ERR_NONFINITE);
-}
-// The same from a row in global memory.
-template <bool CHECK = true>
-__device__ __forceinline__ void kv8_encode_row_warp(const float* __restrict__ xr, int n_blocks, int bd0, int bd1,
-                                                    uint8_t* cr, float* sr, int lane, int32_t* err) {
-    kv8_encode_row_from<CHECK>([xr](int i) { return __ldg(xr + i); }, n_blocks, bd0, bd1, cr, sr, lane, err);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -255,27 +248,6 @@ cudaError_t launch_attn_tc(kvq_format fmt, const kvq_mla_layout& L, const void* 
                            int32_t n_heads, const uint8_t* codes, const float* scales, const int64_t* cu_seqlens,
                            int64_t prefill_past, const AttnPlan& plan, float sm_scale, float* out, void* workspace,
                            cudaStream_t stream, const int64_t* sel = nullptr, int64_t pool_rows = 0);
-
-// Paged pools: page bookkeeping (pages.cu), rotary append (rope.cu), attention
-// (attn_paged.cu, attn_tc_paged.cu)
-cudaError_t launch_pages_reserve(int32_t n_seq, int32_t page_rows, const int64_t* lens, const int64_t* new_lens,
-                                 int32_t* table, int32_t table_stride, int32_t* free_pages, int32_t* n_free,
-                                 int32_t n_pages, int64_t* lens_out, int64_t* cu_new, int64_t* slots,
-                                 int64_t* positions, int64_t max_new, void* workspace, cudaStream_t stream);
-cudaError_t launch_pages_trim(int32_t n_seq, int32_t page_rows, int64_t* lens, const int64_t* keep, int32_t* table,
-                              int32_t table_stride, int32_t* free_pages, int32_t* n_free, int32_t n_pages,
-                              void* workspace, cudaStream_t stream);
-cudaError_t launch_rope_append(kvq_format fmt, const kvq_mla_layout& L, const kvq_rope& rope, const void* x,
-                               kvq_dtype xt, int64_t x_stride, int64_t n, const int64_t* pos, int64_t pos_stride,
-                               const int64_t* slots, const void* qi, kvq_dtype qt, int64_t qi_tok, int64_t qi_head,
-                               void* qo, int64_t qo_tok, int64_t qo_head, int32_t n_heads, uint8_t* codes,
-                               float* scales, int64_t pool_rows, int32_t* err, cudaStream_t stream);
-size_t paged_workspace_bytes(bool tensor);
-cudaError_t launch_attn_paged(kvq_format fmt, const kvq_mla_layout& L, bool tensor, const void* q, kvq_dtype dt,
-                              int64_t n_tok, int32_t n_heads, int32_t n_seq, const int64_t* cu_q, const uint8_t* codes,
-                              const float* scales, const int32_t* table, int32_t table_stride,
-                              const int64_t* kv_lens, int32_t page_rows, int32_t n_pages, float sm_scale, void* out,
-                              void* workspace, cudaStream_t stream);
 
 // K2/V4
 cudaError_t launch_k2v4_encode(const kvq_k2v4_layout& L, const float* k, const float* v, int32_t batch,

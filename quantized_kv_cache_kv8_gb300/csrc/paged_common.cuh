@@ -25,6 +25,7 @@
 #pragma once
 
 #include "attn_common.cuh"
+#include "paged.cuh"
 
 namespace kvq {
 

@@ -20,7 +20,7 @@
 // memory) and of the new table entries.  The counters that are both read and
 // written (n_free, and the lengths where the caller updates them in place) are
 // written by the CTA that arrives last, after every read.
-#include "kvq_internal.cuh"
+#include "paged.cuh"
 
 #include <algorithm>
 

@@ -17,6 +17,7 @@
 // own that come first: a row's chain (load, rotate, amax or rotation, codes) is
 // the longest of the launch.
 #include "encode_common.cuh"
+#include "paged.cuh"
 
 #include <algorithm>
 #include <math.h>
@@ -164,8 +165,8 @@ __device__ __forceinline__ void append_row(const RopeParams& p, int64_t tok, flo
     __syncwarp();
     float* so = p.scales + slot * p.enc.n_blocks;
     if (!TQ4) {
-        kv8_encode_row_from<true>([row](int i) { return row[i]; }, p.enc.n_blocks, p.enc.bd[0], p.enc.bd[1],
-                                  p.codes + slot * D, so, lane, p.err);
+        kv8_encode_row_from([row](int i) { return row[i]; }, p.enc.n_blocks, p.enc.bd[0], p.enc.bd[1], p.codes + slot * D, so,
+                            lane, p.err);
         return;
     }
     int off = 0;
