@@ -427,7 +427,8 @@ def _at(t, dtype, dev, name, shape):
 
 def _widths(fmt, layout):
     """(row dims, code bytes of a row) of a paged pool's format."""
-    D = layout.block_dim[0] + (layout.block_dim[1] if layout.n_blocks > 1 else 0)
+    dims = layout.block_dim
+    D = dims[0] + (dims[1] if layout.n_blocks > 1 else 0)
     return D, D if fmt == KVQ_KV8 else D // 2
 
 
@@ -435,10 +436,11 @@ def kv_pages_workspace_size() -> int:
     return lib().kv_pages_workspace_size()
 
 
-def _flat(t, name):
-    if t.dim() != 1:
-        raise ValueError(f"{name} must have one dimension")
-    return t.shape[0]
+def _bytes(t, dev):
+    """Address of a workspace."""
+    if t.dtype is not torch.uint8 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the current device")
+    return t.data_ptr()
 
 
 def kv_pages_reserve(kv_lens, new_lens, block_table, free_pages, n_free, page_rows: int, lens_out, cu_new, slot_map,
@@ -446,26 +448,30 @@ def kv_pages_reserve(kv_lens, new_lens, block_table, free_pages, n_free, page_ro
     """Pages, slots and positions for new_lens[s] new rows of every sequence (free_pages is the stack of all
     pages, n_free its height).  lens_out may be kv_lens, positions None."""
     dev, st = _here(stream)
-    n, m, n_pages, stride = _flat(kv_lens, "kv_lens"), _flat(slot_map, "slot_map"), free_pages.numel(), block_table.shape[-1]
-    _ok((_lib or lib()).kv_pages_reserve(
-        n, page_rows, _at(kv_lens, torch.int64, dev, "kv_lens", (n,)), _at(new_lens, torch.int64, dev, "new_lens", (n,)),
-        _at(block_table, torch.int32, dev, "block_table", (n, stride)), stride,
-        _at(free_pages, torch.int32, dev, "free_pages", (n_pages,)), _at(n_free, torch.int32, dev, "n_free", (1,)), n_pages,
-        _at(lens_out, torch.int64, dev, "lens_out", (n,)), _at(cu_new, torch.int64, dev, "cu_new", (n + 1,)),
-        _at(slot_map, torch.int64, dev, "slot_map", (m,)),
-        None if positions is None else _at(positions, torch.int64, dev, "positions", (m,)), m,
-        _at(workspace, torch.uint8, dev, "workspace", workspace.shape), workspace.numel(), st), "kv_pages_reserve")
+    i64, i32 = torch.int64, torch.int32
+    n, m, n_pages, stride = kv_lens.numel(), slot_map.numel(), free_pages.numel(), block_table.shape[-1]
+    status = (_lib or lib()).kv_pages_reserve(
+        n, page_rows, _at(kv_lens, i64, dev, "kv_lens", (n,)), _at(new_lens, i64, dev, "new_lens", (n,)),
+        _at(block_table, i32, dev, "block_table", (n, stride)), stride, _at(free_pages, i32, dev, "free_pages", (n_pages,)),
+        _at(n_free, i32, dev, "n_free", (1,)), n_pages, _at(lens_out, i64, dev, "lens_out", (n,)),
+        _at(cu_new, i64, dev, "cu_new", (n + 1,)), _at(slot_map, i64, dev, "slot_map", (m,)),
+        None if positions is None else _at(positions, i64, dev, "positions", (m,)), m, _bytes(workspace, dev),
+        workspace.numel(), st)
+    if status:
+        _ok(status, "kv_pages_reserve")
 
 
 def kv_pages_trim(kv_lens, keep_lens, block_table, free_pages, n_free, page_rows: int, workspace, stream=None):
     """Cuts every sequence back to keep_lens[s] rows (negative: keeps it, 0: ends it); its pages return to the stack."""
     dev, st = _here(stream)
-    n, n_pages, stride = _flat(kv_lens, "kv_lens"), free_pages.numel(), block_table.shape[-1]
-    _ok((_lib or lib()).kv_pages_trim(
-        n, page_rows, _at(kv_lens, torch.int64, dev, "kv_lens", (n,)), _at(keep_lens, torch.int64, dev, "keep_lens", (n,)),
-        _at(block_table, torch.int32, dev, "block_table", (n, stride)), stride,
-        _at(free_pages, torch.int32, dev, "free_pages", (n_pages,)), _at(n_free, torch.int32, dev, "n_free", (1,)), n_pages,
-        _at(workspace, torch.uint8, dev, "workspace", workspace.shape), workspace.numel(), st), "kv_pages_trim")
+    i64, i32 = torch.int64, torch.int32
+    n, n_pages, stride = kv_lens.numel(), free_pages.numel(), block_table.shape[-1]
+    status = (_lib or lib()).kv_pages_trim(
+        n, page_rows, _at(kv_lens, i64, dev, "kv_lens", (n,)), _at(keep_lens, i64, dev, "keep_lens", (n,)),
+        _at(block_table, i32, dev, "block_table", (n, stride)), stride, _at(free_pages, i32, dev, "free_pages", (n_pages,)),
+        _at(n_free, i32, dev, "n_free", (1,)), n_pages, _bytes(workspace, dev), workspace.numel(), st)
+    if status:
+        _ok(status, "kv_pages_trim")
 
 
 def _strided(t, dims, dev, name):
@@ -487,9 +493,9 @@ def kv_rope_append(fmt: int, rope: Rope, x_new, positions, slot_map, q_in, q_out
     layout = layout or mla_layout()
     dev, st = _here(stream)
     D, row = _widths(fmt, layout)
-    dim, axes = rope.dim, rope.n_axes
+    dim, axes, i64 = rope.dim, rope.n_axes, torch.int64
     n = x_new.shape[0] if x_new is not None else q_in.shape[0]
-    pos = _at(positions, torch.int64, dev, "positions", (n,) if axes == 1 and positions.dim() == 1 else (axes, n))
+    pos = _at(positions, i64, dev, "positions", (n,) if axes == 1 and positions.dim() == 1 else (axes, n))
     xp = sp = cp = fp = None
     xd, xs, rows = KVQ_F32, 0, 0
     if x_new is not None:
@@ -498,25 +504,28 @@ def kv_rope_append(fmt: int, rope: Rope, x_new, positions, slot_map, q_in, q_out
         if x_new.shape[1] != D:
             raise ValueError(f"x_new must have {D} columns")
         rows = codes.shape[0]
-        sp = _at(slot_map, torch.int64, dev, "slot_map", (n,))
+        sp = _at(slot_map, i64, dev, "slot_map", (n,))
         cp = _at(codes, torch.uint8, dev, "codes", (rows, row))
         fp = _at(scales, torch.float32, dev, "scales", (rows, layout.n_blocks))
     qi = qo = None
-    qd, heads, si, so = KVQ_F32, 0, (0, 0), (0, 0)
+    qd, heads, it, ih, ot, oh = KVQ_F32, 0, 0, 0, 0, 0
     if q_in is not None:
-        qi, si = _strided(q_in, 3, dev, "q_in")
-        qo, so = _strided(q_out, 3, dev, "q_out")
-        qd, heads = _qdtype(q_in), q_in.shape[1]
-        # the stride of a dimension of size one says nothing
-        si, so = ((s[0] if n > 1 else 0, s[1] if heads > 1 else 0) for s in (si, so))
-        width = q_out.shape[2]
-        if q_in.shape != (n, heads, dim) or q_out.shape != (n, heads, width) or width not in (dim, D) or \
-                q_out.dtype is not q_in.dtype:
+        qi, (it, ih, _) = _strided(q_in, 3, dev, "q_in")
+        qo, (ot, oh, _) = _strided(q_out, 3, dev, "q_out")
+        qd, shape, to = _qdtype(q_in), q_in.shape, q_out.shape
+        heads, width = shape[1], to[2]
+        if shape != (n, heads, dim) or to != (n, heads, width) or width not in (dim, D) or q_out.dtype is not q_in.dtype:
             raise ValueError(f"q_in must be [{n}][n_heads][{dim}] and q_out match it")
+        if n <= 1:          # the stride of a dimension of size one says nothing
+            it = ot = 0
+        if heads <= 1:
+            ih = oh = 0
         qo += (width - dim) * q_out.element_size()
     err = None if err_word is None else _err_ptr(err_word)
-    _ok((_lib or lib()).kv_rope_append(fmt, C.byref(layout), C.byref(rope), xp, xd, xs, n, pos, n, sp, qi, qd, si[0], si[1],
-                                       qo, so[0], so[1], heads, cp, fp, rows, err, st), "kv_rope_append")
+    status = (_lib or lib()).kv_rope_append(fmt, C.byref(layout), C.byref(rope), xp, xd, xs, n, pos, n, sp, qi, qd, it, ih,
+                                            qo, ot, oh, heads, cp, fp, rows, err, st)
+    if status:
+        _ok(status, "kv_rope_append")
 
 
 def kv_attn_paged_workspace_size(fmt: int, n_seq: int, n_heads: int, n_tokens: int, layout: MLALayout | None = None,
@@ -532,18 +541,23 @@ def kv_attn_paged(fmt: int, q, cu_q, codes, scales, block_table, kv_lens, page_r
     of its kv_lens[b] rows) over paged rows; out [n_tokens][n_heads][512] in q's type."""
     layout = layout or mla_layout()
     dev, st = _here(stream)
-    n, H, B, rows, stride = q.shape[0], q.shape[1], _flat(kv_lens, "kv_lens"), codes.shape[0], block_table.shape[-1]
+    i64 = torch.int64
+    B, rows, stride = kv_lens.numel(), codes.shape[0], block_table.shape[-1]
     if page_rows <= 0 or rows % page_rows != 0:
         raise ValueError("the pool must hold whole pages")
-    qd = _qdtype(q)
-    _ok((_lib or lib()).kv_attn_paged(
-        fmt, C.byref(layout), _at(q, q.dtype, dev, "q", (n, H, 576)), qd, n, H, B,
-        _at(cu_q, torch.int64, dev, "cu_q", (B + 1,)), _at(codes, torch.uint8, dev, "codes", (rows, _widths(fmt, layout)[1])),
+    if q.dim() != 3:
+        raise ValueError("q must be [n_tokens][n_heads][576]")
+    n, H, _ = q.shape
+    qd, dt = _qdtype(q), q.dtype
+    status = (_lib or lib()).kv_attn_paged(
+        fmt, C.byref(layout), _at(q, dt, dev, "q", (n, H, 576)), qd, n, H, B, _at(cu_q, i64, dev, "cu_q", (B + 1,)),
+        _at(codes, torch.uint8, dev, "codes", (rows, _widths(fmt, layout)[1])),
         _at(scales, torch.float32, dev, "scales", (rows, layout.n_blocks)),
-        _at(block_table, torch.int32, dev, "block_table", (B, stride)), stride,
-        _at(kv_lens, torch.int64, dev, "kv_lens", (B,)), page_rows, rows // page_rows, float(sm_scale),
-        _at(out, q.dtype, dev, "out", (n, H, 512)), _at(workspace, torch.uint8, dev, "workspace", workspace.shape),
-        workspace.numel(), path, st), "kv_attn_paged")
+        _at(block_table, torch.int32, dev, "block_table", (B, stride)), stride, _at(kv_lens, i64, dev, "kv_lens", (B,)),
+        page_rows, rows // page_rows, float(sm_scale), _at(out, dt, dev, "out", (n, H, 512)), _bytes(workspace, dev),
+        workspace.numel(), path, st)
+    if status:
+        _ok(status, "kv_attn_paged")
 
 
 def read_device_error(workspace, clear: bool = True, stream=None) -> int:
