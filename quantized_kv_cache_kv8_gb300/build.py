@@ -1,7 +1,9 @@
 """Builds ``libkvq.so`` in-tree with nvcc for sm_103a (GB300).
 
 Each .cu file compiles to an object in ``_build/`` (in parallel), then one
-shared library is linked next to this file.  No fast-math: the encoders rely
+shared library is linked next to this file; beside it the Python extension
+``_paged_host.so`` (g++, PyTorch's headers), which checks the tensors of the
+paged calls.  No fast-math: the encoders rely
 on IEEE f32 division and square root and on the absence of fused
 multiply-adds the source does not write.
 """
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkvq.so")
+HOST = os.path.join(HERE, "_paged_host.so")
+HOST_SOURCE = os.path.join(CSRC, "paged_host.cpp")
+HEADER = os.path.join(ROOT, "include", "kvq.h")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -40,14 +46,36 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.inc")) + \
-        [os.path.join(ROOT, "include", "kvq.h")]
+        [HEADER]
+
+
+def _newer(target: str, deps) -> bool:
+    if not os.path.exists(target):
+        return False
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(p) <= t for p in deps)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(LIB, _deps()) and _newer(HOST, [HOST_SOURCE, HEADER])
+
+
+def _build_host(verbose: bool) -> None:
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    include = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
+    tmp = HOST + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{p}" for p in include), HOST_SOURCE,
+           "-o", tmp, f"-L{os.path.join(base, 'lib')}", "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {HOST_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, HOST)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -67,8 +95,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        host = ex.submit(_build_host, verbose)
         objs = list(ex.map(compile_one, srcs))
+        host.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [cc, ARCH, "-shared", "-o", tmp, *objs, "-lcuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -8,6 +8,8 @@ is no CPU path: if the library cannot be built or loaded, every call raises.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.machinery
+import importlib.util
 import math
 import threading
 
@@ -396,10 +398,26 @@ def kv_attn_prefill(fmt: int, x_new, q, codes, scales, n_past: int, out, workspa
 
 # -- paged pools ---------------------------------------------------------------
 # A serving loop makes these calls every step, on a few KB, so what they cost the
-# host is what they cost: each argument is checked once, in a few attribute reads,
-# and passed as a plain address.
+# host is what they cost: the tensors are checked in an extension of their own
+# (csrc/paged_host.cpp), which calls the same entry points.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_host = None
+
+
+def _paged():
+    """The extension, with the library's entry points."""
+    global _host
+    L = lib()
+    with _lock:
+        if _host is None:
+            loader = importlib.machinery.ExtensionFileLoader("_paged_host", _build.HOST)
+            m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_paged_host", loader))
+            loader.exec_module(m)
+            m.init(*(C.cast(f, C.c_void_p).value for f in (L.kv_pages_reserve, L.kv_pages_trim, L.kv_rope_append,
+                                                           L.kv_attn_paged)))
+            _host = m
+    return _host
 
 
 def _here(stream):
@@ -410,37 +428,8 @@ def _here(stream):
     return dev, _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
-def _at(t, dtype, dev, name, shape):
-    """Address of a contiguous tensor on the current device; its type and shape are checked."""
-    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, not on the current device")
-        if t.dtype is not dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _widths(fmt, layout):
-    """(row dims, code bytes of a row) of a paged pool's format."""
-    dims = layout.block_dim
-    D = dims[0] + (dims[1] if layout.n_blocks > 1 else 0)
-    return D, D if fmt == KVQ_KV8 else D // 2
-
-
 def kv_pages_workspace_size() -> int:
     return lib().kv_pages_workspace_size()
-
-
-def _bytes(t, dev):
-    """Address of a workspace."""
-    if t.dtype is not torch.uint8 or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor on the current device")
-    return t.data_ptr()
 
 
 def kv_pages_reserve(kv_lens, new_lens, block_table, free_pages, n_free, page_rows: int, lens_out, cu_new, slot_map,
@@ -448,15 +437,8 @@ def kv_pages_reserve(kv_lens, new_lens, block_table, free_pages, n_free, page_ro
     """Pages, slots and positions for new_lens[s] new rows of every sequence (free_pages is the stack of all
     pages, n_free its height).  lens_out may be kv_lens, positions None."""
     dev, st = _here(stream)
-    i64, i32 = torch.int64, torch.int32
-    n, m, n_pages, stride = kv_lens.numel(), slot_map.numel(), free_pages.numel(), block_table.shape[-1]
-    status = (_lib or lib()).kv_pages_reserve(
-        n, page_rows, _at(kv_lens, i64, dev, "kv_lens", (n,)), _at(new_lens, i64, dev, "new_lens", (n,)),
-        _at(block_table, i32, dev, "block_table", (n, stride)), stride, _at(free_pages, i32, dev, "free_pages", (n_pages,)),
-        _at(n_free, i32, dev, "n_free", (1,)), n_pages, _at(lens_out, i64, dev, "lens_out", (n,)),
-        _at(cu_new, i64, dev, "cu_new", (n + 1,)), _at(slot_map, i64, dev, "slot_map", (m,)),
-        None if positions is None else _at(positions, i64, dev, "positions", (m,)), m, _bytes(workspace, dev),
-        workspace.numel(), st)
+    status = (_host or _paged()).reserve(kv_lens, new_lens, block_table, free_pages, n_free, page_rows, lens_out, cu_new,
+                                         slot_map, positions, workspace, dev, st)
     if status:
         _ok(status, "kv_pages_reserve")
 
@@ -464,24 +446,9 @@ def kv_pages_reserve(kv_lens, new_lens, block_table, free_pages, n_free, page_ro
 def kv_pages_trim(kv_lens, keep_lens, block_table, free_pages, n_free, page_rows: int, workspace, stream=None):
     """Cuts every sequence back to keep_lens[s] rows (negative: keeps it, 0: ends it); its pages return to the stack."""
     dev, st = _here(stream)
-    i64, i32 = torch.int64, torch.int32
-    n, n_pages, stride = kv_lens.numel(), free_pages.numel(), block_table.shape[-1]
-    status = (_lib or lib()).kv_pages_trim(
-        n, page_rows, _at(kv_lens, i64, dev, "kv_lens", (n,)), _at(keep_lens, i64, dev, "keep_lens", (n,)),
-        _at(block_table, i32, dev, "block_table", (n, stride)), stride, _at(free_pages, i32, dev, "free_pages", (n_pages,)),
-        _at(n_free, i32, dev, "n_free", (1,)), n_pages, _bytes(workspace, dev), workspace.numel(), st)
+    status = (_host or _paged()).trim(kv_lens, keep_lens, block_table, free_pages, n_free, page_rows, workspace, dev, st)
     if status:
         _ok(status, "kv_pages_trim")
-
-
-def _strided(t, dims, dev, name):
-    """Address and strides of a tensor on the current device whose last dimension is contiguous."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    st = t.stride()
-    if len(st) != dims or (st[-1] != 1 and t.shape[-1] > 1):
-        raise ValueError(f"{name} must have {dims} dimensions, the last one contiguous")
-    return t.data_ptr(), st
 
 
 def kv_rope_append(fmt: int, rope: Rope, x_new, positions, slot_map, q_in, q_out, codes, scales,
@@ -490,40 +457,9 @@ def kv_rope_append(fmt: int, rope: Rope, x_new, positions, slot_map, q_in, q_out
     [n][n_heads][D] whose last dims it fills; q_in itself rotates in place), x_new [n][D] rotated, encoded and
     stored in the pool rows slot_map (negative: skipped).  positions int64 [n_axes][n] (or [n] for one axis).
     x_new None: only queries; q_in None: only rows."""
-    layout = layout or mla_layout()
     dev, st = _here(stream)
-    D, row = _widths(fmt, layout)
-    dim, axes, i64 = rope.dim, rope.n_axes, torch.int64
-    n = x_new.shape[0] if x_new is not None else q_in.shape[0]
-    pos = _at(positions, i64, dev, "positions", (n,) if axes == 1 and positions.dim() == 1 else (axes, n))
-    xp = sp = cp = fp = None
-    xd, xs, rows = KVQ_F32, 0, 0
-    if x_new is not None:
-        xp, xs = _strided(x_new, 2, dev, "x_new")
-        xd, xs = _qdtype(x_new), xs[0] if n > 1 else D
-        if x_new.shape[1] != D:
-            raise ValueError(f"x_new must have {D} columns")
-        rows = codes.shape[0]
-        sp = _at(slot_map, i64, dev, "slot_map", (n,))
-        cp = _at(codes, torch.uint8, dev, "codes", (rows, row))
-        fp = _at(scales, torch.float32, dev, "scales", (rows, layout.n_blocks))
-    qi = qo = None
-    qd, heads, it, ih, ot, oh = KVQ_F32, 0, 0, 0, 0, 0
-    if q_in is not None:
-        qi, (it, ih, _) = _strided(q_in, 3, dev, "q_in")
-        qo, (ot, oh, _) = _strided(q_out, 3, dev, "q_out")
-        qd, shape, to = _qdtype(q_in), q_in.shape, q_out.shape
-        heads, width = shape[1], to[2]
-        if shape != (n, heads, dim) or to != (n, heads, width) or width not in (dim, D) or q_out.dtype is not q_in.dtype:
-            raise ValueError(f"q_in must be [{n}][n_heads][{dim}] and q_out match it")
-        if n <= 1:          # the stride of a dimension of size one says nothing
-            it = ot = 0
-        if heads <= 1:
-            ih = oh = 0
-        qo += (width - dim) * q_out.element_size()
-    err = None if err_word is None else _err_ptr(err_word)
-    status = (_lib or lib()).kv_rope_append(fmt, C.byref(layout), C.byref(rope), xp, xd, xs, n, pos, n, sp, qi, qd, it, ih,
-                                            qo, ot, oh, heads, cp, fp, rows, err, st)
+    status = (_host or _paged()).rope_append(fmt, rope, x_new, positions, slot_map, q_in, q_out, codes, scales,
+                                             layout or mla_layout(), err_word, dev, st)
     if status:
         _ok(status, "kv_rope_append")
 
@@ -539,23 +475,9 @@ def kv_attn_paged(fmt: int, q, cu_q, codes, scales, block_table, kv_lens, page_r
                   sm_scale: float = SM_SCALE_MLA, layout: MLALayout | None = None, path: int = PATH_AUTO, stream=None):
     """Causal attention of the new tokens q [n_tokens][n_heads][576] (sequence b: q[cu_q[b]:cu_q[b+1]], the last
     of its kv_lens[b] rows) over paged rows; out [n_tokens][n_heads][512] in q's type."""
-    layout = layout or mla_layout()
     dev, st = _here(stream)
-    i64 = torch.int64
-    B, rows, stride = kv_lens.numel(), codes.shape[0], block_table.shape[-1]
-    if page_rows <= 0 or rows % page_rows != 0:
-        raise ValueError("the pool must hold whole pages")
-    if q.dim() != 3:
-        raise ValueError("q must be [n_tokens][n_heads][576]")
-    n, H, _ = q.shape
-    qd, dt = _qdtype(q), q.dtype
-    status = (_lib or lib()).kv_attn_paged(
-        fmt, C.byref(layout), _at(q, dt, dev, "q", (n, H, 576)), qd, n, H, B, _at(cu_q, i64, dev, "cu_q", (B + 1,)),
-        _at(codes, torch.uint8, dev, "codes", (rows, _widths(fmt, layout)[1])),
-        _at(scales, torch.float32, dev, "scales", (rows, layout.n_blocks)),
-        _at(block_table, torch.int32, dev, "block_table", (B, stride)), stride, _at(kv_lens, i64, dev, "kv_lens", (B,)),
-        page_rows, rows // page_rows, float(sm_scale), _at(out, dt, dev, "out", (n, H, 512)), _bytes(workspace, dev),
-        workspace.numel(), path, st)
+    status = (_host or _paged()).attn_paged(fmt, q, cu_q, codes, scales, block_table, kv_lens, page_rows, out, workspace,
+                                            sm_scale, layout or mla_layout(), path, dev, st)
     if status:
         _ok(status, "kv_attn_paged")
 

@@ -126,3 +126,20 @@ def test_attn_paged_workspace_is_independent_of_lengths(kvq):
 
 def test_rope_append_refuses_outputs_that_overlap(kvq):
     assert rope_call(kvq, qoh=0) == 1 and rope_call(kvq, qot=0) == 1
+
+
+def test_paged_calls_check_their_tensors(kvq):
+    """The extension's own refusals that need no GPU."""
+    import torch
+    host = kvq._paged()
+    t = torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(ValueError):
+        host.trim(t, t, t, t, t, 16, t, 0, 0)          # not on a GPU
+    with pytest.raises(TypeError):
+        host.trim(1, t, t, t, t, 16, t, 0, 0)          # not a tensor
+    with pytest.raises(TypeError):
+        host.trim(t, t)
+    with pytest.raises(TypeError):
+        host.reserve(t, t, t, t, t, 16, t, t, t, t, t, "0", 0)
+    with pytest.raises(ValueError):                    # a rotary layout where the row layout belongs
+        host.rope_append(1, kvq.rope_layout([1.0]), None, t, t, None, t, t, t, kvq.rope_layout([1.0]), None, 0, 0)
