@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t cta = blockIdx.x;
     if (tid < 16) lvs[tid] = p.lv[tid];
+    grid_dependency_wait();
     if (tid < 4) p.ws_desc[cta * 4 + tid] = 0;
     PagedWalk<PagedSimt> walk;
     if (!walk.template start<kNT>(p, cta, gridDim.x, part)) return;
@@ -319,6 +320,7 @@ __global__ void __launch_bounds__(kMergeNT) paged_merge_kernel(const __grid_cons
     constexpr int kListWarps = (kWalkers + 31) / 32;
     __shared__ int32_t cut[kWalkers], in_warp[kListWarps];
     const int sub = threadIdx.x >> 7, tid = threadIdx.x & 127, lane = tid & 31, warp = threadIdx.x >> 5;
+    launch_dependents();
     grid_dependency_wait();
     // the walkers with a cut tile, in order: every CTA has the same list
     const bool mine = threadIdx.x < kWalkers && p.ws_desc[threadIdx.x * 4] > 0;
@@ -402,22 +404,12 @@ cudaError_t launch_exact(const PagedParams& p, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(paged_exact_kernel<TQ4, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmem);
     if (e != cudaSuccess) return e;
-    paged_exact_kernel<TQ4, BF16><<<kPagedCtas, kNT, kSmem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_chained(paged_exact_kernel<TQ4, BF16>, kPagedCtas, kNT, kSmem, stream, p);
 }
 
 template <bool TQ4, bool BF16, int M>
 cudaError_t launch_merge(const PagedParams& p, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kMergeCtas);
-    cfg.blockDim = dim3(kMergeNT);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<TQ4, BF16, M>, p);
+    return launch_chained(paged_merge_kernel<TQ4, BF16, M>, kMergeCtas, kMergeNT, 0, stream, p);
 }
 
 // query vectors of partial state: two tiles a walker

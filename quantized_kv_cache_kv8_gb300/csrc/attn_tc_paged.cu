@@ -625,7 +625,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int rank = (int)cta_rank();
     const int64_t pair = blockIdx.x >> 1;
     const int64_t wl = p.wait_limit;
-    if (rank == 0 && tid < 4) p.ws_desc[pair * 4 + tid] = 0;
     const bool aligned = (smem_u32(sm) & 1023u) == 0;   // else the swizzled operands would be misread
 
     if (warp == 1) {
@@ -661,6 +660,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     cluster_arrive();
+    grid_dependency_wait();
+    if (rank == 0 && tid < 4) p.ws_desc[pair * 4 + tid] = 0;
     PagedWalk<PagedTensor> walk;
     // the same answer in both CTAs
     const bool any = walk.template start<kThreads>(p, pair, gridDim.x >> 1, reinterpret_cast<int64_t*>(sm + kOffPart));
@@ -1386,6 +1387,14 @@ cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
     if (!TQ4 && p.n_pages > 0 && (e = pool_map(p, &map)) != cudaSuccess) return e;
     e = cudaFuncSetAttribute(paged_tensor_kernel<TQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemUsed);
     if (e != cudaSuccess) return e;
+    // Launched while its predecessor runs, the kernel is there 3.5 us sooner (8 sequences
+    // of 4096 rows 29.8 us a call, 33.4 else) but then runs 5% slower (512 tokens on
+    // 32,768 rows 3.35 ms, 3.18 else): for short calls, of at most some 60 us, by the most
+    // steps that a pair can have.
+    const int64_t tiles = p.max_tok * p.n_heads / kVecs + min(p.max_tok, (int64_t)p.n_seq);
+    const int64_t rows = (int64_t)min(p.table_stride, p.n_pages) << p.shift;
+    if (tiles * (rows / kRows + 1) <= 32 * kPagedPairs)
+        return launch_chained(paged_tensor_kernel<TQ4>, 2 * kPagedPairs, kThreads, kSmemUsed, stream, p, map);
     paged_tensor_kernel<TQ4><<<2 * kPagedPairs, kThreads, kSmemUsed, stream>>>(p, map);
     return cudaGetLastError();
 }

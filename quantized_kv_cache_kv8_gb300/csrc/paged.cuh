@@ -3,9 +3,30 @@
 // attn_tc_paged.cu).
 #pragma once
 
-#include "kvq_internal.cuh"
+#include "attn_common.cuh"
+
+#include <utility>
 
 namespace kvq {
+
+// The kernels of a serving step follow one another, each a few microseconds, so each
+// is launched while the one before it runs (a launch gap less, about 1.5 us).  Every
+// kernel lets its successor come at once and, before it touches global memory, waits
+// for its predecessor to have completed, which had waited for its own.
+template <class K, class... A>
+cudaError_t launch_chained(K* kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t stream, A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
 
 cudaError_t launch_pages_reserve(int32_t n_seq, int32_t page_rows, const int64_t* lens, const int64_t* new_lens,
                                  int32_t* table, int32_t table_stride, int32_t* free_pages, int32_t* n_free,

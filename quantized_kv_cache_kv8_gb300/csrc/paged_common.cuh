@@ -24,7 +24,6 @@
 // (floors of quotients nest), a sum of floors over consecutive integers.
 #pragma once
 
-#include "attn_common.cuh"
 #include "paged.cuh"
 
 namespace kvq {

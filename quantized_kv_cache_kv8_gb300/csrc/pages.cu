@@ -139,6 +139,8 @@ __global__ void __launch_bounds__(kNT) pages_kernel(PagesParams p) {
     __shared__ int64_t s_len[kNT];
     __shared__ int32_t s_row[kNT], s_page[kNT], s_p0[kNT];   // s_row, s_page: exclusive prefixes within the chunk
     __shared__ int s_last;
+    launch_dependents();
+    grid_dependency_wait();
     const int tid = threadIdx.x;
     const int64_t G = gridDim.x, c = blockIdx.x;
     const int n_chunks = (p.n_seq + kNT - 1) / kNT;
@@ -291,12 +293,11 @@ cudaError_t launch_pages_reserve(int32_t n_seq, int32_t page_rows, const int64_t
     p.max_new = max_new;
     // about two rows a thread: one CTA (no ticket) for a decode step's rows
     if (n_seq <= kSmall && max_new <= 2 * kSmall) {
-        pages_kernel<false, kSmall><<<1, kSmall, 0, stream>>>(p);
+        return launch_chained(pages_kernel<false, kSmall>, 1, kSmall, 0, stream, p);
     } else {
         const int64_t grid = std::min<int64_t>(152, std::max<int64_t>(1, (max_new + 2 * kLarge - 1) / (2 * kLarge)));
-        pages_kernel<false, kLarge><<<(unsigned)grid, kLarge, 0, stream>>>(p);
+        return launch_chained(pages_kernel<false, kLarge>, (unsigned)grid, kLarge, 0, stream, p);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t launch_pages_trim(int32_t n_seq, int32_t page_rows, int64_t* lens, const int64_t* keep, int32_t* table,
@@ -305,9 +306,9 @@ cudaError_t launch_pages_trim(int32_t n_seq, int32_t page_rows, int64_t* lens, c
     PagesParams p =
         base_params(n_seq, page_rows, lens, keep, table, table_stride, free_pages, n_free, n_pages, workspace);
     p.lens_out = lens;
-    if (n_seq <= kSmall) pages_kernel<true, kSmall><<<1, kSmall, 0, stream>>>(p);
-    else pages_kernel<true, kLarge><<<(unsigned)std::min(8, (n_seq + kLarge - 1) / kLarge), kLarge, 0, stream>>>(p);
-    return cudaGetLastError();
+    if (n_seq <= kSmall) return launch_chained(pages_kernel<true, kSmall>, 1, kSmall, 0, stream, p);
+    return launch_chained(pages_kernel<true, kLarge>, (unsigned)std::min(8, (n_seq + kLarge - 1) / kLarge), kLarge, 0, stream,
+                          p);
 }
 
 }  // namespace kvq

@@ -191,6 +191,8 @@ __global__ void __launch_bounds__(kNT) rope_append_kernel(const __grid_constant_
         float row[kNT / 32][kMaxRow];
     } sm;
     __shared__ float th[16];
+    launch_dependents();
+    grid_dependency_wait();
     if ((int64_t)blockIdx.x >= p.row_ctas) {
         rotate_queries<QT, V, ADJ>(p, (int64_t)blockIdx.x - p.row_ctas, sm.cs);
         return;
@@ -206,9 +208,8 @@ __global__ void __launch_bounds__(kNT) rope_append_kernel(const __grid_constant_
 
 template <bool TQ4, typename XT, typename QT, int V>
 cudaError_t launch_pairs(const RopeParams& p, bool adjacent, int64_t grid, cudaStream_t st) {
-    if (adjacent) rope_append_kernel<TQ4, XT, QT, V, true><<<(unsigned)grid, kNT, 0, st>>>(p);
-    else rope_append_kernel<TQ4, XT, QT, V, false><<<(unsigned)grid, kNT, 0, st>>>(p);
-    return cudaGetLastError();
+    return adjacent ? launch_chained(rope_append_kernel<TQ4, XT, QT, V, true>, (unsigned)grid, kNT, 0, st, p)
+                    : launch_chained(rope_append_kernel<TQ4, XT, QT, V, false>, (unsigned)grid, kNT, 0, st, p);
 }
 template <bool TQ4, typename XT, typename QT>
 cudaError_t launch_width(const RopeParams& p, bool adjacent, bool vec, int64_t grid, cudaStream_t st) {

@@ -797,3 +797,53 @@ def test_a_captured_step_replays_a_serving_loop(kvq, oracle, fmt):
     assert lens.tolist() == [len(h) for h in held] == [55, 8, 5]
     kvq.kv_pages_trim(lens, torch.zeros_like(lens), table, free, n_free, page, pws)
     assert n_free.item() == n_pages and sorted(free.tolist()) == list(range(n_pages))
+
+
+@pytest.mark.parametrize("fmt,path", [(1, 0), (2, 0), (1, 1)])
+def test_steps_back_to_back_equal_steps_waited_for(kvq, fmt, path):
+    """Each launch begins while the one before it runs and waits for its results: the bits of calls waited for one by
+    one, over steps of changing lengths in which every call reads what the one before it wrote."""
+    B, H, page, m = 5, 8, 16, 96
+    layout, rope = kvq.mla_layout(seed=3), kvq.rope_layout(freqs(64))
+    rng = np.random.default_rng(7)
+    new = [to_dev(rng.integers(0, 2 if i % 3 else 19, B).astype(np.int64)) for i in range(12)]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(12, m, 576, generator=g, device="cuda")
+    dt = torch.float32 if path == 1 else torch.bfloat16
+    q = torch.randn(12, m, H, 576, generator=g, device="cuda").to(dt)
+
+    def run(wait):
+        n_pages = 40
+        free = torch.arange(n_pages, dtype=torch.int32, device="cuda")
+        n_free = torch.tensor([n_pages], dtype=torch.int32, device="cuda")
+        table = torch.zeros(B, 20, dtype=torch.int32, device="cuda")
+        lens, keep = torch.zeros(B, dtype=torch.int64, device="cuda"), torch.zeros(B, dtype=torch.int64, device="cuda")
+        codes = torch.zeros(n_pages * page, kvq.row_bytes(fmt, layout), dtype=torch.uint8, device="cuda")
+        scales = torch.zeros(n_pages * page, 2, device="cuda")
+        cu = torch.zeros(B + 1, dtype=torch.int64, device="cuda")
+        slots, pos = torch.zeros(m, dtype=torch.int64, device="cuda"), torch.zeros(m, dtype=torch.int64, device="cuda")
+        pws = torch.zeros(kvq.kv_pages_workspace_size(), dtype=torch.uint8, device="cuda")
+        aws = torch.zeros(kvq.kv_attn_paged_workspace_size(fmt, B, H, m, layout, dt == torch.bfloat16, path),
+                          dtype=torch.uint8, device="cuda")
+        out = torch.zeros(12, m, H, 512, dtype=dt, device="cuda")
+        w = q.clone()
+        torch.cuda.synchronize()
+        pause = torch.cuda.synchronize if wait else lambda: None
+        for i in range(12):
+            kvq.kv_pages_reserve(lens, new[i], table, free, n_free, page, lens, cu, slots, pos, pws)
+            pause()
+            kvq.kv_rope_append(fmt, rope, x[i], pos, slots, w[i][..., 512:], w[i][..., 512:], codes, scales, layout)
+            pause()
+            kvq.kv_attn_paged(fmt, w[i], cu, codes, scales, table, lens, page, out[i], aws, SM, layout, path)
+            pause()
+            if i % 4 == 3:
+                kvq.kv_pages_trim(lens, keep, table, free, n_free, page, pws)      # ends every sequence
+                pause()
+        torch.cuda.synchronize()
+        assert kvq.read_device_error(pws) == 0 and kvq.read_device_error(aws) == 0
+        return out, w, codes, scales, lens, table, free, n_free
+
+    want = run(True)
+    for _ in range(5):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
