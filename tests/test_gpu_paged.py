@@ -625,6 +625,32 @@ def test_attn_paged_shared_prefix(kvq, oracle, path, bf16):
 
 
 @pytest.mark.parametrize("path,bf16", PATHS)
+@pytest.mark.parametrize("fmt", [1, 2])
+def test_attn_paged_offsets_past_32_bits(kvq, oracle, fmt, path, bf16):
+    """A pool of 8 (16) million rows, 4.8 GB: pages at its end, and rows appended there."""
+    page, n_pages = 64, (1 << 17) * fmt
+    p = Paged(kvq, oracle, fmt, [300, 70], [5, 1], page, seed=2)
+    q = query(6, 16, 4, bf16)
+    want = p.run(q, path)
+    codes = torch.empty(n_pages * page, p.codes.shape[1], dtype=torch.uint8, device="cuda")
+    scales = torch.empty(n_pages * page, p.scales.shape[1], device="cuda")
+    assert codes.numel() > 1 << 32
+    far = p.n_pages * page
+    codes[-far:], scales[-far:] = p.codes, p.scales
+    small = p.codes, p.scales, p.table
+    p.codes, p.scales = codes, scales
+    p.table = np.where(p.table < p.n_pages, p.table + n_pages - p.n_pages, p.table).astype(np.int32)
+    assert torch.equal(p.run(q, path).view(torch.int16), want.view(torch.int16)) and p.err == 0
+    rope, pos = kvq.rope_layout(freqs(64)), torch.arange(3, device="cuda")
+    x = torch.randn(3, 576, generator=torch.Generator().manual_seed(1)).cuda()
+    near = torch.zeros(3, codes.shape[1], dtype=torch.uint8, device="cuda"), torch.zeros(3, scales.shape[1], device="cuda")
+    kvq.kv_rope_append(fmt, rope, x, pos, torch.arange(3, device="cuda"), None, None, *near, p.layout)
+    last = torch.tensor([n_pages * page - 1, n_pages * page - 70, n_pages * page - 3], device="cuda")
+    kvq.kv_rope_append(fmt, rope, x, pos, last, None, None, codes, scales, p.layout)
+    assert torch.equal(codes[last], near[0]) and torch.equal(scales[last], near[1])
+
+
+@pytest.mark.parametrize("path,bf16", PATHS)
 def test_attn_paged_empty_pool(kvq, path, bf16):
     layout = kvq.mla_layout()
     q = query(3, 4, 1, bf16)
