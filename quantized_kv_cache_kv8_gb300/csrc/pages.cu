@@ -188,9 +188,13 @@ __global__ void __launch_bounds__(kNT) pages_kernel(PagesParams p) {
     int64_t row_base = 0, page_base = 0;
     for (int k = 0; k < n_chunks; ++k) {
         const int s = k * kNT + tid;
-        if (n_chunks > 1) one = seq_need<TRIM>(p, s);
-        int64_t ri = TRIM ? 0 : one.rows, pi = one.p1 - one.p0;
-        block_scan2<kNT>(ri, pi, part, tot);
+        int64_t ri = row_incl, pi = page_incl;   // the totals' scan is the only chunk's
+        if (n_chunks > 1) {
+            one = seq_need<TRIM>(p, s);
+            ri = TRIM ? 0 : one.rows;
+            pi = one.p1 - one.p0;
+            block_scan2<kNT>(ri, pi, part, tot);
+        }
         const int64_t chunk_rows = tot[0], chunk_pages = tot[1];
         s_len[tid] = one.len;
         s_row[tid] = (int32_t)(ri - (TRIM ? 0 : one.rows));
