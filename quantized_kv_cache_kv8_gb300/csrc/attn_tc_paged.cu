@@ -15,7 +15,7 @@
 // reads 6 KB of operands for each 32 cycles of products, where shared memory
 // delivers 128 B a cycle (48 cycles; 575 KB a step with the decoded stores, 4.5k
 // cycles); here the scores read 4 KB in 32 cycles and the context 6 KB in 64
-// (400 KB, 3.1k).  More vectors a CTA do not fit: 64 x 512 f32 of context are
+// (400 KB, 3.1k; 243 KB and 1.9k with KV8's scores in fp8).  More vectors a CTA do not fit: 64 x 512 f32 of context are
 // half of a CTA's tensor memory.
 //
 // Operands.  KV8: the scores run as fp8 MMAs on the codes themselves: TMA puts
@@ -34,8 +34,8 @@
 // Roles (a CTA): 8 softmax warps, 8 decode warps, one issuing warp (in the first
 // CTA; the second's passes on that its codes have arrived), one that announces
 // segments, one that fetches row scales, one that loads codes by TMA; registers
-// move to the decode warps, which hold a step's codes (setmaxnreg).  The decode warps store the score rows of
-// step t+1 once the scores of step t are complete and the context rows of step t
+// move to the warps that need them (Regs).  The decode warps store the score rows of
+// step t+1 (TQ4) once the scores of step t are complete and the context rows of step t
 // once the context of step t-1 is; the scores of t+1 are issued before the
 // context of t.  So the tensor pipe alternates between the two while the other
 // operand is being stored and while the softmax of the step runs:
@@ -54,6 +54,14 @@
 // exact path: row maxima, new m, R and E, O rescaled in tensor memory.  Both
 // limits keep w under the f16 maximum.  Rows that a vector does not see get
 // z = -inf; a vector that has seen no row has m = -inf and E = 0.
+//
+// What bounds it.  KV8, many rows a tile: the softmax warps, 3,350 cycles a step (scores
+// 1,350, vote 290, exponentials 600, weights 450, the rest hand-overs) for 2,200 of
+// products: 512 tokens on 32,768 rows x 128 heads 3.2 ms, 1,470 TFLOP/s; 32 sequences of
+// 1,024 to 131,072 rows 361 us.  TQ4: the decode warps' integer work, 5,500 a step (256
+// tokens on 16,384 rows 1.6 ms, 735 TFLOP/s).  Short tiles: rotation of queries and
+// outputs (TQ4, 777 tokens without rows before 269 us), and the start (6k cycles), the
+// queries (8k) and the partial results (6k) of a decode step (8 x 4096 rows 27 us).
 #include "tc_common.cuh"
 #include "paged_common.cuh"
 

@@ -20,6 +20,8 @@
 // memory) and of the new table entries.  The counters that are both read and
 // written (n_free, and the lengths where the caller updates them in place) are
 // written by the CTA that arrives last, after every read.
+// Measured, a reservation and its trim in a replayed graph: 64 sequences of one new
+// row 5.7 us, 1024 sequences of up to 63 12.1 us.
 #include "paged.cuh"
 
 #include <algorithm>
