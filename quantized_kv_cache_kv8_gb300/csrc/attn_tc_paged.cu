@@ -252,6 +252,22 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
         : "memory");
 }
 
+// A barrier of the four softmax warps that share 32 vectors (group 0 or 1), and the
+// same with a vote.  The groups' references are their own: they part and meet at the
+// segment's end only.
+__device__ __forceinline__ void group_sync(int group) {
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + group) : "memory");
+}
+__device__ __forceinline__ bool group_any(int group, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(2 + group)
+        : "memory");
+    return r != 0;
+}
+
 // ---- loads (KV8) --------------------------------------------------------------
 __device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
@@ -1035,8 +1051,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int r = tid & (kHalf - 1), half = (tid >> 6) & 1, sub = tid >> 7;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         unsigned char* sP = sm + kOffP + half * kChunkBytes;
-        // between the four threads of a vector: the weights' buffer, while no step's weights are in it
+        // between the four threads of a vector: the weights' buffer, while no step's
+        // weights are in it; a group's part of it, while none of its own are
         float* sX = reinterpret_cast<float*>(sm + kOffP);
+        const int group = warp & 1;
+        float* gX = reinterpret_cast<float*>(sm + kOffP + 32 * 128 * group);
         uint32_t it = 0;
         bool aborted = false;
         for (int n = 0;; ++n) {
@@ -1115,13 +1134,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const float dmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                         const bool flag = aborted | (seen_abort != 0) | (smax * (st.none ? INFINITY : st.E) > kScaleLim) |
                                           (dmax > kLagLog2);
-                        if (!worker_any<kSoft>(flag)) break;
+                        if (!group_any(group, flag)) break;
                         exact = true;
                         continue;
                     }
                     // ---- exact path: row maxima, new references, O rescaled ----
                     if (it > 0 && !warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)) aborted = true;
-                    if (worker_any<kSoft>(aborted | (*sAbort != 0))) {
+                    if (group_any(group, aborted | (*sAbort != 0))) {
                         stop = true;
                         break;
                     }
@@ -1137,15 +1156,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             yt = fmaxf(yt, z[j + k] + (s[k] > 0.0f ? __log2f(s[k]) : -INFINITY));   // -inf: an inert latent block
                         }
                     }
-                    sX[tid] = zt;
-                    sX[kSoft + tid] = yt;
-                    worker_sync<kSoft>();
+                    gX[32 * (warp >> 1) + lane] = zt;
+                    gX[128 + 32 * (warp >> 1) + lane] = yt;
+                    group_sync(group);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        zt = fmaxf(zt, sX[kHalf * k + r]);
-                        yt = fmaxf(yt, sX[kSoft + kHalf * k + r]);
+                        zt = fmaxf(zt, gX[32 * k + lane]);
+                        yt = fmaxf(yt, gX[128 + 32 * k + lane]);
                     }
-                    worker_sync<kSoft>();   // read before any thread's weights go there
+                    group_sync(group);   // read before any thread's weights go there
                     const float mn = fmaxf(st.m, zt), rn = fmaxf(st.R, yt);
                     const bool inert = rn == -INFINITY;
                     const float le = fminf(mn - rn - kHeadroom, kLogEmax);
@@ -1171,7 +1190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             tmem_st16(tmem + lane_base + kColO + 16 * c, o);
                         }
                         tmem_wait_st();
-                        if (tid == 0 && rank == 0) atomicAdd(p.exact_count, 1u);
+                        if (warp < 2 && lane == 0) atomicAdd(p.exact_count, 1u);
                     }
                     // a vector that has seen no row keeps z = -inf
                     const float ref = mn == -INFINITY ? 0.0f : mn;
