@@ -57,10 +57,10 @@
 //
 // What bounds it.  KV8, many rows a tile: the softmax warps, 3,350 cycles a step (scores
 // 1,350, vote 290, exponentials 600, weights 450, the rest hand-overs) for 2,200 of
-// products: 512 tokens on 32,768 rows x 128 heads 3.2 ms, 1,470 TFLOP/s; 32 sequences of
-// 1,024 to 131,072 rows 361 us.  TQ4: the decode warps' integer work, 5,500 a step (256
-// tokens on 16,384 rows 1.6 ms, 735 TFLOP/s).  Short tiles: rotation of queries and
-// outputs (TQ4, 777 tokens without rows before 269 us), and the start (6k cycles), the
+// products: 512 tokens on 32,768 rows x 128 heads 3.1 ms, 1,500 TFLOP/s; 32 sequences of
+// 1,024 to 131,072 rows 356 us.  TQ4: the decode warps' integer work, 5,500 a step (256
+// tokens on 16,384 rows 1.6 ms, 740 TFLOP/s).  Short tiles: rotation of queries and
+// outputs (TQ4, 777 tokens without rows before 272 us), and the start (6k cycles), the
 // queries (8k) and the partial results (6k) of a decode step (8 x 4096 rows 27 us).
 #include "tc_common.cuh"
 #include "paged_common.cuh"
