@@ -624,6 +624,29 @@ def test_attn_paged_shared_prefix(kvq, oracle, path, bf16):
     p.check(q, p.run(q, path), tolerance(1, path, bf16))
 
 
+def test_attn_paged_counts_rescales_and_time(kvq, oracle):
+    """The diagnostics of the other attention calls: steps on the exact path, launch times."""
+    T = 1500
+    x = synth.mla_rows(5, T)
+    # 30 tiles of 12 steps: a walker has several steps of a tile
+    flat = Paged(kvq, oracle, 1, [T - 30], [30], 32, seed=5, x=x)
+    climb = Paged(kvq, oracle, 1, [T - 30], [30], 32, seed=5, x=x * np.exp2(np.linspace(-12.0, 3.0, T)).astype(np.float32)[:, None])
+    counts = []
+    kvq.timing_enable(4)
+    try:
+        for p in (flat, climb):
+            q = query(30, 128, 6, True, scale=0.1 if p is flat else 3.0)
+            ws = torch.zeros(kvq.kv_attn_paged_workspace_size(1, 1, 128, 30, p.layout), dtype=torch.uint8, device="cuda")
+            out = torch.empty(30, 128, 512, dtype=torch.bfloat16, device="cuda")
+            kvq.kv_attn_paged(1, q, to_dev(p.cu), p.codes, p.scales, to_dev(p.table), to_dev(p.lens), 32, out, ws, SM, p.layout)
+            counts.append(kvq.read_exact_rescales(ws))
+        partial, merge, calls = kvq.timing_read()
+    finally:
+        kvq.timing_enable(0)
+    assert calls == 2 and partial > 0 and merge > 0
+    assert counts[0] == 0 and counts[1] > 0
+
+
 @pytest.mark.parametrize("path,bf16", PATHS)
 @pytest.mark.parametrize("fmt", [1, 2])
 def test_attn_paged_offsets_past_32_bits(kvq, oracle, fmt, path, bf16):
