@@ -49,10 +49,11 @@
 // row sum in f32, and the context takes the f16 weight w = p s_L E,
 // E = 2^(m - R - 3) with R the largest z + log2 s_L of the steps that set the
 // references, so that weights are relative to the largest p s_L and rows of
-// small latent scale keep f16 precision where they matter.  A score that passes
-// m by more than 2^14, or a latent scale past 3.5 / E, sends the step down the
-// exact path: row maxima, new m, R and E, O rescaled in tensor memory.  Both
-// limits keep w under the f16 maximum.  Rows that a vector does not see get
+// small latent scale keep f16 precision where they matter.  A step in which w might
+// pass 2^15.75, by its largest z - m and its largest s_L, goes down the exact path: row
+// maxima, new m, R and E, O rescaled in tensor memory.  (A bound of its own for each,
+// 2^14 and 3.5, sent more steps there: mixed batch of 24 sequences 212 us, 206 with the
+// one for both; 235 with 2^10.)  Rows that a vector does not see get
 // z = -inf; a vector that has seen no row has m = -inf and E = 0.
 //
 // What bounds it.  KV8, many rows a tile: the softmax warps, 3,350 cycles a step (scores
@@ -61,7 +62,7 @@
 // 1,024 to 131,072 rows 356 us.  TQ4: the decode warps' integer work, 5,500 a step (256
 // tokens on 16,384 rows 1.6 ms, 740 TFLOP/s).  Short tiles: rotation of queries and
 // outputs (TQ4, 777 tokens without rows before 272 us), and the start (6k cycles), the
-// queries (8k) and the partial results (6k) of a decode step (8 x 4096 rows 27 us).
+// queries (8k) and the partial results (6k) of a decode step (8 x 4096 rows 26.7 us).
 #include "tc_common.cuh"
 #include "paged_common.cuh"
 
@@ -112,7 +113,7 @@ constexpr uint32_t kOffScale = kOffP + 2 * kChunkBytes;     // s_L, then s_R, of
 constexpr uint32_t kScaleBytes = kRows * 8;
 constexpr uint32_t kOffCz = kOffScale + 2 * kScaleBytes;    // score scale of a vector, two segments
 constexpr uint32_t kOffBar = kOffCz + 2 * kHalf * 4;
-constexpr uint32_t kOffMax = kOffBar + 26 * 8;              // largest s_L of two steps
+constexpr uint32_t kOffMax = kOffBar + 26 * 8;              // log2 of the largest s_L of two steps
 constexpr uint32_t kOffLevels = kOffMax + 16;
 constexpr uint32_t kOffMisc = kOffLevels + 16;              // abort flag, TMEM base
 constexpr uint32_t kOffWork = kOffMisc + 16;                // two segments, announced one ahead
@@ -142,7 +143,7 @@ enum {
 // Scores, announcements, queries and scales have two barriers each, used in turn:
 // their next but one event waits for whoever waits for this one, the next does not.
 
-constexpr float kLagLog2 = 14.0f, kScaleLim = 3.5f, kHeadroom = 3.0f, kLogEmax = 120.0f;
+constexpr float kLogWmax = 15.75f, kHeadroom = 3.0f, kLogEmax = 120.0f, kLogMax = 100.0f;
 // levels times this round to f16 within 9.3e-5 (unscaled: 3.2e-4); divided out in f32
 constexpr float kGamma = 1.3338516f;
 constexpr uint32_t kIdescScore = idesc_f16(kVecs, kRows, false, false);   // e4m3 x e4m3 has the same bits
@@ -607,8 +608,7 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8], bool 
 
 // A query vector's softmax state.
 struct RowState {
-    float m, R, E, logE, l;
-    bool none;   // rows seen, but none with a latent scale yet
+    float m, R, E, logE, l;   // logE = inf: rows seen, but none with a latent scale yet
 };
 
 // The walk's current segment as a record; false at its end.
@@ -914,7 +914,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     float4* dst = reinterpret_cast<float4*>(sm + kOffScale + (it & 1u) * kScaleBytes) + lane;
                     dst[0] = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
                     dst[kRows / 4] = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
-                    if (lane == 0) reinterpret_cast<float*>(sm + kOffMax)[it & 1u] = top;
+                    if (lane == 0) reinterpret_cast<float*>(sm + kOffMax)[it & 1u] = top > 0.0f ? __log2f(top) : -INFINITY;
                     warp_arrive(&bars[kBarScore0 + (it & 1u)], lane);
                 }
             }
@@ -1071,7 +1071,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // vectors past the tile's last repeat its limit: they score 0 and are dropped
             const int vec = kHalf * rank + r;
             const int32_t lim = (int32_t)max((int64_t)0, w.base + 1 + over_heads(p, w.tok0 + min(vec, w.rows - 1)));
-            RowState st{-INFINITY, -INFINITY, 0.0f, 0.0f, 0.0f, false};
+            RowState st{-INFINITY, -INFINITY, 0.0f, 0.0f, 0.0f};
             if (!warp_wait(&bars[kBarQ0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl)) aborted = true;
             const float cz = reinterpret_cast<const float*>(sm + kOffCz)[(n & 1) * kHalf + r];
 
@@ -1081,7 +1081,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const float* s_l = reinterpret_cast<const float*>(sm + kOffScale + (it & 1u) * kScaleBytes) + kHalf * half +
                                    kCols * sub;
                 const int seen_abort = *sAbort;   // read ahead of its use
-                const float smax = reinterpret_cast<const float*>(sm + kOffMax)[it & 1u];
+                const float log_s = reinterpret_cast<const float*>(sm + kOffMax)[it & 1u];   // of the step's largest s_L
                 const uint32_t ts = tmem + lane_base + kColS + 128 * (it & 1u) + kCols * sub;
                 const int32_t t0 = first + t * kRows + kHalf * half + kCols * sub;
                 const bool masked = first + (t + 1) * kRows > seen0;
@@ -1132,8 +1132,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 4; j < kCols; ++j) top[j & 3] = fmaxf(top[j & 3], z[j]);
                         const float dmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                        const bool flag = aborted | (seen_abort != 0) | (smax * (st.none ? INFINITY : st.E) > kScaleLim) |
-                                          (dmax > kLagLog2);
+                        const float log_se = log_s + st.logE;
+                        const bool flag = aborted | (seen_abort != 0) | (dmax + log_se > kLogWmax) | (dmax > kLogMax) |
+                                          (log_se > kLogMax);
                         if (!group_any(group, flag)) break;
                         exact = true;
                         continue;
@@ -1167,18 +1168,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     group_sync(group);   // read before any thread's weights go there
                     const float mn = fmaxf(st.m, zt), rn = fmaxf(st.R, yt);
                     const bool inert = rn == -INFINITY;
-                    const float le = fminf(mn - rn - kHeadroom, kLogEmax);
+                    float le = fminf(mn - rn - kHeadroom, fminf(kLogEmax, kLogMax - log_s));   // s_L E stays finite
                     const float al = st.m == -INFINITY ? 0.0f : ex2(st.m - mn);
                     // O holds sum p s_L E c: rescaled by (E_new / E_old) 2^(m_old - m_new)
                     const float ao = st.R == -INFINITY ? 0.0f : ex2(le - st.logE + (st.m - mn));
                     st.l *= al;
                     st.m = mn;
                     st.R = rn;
-                    st.logE = le;
-                    st.E = inert ? 0.0f : ex2(le);
                     // rows seen without a latent scale: the next one comes here again;
                     // no row seen: the first score does, by m = -inf
-                    st.none = inert && mn > -INFINITY;
+                    st.logE = inert && mn > -INFINITY ? INFINITY : le;
+                    st.E = inert ? 0.0f : ex2(le);
                     if (t > 0) {
 #pragma unroll 1
                         for (int c = 8 * sub; c < 8 * sub + 8; ++c) {   // 128 of the columns a thread
