@@ -59,8 +59,8 @@
 // What bounds it.  KV8, many rows a tile: the softmax warps, 3,350 cycles a step (scores
 // 1,350, vote 290, exponentials 600, weights 450, the rest hand-overs) for 2,200 of
 // products: 512 tokens on 32,768 rows x 128 heads 3.1 ms, 1,500 TFLOP/s; 32 sequences of
-// 1,024 to 131,072 rows 356 us.  TQ4: the decode warps' integer work, 5,500 a step (256
-// tokens on 16,384 rows 1.6 ms, 740 TFLOP/s).  Short tiles: rotation of queries and
+// 1,024 to 131,072 rows 356 us.  TQ4: the decode warps' integer work, 5,300 a step (256
+// tokens on 16,384 rows 1.5 ms, 780 TFLOP/s).  Short tiles: rotation of queries and
 // outputs (TQ4, 777 tokens without rows before 272 us), and the start (6k cycles), the
 // queries (8k) and the partial results (6k) of a decode step (8 x 4096 rows 26.7 us).
 #include "tc_common.cuh"
@@ -329,7 +329,9 @@ __device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint32_t neg = ~in[i] & 0x88888888u, even = neg << 4;   // signs in bit 7 of a byte: odd codes, even codes
-        const uint32_t sel = (in[i] & 0x77777777u) ^ (neg - (neg >> 3));
+        // 7/8 of it, 7 in each code below 8, by a high product: the integer pipe is the
+        // busy one (256 tokens on 16,384 rows 1.51 ms, 1.57 with a shift and a difference)
+        const uint32_t sel = (in[i] & 0x77777777u) ^ __umulhi(neg, 0xe0000000u);
         uint32_t w[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
