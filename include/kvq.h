@@ -496,9 +496,7 @@ size_t kv_attn_paged_workspace_size(kvq_format fmt, const kvq_mla_layout* layout
  * bf16 queries only, f32 accumulation, within 2e-3 of exact before the rounding to
  * bf16, but for what the query's own rounding adds.  KV8: query elements keep their 8
  * bits down to 2^-9 of the vector's largest; smaller ones are off by at most 2^-17 of
- * it.  TQ4: the rotated query is rounded to f16 once, which moves a score by about
- * 2^-12 sm_scale |q'| |x'| / 24 (4e-4 of the outputs in the 2-norm on channel-outlier
- * rows; the rounding to bf16 is 1.7e-3).
+ * it.  TQ4: the rotated query is held in two f16 values, to 2^-22 of each element.
  * A row with a NaN code, or a scale that is no finite number, makes NaN the tokens
  * that see it and leaves the others as they are.  Invalid lengths or offsets and
  * pages outside [0, n_pages) set KVQ_ERR_ARG in the workspace's device word; nothing

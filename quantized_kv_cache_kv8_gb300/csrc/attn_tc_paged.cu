@@ -14,9 +14,9 @@
 // That decides the layout.  One CTA alone, with rows on M and 64 vectors on N,
 // reads 6 KB of operands for each 32 cycles of products, where shared memory
 // delivers 128 B a cycle (48 cycles; 575 KB a step with the decoded stores, 4.5k
-// cycles); here the scores read 4 KB in 32 cycles and the context 6 KB in 64
-// (400 KB, 3.1k; 243 KB and 1.9k with KV8's scores in fp8).  More vectors a CTA do not fit: 64 x 512 f32 of context are
-// half of a CTA's tensor memory.
+// cycles); here the scores read 4 KB in 32 cycles and the context 6 KB in 64 (243 KB
+// and 1.9k with KV8's scores in fp8, 540 KB and 4.2k with TQ4's in two halves of f16).  More
+// vectors a CTA do not fit: 64 x 512 f32 of context are half of a CTA's tensor memory.
 //
 // Operands.  KV8: the scores run as fp8 MMAs on the codes themselves: TMA puts
 // them into swizzled shared memory page by page, no warp touches them, and they
@@ -28,15 +28,20 @@
 // context needs weights with more range than fp8 has: its rows are decoded to f16
 // (e4m3 codes exactly).
 // TQ4: levels are no fp8 values; both operands are decoded to f16 (the 16 levels
-// times kGamma within 9.3e-5), and the rotated query is rounded to f16 once, 2^-12
-// relative.
+// times kGamma within 9.3e-5), and the rotated query is q1 + q2 in f16, value and
+// residual, 22 bits (one f16 alone moves outputs by up to 3e-3 of the largest).  The
+// second half takes the space of the score rows, so score and context rows of a step go
+// through two slots of 32 KB in five fills: three times three chunks of the score rows, then
+// context rows 0-63 and 64-127.  (With the rope dims in a fill of their own, the next fill
+// waits for the products of the one before it: 256 tokens on 16,384 rows 2.01 ms.  Four
+// warps for the scores and four for the context, slots of 16 KB each: 1.99.)
 //
 // Roles (a CTA): 8 softmax warps, 8 decode warps, one issuing warp (in the first
 // CTA; the second's passes on that its codes have arrived), one that announces
 // segments, one that fetches row scales, one that loads codes by TMA; registers
-// move to the warps that need them (Regs).  The decode warps store the score rows of
-// step t+1 (TQ4) once the scores of step t are complete and the context rows of step t
-// once the context of step t-1 is; the scores of t+1 are issued before the
+// move to the warps that need them (Regs).  The decode warps store the context rows of
+// step t once the context of step t-1 is complete (KV8), or each fill once the products of
+// the fill before the last are (TQ4); the scores of t+1 are issued before the
 // context of t.  So the tensor pipe alternates between the two while the other
 // operand is being stored and while the softmax of the step runs:
 //   tensor   S(t)   O(t-1)    S(t+1)    O(t)
@@ -59,9 +64,10 @@
 // What bounds it.  KV8, many rows a tile: the softmax warps, 3,350 cycles a step (scores
 // 1,350, vote 290, exponentials 600, weights 450, the rest hand-overs) for 2,200 of
 // products: 512 tokens on 32,768 rows x 128 heads 3.1 ms, 1,500 TFLOP/s; 32 sequences of
-// 1,024 to 131,072 rows 356 us.  TQ4: the decode warps' integer work, 5,300 a step (256
-// tokens on 16,384 rows 1.5 ms, 780 TFLOP/s).  Short tiles: rotation of queries and
-// outputs (TQ4, 777 tokens without rows before 272 us), and the start (6k cycles), the
+// 1,024 to 131,072 rows 356 us.  TQ4: the decode warps' integer work and shared
+// memory, which the products of two query halves keep busy, 7,500 a step (256 tokens on
+// 16,384 rows 1.70 ms, 690 TFLOP/s).  Short tiles: rotation of queries and
+// outputs (TQ4, 777 tokens without rows before 314 us), and the start (6k cycles), the
 // queries (8k) and the partial results (6k) of a decode step (8 x 4096 rows 26.7 us).
 #include "tc_common.cuh"
 #include "paged_common.cuh"
@@ -105,9 +111,12 @@ constexpr uint32_t kVChunkBytes = kRows * 128;  // 128 rows x 64 f16
 // KV8, the same nine places of 8 KB: queries q1 of 4 x 128 dims, q2 likewise, rope
 // (q1 in the lower 64 bytes of a row, q2 in the upper); codes of 4 x 128 dims of two
 // steps, and the row's last 128 bytes (the rope dims are the upper 64).
+// TQ4: q1, then q2 in the nine places after it; the slots where KV8 has its context rows.
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kOffQ + kChunks * kChunkBytes;
 constexpr uint32_t kOffV = kOffK + kChunks * kChunkBytes;   // 4 chunks: dims 256 j + 128 rank + 64 i
+constexpr uint32_t kOffSlot = kOffV, kSlotBytes = 4 * kChunkBytes;   // TQ4
+static_assert(2 * kSlotBytes <= 4 * kVChunkBytes, "slots");
 constexpr uint32_t kOffP = kOffV + 4 * kVChunkBytes;        // weights: 2 chunks of 64 rows
 constexpr uint32_t kOffScale = kOffP + 2 * kChunkBytes;     // s_L, then s_R, of two steps' rows
 constexpr uint32_t kScaleBytes = kRows * 8;
@@ -126,8 +135,8 @@ static_assert(32 * kMlaDV * 4 <= 4 * kVChunkBytes, "output stage");
 
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 
-// mbarriers.  In the first CTA, arrivals from both: score rows stored (dims 0-255,
-// the rest), context rows stored (rows 0-63, 64-127), weights written.  In
+// mbarriers.  In the first CTA, arrivals from both: slots stored (TQ4), context rows
+// stored (KV8: rows 0-63, 64-127), weights written.  In
 // each CTA: scores complete and their row scales stored (by buffer; commits reach
 // both CTAs), context complete (by row half), segment announced, segment done
 // with, queries stored, output written, row scales read,
@@ -138,7 +147,9 @@ enum {
     // KV8: latent codes of a step (two buffers) and its rope codes have arrived
     // here; in the first CTA, that they have arrived in the second
     kBarLat0 = 20, kBarRope = 22, kBarPeerLat0 = 23, kBarPeerRope = 25, kNumBars = 26,
-    kBarQFirst = kBarK0   // KV8, in the first CTA: queries stored in both
+    kBarQFirst = kBarK0,  // KV8, in the first CTA: queries stored in both
+    // TQ4, by slot: stored in both CTAs (in the first), its products complete (in each)
+    kBarFull0 = kBarK0, kBarFree0 = kBarLat0
 };
 // Scores, announcements, queries and scales have two barriers each, used in turn:
 // their next but one event waits for whoever waits for this one, the next does not.
@@ -283,20 +294,10 @@ __device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int3
 }
 
 // ---- decode -------------------------------------------------------------------
-// 16 codes: a quarter of a row's 64-dim chunk, 32 bytes of f16 in two 16-byte
-// stores.  A warp reads 256 dims of two rows; the 8 lanes that a store serves at
-// a time have one chunk of both rows, whose swizzle phases differ in the low bit:
-// 8 different 16-byte units.
-template <bool TQ4>
-struct PieceOf {
-    using type = uint4;
-};
-template <>
-struct PieceOf<true> {
-    using type = uint2;
-};
-template <bool TQ4>
-using Piece = typename PieceOf<TQ4>::type;
+// KV8: 16 codes, a quarter of a row's 64-dim chunk, 32 bytes of f16 in two 16-byte
+// stores.  A warp reads 256 dims of two rows; the 8 lanes that a store serves at a time
+// have one chunk of both rows, whose swizzle phases differ in the low bit: 8 different
+// 16-byte units.
 
 // The f16 levels of codes 8-15 as byte planes, four levels a word; those of codes
 // 7-0 are their negatives.
@@ -312,7 +313,7 @@ static_assert(levels_mirror(), "decode takes the lower levels from the upper one
 // e4m3: a NaN code becomes the lowest value, for a row counts, weight 0, in the
 // context of the vectors that do not see it too; those that do get their NaN from
 // its score.
-__device__ __forceinline__ void store_piece(unsigned char* chunk, const uint4& c, int row, int q, const Planes&) {
+__device__ __forceinline__ void store_codes(unsigned char* chunk, const uint4& c, int row, int q) {
     const uint32_t in[4] = {c.x, c.y, c.z, c.w};
     uint32_t w[8];
 #pragma unroll
@@ -324,25 +325,23 @@ __device__ __forceinline__ void store_piece(unsigned char* chunk, const uint4& c
 }
 // Nibble codes by byte permutes over the low and the high bytes of the levels: the
 // low 3 bits of a code (their complement below 8) pick the level, bit 3 its sign.
-__device__ __forceinline__ void store_piece(unsigned char* chunk, const uint2& c, int row, int q, const Planes& t) {
-    const uint32_t in[2] = {c.x, c.y};
+// Eight of them, one word, fill a 16-byte unit.
+__device__ __forceinline__ void store_levels(unsigned char* chunk, uint32_t codes, int row, int unit, const Planes& t) {
+    const uint32_t neg = ~codes & 0x88888888u, even = neg << 4;   // signs in bit 7 of a byte: odd codes, even codes
+    // 7/8 of it, 7 in each code below 8, by a high product: the integer pipe is the
+    // busy one (with one query half: 256 tokens on 16,384 rows 1.51 ms, 1.57 with a
+    // shift and a difference)
+    const uint32_t sel = (codes & 0x77777777u) ^ __umulhi(neg, 0xe0000000u);
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t neg = ~in[i] & 0x88888888u, even = neg << 4;   // signs in bit 7 of a byte: odd codes, even codes
-        // 7/8 of it, 7 in each code below 8, by a high product: the integer pipe is the
-        // busy one (256 tokens on 16,384 rows 1.51 ms, 1.57 with a shift and a difference)
-        const uint32_t sel = (in[i] & 0x77777777u) ^ __umulhi(neg, 0xe0000000u);
-        uint32_t w[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t s = h ? sel >> 16 : sel;
-            const uint32_t lo = __byte_perm(t.lo[0], t.lo[1], s);
-            const uint32_t hi = __byte_perm(t.hi[0], t.hi[1], s) | (__byte_perm(even, neg, h ? 0x7362u : 0x5140u) & 0x80808080u);
-            w[2 * h] = __byte_perm(lo, hi, 0x5140u);
-            w[2 * h + 1] = __byte_perm(lo, hi, 0x7362u);
-        }
-        *reinterpret_cast<uint4*>(chunk + sw128(row, 32 * q + 16 * i)) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t s = h ? sel >> 16 : sel;
+        const uint32_t lo = __byte_perm(t.lo[0], t.lo[1], s);
+        const uint32_t hi = __byte_perm(t.hi[0], t.hi[1], s) | (__byte_perm(even, neg, h ? 0x7362u : 0x5140u) & 0x80808080u);
+        w[2 * h] = __byte_perm(lo, hi, 0x5140u);
+        w[2 * h + 1] = __byte_perm(lo, hi, 0x7362u);
     }
+    *reinterpret_cast<uint4*>(chunk + sw128(row, 16 * unit)) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Two f32 operations in one instruction.
@@ -503,23 +502,30 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0,
     }
 }
 
-// TQ4: rotated, to f16.  A lane begins with dims 8 (l + 8 j) .. + 7 of its vector, six
-// of the nine stages in its registers; the warp's 8 KB of stage turn that into the 64
-// dims of chunk l for the other three (shuffles for them take longer than the rest of
-// the transform).
+// TQ4: rotated, to q1 + q2 in f16.  A lane begins with dims 8 (l + 8 j) .. + 7 of its
+// vector, six of the nine stages in its registers; 8 KB of shared memory turn that into
+// the 64 dims of chunk l for the other three (shuffles for them take longer than the rest
+// of the transform).  The warp's eight vectors are one 1 KB atom of each chunk, its own: the
+// first four are turned, and written, while the last four rows of 16 atoms hold the turn,
+// the last four come to lie where they were turned.
 __device__ __forceinline__ uint32_t to_half2(F2 x) {
     const float2 e = unpack(x);
     const __half2 h = __floats2half2_rn(e.x, e.y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ void rotate_queries(const PagedParams& p, int64_t row0, int rows, unsigned char* sQ,
-                                               unsigned char* stage, float* sCz, int warp, int lane) {
-    const int l = lane & 7;
-    const int r0 = (kHalf / kDecWarps) * warp + (lane >> 3);
+                                               float* sCz, int warp, int lane) {
+    const int l = lane & 7, v4 = lane >> 3;
+    const int r0 = (kHalf / kDecWarps) * warp + v4;
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (row0 + r0) * kMlaD) + l;
-    float4* own = reinterpret_cast<float4*>(stage) + 128 * (lane >> 3);
+    static_assert(kHalf / kDecWarps == 8, "a warp has an atom of each chunk");
+    // a vector's 2 KB: the half atoms of four latent chunks (of q1: vectors 0, 1; of q2: 2, 3)
+    unsigned char* own = sQ + (v4 < 2 ? 4 * v4 : 4 * v4 + kChunks - 8) * kChunkBytes + 1024 * warp + 512;
     // place of unit u (four dims): 8 lanes, 2 or 16 units apart, on different banks
-    auto at = [](int u) { return u ^ ((u >> 3) & 7) ^ ((u >> 6) & 1); };
+    auto at = [own](int u) {
+        const int x = u ^ ((u >> 3) & 7) ^ ((u >> 6) & 1);
+        return reinterpret_cast<float4*>(own + (x >> 5) * kChunkBytes + 16 * (x & 31));
+    };
     uint4 raw[9];
     auto fetch = [&](int g) {
         const bool ok = r0 + 4 * g < rows;
@@ -555,7 +561,7 @@ __device__ __forceinline__ void rotate_queries(const PagedParams& p, int64_t row
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float2 a = unpack(x[i][0]), b = unpack(x[i][1]);
-            own[at(2 * (l + 8 * (i >> 1)) + (i & 1))] = make_float4(a.x, a.y, b.x, b.y);
+            *at(2 * (l + 8 * (i >> 1)) + (i & 1)) = make_float4(a.x, a.y, b.x, b.y);
         }
         __syncwarp();
         F2 y[8][4];   // dims 64 l + 8 m + 2 k, + 1
@@ -563,7 +569,7 @@ __device__ __forceinline__ void rotate_queries(const PagedParams& p, int64_t row
         for (int m = 0; m < 8; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float4 v = own[at(2 * (m + 8 * l) + h)];
+                const float4 v = *at(2 * (m + 8 * l) + h);
                 y[m][2 * h] = f2(v.x, v.y);
                 y[m][2 * h + 1] = f2(v.z, v.w);
             }
@@ -585,9 +591,21 @@ __device__ __forceinline__ void rotate_queries(const PagedParams& p, int64_t row
         const float scale = vector_scale<14>(top, &undo);
         if (l == 0) sCz[r] = p.sm_scale * kLog2e * undo * (1.0f / kGamma);
         const F2 s2 = f2(scale, scale);
+        __syncwarp();   // the turn has been read: the last four rows' places too
         auto store = [&](int chunk, int byte, F2 a, F2 b, F2 c, F2 d) {
-            *reinterpret_cast<uint4*>(sQ + chunk * kChunkBytes + sw128(r, byte)) =
-                make_uint4(to_half2(mul2(a, s2)), to_half2(mul2(b, s2)), to_half2(mul2(c, s2)), to_half2(mul2(d, s2)));
+            const F2 x[4] = {mul2(a, s2), mul2(b, s2), mul2(c, s2), mul2(d, s2)};
+            uint32_t q1[4], q2[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 e = unpack(x[i]);
+                const __half2 h = __floats2half2_rn(e.x, e.y);
+                const float2 back = __half22float2(h);
+                q1[i] = *reinterpret_cast<const uint32_t*>(&h);
+                q2[i] = to_half2(f2(e.x - back.x, e.y - back.y));   // the difference is exact
+            }
+            unsigned char* to = sQ + chunk * kChunkBytes + sw128(r, byte);
+            *reinterpret_cast<uint4*>(to) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
+            *reinterpret_cast<uint4*>(to + kChunks * kChunkBytes) = make_uint4(q2[0], q2[1], q2[2], q2[3]);
         };
 #pragma unroll
         for (int m = 0; m < 8; ++m) store(l, 16 * m, y[m][0], y[m][1], y[m][2], y[m][3]);
@@ -728,22 +746,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint64_t dk = umma_desc(smem_u32(sm + kOffK), 16, 1024);
                 const uint64_t dv = umma_desc(smem_u32(sm + kOffV), kVChunkBytes, 1024);
                 const uint64_t dp = umma_desc(smem_u32(sm + kOffP), 16, 1024);
-                constexpr uint64_t kStep = kChunkBytes >> 4, kVStep = kVChunkBytes >> 4;
+                constexpr uint64_t kStep = kChunkBytes >> 4, kVStep = kVChunkBytes >> 4, kSlotStep = kSlotBytes >> 4;
+                const uint64_t dsk = umma_desc(smem_u32(sm + kOffSlot), 16, 1024);            // score rows
+                const uint64_t dsv = umma_desc(smem_u32(sm + kOffSlot), kChunkBytes, 1024);   // context rows
+                uint32_t fill = 0;   // TQ4: fills used so far
                 bool ok = true;
                 if (p.stall_polls > 0) ok = warp_wait(&bars[kBarNever], 0u, sAbort, p.stall_polls);
                 auto scores = [&](uint32_t it) {
                     const uint32_t d = tmem + kColS + 128 * (it & 1u);
                     if (TQ4) {
 #pragma unroll
-                        for (int gr = 0; gr < 2; ++gr) {
-                            if (!warp_wait(&bars[kBarK0 + gr], it & 1u, sAbort, wl)) return false;
-                            tc_after();
+                        for (int c = 0; c < kChunks; ++c) {
+                            if (c % 3 == 0) {
+                                if (!warp_wait(&bars[kBarFull0 + (fill & 1u)], (fill >> 1) & 1u, sAbort, wl)) return false;
+                                tc_after();
+                            }
+                            const uint64_t ds = dsk + (fill & 1u) * kSlotStep + c % 3 * kStep;
 #pragma unroll
-                            for (int kc = 4 * gr; kc < (gr ? kChunks : 4); ++kc)
+                            for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-                                for (int ks = 0; ks < 4; ++ks)
-                                    pair_mma(d + (kc < kRope ? 0 : 64), dq + kc * kStep + 2 * ks, dk + kc * kStep + 2 * ks,
-                                             kIdescScore, ((kc == 0 || kc == kRope) && ks == 0) ? 0u : 1u);
+                                for (int part = 0; part < 2; ++part)
+                                    pair_mma(d + (c < kRope ? 0 : 64), dq + (kChunks * part + c) * kStep + 2 * ks, ds + 2 * ks,
+                                             kIdescScore, ((c > 0 && c < kRope) || ks > 0 || part > 0) ? 1u : 0u);
+                            if (c % 3 == 2) pair_commit(&bars[kBarFree0 + (fill++ & 1u)]);
                         }
                     } else {
                         if (!warp_wait(&bars[kBarLat0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl)) return false;
@@ -792,17 +817,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (!ok) break;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            ok = ok && warp_wait(&bars[kBarV0 + h], s & 1u, sAbort, wl);
+                            ok = ok && (TQ4 ? warp_wait(&bars[kBarFull0 + (fill & 1u)], (fill >> 1) & 1u, sAbort, wl)
+                                            : warp_wait(&bars[kBarV0 + h], s & 1u, sAbort, wl));
                             if (!ok) break;
                             tc_after();
+                            const uint64_t dh = TQ4 ? dsv + (fill & 1u) * kSlotStep : dv + 4 * h * 128;
 #pragma unroll
                             for (int j = 0; j < 2; ++j)
 #pragma unroll
                                 for (int ks = 0; ks < 4; ++ks)
                                     pair_mma(tmem + kColO + 128 * j, dp + h * kStep + 2 * ks,
-                                             dv + 2 * j * kVStep + (4 * h + ks) * 128, kIdescCtx,
+                                             dh + 2 * j * (TQ4 ? kStep : kVStep) + ks * 128, kIdescCtx,
                                              (t > 1 || h > 0 || ks > 0) ? 1u : 0u);
-                            pair_commit(&bars[kBarCtx0 + h]);
+                            if (TQ4) pair_commit(&bars[kBarFree0 + (fill++ & 1u)]);
+                            if (!TQ4 || h == 1) pair_commit(&bars[kBarCtx0 + h]);
                         }
                     }
                     it += steps;
@@ -924,127 +952,173 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp >= kSoftWarps) {
         // ================= decode warps =================
         set_registers<R::kDecode, R::kLaunch>();
-        using P = Piece<TQ4>;
-        constexpr int kRowBytes = TQ4 ? kMlaD / 2 : kMlaD, kQ = sizeof(P);
         const int dw = warp - kSoftWarps;
-        Planes pl{};
-        if (TQ4) {
-            const uint4 a = *reinterpret_cast<const uint4*>(sm + kOffLevels);
-            pl = Planes{{a.x, a.y}, {a.z, a.w}};
-        }
-        // A warp has 8 consecutive rows of each half of a step (8 rows lie in one
-        // page): of the CTA's own half for the scores, of both for the context.
-        //   rows 2 i, 2 i + 1: bit 2 of the lane picks the row, c = lane / 8 the chunk
-        //     (score chunk 4 g + c, g = 0, 1; context chunk c), lane % 4 the quarter
-        //   rope: row lane / 4, quarter lane % 4
-        // The two are loaded apart, each straight into the registers it is stored
-        // from once the load of the step before has left them: codes of the own
-        // half come twice (L2 has room, 10% busy), but no loaded register is
-        // moved, and so waited for, before its step.
-        const int q4 = lane & 3, up = (lane >> 2) & 1, c4 = lane >> 3;
-        unsigned char* k_chunk = sm + kOffK + c4 * kChunkBytes;
-        unsigned char* v_chunk = sm + kOffV + c4 * kVChunkBytes;
-        const int k_piece = 4 * c4 + q4;                                            // 16-code piece of the row's 36
-        const int v_piece = 16 * (c4 >> 1) + 8 * rank + 4 * (c4 & 1) + q4;
         uint32_t it = 0;
         bool ok = true;
-        auto score_done = [&](uint32_t s) { return warp_wait(&bars[kBarScore0 + (s & 1u)], (s >> 1) & 1u, sAbort, wl); };
         for (int n = 0; ok; ++n) {
             if (!(ok = warp_wait(&bars[kBarWork0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl))) break;
-            const Work w = sWork[n & 1];
+            const Work& work = sWork[n & 1];
+            const int32_t steps = work.steps, first = work.first, end = work.end, rows = work.rows;
+            const int64_t row0 = work.row0;
+            const int32_t* table = p.table + (int64_t)work.b * p.table_stride;
             warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
-            if (w.steps == 0) break;
-            const int32_t* table = p.table + (int64_t)w.b * p.table_stride;
-            const int32_t row_k = w.first + kHalf * rank + 8 * dw, row_v = w.first + 8 * dw;
+            if (steps == 0) break;
             // pages are asked for a step before the codes, the codes a step before their use
-            auto page = [&](int32_t r) { return r < w.end ? __ldg(table + (r >> p.shift)) : 0; };
+            auto page = [&](int32_t r) { return r < end ? __ldg(table + (r >> p.shift)) : 0; };
             auto code_rows = [&](int32_t r, int32_t id) {
                 if (id < 0 || id >= p.n_pages) {
-                    if (lane == 0 && r < w.end) set_err(p.err, KVQ_ERR_ARG);
+                    if (lane == 0 && r < end) set_err(p.err, KVQ_ERR_ARG);
                     id = 0;
                 }
-                return p.codes + (((int64_t)id << p.shift) + (r & ((1 << p.shift) - 1))) * kRowBytes;
+                return p.codes + (((int64_t)id << p.shift) + (r & ((1 << p.shift) - 1))) * (TQ4 ? kMlaD / 2 : kMlaD);
             };
-            int32_t id_k = page(row_k), id_v[2] = {page(row_v), page(row_v + kHalf)};
-            P raw[2][4], rope, ctx[2][4];
-            auto request_k = [&](int t) {
-                const int32_t r0 = row_k + t * kRows;
-                const uint8_t* a = code_rows(r0, id_k);
-                const uint8_t* b = a + up * kRowBytes + kQ * k_piece;
-                const int last = w.end - r0 - up;   // rows 2 i up to here exist
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        raw[g][i] = 2 * i < last ? __ldg(reinterpret_cast<const P*>(b + 2 * i * kRowBytes + 16 * kQ * g)) : P{};
-                rope = r0 + (lane >> 2) < w.end
-                           ? __ldg(reinterpret_cast<const P*>(a + (lane >> 2) * kRowBytes + kQ * (32 + q4)))
-                           : P{};
-                if (t + 1 < w.steps) id_k = page(r0 + kRows);
-            };
-            auto request_v = [&](int t) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int32_t r0 = row_v + t * kRows + kHalf * h;
-                    const uint8_t* a = code_rows(r0, id_v[h]) + up * kRowBytes + kQ * v_piece;
-                    const int last = w.end - r0 - up;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        ctx[h][i] = 2 * i < last ? __ldg(reinterpret_cast<const P*>(a + 2 * i * kRowBytes)) : P{};
-                    if (t + 1 < w.steps) id_v[h] = page(r0 + kRows);
-                }
-            };
-            auto store_v = [&](uint32_t s) {   // the context rows of step s (of the whole walk)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (s > 0 && !warp_wait(&bars[kBarCtx0 + h], (s - 1) & 1u, sAbort, wl)) return false;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        store_piece(v_chunk, ctx[h][i], kHalf * h + 8 * dw + 2 * i + up, q4, pl);
-                    fence_async_smem();
-                    warp_arrive_first(&bars[kBarV0 + h], lane);
-                }
-                return true;
-            };
-            if (it > 0 && !(ok = score_done(it - 1))) break;
+            // the scores of the last segment have read its queries
+            if (it > 0 && !(ok = warp_wait(&bars[kBarScore0 + ((it - 1) & 1u)], ((it - 1) >> 1) & 1u, sAbort, wl))) break;
             float* cz = reinterpret_cast<float*>(sm + kOffCz) + (n & 1) * kHalf;
-            if (TQ4)   // (the score rows' buffer is free between segments)
-                rotate_queries(p, w.row0 + kHalf * rank, w.rows - kHalf * rank, sm + kOffQ, sm + kOffK + dw * kChunkBytes, cz,
-                               dw, lane);
+            if (TQ4)
+                rotate_queries(p, row0 + kHalf * rank, rows - kHalf * rank, sm + kOffQ, cz, dw, lane);
             else
-                load_queries(p, w.row0 + kHalf * rank, w.rows - kHalf * rank, sm + kOffQ, cz, dw, lane);
+                load_queries(p, row0 + kHalf * rank, rows - kHalf * rank, sm + kOffQ, cz, dw, lane);
             fence_async_smem();
             warp_arrive(&bars[kBarQ0 + (n & 1)], lane);
             if (!TQ4) warp_arrive_first(&bars[kBarQFirst], lane);
-            if (TQ4) request_k(0);
-            request_v(0);
-            // no score rows before every warp is through with its part of their buffer
-            if (TQ4 && !(ok = warp_wait(&bars[kBarQ0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl))) break;
-            // score rows of step t, then context rows of step t - 1
-            for (int t = 0; t <= w.steps; ++t) {
-                if (TQ4 && t < w.steps) {
-                    if (t > 0 && !(ok = score_done(it + t - 1))) break;
+            // the context rows' place staged the last segment's output
+            auto stage_free = [&]() { return n == 0 || warp_wait(&bars[kBarOut], (uint32_t)(n - 1) & 1u, sAbort, wl); };
+            if constexpr (TQ4) {
+                const uint4 lv = *reinterpret_cast<const uint4*>(sm + kOffLevels);
+                const Planes pl{{lv.x, lv.y}, {lv.z, lv.w}};
+                constexpr int kRowBytes = kMlaD / 2;
+                // A warp has 8 consecutive rows (they lie in one page) of the own 64 for the
+                // scores, and of both halves of the step for the context:
+                //   score rows: row lane / 4, of each chunk the quarter lane % 4 (8 bytes)
+                //   context rows: rows 4 i + lane / 2 % 4, chunk lane / 8, half lane % 2 (16 bytes)
+                // so that the 8 lanes of a store have different 16-byte units.  The codes of
+                // the own half come twice (L2 has room, 10% busy).  The next step's are asked for
+                // fill by fill, into the registers that have just been stored (256 tokens on
+                // 16,384 rows 1.73 ms, 1.80 with all of a kind at once).
+                const int k_row = lane >> 2, k_quarter = lane & 3;
+                const int v_row = (lane >> 1) & 3, v_half = lane & 1, v_chunk = lane >> 3;
+                const int k_byte = k_row * kRowBytes + 8 * k_quarter;
+                const int v_byte = v_row * kRowBytes + 128 * (v_chunk >> 1) + 64 * rank + 32 * (v_chunk & 1) + 16 * v_half;
+                const int32_t row_k = first + kHalf * rank + 8 * dw, row_v = first + 8 * dw;
+                uint32_t fill = 5 * it;   // fills so far
+                int32_t id_k = page(row_k), id_v[2] = {page(row_v), page(row_v + kHalf)};
+                uint2 k[kChunks];
+                uint4 v[2][2];
+                const uint8_t* from_k = nullptr;   // this lane's codes of the step that is asked for
+                bool there_k = false;
+                auto step_k = [&](int t) {
+                    const int32_t r = row_k + t * kRows;
+                    from_k = code_rows(r, id_k) + k_byte;
+                    there_k = t < steps && r + k_row < end;
+                    id_k = t + 1 < steps ? page(r + kRows) : 0;
+                };
+                auto request_k = [&](int g) {   // chunks 3 g ..
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) store_piece(k_chunk, raw[0][i], 8 * dw + 2 * i + up, q4, pl);
-                    fence_async_smem();
-                    warp_arrive_first(&bars[kBarK0], lane);
+                    for (int c = 3 * g; c < 3 * g + 3; ++c)
+                        k[c] = there_k ? __ldg(reinterpret_cast<const uint2*>(from_k + 32 * c)) : make_uint2(0u, 0u);
+                };
+                auto request_v = [&](int t, int h) {   // rows 64 h ..
+                    const int32_t r = row_v + t * kRows + kHalf * h;
+                    const uint8_t* a = code_rows(r, id_v[h]) + v_byte;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        store_piece(k_chunk + 4 * kChunkBytes, raw[1][i], 8 * dw + 2 * i + up, q4, pl);
-                    store_piece(sm + kOffK + kRope * kChunkBytes, rope, 8 * dw + (lane >> 2), q4, pl);   // two rows: phases differ
+                    for (int i = 0; i < 2; ++i)
+                        v[h][i] = t < steps && r + 4 * i + v_row < end
+                                      ? __ldg(reinterpret_cast<const uint4*>(a + 4 * i * kRowBytes))
+                                      : make_uint4(0u, 0u, 0u, 0u);
+                    id_v[h] = t + 1 < steps ? page(r + kRows) : 0;
+                };
+                // A wait that runs out ends the loop with the step; from there on nothing is stored
+                // (the slot may still be read) or handed over.
+                auto begin = [&]() {
+                    if (fill >= 2 && !warp_wait(&bars[kBarFree0 + (fill & 1u)], ((fill >> 1) - 1) & 1u, sAbort, wl)) ok = false;
+                    return sm + kOffSlot + (fill & 1u) * kSlotBytes;
+                };
+                auto finish = [&]() {
                     fence_async_smem();
-                    warp_arrive_first(&bars[kBarK0 + 1], lane);
-                    if (t + 1 < w.steps) request_k(t + 1);
+                    if (ok) warp_arrive_first(&bars[kBarFull0 + (fill & 1u)], lane);
+                    ++fill;
+                };
+                step_k(0);
+#pragma unroll
+                for (int g = 0; g < 3; ++g) request_k(g);
+                request_v(0, 0);
+                request_v(0, 1);
+                if (!(ok = stage_free())) break;
+                // score rows of step t, then context rows of step t - 1
+                for (int t = 0; t <= steps; ++t) {
+                    if (t < steps) {
+                        step_k(t + 1);
+#pragma unroll
+                        for (int g = 0; g < 3; ++g) {
+                            unsigned char* to = begin();
+                            if (ok) {
+#pragma unroll
+                                for (int c = 0; c < 3; ++c) {
+                                    store_levels(to + c * kChunkBytes, k[3 * g + c].x, 8 * dw + k_row, 2 * k_quarter, pl);
+                                    store_levels(to + c * kChunkBytes, k[3 * g + c].y, 8 * dw + k_row, 2 * k_quarter + 1, pl);
+                                }
+                            }
+                            finish();
+                            request_k(g);
+                        }
+                    }
+                    if (t == 0) continue;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        unsigned char* to = begin() + v_chunk * kChunkBytes;
+                        if (ok) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t in[4] = {v[h][i].x, v[h][i].y, v[h][i].z, v[h][i].w};
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) store_levels(to, in[u], 8 * dw + 4 * i + v_row, 4 * v_half + u, pl);
+                            }
+                        }
+                        finish();
+                        request_v(t, h);
+                    }
+                    if (!ok) break;
                 }
-                if (t == 0) {
-                    // (the context buffer staged the last segment's output)
-                    if (n > 0 && !(ok = warp_wait(&bars[kBarOut], (uint32_t)(n - 1) & 1u, sAbort, wl))) break;
-                    continue;
+            } else {
+                // Context rows: a warp has 8 consecutive rows of each half of a step (8 rows
+                // lie in one page): rows 2 i, 2 i + 1, bit 2 of the lane picks the row, lane / 8
+                // the chunk, lane % 4 the quarter.
+                const int q4 = lane & 3, up = (lane >> 2) & 1, c4 = lane >> 3;
+                unsigned char* v_chunk = sm + kOffV + c4 * kVChunkBytes;
+                const int v_piece = 16 * (c4 >> 1) + 8 * rank + 4 * (c4 & 1) + q4;   // of the row's 36
+                const int32_t row_v = first + 8 * dw;
+                int32_t id_v[2] = {page(row_v), page(row_v + kHalf)};
+                uint4 ctx[2][4];
+                auto request_v = [&](int t) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int32_t r0 = row_v + t * kRows + kHalf * h;
+                        const uint8_t* a = code_rows(r0, id_v[h]) + up * kMlaD + 16 * v_piece;
+                        const int last = end - r0 - up;   // rows 2 i up to here exist
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            ctx[h][i] = 2 * i < last ? __ldg(reinterpret_cast<const uint4*>(a + 2 * i * kMlaD))
+                                                     : make_uint4(0u, 0u, 0u, 0u);
+                        if (t + 1 < steps) id_v[h] = page(r0 + kRows);
+                    }
+                };
+                request_v(0);
+                if (!(ok = stage_free())) break;
+                for (int t = 0; t < steps && ok; ++t) {
+                    const uint32_t s = it + t;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (s > 0 && !(ok = warp_wait(&bars[kBarCtx0 + h], (s - 1) & 1u, sAbort, wl))) break;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) store_codes(v_chunk, ctx[h][i], kHalf * h + 8 * dw + 2 * i + up, q4);
+                        fence_async_smem();
+                        warp_arrive_first(&bars[kBarV0 + h], lane);
+                    }
+                    if (ok && t + 1 < steps) request_v(t + 1);
                 }
-                if (!(ok = store_v(it + t - 1))) break;
-                if (t < w.steps) request_v(t);
             }
-            it += w.steps;
+            it += steps;
         }
     } else {
         // ================= softmax warps =================

@@ -1,0 +1,67 @@
+"""Paged attention where its rounding could show: 2e-3 of exact attention before the
+rounding to bf16, whatever the rows and scores."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_common import TENSOR_TOL, to_dev
+from quantized_kv_cache_kv8_gb300 import synth
+from test_gpu_paged import BF16_STEP, SM, kvq  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def two_rows(kvq, oracle, fmt, x, seed, n_new, order, page=64):
+    """A pool whose rows are copies of the two rows x: row t is x[order[t]].  Returns (layout, codes, scales, block table,
+    reconstructed rows)."""
+    layout = kvq.mla_layout(seed=seed)
+    codes = torch.empty(2, kvq.row_bytes(fmt, layout), dtype=torch.uint8, device="cuda")
+    scales = torch.empty(2, 2, device="cuda")
+    (kvq.kv8_encode if fmt == 1 else kvq.tq4_encode)(to_dev(x), codes, scales, layout)
+    xh = np.asarray(oracle.reconstruct(fmt, codes.cpu().numpy(), scales.cpu().numpy(), seed=seed), np.float64)
+    pages = -(-len(order) // page)
+    rows = torch.zeros(pages * page, dtype=torch.int64, device="cuda")
+    rows[:len(order)] = to_dev(np.asarray(order, np.int64))
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None].contiguous()
+    return layout, codes[rows].contiguous(), scales[rows].contiguous(), table, xh
+
+
+def attend(kvq, fmt, q, layout, codes, scales, table, n_rows, page=64):
+    n, H = q.shape[:2]
+    out = torch.full((n, H, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(kvq.kv_attn_paged_workspace_size(fmt, 1, H, n, layout), dtype=torch.uint8, device="cuda")
+    kvq.kv_attn_paged(fmt, q, to_dev(np.array([0, n])), codes, scales, table, to_dev(np.array([n_rows])), page, out, ws, SM,
+                      layout)
+    assert kvq.read_device_error(ws) == 0
+    return out.double().cpu().numpy()
+
+
+def row_weights(out, xh):
+    """The weight of row 0 in outputs that mix two rows, by projection, over the exact weight's output."""
+    d = xh[0, :512] - xh[1, :512]
+    return (out - xh[1, :512]) @ d / (d @ d), d
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+def test_query_keeps_its_bits(kvq, oracle, fmt):  # noqa: F811
+    """Queries for which two rows score alike: the weight of row 0 is near 1/2 and moves by a quarter of what a score is
+    off.  Outputs within 2e-3 of the largest put the projected weight off by at most 2e-3 max|out| |d|_1 / |d|_2^2; their
+    rounding to bf16, 512 independent errors, each uniform up to 2^-8 of the value, adds 8 sigma (once in 10^15)."""
+    H, T, seed = 256, 256, 12
+    x = synth.mla_rows(seed, 2)
+    layout, codes, scales, table, xh = two_rows(kvq, oracle, fmt, x, seed, 1, np.arange(T) % 2)
+    full = xh[0] - xh[1]
+    q = torch.randn(H, 576, generator=torch.Generator().manual_seed(seed)).double().numpy() * 6.0
+    q -= np.outer(q @ full, full) / (full @ full)
+    q = torch.from_numpy(q).bfloat16()
+    out = attend(kvq, fmt, q[None].cuda(), layout, codes, scales, table, T)[0]
+    got, d = row_weights(out, xh)
+    z = q.double().numpy() @ xh.T * SM
+    want = 1.0 / (1.0 + np.exp(z[:, 1] - z[:, 0]))
+    ref = want[:, None] * xh[0, :512] + (1.0 - want)[:, None] * xh[1, :512]
+    allowed = TENSOR_TOL * np.abs(ref).max(1) * np.abs(d).sum() / (d @ d)
+    allowed += 8 * BF16_STEP / math.sqrt(3.0) * np.sqrt(((ref * d) ** 2).sum(1)) / (d @ d)
+    ratio = np.abs(got - want) / allowed
+    assert ratio.max() <= 1.0, (int(ratio.argmax()), float(ratio.max()))
