@@ -473,7 +473,7 @@ kvq_status kv_rope_append(kvq_format fmt, const kvq_mla_layout* layout, const kv
                           uint8_t* codes, float* scales, int64_t pool_rows, int32_t* err_word, void* stream);
 
 /* Bytes of workspace kv_attn_paged needs: one size for every length, page size
- * and batch (two partial tiles per SM).  0 for invalid or unsupported
+ * and batch (two partial tiles a walker, its long sums).  0 for invalid or unsupported
  * arguments. */
 size_t kv_attn_paged_workspace_size(kvq_format fmt, const kvq_mla_layout* layout, kvq_dtype q_dtype, int32_t n_seq,
                                     int32_t n_heads, int64_t n_tokens, kvq_path path);

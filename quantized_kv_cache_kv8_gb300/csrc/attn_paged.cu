@@ -422,7 +422,8 @@ constexpr int64_t state_rows(bool tensor) {
 }  // namespace
 
 size_t paged_workspace_bytes(bool tensor) {
-    return kWsHeader + (size_t)kPagedCtas * 4 * sizeof(int64_t) + (size_t)state_rows(tensor) * (kMlaDV + 2) * sizeof(float);
+    return kWsHeader + (size_t)kPagedCtas * 4 * sizeof(int64_t) + (size_t)state_rows(tensor) * (kMlaDV + 2) * sizeof(float) +
+           (tensor ? (size_t)kPagedCtas * 256 * sizeof(float2) : 0);
 }
 
 cudaError_t launch_attn_paged(kvq_format fmt, const kvq_mla_layout& L, bool tensor, const void* q, kvq_dtype dt,
@@ -455,6 +456,7 @@ cudaError_t launch_attn_paged(kvq_format fmt, const kvq_mla_layout& L, bool tens
     p.ws_desc = reinterpret_cast<int64_t*>(ws + kWsHeader);
     p.ws_o = reinterpret_cast<float*>(ws + kWsHeader + (size_t)kPagedCtas * 4 * sizeof(int64_t));
     p.ws_ml = p.ws_o + state_rows(tensor) * kMlaDV;
+    p.ws_l = reinterpret_cast<float2*>(p.ws_ml + state_rows(tensor) * 2);
     if (fmt == KVQ_TQ4) {
         p.signs = tq4_sign_words(L);
         p.kn[0] = (float)(1.0 / sqrt((double)L.block_dim[0]));

@@ -61,6 +61,13 @@
 // one for both; 235 with 2^10.)  Rows that a vector does not see get
 // z = -inf; a vector that has seen no row has m = -inf and E = 0.
 //
+// The products round their f32 sums towards zero: what the 65,536 MMAs of a million rows
+// add to one accumulator came out 0.3% small, and 3% off where the first row outweighs the
+// rest.  So the sums run in two levels: every kFold steps (32,768 rows) the softmax warps
+// add O, and the row sum, to totals, O's in the walker's second slot of the workspace (free
+// until its last segment ends), and the next product starts from zero (1 to 2% of a long
+// walk).
+//
 // What bounds it.  KV8, many rows a tile: the softmax warps, 3,350 cycles a step (scores
 // 1,350, vote 290, exponentials 600, weights 450, the rest hand-overs) for 2,200 of
 // products: 512 tokens on 32,768 rows x 128 heads 3.1 ms, 1,500 TFLOP/s; 32 sequences of
@@ -155,6 +162,7 @@ enum {
 // their next but one event waits for whoever waits for this one, the next does not.
 
 constexpr float kLogWmax = 15.75f, kHeadroom = 3.0f, kLogEmax = 120.0f, kLogMax = 100.0f;
+constexpr int kFold = 256;   // steps that one accumulator sums
 // levels times this round to f16 within 9.3e-5 (unscaled: 3.2e-4); divided out in f32
 constexpr float kGamma = 1.3338516f;
 constexpr uint32_t kIdescScore = idesc_f16(kVecs, kRows, false, false);   // e4m3 x e4m3 has the same bits
@@ -631,6 +639,60 @@ struct RowState {
     float m, R, E, logE, l;   // logE = inf: rows seen, but none with a latent scale yet
 };
 
+// What a softmax thread has summed up before the current kFold steps, in the workspace: its
+// 128 columns of O, in the walker's second slot, its row sum l, and the factor that
+// takes O's total to the current references.  Out of line and out of the step's registers:
+// touched every kFold steps, and where an exact step follows the first of them.
+struct Totals {
+    float* o;
+    float2* l;   // row sum, factor
+};
+__device__ __forceinline__ Totals totals_of(const PagedParams& p, int64_t pair, int rank, int tid) {
+    const int vec = kHalf * rank + (tid & (kHalf - 1)), d0 = 256 * (tid >> 7) + 128 * ((tid >> 6) & 1);
+    return {p.ws_o + ((2 * pair + 1) * kVecs + vec) * kMlaDV + d0, p.ws_l + (2 * pair + rank) * kSoft + tid};
+}
+// The accumulators (O from column `col`, l) into the totals, the first time or in addition.
+static __device__ __noinline__ void fold_sums(const PagedParams& p, int64_t pair, int rank, uint32_t col, float l, bool first) {
+    const Totals to = totals_of(p, pair, rank, threadIdx.x);
+    const float2 had = first ? make_float2(0.0f, 0.0f) : *to.l;
+    *to.l = make_float2(had.x + l, 1.0f);
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+        uint32_t o[16];
+        tmem_ld16(col + 16 * c, o);
+        tmem_wait_ld();
+        float4* g = reinterpret_cast<float4*>(to.o + 16 * c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 v = first ? make_float4(0.f, 0.f, 0.f, 0.f) : g[j];
+            g[j] = make_float4(fmaf(v.x, had.y, __uint_as_float(o[4 * j])), fmaf(v.y, had.y, __uint_as_float(o[4 * j + 1])),
+                               fmaf(v.z, had.y, __uint_as_float(o[4 * j + 2])), fmaf(v.w, had.y, __uint_as_float(o[4 * j + 3])));
+        }
+    }
+}
+// The totals back into O; returns l's.
+static __device__ __noinline__ float unfold_sums(const PagedParams& p, int64_t pair, int rank, uint32_t col) {
+    const Totals from = totals_of(p, pair, rank, threadIdx.x);
+    const float2 had = *from.l;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+        uint32_t o[16];
+        tmem_ld16(col + 16 * c, o);
+        tmem_wait_ld();
+        const float4* g = reinterpret_cast<const float4*>(from.o + 16 * c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 v = g[j];
+            o[4 * j] = __float_as_uint(fmaf(v.x, had.y, __uint_as_float(o[4 * j])));
+            o[4 * j + 1] = __float_as_uint(fmaf(v.y, had.y, __uint_as_float(o[4 * j + 1])));
+            o[4 * j + 2] = __float_as_uint(fmaf(v.z, had.y, __uint_as_float(o[4 * j + 2])));
+            o[4 * j + 3] = __float_as_uint(fmaf(v.w, had.y, __uint_as_float(o[4 * j + 3])));
+        }
+        tmem_st16(col + 16 * c, o);
+    }
+    tmem_wait_st();
+    return had.x;
+}
 // The walk's current segment as a record; false at its end.
 __device__ __forceinline__ bool announce(const PagedParams& p, const PagedWalk<PagedTensor>& walk, int64_t pair, Work* to) {
     Segment g;
@@ -828,7 +890,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 for (int ks = 0; ks < 4; ++ks)
                                     pair_mma(tmem + kColO + 128 * j, dp + h * kStep + 2 * ks,
                                              dh + 2 * j * (TQ4 ? kStep : kVStep) + ks * 128, kIdescCtx,
-                                             (t > 1 || h > 0 || ks > 0) ? 1u : 0u);
+                                             ((t - 1) % kFold > 0 || h > 0 || ks > 0) ? 1u : 0u);
                             if (TQ4) pair_commit(&bars[kBarFree0 + (fill++ & 1u)]);
                             if (!TQ4 || h == 1) pair_commit(&bars[kBarCtx0 + h]);
                         }
@@ -1150,163 +1212,178 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             RowState st{-INFINITY, -INFINITY, 0.0f, 0.0f, 0.0f};
             if (!warp_wait(&bars[kBarQ0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl)) aborted = true;
             const float cz = reinterpret_cast<const float*>(sm + kOffCz)[(n & 1) * kHalf + r];
-
-            for (int t = 0; t < steps; ++t, ++it) {
-                warp_wait(&bars[kBarScore0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl);
-                tc_after();
-                const float* s_l = reinterpret_cast<const float*>(sm + kOffScale + (it & 1u) * kScaleBytes) + kHalf * half +
-                                   kCols * sub;
-                const int seen_abort = *sAbort;   // read ahead of its use
-                const float log_s = reinterpret_cast<const float*>(sm + kOffMax)[it & 1u];   // of the step's largest s_L
-                const uint32_t ts = tmem + lane_base + kColS + 128 * (it & 1u) + kCols * sub;
-                const int32_t t0 = first + t * kRows + kHalf * half + kCols * sub;
-                const bool masked = first + (t + 1) * kRows > seen0;
-                float z[kCols];
-                float4 s_lat[kCols / 4];
-                auto scores = [&](float ref) {   // z - ref of this thread's rows
-                    const F2 cz2 = f2(cz, cz), ref2 = f2(-ref, -ref);
+            int t = 0;
+            for (int until = min(steps, kFold);; until = min(steps, until + kFold)) {
+                for (; t < until; ++t, ++it) {
+                    warp_wait(&bars[kBarScore0 + (it & 1u)], (it >> 1) & 1u, sAbort, wl);
+                    tc_after();
+                    const float* s_l = reinterpret_cast<const float*>(sm + kOffScale + (it & 1u) * kScaleBytes) + kHalf * half +
+                                       kCols * sub;
+                    const int seen_abort = *sAbort;   // read ahead of its use
+                    const float log_s = reinterpret_cast<const float*>(sm + kOffMax)[it & 1u];   // of the step's largest s_L
+                    const uint32_t ts = tmem + lane_base + kColS + 128 * (it & 1u) + kCols * sub;
+                    const int32_t t0 = first + t * kRows + kHalf * half + kCols * sub;
+                    const bool masked = first + (t + 1) * kRows > seen0;
+                    float z[kCols];
+                    float4 s_lat[kCols / 4];
+                    auto scores = [&](float ref) {   // z - ref of this thread's rows
+                        const F2 cz2 = f2(cz, cz), ref2 = f2(-ref, -ref);
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 16) {
-                        uint32_t a[16], b[16];
-                        tmem_ld16(ts + c, a);
-                        tmem_ld16(ts + 64 + c, b);
-                        float4 s_r[4];
+                        for (int c = 0; c < kCols; c += 16) {
+                            uint32_t a[16], b[16];
+                            tmem_ld16(ts + c, a);
+                            tmem_ld16(ts + 64 + c, b);
+                            float4 s_r[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            s_lat[c / 4 + j] = *reinterpret_cast<const float4*>(s_l + c + 4 * j);
-                            s_r[j] = *reinterpret_cast<const float4*>(s_l + kRows + c + 4 * j);
+                            for (int j = 0; j < 4; ++j) {
+                                s_lat[c / 4 + j] = *reinterpret_cast<const float4*>(s_l + c + 4 * j);
+                                s_r[j] = *reinterpret_cast<const float4*>(s_l + kRows + c + 4 * j);
+                            }
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 sl = s_lat[(c + j) / 4], sr = s_r[j / 4];
+                                const F2 z0 = fma2(fma2(f2(a[j], a[j + 1]), f2(sl.x, sl.y), mul2(f2(b[j], b[j + 1]), f2(sr.x, sr.y))),
+                                                   cz2, ref2);
+                                const F2 z1 = fma2(
+                                    fma2(f2(a[j + 2], a[j + 3]), f2(sl.z, sl.w), mul2(f2(b[j + 2], b[j + 3]), f2(sr.z, sr.w))), cz2,
+                                    ref2);
+                                const float2 u0 = unpack(z0), u1 = unpack(z1);
+                                z[c + j] = u0.x;
+                                z[c + j + 1] = u0.y;
+                                z[c + j + 2] = u1.x;
+                                z[c + j + 3] = u1.y;
+                            }
                         }
-                        tmem_wait_ld();
+                        if (masked) {
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 sl = s_lat[(c + j) / 4], sr = s_r[j / 4];
-                            const F2 z0 = fma2(fma2(f2(a[j], a[j + 1]), f2(sl.x, sl.y), mul2(f2(b[j], b[j + 1]), f2(sr.x, sr.y))),
-                                               cz2, ref2);
-                            const F2 z1 = fma2(
-                                fma2(f2(a[j + 2], a[j + 3]), f2(sl.z, sl.w), mul2(f2(b[j + 2], b[j + 3]), f2(sr.z, sr.w))), cz2,
-                                ref2);
-                            const float2 u0 = unpack(z0), u1 = unpack(z1);
-                            z[c + j] = u0.x;
-                            z[c + j + 1] = u0.y;
-                            z[c + j + 2] = u1.x;
-                            z[c + j + 3] = u1.y;
+                            for (int j = 0; j < kCols; ++j)
+                                if (t0 + j >= lim) z[j] = -INFINITY;
                         }
-                    }
-                    if (masked) {
+                    };
+                    // The first step has no reference yet and goes to the exact path with
+                    // plain scores; a later one comes back for them if a vote sends it there.
+                    bool exact = t == 0, stop = false;
+                    for (;;) {
+                        scores(exact ? 0.0f : st.m);
+                        if (!exact) {
+                            float top[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
-                        for (int j = 0; j < kCols; ++j)
-                            if (t0 + j >= lim) z[j] = -INFINITY;
-                    }
-                };
-                // The first step has no reference yet and goes to the exact path with
-                // plain scores; a later one comes back for them if a vote sends it there.
-                bool exact = t == 0, stop = false;
-                for (;;) {
-                    scores(exact ? 0.0f : st.m);
-                    if (!exact) {
-                        float top[4] = {z[0], z[1], z[2], z[3]};
+                            for (int j = 4; j < kCols; ++j) top[j & 3] = fmaxf(top[j & 3], z[j]);
+                            const float dmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                            const float log_se = log_s + st.logE;
+                            const bool flag = aborted | (seen_abort != 0) | (dmax + log_se > kLogWmax) | (dmax > kLogMax) |
+                                              (log_se > kLogMax);
+                            if (!group_any(group, flag)) break;
+                            exact = true;
+                            continue;
+                        }
+                        // ---- exact path: row maxima, new references, O rescaled ----
+                        if (it > 0 && !warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)) aborted = true;
+                        if (group_any(group, aborted | (*sAbort != 0))) {
+                            stop = true;
+                            break;
+                        }
+                        tc_after();
+                        float zt = -INFINITY, yt = -INFINITY;
 #pragma unroll
-                        for (int j = 4; j < kCols; ++j) top[j & 3] = fmaxf(top[j & 3], z[j]);
-                        const float dmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                        const float log_se = log_s + st.logE;
-                        const bool flag = aborted | (seen_abort != 0) | (dmax + log_se > kLogWmax) | (dmax > kLogMax) |
-                                          (log_se > kLogMax);
-                        if (!group_any(group, flag)) break;
-                        exact = true;
-                        continue;
-                    }
-                    // ---- exact path: row maxima, new references, O rescaled ----
-                    if (it > 0 && !warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)) aborted = true;
-                    if (group_any(group, aborted | (*sAbort != 0))) {
-                        stop = true;
+                        for (int j = 0; j < kCols; j += 4) {
+                            const float4 sl = TQ4 ? *reinterpret_cast<const float4*>(s_l + j) : s_lat[j / 4];
+                            const float s[4] = {sl.x, sl.y, sl.z, sl.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                zt = fmaxf(zt, z[j + k]);
+                                yt = fmaxf(yt, z[j + k] + (s[k] > 0.0f ? __log2f(s[k]) : -INFINITY));   // -inf: an inert latent block
+                            }
+                        }
+                        gX[32 * (warp >> 1) + lane] = zt;
+                        gX[128 + 32 * (warp >> 1) + lane] = yt;
+                        group_sync(group);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            zt = fmaxf(zt, gX[32 * k + lane]);
+                            yt = fmaxf(yt, gX[128 + 32 * k + lane]);
+                        }
+                        group_sync(group);   // read before any thread's weights go there
+                        const float mn = fmaxf(st.m, zt), rn = fmaxf(st.R, yt);
+                        const bool inert = rn == -INFINITY;
+                        float le = fminf(mn - rn - kHeadroom, fminf(kLogEmax, kLogMax - log_s));   // s_L E stays finite
+                        const float al = st.m == -INFINITY ? 0.0f : ex2(st.m - mn);
+                        // O holds sum p s_L E c: rescaled by (E_new / E_old) 2^(m_old - m_new)
+                        const float ao = st.R == -INFINITY ? 0.0f : ex2(le - st.logE + (st.m - mn));
+                        st.l *= al;
+                        if (t >= kFold) {
+                            float2* had = totals_of(p, pair, rank, tid).l;
+                            *had = make_float2(had->x * al, had->y * ao);
+                        }
+                        st.m = mn;
+                        st.R = rn;
+                        // rows seen without a latent scale: the next one comes here again;
+                        // no row seen: the first score does, by m = -inf
+                        st.logE = inert && mn > -INFINITY ? INFINITY : le;
+                        st.E = inert ? 0.0f : ex2(le);
+                        if (t > 0) {   // (to no use where this step's product starts from zero)
+#pragma unroll 1
+                            for (int c = 8 * sub; c < 8 * sub + 8; ++c) {   // 128 of the columns a thread
+                                uint32_t o[16];
+                                tmem_ld16(tmem + lane_base + kColO + 16 * c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * ao);
+                                tmem_st16(tmem + lane_base + kColO + 16 * c, o);
+                            }
+                            tmem_wait_st();
+                            if (warp < 2 && lane == 0) atomicAdd(p.exact_count, 1u);
+                        }
+                        // a vector that has seen no row keeps z = -inf
+                        const float ref = mn == -INFINITY ? 0.0f : mn;
+#pragma unroll
+                        for (int j = 0; j < kCols; ++j) z[j] -= ref;
                         break;
                     }
-                    tc_after();
-                    float zt = -INFINITY, yt = -INFINITY;
+                    if (stop) {
+                        aborted = true;
+                        break;
+                    }
+                    // asked before the weights are computed, used after: has the context
+                    // of the step before read its weights?
+                    const bool free_p = it == 0 || try_once(smem_u32(&bars[kBarCtx0 + 1]), (it - 1) & 1u);
+                    uint32_t pk[kCols / 2];
+                    F2 sum2 = f2(0.0f, 0.0f);
+                    const F2 e2 = f2(st.E, st.E);
 #pragma unroll
                     for (int j = 0; j < kCols; j += 4) {
                         const float4 sl = TQ4 ? *reinterpret_cast<const float4*>(s_l + j) : s_lat[j / 4];
-                        const float s[4] = {sl.x, sl.y, sl.z, sl.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            zt = fmaxf(zt, z[j + k]);
-                            yt = fmaxf(yt, z[j + k] + (s[k] > 0.0f ? __log2f(s[k]) : -INFINITY));   // -inf: an inert latent block
-                        }
+                        const float e[4] = {ex2(z[j]), ex2(z[j + 1]), ex2(z[j + 2]), ex2(z[j + 3])};
+                        const F2 p0 = f2(e[0], e[1]), p1 = f2(e[2], e[3]);
+                        sum2 = add2(sum2, add2(p0, p1));
+                        const float2 w0 = unpack(mul2(p0, mul2(e2, f2(sl.x, sl.y))));
+                        const float2 w1 = unpack(mul2(p1, mul2(e2, f2(sl.z, sl.w))));
+                        const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
+                        pk[j / 2] = *reinterpret_cast<const uint32_t*>(&h0);
+                        pk[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
                     }
-                    gX[32 * (warp >> 1) + lane] = zt;
-                    gX[128 + 32 * (warp >> 1) + lane] = yt;
-                    group_sync(group);
+                    const float2 sum = unpack(sum2);
+                    st.l += sum.x + sum.y;
+                    warp_arrive(&bars[kBarScaleFree0 + (it & 1u)], lane);
+                    if (!__all_sync(kFull, free_p)) warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        zt = fmaxf(zt, gX[32 * k + lane]);
-                        yt = fmaxf(yt, gX[128 + 32 * k + lane]);
-                    }
-                    group_sync(group);   // read before any thread's weights go there
-                    const float mn = fmaxf(st.m, zt), rn = fmaxf(st.R, yt);
-                    const bool inert = rn == -INFINITY;
-                    float le = fminf(mn - rn - kHeadroom, fminf(kLogEmax, kLogMax - log_s));   // s_L E stays finite
-                    const float al = st.m == -INFINITY ? 0.0f : ex2(st.m - mn);
-                    // O holds sum p s_L E c: rescaled by (E_new / E_old) 2^(m_old - m_new)
-                    const float ao = st.R == -INFINITY ? 0.0f : ex2(le - st.logE + (st.m - mn));
-                    st.l *= al;
-                    st.m = mn;
-                    st.R = rn;
-                    // rows seen without a latent scale: the next one comes here again;
-                    // no row seen: the first score does, by m = -inf
-                    st.logE = inert && mn > -INFINITY ? INFINITY : le;
-                    st.E = inert ? 0.0f : ex2(le);
-                    if (t > 0) {
-#pragma unroll 1
-                        for (int c = 8 * sub; c < 8 * sub + 8; ++c) {   // 128 of the columns a thread
-                            uint32_t o[16];
-                            tmem_ld16(tmem + lane_base + kColO + 16 * c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * ao);
-                            tmem_st16(tmem + lane_base + kColO + 16 * c, o);
-                        }
-                        tmem_wait_st();
-                        if (warp < 2 && lane == 0) atomicAdd(p.exact_count, 1u);
-                    }
-                    // a vector that has seen no row keeps z = -inf
-                    const float ref = mn == -INFINITY ? 0.0f : mn;
-#pragma unroll
-                    for (int j = 0; j < kCols; ++j) z[j] -= ref;
-                    break;
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4*>(sP + sw128(r, 64 * sub + 16 * i)) =
+                            make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                    fence_async_smem();
+                    tc_before();
+                    warp_arrive_first(&bars[kBarP], lane);
                 }
-                if (stop) {
+                if (aborted || t == steps) break;
+                // ---- the next product starts from zero ----
+                if (!warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)) {
                     aborted = true;
                     break;
                 }
-                // asked before the weights are computed, used after: has the context
-                // of the step before read its weights?
-                const bool free_p = it == 0 || try_once(smem_u32(&bars[kBarCtx0 + 1]), (it - 1) & 1u);
-                uint32_t pk[kCols / 2];
-                F2 sum2 = f2(0.0f, 0.0f);
-                const F2 e2 = f2(st.E, st.E);
-#pragma unroll
-                for (int j = 0; j < kCols; j += 4) {
-                    const float4 sl = TQ4 ? *reinterpret_cast<const float4*>(s_l + j) : s_lat[j / 4];
-                    const float e[4] = {ex2(z[j]), ex2(z[j + 1]), ex2(z[j + 2]), ex2(z[j + 3])};
-                    const F2 p0 = f2(e[0], e[1]), p1 = f2(e[2], e[3]);
-                    sum2 = add2(sum2, add2(p0, p1));
-                    const float2 w0 = unpack(mul2(p0, mul2(e2, f2(sl.x, sl.y))));
-                    const float2 w1 = unpack(mul2(p1, mul2(e2, f2(sl.z, sl.w))));
-                    const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
-                    pk[j / 2] = *reinterpret_cast<const uint32_t*>(&h0);
-                    pk[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-                }
-                const float2 sum = unpack(sum2);
-                st.l += sum.x + sum.y;
-                warp_arrive(&bars[kBarScaleFree0 + (it & 1u)], lane);
-                if (!__all_sync(kFull, free_p)) warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4*>(sP + sw128(r, 64 * sub + 16 * i)) =
-                        make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-                fence_async_smem();
-                tc_before();
-                warp_arrive_first(&bars[kBarP], lane);
+                tc_after();
+                fold_sums(p, pair, rank, tmem + lane_base + kColO + 128 * sub, st.l, t == kFold);
+                st.l = 0.0f;
             }
             // ---- output ----
             if (!aborted && !warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)) aborted = true;
@@ -1315,6 +1392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_after();
+            if (steps > kFold) st.l += unfold_sums(p, pair, rank, tmem + lane_base + kColO + 128 * sub);
             sX[tid] = st.l;
             worker_sync<kSoft>();
             const float l = (sX[r] + sX[kHalf + r]) + (sX[2 * kHalf + r] + sX[3 * kHalf + r]);   // the same in all four
@@ -1333,11 +1411,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 p.ws_desc[pair * 4 + 1] = w.row0;
                 p.ws_desc[pair * 4 + 2] = w.rows;
             }
+            // dims d0 + 16 c .. + 15 of this vector, c < 8
+            const int d0 = 256 * sub + 128 * half;
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + w.row0 * kMlaDV;
             const int rows = w.rows;
             const bool wide = (((uintptr_t)p.out | (uintptr_t)p.ws_o) & 31) == 0;
-            // dims d0 + 16 c .. + 15 of this vector, c < 8
-            const int d0 = 256 * sub + 128 * half;
             auto context = [&](int c, float (&o)[16]) {
                 uint32_t u[16];
                 tmem_ld16(tmem + lane_base + kColO + 128 * sub + 16 * c, u);

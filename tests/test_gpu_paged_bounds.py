@@ -13,12 +13,12 @@ from test_gpu_paged import BF16_STEP, SM, kvq  # noqa: F401
 pytestmark = pytest.mark.gpu
 
 
-def two_rows(kvq, oracle, fmt, x, seed, n_new, order, page=64):
-    """A pool whose rows are copies of the two rows x: row t is x[order[t]].  Returns (layout, codes, scales, block table,
+def copies(kvq, oracle, fmt, x, seed, order, page=64):
+    """A pool whose rows are copies of the rows x: row t is x[order[t]].  Returns (layout, codes, scales, block table,
     reconstructed rows)."""
     layout = kvq.mla_layout(seed=seed)
-    codes = torch.empty(2, kvq.row_bytes(fmt, layout), dtype=torch.uint8, device="cuda")
-    scales = torch.empty(2, 2, device="cuda")
+    codes = torch.empty(len(x), kvq.row_bytes(fmt, layout), dtype=torch.uint8, device="cuda")
+    scales = torch.empty(len(x), 2, device="cuda")
     (kvq.kv8_encode if fmt == 1 else kvq.tq4_encode)(to_dev(x), codes, scales, layout)
     xh = np.asarray(oracle.reconstruct(fmt, codes.cpu().numpy(), scales.cpu().numpy(), seed=seed), np.float64)
     pages = -(-len(order) // page)
@@ -51,7 +51,7 @@ def test_query_keeps_its_bits(kvq, oracle, fmt):  # noqa: F811
     rounding to bf16, 512 independent errors, each uniform up to 2^-8 of the value, adds 8 sigma (once in 10^15)."""
     H, T, seed = 256, 256, 12
     x = synth.mla_rows(seed, 2)
-    layout, codes, scales, table, xh = two_rows(kvq, oracle, fmt, x, seed, 1, np.arange(T) % 2)
+    layout, codes, scales, table, xh = copies(kvq, oracle, fmt, x, seed, np.arange(T) % 2)
     full = xh[0] - xh[1]
     q = torch.randn(H, 576, generator=torch.Generator().manual_seed(seed)).double().numpy() * 6.0
     q -= np.outer(q @ full, full) / (full @ full)
@@ -65,3 +65,45 @@ def test_query_keeps_its_bits(kvq, oracle, fmt):  # noqa: F811
     allowed += 8 * BF16_STEP / math.sqrt(3.0) * np.sqrt(((ref * d) ** 2).sum(1)) / (d @ d)
     ratio = np.abs(got - want) / allowed
     assert ratio.max() <= 1.0, (int(ratio.argmax()), float(ratio.max()))
+
+
+ORDERS = {"falling": lambda order, rng: order, "rising": lambda order, rng: order[::-1], "mixed": lambda order, rng: rng.permutation(order)}
+
+
+def check_kinds(kvq, oracle, fmt, binades, counts, order):  # noqa: F811
+    """Rows of a few kinds whose scores lie `binades` apart; each kind has dims of its own, so that an output shows what
+    the kind weighs.  80 tiles of 128 heads: a walker has nearly all rows of a tile.  Outputs within 2e-3 of the largest,
+    their rounding to bf16 (2^-8 of the value) aside."""
+    H, n, seed = 128, 80, 3
+    rng = np.random.default_rng(seed)
+    kinds = len(binades)
+    x = 0.3 * rng.standard_normal((kinds, 576)).astype(np.float32)
+    for k in range(kinds):
+        x[k, 64 * (k + 1):64 * (k + 2)] += 2.0
+    kind = ORDERS[order](np.repeat(np.arange(kinds), counts), rng)
+    T = len(kind)
+    layout, codes, scales, table, xh = copies(kvq, oracle, fmt, x, seed, kind)
+    # queries: a random one for each head, moved so that the kinds' scores lie as asked, times 0.9 to 1.1
+    q = rng.standard_normal((H, 576))
+    goal = np.outer(np.linspace(0.9, 1.1, H), np.array(binades) * math.log(2.0) / SM)
+    steps = xh[1:] - xh[0]
+    q += np.linalg.solve(steps @ steps.T, (goal[:, 1:] - goal[:, :1] - q @ steps.T).T).T @ steps
+    q = torch.from_numpy(q).bfloat16()
+    out = attend(kvq, fmt, q.expand(n, H, 576).contiguous().cuda(), layout, codes, scales, table, T)
+    z = q.double().numpy() @ xh.T * SM
+    w = np.exp(z - z.max(1, keepdims=True))
+    worst = 0.0
+    seen = np.stack([np.cumsum(kind == k) for k in range(kinds)])       # of each kind up to row t
+    for i in range(n):
+        m = w * seen[:, T - n + i]
+        ref = (m / m.sum(1, keepdims=True)) @ xh[:, :512]
+        top = TENSOR_TOL * np.abs(ref).max(1, keepdims=True)
+        worst = max(worst, float((np.abs(out[i] - ref) / (top + BF16_STEP * (np.abs(ref) + top))).max()))
+    assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("counts", [[1 << 19, 1 << 19], [5, (1 << 20) - 5]])
+def test_long_sums(kvq, oracle, fmt, counts):  # noqa: F811
+    """A million rows by one walker: what 65,536 products add to one accumulator."""
+    check_kinds(kvq, oracle, fmt, [0, 0], counts, "mixed")
