@@ -52,7 +52,7 @@
 // Softmax, per query vector (a thread has one and a quarter of the rows), in log2
 // units: m is a lagged running maximum of the scores, p = 2^(z - m) enters the
 // row sum in f32, and the context takes the f16 weight w = p s_L E,
-// E = 2^(m - R - 3) with R the largest z + log2 s_L of the steps that set the
+// E = 2^(m - R - 2) with R the largest z + log2 s_L of the steps that set the
 // references, so that weights are relative to the largest p s_L and rows of
 // small latent scale keep f16 precision where they matter.  A step in which w might
 // pass 2^15.75, by its largest z - m and its largest s_L, goes down the exact path: row
@@ -60,6 +60,17 @@
 // 2^14 and 3.5, sent more steps there: mixed batch of 24 sequences 212 us, 206 with the
 // one for both; 235 with 2^10.)  Rows that a vector does not see get
 // z = -inf; a vector that has seen no row has m = -inf and E = 0.
+//
+// Weights under 2^-14 lose bits, up to 2^-25 a row: nothing beside one large weight, but
+// 131,072 rows 20 binades below the first lost a third of their sum, 3% of the output.  So
+// each thread keeps the sum of its weights and that bound of what it lost (32 rows a
+// step).  Where the loss may pass 2^-11 of the sum, the step takes the exact path and R
+// comes down to its largest z + log2 s_L, by 2^24 at most; each fall after that waits for a
+// sixteenth of it (2^24 steps, then).  A vector's largest weight is one thread's, so the
+// least of its four sums is at most a third of all its weights, and less than 2^-10 of them
+// is lost before the first fall, beside the 2^-11 of its own by which any weight is rounded.
+// (A larger E has fewer falls and more rises: mixed batch of 24 sequences 206 us; 213 with
+// 2^(m - R - 3), 211 with 2^(m - R).)
 //
 // The products round their f32 sums towards zero: what the 65,536 MMAs of a million rows
 // add to one accumulator came out 0.3% small, and 3% off where the first row outweighs the
@@ -98,10 +109,10 @@ constexpr int kThreads = kSoft + kDec + 128;   // five warpgroups
 // Registers a thread after the split.  KV8: the decode warps hold half the codes
 // (none of the score rows), and the softmax keeps a step's latent scales between scores
 // and weights instead of reading them twice (512 tokens on 32,768 rows x 128 heads
-// 3.17 ms; 3.34 with TQ4's split).
+// 3.16 ms, 3.25 with 112 and 96).
 template <bool TQ4>
 struct Regs {
-    static constexpr int kLaunch = 96, kSoftmax = TQ4 ? 88 : 112, kDecode = TQ4 ? 120 : 96, kRest = 64;
+    static constexpr int kLaunch = 96, kSoftmax = TQ4 ? 88 : 120, kDecode = TQ4 ? 120 : 88, kRest = 64;
     static_assert(kSoft * kSoftmax + kDec * kDecode + 128 * kRest <= kThreads * kLaunch, "register split");
 };
 // To N from the launch's count, by a whole warpgroup (N = FROM is written too: the
@@ -161,8 +172,10 @@ enum {
 // Scores, announcements, queries and scales have two barriers each, used in turn:
 // their next but one event waits for whoever waits for this one, the next does not.
 
-constexpr float kLogWmax = 15.75f, kHeadroom = 3.0f, kLogEmax = 120.0f, kLogMax = 100.0f;
+constexpr float kLogWmax = 15.75f, kHeadroom = 2.0f, kLogEmax = 120.0f, kLogMax = 100.0f;
 constexpr int kFold = 256;   // steps that one accumulator sums
+constexpr float kLossStep = 0x1p-20f, kLossShare = 0x1p-11f, kMaxDrop = 24.0f;
+static_assert(kCols == 32, "a thread's rows a step, 2^-25 each");
 // levels times this round to f16 within 9.3e-5 (unscaled: 3.2e-4); divided out in f32
 constexpr float kGamma = 1.3338516f;
 constexpr uint32_t kIdescScore = idesc_f16(kVecs, kRows, false, false);   // e4m3 x e4m3 has the same bits
@@ -637,6 +650,8 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8], bool 
 // A query vector's softmax state.
 struct RowState {
     float m, R, E, logE, l;   // logE = inf: rows seen, but none with a latent scale yet
+    float kept, lost;         // sum of this thread's weights, a quarter of the vector's before the
+                              // last exact step; what their rounding may have lost
 };
 
 // What a softmax thread has summed up before the current kFold steps, in the workspace: its
@@ -1209,7 +1224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // vectors past the tile's last repeat its limit: they score 0 and are dropped
             const int vec = kHalf * rank + r;
             const int32_t lim = (int32_t)max((int64_t)0, w.base + 1 + over_heads(p, w.tok0 + min(vec, w.rows - 1)));
-            RowState st{-INFINITY, -INFINITY, 0.0f, 0.0f, 0.0f};
+            RowState st{-INFINITY, -INFINITY, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
             if (!warp_wait(&bars[kBarQ0 + (n & 1)], (uint32_t)(n >> 1) & 1u, sAbort, wl)) aborted = true;
             const float cz = reinterpret_cast<const float*>(sm + kOffCz)[(n & 1) * kHalf + r];
             int t = 0;
@@ -1263,6 +1278,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     };
                     // The first step has no reference yet and goes to the exact path with
                     // plain scores; a later one comes back for them if a vote sends it there.
+                    const bool low = st.lost > kLossShare * st.kept;   // (NaN: no)
                     bool exact = t == 0, stop = false;
                     for (;;) {
                         scores(exact ? 0.0f : st.m);
@@ -1273,7 +1289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             const float dmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                             const float log_se = log_s + st.logE;
                             const bool flag = aborted | (seen_abort != 0) | (dmax + log_se > kLogWmax) | (dmax > kLogMax) |
-                                              (log_se > kLogMax);
+                                              (log_se > kLogMax) | low;
                             if (!group_any(group, flag)) break;
                             exact = true;
                             continue;
@@ -1298,19 +1314,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                         gX[32 * (warp >> 1) + lane] = zt;
                         gX[128 + 32 * (warp >> 1) + lane] = yt;
+                        gX[256 + 32 * (warp >> 1) + lane] = low ? -st.kept : st.kept;
                         group_sync(group);
+                        float kept = 0.0f;
+                        bool fall = false;   // the same in all four
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             zt = fmaxf(zt, gX[32 * k + lane]);
                             yt = fmaxf(yt, gX[128 + 32 * k + lane]);
+                            const float w = gX[256 + 32 * k + lane];
+                            kept += fabsf(w);
+                            fall |= __float_as_int(w) < 0;
                         }
                         group_sync(group);   // read before any thread's weights go there
-                        const float mn = fmaxf(st.m, zt), rn = fmaxf(st.R, yt);
+                        const float mn = fmaxf(st.m, zt), rn = fmaxf(fall ? st.R - kMaxDrop : st.R, yt);
                         const bool inert = rn == -INFINITY;
                         float le = fminf(mn - rn - kHeadroom, fminf(kLogEmax, kLogMax - log_s));   // s_L E stays finite
                         const float al = st.m == -INFINITY ? 0.0f : ex2(st.m - mn);
                         // O holds sum p s_L E c: rescaled by (E_new / E_old) 2^(m_old - m_new)
                         const float ao = st.R == -INFINITY ? 0.0f : ex2(le - st.logE + (st.m - mn));
+                        // the weights are shared out, and this step's largest counts in all four threads
+                        st.kept = inert ? 0.0f : 0.25f * fmaf(kept, ao, ex2(yt + (le - mn)));
+                        st.lost *= ao;
+                        if (fall) st.lost = fminf(st.lost, 0.9375f * kLossShare * st.kept);
                         st.l *= al;
                         if (t >= kFold) {
                             float2* had = totals_of(p, pair, rank, tid).l;
@@ -1349,7 +1375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     // of the step before read its weights?
                     const bool free_p = it == 0 || try_once(smem_u32(&bars[kBarCtx0 + 1]), (it - 1) & 1u);
                     uint32_t pk[kCols / 2];
-                    F2 sum2 = f2(0.0f, 0.0f);
+                    F2 sum2 = f2(0.0f, 0.0f), kept2 = f2(0.0f, 0.0f);
                     const F2 e2 = f2(st.E, st.E);
 #pragma unroll
                     for (int j = 0; j < kCols; j += 4) {
@@ -1357,14 +1383,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const float e[4] = {ex2(z[j]), ex2(z[j + 1]), ex2(z[j + 2]), ex2(z[j + 3])};
                         const F2 p0 = f2(e[0], e[1]), p1 = f2(e[2], e[3]);
                         sum2 = add2(sum2, add2(p0, p1));
-                        const float2 w0 = unpack(mul2(p0, mul2(e2, f2(sl.x, sl.y))));
-                        const float2 w1 = unpack(mul2(p1, mul2(e2, f2(sl.z, sl.w))));
+                        const F2 x0 = mul2(p0, mul2(e2, f2(sl.x, sl.y))), x1 = mul2(p1, mul2(e2, f2(sl.z, sl.w)));
+                        kept2 = add2(kept2, add2(x0, x1));
+                        const float2 w0 = unpack(x0), w1 = unpack(x1);
                         const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
                         pk[j / 2] = *reinterpret_cast<const uint32_t*>(&h0);
                         pk[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
                     }
                     const float2 sum = unpack(sum2);
                     st.l += sum.x + sum.y;
+                    const float2 kept = unpack(kept2);
+                    st.kept += kept.x + kept.y;
+                    st.lost = st.E > 0.0f ? st.lost + kLossStep : 0.0f;
                     warp_arrive(&bars[kBarScaleFree0 + (it & 1u)], lane);
                     if (!__all_sync(kFull, free_p)) warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl);
 #pragma unroll

@@ -107,3 +107,14 @@ def check_kinds(kvq, oracle, fmt, binades, counts, order):  # noqa: F811
 def test_long_sums(kvq, oracle, fmt, counts):  # noqa: F811
     """A million rows by one walker: what 65,536 products add to one accumulator."""
     check_kinds(kvq, oracle, fmt, [0, 0], counts, "mixed")
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("binades,counts,order", [
+    ([0, -20.5], [1, 131071], "falling"), ([0, -20.5], [1, 131071], "mixed"), ([0, -17], [33, 131039], "mixed"),
+    ([0, -9, -18], [1, 700, 130000], "falling"), ([0, -9, -18], [1, 700, 130000], "rising"),
+    ([0, -9, -18], [1, 700, 130000], "mixed"), ([0, -14, -28], [1, 3, 90000], "falling"), ([0, -60], [1, 70000], "falling"),
+])
+def test_many_small_weights_add_up(kvq, oracle, fmt, binades, counts, order):  # noqa: F811
+    """One kind outweighs another by many binades, but for the number of its rows."""
+    check_kinds(kvq, oracle, fmt, binades, counts, order)
