@@ -425,7 +425,9 @@ kvq_status kv_pages_reserve(int32_t n_seq, int32_t page_rows, const int64_t* kv_
  *   kv_lens      [n_seq] int64, updated
  *   keep_lens    [n_seq] int64 (not kv_lens itself)
  * Block-table entries are left as they are.  More pages than the stack has
- * room for, or an invalid length, changes nothing and sets KVQ_ERR_ARG. */
+ * room for, an invalid length, or a page outside [0, n_pages) among those to be
+ * given back: lengths, n_free and the pages on the stack stay as they are (the
+ * entries above its top do not) and KVQ_ERR_ARG is set. */
 kvq_status kv_pages_trim(int32_t n_seq, int32_t page_rows, int64_t* kv_lens, const int64_t* keep_lens,
                          int32_t* block_table, int32_t table_stride, int32_t* free_pages, int32_t* n_free,
                          int32_t n_pages, void* workspace, size_t workspace_bytes, void* stream);

@@ -19,7 +19,9 @@
 // share of the rows (a binary search over the scanned offsets in shared
 // memory) and of the new table entries.  The counters that are both read and
 // written (n_free, and the lengths where the caller updates them in place) are
-// written by the CTA that arrives last, after every read.
+// written by the CTA that arrives last, after every read.  A trim writes the pages
+// above the stack's top first: where one of them is no page, that CTA, which has heard
+// of it with the arrivals, leaves the top and the lengths as they were.
 // Measured, a reservation and its trim in a replayed graph: 64 sequences of one new
 // row 5.7 us, 1024 sequences of up to 63 12.1 us.
 #include "paged.cuh"
@@ -31,6 +33,7 @@ namespace {
 
 constexpr int kSmall = 256, kLarge = 1024;   // threads of a CTA = sequences scanned at once
 constexpr int64_t kMaxLen = 1ll << 40;
+constexpr uint32_t kBadTicket = 1u << 16;    // arrivals below it, CTAs with a broken entry above
 
 struct PagesParams {
     int32_t n_seq, shift, table_stride, n_pages;
@@ -140,7 +143,7 @@ __global__ void __launch_bounds__(kNT) pages_kernel(PagesParams p) {
     __shared__ int64_t part[kNT / 32][2], tot[2];
     __shared__ int64_t s_len[kNT];
     __shared__ int32_t s_row[kNT], s_page[kNT], s_p0[kNT];   // s_row, s_page: exclusive prefixes within the chunk
-    __shared__ int s_last;
+    __shared__ int s_last, s_bad;
     launch_dependents();
     grid_dependency_wait();
     const int tid = threadIdx.x;
@@ -246,25 +249,26 @@ __global__ void __launch_bounds__(kNT) pages_kernel(PagesParams p) {
     if (bad_page && p.err) atomicCAS(p.err, 0, (int32_t)KVQ_ERR_ARG);
 
     // the last CTA to get here updates what the others have read
+    bad_page = __syncthreads_or(bad_page);
     if (G > 1) {
-        __syncthreads();
         if (tid == 0) {
             __threadfence();
-            s_last = atomicAdd(p.ticket, 1u) == (uint32_t)(G - 1);
+            const uint32_t before = atomicAdd(p.ticket, bad_page ? kBadTicket + 1u : 1u);
+            s_last = (before & (kBadTicket - 1u)) == (uint32_t)(G - 1);
+            s_bad = bad_page || before >= kBadTicket;
             __threadfence();
         }
         __syncthreads();
         if (!s_last) return;
+        bad_page = s_bad;
+        if (tid == 0) *p.ticket = 0u;
     }
-    __syncthreads();
+    if (TRIM && bad_page) return;
     for (int s = tid; s < p.n_seq; s += kNT) {
         const SeqNeed r = n_chunks > 1 ? seq_need<TRIM>(p, s) : one;
         p.lens_out[s] = TRIM ? r.rows : r.len + r.rows;
     }
-    if (tid == 0) {
-        *p.n_free = n_free + (int32_t)(TRIM ? page_total : -page_total);
-        if (G > 1) *p.ticket = 0u;
-    }
+    if (tid == 0) *p.n_free = n_free + (int32_t)(TRIM ? page_total : -page_total);
 }
 
 PagesParams base_params(int32_t n_seq, int32_t page_rows, const int64_t* lens, const int64_t* arg, int32_t* table,
