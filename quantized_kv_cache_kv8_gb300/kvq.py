@@ -76,7 +76,7 @@ def lib():
     global _lib
     with _lock:
         if _lib is None:
-            path = _build.build()
+            path = _build.build_library()
             L = C.CDLL(path)
             _declare(L)
             _lib = L
@@ -411,7 +411,7 @@ def _paged():
     L = lib()
     with _lock:
         if _host is None:
-            loader = importlib.machinery.ExtensionFileLoader("_paged_host", _build.HOST)
+            loader = importlib.machinery.ExtensionFileLoader("_paged_host", _build.build_host())
             m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_paged_host", loader))
             loader.exec_module(m)
             m.init(*(C.cast(f, C.c_void_p).value for f in (L.kv_pages_reserve, L.kv_pages_trim, L.kv_rope_append,
