@@ -1,5 +1,6 @@
 """Paged attention where its rounding could show: 2e-3 of exact attention before the
 rounding to bf16, whatever the rows and scores."""
+import ctypes as C
 import math
 
 import numpy as np
@@ -118,3 +119,20 @@ def test_long_sums(kvq, oracle, fmt, counts):  # noqa: F811
 def test_many_small_weights_add_up(kvq, oracle, fmt, binades, counts, order):  # noqa: F811
     """One kind outweighs another by many binades, but for the number of its rows."""
     check_kinds(kvq, oracle, fmt, binades, counts, order)
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("path,bf16", [(1, False), (1, True), (2, True)])
+def test_tables_without_entries(kvq, fmt, path, bf16):  # noqa: F811
+    """A pool that no table can list anything of, its addresses null: nothing is read, every token yields zeros."""
+    layout, H, n = kvq.mla_layout(), 4, 3
+    dtype = torch.bfloat16 if bf16 else torch.float32
+    q, out = torch.ones(n, H, 576, dtype=dtype, device="cuda"), torch.full((n, H, 512), 7.0, dtype=dtype, device="cuda")
+    cu, lens = to_dev(np.array([0, 1, 3])), torch.zeros(2, dtype=torch.int64, device="cuda")
+    size = kvq.kv_attn_paged_workspace_size(fmt, 2, H, n, layout, bf16, path)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    status = kvq.lib().kv_attn_paged(fmt, C.byref(layout), q.data_ptr(), int(bf16), n, H, 2, cu.data_ptr(), None, None, None, 0,
+                                     lens.data_ptr(), 16, 5, SM, out.data_ptr(), ws.data_ptr(), size, path, None)
+    torch.cuda.synchronize()
+    assert status == 0 and kvq.read_device_error(ws) == 0 and bool((out == 0).all())
