@@ -7,10 +7,13 @@
 // sums as in the contiguous kernels.  Scores: a thread takes 2 vectors x 2
 // rows, so four 16-byte reads serve 16 multiply-adds (a head and a row a thread
 // needs two for 4).  Context: a thread takes 8 vectors x 8 dims in registers.
-// Sums run in two levels (blocks of 1024 rows, then their total), as in the
-// contiguous kernel.  It is bound by the FMA pipe and shared memory: 11 TFLOP/s for 16
-// sequences of 60 to 1000 rows x 32 heads (44 us), by latency for a few (29 us for 4
-// sequences of 100 to 700 rows x 16 heads).
+// Sums run in three levels -- the 32 rows of a step, 32 steps, and the totals of those in
+// the workspace, two f32 each -- so that roundings that all point one way stay under
+// (32 + 32) 2^-24 whatever the length (with first sums of 1,024 rows, 131,072 rows alike
+// behind one that outweighs them came out 4.6e-5 off).  What bounds it is latency: one CTA of 8 warps an SM, and loads,
+// scores and context of a step one after the other, 11 TFLOP/s for 16 sequences of 60 to
+// 1000 rows x 32 heads (44 us), a seventh of the FMA rate; 29 us for 4 sequences of 100 to
+// 700 rows x 16 heads.
 #include "paged_common.cuh"
 
 #include <math.h>
@@ -24,7 +27,7 @@ constexpr int kM = PagedSimt::kM, kN = PagedSimt::kN;
 constexpr int kXS = 580;             // row stride in floats (4 banks apart)
 constexpr int kPS = kM + 4;          // weights: [row][vector]
 constexpr int kFlush = 1024 / kN;    // steps per block sum
-constexpr size_t kSmemFloats = (size_t)(kM + kN) * kXS + kN * 2 + (size_t)kN * kPS + kM + 16;
+constexpr size_t kSmemFloats = (size_t)(kM + kN) * kXS + kN * 2 + (size_t)kN * kPS + 3 * kM + 16;
 constexpr size_t kSmem = kSmemFloats * 4 + kN * 4 + kM * 8 + kWalkScratch<kNT> * 8 + 16;
 
 __device__ __forceinline__ void store_out(float* o, int64_t i, float4 v) { *reinterpret_cast<float4*>(o + i) = v; }
@@ -61,7 +64,9 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
     float* sc = xs + kN * kXS;
     float* P = sc + kN * 2;
     float* alpha = P + kN * kPS;
-    float* lvs = alpha + kM;
+    float* scale = alpha + kM;   // what a vector's total counts by now
+    float* lost_l = scale + kM;  // what additions of the row sum rounded away
+    float* lvs = lost_l + kM;
     int32_t* prow = reinterpret_cast<int32_t*>(lvs + 16);
     int64_t* lim = reinterpret_cast<int64_t*>(prow + kN);
     int64_t* part = lim + kM;
@@ -83,7 +88,11 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
             const int r = i / kMlaD, d = i - r * kMlaD;
             qs[r * kXS + d] = r < g.rows ? load_q<BF16>(p.q, (g.row0 + r) * kMlaD + d) : 0.0f;
         }
-        if (tid < kM) lim[tid] = tid < g.rows ? row_limit(p, g, tid) : 0;
+        if (tid < kM) {
+            lim[tid] = tid < g.rows ? row_limit(p, g, tid) : 0;
+            scale[tid] = 1.0f;
+            lost_l[tid] = 0.0f;
+        }
         __syncthreads();
         if (TQ4) {
             for (int r = warp; r < kM; r += kNT / 32) {
@@ -104,11 +113,46 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
             __syncthreads();
         }
         float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f}, l_blk[2] = {0.f, 0.f};
-        float o[8][8], o_tot[8][8];
+        float o[8][8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[i][k] = o_tot[i][k] = 0.0f;
+            for (int k = 0; k < 8; ++k) o[i][k] = 0.0f;
+        // totals of the block sums, in the walker's second slot (free until its last segment
+        // ends), and what their additions rounded away
+        float* total = p.ws_o + ((2 * cta + 1) * kM + 8 * cq) * kMlaDV + 4 * cc;
+        float* lost = p.ws_c + (cta * kM + 8 * cq) * kMlaDV + 4 * cc;
+        bool folded = false;
+        // 4 dims d .. of vector i: o into their total (exactly, with `lost`), or the total into o
+        auto fold4 = [&](int i, int d, float* o4, bool back) {
+            float4* to = reinterpret_cast<float4*>(total + i * kMlaDV + d);
+            float4* lo = reinterpret_cast<float4*>(lost + i * kMlaDV + d);
+            const float f = scale[8 * cq + i];
+            float t[4] = {}, c[4] = {};
+            if (folded) {
+                const float4 a = *to, b = *lo;
+                const float va[4] = {a.x, a.y, a.z, a.w}, vb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    t[k] = __fmul_rn(va[k], f);
+                    c[k] = __fmul_rn(vb[k], f);
+                }
+            }
+            if (back) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o4[k] = __fadd_rn(__fadd_rn(o4[k], c[k]), t[k]);
+                return;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float s = __fadd_rn(t[k], o4[k]), part = __fsub_rn(s, t[k]);
+                c[k] = __fadd_rn(c[k], __fadd_rn(__fsub_rn(t[k], __fsub_rn(s, part)), __fsub_rn(o4[k], part)));
+                t[k] = s;
+                o4[k] = 0.0f;
+            }
+            *to = make_float4(t[0], t[1], t[2], t[3]);
+            *lo = make_float4(c[0], c[1], c[2], c[3]);
+        };
         const int64_t end = row_limit(p, g, g.rows - 1);   // rows any vector of the tile sees
         int steps = 0;
         for (int64_t u = g.u0; u < g.u1; ++u) {
@@ -198,21 +242,19 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
                     l_blk[i] = l_blk[i] * a + sum;
                     l_run[i] *= a;
                     m_run[i] = m_new;
-                    if (tx == 0) alpha[2 * ty + i] = a;
+                    if (tx == 0) {
+                        alpha[2 * ty + i] = a;
+                        scale[2 * ty + i] *= a;
+                    }
                 }
             }
             __syncthreads();
             {
-                float al[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) al[i] = alpha[8 * cq + i];
+                float step[8][8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        o[i][k] *= al[i];
-                        o_tot[i][k] *= al[i];
-                    }
+                    for (int k = 0; k < 8; ++k) step[i][k] = 0.0f;
                 for (int t = 0; t < nt; ++t) {
                     const float4 xa = *reinterpret_cast<const float4*>(xs + t * kXS + 4 * cc);
                     const float4 xb = *reinterpret_cast<const float4*>(xs + t * kXS + 256 + 4 * cc);
@@ -227,30 +269,49 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) o[i][k] = fmaf(w[i], x[k], o[i][k]);
+                        for (int k = 0; k < 8; ++k) step[i][k] = fmaf(w[i], x[k], step[i][k]);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float al = alpha[8 * cq + i];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[i][k] = fmaf(o[i][k], al, step[i][k]);
                 }
             }
             if (++steps == kFlush) {
                 steps = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        o_tot[i][k] += o[i][k];
-                        o[i][k] = 0.0f;
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    fold4(i, 0, o[i], false);
+                    fold4(i, 256, o[i] + 4, false);
+                }
+                folded = true;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    l_run[i] += l_blk[i];
+                    const int r = 2 * ty + i;
+                    const float s = __fadd_rn(l_run[i], l_blk[i]), part = __fsub_rn(s, l_run[i]);
+                    const float c = __fmul_rn(lost_l[r], scale[r]) +
+                                    __fadd_rn(__fsub_rn(l_run[i], __fsub_rn(s, part)), __fsub_rn(l_blk[i], part));
+                    __syncwarp();
+                    if (tx == 0) lost_l[r] = c;
+                    l_run[i] = s;
                     l_blk[i] = 0.0f;
                 }
+                __syncthreads();   // every thread has read its scales
+                if (tid < kM) scale[tid] = 1.0f;
             }
             __syncthreads();
         }
         int64_t parts;
         const int64_t slot = walk.slot(g, cta, &parts);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) l_run[i] += l_blk[i];
+        for (int i = 0; i < 2; ++i) l_run[i] += l_blk[i] + lost_l[2 * ty + i] * scale[2 * ty + i];
+        if (folded)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                fold4(i, 0, o[i], true);
+                fold4(i, 256, o[i] + 4, true);
+            }
         if (slot >= 0) {
             if (tx == 0)
 #pragma unroll
@@ -262,10 +323,8 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float* dst = p.ws_o + (slot * kM + 8 * cq + i) * kMlaDV;
-                *reinterpret_cast<float4*>(dst + 4 * cc) = make_float4(o[i][0] + o_tot[i][0], o[i][1] + o_tot[i][1],
-                                                                       o[i][2] + o_tot[i][2], o[i][3] + o_tot[i][3]);
-                *reinterpret_cast<float4*>(dst + 256 + 4 * cc) = make_float4(
-                    o[i][4] + o_tot[i][4], o[i][5] + o_tot[i][5], o[i][6] + o_tot[i][6], o[i][7] + o_tot[i][7]);
+                *reinterpret_cast<float4*>(dst + 4 * cc) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                *reinterpret_cast<float4*>(dst + 256 + 4 * cc) = make_float4(o[i][4], o[i][5], o[i][6], o[i][7]);
             }
             if (parts > 0 && tid == 0) {
                 p.ws_desc[cta * 4] = parts;
@@ -285,7 +344,7 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
             const float f = alpha[r];
             float v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = (o[i][k] + o_tot[i][k]) * f;
+            for (int k = 0; k < 8; ++k) v[k] = o[i][k] * f;
             const float4 a = make_float4(v[0], v[1], v[2], v[3]), b = make_float4(v[4], v[5], v[6], v[7]);
             if (TQ4) {
                 *reinterpret_cast<float4*>(qs + r * kXS + 4 * cc) = a;
@@ -423,7 +482,7 @@ constexpr int64_t state_rows(bool tensor) {
 
 size_t paged_workspace_bytes(bool tensor) {
     return kWsHeader + (size_t)kPagedCtas * 4 * sizeof(int64_t) + (size_t)state_rows(tensor) * (kMlaDV + 2) * sizeof(float) +
-           (tensor ? (size_t)kPagedCtas * 256 * sizeof(float2) : 0);
+           (tensor ? (size_t)kPagedCtas * 256 * sizeof(float2) : (size_t)kPagedCtas * kM * kMlaDV * sizeof(float));
 }
 
 cudaError_t launch_attn_paged(kvq_format fmt, const kvq_mla_layout& L, bool tensor, const void* q, kvq_dtype dt,
@@ -456,7 +515,8 @@ cudaError_t launch_attn_paged(kvq_format fmt, const kvq_mla_layout& L, bool tens
     p.ws_desc = reinterpret_cast<int64_t*>(ws + kWsHeader);
     p.ws_o = reinterpret_cast<float*>(ws + kWsHeader + (size_t)kPagedCtas * 4 * sizeof(int64_t));
     p.ws_ml = p.ws_o + state_rows(tensor) * kMlaDV;
-    p.ws_l = reinterpret_cast<float2*>(p.ws_ml + state_rows(tensor) * 2);
+    p.ws_c = p.ws_ml + state_rows(tensor) * 2;
+    p.ws_l = reinterpret_cast<float2*>(p.ws_c);
     if (fmt == KVQ_TQ4) {
         p.signs = tq4_sign_words(L);
         p.kn[0] = (float)(1.0 / sqrt((double)L.block_dim[0]));

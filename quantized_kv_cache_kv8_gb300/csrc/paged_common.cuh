@@ -48,6 +48,7 @@ struct PagedParams {
     float* ws_ml;              // [2 * CTAs][M][2]
     int64_t* ws_desc;          // [CTAs][4]: parts, first query vector, vectors
     float2* ws_l;              // tensor kernel: [CTAs][256 threads], totals of long sums
+    float* ws_c;               // exact kernel: [CTAs][M][512], what the totals rounded away
     SignWords signs;
     float kn[2];
     float lv[16];

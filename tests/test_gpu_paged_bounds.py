@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from gpu_common import TENSOR_TOL, to_dev
+from gpu_common import SIMT_TOL, TENSOR_TOL, to_dev
 from quantized_kv_cache_kv8_gb300 import synth
 from test_gpu_paged import BF16_STEP, SM, kvq  # noqa: F401
 
@@ -31,8 +31,9 @@ def copies(kvq, oracle, fmt, x, seed, order, page=64):
 
 def attend(kvq, fmt, q, layout, codes, scales, table, n_rows, page=64):
     n, H = q.shape[:2]
-    out = torch.full((n, H, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
-    ws = torch.zeros(kvq.kv_attn_paged_workspace_size(fmt, 1, H, n, layout), dtype=torch.uint8, device="cuda")
+    out = torch.full((n, H, 512), float("nan"), dtype=q.dtype, device="cuda")
+    size = kvq.kv_attn_paged_workspace_size(fmt, 1, H, n, layout, bf16=q.dtype == torch.bfloat16)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
     kvq.kv_attn_paged(fmt, q, to_dev(np.array([0, n])), codes, scales, table, to_dev(np.array([n_rows])), page, out, ws, SM,
                       layout)
     assert kvq.read_device_error(ws) == 0
@@ -71,24 +72,30 @@ def test_query_keeps_its_bits(kvq, oracle, fmt):  # noqa: F811
 ORDERS = {"falling": lambda order, rng: order, "rising": lambda order, rng: order[::-1], "mixed": lambda order, rng: rng.permutation(order)}
 
 
-def check_kinds(kvq, oracle, fmt, binades, counts, order):  # noqa: F811
-    """Rows of a few kinds whose scores lie `binades` apart; each kind has dims of its own, so that an output shows what
-    the kind weighs.  80 tiles of 128 heads: a walker has nearly all rows of a tile.  Outputs within 2e-3 of the largest,
-    their rounding to bf16 (2^-8 of the value) aside."""
-    H, n, seed = 128, 80, 3
+def kinds_of(kvq, oracle, fmt, binades, counts, order, H, seed):  # noqa: F811
+    """Rows of a few kinds, each with dims of its own, so that an output shows what the kind weighs, and queries for which
+    their scores lie `binades` apart, times 0.9 to 1.1."""
     rng = np.random.default_rng(seed)
     kinds = len(binades)
     x = 0.3 * rng.standard_normal((kinds, 576)).astype(np.float32)
     for k in range(kinds):
         x[k, 64 * (k + 1):64 * (k + 2)] += 2.0
     kind = ORDERS[order](np.repeat(np.arange(kinds), counts), rng)
-    T = len(kind)
     layout, codes, scales, table, xh = copies(kvq, oracle, fmt, x, seed, kind)
-    # queries: a random one for each head, moved so that the kinds' scores lie as asked, times 0.9 to 1.1
     q = rng.standard_normal((H, 576))
     goal = np.outer(np.linspace(0.9, 1.1, H), np.array(binades) * math.log(2.0) / SM)
     steps = xh[1:] - xh[0]
     q += np.linalg.solve(steps @ steps.T, (goal[:, 1:] - goal[:, :1] - q @ steps.T).T).T @ steps
+    return layout, codes, scales, table, xh, kind, q
+
+
+def check_kinds(kvq, oracle, fmt, binades, counts, order):  # noqa: F811
+    """80 tiles of 128 heads: a walker has nearly all rows of a tile.  Outputs within 2e-3 of the largest, their rounding to
+    bf16 (2^-8 of the value) aside."""
+    H, n, seed = 128, 80, 3
+    kinds = len(binades)
+    layout, codes, scales, table, xh, kind, q = kinds_of(kvq, oracle, fmt, binades, counts, order, H, seed)
+    T = len(kind)
     q = torch.from_numpy(q).bfloat16()
     out = attend(kvq, fmt, q.expand(n, H, 576).contiguous().cuda(), layout, codes, scales, table, T)
     z = q.double().numpy() @ xh.T * SM
@@ -101,6 +108,28 @@ def check_kinds(kvq, oracle, fmt, binades, counts, order):  # noqa: F811
         top = TENSOR_TOL * np.abs(ref).max(1, keepdims=True)
         worst = max(worst, float((np.abs(out[i] - ref) / (top + BF16_STEP * (np.abs(ref) + top))).max()))
     assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("binades,counts,order", [
+    ([0, -20.5], [1, 131071], "falling"), ([0, -9, -18], [1, 700, 130000], "falling"), ([0, 0], [1 << 16, 1 << 16], "mixed"),
+    ([0, -17], [33, 131039], "mixed"), ([0, 0], [5, (1 << 20) - 5], "mixed"),
+])
+def test_exact_path_keeps_its_bound(kvq, oracle, fmt, binades, counts, order):  # noqa: F811
+    """The same on the exact path with f32 queries: 1e-5 of the largest output, with rows whose roundings all point one
+    way."""
+    H, n, seed = 32, 6, 3
+    layout, codes, scales, table, xh, kind, q = kinds_of(kvq, oracle, fmt, binades, counts, order, H, seed)
+    T = len(kind)
+    q = torch.from_numpy(q).float()
+    out = attend(kvq, fmt, q.expand(n, H, 576).contiguous().cuda(), layout, codes, scales, table, T)
+    z = q.double().numpy() @ xh.T * SM
+    w = np.exp(z - z.max(1, keepdims=True))
+    for i in range(n):
+        m = w * np.bincount(kind[:T - n + i + 1], minlength=len(binades))
+        ref = (m / m.sum(1, keepdims=True)) @ xh[:, :512]
+        e = np.abs(out[i] - ref).max(1) / np.abs(ref).max(1)
+        assert e.max() <= SIMT_TOL, (i, int(e.argmax()), float(e.max()))
 
 
 @pytest.mark.parametrize("fmt", [1, 2])
