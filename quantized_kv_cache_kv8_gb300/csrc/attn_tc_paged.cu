@@ -79,14 +79,14 @@
 // until its last segment ends), and the next product starts from zero (1 to 2% of a long
 // walk).
 //
-// What bounds it.  KV8, many rows a tile: the softmax warps, 3,350 cycles a step (scores
-// 1,350, vote 290, exponentials 600, weights 450, the rest hand-overs) for 2,200 of
-// products: 512 tokens on 32,768 rows x 128 heads 3.1 ms, 1,500 TFLOP/s; 32 sequences of
-// 1,024 to 131,072 rows 356 us.  TQ4: the decode warps' integer work and shared
-// memory, which the products of two query halves keep busy, 7,500 a step (256 tokens on
-// 16,384 rows 1.70 ms, 690 TFLOP/s).  Short tiles: rotation of queries and
-// outputs (TQ4, 777 tokens without rows before 314 us), and the start (6k cycles), the
-// queries (8k) and the partial results (6k) of a decode step (8 x 4096 rows 26.7 us).
+// What bounds it.  KV8, many rows a tile: the softmax warps, some 3,450 cycles a step (scores
+// 1,350, vote 290, exponentials 600, weights 500, the rest hand-overs) for 2,200 of
+// products: 512 tokens on 32,768 rows x 128 heads 3.2 ms, 1,470 TFLOP/s; 32 sequences of
+// 1,024 to 131,072 rows 360 us.  TQ4: the hand-over of the fills, 7,700 a step for 3,350
+// of products; no pipe is full (integer 46%, tensor 44%, issue slots 41%; 256 tokens on
+// 16,384 rows 1.78 ms, 660 TFLOP/s).  Short tiles: rotation of queries and
+// outputs (TQ4, 777 tokens without rows before 319 us), and the start (6k cycles), the
+// queries (8k) and the partial results (6k) of a decode step (8 x 4096 rows 27.1 us).
 #include "tc_common.cuh"
 #include "paged_common.cuh"
 
@@ -108,8 +108,8 @@ constexpr int kIssueWarp = kSoftWarps + kDecWarps, kWalkWarp = kIssueWarp + 1, k
 constexpr int kThreads = kSoft + kDec + 128;   // five warpgroups
 // Registers a thread after the split.  KV8: the decode warps hold half the codes
 // (none of the score rows), and the softmax keeps a step's latent scales between scores
-// and weights instead of reading them twice (512 tokens on 32,768 rows x 128 heads
-// 3.16 ms, 3.25 with 112 and 96).
+// and weights instead of reading them twice (32 sequences of 1,024 to 131,072 rows 360 us,
+// 368 with 112 and 96 registers).
 template <bool TQ4>
 struct Regs {
     static constexpr int kLaunch = 96, kSoftmax = TQ4 ? 88 : 120, kDecode = TQ4 ? 120 : 88, kRest = 64;
@@ -350,8 +350,7 @@ __device__ __forceinline__ void store_codes(unsigned char* chunk, const uint4& c
 __device__ __forceinline__ void store_levels(unsigned char* chunk, uint32_t codes, int row, int unit, const Planes& t) {
     const uint32_t neg = ~codes & 0x88888888u, even = neg << 4;   // signs in bit 7 of a byte: odd codes, even codes
     // 7/8 of it, 7 in each code below 8, by a high product: the integer pipe is the
-    // busy one (with one query half: 256 tokens on 16,384 rows 1.51 ms, 1.57 with a
-    // shift and a difference)
+    // busiest one (256 tokens on 16,384 rows 1.78 ms, 1.80 with a shift and a difference)
     const uint32_t sel = (codes & 0x77777777u) ^ __umulhi(neg, 0xe0000000u);
     uint32_t w[4];
 #pragma unroll
@@ -1598,10 +1597,11 @@ cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
     if (!TQ4 && p.n_pages > 0 && (e = pool_map(p, &map)) != cudaSuccess) return e;
     e = cudaFuncSetAttribute(paged_tensor_kernel<TQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemUsed);
     if (e != cudaSuccess) return e;
-    // Launched while its predecessor runs, the kernel is there 3.5 us sooner (8 sequences
-    // of 4096 rows 29.8 us a call, 33.4 else) but then runs 5% slower (512 tokens on
-    // 32,768 rows 3.35 ms, 3.18 else): for short calls, of at most some 60 us, by the most
-    // steps that a pair can have.
+    // Launched while its predecessor runs, the kernel is there sooner (8 sequences of 4096
+    // rows 27.1 us in a replayed graph, 28.2 else) but then runs 6% slower, for a reason not
+    // known (512 tokens on 32,768 rows 3.41 ms, 3.2 else): for short calls, of at most some
+    // 60 us, by the most steps that a pair can have.  The table's width bounds those, so a
+    // table kept wide for the longest context is launched the other way.
     const int64_t tiles = p.max_tok * p.n_heads / kVecs + min(p.max_tok, (int64_t)p.n_seq);
     const int64_t rows = (int64_t)min(p.table_stride, p.n_pages) << p.shift;
     if (tiles * (rows / kRows + 1) <= 32 * kPagedPairs)

@@ -321,8 +321,8 @@ __device__ __forceinline__ float2 row_scales(float latent, float rope) {
 // The exact (fp32) kernel and the tensor-core kernel: query vectors a tile,
 // rows a step, prologue allowance in steps (the exact kernel: 16 sequences of 60 to
 // 1000 rows x 32 heads 44 us with 4, 46 with 2, 59 with 8; the tensor kernel: first
-// chunk of 777 in 4 bits 269 us with 4, 299 with 2, 284 with 6, mixed 24 sequences
-// 216, 226, 213); CTAs, and pairs of CTAs, that walk.
+// chunk of 777 in 4 bits 320 us with 4, 362 with 2, 341 with 6, mixed 24 sequences
+// 206, 218, 211); CTAs, and pairs of CTAs, that walk.
 using PagedSimt = SchedOf<32, 32, 4>;
 using PagedTensor = SchedOf<128, 128, 4>;
 constexpr int kPagedCtas = 152, kPagedPairs = 76;

@@ -5,13 +5,13 @@
 // Pair i of the rotary dims turns by the angle pos[axis_i] * w_i, w_i the pair's
 // inverse frequency: (u, v) -> (u cos - v sin, v cos + u sin).  An angle in f32
 // is wrong by 2^-24 of its own size (0.06 rad at position 10^6), so the phase
-// is kept in turns as a 64-bit fraction: inc_i = round(w_i / 2 pi * 2^64) on
-// the host, pos * inc_i mod 2^64 on the device, exact but for the rounding of
-// inc_i (2^-53 of w_i); its signed value over 2^63 goes to sincospi in f32.
+// is kept in turns as a 64-bit fraction: inc_i = w_i / 2 pi * 2^64 on the host,
+// whole turns dropped, pos * inc_i mod 2^64 on the device, exact but for the rounding of
+// inc_i (2^-53 of w_i, and down to a multiple of 2^-64 turns); its signed value over 2^63 goes to sincospi in f32.
 //
 // What bounds it: memory, 128 bytes of query in and out per head (2048 tokens
-// x 128 heads: 67 MB, 10 us at 6.8 TB/s; measured 14.3 us, 5.0 TB/s); a decode step
-// only its latency (8 tokens 4.8 us).  The
+// x 128 heads: 67 MB, 10 us at 6.8 TB/s; measured 14.3 us, 5.0 TB/s, and what keeps it
+// from the rest is not known); a decode step only its latency (8 tokens 4.9 us).  The
 // cos and sin of a token are shared by its heads, so a CTA tabulates them in
 // shared memory for the tokens it serves and then runs through its share of
 // the (token, head, 16 bytes) units.  Rows take a warp each, in CTAs of their
@@ -273,8 +273,8 @@ cudaError_t launch_rope_append(kvq_format fmt, const kvq_mla_layout& L, const kv
     if (n_heads > 0) {
         const int64_t unit_pairs = !vec ? 1 : adjacent ? v / 2 : v;
         p.per_tok = (int32_t)(n_heads * (p.pairs / unit_pairs));
-        // 2 units a thread once that fills the GPU (2048 tokens x 128 heads: 14.6 us,
-        // 4.8 TB/s in pieces of 128 bytes; 4 units 15.2, one 17.4)
+        // 2 units a thread once that fills the GPU (2048 tokens x 128 heads: 14.3 us,
+        // 4 units 15.2, one 17.4)
         int64_t per = 2 * kNT;
         while (per > kNT && n * p.per_tok < per * 304) per /= 2;
         p.per_cta = (int32_t)std::min<int64_t>(per, (int64_t)p.per_tok * (kSpan - 2));
