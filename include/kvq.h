@@ -540,7 +540,8 @@ int32_t kvq_read_device_error(void* workspace, int32_t clear, void* stream);
  * first of a work item took the exact path of the lagged running maxima (a
  * score passing the running reference by more than the lag: column maxima,
  * then the context accumulator rescaled in tensor memory) since the counter
- * was last cleared; kv_attn_paged counts them per 32 query vectors.  The
+ * was last cleared; kv_attn_paged counts them per 32 query vectors, and with them
+ * the steps that bring the reference of too small weights down.  The
  * counter is bytes 16..19 of an attention workspace (zero in a zeroed workspace;
  * wraps at 2^32).  Synchronizes
  * `stream`; clears the counter when `clear` is non-zero.  Returns -1 for a

@@ -1406,13 +1406,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (aborted || t == steps) break;
                 // ---- the next product starts from zero ----
-                if (!warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)) {
+                // (a wait that runs out in one warp alone is told to the others by the next vote:
+                // warps that part here would wait for one another at different barriers)
+                if (warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)) {
+                    tc_after();
+                    fold_sums(p, pair, rank, tmem + lane_base + kColO + 128 * sub, st.l, t == kFold);
+                    st.l = 0.0f;
+                } else {
                     aborted = true;
-                    break;
                 }
-                tc_after();
-                fold_sums(p, pair, rank, tmem + lane_base + kColO + 128 * sub, st.l, t == kFold);
-                st.l = 0.0f;
             }
             // ---- output ----
             if (!aborted && !warp_wait(&bars[kBarCtx0 + 1], (it - 1) & 1u, sAbort, wl)) aborted = true;
