@@ -496,9 +496,11 @@ size_t kv_attn_paged_workspace_size(kvq_format fmt, const kvq_mla_layout* layout
  * Layouts as kv_attn_decode.  KVQ_PATH_SIMT (AUTO with f32 queries): f32, within
  * 1e-5 before the rounding to q_dtype.  KVQ_PATH_TENSOR (AUTO with bf16 queries):
  * bf16 queries only, f32 accumulation, within 2e-3 of exact before the rounding to
- * bf16, but for what the query's own rounding adds.  KV8: query elements keep their 8
+ * bf16, but for what the operands' own rounding adds.  KV8: query elements keep their 8
  * bits down to 2^-9 of the vector's largest; smaller ones are off by at most 2^-17 of
- * it.  TQ4: the rotated query is held in two f16 values, to 2^-22 of each element.
+ * it.  TQ4: the rotated query is held in two f16 values, to 2^-22 of each element, the
+ * levels in one, to 9.3e-5 of themselves (as in the contiguous calls), which moves a score
+ * by about 6e-5 sm_scale (sum_i (q'_i x'_i)^2)^(1/2): the 2e-3 are for scores of some tens.
  * A row with a NaN code, or a scale that is no finite number, makes NaN the tokens
  * that see it and leaves the others as they are.  Invalid lengths or offsets and
  * pages outside [0, n_pages) set KVQ_ERR_ARG in the workspace's device word; nothing

@@ -9,7 +9,7 @@ import torch
 
 from gpu_common import SIMT_TOL, TENSOR_TOL, to_dev
 from quantized_kv_cache_kv8_gb300 import synth
-from test_gpu_paged import BF16_STEP, SM, kvq  # noqa: F401
+from test_gpu_paged import BF16_STEP, SM, Paged, kvq, query  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -148,6 +148,26 @@ def test_long_sums(kvq, oracle, fmt, counts):  # noqa: F811
 def test_many_small_weights_add_up(kvq, oracle, fmt, binades, counts, order):  # noqa: F811
     """One kind outweighs another by many binades, but for the number of its rows."""
     check_kinds(kvq, oracle, fmt, binades, counts, order)
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+def test_long_walks_over_different_rows(kvq, oracle, fmt):  # noqa: F811
+    """70,000 rows and 80 tiles, so that walkers fold their sums twice and their references move in between; some of the
+    vectors against f64."""
+    T, n, H = 70000, 80, 128
+    p = Paged(kvq, oracle, fmt, [T - n], [n], 64, seed=9)
+    q = query(n, H, 9, True)
+    out = p.run(q, 0)
+    assert p.err == 0
+    rows = torch.from_numpy(p.xh[0]).cuda()
+    rng = np.random.default_rng(1)
+    for i in np.concatenate([[0, n - 1], rng.integers(0, n, 30)]):
+        heads = torch.from_numpy(rng.integers(0, H, 16)).cuda()
+        K = rows[:T - n + int(i) + 1]
+        ref = torch.softmax(q[int(i), heads].double() @ K.T * SM, -1) @ K[:, :512]
+        top = TENSOR_TOL * ref.abs().amax(1, keepdim=True)
+        ratio = (out[int(i), heads].double() - ref).abs() / (top + BF16_STEP * (ref.abs() + top))
+        assert float(ratio.max()) <= 1.0, (int(i), float(ratio.max()))
 
 
 @pytest.mark.parametrize("fmt", [1, 2])
