@@ -384,7 +384,7 @@ kvq_status kv_attn_prefill(kvq_format fmt, const kvq_mla_layout* layout,
  *
  * page_rows is a power of two (pages: 1 .. 65536, attention: 16 .. 65536), and
  * n_pages * page_rows at most 2^31 - 1.  Rows are of the formats KVQ_KV8 and
- * KVQ_TQ4.  block_table is int32 [n_seq][table_stride].  A sequence appears once
+ * KVQ_TQ4 (pools with grouped query heads: below).  block_table is int32 [n_seq][table_stride].  A sequence appears once
  * in a batch.  Attention only reads, so sequences may list the same page there (a
  * shared prefix); the stack of free pages knows no counts, so such a page is given
  * back by one of them alone, and no new row goes into it.  A workspace serves one
@@ -512,10 +512,152 @@ kvq_status kv_attn_paged(kvq_format fmt, const kvq_mla_layout* layout, const voi
                          float sm_scale, void* out, void* workspace, size_t workspace_bytes, kvq_path path,
                          void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Paged KV8 pools with grouped query heads                                 */
+/* ------------------------------------------------------------------------ */
+
+/* A model with separate keys and values keeps, per token and key-value head, a
+ * row of head_dim keys and one of head_dim values, each as e4m3 codes with one
+ * f32 scale (amax / 448, the rule of kv8_encode), in the pages of a pool:
+ *   k_codes, v_codes  [n_pages][n_kv_heads][page_rows][head_dim] bytes
+ *   scales            [n_pages][n_kv_heads][page_rows][2] f32 (key, value)
+ * 2 * head_dim + 8 bytes a row and head.  Pages, tables, slots and lengths are those
+ * of kv_pages_reserve and kv_pages_trim; slot = page * page_rows + place.  head_dim is
+ * 64, 128 or 256, n_heads a multiple of n_kv_heads; query head h reads kv head
+ * h / (n_heads / n_kv_heads).  page_rows: a power of two, 16 .. 65536.  Pools are
+ * 16-byte aligned, other pointers to their elements. */
+
+/* One step's producer, one launch: rotates the leading rope->dim dims of every
+ * query and key head (rotation and angles as kv_rope_append; there the trailing dims
+ * of a latent row), encodes the rotated keys and the values and stores them.
+ *   rope         NULL: no rotation (an encoder's states); dim at most head_dim
+ *   k_new, v_new [n][n_kv_heads][head_dim] in dtype, strides in elements; both NULL:
+ *                only queries
+ *   positions    [n_axes][n] int64, axis stride pos_stride; unused without rope
+ *   slot_map     [n] int64, as kv_rope_append; unused without k_new
+ *   q_in, q_out  [n][n_heads][head_dim] in dtype; q_in itself (same strides)
+ *                rotates in place, no other overlap; n_heads = 0: only rows.  With both
+ *                queries and rows n_heads must be a multiple of n_kv_heads
+ *   err_word     NULL, or a device int32 error word
+ * A row with a NaN or an infinity is stored with a scale of NaN and codes 0 and sets
+ * KVQ_ERR_NONFINITE: tokens that see it yield NaN.  Any alignment of element size;
+ * 16-byte aligned rows move fastest.  The same slot twice leaves one of the rows'
+ * bytes or a mixture. */
+kvq_status kv_gqa_append(const kvq_rope* rope, kvq_dtype dtype, int64_t n, int32_t n_heads, int32_t n_kv_heads,
+                         int32_t head_dim, const void* k_new, int64_t k_token, int64_t k_head, const void* v_new,
+                         int64_t v_token, int64_t v_head, const int64_t* positions, int64_t pos_stride,
+                         const int64_t* slot_map, const void* q_in, int64_t q_in_token, int64_t q_in_head,
+                         void* q_out, int64_t q_out_token, int64_t q_out_head, uint8_t* k_codes, uint8_t* v_codes,
+                         float* scales, int32_t page_rows, int32_t n_pages, int32_t* err_word, void* stream);
+
+/* Bytes of workspace kv_gqa_attn_paged needs: one size for every batch and page
+ * size.  0 for what the call would refuse. */
+size_t kv_gqa_attn_paged_workspace_size(kvq_dtype q_dtype, int32_t n_seq, int32_t n_heads, int32_t n_kv_heads,
+                                        int32_t head_dim, int64_t n_tokens);
+
+/* Attention of new tokens over paged keys and values.  Token i of sequence b
+ * (i < n = cu_q[b+1] - cu_q[b]) attends
+ *   causal != 0   rows [0, kv_lens[b] - n + i], its own the last of them: a decode
+ *                 step, a window of speculative tokens, a prompt's chunk, any mixture
+ *   causal == 0   all kv_lens[b] rows: cross attention to an encoder's states, whose
+ *                 number has nothing to do with n (several beams of a request are
+ *                 tokens of one sequence here and share its rows)
+ *   z_t = sm_scale (q . k_t),  out = sum_t softmax(z)_t v_t
+ * A token that sees no row yields zeros.
+ *   q, out       [n_tokens][n_heads][head_dim] in q_dtype
+ *   cu_q         [n_seq + 1] int64, non-decreasing, cu_q[n_seq] <= n_tokens; rows of out
+ *                behind cu_q[n_seq] are left as they are
+ *   kv_lens      [n_seq] int64, at most min(table_stride, n_pages) * page_rows
+ * Products take 16-bit operands, the weights of a row (and f32 queries) in two of
+ * them, sums are f32: outputs are within 1e-5 of a vector's largest before the rounding to
+ * q_dtype, but for what f32 scores of some hundreds lose.  A row with a NaN code, or a scale that
+ * is no finite number, makes NaN the tokens that see it and leaves the others as they are.  Invalid
+ * lengths or offsets and pages outside [0, n_pages) set KVQ_ERR_ARG in the workspace's
+ * device word; nothing outside the pool is read.  q, out, pools and workspace are 16-byte
+ * aligned.  The workspace starts zeroed; calls leave it ready for the next. */
+kvq_status kv_gqa_attn_paged(const void* q, kvq_dtype q_dtype, int64_t n_tokens, int32_t n_heads, int32_t n_kv_heads,
+                             int32_t head_dim, int32_t n_seq, const int64_t* cu_q, const uint8_t* k_codes,
+                             const uint8_t* v_codes, const float* scales, const int32_t* block_table,
+                             int32_t table_stride, const int64_t* kv_lens, int32_t page_rows, int32_t n_pages,
+                             float sm_scale, int32_t causal, void* out, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Beam search over paged caches                                            */
+/* ------------------------------------------------------------------------ */
+
+/* A request's beams are consecutive sequences of a batch: beam b of request s is
+ * sequence s * n_beams + b.  After a step's logits,
+ *   kv_beam_select   the best continuations: scores, parent sequences, tokens
+ *   kv_pages_fork    block tables and lengths follow the parents (of the chosen ones)
+ *   kv_pages_copy    the pages in progress that several children continue
+ * and the next step's kv_pages_reserve appends as usual.  The tables serve any pool
+ * (latent rows or grouped heads). */
+
+/* Bytes of workspace kv_beam_select needs; 0 for what it would refuse. */
+size_t kv_beam_workspace_size(int32_t n_seq, int32_t n_beams, int64_t vocab, int32_t keep);
+
+/* For every request the `keep` best pairs of a beam b and a token v by
+ *   scores[s][b] + x_v - log sum_w exp(x_w),  x = logits[s][b],
+ * best first; ties go to the lower beam, within a beam to the larger logit, then to the
+ * lower token.
+ *   logits      [n_seq * n_beams][vocab] f32 or bf16, rows row_stride elements apart.  A
+ *               logit of -inf, or NaN, is a token that may not come; the mass of a row with
+ *               infinite logits is shared among those
+ *   scores      [n_seq][n_beams] f32; a beam whose score is not finite has no continuation
+ *   out_scores  [n_seq][keep] f32
+ *   parents     [n_seq][keep] int32: s * n_beams + b
+ *   tokens      [n_seq][keep] int32
+ * Where a request has fewer continuations the rest are -inf, -1, -1.  n_beams 1 .. 32,
+ * keep 1 .. 64, vocab 1 .. 2^31 - 1.  The workspace starts zeroed; calls leave it ready for
+ * the next.  No output may overlap an input. */
+kvq_status kv_beam_select(const void* logits, kvq_dtype dtype, int64_t row_stride, int32_t n_seq, int32_t n_beams,
+                          int64_t vocab, const float* scores, int32_t keep, float* out_scores, int32_t* parents,
+                          int32_t* tokens, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace kv_pages_fork needs: the error word, a mark per page (zero
+ * before the first call; each call leaves them so) and the new table. */
+size_t kv_pages_fork_workspace_size(int32_t n_seq, int32_t table_stride, int32_t n_pages);
+
+/* Sequence i continues the rows of sequence parents[i]; -1 ends it (length 0).
+ * Full pages are listed by all children of a sequence.  The page in progress (of
+ * kv_lens mod page_rows rows) stays with the first child, every other child takes a
+ * page from the top of the stack, in sequence order, and an entry of `copies`.  Pages
+ * that no sequence holds any more go onto the stack, in the order of (sequence, page)
+ * from the top, each at the first sequence that held it.
+ *   parents      [n_seq] int32, -1 .. n_seq - 1
+ *   kv_lens      [n_seq] int64, updated
+ *   block_table  [n_seq][table_stride], the entries of each sequence's pages updated, the
+ *                others kept
+ *   free_pages   int32 [n_pages], n_free int32 [1]: the stack
+ *   copies       [n_seq][2] int32: (from, to) of sequence i, or (-1, -1)
+ * The batch holds every sequence that lists one of its pages, each page at most once a
+ * sequence, and a page in progress is listed by one.  All or nothing: with too few free pages (device
+ * word KVQ_ERR_WORKSPACE), or an invalid parent, length, page or free count
+ * (KVQ_ERR_ARG), nothing changes and copies are -1.  Pages that are shared are given
+ * back here (parent -1), not by kv_pages_trim, which may cut a sequence back within the pages it holds alone.
+ * n_seq up to 4096, n_seq * table_stride below 2^31. */
+kvq_status kv_pages_fork(int32_t n_seq, int32_t page_rows, const int32_t* parents, int64_t* kv_lens,
+                         int32_t* block_table, int32_t table_stride, int32_t* free_pages, int32_t* n_free,
+                         int32_t n_pages, int32_t* copies, void* workspace, size_t workspace_bytes, void* stream);
+
+/* A pool of pages of page_bytes consecutive bytes: codes or scales of one layer. */
+typedef struct kvq_pool {
+    void* data;
+    int64_t page_bytes;
+} kvq_pool;
+
+/* Copies page copies[i][0] to page copies[i][1] in every pool, for i < n; entries with a
+ * negative page are skipped, pages outside [0, n_pages) skipped and KVQ_ERR_ARG set in
+ * err_word (NULL or a device int32 error word).  `pools` is read on the host, any number of
+ * them.  No page may be both copied from and copied to.  16-byte aligned pages move fastest. */
+kvq_status kv_pages_copy(int32_t n, const int32_t* copies, int32_t n_pages, int32_t n_pools, const kvq_pool* pools,
+                         int32_t* err_word, void* stream);
+
 /* Opt-in launch timing, for kernel-level rooflines (instrumentation, not part
  * of the pages' method).  With capacity > 0, every kv_attn_decode,
- * kv_attn_decode_append, kv_attn_decode_gather, kv_attn_prefill, kv_attn_paged
- * and kv_attn_decode_k2v4 call records three CUDA events on its stream -- before
+ * kv_attn_decode_append, kv_attn_decode_gather, kv_attn_prefill, kv_attn_paged,
+ * kv_gqa_attn_paged and kv_attn_decode_k2v4 call records three CUDA events on its stream -- before
  * its partial kernel, before its merge, after its merge -- into the next of
  * `capacity` slots (a ring: older calls are overwritten); capacity 0 turns it
  * off and frees the events.  The record between the two kernels ends the

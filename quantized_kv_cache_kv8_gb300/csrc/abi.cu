@@ -4,6 +4,7 @@
 // failed check returns a status and launches nothing.  No call allocates or
 // frees device memory.
 #include "kvq_internal.cuh"
+#include "gqa.cuh"
 #include "paged.cuh"
 #include "pq_common.cuh"
 
@@ -556,6 +557,148 @@ kvq_status kv_attn_paged(kvq_format fmt, const kvq_mla_layout* layout, const voi
     return cuda_status(launch_attn_paged(fmt, *layout, tensor, q, q_dtype, n_tokens, n_heads, n_seq, cu_q, codes,
                                          scales, block_table, table_stride, kv_lens, page_rows, n_pages, sm_scale, out,
                                          workspace, (cudaStream_t)stream));
+}
+
+// Heads of a grouped-query pool.
+static kvq_status check_gqa(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
+    if (n_heads < 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0) return KVQ_ERR_ARG;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return KVQ_ERR_UNSUPPORTED;
+    if (n_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+    return KVQ_OK;
+}
+
+kvq_status kv_gqa_append(const kvq_rope* rope, kvq_dtype dtype, int64_t n, int32_t n_heads, int32_t n_kv_heads,
+                         int32_t head_dim, const void* k_new, int64_t k_token, int64_t k_head, const void* v_new,
+                         int64_t v_token, int64_t v_head, const int64_t* positions, int64_t pos_stride,
+                         const int64_t* slot_map, const void* q_in, int64_t q_in_token, int64_t q_in_head,
+                         void* q_out, int64_t q_out_token, int64_t q_out_head, uint8_t* k_codes, uint8_t* v_codes,
+                         float* scales, int32_t page_rows, int32_t n_pages, int32_t* err_word, void* stream) {
+    if (!k_new != !v_new) return KVQ_ERR_ARG;
+    kvq_status s = check_gqa(n_heads, k_new ? n_kv_heads : 1, head_dim);
+    if (s != KVQ_OK) return s;
+    if (n_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+    if (dtype != KVQ_F32 && dtype != KVQ_BF16) return KVQ_ERR_ARG;
+    if (k_new && (s = check_pages(0, page_rows, 0, n_pages, 16)) != KVQ_OK) return s;
+    if (rope) {
+        if (rope->dim <= 0 || rope->dim % 2 != 0 || rope->n_axes < 1) return KVQ_ERR_ARG;
+        if (rope->dim > 128 || rope->n_axes > 4) return KVQ_ERR_UNSUPPORTED;
+        if (rope->dim > head_dim) return KVQ_ERR_ARG;
+        for (int i = 0; i < rope->dim / 2; ++i)
+            if (rope->axis[i] >= rope->n_axes || !isfinite(rope->inv_freq[i])) return KVQ_ERR_ARG;
+    }
+    if (n < 0) return KVQ_ERR_ARG;
+    if (n > 0x7fffffff) return KVQ_ERR_UNSUPPORTED;
+    if (n == 0 || (!k_new && n_heads == 0)) return KVQ_OK;
+    if (rope && (!positions || (rope->n_axes > 1 && pos_stride < n))) return KVQ_ERR_ARG;
+    if (k_new && (!slot_map || (n_pages > 0 && (!k_codes || !v_codes || !scales)))) return KVQ_ERR_ARG;
+    if (n_heads > 0 && (!q_in || !q_out)) return KVQ_ERR_ARG;
+    const uintptr_t size = dtype == KVQ_BF16 ? 2 : 4;
+    if (!aligned(k_new, size) || !aligned(v_new, size) || !aligned(q_in, size) || !aligned(q_out, size) ||
+        !aligned(positions, 8) || !aligned(slot_map, 8) || !aligned(k_codes, 16) || !aligned(v_codes, 16) ||
+        !aligned(scales, 16) || !aligned(err_word, 4))
+        return KVQ_ERR_ARG;
+    if (n_heads > 0 && q_in == q_out && (q_in_token != q_out_token || q_in_head != q_out_head)) return KVQ_ERR_ARG;
+    if ((n_heads > 1 && q_out_head == 0) || (n_heads > 0 && n > 1 && q_out_token == 0)) return KVQ_ERR_ARG;
+    GqaAppendCall c{rope, dtype, n, n_heads, n_kv_heads, head_dim, k_new, k_token, k_head, v_new, v_token, v_head,
+                    positions, pos_stride, slot_map, q_in, q_in_token, q_in_head, q_out, q_out_token, q_out_head,
+                    k_codes, v_codes, scales, k_new ? page_rows : 1, k_new ? n_pages : 0, err_word};
+    return cuda_status(launch_gqa_append(c, (cudaStream_t)stream));
+}
+
+size_t kv_gqa_attn_paged_workspace_size(kvq_dtype q_dtype, int32_t n_seq, int32_t n_heads, int32_t n_kv_heads,
+                                        int32_t head_dim, int64_t n_tokens) {
+    if (n_seq < 0 || n_tokens < 0 || (q_dtype != KVQ_F32 && q_dtype != KVQ_BF16)) return 0;
+    if (check_gqa(n_heads, n_kv_heads, head_dim) != KVQ_OK) return 0;
+    return gqa_attn_workspace_bytes(head_dim);
+}
+
+kvq_status kv_gqa_attn_paged(const void* q, kvq_dtype q_dtype, int64_t n_tokens, int32_t n_heads, int32_t n_kv_heads,
+                             int32_t head_dim, int32_t n_seq, const int64_t* cu_q, const uint8_t* k_codes,
+                             const uint8_t* v_codes, const float* scales, const int32_t* block_table,
+                             int32_t table_stride, const int64_t* kv_lens, int32_t page_rows, int32_t n_pages,
+                             float sm_scale, int32_t causal, void* out, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+    kvq_status s = check_gqa(n_heads, n_kv_heads, head_dim);
+    if (s != KVQ_OK) return s;
+    if (q_dtype != KVQ_F32 && q_dtype != KVQ_BF16) return KVQ_ERR_ARG;
+    if ((s = check_pages(n_seq, page_rows, table_stride, n_pages, 16)) != KVQ_OK) return s;
+    if (n_tokens < 0) return KVQ_ERR_ARG;
+    if (n_tokens > 0x7fffffff || n_tokens * (n_heads / n_kv_heads) > 0x7fffffff - 1024) return KVQ_ERR_UNSUPPORTED;
+    if (!isfinite(sm_scale)) return KVQ_ERR_ARG;
+    if (n_heads == 0 || n_tokens == 0 || n_seq == 0) return KVQ_OK;
+    if (!q || !out || !cu_q || !kv_lens) return KVQ_ERR_ARG;
+    if (n_pages > 0 && table_stride > 0 && (!k_codes || !v_codes || !scales || !block_table)) return KVQ_ERR_ARG;
+    if (n_pages == 0) table_stride = 0;   // nothing to read: every length but 0 is invalid
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(scales, 16) ||
+        !aligned(cu_q, 8) || !aligned(kv_lens, 8) || !aligned(block_table, 4) || !aligned(workspace, 16))
+        return KVQ_ERR_ARG;
+    if (!workspace || workspace_bytes < gqa_attn_workspace_bytes(head_dim)) return KVQ_ERR_WORKSPACE;
+    GqaAttnCall c{q, q_dtype, n_tokens, n_heads, n_kv_heads, head_dim, n_seq, cu_q, k_codes, v_codes, scales, block_table,
+                  table_stride, kv_lens, page_rows, n_pages, sm_scale, causal != 0, out, workspace};
+    return cuda_status(launch_gqa_attn(c, (cudaStream_t)stream));
+}
+
+static kvq_status check_beam(int32_t n_seq, int32_t n_beams, int64_t vocab, int32_t keep) {
+    if (n_seq < 0 || n_beams < 1 || vocab < 1 || keep < 1) return KVQ_ERR_ARG;
+    if (n_beams > 32 || keep > 64 || vocab > 0x7fffffff || n_seq > 65535) return KVQ_ERR_UNSUPPORTED;
+    return KVQ_OK;
+}
+
+size_t kv_beam_workspace_size(int32_t n_seq, int32_t n_beams, int64_t vocab, int32_t keep) {
+    return check_beam(n_seq, n_beams, vocab, keep) == KVQ_OK ? beam_workspace_bytes(n_seq, n_beams, vocab, keep) : 0;
+}
+
+kvq_status kv_beam_select(const void* logits, kvq_dtype dtype, int64_t row_stride, int32_t n_seq, int32_t n_beams,
+                          int64_t vocab, const float* scores, int32_t keep, float* out_scores, int32_t* parents,
+                          int32_t* tokens, void* workspace, size_t workspace_bytes, void* stream) {
+    kvq_status s = check_beam(n_seq, n_beams, vocab, keep);
+    if (s != KVQ_OK) return s;
+    if (dtype != KVQ_F32 && dtype != KVQ_BF16) return KVQ_ERR_ARG;
+    if (row_stride < vocab) return KVQ_ERR_ARG;
+    if (n_seq == 0) return KVQ_OK;
+    if (!logits || !scores || !out_scores || !parents || !tokens) return KVQ_ERR_ARG;
+    if (!aligned(logits, dtype == KVQ_BF16 ? 2 : 4) || !aligned(scores, 4) || !aligned(out_scores, 4) ||
+        !aligned(parents, 4) || !aligned(tokens, 4) || !aligned(workspace, 16))
+        return KVQ_ERR_ARG;
+    if (!workspace || workspace_bytes < beam_workspace_bytes(n_seq, n_beams, vocab, keep)) return KVQ_ERR_WORKSPACE;
+    return cuda_status(launch_beam_select(logits, dtype, row_stride, n_seq, n_beams, vocab, scores, keep, out_scores,
+                                          parents, tokens, workspace, (cudaStream_t)stream));
+}
+
+size_t kv_pages_fork_workspace_size(int32_t n_seq, int32_t table_stride, int32_t n_pages) {
+    if (n_seq < 0 || table_stride < 0 || n_pages < 0 || n_seq > 4096) return 0;
+    if ((int64_t)n_seq * table_stride > 0x7fffffff) return 0;
+    return fork_workspace_bytes(n_seq, table_stride, n_pages);
+}
+
+kvq_status kv_pages_fork(int32_t n_seq, int32_t page_rows, const int32_t* parents, int64_t* kv_lens,
+                         int32_t* block_table, int32_t table_stride, int32_t* free_pages, int32_t* n_free,
+                         int32_t n_pages, int32_t* copies, void* workspace, size_t workspace_bytes, void* stream) {
+    kvq_status s = check_pages(n_seq, page_rows, table_stride, n_pages, 1);
+    if (s != KVQ_OK) return s;
+    if (n_seq > 4096 || (int64_t)n_seq * table_stride > 0x7fffffff) return KVQ_ERR_UNSUPPORTED;
+    if (n_seq == 0) return KVQ_OK;
+    if (!parents || !kv_lens || !n_free || !copies) return KVQ_ERR_ARG;
+    if (n_pages > 0 && (!block_table || !free_pages)) return KVQ_ERR_ARG;
+    if (n_pages == 0) table_stride = 0;   // no page to list: every length but 0 is invalid
+    if (!aligned(parents, 4) || !aligned(kv_lens, 8) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
+        !aligned(n_free, 4) || !aligned(copies, 4) || !aligned(workspace, 16))
+        return KVQ_ERR_ARG;
+    if (!workspace || workspace_bytes < fork_workspace_bytes(n_seq, table_stride, n_pages)) return KVQ_ERR_WORKSPACE;
+    return cuda_status(launch_pages_fork(n_seq, page_rows, parents, kv_lens, block_table, table_stride, free_pages, n_free,
+                                         n_pages, copies, workspace, (cudaStream_t)stream));
+}
+
+kvq_status kv_pages_copy(int32_t n, const int32_t* copies, int32_t n_pages, int32_t n_pools, const kvq_pool* pools,
+                         int32_t* err_word, void* stream) {
+    if (n < 0 || n_pages < 0 || n_pools < 0) return KVQ_ERR_ARG;
+    if (n == 0 || n_pools == 0) return KVQ_OK;
+    if (!copies || !pools || !aligned(copies, 4) || !aligned(err_word, 4)) return KVQ_ERR_ARG;
+    for (int32_t k = 0; k < n_pools; ++k) {
+        if (pools[k].page_bytes < 0 || (pools[k].page_bytes > 0 && n_pages > 0 && !pools[k].data)) return KVQ_ERR_ARG;
+        if (pools[k].page_bytes > (1ll << 40)) return KVQ_ERR_UNSUPPORTED;
+    }
+    return cuda_status(launch_pages_copy(n, copies, n_pages, n_pools, pools, err_word, (cudaStream_t)stream));
 }
 
 int32_t kvq_read_device_error(void* workspace, int32_t clear, void* stream) {

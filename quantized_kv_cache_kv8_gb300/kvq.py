@@ -148,6 +148,24 @@ def _declare(L):
     L.kv_attn_paged.restype = C.c_int
     L.kv_attn_paged.argtypes = [C.c_int, pl, P, C.c_int, I64, I32, I32, P, P, P, P, I32, P, I32, I32, C.c_float, P, P, S,
                                 C.c_int, P]
+    L.kv_gqa_append.restype = C.c_int
+    L.kv_gqa_append.argtypes = [C.POINTER(Rope), C.c_int, I64, I32, I32, I32, P, I64, I64, P, I64, I64, P, I64, P, P, I64,
+                                I64, P, I64, I64, P, P, P, I32, I32, P, P]
+    L.kv_gqa_attn_paged_workspace_size.restype = S
+    L.kv_gqa_attn_paged_workspace_size.argtypes = [C.c_int, I32, I32, I32, I32, I64]
+    L.kv_gqa_attn_paged.restype = C.c_int
+    L.kv_gqa_attn_paged.argtypes = [P, C.c_int, I64, I32, I32, I32, I32, P, P, P, P, P, I32, P, I32, I32, C.c_float, I32, P,
+                                    P, S, P]
+    L.kv_beam_workspace_size.restype = S
+    L.kv_beam_workspace_size.argtypes = [I32, I32, I64, I32]
+    L.kv_beam_select.restype = C.c_int
+    L.kv_beam_select.argtypes = [P, C.c_int, I64, I32, I32, I64, P, I32, P, P, P, P, S, P]
+    L.kv_pages_fork_workspace_size.restype = S
+    L.kv_pages_fork_workspace_size.argtypes = [I32, I32, I32]
+    L.kv_pages_fork.restype = C.c_int
+    L.kv_pages_fork.argtypes = [I32, I32, P, P, P, I32, P, P, I32, P, P, S, P]
+    L.kv_pages_copy.restype = C.c_int
+    L.kv_pages_copy.argtypes = [I32, P, I32, I32, P, P, P]
     L.kvq_read_device_error.restype = I32
     L.kvq_read_device_error.argtypes = [P, I32, P]
     L.kvq_read_exact_rescales.restype = I64
@@ -414,8 +432,9 @@ def _paged():
             loader = importlib.machinery.ExtensionFileLoader("_paged_host", _build.build_host())
             m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_paged_host", loader))
             loader.exec_module(m)
-            m.init(*(C.cast(f, C.c_void_p).value for f in (L.kv_pages_reserve, L.kv_pages_trim, L.kv_rope_append,
-                                                           L.kv_attn_paged)))
+            m.init(*(C.cast(f, C.c_void_p).value for f in (
+                L.kv_pages_reserve, L.kv_pages_trim, L.kv_rope_append, L.kv_attn_paged, L.kv_gqa_append,
+                L.kv_gqa_attn_paged, L.kv_beam_select, L.kv_pages_fork, L.kv_pages_copy)))
             _host = m
     return _host
 
@@ -480,6 +499,76 @@ def kv_attn_paged(fmt: int, q, cu_q, codes, scales, block_table, kv_lens, page_r
                                             sm_scale, layout or mla_layout(), path, dev, st)
     if status:
         _ok(status, "kv_attn_paged")
+
+
+# -- paged KV8 pools with grouped query heads ------------------------------------
+
+def kv_gqa_append(rope: Rope | None, k_new, v_new, positions, slot_map, q_in, q_out, k_codes, v_codes, scales,
+                  err_word=None, stream=None):
+    """One step's producer: q_in [n][n_heads][head_dim] with its leading rope.dim dims rotated into q_out (q_in
+    itself: in place), k_new (rotated) and v_new [n][n_kv_heads][head_dim] encoded into the pool rows slot_map
+    (negative: skipped) of k_codes, v_codes [n_pages][n_kv_heads][page_rows][head_dim] and scales [..][2].  rope
+    None: no rotation.  k_new and v_new None: only queries; q_in None: only rows."""
+    dev, st = _here(stream)
+    status = (_host or _paged()).gqa_append(rope, k_new, v_new, positions, slot_map, q_in, q_out, k_codes, v_codes,
+                                            scales, err_word, dev, st)
+    if status:
+        _ok(status, "kv_gqa_append")
+
+
+def kv_gqa_attn_paged_workspace_size(n_seq: int, n_heads: int, n_kv_heads: int, head_dim: int, n_tokens: int,
+                                     bf16: bool = True) -> int:
+    return lib().kv_gqa_attn_paged_workspace_size(KVQ_BF16 if bf16 else KVQ_F32, n_seq, n_heads, n_kv_heads, head_dim,
+                                                  n_tokens)
+
+
+def kv_gqa_attn_paged(q, cu_q, k_codes, v_codes, scales, block_table, kv_lens, out, workspace, sm_scale: float,
+                      causal: bool = True, stream=None):
+    """Attention of the tokens q [n_tokens][n_heads][head_dim] (sequence b: q[cu_q[b]:cu_q[b+1]]) over its kv_lens[b]
+    paged rows, of which the tokens are the last (causal), or over all of them (cross attention); out as q."""
+    dev, st = _here(stream)
+    status = (_host or _paged()).gqa_attn(q, cu_q, k_codes, v_codes, scales, block_table, kv_lens, out, workspace,
+                                          sm_scale, bool(causal), dev, st)
+    if status:
+        _ok(status, "kv_gqa_attn_paged")
+
+
+# -- beam search over paged caches -----------------------------------------------
+
+def kv_beam_workspace_size(n_seq: int, n_beams: int, vocab: int, keep: int) -> int:
+    return lib().kv_beam_workspace_size(n_seq, n_beams, vocab, keep)
+
+
+def kv_beam_select(logits, scores, out_scores, parents, tokens, workspace, stream=None):
+    """The best continuations of every request: logits [n_seq][n_beams][vocab], scores [n_seq][n_beams]; out_scores,
+    parents (s * n_beams + beam) and tokens [n_seq][keep], best first, -inf and -1 where there are fewer."""
+    dev, st = _here(stream)
+    status = (_host or _paged()).beam_select(logits, scores, out_scores, parents, tokens, workspace, dev, st)
+    if status:
+        _ok(status, "kv_beam_select")
+
+
+def kv_pages_fork_workspace_size(n_seq: int, table_stride: int, n_pages: int) -> int:
+    return lib().kv_pages_fork_workspace_size(n_seq, table_stride, n_pages)
+
+
+def kv_pages_fork(parents, kv_lens, block_table, free_pages, n_free, page_rows: int, copies, workspace, stream=None):
+    """Sequence i continues sequence parents[i] (-1: it ends): lengths and tables follow, full pages are shared, pages
+    nobody holds return to the stack; copies [n_seq][2] lists the pages kv_pages_copy has to copy."""
+    dev, st = _here(stream)
+    status = (_host or _paged()).fork_pages(parents, kv_lens, block_table, free_pages, n_free, page_rows, copies, workspace,
+                                            dev, st)
+    if status:
+        _ok(status, "kv_pages_fork")
+
+
+def kv_pages_copy(copies, pools, err_word=None, n_pages: int | None = None, stream=None):
+    """Page copies[i][0] to page copies[i][1] (negative: none) in every tensor of `pools`, each of n_pages equal
+    pages (None: the first pool's first dimension)."""
+    dev, st = _here(stream)
+    status = (_host or _paged()).copy_pages(copies, pools, err_word, -1 if n_pages is None else n_pages, dev, st)
+    if status:
+        _ok(status, "kv_pages_copy")
 
 
 def read_device_error(workspace, clear: bool = True, stream=None) -> int:

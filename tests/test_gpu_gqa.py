@@ -1,0 +1,353 @@
+"""Grouped-query KV8 pools on the GPU: append and attention against plain implementations in 64 bits."""
+import math
+
+import pytest
+import torch
+
+from gpu_common import kvq_module
+from gqa_common import Pool, attention, close, encode_rows
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kvq():
+    return kvq_module()
+
+
+def workspace(kvq, heads, kv, dim, bf16):
+    return torch.zeros(kvq.kv_gqa_attn_paged_workspace_size(1, heads, kv, dim, 1, bf16=bf16), dtype=torch.uint8, device="cuda")
+
+
+def offsets(new):
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    return torch.tensor(cu, device="cuda")
+
+
+def queries(n, heads, dim, dtype, seed=1, gain=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(n, heads, dim, generator=g) * gain).to(dtype).cuda()
+
+
+def attend(kvq, pool, q, lens, new, causal=True, sm=None, ws=None, extra=0, stream=None):
+    """(out, workspace); `extra` rows behind the last sequence hold 7."""
+    n, heads, dim = q.shape
+    ws = workspace(kvq, heads, pool.heads, dim, q.dtype == torch.bfloat16) if ws is None else ws
+    out = torch.full((n, heads, dim), 7.0, dtype=q.dtype, device="cuda")
+    kvq.kv_gqa_attn_paged(q, offsets(new), pool.k, pool.v, pool.scales, pool.table,
+                          torch.tensor(lens, dtype=torch.int64, device="cuda"), out, ws,
+                          1 / math.sqrt(dim) if sm is None else sm, causal=causal, stream=stream)
+    if extra:
+        assert bool((out[n - extra:] == 7.0).all()), "rows behind the last sequence"
+    return out, ws
+
+
+DT = [torch.bfloat16, torch.float32]
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("dim,heads,kv", [(64, 1, 1), (64, 16, 16), (128, 32, 8), (128, 7, 1), (256, 16, 2), (256, 36, 4)])
+def test_decode(kvq, dtype, dim, heads, kv):
+    lens = [1, 2, 15, 16, 17, 63, 64, 65, 0, 127, 128, 129, 1000, 3001]
+    new = [1] * len(lens)
+    pool = Pool(kv, dim, 16, lens, seed=dim + heads)
+    q = queries(len(lens) + 2, heads, dim, dtype)
+    out, ws = attend(kvq, pool, q, lens, new, extra=2)
+    close(out[:-2], attention(q[:-2], pool, lens, new, 1 / math.sqrt(dim), True))
+    assert kvq.read_device_error(ws) == 0
+    assert int(ws.view(torch.int32)[64:64 + 608].abs().sum()) == 0   # tickets returned
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim,heads,kv,page", [(64, 12, 4, 64), (128, 32, 8, 32), (128, 40, 8, 256), (256, 8, 2, 16)])
+def test_mixtures_of_lengths(kvq, dtype, causal, dim, heads, kv, page):
+    new = [3, 0, 1, 40, 17, 1, 200, 0, 5]
+    lens = [3, 9, 700, 300, 5, 1, 260, 0, 2] if causal else [0, 9, 700, 1, 5, 64, 1501, 3, 16]
+    pool = Pool(kv, dim, page, lens, seed=page)
+    q = queries(sum(new), heads, dim, dtype)
+    out, ws = attend(kvq, pool, q, lens, new, causal)   # causal: 17 tokens on 5 rows, 5 on 2: the first see none
+    close(out, attention(q, pool, lens, new, 1 / math.sqrt(dim), causal))
+    assert kvq.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("past,new", [(0, 1), (0, 333), (1000, 130), (4097, 64), (31, 515)])
+def test_chunks(kvq, dtype, past, new):
+    pool = Pool(2, 128, 64, [past + new], seed=past)
+    q = queries(new, 10, 128, dtype)
+    out, _ = attend(kvq, pool, q, [past + new], [new])
+    close(out, attention(q, pool, [past + new], [new], 1 / math.sqrt(128), True))
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_spread_of_scales_and_scores(kvq, dtype):
+    lens, new = [5000, 4000, 90], [1, 9, 2]
+    pool = Pool(4, 128, 64, lens, seed=5, gain=4.0, scale_spread=8.0)
+    q = queries(12, 16, 128, dtype, gain=3.0)
+    out, _ = attend(kvq, pool, q, lens, new, sm=0.25)
+    ref = attention(q, pool, lens, new, 0.25, True)
+    # scores reach 500: f32 holds a score to 2^-24 of its size several times over, a weight to
+    # 500 * 2^-21 = 2.4e-4 then; in the type's own rounding besides
+    half = torch.finfo(dtype).eps / 2
+    top = ref.abs().amax(-1, keepdim=True)
+    assert bool(((out.double() - ref).abs() <= half * ref.abs() + 5e-4 * top).all())
+
+
+def test_small_weights_and_small_scales_add_up(kvq):
+    """131,072 rows some 20 binades below one row, by score and by scale: they weigh a third of it."""
+    n = 131073
+    pool = Pool(1, 64, 256, [n])
+    one = torch.zeros(1, 64)
+    one[0, 0] = 1.0
+    codes, _ = encode_rows(one)
+    pool.k[:] = codes.cuda()[0]
+    pool.v[:] = 0
+    pool.v[..., 1] = codes.cuda()[0, 0]
+    for by_scale in (False, True):
+        pool.scales[..., 0] = 0.0 if by_scale else -20 * math.log(2) / 448 / 1.0
+        pool.scales[..., 1] = 2.0 ** -20 / 448 if by_scale else 1 / 448
+        pg = int(pool.table[0, 0])
+        pool.scales[pg, 0, 0, 0] = 0.0
+        if by_scale:
+            pool.scales[pg, 0, 0, 1] = 1 / 448
+        q = torch.zeros(1, 1, 64, device="cuda")
+        q[..., 0] = 1.0
+        out, _ = attend(kvq, pool, q, [n], [1], sm=1.0)
+        close(out, attention(q, pool, [n], [1], 1.0, True), f"by_scale={by_scale}")
+
+
+def test_a_million_rows(kvq):
+    """Long sums whose roundings point one way, by as few walkers as the grid has."""
+    n, kv = 1 << 20, 1
+    pool = Pool(kv, 64, 1024, [n], seed=3)
+    b = 456   # sequences that list the same pages
+    pool.table = pool.table.expand(b, -1).contiguous()
+    pool.v[:] = 0x35
+    pool.scales[..., 1] = 0.3
+    q = queries(b, 1, 64, torch.float32)
+    out, _ = attend(kvq, pool, q, [n] * b, [1] * b)
+    ref = attention(q[:1], pool, [n], [1], 0.125, True)
+    close(out[:1], ref)
+    assert float((out.double() - float(ref[0, 0, 0])).abs().max()) <= 1e-5 * float(ref[0, 0, 0])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_that_are_no_numbers(kvq, causal):
+    """NaN codes and scales reach the tokens that see them, and no other; rows behind the last are never seen."""
+    lens, new, dim = [70, 33], [6, 2], 128
+    for bad in ("k", "v", "sk", "sv", "inf"):
+        pool = Pool(2, dim, 16, lens, seed=9)
+        q = queries(8, 6, dim, torch.float32)
+        ref = attention(q, pool, lens, new, 0.1, causal)
+        pg, at = int(pool.table[0, 4]), 67 - 64   # row 67 of sequence 0, seen by its last three tokens
+        last, end = int(pool.table[1, 2]), 33 - 32   # behind sequence 1's end
+        for p_, a in ((pg, slice(at, at + 1)), (last, slice(end, 16))):
+            if bad in "kv":
+                (pool.k if bad == "k" else pool.v)[p_, :, a, 5] = 0xff
+            else:
+                pool.scales[p_, :, a, 0 if bad == "sk" else 1] = math.inf if bad == "inf" else math.nan
+        out, ws = attend(kvq, pool, q, lens, new, causal, sm=0.1)
+        sees = [i for i in range(6) if not causal or 64 + i >= 67]
+        for i in range(8):
+            if i in sees:
+                hit = torch.isnan(out[i]) if bad != "k" else torch.isnan(out[i])
+                assert bool(hit.any(-1).all()), (bad, i)
+            else:
+                close(out[i], ref[i], f"{bad} {i}")
+
+
+def test_zero_queries_and_zero_rows(kvq):
+    pool = Pool(1, 64, 16, [20])
+    pool.scales[..., 1] = 0.0
+    out, _ = attend(kvq, pool, queries(1, 2, 64, torch.float32), [20], [1])
+    assert float(out.abs().max()) == 0.0
+    pool = Pool(1, 64, 16, [20])
+    q = torch.zeros(1, 2, 64, device="cuda")
+    out, _ = attend(kvq, pool, q, [20], [1])
+    close(out, attention(q, pool, [20], [1], 0.125, True))
+
+
+@pytest.mark.parametrize("gain", [1e-30, 1e-8, 1e8, 1e30])
+def test_sizes_of_queries(kvq, gain):
+    pool = Pool(2, 128, 32, [300])
+    for dtype in DT:
+        q = queries(1, 4, 128, dtype, gain=gain)
+        out, _ = attend(kvq, pool, q, [300], [1], sm=0.1 / gain)
+        close(out, attention(q, pool, [300], [1], 0.1 / gain, True), f"{dtype}")
+
+
+def test_the_same_bits_again(kvq):
+    lens, new = [9000, 20, 1, 3000], [2, 3, 1, 40]
+    pool = Pool(4, 128, 64, lens)
+    q = queries(sum(new), 8, 128, torch.bfloat16)
+    a, ws = attend(kvq, pool, q, lens, new)
+    for _ in range(3):
+        b, _ = attend(kvq, pool, q, lens, new, ws=ws)
+        assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits(kvq):
+    dim, kv, page = 256, 8, 256
+    n_pages = (1 << 32) // (dim * kv * page) * 2 + 5   # codes of 8 GB each
+    k = torch.empty(n_pages, kv, page, dim, dtype=torch.uint8, device="cuda")
+    v, scales = torch.empty_like(k), torch.empty(n_pages, kv, page, 2, device="cuda")
+    small = Pool(kv, dim, page, [600], seed=2, spare=0)
+    ids = torch.tensor([[n_pages - 1, n_pages - 4, n_pages // 2 + 1]], dtype=torch.int32, device="cuda")
+    for i in range(3):
+        for big, little in ((k, small.k), (v, small.v), (scales, small.scales)):
+            big[ids[0, i]] = little[small.table[0, i]]
+    q = queries(1, 16, dim, torch.bfloat16)
+    ref = attention(q, small, [600], [1], 1 / 16, True)
+    small.k, small.v, small.scales, small.table = k, v, scales, ids
+    out, ws = attend(kvq, small, q, [600], [1])
+    close(out, ref)
+    rows = queries(1, kv, dim, torch.bfloat16, seed=8)
+    slot = torch.tensor([(n_pages - 1) * page + 255], device="cuda")
+    kvq.kv_gqa_append(None, rows, rows, None, slot, None, None, k, v, scales, ws)
+    c, s = encode_rows(rows[0].float())
+    assert torch.equal(k[-1, :, 255], c) and torch.equal(v[-1, :, 255], c) and torch.equal(scales[-1, :, 255, 1], s)
+
+
+def test_broken_tables_and_lengths_are_reported(kvq):
+    lens, new = [40, 50], [1, 1]
+    pool = Pool(2, 64, 16, lens)
+    q = queries(2, 4, 64, torch.float32)
+    ref = attention(q, pool, lens, new, 0.125, True)
+    pool.table[1, 1] = pool.n_pages
+    out, ws = attend(kvq, pool, q, lens, new)
+    assert kvq.read_device_error(ws) == 1
+    close(out[:1], ref[:1])
+    for bad in ([-1, 50], [40, 17 * 16]):
+        pool = Pool(2, 64, 16, lens)
+        out, ws = attend(kvq, pool, q, bad, new, ws=ws)
+        assert kvq.read_device_error(ws) == 1
+        out, ws = attend(kvq, pool, q, lens, new, ws=ws)   # the workspace serves on
+        assert kvq.read_device_error(ws) == 0
+        close(out, ref)
+    cu = torch.tensor([0, 3, 2], device="cuda")
+    kvq.kv_gqa_attn_paged(q, cu, pool.k, pool.v, pool.scales, pool.table, pool.lens, out, ws, 0.125)
+    assert kvq.read_device_error(ws) == 1
+
+
+def test_captured_on_another_stream_and_replayed(kvq):
+    lens, new = [200, 1000, 64], [1, 1, 1]
+    pool = Pool(2, 128, 64, [256, 1088, 128])   # room for every length below
+    q = queries(3, 8, 128, torch.bfloat16)
+    kv_lens, cu = torch.tensor(lens, device="cuda"), offsets(new)
+    graphs = []
+    for _ in range(2):   # two graphs, a workspace each
+        ws, out = workspace(kvq, 8, 2, 128, True), torch.zeros_like(q)
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            kvq.kv_gqa_attn_paged(q, cu, pool.k, pool.v, pool.scales, pool.table, kv_lens, out, ws, 0.1)
+        graphs.append((graph, out, ws))
+    for shift in (0, 1, 50, -60):
+        kv_lens.copy_(torch.tensor([t + shift for t in lens], device="cuda"))
+        ref = attention(q, pool, [t + shift for t in lens], new, 0.1, True)
+        for graph, _, _ in graphs:
+            graph.replay()
+        for _, out, _ in graphs:
+            close(out, ref)
+
+
+# -- append ----------------------------------------------------------------------
+
+def turn(x, positions, inv, axis, adjacent):
+    """Rotation of the leading dims in f64."""
+    rot = 2 * len(inv)
+    angle = positions.double()[axis].T * torch.tensor(inv, dtype=torch.float64, device="cuda")   # [n][pairs]
+    c, s = torch.cos(angle)[:, None], torch.sin(angle)[:, None]
+    y = x.double().clone()
+    i = torch.arange(rot // 2, device="cuda")
+    a, b = (2 * i, 2 * i + 1) if adjacent else (i, i + rot // 2)
+    y[..., a], y[..., b] = x[..., a].double() * c - x[..., b].double() * s, x[..., b].double() * c + x[..., a].double() * s
+    return y
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("dim,heads,kv,pairs,axes", [(64, 5, 5, 32, 1), (128, 32, 8, 64, 3), (256, 16, 2, 32, 1), (128, 6, 2, 3, 2),
+                                                     (64, 4, 1, 1, 1), (256, 3, 1, 64, 4)])
+def test_append(kvq, dtype, adjacent, dim, heads, kv, pairs, axes):
+    n, page, n_pages = 37, 16, 5
+    g = torch.Generator().manual_seed(dim + pairs)
+    fused = torch.randn(n, heads + 2 * kv, dim, generator=g).to(dtype).cuda()   # strided slices of one projection
+    q, k, v = fused[:, :heads], fused[:, heads:heads + kv], fused[:, heads + kv:]
+    inv = [10000.0 ** (-i / pairs) for i in range(pairs)]
+    axis = [i % axes for i in range(pairs)]
+    rope = kvq.rope_layout(inv, axis, n_axes=axes, adjacent=adjacent)
+    pos = torch.randint(0, 1 << 20, (axes, n), generator=g).cuda()
+    slots = torch.randperm(page * n_pages, generator=g)[:n].cuda()
+    slots[3] = -1
+    kc = torch.full((n_pages, kv, page, dim), 9, dtype=torch.uint8, device="cuda")
+    vc, sc = kc.clone(), torch.full((n_pages, kv, page, 2), 5.0, device="cuda")
+    out = torch.zeros(n, heads, dim, dtype=dtype, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kvq.kv_gqa_append(rope, k, v, pos, slots, q, out, kc, vc, sc, err)
+    assert int(err) == 0
+    # products, sum and cos / sin in f32: 2^-22 of the two elements, then the type's rounding
+    half = torch.finfo(dtype).eps / 2
+    ref = turn(q, pos, inv, axis, adjacent)
+    size = turn(q.abs().float() * 0 + q.abs(), pos * 0, inv, axis, adjacent).amax(-1, keepdim=True)
+    assert bool(((out.double() - ref).abs() <= half * ref.abs() + 2.0 ** -22 * size * 2).all())
+    rk, rv = turn(k, pos, inv, axis, adjacent), v.double()
+    wrote = torch.zeros(n_pages, page, dtype=torch.bool, device="cuda")
+    for i in range(n):
+        if i == 3:
+            continue
+        p, a = int(slots[i]) // page, int(slots[i]) % page
+        wrote[p, a] = True
+        for codes, x, j in ((kc, rk[i], 0), (vc, rv[i], 1)):
+            s = sc[p, :, a, j].double()
+            amax = x.abs().amax(-1)
+            assert bool(((s - amax / 448).abs() <= 2.0 ** -21 * amax / 448).all())
+            got = codes[p, :, a].view(torch.float8_e4m3fn).double() * s[:, None]
+            # half a step of e4m3: 2^-4 of the value, or 2^-10 scales below its normals
+            assert bool(((got - x).abs() <= (2.0 ** -4 + 1e-5) * x.abs() + (2.0 ** -10 + 1e-6) * s[:, None] + 1e-6 * amax[:, None]).all())
+    if True:   # values are not rotated: the encoder's very bytes
+        c, s = encode_rows(v.float())
+        keep = [i for i in range(n) if i != 3]
+        assert torch.equal(vc[slots[keep] // page, :, slots[keep] % page], c[keep])
+        assert torch.equal(sc[slots[keep] // page, :, slots[keep] % page, 1], s[keep])
+    rest = ~wrote
+    assert bool((kc.transpose(1, 2)[rest] == 9).all()) and bool((sc.transpose(1, 2)[rest] == 5.0).all())
+
+
+def test_append_in_place_without_rotation_and_parts(kvq):
+    n, dim = 9, 128
+    q = queries(n, 4, dim, torch.bfloat16)
+    rope = kvq.rope_layout([0.5 ** i for i in range(64)])
+    pos = torch.arange(n, device="cuda") * 1001
+    out = torch.zeros_like(q)
+    kvq.kv_gqa_append(rope, None, None, pos, None, q, out, None, None, None)
+    again = q.clone()
+    kvq.kv_gqa_append(rope, None, None, pos, None, again, again, None, None, None)
+    assert torch.equal(out, again)
+    odd = torch.zeros(n * 4 * dim + 1, dtype=torch.bfloat16, device="cuda")[1:].view(n, 4, dim)   # not 16-byte aligned
+    kvq.kv_gqa_append(rope, None, None, pos, None, q, odd, None, None, None)
+    assert torch.equal(out, odd)
+    pool = Pool(4, dim, 16, [32])
+    kvq.kv_gqa_append(None, q, q, None, torch.arange(n, device="cuda"), None, None, pool.k, pool.v, pool.scales)
+    c, s = encode_rows(q.float())
+    assert torch.equal(pool.k[0, :, :n].transpose(0, 1), c) and torch.equal(pool.scales[0, :, :n, 0].T, s)
+
+
+def test_append_reports_what_is_no_number_and_what_is_no_slot(kvq):
+    pool = Pool(2, 64, 16, [16], spare=0)
+    x = queries(3, 2, 64, torch.float32)
+    x[1, 0, 7] = math.nan
+    x[2, 1, 9] = math.inf
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    v = torch.ones_like(x)
+    kvq.kv_gqa_append(None, x, v, None, torch.tensor([0, 1, 2], device="cuda"), None, None, pool.k, pool.v, pool.scales, err)
+    assert int(err) == 9
+    assert torch.isnan(pool.scales[0, :, :3, 0]).tolist() == [[False, True, False], [False, False, True]]
+    assert not bool(torch.isnan(pool.scales[0, :, :3, 1]).any())
+    err.zero_()
+    kvq.kv_gqa_append(None, v, v, None, torch.tensor([16, -1, 99], device="cuda"), None, None, pool.k, pool.v, pool.scales, err)
+    assert int(err) == 1
