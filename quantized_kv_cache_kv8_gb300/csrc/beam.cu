@@ -6,16 +6,17 @@
 // within a beam to the larger logit, then to the lower token.
 //
 // What bounds it: reading the logits, once.  A beam's row is cut into slices, one CTA
-// each.  A thread keeps 4 vectors of 16 bytes in flight and sums 2^((x - r) l) as it goes,
-// l = log2(e) in f32 and r a reference of its own, in f32 (4 partial sums); from there on in f64.
+// each.  A thread asks for the next 4 vectors of 16 bytes and sums 2^(x l - r l) over the last 4,
+// l = log2(e) in f32 and r a reference of its own, in f32, trip by trip; what the rounding of
+// r l adds is a factor of the trip's sum.
 // With the same l in the sum and behind it, the error of l moves a score by 1.3e-8 of
 // the row's entropy, not of its logits.
 //
-// Selection without sorting.  The `keep`-th largest of the threads' maxima over the
-// first trip is a bound that at least `keep` elements reach, so elements below it are
-// out, and so are later ones that only equal it (their index is higher).  What passes goes to a
-// list in shared memory, about `keep` elements a trip, and each finds its rank by
-// counting.  Should the list overflow (ascending or equal logits), the slice's best are found
+// Selection without sorting.  Over the first trip each warp finds the (keep / 8)-th largest
+// of its lanes' maxima; the least of these is a bound that at least `keep` elements reach, so
+// elements below it are out, and later ones that only equal it too (their index is higher).  Vectors that hold
+// more go to a list in shared memory; when it has grown by 16 their elements find their ranks by
+// counting, the best `keep` stay and the last of them is the new bound.  Should a list overflow (ascending or equal logits), the slice's best are found
 // one after another by maxima over the slice, `keep` passes in L2: slower, the same answer.
 // The slice lists of a request are merged by the CTA that comes last, a head a lane.
 #include "gqa.cuh"
@@ -29,8 +30,9 @@ namespace {
 using tc::ex2;
 
 constexpr int kNT = 256, kWarps = kNT / 32;
-constexpr int kTrip = 4;             // vectors of a thread and trip
-constexpr int kList = 1024;          // elements that may pass the bound
+constexpr int kTrip = 4;             // vectors of a thread and trip (odd_sum lists them)
+constexpr int kVec = 256;            // vectors that may hold elements past the bound
+constexpr int kList = 512;           // such elements
 constexpr int kMaxKeep = 64, kMaxBeams = 32;
 constexpr int kMaxLists = kNT;       // slice lists of a request
 constexpr int kMaxCand = 2048;       // their elements
@@ -41,13 +43,13 @@ struct BeamParams {
     int64_t stride;       // elements between rows
     int64_t vocab;
     int32_t n_beams, keep, splits;
-    int64_t per_split;    // vectors
+    uint32_t per_split;   // vectors
     const float* scores;
     float* out_scores;
     int32_t* parents;
     int32_t* tokens;
     uint32_t* tickets;    // [n_seq]
-    double2* sums;        // [rows][splits]: reference, sum
+    float2* sums;         // [rows][splits]: reference, sum
     int32_t* counts;      // [rows][splits]
     uint64_t* keys;       // [rows][splits][keep]
 };
@@ -60,10 +62,10 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ uint64_t make_key(float x, uint32_t index) {
     return ((uint64_t)ordered(x) << 32) | (uint32_t)~index;
 }
-__device__ __forceinline__ float key_value(uint64_t k) {
-    const uint32_t o = (uint32_t)(k >> 32);
+__device__ __forceinline__ float from_ordered(uint32_t o) {
     return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
 }
+__device__ __forceinline__ float key_value(uint64_t k) { return from_ordered((uint32_t)(k >> 32)); }
 __device__ __forceinline__ uint32_t key_index(uint64_t k) { return ~(uint32_t)k; }
 
 // A row in vectors of 16 bytes, counted from its first element wherever that lies: beams
@@ -72,11 +74,12 @@ __device__ __forceinline__ uint32_t key_index(uint64_t k) { return ~(uint32_t)k;
 template <typename T>
 struct Row {
     static constexpr int V = 16 / sizeof(T);
-    const T* x;
+    const char* x;
     uint32_t shift;    // bytes between the 16-byte boundary before the row and it
-    int64_t n;
-    __device__ __forceinline__ Row(const T* p, int64_t vocab) : x(p), shift((uint32_t)((uintptr_t)p & 15u)), n(vocab) {}
-    __device__ __forceinline__ int64_t vectors() const { return (n + V - 1) / V; }
+    uint32_t n, whole; // elements; whole vectors
+    __device__ __forceinline__ Row(const T* p, int64_t vocab)
+        : x(reinterpret_cast<const char*>(p)), shift((uint32_t)((uintptr_t)p & 15u)), n((uint32_t)vocab), whole(n / V) {}
+    __device__ __forceinline__ uint32_t vectors() const { return (n + V - 1) / V; }
     static __device__ __forceinline__ uint4 ldg(const char* p) {
         uint4 r;
         asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -84,10 +87,21 @@ struct Row {
                      : "l"(p));
         return r;
     }
-    __device__ __forceinline__ uint4 load(int64_t v) const {
-        const int64_t e = v * V;
-        const char* at = reinterpret_cast<const char*>(x + e);
-        if (e + V <= n) {
+    // The vectors from, from + step, ...: `none` from `end` on.
+    template <int N>
+    __device__ __forceinline__ void load(uint4 (&r)[N], uint32_t from, uint32_t step, uint32_t end) const {
+        if (shift == 0 && from + (N - 1) * step < min(end, whole)) {
+            const char* at = x + (uint64_t)from * 16u;
+#pragma unroll
+            for (int u = 0; u < N; ++u) r[u] = ldg(at + u * step * 16u);
+        } else {
+#pragma unroll
+            for (int u = 0; u < N; ++u) r[u] = from + u * step < end ? load(from + u * step) : none();
+        }
+    }
+    __device__ __noinline__ uint4 load(uint32_t v) const {
+        const char* at = x + (uint64_t)v * 16u;
+        if (v < whole) {
             if (shift == 0) return ldg(at);
             // both aligned pieces hold elements of the vector
             const uint4 lo = *reinterpret_cast<const uint4*>(at - shift), hi = *reinterpret_cast<const uint4*>(at - shift + 16);
@@ -108,69 +122,98 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (sizeof(T) == 4) {
-                w[i] = e + i < n ? reinterpret_cast<const uint32_t*>(x)[e + i] : 0xff800000u;
+                w[i] = v * V + i < n ? reinterpret_cast<const uint32_t*>(at)[i] : 0xff800000u;
             } else {
-                const int64_t a = e + 2 * i;
-                const uint32_t lo = a < n ? reinterpret_cast<const uint16_t*>(x)[a] : 0xff80u;
-                const uint32_t hi = a + 1 < n ? reinterpret_cast<const uint16_t*>(x)[a + 1] : 0xff80u;
+                const uint32_t a = v * V + 2 * i;
+                const uint32_t lo = a < n ? reinterpret_cast<const uint16_t*>(at)[2 * i] : 0xff80u;
+                const uint32_t hi = a + 1 < n ? reinterpret_cast<const uint16_t*>(at)[2 * i + 1] : 0xff80u;
                 w[i] = lo | (hi << 16);
             }
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __device__ static __forceinline__ void floats(uint4 r, float (&f)[V]) {
+    // Nothing: -inf in every place.
+    static __device__ __forceinline__ uint4 none() {
+        const uint32_t w = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+        return make_uint4(w, w, w, w);
+    }
+    static __device__ __forceinline__ void floats(uint4 r, float (&f)[V]) {   // NaN as it is
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = fmaxf(__uint_as_float(w[i]), -INFINITY);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 none = __halves2bfloat162(__ushort_as_bfloat16(0xff80), __ushort_as_bfloat16(0xff80));
-                const __nv_bfloat162 v = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), none);
-                const uint32_t u = *reinterpret_cast<const uint32_t*>(&v);
-                f[2 * i] = __uint_as_float(u << 16);
-                f[2 * i + 1] = __uint_as_float(u & 0xffff0000u);
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                f[i] = __uint_as_float(w[i]);
+            } else {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
             }
+        }
+    }
+    static __device__ __forceinline__ float top(uint4 r) {   // NaN passed over
+        if constexpr (sizeof(T) == 4) {
+            return fmaxf(fmaxf(fmaxf(__uint_as_float(r.x), -INFINITY), __uint_as_float(r.y)),
+                         fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+        } else {
+            const auto v = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+            const __nv_bfloat162 m = __hmax2(__hmax2(v(r.x), v(r.y)), __hmax2(v(r.z), v(r.w)));
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
+            return fmaxf(fmaxf(__uint_as_float(u << 16), -INFINITY), __uint_as_float(u & 0xffff0000u));
         }
     }
 };
 
 // sum e^(x - ref) of some elements; two of them joined (nothing so far: -inf, 0).
 struct Mass {
-    double ref, sum;
+    float ref, sum;
 };
 __device__ __forceinline__ Mass join(Mass a, Mass b) {
-    const double t = fmax(a.ref, b.ref);
-    return Mass{t, (a.ref == t ? a.sum : a.sum * (double)ex2((float)(a.ref - t) * kL)) +
-                       (b.ref == t ? b.sum : b.sum * (double)ex2((float)(b.ref - t) * kL))};
+    const float t = fmaxf(a.ref, b.ref);
+    return Mass{t, (a.ref == t ? a.sum : a.sum * ex2((a.ref - t) * kL)) + (b.ref == t ? b.sum : b.sum * ex2((b.ref - t) * kL))};
+}
+
+// A sum of two f32, |lo| at most half a unit of hi: 48 bits (f64 arithmetic is slow here, and
+// every step of the merge would wait for it).
+struct Wide {
+    float hi, lo;
+};
+__device__ __forceinline__ Wide two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return Wide{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Wide add(Wide a, Wide b) {
+    const Wide s = two_sum(a.hi, b.hi);
+    return two_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+// log s = k ln 2 + log m, m in [1, 2): logf's error is 2^-24 of log 2, k ln 2 is exact to 2^-48.
+__device__ __forceinline__ Wide wide_log(float s) {
+    const int k = (int)(__float_as_uint(s) >> 23) - 127;
+    const float m = __uint_as_float((__float_as_uint(s) & 0x007fffffu) | 0x3f800000u);
+    const float hi = 0.693147182464599609375f, lo = -1.904654299957768e-9f, f = (float)k;   // ln 2 in two
+    const float p = __fmul_rn(f, hi);
+    return add(Wide{p, __fadd_rn(__fmaf_rn(f, hi, -p), __fmul_rn(f, lo))}, Wide{logf(m), 0.0f});
 }
 
 struct Shared {
-    union {
+    union alignas(16) {
         uint64_t list[kList];
         uint64_t cand[kMaxCand];
     };
-    float maxima[kNT];
     Mass warp_mass[kWarps];
     uint64_t warp_key[kWarps];
-    double lse[kMaxBeams];
+    float warp_bound[kWarps];
+    Wide base[kMaxBeams];    // cum - log of the mass against the largest logit
     float cum[kMaxBeams], top[kMaxBeams];
     int32_t count[kMaxLists];
     uint64_t best_key[kWarps][kMaxKeep];
     uint64_t best_score[kWarps][kMaxKeep];
     uint8_t best_beam[kWarps][kMaxKeep];
     int32_t best_count[kWarps];
-    int n_list, last;
+    uint4 vec[kVec];
+    uint32_t vec_id[kVec];
+    int n_vec, n_list, last;
 };
 
-__device__ __forceinline__ uint64_t ordered64(double x) {
-    const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);
-    return b ^ ((b >> 63) ? ~0ull : 0x8000000000000000ull);
-}
-__device__ __forceinline__ double from_ordered64(uint64_t o) {
-    return __longlong_as_double((long long)(o ^ ((o >> 63) ? 0x8000000000000000ull : ~0ull)));
-}
+__device__ __forceinline__ uint64_t ordered64(Wide x) { return ((uint64_t)ordered(x.hi) << 32) | ordered(x.lo); }
 // The lane among `who` with the largest v (uniform); those that share it.
 __device__ __forceinline__ unsigned warp_best(unsigned who, uint64_t v, int lane) {
     const bool in = (who >> lane) & 1u;
@@ -209,8 +252,49 @@ __device__ __forceinline__ int merge_lists(int keep, int n, int beam, int lane, 
     return found;
 }
 
+// How many of the first n keys are better than k.
+__device__ __forceinline__ int rank_of(const uint64_t* list, int n, uint64_t k) {
+    int rank = 0, j = 0;
+#pragma unroll 4
+    for (; j + 1 < n; j += 2) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(list + j);
+        rank += (x.x > k) + (x.y > k);
+    }
+    return j < n ? rank + (list[j] > k) : rank;
+}
+// Elements of the listed vectors that reach the bound, to the list of keys.  By the whole CTA; the
+// vectors are stored, the keys need a barrier.
 template <typename T>
-__global__ void __launch_bounds__(kNT) beam_select_kernel(const __grid_constant__ BeamParams p) {
+__device__ __forceinline__ void expand(Shared& sm, int n_vec, float bound) {
+    constexpr int V = Row<T>::V;
+    for (int i = threadIdx.x; i < n_vec * V; i += kNT) {
+        const int at = i / V, e = i % V;
+        const float f = sizeof(T) == 4 ? reinterpret_cast<const float*>(&sm.vec[at])[e]
+                                       : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(&sm.vec[at])[e] << 16);
+        if (f >= bound && f > -INFINITY) {
+            const int to = atomicAdd(&sm.n_list, 1);
+            if (to < kList) sm.list[to] = make_key(f, sm.vec_id[at] * V + e);
+        }
+    }
+}
+// The sum of a trip that holds NaN, infinite logits (these share the whole mass: their number) or large ones.
+template <typename T>
+__device__ __noinline__ float odd_sum(const uint4 (&r)[kTrip], float ref) {
+    constexpr int V = Row<T>::V;
+    float s = 0.0f;
+#pragma unroll 1
+    for (int u = 0; u < kTrip; ++u) {
+        float f[V];
+        Row<T>::floats(u == 0 ? r[0] : u == 1 ? r[1] : u == 2 ? r[2] : r[3], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            s += f[i] == ref ? 1.0f : f[i] < ref ? ex2((f[i] - ref) * kL) : f[i] > ref ? ex2((f[i] - ref) * kL) : 0.0f;
+    }
+    return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kNT, 4) beam_select_kernel(const __grid_constant__ BeamParams p) {
     using R = Row<T>;
     constexpr int V = R::V;
     __shared__ Shared sm;
@@ -220,111 +304,121 @@ __global__ void __launch_bounds__(kNT) beam_select_kernel(const __grid_constant_
     const int64_t row = blockIdx.x / p.splits;
     const int split = (int)(blockIdx.x - row * p.splits);
     const R x(static_cast<const T*>(p.logits) + row * p.stride, p.vocab);
-    const int64_t v0 = split * p.per_split, v1 = min(v0 + p.per_split, x.vectors());
-    const int keep = p.keep;
-    if (tid == 0) sm.n_list = 0;
+    const uint32_t v0 = min(split * p.per_split, x.vectors()), v1 = min(v0 + p.per_split, x.vectors());
+    const int keep = p.keep, share = (keep + kWarps - 1) / kWarps;
+    if (tid == 0) sm.n_list = sm.n_vec = 0;
 
-    float ref = -INFINITY;
-    float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float ref = -INFINITY, sum = 0.0f;
     float bound = -INFINITY;
     bool first = true;
-    for (int64_t t0 = v0; t0 < v1; t0 += kTrip * kNT) {
-        uint4 r[kTrip];
-        float top = -INFINITY;
+    uint4 r[kTrip];
+    x.load(r, v0 + tid, kNT, v1);
+    float rl = 0.0f, off = 1.0f;   // ref l in f32; 2^(what that rounding added)
+    int trip = 0;
+#pragma unroll 1
+    for (uint32_t t0 = v0; t0 < v1; t0 += kTrip * kNT, ++trip) {
+        uint4 ahead[kTrip];
+        x.load(ahead, t0 + kTrip * kNT + tid, kNT, v1);
+        float vtop[kTrip], top = -INFINITY;
 #pragma unroll
         for (int u = 0; u < kTrip; ++u) {
-            const int64_t v = t0 + u * kNT + tid;
-            r[u] = v < v1 ? x.load(v)
-                          : (sizeof(T) == 4 ? make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u)
-                                            : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u));
-        }
-#pragma unroll
-        for (int u = 0; u < kTrip; ++u) {
-            float f[V];
-            R::floats(r[u], f);
-#pragma unroll
-            for (int i = 0; i < V; ++i) top = fmaxf(top, f[i]);
+            vtop[u] = R::top(r[u]);
+            top = fmaxf(top, vtop[u]);
         }
         if (top > -INFINITY) {
-            if (top == INFINITY || ref == INFINITY) {   // infinite logits share the whole mass
-                if (ref != INFINITY) s4[0] = s4[1] = s4[2] = s4[3] = 0.0f;
-                ref = INFINITY;
-#pragma unroll
-                for (int u = 0; u < kTrip; ++u) {
-                    float f[V];
-                    R::floats(r[u], f);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) s4[i & 3] += f[i] == INFINITY ? 1.0f : 0.0f;
-                }
-            } else {
-                if (top > ref + 16.0f) {   // sums of terms up to e^16 stay well inside f32
-                    const float k = ref == -INFINITY ? 0.0f : ex2((ref - top) * kL);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s4[i] *= k;
-                    ref = top;
-                }
-#pragma unroll
-                for (int u = 0; u < kTrip; ++u) {
-                    float f[V];
-                    R::floats(r[u], f);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) s4[i & 3] += ex2((f[i] - ref) * kL);
-                }
+            if (top > ref + 16.0f || top == INFINITY) {   // sums of terms up to e^16 stay well inside f32
+                sum = ref == top ? sum : ref == -INFINITY ? 0.0f : sum * ex2((ref - top) * kL);
+                ref = top;
+                rl = ref * kL;
+                off = ex2(__fmaf_rn(-ref, kL, rl));
             }
-        }
-        if (first) {
-            sm.maxima[tid] = top;
-            __syncthreads();
-            // rank of this thread's maximum; the one of rank keep - 1 is the bound
-            int rank = 0;
-            for (int i = 0; i < kNT; i += 4) {
-                const float4 o = *reinterpret_cast<const float4*>(&sm.maxima[i]);
-                rank += o.x > top || (o.x == top && i < tid);
-                rank += o.y > top || (o.y == top && i + 1 < tid);
-                rank += o.z > top || (o.z == top && i + 2 < tid);
-                rank += o.w > top || (o.w == top && i + 3 < tid);
-            }
-            __syncthreads();
-            if (rank == keep - 1) sm.maxima[0] = top;
-            __syncthreads();
-            bound = sm.maxima[0];
-        }
-        if (top > bound || (first && top == bound && top > -INFINITY)) {
+            float part[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int u = 0; u < kTrip; ++u) {
                 float f[V];
                 R::floats(r[u], f);
-                const int64_t e = (t0 + u * kNT + tid) * V;
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (f[i] > bound || (first && f[i] == bound && f[i] > -INFINITY)) {
-                        const int at = atomicAdd(&sm.n_list, 1);
-                        if (at < kList) sm.list[at] = make_key(f[i], (uint32_t)(e + i));
+                for (int i = 0; i < V; ++i) part[i & 1] += ex2(__fmaf_rn(f[i], kL, -rl));
+            }
+            const float all = (part[0] + part[1]) * off;
+            // NaN or infinite logits, and such that ref l is off by more than 2^-4
+            sum += all == all && fabsf(ref) <= 0x1p19f ? all : odd_sum<T>(r, ref);
+        }
+        if (first) {
+            // a warp's share-th largest of its lanes' maxima; the least of the warps' is reached by
+            // `keep` elements at least
+            float mine = top, reach = -INFINITY;
+            for (int k = 0; k < share; ++k) {
+                const uint32_t best = __reduce_max_sync(kFull, ordered(mine));
+                reach = from_ordered(best);
+                const unsigned who = __ballot_sync(kFull, ordered(mine) == best);
+                if (lane == __ffs(who) - 1) mine = -INFINITY;
+            }
+            if (lane == 0) sm.warp_bound[warp] = reach;
+            __syncthreads();
+            bound = sm.warp_bound[0];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) bound = fminf(bound, sm.warp_bound[w]);
+        }
+        if (top >= bound && top > -INFINITY) {
+#pragma unroll
+            for (int u = 0; u < kTrip; ++u)
+                if (vtop[u] > bound || (first && vtop[u] == bound)) {
+                    const int at = atomicAdd(&sm.n_vec, 1);
+                    if (at < kVec) {
+                        sm.vec[at] = r[u];
+                        sm.vec_id[at] = t0 + u * kNT + tid;
                     }
+                }
+        }
+        // once some more than `keep` are listed, the best `keep` stay and the last of them is the bound
+        if (t0 + kTrip * kNT < v1 && (trip < 2 || (trip & 3) == 0) &&
+            __syncthreads_or(tid == 0 && sm.n_vec + sm.n_list >= keep + 16)) {
+            const int n_vec = sm.n_vec, listed = sm.n_list;
+            __syncthreads();   // read by all before it grows
+            if (n_vec <= kVec && listed <= kList) {
+                expand<T>(sm, n_vec, bound);
+                __syncthreads();
+                const int n = sm.n_list;
+                if (n <= kNT) {   // else the list waits
+                    const uint64_t k = tid < n ? sm.list[tid] : 0ull;
+                    const int rank = 32 * warp < n ? rank_of(sm.list, n, k) : 0;
+                    __syncthreads();
+                    if (tid < n && rank < keep) sm.list[rank] = k;
+                    if (tid == 0) sm.n_list = min(n, keep);
+                }
+                if (tid == 0) sm.n_vec = 0;
+                __syncthreads();
+                if (n <= kNT && n >= keep) bound = key_value(sm.list[keep - 1]);
             }
         }
         first = false;
+#pragma unroll
+        for (int u = 0; u < kTrip; ++u) r[u] = ahead[u];
     }
-    // the slice's sum: references and partial sums joined in f64, in a fixed order
-    Mass mass{ref, ((double)s4[0] + s4[1]) + ((double)s4[2] + s4[3])};
+    // the slice's sum, joined in a fixed order
+    Mass mass{ref, sum};
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1)
         mass = join(mass, Mass{__shfl_xor_sync(kFull, mass.ref, o), __shfl_xor_sync(kFull, mass.sum, o)});
     if (lane == 0) sm.warp_mass[warp] = mass;
     __syncthreads();
-    const int n = sm.n_list;
+    const int n_vec = sm.n_vec, listed = sm.n_list;
+    __syncthreads();
+    if (n_vec <= kVec && listed <= kList) expand<T>(sm, n_vec, bound);
+    __syncthreads();
+    const int n = n_vec <= kVec ? sm.n_list : kList + 1;
     const int64_t out = row * p.splits + split;
     if (tid == 0) {
         mass = sm.warp_mass[0];
         for (int w = 1; w < kWarps; ++w) mass = join(mass, sm.warp_mass[w]);
-        p.sums[out] = make_double2(mass.ref, mass.sum);
+        p.sums[out] = make_float2(mass.ref, mass.sum);
     }
     uint64_t* keys = p.keys + out * keep;
     if (n <= kList) {
         for (int i = tid; i < n; i += kNT) {
             const uint64_t k = sm.list[i];
-            int rank = 0;
-            for (int j = 0; j < n; ++j) rank += sm.list[j] > k;
+            const int rank = rank_of(sm.list, n, k);
             if (rank < keep) keys[rank] = k;
         }
         if (tid == 0) p.counts[out] = min(n, keep);
@@ -333,14 +427,13 @@ __global__ void __launch_bounds__(kNT) beam_select_kernel(const __grid_constant_
         int found = 0;
         for (; found < keep; ++found) {
             uint64_t best = 0ull;
-            for (int64_t v = v0 + tid; v < v1; v += kNT) {
+            for (uint32_t v = v0 + tid; v < v1; v += kNT) {
                 float f[V];
                 R::floats(x.load(v), f);
-                const int64_t e = v * V;
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (f[i] > -INFINITY) {
-                        const uint64_t k = make_key(f[i], (uint32_t)(e + i));
+                    if (f[i] > -INFINITY) {   // no NaN either
+                        const uint64_t k = make_key(f[i], v * V + i);
                         if (k < before && k > best) best = k;
                     }
             }
@@ -371,30 +464,36 @@ __global__ void __launch_bounds__(kNT) beam_select_kernel(const __grid_constant_
     for (int i = tid; i < lists * keep; i += kNT) sm.cand[i] = __ldcg(p.keys + list0 * keep + i);
     if (tid < lists) sm.count[tid] = __ldcg(p.counts + list0 + tid);
     if (tid < p.n_beams) {
-        Mass mass{-INFINITY, 0.0};
+        Mass mass{-INFINITY, 0.0f};
         float top = -INFINITY;
         for (int i = 0; i < p.splits; ++i) {
             const int64_t l = list0 + tid * p.splits + i;
-            const double2 o = __ldcg(p.sums + l);
+            const float2 o = __ldcg(p.sums + l);
             mass = join(mass, Mass{o.x, o.y});
             if (__ldcg(p.counts + l) > 0) top = fmaxf(top, key_value(__ldcg(p.keys + l * keep)));
         }
-        // log of the mass against the largest logit
+        const float cum = p.scores[seq * p.n_beams + tid];
         sm.top[tid] = top;
-        sm.lse[tid] = top == INFINITY ? log(mass.sum) : (mass.ref - (double)top) + log2(mass.sum) / (double)kL;
-        sm.cum[tid] = p.scores[seq * p.n_beams + tid];
+        sm.cum[tid] = cum;
+        // log of the mass against the largest logit (its reference is no further than 16 below)
+        const Wide l = wide_log(mass.sum), away = top == INFINITY ? Wide{0.0f, 0.0f} : two_sum(top, -mass.ref);
+        sm.base[tid] = add(Wide{cum, 0.0f}, add(away, Wide{-l.hi, -l.lo}));
     }
     __syncthreads();
     const int beam = tid < lists ? tid / p.splits : 0;
     const float cum = sm.cum[beam];
     const float top = sm.top[beam];
     const bool alive = fabsf(cum) <= 3.402823466e38f;
-    const double lse = sm.lse[beam];
+    const Wide base = sm.base[beam];
     const uint64_t* mine = sm.cand + tid * keep;
+    // cum + (v - top) - log mass; what lies past f32 counts as its end
     auto score = [&](int i) -> uint64_t {
         const float v = key_value(mine[i]);
-        const double sc = (double)cum + ((v == top ? 0.0 : (double)v - (double)top) - lse);
-        return sc > -INFINITY ? ordered64(sc) : 0ull;   // beside an infinite logit
+        if (v == top) return ordered64(base);
+        if (top == INFINITY) return 0ull;   // beside an infinite logit
+        Wide d = two_sum(v, -top);
+        if (!(d.hi >= -3.4e38f)) d = Wide{-3.4e38f, 0.0f};
+        return ordered64(add(base, d));
     };
     const int n_mine = tid < lists && alive ? sm.count[tid] : 0;
     const int warps = (lists + 31) / 32;
@@ -402,7 +501,7 @@ __global__ void __launch_bounds__(kNT) beam_select_kernel(const __grid_constant_
     int32_t* op = p.parents + seq * keep;
     int32_t* ot = p.tokens + seq * keep;
     auto emit = [&](int k, uint64_t sc, uint64_t key, int bm) {
-        os[k] = (float)from_ordered64(sc);
+        os[k] = from_ordered((uint32_t)(sc >> 32));
         op[k] = (int32_t)(seq * p.n_beams + bm);
         ot[k] = (int32_t)key_index(key);
     };
@@ -454,9 +553,9 @@ __global__ void __launch_bounds__(kNT) beam_select_kernel(const __grid_constant_
         }
 }
 
-// Slices of a row: CTAs for 8 a SM, slices of at least 16 KB, lists within a request's limits.
+// Slices of a row: 3 CTAs a SM at least, slices of at least 16 KB, lists within a request's limits.
 int splits_for(int64_t rows, int32_t n_beams, int64_t vocab, int32_t keep, int size) {
-    int64_t s = (152 * 8 + rows - 1) / std::max<int64_t>(1, rows);
+    int64_t s = (152 * 3 + rows - 1) / std::max<int64_t>(1, rows);
     s = std::min<int64_t>(s, vocab * size / 16384);
     s = std::min<int64_t>(s, std::min(kMaxLists / n_beams, kMaxCand / (n_beams * keep)));
     return (int)std::max<int64_t>(1, s);
@@ -469,7 +568,7 @@ size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 size_t beam_workspace_bytes(int32_t n_seq, int32_t n_beams, int64_t vocab, int32_t keep) {
     const int64_t rows = (int64_t)n_seq * n_beams;
     const size_t lists = (size_t)rows * splits_for(rows, n_beams, vocab, keep, 4);
-    return kWsHeader + round_up((size_t)n_seq * 4) + lists * (sizeof(double2) + 8 * (size_t)keep + 4);
+    return kWsHeader + round_up((size_t)n_seq * 4) + lists * (sizeof(float2) + 8 * (size_t)keep + 4);
 }
 
 cudaError_t launch_beam_select(const void* logits, kvq_dtype dt, int64_t row_stride, int32_t n_seq, int32_t n_beams,
@@ -485,7 +584,7 @@ cudaError_t launch_beam_select(const void* logits, kvq_dtype dt, int64_t row_str
     p.keep = keep;
     p.splits = splits_for(rows, n_beams, vocab, keep, size);
     const int64_t v = 16 / size, vectors = (vocab + v - 1) / v;
-    p.per_split = (vectors + p.splits - 1) / p.splits;
+    p.per_split = (uint32_t)((vectors + p.splits - 1) / p.splits);
     p.scores = scores;
     p.out_scores = out_scores;
     p.parents = parents;
@@ -493,7 +592,7 @@ cudaError_t launch_beam_select(const void* logits, kvq_dtype dt, int64_t row_str
     char* ws = static_cast<char*>(workspace) + kWsHeader;
     p.tickets = reinterpret_cast<uint32_t*>(ws);
     ws += round_up((size_t)n_seq * 4);
-    p.sums = reinterpret_cast<double2*>(ws);
+    p.sums = reinterpret_cast<float2*>(ws);
     p.keys = reinterpret_cast<uint64_t*>(p.sums + rows * p.splits);
     p.counts = reinterpret_cast<int32_t*>(p.keys + rows * p.splits * keep);
     const int64_t grid = rows * p.splits;

@@ -10,7 +10,8 @@
 // c of C takes the numbers [V c / C, V (c+1) / C): the same work for every CTA,
 // whatever the lengths, and no length is read back by the host.  A tile that one CTA
 // finishes is written at once; of a cut one, each CTA leaves its partial state
-// in the workspace, and the CTA that comes last joins the states, in the rows' order.
+// in the workspace, and a second kernel joins the states, in the rows' order.  (Joined by
+// the CTA that came last, 38 states of 16 x 256 took some 25 us.)
 //
 // The numbering needs sum_{i<j} units(i) in closed form.  Unmasked, units is the same
 // for every tile.  Causal, with base = rows - n, for tiles with limit >= 1 but the last,
@@ -38,13 +39,19 @@ struct GqaParams {
     int64_t max_tok;
     float sm_scale;
     int32_t* err;
-    uint32_t* tickets;        // [CTAs], of the tile that CTA c begins and does not end
+    struct GqaCut* cuts;      // [CTAs]
     float2* ws_ml;            // [2 CTAs][M]
     float* ws_o;              // [2 CTAs][M * D], a kernel's own order
 };
 
 struct GqaSeq {
     int64_t q0, n, base, rows, tiles, j0, D, before, per_head;
+};
+// The tile that a CTA begins and does not end: how many CTAs share it (0: there is none), where its outputs go.
+struct GqaCut {
+    int32_t count, h, vec0, vecs;
+    int64_t q0;
+    int64_t pad;
 };
 // Part of a tile, as its CTA works on it (row counts fit 32 bits: a pool has fewer rows).
 struct GqaSegment {
@@ -62,6 +69,8 @@ struct GqaSegment {
 template <int M, int N, int OV>
 struct GqaWalk {
     static_assert(N % M == 0, "closed form");
+    template <int NT>
+    static constexpr int kScratch = NT / 32 + 2 + sizeof(GqaSeq) / 8;
     int64_t v_end, total, ctas, c;
     int32_t b;
     int64_t x;        // h * tiles + j of the current tile
@@ -121,7 +130,7 @@ struct GqaWalk {
         return k;
     }
 
-    // By all NT threads; part: NT / 32 + 10 int64s.  False when CTA k has nothing to do.
+    // By all NT threads; part: kScratch<NT> int64s.  False when CTA k has nothing to do.
     template <int NT>
     __device__ __forceinline__ bool start(const GqaParams& p, int64_t k, int64_t n_cta, int64_t* part) {
         const int tid = threadIdx.x;
@@ -143,9 +152,10 @@ struct GqaWalk {
                     continue;
                 }
                 if (v0 >= first + incl - n && v0 < first + incl) {
-                    int64_t* own = part + NT / 32;
-                    own[0] = k0 + tid;
-                    own[1] = first + incl - n;
+                    GqaSeq* own = reinterpret_cast<GqaSeq*>(part + NT / 32 + 2);
+                    *own = y;
+                    part[NT / 32] = k0 + tid;
+                    part[NT / 32 + 1] = first + incl - n;
                 }
                 first += sum;
                 if (v0 < first) break;
@@ -160,7 +170,7 @@ struct GqaWalk {
         __syncthreads();
         b = (int32_t)part[NT / 32];
         seq_v = part[NT / 32 + 1];
-        s = shape(p, b);
+        s = *reinterpret_cast<const GqaSeq*>(part + NT / 32 + 2);
         const int64_t h = quot(v0 - seq_v, s.per_head), v = v0 - seq_v - h * s.per_head;
         int64_t lo = 0, hi = s.tiles;
         while (hi - lo > 1) {
@@ -245,6 +255,7 @@ __device__ __forceinline__ int32_t gqa_page(const GqaParams& p, int32_t b, int32
     return id;
 }
 
-constexpr int kGqaMaxCtas = 608;
+constexpr int kGqaMaxCtas = 760;
+constexpr size_t kGqaCutBytes = kGqaMaxCtas * sizeof(GqaCut);
 
 }  // namespace kvq

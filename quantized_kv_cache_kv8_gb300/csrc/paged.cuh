@@ -14,9 +14,9 @@ namespace kvq {
 // kernel lets its successor come at once and, before it touches global memory, waits
 // for its predecessor to have completed, which had waited for its own.
 template <class K, class... A>
-cudaError_t launch_chained(K* kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t stream, A&&... args) {
+cudaError_t launch_chained(K* kernel, dim3 grid, unsigned block, size_t smem, cudaStream_t stream, A&&... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;

@@ -57,7 +57,6 @@ def test_decode(kvq, dtype, dim, heads, kv):
     out, ws = attend(kvq, pool, q, lens, new, extra=2)
     close(out[:-2], attention(q[:-2], pool, lens, new, 1 / math.sqrt(dim), True))
     assert kvq.read_device_error(ws) == 0
-    assert int(ws.view(torch.int32)[64:64 + 608].abs().sum()) == 0   # tickets returned
 
 
 @pytest.mark.parametrize("dtype", DT)
