@@ -6,13 +6,13 @@
 // turns as 64-bit fractions (see rope.cu).  A row of D values gets s = amax / 448 and
 // the codes e4m3(x / s), the bytes kv8_encode gives for the rotated f32 row.
 //
-// What bounds it: memory (queries in and out, keys and values in, codes out).  A CTA
-// serves one token: a group of T threads holds one head's row, 16 bytes or two times
-// 16 a thread, and runs through the token's heads with the same dims, so a thread works
-// out its dims' cos and sin once.  Keys and values come first: their chain (load,
-// rotate, amax over the group, codes) is the longest.
+// What bounds it: memory (queries in and out, keys and values in, codes out).  A group of
+// D / 8 threads holds one head's row, 8 elements a thread.  The rows of all tokens are
+// numbered through and a CTA takes a run of them; the cos and sin of its tokens are shared
+// by their heads, so it tabulates them first.
 #include "gqa.cuh"
 
+#include <algorithm>
 #include <math.h>
 
 namespace kvq {
@@ -20,11 +20,16 @@ namespace {
 
 constexpr int kNT = 256;
 constexpr int kMaxPairs = 64;
+constexpr int kSpan = 18;   // tokens a CTA's rows may belong to
 
 struct AppendParams {
     GqaAppendCall c;
     int32_t rot, pairs, shift;
     int64_t pool_rows;
+    int64_t total;      // rows of all tokens
+    int32_t per_tok;    // of one token
+    int32_t per_cta;
+    uint32_t ctas;
     uint64_t inc[kMaxPairs];
     uint8_t axis[kMaxPairs];
 };
@@ -66,115 +71,112 @@ __device__ __forceinline__ void store_elems(T* dst, const float (&x)[E]) {
     }
 }
 
-// E elements a thread: 8, a row of D by D / 8 threads.
 template <typename T, int D, bool VEC, bool ADJ>
 __global__ void __launch_bounds__(kNT) gqa_append_kernel(const __grid_constant__ AppendParams p) {
-    constexpr int E = 8, T_ = D / E, kRows = kNT / T_;   // threads of a row, rows a CTA holds at once
+    constexpr int E = 8, kGroup = D / E, kRows = kNT / kGroup;   // threads of a row, rows a CTA holds at once
+    __shared__ float2 table[kSpan][kMaxPairs];
     launch_dependents();
     grid_dependency_wait();
     const GqaAppendCall& a = p.c;
-    const int tid = threadIdx.x, t = tid % T_, d0 = t * E;
-    const int64_t tok = blockIdx.x;
-    // this thread's cos and sin: of pair (d / 2) or (d mod pairs), with the partner's sign
-    float cs[E], sn[E];
-    const bool turns = d0 < p.rot;
-    if (turns) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int d = d0 + i, k = min(ADJ ? d / 2 : (d < p.pairs ? d : d - p.pairs), p.pairs - 1);
-            if (ADJ && (i & 1)) {
-                cs[i] = cs[i - 1];
-                sn[i] = -sn[i - 1];
-            } else {
-                const int64_t pos = a.positions[p.axis[k] * a.pos_stride + tok];
-                const int64_t phase = (int64_t)((uint64_t)pos * p.inc[k]);
-                sincospif(__ll2float_rn(phase) * 0x1p-63f, &sn[i], &cs[i]);
-                // x cos - y sin for the first of a pair, x cos + y sin for the second
-                if (ADJ || d < p.pairs) sn[i] = -sn[i];
-            }
-            if (d >= p.rot) {
-                cs[i] = 1.0f;
-                sn[i] = 0.0f;
-            }
+    const int tid = threadIdx.x, t = tid % kGroup, d0 = t * E;
+    const int n_kv = a.k ? a.n_kv_heads : 0;
+    const int64_t u0 = (int64_t)blockIdx.x * p.per_cta;
+    const int count = (int)min((int64_t)p.per_cta, p.total - u0);
+    const int64_t t0 = u0 / p.per_tok;
+    const int off0 = (int)(u0 - t0 * p.per_tok);   // the run's first row within token t0
+    if (p.rot > 0) {
+        const int n_tok = (off0 + count - 1) / p.per_tok + 1;
+        for (int i = tid; i < n_tok * p.pairs; i += kNT) {
+            const int tok = i / p.pairs, k = i - tok * p.pairs;
+            const int64_t pos = a.positions[p.axis[k] * a.pos_stride + t0 + tok];
+            const int64_t phase = (int64_t)((uint64_t)pos * p.inc[k]);
+            float2 cs;
+            sincospif(__ll2float_rn(phase) * 0x1p-63f, &cs.y, &cs.x);
+            table[tok][k] = cs;
         }
+        __syncthreads();
     }
-    const int64_t slot = a.k ? a.slots[tok] : -1;
-    const bool store = slot >= 0 && slot < p.pool_rows;
-    if (a.k && slot >= p.pool_rows && tid == 0 && a.err) atomicCAS(a.err, 0, (int32_t)KVQ_ERR_ARG);
-    const int n_kv = a.k ? a.n_kv_heads : 0, n_rows = 2 * n_kv + a.n_heads;
-    const int64_t page_row = store ? ((slot >> p.shift) * a.n_kv_heads << p.shift) + (slot & ((1ll << p.shift) - 1)) : 0;
+    const bool turns = d0 < p.rot, first = ADJ || d0 < p.pairs;
     // every thread of a warp makes every trip: rows past the last are not stored
-    for (int row0 = 0; row0 < n_rows; row0 += kRows) {
-        const int row = row0 + tid / T_;
-        const bool live = row < n_rows, query = row >= 2 * n_kv, value = !query && row >= n_kv;
+#pragma unroll 2
+    for (int i0 = 0; i0 < count; i0 += kRows) {
+        const int i = i0 + tid / kGroup, y_ = off0 + min(i, count - 1), tok = y_ / p.per_tok, row = y_ - tok * p.per_tok;
+        const bool live = i < count, query = row >= 2 * n_kv, value = !query && row >= n_kv;
         const int h = query ? row - 2 * n_kv : value ? row - n_kv : row;
-        const T* src = query ? static_cast<const T*>(a.qi) + tok * a.qi_token + (int64_t)h * a.qi_head
-                       : value ? static_cast<const T*>(a.v) + tok * a.v_token + (int64_t)h * a.v_head
-                               : static_cast<const T*>(a.k) + tok * a.k_token + (int64_t)h * a.k_head;
+        const T* src = query ? static_cast<const T*>(a.qi) + (t0 + tok) * a.qi_token + (int64_t)h * a.qi_head
+                       : value ? static_cast<const T*>(a.v) + (t0 + tok) * a.v_token + (int64_t)h * a.v_head
+                               : static_cast<const T*>(a.k) + (t0 + tok) * a.k_token + (int64_t)h * a.k_head;
         float x[E], y[E];
-        if (live) load_elems<T, E, VEC>(x, src + d0);
-        if (live && turns && !value) {
+        load_elems<T, E, VEC>(x, src + d0);
+        if (turns && !value) {
             if (ADJ) {
 #pragma unroll
-                for (int i = 0; i < E; ++i) y[i] = x[i ^ 1];
+                for (int j = 0; j < E; ++j) y[j] = x[j ^ 1];
             } else if (p.pairs % E == 0) {
-                load_elems<T, E, VEC>(y, src + (d0 < p.pairs ? d0 + p.pairs : d0 - p.pairs));
+                load_elems<T, E, VEC>(y, src + (first ? d0 + p.pairs : d0 - p.pairs));
             } else {
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const int d = d0 + i;
-                    y[i] = d >= p.rot ? 0.0f : to_f(src[d < p.pairs ? d + p.pairs : d - p.pairs]);
+                for (int j = 0; j < E; ++j) {
+                    const int d = d0 + j;
+                    y[j] = d >= p.rot ? 0.0f : to_f(src[d < p.pairs ? d + p.pairs : d - p.pairs]);
                 }
             }
-            // each product rounded, then one sum
+            // x cos - y sin for the first of a pair, x cos + y sin for the second: each product
+            // rounded, then one sum
 #pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (d0 + i < p.rot) x[i] = __fadd_rn(__fmul_rn(x[i], cs[i]), __fmul_rn(y[i], sn[i]));
+            for (int j = 0; j < E; ++j) {
+                const int d = d0 + j, k = ADJ ? d / 2 : d < p.pairs ? d : d - p.pairs;
+                if (d < p.rot) {
+                    const float2 cs = table[tok][k];
+                    const bool one = ADJ ? (j & 1) == 0 : d < p.pairs;
+                    x[j] = __fadd_rn(__fmul_rn(x[j], cs.x), __fmul_rn(y[j], one ? -cs.y : cs.y));
+                }
+            }
         }
         __syncwarp();   // a head rotated in place: read before it is written
-        if (query) {
-            if (live) store_elems<T, E, VEC>(static_cast<T*>(a.qo) + tok * a.qo_token + (int64_t)h * a.qo_head + d0, x);
-        }
+        if (query && live)
+            store_elems<T, E, VEC>(static_cast<T*>(a.qo) + (t0 + tok) * a.qo_token + (int64_t)h * a.qo_head + d0, x);
+        if (!__any_sync(kFull, !query)) continue;
         float amax = 0.0f;
         bool bad = false;
-        if (live && !query) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                bad |= !(fabsf(x[i]) <= 3.402823466e38f);
-                amax = fmaxf(amax, fabsf(x[i]));
-            }
+        for (int j = 0; j < E; ++j) {
+            bad |= !(fabsf(x[j]) <= 3.402823466e38f);
+            amax = fmaxf(amax, fabsf(x[j]));
         }
-        if (row0 < 2 * n_kv) {   // alike for the whole CTA
 #pragma unroll
-            for (int o = T_ / 2; o >= 1; o >>= 1) {
-                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-                bad |= __shfl_xor_sync(kFull, (int)bad, o) != 0;
-            }
-            if (live && !query && store) {
-                const float s = __fdiv_rn(amax, 448.0f);
-                uint32_t w[2] = {0u, 0u};
-                if (s != 0.0f && !bad) {
+        for (int o = kGroup / 2; o >= 1; o >>= 1) {
+            amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+            bad |= __shfl_xor_sync(kFull, (int)bad, o) != 0;
+        }
+        if (!live || query) continue;
+        const int64_t slot = a.slots[t0 + tok];
+        if (slot < 0) continue;   // a padded row
+        if (slot >= p.pool_rows) {
+            if (t == 0 && a.err) atomicCAS(a.err, 0, (int32_t)KVQ_ERR_ARG);
+            continue;
+        }
+        const float s = __fdiv_rn(amax, 448.0f);
+        uint32_t w[2] = {0u, 0u};
+        if (s != 0.0f && !bad) {
 #pragma unroll
-                    for (int i = 0; i < E; ++i)
-                        w[i / 4] |= (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(x[i], s), __NV_SATFINITE, __NV_E4M3)
-                                    << (8 * (i & 3));
-                }
-                const int64_t at = page_row + ((int64_t)h << p.shift);
-                *reinterpret_cast<uint2*>((value ? a.v_codes : a.k_codes) + at * D + d0) = make_uint2(w[0], w[1]);
-                // a row that is no number: no codes exist, and its scale says so
-                if (t == 0) {
-                    a.scales[2 * at + value] = bad ? __uint_as_float(0x7fffffffu) : s;
-                    if (bad && a.err) atomicCAS(a.err, 0, (int32_t)KVQ_ERR_NONFINITE);
-                }
-            }
+            for (int j = 0; j < E; ++j)
+                w[j / 4] |= (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(x[j], s), __NV_SATFINITE, __NV_E4M3) << (8 * (j & 3));
+        }
+        const int64_t at = (((slot >> p.shift) * a.n_kv_heads + h) << p.shift) + (slot & ((1ll << p.shift) - 1));
+        *reinterpret_cast<uint2*>((value ? a.v_codes : a.k_codes) + at * D + d0) = make_uint2(w[0], w[1]);
+        // a row that is no number: no codes exist, and its scale says so
+        if (t == 0) {
+            a.scales[2 * at + value] = bad ? __uint_as_float(0x7fffffffu) : s;
+            if (bad && a.err) atomicCAS(a.err, 0, (int32_t)KVQ_ERR_NONFINITE);
         }
     }
 }
 
 template <typename T, int D, bool VEC>
 cudaError_t launch_pairs(const AppendParams& p, bool adj, cudaStream_t st) {
-    return adj ? launch_chained(gqa_append_kernel<T, D, VEC, true>, (unsigned)p.c.n, kNT, 0, st, p)
-               : launch_chained(gqa_append_kernel<T, D, VEC, false>, (unsigned)p.c.n, kNT, 0, st, p);
+    return adj ? launch_chained(gqa_append_kernel<T, D, VEC, true>, p.ctas, kNT, 0, st, p)
+               : launch_chained(gqa_append_kernel<T, D, VEC, false>, p.ctas, kNT, 0, st, p);
 }
 template <typename T, int D>
 cudaError_t launch_width(const AppendParams& p, bool vec, bool adj, cudaStream_t st) {
@@ -205,7 +207,16 @@ cudaError_t launch_gqa_append(const GqaAppendCall& c, cudaStream_t stream) {
     }
     while ((1 << p.shift) < c.page_rows) ++p.shift;
     p.pool_rows = (int64_t)c.n_pages << p.shift;
-    if (c.n > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    p.per_tok = (c.k ? 2 * c.n_kv_heads : 0) + c.n_heads;
+    p.total = c.n * p.per_tok;
+    // up to 4 rows a thread group once that fills the GPU
+    const int64_t rows = kNT * 8 / c.head_dim;
+    int64_t per = 4 * rows;
+    while (per > rows && p.total < per * 304) per /= 2;
+    p.per_cta = (int32_t)std::min<int64_t>(per, (int64_t)p.per_tok * (kSpan - 2));
+    const int64_t ctas = (p.total + p.per_cta - 1) / p.per_cta;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    p.ctas = (uint32_t)ctas;
     // 16-byte accesses where every row starts on 16 bytes
     const int64_t v = c.dtype == KVQ_BF16 ? 8 : 4;
     uintptr_t where = 0;
