@@ -628,11 +628,15 @@ cudaError_t launch_type(const GqaParams& p, kvq_dtype dt, cudaStream_t stream) {
     return dt == KVQ_BF16 ? launch_dims<D, 1, __nv_bfloat16>(p, stream) : launch_dims<D, 2, float>(p, stream);
 }
 
+// Above so many vectors of a sequence and kv head, on average, the tensor-core kernel.
+constexpr int64_t kTensorVectors = 32;
+
 }  // namespace
 
 // Error word, the cut tiles, their maxima and sums, their contexts.
 size_t gqa_attn_workspace_bytes(int32_t head_dim) {
-    return kWsHeader + kGqaCutBytes + (size_t)2 * kGqaMaxCtas * 16 * (sizeof(float2) + head_dim * sizeof(float));
+    const size_t own = (size_t)2 * kGqaMaxCtas * 16 * (sizeof(float2) + head_dim * sizeof(float));
+    return kWsHeader + kGqaCutBytes + std::max(own, gqa_tc_state_bytes(head_dim));
 }
 
 cudaError_t launch_gqa_attn(const GqaAttnCall& c, cudaStream_t stream) {
@@ -660,6 +664,8 @@ cudaError_t launch_gqa_attn(const GqaAttnCall& c, cudaStream_t stream) {
     p.cuts = reinterpret_cast<GqaCut*>(ws + kWsHeader);
     p.ws_ml = reinterpret_cast<float2*>(ws + kWsHeader + kGqaCutBytes);
     p.ws_o = reinterpret_cast<float*>(p.ws_ml + 2 * kGqaMaxCtas * 16);
+    if (gqa_tc_supported(c.head_dim, c.dtype) && p.max_tok * p.group > kTensorVectors * (int64_t)p.n_seq)
+        return launch_gqa_tc(p, c.head_dim, c.dtype, p.ws_ml, stream);
     switch (c.head_dim) {
         case 64: return launch_type<64>(p, c.dtype, stream);
         case 128: return launch_type<128>(p, c.dtype, stream);

@@ -42,6 +42,8 @@ struct GqaParams {
     struct GqaCut* cuts;      // [CTAs]
     float2* ws_ml;            // [2 CTAs][M]
     float* ws_o;              // [2 CTAs][M * D], a kernel's own order
+    float* ws_tot;            // tensor kernel: [CTAs][M * D], totals of long sums
+    int64_t wait_limit, stall_polls;
 };
 
 struct GqaSeq {
@@ -254,6 +256,11 @@ __device__ __forceinline__ int32_t gqa_page(const GqaParams& p, int32_t b, int32
     }
     return id;
 }
+
+// The tensor-core kernel (gqa_tc.cu): f32 queries up to 128 dims.
+size_t gqa_tc_state_bytes(int32_t head_dim);
+bool gqa_tc_supported(int32_t head_dim, kvq_dtype dt);
+cudaError_t launch_gqa_tc(const GqaParams& p, int32_t head_dim, kvq_dtype dt, void* state, cudaStream_t stream);
 
 constexpr int kGqaMaxCtas = 760;
 constexpr size_t kGqaCutBytes = kGqaMaxCtas * sizeof(GqaCut);

@@ -1,0 +1,683 @@
+// gqa_tc.cu -- attention over paged KV8 keys and values where a sequence brings many
+// query vectors to a kv head (prompt chunks, decoder prompts over an encoder's states,
+// wide windows): tiles of 128 vectors on the tensor cores.
+//
+//   S = Q C_k^T (128 vectors x 128 rows), P = 2^(z - R) s_v, O += P C_v
+// with z = S s_k sm log2(e), the codes in f16 (exact), f32 accumulators in tensor memory.
+//
+// What bounds it: shared memory (256 vectors x 128 rows x D = 128 read 192 KB of operands
+// and move 192 KB of converted codes, at 128 bytes a cycle 3,000 cycles, for 2,048 of
+// products) and the softmax (about 4.5 instructions a score).  So two CTAs share an SM, one's
+// softmax beside the other's products, and the weights go into the second product from
+// tensor memory, over the scores they came from, instead of through shared memory.
+//   * warps 0-3: softmax, a vector a thread, so maxima and sums need no exchange; 32 scores at
+//     a time are loaded, turned into 32 weights and stored over the first half of their
+//     place (f32 queries: two f16 halves, over the whole place);
+//   * warps 4-7: codes to f16, in the layout of 128-byte swizzled rows, which the first
+//     product reads with dims along K and the second with rows along K; keys and values are asked
+//     for in turn, each as soon as the other is stored;
+//   * warp 8: one lane issues the products.
+//
+// Numbers.  Queries as in gqa_attn.cu (bf16 exactly, f32 in two f16 halves).  R is an
+// integer per vector, at least max(z + log2 s_v) - 14 when it is set, so weights reach 2^14; it rises
+// when one passes 60000, and then what has been summed is brought to it by a power of two.  bf16
+// queries: weights in one f16 (2^-11 of themselves, down to 2^-28 of the largest).
+// f32 queries: in two (2^-22).  Every 256 steps (f32 queries: 8) the accumulators, which round
+// towards zero, go to totals in the workspace.  Rows that are no numbers as in gqa_attn.cu.
+#include "gqa_common.cuh"
+#include "tc_common.cuh"
+
+#include <algorithm>
+
+namespace kvq {
+namespace {
+
+using namespace tc;
+
+constexpr int kM = 128, kN = 128, kOv = 3;
+constexpr int kSoft = 128, kConv = 128, kNT = kSoft + kConv + 32;
+constexpr float kNone = -3.402823466e38f;
+using Walk = GqaWalk<kM, kN, kOv>;
+
+template <int D, int QP>
+struct Cfg {
+    static constexpr int kChunks = D / 64;                      // of 64 dims, 128 rows x 128 bytes each
+    static constexpr uint32_t kChunk = 128 * 128;
+    static constexpr uint32_t kOffQ = 0, kOffK = QP * kChunks * kChunk, kOffV = kOffK + kChunks * kChunk;
+    static constexpr uint32_t kOffMisc = kOffV + kChunks * kChunk;
+    static constexpr int kCols = D == 256 ? 512 : 256;          // tensor memory: scores and weights, context
+    static constexpr int kColO = 128;
+    // steps between additions to the totals: 8 QP products a step, each off by up to 2^-24 of the
+    // sum towards zero, add up to 8e-6 (f32) and 1.2e-4 of it
+    static constexpr int kFlush = QP == 2 ? 8 : 256;
+    static constexpr int kCtas = D == 256 || (D == 128 && QP == 2) ? 1 : 2;   // an SM
+};
+enum { kBarK, kBarS, kBarV, kBarP, kBarO, kBarDone, kBarNever, kBars };
+
+struct Misc {
+    float sk[2][kN], sv[2][kN];
+    float qs[kM];
+    uint64_t bars[kBars];
+    int64_t part[Walk::kScratch<kNT>];
+    Walk walk;
+    GqaSegment seg;
+    uint32_t tmem;
+    int more, abort;
+};
+
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 un2(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_of(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 ldg16(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Columns of weights of scores 32 j ..: over the first half of their place, or (two halves)
+// over all of it.
+template <int QP>
+__device__ __forceinline__ constexpr uint32_t weight_col(int j) { return QP == 1 ? 16u * j : 32u * j; }
+
+// A vector's reference raised for chunk j of a step (see the file's head), by a whole warp: its weights of
+// the chunks before, its context and its sums are brought to the new one.  Returns it; *alpha: the factor.
+template <int D, int QP>
+__device__ __noinline__ float raise(const Misc& sm, uint32_t tm, int j, int st, float qs, float R, bool lift, int32_t lim,
+                                    int32_t row0, bool context, float* alpha) {
+    uint32_t s[32];
+    tmem_ld32(tm + 32 * j, s);
+    tmem_wait_ld();
+    float y = kNone, zm = kNone;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float sv = fabsf(sm.sv[st][32 * j + i]), z = __uint_as_float(s[i]) * (sm.sk[st][32 * j + i] * qs);
+        if (row0 + 32 * j + i < lim) {
+            zm = fmaxf(zm, z);
+            if (sv > 0.0f) y = fmaxf(y, z + __log2f(sv));
+        }
+    }
+    float n = R;
+    if (lift) n = fmaxf(R, ceilf(fmaxf(y - 14.0f, zm - 100.0f)));
+    if (!(n >= kNone)) n = kNone;   // no score but -inf
+    const float a = n == R ? 1.0f : ex2(R - n);
+    const __half2 a2 = __float2half2_rn(a);
+#pragma unroll 1
+    for (int k = 0; k < j; ++k) {
+        uint32_t w[QP == 1 ? 16 : 32];
+        if constexpr (QP == 1) tmem_ld16(tm + weight_col<QP>(k), w);
+        else tmem_ld32(tm + weight_col<QP>(k), w);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < (QP == 1 ? 16 : 32); ++i) {
+            __half2 h = __hmul2(*reinterpret_cast<__half2*>(&w[i]), a2);
+            w[i] = *reinterpret_cast<uint32_t*>(&h);
+        }
+        if constexpr (QP == 1) tmem_st16(tm + weight_col<QP>(k), w);
+        else tmem_st32(tm + weight_col<QP>(k), w);
+    }
+    if (context) {
+#pragma unroll 1
+        for (int k = 0; k < D / 32; ++k) {
+            uint32_t o[32];
+            tmem_ld32(tm + Cfg<D, QP>::kColO + 32 * k, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+            tmem_st32(tm + Cfg<D, QP>::kColO + 32 * k, o);
+        }
+    }
+    tmem_wait_st();
+    *alpha = a;
+    return n;
+}
+
+// Scores 32 j .. of a step to weights; their sum.  PART: some are hidden from some vector.
+template <int QP, bool PART>
+__device__ __forceinline__ float weights(const Misc& sm, uint32_t tm, int j, int st, float qs, float R, int32_t visible,
+                                         uint32_t (&pk)[QP == 1 ? 16 : 32], float* most) {
+    uint32_t s[32];
+    tmem_ld32(tm + 32 * j, s);
+    tmem_wait_ld();
+    const F2 qs2 = f2(qs, qs), r2 = f2(-R, -R);
+    F2 sum[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+    float top = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const float4 k4 = *reinterpret_cast<const float4*>(&sm.sk[st][32 * j + 4 * q]);
+        const float4 v4 = *reinterpret_cast<const float4*>(&sm.sv[st][32 * j + 4 * q]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = 4 * q + 2 * h;
+            const F2 b = mul2(h == 0 ? f2(k4.x, k4.y) : f2(k4.z, k4.w), qs2);
+            const float2 t = un2(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), b, r2));
+            float2 p = make_float2(ex2(t.x), ex2(t.y));
+            if (PART) {
+                if (c >= visible) p.x = 0.0f;
+                if (c + 1 >= visible) p.y = 0.0f;
+            }
+            const F2 pp = f2(p.x, p.y);
+            sum[h] = add2(sum[h], pp);
+            float2 w = un2(mul2(pp, h == 0 ? f2(v4.x, v4.y) : f2(v4.z, v4.w)));
+            if (PART) {   // a hidden row's scale may be no number
+                if (c >= visible) w.x = 0.0f;
+                if (c + 1 >= visible) w.y = 0.0f;
+            }
+            top = fmaxf(top, fmaxf(fabsf(w.x), fabsf(w.y)));
+            const uint32_t hi = half2_of(w.x, w.y);
+            pk[c / 2] = hi;
+            if constexpr (QP == 2) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                pk[16 + c / 2] = half2_of(w.x - x.x, w.y - x.y);
+            }
+        }
+    }
+    *most = top;
+    const float2 u = un2(add2(sum[0], sum[1]));
+    return u.x + u.y;
+}
+
+// The codes of one step's keys or values as a converter warp holds them: 32 rows, 16 bytes a lane
+// and load, D / 16 lanes a row.
+template <int D>
+struct Codes {
+    static constexpr int kLanes = D / 16, kAt = 32 / kLanes, kLoads = 32 / kAt;   // lanes of a row, rows a load, loads
+    uint4 v[kLoads];
+    // page: of row `lane` of the warp's 32 (-1: none)
+    __device__ __forceinline__ void load(const GqaParams& p, const uint8_t* base, int h, int32_t page, int32_t row0, int lane) {
+        const int32_t in_page = (1 << p.shift) - 1;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = i * kAt + lane / kLanes;
+            const int32_t id = __shfl_sync(kFull, page, r);
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (id >= 0) {
+                const int64_t at = (((int64_t)id * p.n_kv + h) << p.shift) + ((row0 + r) & in_page);
+                v[i] = ldg16(base + at * D + 16 * (lane % kLanes));
+            }
+        }
+    }
+    // to f16 in swizzled rows: region: the operand's first chunk; row0: the warp's first row in it
+    __device__ __forceinline__ void store(unsigned char* region, int row0, int lane) const {
+        const int j = lane % kLanes, c = j / 4, q = j % 4;
+        const bool odd = c & 1;   // lanes of odd chunks store their second half first: other banks
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = row0 + i * kAt + lane / kLanes;
+            uint4 lo, hi;
+            e4m3x4_to_half2x2(v[i].x, lo.x, lo.y);
+            e4m3x4_to_half2x2(v[i].y, lo.z, lo.w);
+            e4m3x4_to_half2x2(v[i].z, hi.x, hi.y);
+            e4m3x4_to_half2x2(v[i].w, hi.z, hi.w);
+            unsigned char* at = region + c * (128 * 128);
+            *reinterpret_cast<uint4*>(at + sw128(r, 32 * q + (odd ? 16 : 0))) = odd ? hi : lo;
+            *reinterpret_cast<uint4*>(at + sw128(r, 32 * q + (odd ? 0 : 16))) = odd ? lo : hi;
+        }
+    }
+    // NaN codes replaced; true for the lane whose row holds one
+    __device__ __forceinline__ bool mend(int lane) {
+        bool mine = false;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v[i]);
+            bool bad = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t nan = (((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+                bad |= nan != 0u;
+                w[k] ^= nan;
+            }
+            const unsigned who = __ballot_sync(kFull, bad);
+            if (lane / kAt == i) mine = (who >> (kLanes * (lane % kAt))) & (kLanes == 32 ? ~0u : (1u << kLanes) - 1u);
+        }
+        return mine;
+    }
+};
+
+// Queries of the tile to f16, two threads a vector; threads 0 .. 255.
+template <int D, int QP, typename QT>
+__device__ __forceinline__ void load_queries(const GqaParams& p, const GqaSegment& g, Misc& sm, unsigned char* sq) {
+    constexpr int E = D / 2;
+    const int r = threadIdx.x / 2, half = threadIdx.x % 2;
+    const bool live = r < g.vecs;
+    const QT* src = static_cast<const QT*>(p.q) + (live ? gqa_vector<D>(p, g, g.vec0 + r) : 0) + half * E;
+    constexpr int V = 16 / sizeof(QT);
+    float amax = 0.0f;
+    auto load8 = [&](int i, float (&x)[8]) {
+#pragma unroll
+        for (int k = 0; k < 8; k += V) {
+            struct alignas(16) { QT e[V]; } v;
+            *reinterpret_cast<uint4*>(&v) =
+                live ? __ldg(reinterpret_cast<const uint4*>(src + 8 * i + k)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[k + e] = (float)v.e[e];
+        }
+    };
+#pragma unroll 4
+    for (int i = 0; i < E / 8; ++i) {
+        float x[8];
+        load8(i, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(x[k]));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+    const int e = max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -110);
+    const float up = __uint_as_float((uint32_t)(127 - e) << 23);
+    if (half == 0) sm.qs[r] = p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll 4
+    for (int i = 0; i < E / 8; ++i) {
+        float x[8];
+        load8(i, x);   // from L1
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float a = x[2 * k] * up, b = x[2 * k + 1] * up;
+            hi[k] = half2_of(a, b);
+            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
+            lo[k] = half2_of(a - h.x, b - h.y);
+        }
+        const int d = half * E + 8 * i;
+        unsigned char* at = sq + (d / 64) * (128 * 128) + sw128(r, 2 * (d % 64));
+        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if constexpr (QP == 2)
+            *reinterpret_cast<uint4*>(at + (D / 64) * (128 * 128)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+}
+
+template <typename QT>
+__device__ __forceinline__ void store8(QT* dst, const float (&x)[8]) {
+    if constexpr (sizeof(QT) == 4) {
+        reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+            w[k] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// State of a cut tile's vector: (log2 of its sum of 2^z, context over that sum).
+template <int D, int QP, typename QT>
+__global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const __grid_constant__ GqaParams p) {
+    extern __shared__ __align__(1024) unsigned char raw[];
+    using C = Cfg<D, QP>;
+    Misc& sm = *reinterpret_cast<Misc*>(raw + C::kOffMisc);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dependency_wait();
+    if (tid == 0) p.cuts[blockIdx.x].count = 0;
+    {
+        Walk walk;
+        if (!walk.template start<kNT>(p, blockIdx.x, gridDim.x, sm.part)) return;
+        if (tid == 0) sm.walk = walk;
+    }
+    if (smem_u32(raw) & 1023u) {   // the swizzle counts on it
+        if (tid == 0) set_err(p.err, KVQ_ERR_DEVICE);
+        return;
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)),
+                     "r"(C::kCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < kBars; ++i)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&sm.bars[i])),
+                         "r"(i == kBarK || i == kBarV || i == kBarP ? 128u : 1u));
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        sm.abort = 0;
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    launch_dependents();   // a kernel that allocates tensor memory may come now: this CTA has its own
+    const uint32_t tmem = sm.tmem;
+    volatile int* abort_flag = &sm.abort;
+    if (p.stall_polls > 0 && tid == 0) mbar_wait(&sm.bars[kBarNever], 0, abort_flag, p.stall_polls);
+    const GqaSegment& seg = sm.seg;
+    uint32_t it = 0;       // steps so far: the barriers' phases
+    uint32_t tiles = 0;
+    for (;; ++tiles) {
+        if (tid == 0) sm.more = sm.walk.get(p, sm.seg);
+        __syncthreads();
+        if (!sm.more || sm.abort) break;
+        const int u0 = seg.u0, n_steps = seg.limit > u0 * kN ? min(seg.u1 - u0, (seg.limit - u0 * kN + kN - 1) / kN) : 0;
+        const int32_t all = gqa_limit(p, seg, seg.vec0);   // rows that all vectors see
+        if (tid < 256) load_queries<D, QP, QT>(p, seg, sm, raw + C::kOffQ);
+        fence_async_smem();
+        __syncthreads();
+        if (warp < 4) {
+            // ---- softmax: vector tid -----------------------------------------------
+            const int32_t lim = gqa_limit(p, seg, seg.vec0 + min(tid, seg.vecs - 1));
+            const float qs = sm.qs[tid];
+            const uint32_t tm = tmem + ((uint32_t)(warp * 32) << 16);
+            float R = kNone, l = 0.0f, Rt = kNone, lt = 0.0f;   // reference and sum; those of the totals
+            float4* tot = reinterpret_cast<float4*>(p.ws_tot) + (int64_t)blockIdx.x * (D / 4) * kM + tid;
+            // accumulators to the totals: first: they start there
+            auto flush = [&](bool first) {
+                const float n = fmaxf(Rt, R), a = first ? 0.0f : ex2(Rt - n), b = ex2(R - n);
+#pragma unroll 1
+                for (int k = 0; k < D / 32; ++k) {
+                    uint32_t o[32];
+                    tmem_ld32(tm + C::kColO + 32 * k, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float4 v = first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : tot[(8 * k + i) * kM];
+                        v.x = v.x * a + __uint_as_float(o[4 * i]) * b;
+                        v.y = v.y * a + __uint_as_float(o[4 * i + 1]) * b;
+                        v.z = v.z * a + __uint_as_float(o[4 * i + 2]) * b;
+                        v.w = v.w * a + __uint_as_float(o[4 * i + 3]) * b;
+                        tot[(8 * k + i) * kM] = v;
+                    }
+                }
+                lt = lt * a + l * b;
+                Rt = n;
+                l = 0.0f;
+            };
+            bool ok = true;
+            for (int s = 0; s < n_steps; ++s) {
+                const uint32_t ph = (it + s) & 1u;
+                const int st = (int)ph;
+                // the scales' writers arrived on the first, the scores are the second's
+                ok = mbar_wait(&sm.bars[kBarK], ph, abort_flag, p.wait_limit) &&
+                     mbar_wait(&sm.bars[kBarS], ph, abort_flag, p.wait_limit);
+                if (!__all_sync(kFull, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_after();
+                if (s > 0 && s % C::kFlush == 0) flush(s == C::kFlush);
+                const int32_t row0 = (u0 + s) * kN;
+                const bool partly = row0 + kN > all, context = s % C::kFlush != 0;
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t pk[QP == 1 ? 16 : 32];
+                    const int32_t visible = min(max(lim - row0 - 32 * j, 0), 32);
+                    float most, sum;
+                    auto run = [&]() {
+                        if (partly) sum = weights<QP, true>(sm, tm, j, st, qs, R, visible, pk, &most);
+                        else sum = weights<QP, false>(sm, tm, j, st, qs, R, 32, pk, &most);
+                    };
+                    run();
+                    const bool lift = (R == kNone && visible > 0) || !(most <= 60000.0f) || !(sum <= 0x1p110f);
+                    if (__any_sync(kFull, lift)) {
+                        float a;
+                        R = raise<D, QP>(sm, tm, j, st, qs, R, lift, lim, row0, context, &a);
+                        l *= a;
+                        run();
+                    }
+                    l += sum;
+                    if constexpr (QP == 1) tmem_st16(tm + weight_col<QP>(j), pk);
+                    else tmem_st32(tm + weight_col<QP>(j), pk);
+                }
+                tmem_wait_st();
+                tc_before();
+                mbar_arrive(&sm.bars[kBarP]);
+            }
+            // the last product's end
+            if (ok && n_steps > 0) ok = mbar_wait(&sm.bars[kBarO], (it + n_steps - 1) & 1u, abort_flag, p.wait_limit);
+            ok = __all_sync(kFull, ok);
+            if (ok) {
+                tc_after();
+                const bool summed = n_steps > C::kFlush;
+                if (summed) flush(false);
+                const float sum = summed ? lt : l, ref = summed ? Rt : R, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const bool live = tid < seg.vecs;
+                QT* out = static_cast<QT*>(p.out) + (live ? gqa_vector<D>(p, seg, seg.vec0 + tid) : 0);
+                float4* dst = reinterpret_cast<float4*>(p.ws_o) + (int64_t)max(seg.slot, 0) * (D / 4) * kM + tid;
+#pragma unroll 1
+                for (int k = 0; k < D / 32; ++k) {
+                    uint32_t o[32];
+                    if (n_steps > 0 && !summed) {
+                        tmem_ld32(tm + C::kColO + 32 * k, o);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = n_steps > 0 && !summed ? __uint_as_float(o[8 * i + e]) : 0.0f;
+                        if (summed) {
+                            const float4 a = tot[(8 * k + 2 * i) * kM], b = tot[(8 * k + 2 * i + 1) * kM];
+                            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+                            x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] *= inv;
+                        if (seg.slot < 0) {
+                            if (live) store8(out + 32 * k + 8 * i, x);
+                        } else {
+                            dst[(8 * k + 2 * i) * kM] = make_float4(x[0], x[1], x[2], x[3]);
+                            dst[(8 * k + 2 * i + 1) * kM] = make_float4(x[4], x[5], x[6], x[7]);
+                        }
+                    }
+                }
+                if (seg.slot >= 0)
+                    p.ws_ml[seg.slot * kM + tid] = make_float2(sum == 0.0f ? kNone : ref + log2f(sum), 0.0f);
+                if (tid == 0 && seg.slot >= 0 && seg.u0 == 0)
+                    p.cuts[blockIdx.x] = GqaCut{seg.count, seg.h, seg.vec0, seg.vecs, seg.q0, 0};
+            }
+        } else if (warp < 8) {
+            // ---- codes to f16: rows 32 (warp - 4) .. of each step ---------------------
+            const int w0 = 32 * (warp - 4);
+            auto page_of = [&](int s) {
+                const int32_t r = (u0 + s) * kN + w0 + lane;
+                return s < n_steps && r < seg.limit ? gqa_page(p, seg.b, r) : -1;
+            };
+            auto scale_of = [&](int32_t page, int s) {
+                const int32_t r = (u0 + s) * kN + w0 + lane;
+                return page < 0 ? make_float2(0.0f, 0.0f)
+                                : p.scales[(((int64_t)page * p.n_kv + seg.h) << p.shift) + (r & ((1 << p.shift) - 1))];
+            };
+            // keys and values take turns in the same registers: the values of a step are needed a
+            // softmax after its keys, the next keys a product later still
+            Codes<D> codes;
+            int32_t page = page_of(0);
+            codes.load(p, p.k_codes, seg.h, page, u0 * kN + w0, lane);
+            float2 sc = scale_of(page, 0);
+            for (int s = 0; s < n_steps; ++s) {
+                const uint32_t ph = (it + s) & 1u;
+                const int32_t row0 = (u0 + s) * kN + w0;
+                bool ok = s == 0 || mbar_wait(&sm.bars[kBarS], ph ^ 1u, abort_flag, p.wait_limit);
+                if (!__all_sync(kFull, ok)) break;
+                codes.store(raw + C::kOffK, w0, lane);
+                codes.load(p, p.v_codes, seg.h, page, row0, lane);
+                if ((u0 + s) * kN + kN > all && codes.mend(lane)) sc.y = __uint_as_float(0x7fffffffu);
+                sm.sk[ph][w0 + lane] = sc.x;
+                sm.sv[ph][w0 + lane] = sc.y;
+                fence_async_smem();
+                mbar_arrive(&sm.bars[kBarK]);
+                page = page_of(s + 1);
+                ok = s == 0 || mbar_wait(&sm.bars[kBarO], ph ^ 1u, abort_flag, p.wait_limit);
+                if (!__all_sync(kFull, ok)) break;
+                codes.store(raw + C::kOffV, w0, lane);
+                fence_async_smem();
+                mbar_arrive(&sm.bars[kBarV]);
+                codes.load(p, p.k_codes, seg.h, page, row0 + kN, lane);
+                sc = scale_of(page, s + 1);
+            }
+        } else if (lane == 0) {
+            // ---- products -----------------------------------------------------------
+            constexpr uint32_t kIdescS = idesc_f16(kM, kN, false, false), kIdescO = idesc_f16(kM, D, false, true);
+            const uint64_t dq = umma_desc(smem_u32(raw + C::kOffQ), 16, 1024), dk = umma_desc(smem_u32(raw + C::kOffK), 16, 1024);
+            const uint64_t dv = umma_desc(smem_u32(raw + C::kOffV), C::kChunk, 1024);
+            constexpr uint32_t kStep = C::kChunk >> 4;
+            bool ok = true;
+            for (int s = 0; s < n_steps && ok; ++s) {
+                const uint32_t ph = (it + s) & 1u;
+                // the weights of the step before lie over these scores
+                ok = mbar_wait(&sm.bars[kBarK], ph, abort_flag, p.wait_limit) &&
+                     (s == 0 || mbar_wait(&sm.bars[kBarO], ph ^ 1u, abort_flag, p.wait_limit));
+                if (!ok) break;
+                tc_after();
+#pragma unroll
+                for (int q = 0; q < QP; ++q)
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t at = (i / 4) * kStep + 2 * (i % 4);
+                        umma_f16(tmem, dq + q * C::kChunks * kStep + at, dk + at, kIdescS, q > 0 || i > 0);
+                    }
+                umma_commit(&sm.bars[kBarS]);
+                ok = mbar_wait(&sm.bars[kBarV], ph, abort_flag, p.wait_limit) &&
+                     mbar_wait(&sm.bars[kBarP], ph, abort_flag, p.wait_limit);
+                if (!ok) break;
+                tc_after();
+#pragma unroll
+                for (int i = 0; i < kN / 16; ++i) {
+                    const uint32_t a = tmem + weight_col<QP>(i / 2) + 8 * (i % 2);
+                    umma_f16_ts(tmem + C::kColO, a, dv + 128 * i, kIdescO, s % C::kFlush != 0 || i > 0);
+                    if constexpr (QP == 2) umma_f16_ts(tmem + C::kColO, a + 16, dv + 128 * i, kIdescO, 1u);
+                }
+                umma_commit(&sm.bars[kBarO]);
+            }
+            // every product issued is done before the tile ends, after an abort too
+            umma_commit(&sm.bars[kBarDone]);
+            int own = 0;
+            mbar_wait(&sm.bars[kBarDone], tiles & 1u, &own);
+            if (own) sm.abort = 1;
+        }
+        it += n_steps;
+        if (warp == 8) {
+            __syncwarp();
+            Walk walk = sm.walk;
+            walk.next(p);
+            __syncwarp();
+            if (lane == 0) sm.walk = walk;
+        }
+        tc_before();
+        __syncthreads();
+        tc_after();
+        if (sm.abort) break;
+    }
+    tc_before();
+    __syncthreads();
+    if (tid == 0 && sm.abort) set_err(p.err, KVQ_ERR_TIMEOUT);
+    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+}
+
+// Cut tiles joined: CTA (c, k) the dims 32 k .. of the tile that CTA c began, a vector a thread.
+template <int D, typename QT>
+__global__ void __launch_bounds__(kM) gqa_tc_merge_kernel(const __grid_constant__ GqaParams p) {
+    grid_dependency_wait();
+    launch_dependents();
+    const int first = blockIdx.x, k = blockIdx.y, v = threadIdx.x;
+    const GqaCut cut = p.cuts[first];
+    if (cut.count == 0) return;
+    float top = kNone, sum = 0.0f;
+    float4 o[8] = {};
+#pragma unroll 2
+    for (int i = 0; i < cut.count; ++i) {
+        const int sl = Walk::slot(first + i, first);
+        const float L = __ldcg(&p.ws_ml[sl * kM + v]).x;
+        const float4* src = reinterpret_cast<const float4*>(p.ws_o) + ((int64_t)sl * (D / 4) + 8 * k) * kM + v;
+        float4 x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __ldcg(src + e * kM);
+        const float n = fmaxf(top, L), a = ex2(top - n), b = L == kNone ? 0.0f : ex2(L - n);
+        sum = sum * a + b;
+        top = n;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            o[e].x = o[e].x * a + x[e].x * b;
+            o[e].y = o[e].y * a + x[e].y * b;
+            o[e].z = o[e].z * a + x[e].z * b;
+            o[e].w = o[e].w * a + x[e].w * b;
+        }
+    }
+    if (v >= cut.vecs) return;
+    GqaSegment seg;
+    seg.h = cut.h;
+    seg.q0 = cut.q0;
+    QT* out = static_cast<QT*>(p.out) + gqa_vector<D>(p, seg, cut.vec0 + v) + 32 * k;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float4 a = o[2 * e], b = o[2 * e + 1];
+        const float x[8] = {a.x * inv, a.y * inv, a.z * inv, a.w * inv, b.x * inv, b.y * inv, b.z * inv, b.w * inv};
+        store8(out + 8 * e, x);
+    }
+}
+
+template <int D, int QP, typename QT>
+cudaError_t launch_kernel(const GqaParams& p, cudaStream_t stream) {
+    using C = Cfg<D, QP>;
+    constexpr size_t smem = C::kOffMisc + sizeof(Misc);
+    static_assert(smem <= 227 * 1024, "shared memory");
+    constexpr int ctas = 152 * C::kCtas;
+    cudaError_t e = cudaFuncSetAttribute(gqa_tc_kernel<D, QP, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    timing_mark(stream, 0);
+    e = launch_chained(gqa_tc_kernel<D, QP, QT>, ctas, kNT, smem, stream, p);
+    timing_mark(stream, 1);
+    if (e == cudaSuccess) e = launch_chained(gqa_tc_merge_kernel<D, QT>, dim3(ctas, D / 32), kM, 0, stream, p);
+    timing_mark(stream, 2);
+    return e;
+}
+
+}  // namespace
+
+// Partial states, two a CTA, and totals.
+size_t gqa_tc_state_bytes(int32_t head_dim) {
+    const size_t ctas = head_dim == 256 ? 152 : 304;
+    return ctas * kM * (2 * (sizeof(float2) + head_dim * sizeof(float)) + head_dim * sizeof(float));
+}
+bool gqa_tc_supported(int32_t head_dim, kvq_dtype dt) { return head_dim != 256 || dt == KVQ_BF16; }
+
+cudaError_t launch_gqa_tc(const GqaParams& p0, int32_t head_dim, kvq_dtype dt, void* state, cudaStream_t stream) {
+    GqaParams p = p0;
+    const size_t ctas = head_dim == 256 ? 152 : 304;
+    p.ws_ml = static_cast<float2*>(state);
+    p.ws_o = reinterpret_cast<float*>(p.ws_ml + 2 * ctas * kM);
+    p.ws_tot = p.ws_o + 2 * ctas * kM * head_dim;
+    p.stall_polls = test_stall_polls();
+    p.wait_limit = p.stall_polls > 0 ? p.stall_polls : kWaitLimit;
+    switch (head_dim) {
+        case 64:
+            return dt == KVQ_BF16 ? launch_kernel<64, 1, __nv_bfloat16>(p, stream) : launch_kernel<64, 2, float>(p, stream);
+        case 128:
+            return dt == KVQ_BF16 ? launch_kernel<128, 1, __nv_bfloat16>(p, stream) : launch_kernel<128, 2, float>(p, stream);
+        default: return dt == KVQ_BF16 ? launch_kernel<256, 1, __nv_bfloat16>(p, stream) : cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace kvq

@@ -46,8 +46,8 @@ class Pool:
         return k.transpose(0, 1), v.transpose(0, 1)
 
 
-def attention(q, pool, lens, new, sm, causal):
-    """Outputs in f64, [tokens][heads][dim]."""
+def attention(q, pool, lens, new, sm, causal, absolute=False):
+    """Outputs in f64, [tokens][heads][dim]; absolute: sums of the values' sizes."""
     n_tok, heads, dim = q.shape
     group = heads // pool.heads
     out = torch.zeros(n_tok, heads, dim, dtype=torch.float64, device="cuda")
@@ -55,6 +55,7 @@ def attention(q, pool, lens, new, sm, causal):
     for b, (t, n) in enumerate(zip(lens, new)):
         if n and t:
             k, v = pool.rows(b, t)
+            v = v.abs() if absolute else v
             x = q[at:at + n].double().view(n, pool.heads, group, dim)
             z = torch.einsum("nhgd,htd->nhgt", x, k) * sm
             if causal:
@@ -68,11 +69,13 @@ def attention(q, pool, lens, new, sm, causal):
     return out
 
 
-def close(got, ref, what=""):
-    """1e-5 of a vector's largest before the rounding to the output's type (half a step of it)."""
+def close(got, ref, what="", mass=None):
+    """1e-5 of a vector's largest before the rounding to the output's type (half a step of it); mass (sums of the
+    values' sizes): each weight besides off by half a step of f16, which holds 11 bits: 2^-11 of itself."""
     half = torch.finfo(got.dtype).eps / 2
     top = ref.abs().amax(-1, keepdim=True)
-    bad = (got.double() - ref).abs() - (half * ref.abs() + 1e-5 * (1 + half) * top)
+    own = 1e-5 * top if mass is None else 1e-5 * top + 2.0 ** -11 * mass
+    bad = (got.double() - ref).abs() - (half * ref.abs() + (1 + half) * own)
     assert not torch.isnan(got).any(), what + ": NaN"
     assert bool((bad <= 0).all()), f"{what}: off by {float((got.double() - ref).abs().div(top.clamp(min=1e-300)).max()):.3g} of the largest"
 

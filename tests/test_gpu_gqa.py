@@ -44,6 +44,13 @@ def attend(kvq, pool, q, lens, new, causal=True, sm=None, ws=None, extra=0, stre
     return out, ws
 
 
+def check(out, q, pool, lens, new, sm, causal, what=""):
+    """Against 64 bits; bf16 queries with many vectors of a kv head go the tensor cores' way, with weights in f16."""
+    wide = q.dtype == torch.bfloat16 and len(q) * (q.shape[1] // pool.heads) > 32 * len(lens)
+    mass = attention(q, pool, lens, new, sm, causal, absolute=True) if wide else None
+    close(out, attention(q, pool, lens, new, sm, causal), what, mass)
+
+
 DT = [torch.bfloat16, torch.float32]
 
 
@@ -68,17 +75,19 @@ def test_mixtures_of_lengths(kvq, dtype, causal, dim, heads, kv, page):
     pool = Pool(kv, dim, page, lens, seed=page)
     q = queries(sum(new), heads, dim, dtype)
     out, ws = attend(kvq, pool, q, lens, new, causal)   # causal: 17 tokens on 5 rows, 5 on 2: the first see none
-    close(out, attention(q, pool, lens, new, 1 / math.sqrt(dim), causal))
+    check(out, q, pool, lens, new, 1 / math.sqrt(dim), causal)
     assert kvq.read_device_error(ws) == 0
 
 
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("past,new", [(0, 1), (0, 333), (1000, 130), (4097, 64), (31, 515)])
 def test_chunks(kvq, dtype, past, new):
-    pool = Pool(2, 128, 64, [past + new], seed=past)
-    q = queries(new, 10, 128, dtype)
-    out, _ = attend(kvq, pool, q, [past + new], [new])
-    close(out, attention(q, pool, [past + new], [new], 1 / math.sqrt(128), True))
+    for dim in (64, 128, 256):
+        pool = Pool(2, dim, 64, [past + new], seed=past)
+        q = queries(new, 10, dim, dtype)
+        out, ws = attend(kvq, pool, q, [past + new], [new])
+        check(out, q, pool, [past + new], [new], 1 / math.sqrt(dim), True, f"dim {dim}")
+        assert kvq.read_device_error(ws) == 0
 
 
 @pytest.mark.parametrize("dtype", DT)
@@ -116,6 +125,82 @@ def test_small_weights_and_small_scales_add_up(kvq):
         q[..., 0] = 1.0
         out, _ = attend(kvq, pool, q, [n], [1], sm=1.0)
         close(out, attention(q, pool, [n], [1], 1.0, True), f"by_scale={by_scale}")
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_many_vectors_and_rows_that_are_no_numbers(kvq, dim, causal):
+    """Tiles of 128 vectors: NaN codes and scales reach the tokens that see them, and no other."""
+    lens, new = [400, 150], [70, 20]
+    for dtype in DT if dim < 256 else DT[:1]:
+        for bad in ("k", "v", "sk", "sv", "inf"):
+            pool = Pool(2, dim, 16, lens, seed=9)
+            q = queries(90, 8, dim, dtype)
+            clean = Pool(2, dim, 16, lens, seed=9)
+            row = 371   # seen by sequence 0's tokens from the 41st on
+            pg, last = int(pool.table[0, row // 16]), int(pool.table[1, 150 // 16])
+            for p_, a in ((pg, slice(row % 16, row % 16 + 1)), (last, slice(150 % 16, 16))):
+                if bad in "kv":
+                    (pool.k if bad == "k" else pool.v)[p_, :, a, 5] = 0x7f
+                else:
+                    pool.scales[p_, :, a, 0 if bad == "sk" else 1] = math.inf if bad == "inf" else math.nan
+            out, ws = attend(kvq, pool, q, lens, new, causal, sm=0.1)
+            sees = [i for i in range(70) if not causal or 330 + i >= row]
+            rest = [i for i in range(90) if i not in sees]
+            assert bool(torch.isnan(out[sees]).any(-1).all()), bad
+            ref, mass = attention(q, clean, lens, new, 0.1, causal), attention(q, clean, lens, new, 0.1, causal, absolute=True)
+            close(out[rest], ref[rest], f"{bad} {dtype}", mass[rest])
+            assert kvq.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_many_vectors_over_spread_scales(kvq, dtype):
+    """References rise again and again, by scores and by scales; rows of large scale and no weight change nothing."""
+    lens, new = [3000], [64]
+    pool = Pool(2, 128, 64, lens, seed=5, scale_spread=6.0)
+    rise = torch.linspace(0, 30, 3000, device="cuda").exp2()   # values 2^30 apart along the rows
+    t = torch.arange(3000, device="cuda")
+    pg = pool.table[0].long()[t // 64]
+    pool.scales[pg, :, t % 64, 1] *= rise[:, None]
+    q = queries(64, 8, 128, dtype, gain=3.0)
+    out, ws = attend(kvq, pool, q, lens, new)
+    check(out, q, pool, lens, new, 1 / math.sqrt(128), True)
+    assert kvq.read_device_error(ws) == 0
+
+
+def test_many_vectors_long_sums(kvq):
+    """More than 256 steps by one walker: the totals in the workspace, to f32's 1e-5."""
+    n, b = 70000, 304
+    pool = Pool(1, 64, 1024, [n], seed=3)
+    pool.table = pool.table.expand(b, -1).contiguous()
+    q = queries(40 * b, 1, 64, torch.float32)
+    q[40:] = q[:40].repeat(b - 1, 1, 1)
+    out, ws = attend(kvq, pool, q, [n] * b, [40] * b, causal=False)
+    ref = attention(q[:40], pool, [n], [40], 0.125, False)
+    for i in (0, 1, 150, 303):
+        close(out[40 * i:40 * i + 40], ref, f"sequence {i}")
+    pool.v[:] = 0x35
+    pool.scales[..., 1] = 0.3
+    out, _ = attend(kvq, pool, q, [n] * b, [40] * b, causal=False, ws=ws)
+    ref = attention(q[:1], pool, [n], [1], 0.125, False)
+    assert float((out.double() - float(ref[0, 0, 0])).abs().max()) <= 1e-5 * float(ref[0, 0, 0])
+    assert kvq.read_device_error(ws) == 0
+
+
+def test_wait_that_runs_out(kvq):
+    pool = Pool(2, 128, 64, [300])
+    q = queries(64, 4, 128, torch.bfloat16)
+    ws = workspace(kvq, 4, 2, 128, True)
+    kvq.test_stall_waits(2000)
+    try:
+        attend(kvq, pool, q, [300], [64], ws=ws)
+        torch.cuda.synchronize()
+    finally:
+        kvq.test_stall_waits(0)
+    assert kvq.read_device_error(ws) == 10
+    out, _ = attend(kvq, pool, q, [300], [64], ws=ws)
+    check(out, q, pool, [300], [64], 1 / math.sqrt(128), True)
+    assert kvq.read_device_error(ws) == 0
 
 
 def test_a_million_rows(kvq):
@@ -179,13 +264,14 @@ def test_sizes_of_queries(kvq, gain):
 
 
 def test_the_same_bits_again(kvq):
-    lens, new = [9000, 20, 1, 3000], [2, 3, 1, 40]
-    pool = Pool(4, 128, 64, lens)
-    q = queries(sum(new), 8, 128, torch.bfloat16)
-    a, ws = attend(kvq, pool, q, lens, new)
-    for _ in range(3):
-        b, _ = attend(kvq, pool, q, lens, new, ws=ws)
-        assert torch.equal(a, b)
+    for new in ([2, 3, 1, 40], [100, 20, 1, 400]):
+        lens = [9000, 20, 1, 3000]
+        pool = Pool(4, 128, 64, lens)
+        q = queries(sum(new), 8, 128, torch.bfloat16)
+        a, ws = attend(kvq, pool, q, lens, new)
+        for _ in range(3):
+            b, _ = attend(kvq, pool, q, lens, new, ws=ws)
+            assert torch.equal(a, b)
 
 
 def test_offsets_past_32_bits(kvq):
