@@ -10,18 +10,19 @@
 // products) and the softmax (about 4.5 instructions a score).  So two CTAs share an SM, one's
 // softmax beside the other's products, and the weights go into the second product from
 // tensor memory, over the scores they came from, instead of through shared memory.
-//   * warps 0-3: softmax, a vector a thread, so maxima and sums need no exchange; 32 scores at
-//     a time are loaded, turned into 32 weights and stored over the first half of their
+//   * warps 0-3: softmax, a vector a thread, so maxima and sums need no exchange; 16 scores at
+//     a time are loaded, turned into weights and stored over the first half of their
 //     place (f32 queries: two f16 halves, over the whole place);
 //   * warps 4-7: codes to f16, in the layout of 128-byte swizzled rows, which the first
 //     product reads with dims along K and the second with rows along K; keys and values are asked
 //     for in turn, each as soon as the other is stored;
-//   * warp 8: one lane issues the products.
+//   * a lane of warp 0 issues the products: between its weights and the next scores the
+//     softmax has nothing to do (with a ninth warp for it, 96 registers a thread spilled).
 //
 // Numbers.  Queries as in gqa_attn.cu (bf16 exactly, f32 in two f16 halves).  R is an
-// integer per vector, at least max(z + log2 s_v) - 14 when it is set, so weights reach 2^14; it rises
-// when one passes 60000, and then what has been summed is brought to it by a power of two.  bf16
-// queries: weights in one f16 (2^-11 of themselves, down to 2^-28 of the largest).
+// integer per vector, max(z + log2 s_v) - 8 when it is set (f32 queries: 12); it rises
+// when a weight passes 60000, and then what has been summed is brought to it by a power of two.  bf16
+// queries: weights in one f16 (2^-11 of themselves, down to 2^-22 of the largest).
 // f32 queries: in two (2^-22).  Every 256 steps (f32 queries: 8) the accumulators, which round
 // towards zero, go to totals in the workspace.  Rows that are no numbers as in gqa_attn.cu.
 #include "gqa_common.cuh"
@@ -35,7 +36,7 @@ namespace {
 using namespace tc;
 
 constexpr int kM = 128, kN = 128, kOv = 3;
-constexpr int kSoft = 128, kConv = 128, kNT = kSoft + kConv + 32;
+constexpr int kSoft = 128, kConv = 128, kNT = kSoft + kConv;
 constexpr float kNone = -3.402823466e38f;
 using Walk = GqaWalk<kM, kN, kOv>;
 
@@ -52,11 +53,12 @@ struct Cfg {
     static constexpr int kFlush = QP == 2 ? 8 : 256;
     static constexpr int kCtas = D == 256 || (D == 128 && QP == 2) ? 1 : 2;   // an SM
 };
-enum { kBarK, kBarS, kBarV, kBarP, kBarO, kBarDone, kBarNever, kBars };
+enum { kBarK, kBarS, kBarV, kBarO, kBarDone, kBarNever, kBars };
 
 struct Misc {
     float sk[2][kN], sv[2][kN];
     float qs[kM];
+    float ref_tot[kM], sum_tot[kM];   // of the totals
     uint64_t bars[kBars];
     int64_t part[Walk::kScratch<kNT>];
     Walk walk;
@@ -111,46 +113,79 @@ __device__ __forceinline__ uint4 ldg16(const void* p) {
     return v;
 }
 
-// Columns of weights of scores 32 j ..: over the first half of their place, or (two halves)
+// Columns of weights of scores 16 j ..: over the first half of their place, or (two halves)
 // over all of it.
 template <int QP>
-__device__ __forceinline__ constexpr uint32_t weight_col(int j) { return QP == 1 ? 16u * j : 32u * j; }
+__device__ __forceinline__ constexpr uint32_t weight_col(int j) { return QP == 1 ? 8u * j : 16u * j; }
+template <int QP>
+constexpr int kWords = QP == 1 ? 8 : 16;   // of 16 weights
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]));
+}
+__device__ __forceinline__ void load_weights(uint32_t t, uint32_t (&v)[8]) { tmem_ld8(t, v); }
+__device__ __forceinline__ void load_weights(uint32_t t, uint32_t (&v)[16]) { tmem_ld16(t, v); }
+__device__ __forceinline__ void store_weights(uint32_t t, const uint32_t (&v)[8]) { tmem_st8(t, v); }
+__device__ __forceinline__ void store_weights(uint32_t t, const uint32_t (&v)[16]) { tmem_st16(t, v); }
+
+// The issuing lane's waits: polls without suspending (a suspended lane woke some 800 cycles
+// late, with every product of the CTA behind it).
+__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
+    if (*abort_flag) return false;
+    const uint32_t a = smem_u32(bar);
+    for (long long i = 0; i < 16 * limit; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(a), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((i & 63) == 63 && *abort_flag) return false;
+    }
+    *abort_flag = 1;
+    return false;
+}
 
 // A vector's reference raised for chunk j of a step (see the file's head), by a whole warp: its weights of
 // the chunks before, its context and its sums are brought to the new one.  Returns it; *alpha: the factor.
 template <int D, int QP>
 __device__ __noinline__ float raise(const Misc& sm, uint32_t tm, int j, int st, float qs, float R, bool lift, int32_t lim,
                                     int32_t row0, bool context, float* alpha) {
-    uint32_t s[32];
-    tmem_ld32(tm + 32 * j, s);
+    uint32_t s[16];
+    tmem_ld16(tm + 16 * j, s);
     tmem_wait_ld();
     float y = kNone, zm = kNone;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float sv = fabsf(sm.sv[st][32 * j + i]), z = __uint_as_float(s[i]) * (sm.sk[st][32 * j + i] * qs);
-        if (row0 + 32 * j + i < lim) {
+    for (int i = 0; i < 16; ++i) {
+        const float sv = fabsf(sm.sv[st][16 * j + i]), z = __uint_as_float(s[i]) * (sm.sk[st][16 * j + i] * qs);
+        if (row0 + 16 * j + i < lim) {
             zm = fmaxf(zm, z);
             if (sv > 0.0f) y = fmaxf(y, z + __log2f(sv));
         }
     }
     float n = R;
-    if (lift) n = fmaxf(R, ceilf(fmaxf(y - 14.0f, zm - 100.0f)));
+    if (lift) n = fmaxf(R, ceilf(fmaxf(y - (QP == 1 ? 8.0f : 12.0f), zm - 100.0f)));
     if (!(n >= kNone)) n = kNone;   // no score but -inf
     const float a = n == R ? 1.0f : ex2(R - n);
     const __half2 a2 = __float2half2_rn(a);
 #pragma unroll 1
     for (int k = 0; k < j; ++k) {
-        uint32_t w[QP == 1 ? 16 : 32];
-        if constexpr (QP == 1) tmem_ld16(tm + weight_col<QP>(k), w);
-        else tmem_ld32(tm + weight_col<QP>(k), w);
+        uint32_t w[kWords<QP>];
+        load_weights(tm + weight_col<QP>(k), w);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < (QP == 1 ? 16 : 32); ++i) {
+        for (int i = 0; i < kWords<QP>; ++i) {
             __half2 h = __hmul2(*reinterpret_cast<__half2*>(&w[i]), a2);
             w[i] = *reinterpret_cast<uint32_t*>(&h);
         }
-        if constexpr (QP == 1) tmem_st16(tm + weight_col<QP>(k), w);
-        else tmem_st32(tm + weight_col<QP>(k), w);
+        store_weights(tm + weight_col<QP>(k), w);
     }
     if (context) {
 #pragma unroll 1
@@ -168,20 +203,17 @@ __device__ __noinline__ float raise(const Misc& sm, uint32_t tm, int j, int st, 
     return n;
 }
 
-// Scores 32 j .. of a step to weights; their sum.  PART: some are hidden from some vector.
+// Scores 16 j .. of a step to weights; their sum.  PART: some are hidden from some vector.
 template <int QP, bool PART>
-__device__ __forceinline__ float weights(const Misc& sm, uint32_t tm, int j, int st, float qs, float R, int32_t visible,
-                                         uint32_t (&pk)[QP == 1 ? 16 : 32], float* most) {
-    uint32_t s[32];
-    tmem_ld32(tm + 32 * j, s);
-    tmem_wait_ld();
+__device__ __forceinline__ float weights(const Misc& sm, const uint32_t (&s)[16], int j, int st, float qs, float R,
+                                         int32_t visible, uint32_t (&pk)[kWords<QP>], float* most) {
     const F2 qs2 = f2(qs, qs), r2 = f2(-R, -R);
     F2 sum[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
     float top = 0.0f;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        const float4 k4 = *reinterpret_cast<const float4*>(&sm.sk[st][32 * j + 4 * q]);
-        const float4 v4 = *reinterpret_cast<const float4*>(&sm.sv[st][32 * j + 4 * q]);
+    for (int q = 0; q < 4; ++q) {
+        const float4 k4 = *reinterpret_cast<const float4*>(&sm.sk[st][16 * j + 4 * q]);
+        const float4 v4 = *reinterpret_cast<const float4*>(&sm.sv[st][16 * j + 4 * q]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int c = 4 * q + 2 * h;
@@ -204,7 +236,7 @@ __device__ __forceinline__ float weights(const Misc& sm, uint32_t tm, int j, int
             pk[c / 2] = hi;
             if constexpr (QP == 2) {
                 const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-                pk[16 + c / 2] = half2_of(w.x - x.x, w.y - x.y);
+                pk[8 + c / 2] = half2_of(w.x - x.x, w.y - x.y);
             }
         }
     }
@@ -214,45 +246,50 @@ __device__ __forceinline__ float weights(const Misc& sm, uint32_t tm, int j, int
 }
 
 // The codes of one step's keys or values as a converter warp holds them: 32 rows, 16 bytes a lane
-// and load, D / 16 lanes a row.
+// and load, D / 16 lanes a row.  Lanes of odd chunks (of 64 dims) take the neighbouring row, so
+// that the f16 of 8 lanes go to different banks.
 template <int D>
 struct Codes {
     static constexpr int kLanes = D / 16, kAt = 32 / kLanes, kLoads = 32 / kAt;   // lanes of a row, rows a load, loads
     uint4 v[kLoads];
-    // page: of row `lane` of the warp's 32 (-1: none)
-    __device__ __forceinline__ void load(const GqaParams& p, const uint8_t* base, int h, int32_t page, int32_t row0, int lane) {
-        const int32_t in_page = (1 << p.shift) - 1;
+    static __device__ __forceinline__ int row(int lane) { return (lane / kLanes) ^ ((lane % kLanes / 4) & 1); }
+    // at: the pool rows that hold rows 0 .. 15 and 16 .. 31 (pages hold at least 16 rows), -1: none of them
+    // is seen
+    __device__ __forceinline__ void load(const uint8_t* base, const int64_t (&at)[2], int lane) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int r = i * kAt + lane / kLanes;
-            const int32_t id = __shfl_sync(kFull, page, r);
-            v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (id >= 0) {
-                const int64_t at = (((int64_t)id * p.n_kv + h) << p.shift) + ((row0 + r) & in_page);
-                v[i] = ldg16(base + at * D + 16 * (lane % kLanes));
-            }
+        for (int g = 0; g < 2; ++g) {
+            const uint8_t* src = base + at[g] * D + row(lane) * D + 16 * (lane % kLanes);
+#pragma unroll
+            for (int i = 0; i < kLoads / 2; ++i)
+                v[g * (kLoads / 2) + i] = at[g] >= 0 ? ldg16(src + i * kAt * D) : make_uint4(0u, 0u, 0u, 0u);
         }
     }
-    // to f16 in swizzled rows: region: the operand's first chunk; row0: the warp's first row in it
-    __device__ __forceinline__ void store(unsigned char* region, int row0, int lane) const {
-        const int j = lane % kLanes, c = j / 4, q = j % 4;
-        const bool odd = c & 1;   // lanes of odd chunks store their second half first: other banks
+    // to f16 in swizzled rows; region: the operand's first chunk, at the warp's first row
+    __device__ __forceinline__ void store(unsigned char* region, int lane) const {
+        const int q = lane % 4, c = lane % kLanes / 4, r0 = row(lane);
+        unsigned char* at = region + c * (128 * 128) + r0 * 128;
+        // row i kAt + r0 of the warp's: its place in the swizzle repeats every 8 rows
+        constexpr int kTurn = kAt >= 8 ? 1 : 8 / kAt;
+        uint32_t lo_at[kTurn], hi_at[kTurn];
+#pragma unroll
+        for (int t = 0; t < kTurn; ++t) {
+            lo_at[t] = (uint32_t)(((2 * q) ^ (t * kAt + r0)) & 7) << 4;
+            hi_at[t] = lo_at[t] ^ 16u;
+        }
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int r = row0 + i * kAt + lane / kLanes;
             uint4 lo, hi;
             e4m3x4_to_half2x2(v[i].x, lo.x, lo.y);
             e4m3x4_to_half2x2(v[i].y, lo.z, lo.w);
             e4m3x4_to_half2x2(v[i].z, hi.x, hi.y);
             e4m3x4_to_half2x2(v[i].w, hi.z, hi.w);
-            unsigned char* at = region + c * (128 * 128);
-            *reinterpret_cast<uint4*>(at + sw128(r, 32 * q + (odd ? 16 : 0))) = odd ? hi : lo;
-            *reinterpret_cast<uint4*>(at + sw128(r, 32 * q + (odd ? 0 : 16))) = odd ? lo : hi;
+            *reinterpret_cast<uint4*>(at + i * kAt * 128 + lo_at[i % kTurn]) = lo;
+            *reinterpret_cast<uint4*>(at + i * kAt * 128 + hi_at[i % kTurn]) = hi;
         }
     }
     // NaN codes replaced; true for the lane whose row holds one
     __device__ __forceinline__ bool mend(int lane) {
-        bool mine = false;
+        uint32_t rows = 0u;   // rows with one, as this lane sees them
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             uint32_t* w = reinterpret_cast<uint32_t*>(&v[i]);
@@ -263,10 +300,9 @@ struct Codes {
                 bad |= nan != 0u;
                 w[k] ^= nan;
             }
-            const unsigned who = __ballot_sync(kFull, bad);
-            if (lane / kAt == i) mine = (who >> (kLanes * (lane % kAt))) & (kLanes == 32 ? ~0u : (1u << kLanes) - 1u);
+            if (bad) rows |= 1u << (i * kAt + row(lane));
         }
-        return mine;
+        return (__reduce_or_sync(kFull, rows) >> lane) & 1u;
     }
 };
 
@@ -354,7 +390,7 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
         if (tid == 0) set_err(p.err, KVQ_ERR_DEVICE);
         return;
     }
-    if (warp == 8) {
+    if (warp == 4) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)),
                      "r"(C::kCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -362,7 +398,7 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i)
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&sm.bars[i])),
-                         "r"(i == kBarK || i == kBarV || i == kBarP ? 128u : 1u));
+                         "r"(i == kBarK || i == kBarV ? 128u : 1u));
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sm.abort = 0;
     }
@@ -382,7 +418,7 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
         if (!sm.more || sm.abort) break;
         const int u0 = seg.u0, n_steps = seg.limit > u0 * kN ? min(seg.u1 - u0, (seg.limit - u0 * kN + kN - 1) / kN) : 0;
         const int32_t all = gqa_limit(p, seg, seg.vec0);   // rows that all vectors see
-        if (tid < 256) load_queries<D, QP, QT>(p, seg, sm, raw + C::kOffQ);
+        load_queries<D, QP, QT>(p, seg, sm, raw + C::kOffQ);
         fence_async_smem();
         __syncthreads();
         if (warp < 4) {
@@ -390,10 +426,11 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
             const int32_t lim = gqa_limit(p, seg, seg.vec0 + min(tid, seg.vecs - 1));
             const float qs = sm.qs[tid];
             const uint32_t tm = tmem + ((uint32_t)(warp * 32) << 16);
-            float R = kNone, l = 0.0f, Rt = kNone, lt = 0.0f;   // reference and sum; those of the totals
-            float4* tot = reinterpret_cast<float4*>(p.ws_tot) + (int64_t)blockIdx.x * (D / 4) * kM + tid;
+            float R = kNone, l = 0.0f;   // reference and sum
             // accumulators to the totals: first: they start there
             auto flush = [&](bool first) {
+                float4* tot = reinterpret_cast<float4*>(p.ws_tot) + (int64_t)blockIdx.x * (D / 4) * kM + tid;
+                const float Rt = first ? kNone : sm.ref_tot[tid], lt = first ? 0.0f : sm.sum_tot[tid];
                 const float n = fmaxf(Rt, R), a = first ? 0.0f : ex2(Rt - n), b = ex2(R - n);
 #pragma unroll 1
                 for (int k = 0; k < D / 32; ++k) {
@@ -410,50 +447,106 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                         tot[(8 * k + i) * kM] = v;
                     }
                 }
-                lt = lt * a + l * b;
-                Rt = n;
+                sm.sum_tot[tid] = lt * a + l * b;
+                sm.ref_tot[tid] = n;
                 l = 0.0f;
             };
+            // the products, by one lane
+            constexpr uint32_t kIdescS = idesc_f16(kM, kN, false, false), kIdescO = idesc_f16(kM, D, false, true);
+            constexpr uint32_t kStep = C::kChunk >> 4;
+            auto issue_scores = [&](int s) {
+                const uint32_t ph = (it + s) & 1u;
+                // the weights of the step before lie over these scores
+                if (!mbar_spin(&sm.bars[kBarK], ph, abort_flag, p.wait_limit) ||
+                    (s > 0 && !mbar_spin(&sm.bars[kBarO], ph ^ 1u, abort_flag, p.wait_limit)))
+                    return;
+                tc_after();
+                const uint64_t dq = umma_desc(smem_u32(raw + C::kOffQ), 16, 1024);
+                const uint64_t dk = umma_desc(smem_u32(raw + C::kOffK), 16, 1024);
+#pragma unroll
+                for (int q = 0; q < QP; ++q)
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t at = (i / 4) * kStep + 2 * (i % 4);
+                        umma_f16(tmem, dq + q * C::kChunks * kStep + at, dk + at, kIdescS, q > 0 || i > 0);
+                    }
+                umma_commit(&sm.bars[kBarS]);
+            };
+            auto issue_context = [&](int s) {
+                if (!mbar_spin(&sm.bars[kBarV], (it + s) & 1u, abort_flag, p.wait_limit)) return;
+                tc_after();
+                const uint64_t dv = umma_desc(smem_u32(raw + C::kOffV), C::kChunk, 1024);
+#pragma unroll
+                for (int i = 0; i < kN / 16; ++i) {
+                    const uint32_t a = tmem + weight_col<QP>(i);
+                    umma_f16_ts(tmem + C::kColO, a, dv + 128 * i, kIdescO, s % C::kFlush != 0 || i > 0);
+                    if constexpr (QP == 2) umma_f16_ts(tmem + C::kColO, a + 8, dv + 128 * i, kIdescO, 1u);
+                }
+                umma_commit(&sm.bars[kBarO]);
+            };
+            if (tid == 0 && n_steps > 0) issue_scores(0);
+            __syncwarp();
             bool ok = true;
             for (int s = 0; s < n_steps; ++s) {
                 const uint32_t ph = (it + s) & 1u;
                 const int st = (int)ph;
-                // the scales' writers arrived on the first, the scores are the second's
-                ok = mbar_wait(&sm.bars[kBarK], ph, abort_flag, p.wait_limit) &&
-                     mbar_wait(&sm.bars[kBarS], ph, abort_flag, p.wait_limit);
-                if (!__all_sync(kFull, ok)) {
-                    ok = false;
-                    break;
-                }
+                // (the scales too: their writers arrived on kBarK, which the issuing lane waited for.  Not
+                // waited for here: the next keys' arrival could be the phase after, seen as not yet)
+                ok = __all_sync(kFull, mbar_wait(&sm.bars[kBarS], ph, abort_flag, p.wait_limit));
+                if (ok) {
                 tc_after();
                 if (s > 0 && s % C::kFlush == 0) flush(s == C::kFlush);
                 const int32_t row0 = (u0 + s) * kN;
                 const bool partly = row0 + kN > all, context = s % C::kFlush != 0;
-#pragma unroll 1
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t pk[QP == 1 ? 16 : 32];
-                    const int32_t visible = min(max(lim - row0 - 32 * j, 0), 32);
+                uint32_t cur[16], nxt[16];
+                tmem_ld16(tm, cur);
+                // scores 16 j .. while the next 16 come; a reference that had to rise takes them again
+                // (kept in registers over the call, they would be spilled every time)
+                auto chunk = [&](int j, uint32_t (&now)[16], uint32_t (&then)[16]) {
+                    const int32_t visible = partly ? min(max(lim - row0 - 16 * j, 0), 16) : 16;
+                    uint32_t pk[kWords<QP>];
                     float most, sum;
-                    auto run = [&]() {
-                        if (partly) sum = weights<QP, true>(sm, tm, j, st, qs, R, visible, pk, &most);
-                        else sum = weights<QP, false>(sm, tm, j, st, qs, R, 32, pk, &most);
-                    };
-                    run();
-                    const bool lift = (R == kNone && visible > 0) || !(most <= 60000.0f) || !(sum <= 0x1p110f);
-                    if (__any_sync(kFull, lift)) {
+#pragma unroll 1
+                    for (int pass = 0;; ++pass) {
+                        tmem_wait_ld();
+                        if (j < 7) tmem_ld16(tm + 16 * (j + 1), then);
+                        if (partly) sum = weights<QP, true>(sm, now, j, st, qs, R, visible, pk, &most);
+                        else sum = weights<QP, false>(sm, now, j, st, qs, R, 16, pk, &most);
+                        const bool lift = (R == kNone && visible > 0) || !(most <= 60000.0f) || !(sum <= 0x1p110f);
+                        if (pass == 1 || !__any_sync(kFull, lift)) break;
                         float a;
                         R = raise<D, QP>(sm, tm, j, st, qs, R, lift, lim, row0, context, &a);
                         l *= a;
-                        run();
+                        tmem_ld16(tm + 16 * j, now);
                     }
                     l += sum;
-                    if constexpr (QP == 1) tmem_st16(tm + weight_col<QP>(j), pk);
-                    else tmem_st32(tm + weight_col<QP>(j), pk);
+                    store_weights(tm + weight_col<QP>(j), pk);
+                };
+#pragma unroll 1
+                for (int j = 0; j < 8; j += 2) {
+                    chunk(j, cur, nxt);
+                    chunk(j + 1, nxt, cur);
                 }
                 tmem_wait_st();
                 tc_before();
-                mbar_arrive(&sm.bars[kBarP]);
+                }
+                // every softmax warp comes here at every step, and all leave together
+                ok = !worker_any<kSoft>(!ok || *abort_flag != 0);
+                if (!ok) break;
+                if (tid == 0) {
+                    issue_context(s);
+                    if (s + 1 < n_steps) issue_scores(s + 1);
+                }
+                __syncwarp();
             }
+            // every product issued is done before the tile ends, after an abort too
+            if (tid == 0) {
+                umma_commit(&sm.bars[kBarDone]);
+                int own = 0;
+                mbar_wait(&sm.bars[kBarDone], tiles & 1u, &own);
+                if (own) sm.abort = 1;
+            }
+            __syncwarp();
             // the last product's end
             if (ok && n_steps > 0) ok = mbar_wait(&sm.bars[kBarO], (it + n_steps - 1) & 1u, abort_flag, p.wait_limit);
             ok = __all_sync(kFull, ok);
@@ -461,7 +554,8 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                 tc_after();
                 const bool summed = n_steps > C::kFlush;
                 if (summed) flush(false);
-                const float sum = summed ? lt : l, ref = summed ? Rt : R, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const float4* tot = reinterpret_cast<const float4*>(p.ws_tot) + (int64_t)blockIdx.x * (D / 4) * kM + tid;
+                const float sum = summed ? sm.sum_tot[tid] : l, ref = summed ? sm.ref_tot[tid] : R, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 const bool live = tid < seg.vecs;
                 QT* out = static_cast<QT*>(p.out) + (live ? gqa_vector<D>(p, seg, seg.vec0 + tid) : 0);
                 float4* dst = reinterpret_cast<float4*>(p.ws_o) + (int64_t)max(seg.slot, 0) * (D / 4) * kM + tid;
@@ -497,87 +591,59 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                 if (tid == 0 && seg.slot >= 0 && seg.u0 == 0)
                     p.cuts[blockIdx.x] = GqaCut{seg.count, seg.h, seg.vec0, seg.vecs, seg.q0, 0};
             }
-        } else if (warp < 8) {
+        } else {
             // ---- codes to f16: rows 32 (warp - 4) .. of each step ---------------------
             const int w0 = 32 * (warp - 4);
+            const int32_t in_page = (1 << p.shift) - 1;
+            // page of the warp's rows 0 .. 15 and 16 .. 31 of step s: lanes 0 and 1
             auto page_of = [&](int s) {
-                const int32_t r = (u0 + s) * kN + w0 + lane;
+                const int32_t r = (u0 + s) * kN + w0 + 16 * (lane & 1);
                 return s < n_steps && r < seg.limit ? gqa_page(p, seg.b, r) : -1;
             };
-            auto scale_of = [&](int32_t page, int s) {
-                const int32_t r = (u0 + s) * kN + w0 + lane;
-                return page < 0 ? make_float2(0.0f, 0.0f)
-                                : p.scales[(((int64_t)page * p.n_kv + seg.h) << p.shift) + (r & ((1 << p.shift) - 1))];
+            auto rows_of = [&](int32_t page, int s, int64_t (&at)[2]) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const int32_t id = __shfl_sync(kFull, page, g);
+                    at[g] = id < 0 ? -1 : (((int64_t)id * p.n_kv + seg.h) << p.shift) + (((u0 + s) * kN + w0 + 16 * g) & in_page);
+                }
+            };
+            auto scale_of = [&](const int64_t (&at)[2]) {
+                const int64_t x = lane < 16 ? at[0] : at[1];
+                return x < 0 ? make_float2(0.0f, 0.0f) : p.scales[x + (lane & 15)];
             };
             // keys and values take turns in the same registers: the values of a step are needed a
             // softmax after its keys, the next keys a product later still
             Codes<D> codes;
+            int64_t at[2];
             int32_t page = page_of(0);
-            codes.load(p, p.k_codes, seg.h, page, u0 * kN + w0, lane);
-            float2 sc = scale_of(page, 0);
+            rows_of(page, 0, at);
+            codes.load(p.k_codes, at, lane);
+            float2 sc = scale_of(at);
+            page = page_of(1);
             for (int s = 0; s < n_steps; ++s) {
                 const uint32_t ph = (it + s) & 1u;
-                const int32_t row0 = (u0 + s) * kN + w0;
                 bool ok = s == 0 || mbar_wait(&sm.bars[kBarS], ph ^ 1u, abort_flag, p.wait_limit);
                 if (!__all_sync(kFull, ok)) break;
-                codes.store(raw + C::kOffK, w0, lane);
-                codes.load(p, p.v_codes, seg.h, page, row0, lane);
+                codes.store(raw + C::kOffK + w0 * 128, lane);
+                codes.load(p.v_codes, at, lane);
                 if ((u0 + s) * kN + kN > all && codes.mend(lane)) sc.y = __uint_as_float(0x7fffffffu);
                 sm.sk[ph][w0 + lane] = sc.x;
                 sm.sv[ph][w0 + lane] = sc.y;
                 fence_async_smem();
                 mbar_arrive(&sm.bars[kBarK]);
-                page = page_of(s + 1);
+                rows_of(page, s + 1, at);
+                sc = scale_of(at);
+                page = page_of(s + 2);
                 ok = s == 0 || mbar_wait(&sm.bars[kBarO], ph ^ 1u, abort_flag, p.wait_limit);
                 if (!__all_sync(kFull, ok)) break;
-                codes.store(raw + C::kOffV, w0, lane);
+                codes.store(raw + C::kOffV + w0 * 128, lane);
                 fence_async_smem();
                 mbar_arrive(&sm.bars[kBarV]);
-                codes.load(p, p.k_codes, seg.h, page, row0 + kN, lane);
-                sc = scale_of(page, s + 1);
+                codes.load(p.k_codes, at, lane);
             }
-        } else if (lane == 0) {
-            // ---- products -----------------------------------------------------------
-            constexpr uint32_t kIdescS = idesc_f16(kM, kN, false, false), kIdescO = idesc_f16(kM, D, false, true);
-            const uint64_t dq = umma_desc(smem_u32(raw + C::kOffQ), 16, 1024), dk = umma_desc(smem_u32(raw + C::kOffK), 16, 1024);
-            const uint64_t dv = umma_desc(smem_u32(raw + C::kOffV), C::kChunk, 1024);
-            constexpr uint32_t kStep = C::kChunk >> 4;
-            bool ok = true;
-            for (int s = 0; s < n_steps && ok; ++s) {
-                const uint32_t ph = (it + s) & 1u;
-                // the weights of the step before lie over these scores
-                ok = mbar_wait(&sm.bars[kBarK], ph, abort_flag, p.wait_limit) &&
-                     (s == 0 || mbar_wait(&sm.bars[kBarO], ph ^ 1u, abort_flag, p.wait_limit));
-                if (!ok) break;
-                tc_after();
-#pragma unroll
-                for (int q = 0; q < QP; ++q)
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const uint32_t at = (i / 4) * kStep + 2 * (i % 4);
-                        umma_f16(tmem, dq + q * C::kChunks * kStep + at, dk + at, kIdescS, q > 0 || i > 0);
-                    }
-                umma_commit(&sm.bars[kBarS]);
-                ok = mbar_wait(&sm.bars[kBarV], ph, abort_flag, p.wait_limit) &&
-                     mbar_wait(&sm.bars[kBarP], ph, abort_flag, p.wait_limit);
-                if (!ok) break;
-                tc_after();
-#pragma unroll
-                for (int i = 0; i < kN / 16; ++i) {
-                    const uint32_t a = tmem + weight_col<QP>(i / 2) + 8 * (i % 2);
-                    umma_f16_ts(tmem + C::kColO, a, dv + 128 * i, kIdescO, s % C::kFlush != 0 || i > 0);
-                    if constexpr (QP == 2) umma_f16_ts(tmem + C::kColO, a + 16, dv + 128 * i, kIdescO, 1u);
-                }
-                umma_commit(&sm.bars[kBarO]);
-            }
-            // every product issued is done before the tile ends, after an abort too
-            umma_commit(&sm.bars[kBarDone]);
-            int own = 0;
-            mbar_wait(&sm.bars[kBarDone], tiles & 1u, &own);
-            if (own) sm.abort = 1;
         }
         it += n_steps;
-        if (warp == 8) {
+        if (warp == 4) {
             __syncwarp();
             Walk walk = sm.walk;
             walk.next(p);
@@ -592,7 +658,7 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
     tc_before();
     __syncthreads();
     if (tid == 0 && sm.abort) set_err(p.err, KVQ_ERR_TIMEOUT);
-    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+    if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
 }
 
 // Cut tiles joined: CTA (c, k) the dims 32 k .. of the tile that CTA c began, a vector a thread.
