@@ -80,7 +80,7 @@ struct GqaWalk {
     GqaSeq s;
     int64_t u0;
 
-    __device__ static GqaSeq shape(const GqaParams& p, int b) {
+    __device__ __noinline__ static GqaSeq shape(const GqaParams& p, int b) {
         GqaSeq s{0, 0, 0, 0, 0, 0, 0, 0, 0};
         if (b >= p.n_seq) return s;
         const int64_t a = p.cu_q[b], e = p.cu_q[b + 1];
@@ -113,7 +113,7 @@ struct GqaWalk {
     __device__ static int64_t units(const GqaParams& p, const GqaSeq& s, int64_t j) {
         return max((int64_t)1, (limit(p, s, j) + N - 1) / N);
     }
-    __device__ static int64_t floor_sum(const GqaParams& p, int64_t n) {   // sum_{k<n} floor(k / R)
+    __device__ __noinline__ static int64_t floor_sum(const GqaParams& p, int64_t n) {   // sum_{k<n} floor(k / R)
         const int64_t R = (int64_t)p.group * (N / M), q = quot(n, R), r = n - q * R;
         return R * (q * (q - 1) / 2) + q * r;
     }
@@ -212,7 +212,7 @@ struct GqaWalk {
         return true;
     }
     // On to the next tile, by whole warps (sequences without new tokens are passed 32 at a time).
-    __device__ __forceinline__ void next(const GqaParams& p) {
+    __device__ __noinline__ void next(const GqaParams& p) {
         u0 = 0;
         if (++x < s.tiles * p.n_kv) return;
         seq_v += s.per_head * p.n_kv;

@@ -57,6 +57,7 @@ enum { kBarK, kBarS, kBarV, kBarO, kBarDone, kBarNever, kBars };
 
 struct Misc {
     float sk[2][kN], sv[2][kN];
+    float sv_top[2][kN / 32];   // largest of 32 rows
     float qs[kM];
     float ref_tot[kM], sum_tot[kM];   // of the totals
     uint64_t bars[kBars];
@@ -113,26 +114,18 @@ __device__ __forceinline__ uint4 ldg16(const void* p) {
     return v;
 }
 
-// Columns of weights of scores 16 j ..: over the first half of their place, or (two halves)
+// Columns of weights of scores 16 i ..: over the first half of the scores' place, or (two halves)
 // over all of it.
 template <int QP>
-__device__ __forceinline__ constexpr uint32_t weight_col(int j) { return QP == 1 ? 8u * j : 16u * j; }
+__device__ __forceinline__ constexpr uint32_t weight_col(int i) { return QP == 1 ? 8u * i : 16u * i; }
+constexpr int kC = 32;   // scores taken at a time
 template <int QP>
-constexpr int kWords = QP == 1 ? 8 : 16;   // of 16 weights
+constexpr int kWords = QP * kC / 2;   // of so many weights: first halves of 16, second halves of 16, ...
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
-                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]));
-}
-__device__ __forceinline__ void load_weights(uint32_t t, uint32_t (&v)[8]) { tmem_ld8(t, v); }
 __device__ __forceinline__ void load_weights(uint32_t t, uint32_t (&v)[16]) { tmem_ld16(t, v); }
-__device__ __forceinline__ void store_weights(uint32_t t, const uint32_t (&v)[8]) { tmem_st8(t, v); }
+__device__ __forceinline__ void load_weights(uint32_t t, uint32_t (&v)[32]) { tmem_ld32(t, v); }
 __device__ __forceinline__ void store_weights(uint32_t t, const uint32_t (&v)[16]) { tmem_st16(t, v); }
+__device__ __forceinline__ void store_weights(uint32_t t, const uint32_t (&v)[32]) { tmem_st32(t, v); }
 
 // The issuing lane's waits: polls without suspending (a suspended lane woke some 800 cycles
 // late, with every product of the CTA behind it).
@@ -154,18 +147,19 @@ __device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volati
 }
 
 // A vector's reference raised for chunk j of a step (see the file's head), by a whole warp: its weights of
-// the chunks before, its context and its sums are brought to the new one.  Returns it; *alpha: the factor.
+// the chunks before (tm: its scores), its context (to) and its sums are brought to the new one.  Returns it
+// and the factor.
 template <int D, int QP>
-__device__ __noinline__ float raise(const Misc& sm, uint32_t tm, int j, int st, float qs, float R, bool lift, int32_t lim,
-                                    int32_t row0, bool context, float* alpha) {
-    uint32_t s[16];
-    tmem_ld16(tm + 16 * j, s);
+__device__ __forceinline__ float2 raise(const Misc& sm, uint32_t tm, uint32_t to, int j, int st, float qs, float R, bool lift,
+                                     int32_t visible, bool context) {
+    uint32_t s[kC];
+    tmem_ld32(tm + kC * j, s);
     tmem_wait_ld();
     float y = kNone, zm = kNone;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float sv = fabsf(sm.sv[st][16 * j + i]), z = __uint_as_float(s[i]) * (sm.sk[st][16 * j + i] * qs);
-        if (row0 + 16 * j + i < lim) {
+    for (int i = 0; i < kC; ++i) {
+        const float sv = fabsf(sm.sv[st][kC * j + i]), z = __uint_as_float(s[i]) * (sm.sk[st][kC * j + i] * qs);
+        if (i < visible) {
             zm = fmaxf(zm, z);
             if (sv > 0.0f) y = fmaxf(y, z + __log2f(sv));
         }
@@ -178,45 +172,44 @@ __device__ __noinline__ float raise(const Misc& sm, uint32_t tm, int j, int st, 
 #pragma unroll 1
     for (int k = 0; k < j; ++k) {
         uint32_t w[kWords<QP>];
-        load_weights(tm + weight_col<QP>(k), w);
+        load_weights(tm + weight_col<QP>(k * (kC / 16)), w);
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < kWords<QP>; ++i) {
             __half2 h = __hmul2(*reinterpret_cast<__half2*>(&w[i]), a2);
             w[i] = *reinterpret_cast<uint32_t*>(&h);
         }
-        store_weights(tm + weight_col<QP>(k), w);
+        store_weights(tm + weight_col<QP>(k * (kC / 16)), w);
     }
     if (context) {
 #pragma unroll 1
         for (int k = 0; k < D / 32; ++k) {
             uint32_t o[32];
-            tmem_ld32(tm + Cfg<D, QP>::kColO + 32 * k, o);
+            tmem_ld32(to + 32 * k, o);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-            tmem_st32(tm + Cfg<D, QP>::kColO + 32 * k, o);
+            tmem_st32(to + 32 * k, o);
         }
     }
     tmem_wait_st();
-    *alpha = a;
-    return n;
+    return make_float2(n, a);
 }
 
-// Scores 16 j .. of a step to weights; their sum.  PART: some are hidden from some vector.
+// Scores kC j .. of a step to weights; their sum before the values' scales.  PART: some are hidden from
+// some vector.
 template <int QP, bool PART>
-__device__ __forceinline__ float weights(const Misc& sm, const uint32_t (&s)[16], int j, int st, float qs, float R,
+__device__ __forceinline__ float weights(const Misc& sm, const uint32_t (&s)[kC], int j, int st, float qs, float R,
                                          int32_t visible, uint32_t (&pk)[kWords<QP>], float* most) {
     const F2 qs2 = f2(qs, qs), r2 = f2(-R, -R);
     F2 sum[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
-    float top = 0.0f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float4 k4 = *reinterpret_cast<const float4*>(&sm.sk[st][16 * j + 4 * q]);
-        const float4 v4 = *reinterpret_cast<const float4*>(&sm.sv[st][16 * j + 4 * q]);
+    for (int q = 0; q < kC / 4; ++q) {
+        const float4 k4 = *reinterpret_cast<const float4*>(&sm.sk[st][kC * j + 4 * q]);
+        const float4 v4 = *reinterpret_cast<const float4*>(&sm.sv[st][kC * j + 4 * q]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int c = 4 * q + 2 * h;
+            const int c = 4 * q + 2 * h, at = QP * 8 * (c / 16) + c % 16 / 2;
             const F2 b = mul2(h == 0 ? f2(k4.x, k4.y) : f2(k4.z, k4.w), qs2);
             const float2 t = un2(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), b, r2));
             float2 p = make_float2(ex2(t.x), ex2(t.y));
@@ -231,16 +224,15 @@ __device__ __forceinline__ float weights(const Misc& sm, const uint32_t (&s)[16]
                 if (c >= visible) w.x = 0.0f;
                 if (c + 1 >= visible) w.y = 0.0f;
             }
-            top = fmaxf(top, fmaxf(fabsf(w.x), fabsf(w.y)));
             const uint32_t hi = half2_of(w.x, w.y);
-            pk[c / 2] = hi;
+            pk[at] = hi;
             if constexpr (QP == 2) {
+                *most = fmaxf(*most, fmaxf(fabsf(w.x), fabsf(w.y)));
                 const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-                pk[8 + c / 2] = half2_of(w.x - x.x, w.y - x.y);
+                pk[8 + at] = half2_of(w.x - x.x, w.y - x.y);
             }
         }
     }
-    *most = top;
     const float2 u = un2(add2(sum[0], sum[1]));
     return u.x + u.y;
 }
@@ -455,11 +447,8 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
             constexpr uint32_t kIdescS = idesc_f16(kM, kN, false, false), kIdescO = idesc_f16(kM, D, false, true);
             constexpr uint32_t kStep = C::kChunk >> 4;
             auto issue_scores = [&](int s) {
-                const uint32_t ph = (it + s) & 1u;
                 // the weights of the step before lie over these scores
-                if (!mbar_spin(&sm.bars[kBarK], ph, abort_flag, p.wait_limit) ||
-                    (s > 0 && !mbar_spin(&sm.bars[kBarO], ph ^ 1u, abort_flag, p.wait_limit)))
-                    return;
+                if (s > 0 && !mbar_spin(&sm.bars[kBarO], ((it + s) & 1u) ^ 1u, abort_flag, p.wait_limit)) return;
                 tc_after();
                 const uint64_t dq = umma_desc(smem_u32(raw + C::kOffQ), 16, 1024);
                 const uint64_t dk = umma_desc(smem_u32(raw + C::kOffK), 16, 1024);
@@ -473,7 +462,6 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                 umma_commit(&sm.bars[kBarS]);
             };
             auto issue_context = [&](int s) {
-                if (!mbar_spin(&sm.bars[kBarV], (it + s) & 1u, abort_flag, p.wait_limit)) return;
                 tc_after();
                 const uint64_t dv = umma_desc(smem_u32(raw + C::kOffV), C::kChunk, 1024);
 #pragma unroll
@@ -484,7 +472,7 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                 }
                 umma_commit(&sm.bars[kBarO]);
             };
-            if (tid == 0 && n_steps > 0) issue_scores(0);
+            if (tid == 0 && n_steps > 0 && mbar_spin(&sm.bars[kBarK], it & 1u, abort_flag, p.wait_limit)) issue_scores(0);
             __syncwarp();
             bool ok = true;
             for (int s = 0; s < n_steps; ++s) {
@@ -498,38 +486,43 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                 if (s > 0 && s % C::kFlush == 0) flush(s == C::kFlush);
                 const int32_t row0 = (u0 + s) * kN;
                 const bool partly = row0 + kN > all, context = s % C::kFlush != 0;
-                uint32_t cur[16], nxt[16];
-                tmem_ld16(tm, cur);
-                // scores 16 j .. while the next 16 come; a reference that had to rise takes them again
-                // (kept in registers over the call, they would be spilled every time)
-                auto chunk = [&](int j, uint32_t (&now)[16], uint32_t (&then)[16]) {
-                    const int32_t visible = partly ? min(max(lim - row0 - 16 * j, 0), 16) : 16;
-                    uint32_t pk[kWords<QP>];
-                    float most, sum;
+                // a reference that had to rise takes its scores again (kept in registers meanwhile, they
+                // would be spilled every time)
 #pragma unroll 1
-                    for (int pass = 0;; ++pass) {
-                        tmem_wait_ld();
-                        if (j < 7) tmem_ld16(tm + 16 * (j + 1), then);
-                        if (partly) sum = weights<QP, true>(sm, now, j, st, qs, R, visible, pk, &most);
-                        else sum = weights<QP, false>(sm, now, j, st, qs, R, 16, pk, &most);
-                        const bool lift = (R == kNone && visible > 0) || !(most <= 60000.0f) || !(sum <= 0x1p110f);
-                        if (pass == 1 || !__any_sync(kFull, lift)) break;
-                        float a;
-                        R = raise<D, QP>(sm, tm, j, st, qs, R, lift, lim, row0, context, &a);
-                        l *= a;
-                        tmem_ld16(tm + 16 * j, now);
+                for (int j = 0, pass = 0; j < kN / kC;) {
+                    const int32_t visible = partly ? min(max(lim - row0 - kC * j, 0), kC) : kC;
+                    uint32_t now[kC], pk[kWords<QP>];
+                    tmem_ld32(tm + kC * j, now);
+                    const float svt = sm.sv_top[st][j];
+                    tmem_wait_ld();
+                    float sum, most = 0.0f;
+                    if (partly) sum = weights<QP, true>(sm, now, j, st, qs, R, visible, pk, &most);
+                    else sum = weights<QP, false>(sm, now, j, st, qs, R, kC, pk, &most);
+                    // one half: the sum and the scales bound the weights (references leave the room, a false
+                    // alarm only costs time); two: the weights themselves
+                    if (QP == 1) most = sum * svt;
+                    const bool lift = (R == kNone && visible > 0) || !(most <= 60000.0f) || !(sum <= 0x1p110f);
+                    if (pass == 0 && __any_sync(kFull, lift)) {
+                        const float2 up = raise<D, QP>(sm, tm, tm + C::kColO, j, st, qs, R, lift, visible, context);
+                        R = up.x;
+                        l *= up.y;
+                        pass = 1;
+                        continue;
                     }
                     l += sum;
-                    store_weights(tm + weight_col<QP>(j), pk);
-                };
-#pragma unroll 1
-                for (int j = 0; j < 8; j += 2) {
-                    chunk(j, cur, nxt);
-                    chunk(j + 1, nxt, cur);
+                    store_weights(tm + weight_col<QP>(j * (kC / 16)), pk);
+                    pass = 0;
+                    ++j;
                 }
                 tmem_wait_st();
                 tc_before();
                 }
+                // this step's values and the next keys, there for long: waited for before the others are
+                if (tid == 0 && ok) {
+                    ok = mbar_spin(&sm.bars[kBarV], ph, abort_flag, p.wait_limit) &&
+                         (s + 1 == n_steps || mbar_spin(&sm.bars[kBarK], ph ^ 1u, abort_flag, p.wait_limit));
+                }
+                __syncwarp();
                 // every softmax warp comes here at every step, and all leave together
                 ok = !worker_any<kSoft>(!ok || *abort_flag != 0);
                 if (!ok) break;
@@ -629,6 +622,8 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                 if ((u0 + s) * kN + kN > all && codes.mend(lane)) sc.y = __uint_as_float(0x7fffffffu);
                 sm.sk[ph][w0 + lane] = sc.x;
                 sm.sv[ph][w0 + lane] = sc.y;
+                const float top = warp_max(fabsf(sc.y));
+                if (lane == 0) sm.sv_top[ph][warp - 4] = top;
                 fence_async_smem();
                 mbar_arrive(&sm.bars[kBarK]);
                 rows_of(page, s + 1, at);
