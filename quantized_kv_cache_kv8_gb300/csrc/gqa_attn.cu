@@ -65,7 +65,7 @@ struct Smem {
     uint4 q[QP][NV][D / 32][32];          // queries, in operand order, two products' each
     float qs[8 * NV];                     // sm log2(e) 2^e of each vector
     float m[kWarps][8 * NV], l[kWarps][8 * NV], f[kWarps][8 * NV];
-    int64_t part[Walk<NV>::template kScratch<kNT>];
+    int64_t part[2 * kWarps + 2];
     Walk<NV> walk;
     GqaSegment seg;
     int more;
@@ -242,22 +242,32 @@ __global__ void __launch_bounds__(kNT, sm_ctas<D, NV>()) gqa_attn_kernel(const _
     Smem<D, NV, QP>& sm = *reinterpret_cast<Smem<D, NV, QP>*>(raw);
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-    {
+    if (tid == 0) p.cuts[blockIdx.x].count = 0;
+    if (p.n_seq <= W::kFew) {
+        if (warp == 0) {
+            W walk;
+            const bool any = walk.start_few(p, blockIdx.x, gridDim.x);
+            if (lane == 0) {
+                sm.walk = walk;
+                sm.more = any && walk.get(p, sm.seg);
+            }
+        }
+    } else {
         W walk;
-        if (tid == 0) p.cuts[blockIdx.x].count = 0;
-        if (!walk.template start<kNT>(p, blockIdx.x, gridDim.x, sm.part)) return;
-        if (tid == 0) sm.walk = walk;
-        // the merge comes early only to a short call: its waiting CTAs, and those of the call
-        // behind it, would keep this kernel's from starting
-        if (walk.total <= 16 * walk.ctas) launch_dependents();
+        const bool any = walk.template start_many<kNT>(p, blockIdx.x, gridDim.x, sm.part, sm.part + 2 * kWarps);
+        if (tid == 0) {
+            sm.walk = walk;
+            sm.more = any && walk.get(p, sm.seg);
+        }
     }
+    __syncthreads();
+    // the merge comes early only to a short call: its waiting CTAs, and those of the call
+    // behind it, would keep this kernel's from starting
+    if (!sm.more || sm.walk.per <= 16) launch_dependents();
+    if (!sm.more) return;
     const GqaSegment& seg = sm.seg;
     const int32_t in_page = (1 << p.shift) - 1;
     for (;;) {
-        // one copy of the walk: its state would cost every thread 40 registers
-        if (tid == 0) sm.more = sm.walk.get(p, sm.seg);
-        __syncthreads();
-        if (!sm.more) break;
         load_queries<D, NV, QP, QT>(p, seg, sm);
         const int32_t all = gqa_limit(p, seg, seg.vec0);   // rows that all vectors see
         const int32_t end = min(seg.limit, seg.u1 * kN), seq = seg.b;
@@ -532,13 +542,19 @@ __global__ void __launch_bounds__(kNT, sm_ctas<D, NV>()) gqa_attn_kernel(const _
         }
         // a CTA begins one cut tile at most, its last
         if (tid == 0 && !whole && seg.u0 == 0) p.cuts[blockIdx.x] = GqaCut{seg.count, seg.h, seg.vec0, seg.vecs, seg.q0, 0};
+        if (seg.last) break;
+        __syncthreads();   // the segment is read
         if (warp == 0) {
             W walk = sm.walk;
-            walk.next(p);
+            const bool more = walk.next(p);
             __syncwarp();
-            if (lane == 0) sm.walk = walk;
+            if (lane == 0) {
+                sm.walk = walk;
+                sm.more = more && walk.get(p, sm.seg);
+            }
         }
         __syncthreads();   // the totals and queries are free for the next tile
+        if (!sm.more) break;
     }
 }
 

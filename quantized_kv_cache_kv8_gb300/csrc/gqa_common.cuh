@@ -47,7 +47,9 @@ struct GqaParams {
 };
 
 struct GqaSeq {
-    int64_t q0, n, base, rows, tiles, j0, D, before, per_head;
+    int32_t n, rows, base, tiles;
+    int64_t q0, D, before, per_head;
+    int64_t j0;
 };
 // The tile that a CTA begins and does not end: how many CTAs share it (0: there is none), where its outputs go.
 struct GqaCut {
@@ -62,25 +64,28 @@ struct GqaSegment {
     int32_t vecs;           // vectors of the tile
     int32_t base, rows;     // token i sees base + 1 + i rows (causal) or all of them
     int32_t limit;          // rows the tile's last vector sees
-    int32_t u0, u1, units;
+    int32_t u0, u1;
+    int32_t last;           // the CTA's last
     int32_t first, count;   // of a cut tile: the first CTA that holds steps of it, and how many do
     int32_t slot;           // where this CTA leaves its state of it; -1: the tile is whole
     int64_t q0;             // the sequence's first token
 };
 
+// A CTA's walk over its segments, by one warp (the others read the segment from shared memory: the
+// walk would cost every thread 40 registers, and each line of its code may have to be fetched).
+// What only batches with several tiles a head need stands in functions of its own.
 template <int M, int N, int OV>
 struct GqaWalk {
     static_assert(N % M == 0, "closed form");
-    template <int NT>
-    static constexpr int kScratch = NT / 32 + 2 + sizeof(GqaSeq) / 8;
-    int64_t v_end, total, ctas, c;
-    int32_t b;
-    int64_t x;        // h * tiles + j of the current tile
-    int64_t seq_v;
+    static constexpr int kScratch = 2;   // int64s a warp of start_many
+    int64_t v_end, per, total;   // the CTA's last number + 1; numbers a CTA, in all
+    int32_t extra, ctas, c;      // CTAs with one number more; CTAs that hold any; this one
+    int32_t b, h, j;             // sequence, kv head, tile
+    int64_t seq_v;               // the sequence's first number
     GqaSeq s;
     int64_t u0;
 
-    __device__ __noinline__ static GqaSeq shape(const GqaParams& p, int b) {
+    __device__ __forceinline__ static GqaSeq shape(const GqaParams& p, int b) {
         GqaSeq s{0, 0, 0, 0, 0, 0, 0, 0, 0};
         if (b >= p.n_seq) return s;
         const int64_t a = p.cu_q[b], e = p.cu_q[b + 1];
@@ -91,135 +96,177 @@ struct GqaWalk {
         if (a < 0 || e <= a || e > p.max_tok) return s;
         kv = min(max(kv, (int64_t)0), cap);
         s.q0 = a;
-        s.n = e - a;
-        s.rows = kv;
-        s.base = kv - s.n;
-        s.tiles = (s.n * p.group + M - 1) / M;
+        s.n = (int32_t)(e - a);
+        s.rows = (int32_t)kv;
+        s.base = (int32_t)(kv - s.n);
+        s.tiles = (int32_t)(((int64_t)s.n * p.group + M - 1) / M);
+        // the last tile's last vector is the last token's, which sees every row
+        const int64_t last = OV + max(1, (s.rows + N - 1) / N);
+        s.per_head = s.tiles == 1 ? last : many(p, s) + last;
+        return s;
+    }
+    // Numbers of a head before its last tile; fills in the closed form.
+    __device__ __noinline__ static int64_t many(const GqaParams& p, GqaSeq& s) {
         if (p.causal) {
-            const int64_t G = p.group;
-            s.j0 = s.base >= 0 ? 0 : (-s.base * G) / M;   // first tile with limit >= 1
-            const int64_t C = G * (s.base + N) + M - 1;
+            const int64_t G = p.group, base = s.base;
+            s.j0 = base >= 0 ? 0 : (-base * G) / M;   // first tile with limit >= 1
+            const int64_t C = G * (base + N) + M - 1;
             s.D = C >= 0 ? C / M : -((-C + M - 1) / M);
             s.before = floor_sum(p, s.j0 + s.D);
         }
-        s.per_head = prefix(p, s, s.tiles - 1) + OV + units(p, s, s.tiles - 1);
-        return s;
-    }
-    // rows that the last vector of tile j sees
-    __device__ static int64_t limit(const GqaParams& p, const GqaSeq& s, int64_t j) {
-        if (!p.causal) return s.rows;
-        return max((int64_t)0, s.base + 1 + min(s.n - 1, quot(M * j + M - 1, p.group)));
-    }
-    __device__ static int64_t units(const GqaParams& p, const GqaSeq& s, int64_t j) {
-        return max((int64_t)1, (limit(p, s, j) + N - 1) / N);
+        return prefix_many(p, s, s.tiles - 1);
     }
     __device__ __noinline__ static int64_t floor_sum(const GqaParams& p, int64_t n) {   // sum_{k<n} floor(k / R)
         const int64_t R = (int64_t)p.group * (N / M), q = quot(n, R), r = n - q * R;
         return R * (q * (q - 1) / 2) + q * r;
     }
-    // numbers of a head before tile j (j < tiles)
-    __device__ static int64_t prefix(const GqaParams& p, const GqaSeq& s, int64_t j) {
-        if (!p.causal) return j * (OV + max((int64_t)1, (s.rows + N - 1) / N));
+    // Numbers of a head before tile j (j < tiles).
+    __device__ __noinline__ static int64_t prefix_many(const GqaParams& p, const GqaSeq& s, int64_t j) {
+        if (!p.causal) return j * (OV + max(1, (s.rows + N - 1) / N));
         const int64_t v = OV * j + min(j, s.j0);
         return j <= s.j0 ? v : v + floor_sum(p, j + s.D) - s.before;
     }
-    __device__ __forceinline__ int64_t start_of(int64_t k) const { return quot(total * k, ctas); }
-    // CTA of number v
-    __device__ __forceinline__ int64_t cta_of(int64_t v) const {
-        int64_t k = quot(v * ctas, total);
-        while (start_of(k + 1) <= v) ++k;
-        while (start_of(k) > v) --k;
-        return k;
+    __device__ __forceinline__ static int64_t prefix(const GqaParams& p, const GqaSeq& s, int64_t j) {
+        return j == 0 ? 0 : prefix_many(p, s, j);
     }
-
-    // By all NT threads; part: kScratch<NT> int64s.  False when CTA k has nothing to do.
-    template <int NT>
-    __device__ __forceinline__ bool start(const GqaParams& p, int64_t k, int64_t n_cta, int64_t* part) {
-        const int tid = threadIdx.x;
+    // Rows that the last vector of tile j sees.
+    __device__ __forceinline__ static int32_t limit(const GqaParams& p, const GqaSeq& s, int32_t j) {
+        if (!p.causal || j == s.tiles - 1) return s.rows;
+        return max(0, s.base + 1 + (int32_t)((uint32_t)(M * j + M - 1) / (uint32_t)p.group));
+    }
+    __device__ __forceinline__ int64_t start_of(int64_t k) const { return k * per + min(k, (int64_t)extra); }
+    // CTA of number v
+    __device__ __forceinline__ int32_t cta_of(int64_t v) const {
+        const int64_t big = (int64_t)extra * (per + 1);
+        return (int32_t)(v < big ? quot(v, per + 1) : extra + quot(v - big, per));
+    }
+    // The numbers dealt out, this CTA's share; false when it has none.
+    __device__ __forceinline__ bool deal(int64_t sum, int32_t k, int32_t n_cta) {
         c = k;
-        total = 0;
-        GqaSeq y;
-        int64_t n = 0, incl = 0, sum = 0, v0 = 0, first = 0;
-#pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll 1
-            for (int k0 = 0; k0 < p.n_seq; k0 += NT) {
-                if (pass == 0 || p.n_seq > NT) {   // a batch of at most NT sequences is read once
-                    y = shape(p, k0 + tid);
-                    n = y.per_head * p.n_kv;
-                    incl = block_scan<NT>(n, part, &sum);
-                }
-                if (pass == 0) {
-                    total += sum;
-                    continue;
-                }
-                if (v0 >= first + incl - n && v0 < first + incl) {
-                    GqaSeq* own = reinterpret_cast<GqaSeq*>(part + NT / 32 + 2);
-                    *own = y;
-                    part[NT / 32] = k0 + tid;
-                    part[NT / 32 + 1] = first + incl - n;
-                }
-                first += sum;
-                if (v0 < first) break;
-            }
-            if (pass == 0) {
-                ctas = min(n_cta, total);
-                if (c >= ctas) return false;   // every thread alike
-                v0 = start_of(c);
-                v_end = start_of(c + 1);
-            }
-        }
-        __syncthreads();
-        b = (int32_t)part[NT / 32];
-        seq_v = part[NT / 32 + 1];
-        s = *reinterpret_cast<const GqaSeq*>(part + NT / 32 + 2);
-        const int64_t h = quot(v0 - seq_v, s.per_head), v = v0 - seq_v - h * s.per_head;
-        int64_t lo = 0, hi = s.tiles;
+        total = sum;
+        ctas = (int32_t)min((int64_t)n_cta, sum);
+        if (c >= ctas) return false;
+        per = quot(sum, ctas);
+        extra = (int32_t)(sum - per * ctas);
+        v_end = start_of(c + 1);
+        return true;
+    }
+    // The place of number v in sequence b (its shape in s, first number in seq_v).
+    __device__ __forceinline__ void place(const GqaParams& p, int64_t v) {
+        int64_t x = v - seq_v;
+        h = x < s.per_head ? 0 : (int32_t)quot(x, s.per_head);
+        x -= h * s.per_head;
+        int32_t lo = 0, hi = s.tiles;
         while (hi - lo > 1) {
-            const int64_t mid = (lo + hi) / 2;
-            if (prefix(p, s, mid) <= v) lo = mid;
+            const int32_t mid = lo + (hi - lo) / 2;
+            if (prefix_many(p, s, mid) <= x) lo = mid;
             else hi = mid;
         }
-        x = h * s.tiles + lo;
-        u0 = max((int64_t)0, v - prefix(p, s, lo) - OV);
+        j = lo;
+        u0 = max((int64_t)0, x - prefix(p, s, lo) - OV);
+    }
+    // By one warp, for batches of up to kFew sequences.  False when CTA k has nothing to do.
+    static constexpr int kFew = 256;
+    __device__ __forceinline__ bool start_few(const GqaParams& p, int32_t k, int32_t n_cta) {
+        const int lane = threadIdx.x & 31;
+        GqaSeq y = shape(p, lane);
+        int64_t mine = y.per_head * p.n_kv;
+#pragma unroll 1
+        for (int i = lane + 32; i < p.n_seq; i += 32) mine += shape(p, i).per_head * p.n_kv;
+        int64_t sum = mine;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        if (!deal(sum, k, n_cta)) return false;
+        const int64_t v0 = start_of(c);
+        int64_t first = 0;
+#pragma unroll 1
+        for (int k0 = 0;; k0 += 32) {
+            if (k0 > 0) y = shape(p, k0 + lane);
+            const int64_t n = y.per_head * p.n_kv;
+            int64_t incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t t = __shfl_up_sync(kFull, incl, o);
+                if (lane >= o) incl += t;
+            }
+            const unsigned who = __ballot_sync(kFull, v0 >= first + incl - n && v0 < first + incl);
+            if (who) {
+                const int l = __ffs(who) - 1;
+                b = k0 + l;
+                seq_v = __shfl_sync(kFull, first + incl - n, l);
+                break;
+            }
+            first += __shfl_sync(kFull, incl, 31);
+        }
+        s = shape(p, b);
+        place(p, v0);
+        return true;
+    }
+    // By all NT threads of the CTA, any number of sequences; part: 2 NT / 32 int64s, found: 2.
+    template <int NT>
+    __device__ __noinline__ bool start_many(const GqaParams& p, int32_t k, int32_t n_cta, int64_t* part, int64_t* found) {
+        const int tid = threadIdx.x;
+        int64_t all = 0, incl, sum;
+        for (int i = tid; i < p.n_seq; i += NT) all += shape(p, i).per_head * p.n_kv;
+        block_scan<NT>(all, part, &sum);
+        if (!deal(sum, k, n_cta)) return false;   // every thread alike
+        const int64_t v0 = start_of(c);
+        int64_t first = 0;
+        for (int k0 = 0; k0 < p.n_seq; k0 += NT) {
+            const int64_t n = shape(p, k0 + tid).per_head * p.n_kv;
+            incl = block_scan<NT>(n, part, &sum);
+            if (v0 >= first + incl - n && v0 < first + incl) {
+                found[0] = k0 + tid;
+                found[1] = first + incl - n;
+            }
+            first += sum;
+            if (v0 < first) break;
+        }
+        __syncthreads();
+        b = (int32_t)found[0];
+        seq_v = found[1];
+        s = shape(p, b);
+        place(p, v0);
         return true;
     }
     // The current segment; false past the CTA's last.
-    __device__ __noinline__ bool get(const GqaParams& p, GqaSegment& g) const {
-        if (b >= p.n_seq) return false;
-        const int64_t h = quot(x, s.tiles), j = x - h * s.tiles;
-        const int64_t tile_v = seq_v + h * s.per_head + prefix(p, s, j), lim = limit(p, s, j);
-        const int64_t n = max((int64_t)1, (lim + N - 1) / N), u1 = min(n, v_end - tile_v - OV);
+    __device__ __forceinline__ bool get(const GqaParams& p, GqaSegment& g) const {
+        const int64_t tile_v = seq_v + h * s.per_head + prefix(p, s, j);
+        const int32_t lim = limit(p, s, j), n = max(1, (lim + N - 1) / N);
+        const int64_t end = v_end - tile_v - OV;
+        const int32_t u1 = (int32_t)min((int64_t)n, end);
         if (u1 <= u0) return false;
         g.b = b;
-        g.h = (int32_t)h;
-        g.limit = (int32_t)lim;
-        g.units = (int32_t)n;
+        g.h = h;
+        g.limit = lim;
         g.u0 = (int32_t)u0;
-        g.u1 = (int32_t)u1;
+        g.u1 = u1;
+        g.last = end <= n;
         g.q0 = s.q0;
-        g.vec0 = (int32_t)(M * j);
-        g.vecs = (int32_t)min((int64_t)M, s.n * p.group - M * j);
-        g.base = (int32_t)s.base;
-        g.rows = (int32_t)s.rows;
+        g.vec0 = M * j;
+        g.vecs = (int32_t)min((int64_t)M, (int64_t)s.n * p.group - (int64_t)M * j);
+        g.base = s.base;
+        g.rows = s.rows;
         g.slot = -1;
         if (u0 > 0 || u1 < n) {
             // a CTA begins at most one tile that it does not end, and ends one that it did not begin
-            g.first = (int32_t)(u0 == 0 ? c : cta_of(tile_v + OV));
-            g.count = (int32_t)cta_of(tile_v + OV + n - 1) - g.first + 1;
-            g.slot = slot((int32_t)c, g.first);
+            g.first = u0 == 0 ? c : cta_of(tile_v + OV);
+            g.count = (u1 == n ? c : cta_of(tile_v + OV + n - 1)) - g.first + 1;
+            g.slot = slot(c, g.first);
         }
         return true;
     }
-    // On to the next tile, by whole warps (sequences without new tokens are passed 32 at a time).
-    __device__ __noinline__ void next(const GqaParams& p) {
+    // On to the next tile, by a whole warp (sequences without new tokens are passed 32 at a time).
+    // False past the CTA's last.
+    __device__ __forceinline__ bool next(const GqaParams& p) {
         u0 = 0;
-        if (++x < s.tiles * p.n_kv) return;
+        if (++j < s.tiles) return true;
+        j = 0;
+        if (++h < p.n_kv) return true;
+        h = 0;
         seq_v += s.per_head * p.n_kv;
-        x = 0;
-        ++b;
-        if (seq_v >= v_end) b = p.n_seq;   // the rest is for the CTAs after this one
-        for (; b < p.n_seq; b += 32) {
+        if (seq_v >= v_end) return false;
+        for (++b; b < p.n_seq; b += 32) {
             const int k = b + (int)(threadIdx.x & 31);
             bool some = false;
             if (k < p.n_seq) {
@@ -230,9 +277,11 @@ struct GqaWalk {
             if (hit == 0u) continue;
             b += __ffs(hit) - 1;
             s = shape(p, b);
-            return;
+            return true;
         }
+        return false;
     }
+    // Where a CTA leaves its state of a tile: its own begun and not ended, or the end of another's.
     __device__ static int32_t slot(int32_t k, int32_t first) { return k == first ? 2 * k + 1 : 2 * k; }
 };
 

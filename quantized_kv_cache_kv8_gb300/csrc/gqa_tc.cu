@@ -61,7 +61,7 @@ struct Misc {
     float qs[kM];
     float ref_tot[kM], sum_tot[kM];   // of the totals
     uint64_t bars[kBars];
-    int64_t part[Walk::kScratch<kNT>];
+    int64_t part[2 * (kNT / 32) + 2];
     Walk walk;
     GqaSegment seg;
     uint32_t tmem;
@@ -373,11 +373,25 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();
     if (tid == 0) p.cuts[blockIdx.x].count = 0;
-    {
+    if (p.n_seq <= Walk::kFew) {
+        if (warp == 0) {
+            Walk walk;
+            const bool any = walk.start_few(p, blockIdx.x, gridDim.x);
+            if (lane == 0) {
+                sm.walk = walk;
+                sm.more = any && walk.get(p, sm.seg);
+            }
+        }
+    } else {
         Walk walk;
-        if (!walk.template start<kNT>(p, blockIdx.x, gridDim.x, sm.part)) return;
-        if (tid == 0) sm.walk = walk;
+        const bool any = walk.template start_many<kNT>(p, blockIdx.x, gridDim.x, sm.part, sm.part + 2 * (kNT / 32));
+        if (tid == 0) {
+            sm.walk = walk;
+            sm.more = any && walk.get(p, sm.seg);
+        }
     }
+    __syncthreads();
+    if (!sm.more) return;
     if (smem_u32(raw) & 1023u) {   // the swizzle counts on it
         if (tid == 0) set_err(p.err, KVQ_ERR_DEVICE);
         return;
@@ -400,14 +414,15 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
     launch_dependents();   // a kernel that allocates tensor memory may come now: this CTA has its own
     const uint32_t tmem = sm.tmem;
     volatile int* abort_flag = &sm.abort;
-    if (p.stall_polls > 0 && tid == 0) mbar_wait(&sm.bars[kBarNever], 0, abort_flag, p.stall_polls);
+    if (p.stall_polls > 0) {
+        if (tid == 0) mbar_wait(&sm.bars[kBarNever], 0, abort_flag, p.stall_polls);
+        __syncthreads();
+    }
     const GqaSegment& seg = sm.seg;
     uint32_t it = 0;       // steps so far: the barriers' phases
     uint32_t tiles = 0;
     for (;; ++tiles) {
-        if (tid == 0) sm.more = sm.walk.get(p, sm.seg);
-        __syncthreads();
-        if (!sm.more || sm.abort) break;
+        if (sm.abort) break;   // alike for all: nothing raises it here
         const int u0 = seg.u0, n_steps = seg.limit > u0 * kN ? min(seg.u1 - u0, (seg.limit - u0 * kN + kN - 1) / kN) : 0;
         const int32_t all = gqa_limit(p, seg, seg.vec0);   // rows that all vectors see
         load_queries<D, QP, QT>(p, seg, sm, raw + C::kOffQ);
@@ -638,17 +653,22 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
             }
         }
         it += n_steps;
-        if (warp == 4) {
-            __syncwarp();
-            Walk walk = sm.walk;
-            walk.next(p);
-            __syncwarp();
-            if (lane == 0) sm.walk = walk;
-        }
         tc_before();
         __syncthreads();
         tc_after();
-        if (sm.abort) break;
+        if (sm.abort || seg.last) break;
+        __syncthreads();   // the segment is read
+        if (warp == 4) {
+            Walk walk = sm.walk;
+            const bool more = walk.next(p);
+            __syncwarp();
+            if (lane == 0) {
+                sm.walk = walk;
+                sm.more = more && walk.get(p, sm.seg);
+            }
+        }
+        __syncthreads();
+        if (!sm.more) break;
     }
     tc_before();
     __syncthreads();
@@ -656,46 +676,65 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
     if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
 }
 
-// Cut tiles joined: CTA (c, k) the dims 32 k .. of the tile that CTA c began, a vector a thread.
+// Cut tiles joined: CTA (c, k) the dims 16 k .. of the tile that CTA c began, a vector a thread in
+// each of four groups that share the states.
+constexpr int kMergeGroups = 4, kMergeDims = 16;
 template <int D, typename QT>
-__global__ void __launch_bounds__(kM) gqa_tc_merge_kernel(const __grid_constant__ GqaParams p) {
+__global__ void __launch_bounds__(kM * kMergeGroups) gqa_tc_merge_kernel(const __grid_constant__ GqaParams p) {
+    constexpr int kE = kMergeDims / 4;
+    __shared__ float2 stat[kMergeGroups][kM];
+    __shared__ float4 part[kMergeGroups][kE][kM];
     grid_dependency_wait();
     launch_dependents();
-    const int first = blockIdx.x, k = blockIdx.y, v = threadIdx.x;
+    const int first = blockIdx.x, k = blockIdx.y, v = threadIdx.x % kM, grp = threadIdx.x / kM;
     const GqaCut cut = p.cuts[first];
     if (cut.count == 0) return;
+    auto take = [](float4& o, const float4& x, float a, float b) {
+        o.x = o.x * a + x.x * b;
+        o.y = o.y * a + x.y * b;
+        o.z = o.z * a + x.z * b;
+        o.w = o.w * a + x.w * b;
+    };
     float top = kNone, sum = 0.0f;
-    float4 o[8] = {};
-#pragma unroll 2
-    for (int i = 0; i < cut.count; ++i) {
+    float4 o[kE] = {};
+#pragma unroll 4
+    for (int i = grp; i < cut.count; i += kMergeGroups) {
         const int sl = Walk::slot(first + i, first);
         const float L = __ldcg(&p.ws_ml[sl * kM + v]).x;
-        const float4* src = reinterpret_cast<const float4*>(p.ws_o) + ((int64_t)sl * (D / 4) + 8 * k) * kM + v;
-        float4 x[8];
+        const float4* src = reinterpret_cast<const float4*>(p.ws_o) + ((int64_t)sl * (D / 4) + kE * k) * kM + v;
+        float4 x[kE];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __ldcg(src + e * kM);
+        for (int e = 0; e < kE; ++e) x[e] = __ldcg(src + e * kM);
         const float n = fmaxf(top, L), a = ex2(top - n), b = L == kNone ? 0.0f : ex2(L - n);
         sum = sum * a + b;
         top = n;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            o[e].x = o[e].x * a + x[e].x * b;
-            o[e].y = o[e].y * a + x[e].y * b;
-            o[e].z = o[e].z * a + x[e].z * b;
-            o[e].w = o[e].w * a + x[e].w * b;
-        }
+        for (int e = 0; e < kE; ++e) take(o[e], x[e], a, b);
     }
-    if (v >= cut.vecs) return;
+    stat[grp][v] = make_float2(top, sum);
+#pragma unroll
+    for (int e = 0; e < kE; ++e) part[grp][e][v] = o[e];
+    __syncthreads();
+    if (grp != 0 || v >= cut.vecs) return;
+#pragma unroll
+    for (int w = 1; w < kMergeGroups; ++w) {
+        const float2 s = stat[w][v];
+        const float n = fmaxf(top, s.x), a = ex2(top - n), b = ex2(s.x - n);
+        sum = sum * a + s.y * b;
+        top = n;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) take(o[e], part[w][e][v], a, b);
+    }
     GqaSegment seg;
     seg.h = cut.h;
     seg.q0 = cut.q0;
-    QT* out = static_cast<QT*>(p.out) + gqa_vector<D>(p, seg, cut.vec0 + v) + 32 * k;
+    QT* out = static_cast<QT*>(p.out) + gqa_vector<D>(p, seg, cut.vec0 + v) + kMergeDims * k;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float4 a = o[2 * e], b = o[2 * e + 1];
+    for (int e = 0; e < kE; e += 2) {
+        const float4 a = o[e], b = o[e + 1];
         const float x[8] = {a.x * inv, a.y * inv, a.z * inv, a.w * inv, b.x * inv, b.y * inv, b.z * inv, b.w * inv};
-        store8(out + 8 * e, x);
+        store8(out + 4 * e, x);
     }
 }
 
@@ -710,7 +749,7 @@ cudaError_t launch_kernel(const GqaParams& p, cudaStream_t stream) {
     timing_mark(stream, 0);
     e = launch_chained(gqa_tc_kernel<D, QP, QT>, ctas, kNT, smem, stream, p);
     timing_mark(stream, 1);
-    if (e == cudaSuccess) e = launch_chained(gqa_tc_merge_kernel<D, QT>, dim3(ctas, D / 32), kM, 0, stream, p);
+    if (e == cudaSuccess) e = launch_chained(gqa_tc_merge_kernel<D, QT>, dim3(ctas, D / kMergeDims), kM * kMergeGroups, 0, stream, p);
     timing_mark(stream, 2);
     return e;
 }
