@@ -570,7 +570,7 @@ size_t kv_gqa_attn_paged_workspace_size(kvq_dtype q_dtype, int32_t n_seq, int32_
  *   kv_lens      [n_seq] int64, at most min(table_stride, n_pages) * page_rows
  * Products take 16-bit operands, sums are f32: outputs are within 1e-5 of a vector's largest
  * before the rounding to q_dtype, but for what f32 scores of some hundreds lose and, where a
- * sequence brings more than 32 query vectors to a kv head on average and queries are bf16 (tensor
+ * sequence brings more than 24 query vectors to a kv head on average and queries are bf16 (tensor
  * cores), a rounding of each row's weight to f16 (2^-11 of it).  A row with a NaN code, or a scale that
  * is no finite number, makes NaN the tokens that see it and leaves the others as they are.  Invalid
  * lengths or offsets and pages outside [0, n_pages) set KVQ_ERR_ARG in the workspace's

@@ -252,6 +252,11 @@ __device__ __forceinline__ int merge_lists(int keep, int n, int beam, int lane, 
     return found;
 }
 
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
 // How many of the first n keys are better than k.
 __device__ __forceinline__ int rank_of(const uint64_t* list, int n, uint64_t k) {
     int rank = 0, j = 0;
@@ -311,14 +316,11 @@ __global__ void __launch_bounds__(kNT, 4) beam_select_kernel(const __grid_consta
     float ref = -INFINITY, sum = 0.0f;
     float bound = -INFINITY;
     bool first = true;
-    uint4 r[kTrip];
-    x.load(r, v0 + tid, kNT, v1);
+    uint4 even[kTrip], odd[kTrip];
+    x.load(even, v0 + tid, kNT, v1);
     float rl = 0.0f, off = 1.0f;   // ref l in f32; 2^(what that rounding added)
     int trip = 0;
-#pragma unroll 1
-    for (uint32_t t0 = v0; t0 < v1; t0 += kTrip * kNT, ++trip) {
-        uint4 ahead[kTrip];
-        x.load(ahead, t0 + kTrip * kNT + tid, kNT, v1);
+    const auto take = [&](uint32_t t0, const uint4 (&r)[kTrip]) {
         float vtop[kTrip], top = -INFINITY;
 #pragma unroll
         for (int u = 0; u < kTrip; ++u) {
@@ -332,15 +334,26 @@ __global__ void __launch_bounds__(kNT, 4) beam_select_kernel(const __grid_consta
                 rl = ref * kL;
                 off = ex2(__fmaf_rn(-ref, kL, rl));
             }
-            float part[2] = {0.0f, 0.0f};
+            // two elements an instruction
+            const uint64_t l2 = pack2(kL, kL), rl2 = pack2(-rl, -rl);
+            uint64_t part[2] = {0ull, 0ull};
 #pragma unroll
             for (int u = 0; u < kTrip; ++u) {
                 float f[V];
                 R::floats(r[u], f);
 #pragma unroll
-                for (int i = 0; i < V; ++i) part[i & 1] += ex2(__fmaf_rn(f[i], kL, -rl));
+                for (int i = 0; i < V; i += 2) {
+                    uint64_t t;
+                    float a, b;
+                    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(pack2(f[i], f[i + 1])), "l"(l2), "l"(rl2));
+                    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(t));
+                    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(part[i / 2 & 1]) : "l"(part[i / 2 & 1]), "l"(pack2(ex2(a), ex2(b))));
+                }
             }
-            const float all = (part[0] + part[1]) * off;
+            float a0, a1, b0, b1;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(part[0]));
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(b0), "=f"(b1) : "l"(part[1]));
+            const float all = ((a0 + a1) + (b0 + b1)) * off;
             // NaN or infinite logits, and such that ref l is off by more than 2^-4
             sum += all == all && fabsf(ref) <= 0x1p19f ? all : odd_sum<T>(r, ref);
         }
@@ -393,8 +406,16 @@ __global__ void __launch_bounds__(kNT, 4) beam_select_kernel(const __grid_consta
             }
         }
         first = false;
-#pragma unroll
-        for (int u = 0; u < kTrip; ++u) r[u] = ahead[u];
+        ++trip;
+    };
+    constexpr uint32_t kSpan = kTrip * kNT;
+#pragma unroll 1
+    for (uint32_t t0 = v0; t0 < v1; t0 += 2 * kSpan) {
+        x.load(odd, t0 + kSpan + tid, kNT, v1);
+        take(t0, even);
+        if (t0 + kSpan >= v1) break;
+        x.load(even, t0 + 2 * kSpan + tid, kNT, v1);
+        take(t0 + kSpan, odd);
     }
     // the slice's sum, joined in a fixed order
     Mass mass{ref, sum};

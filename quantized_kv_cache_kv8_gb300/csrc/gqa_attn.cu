@@ -52,7 +52,7 @@ constexpr int kFlush = 32;          // steps between additions to the totals
 constexpr int kOv = 1;              // prologue allowance, in steps
 // NV blocks of 8 vectors a tile
 template <int NV>
-using Walk = GqaWalk<8 * NV, kN, kOv>;
+using Walk = GqaWalk<8 * NV, kN, kOv, 1>;
 
 template <int D, int NV>
 constexpr int sm_ctas() {   // CTAs an SM holds (registers)
@@ -644,8 +644,10 @@ cudaError_t launch_type(const GqaParams& p, kvq_dtype dt, cudaStream_t stream) {
     return dt == KVQ_BF16 ? launch_dims<D, 1, __nv_bfloat16>(p, stream) : launch_dims<D, 2, float>(p, stream);
 }
 
-// Above so many vectors of a sequence and kv head, on average, the tensor-core kernel.
-constexpr int64_t kTensorVectors = 32;
+// Above so many vectors of a sequence and kv head, on average, the tensor-core kernel takes less
+// time (16 sequences of 4000 rows, 8 kv heads of 128, bf16: 16 vectors 72 us against 58, 32
+// vectors 72 against 89; f32: 32 vectors 134 against 96, 64 vectors 144 against 164).
+constexpr int64_t tensor_vectors(kvq_dtype dt) { return dt == KVQ_BF16 ? 24 : 48; }
 
 }  // namespace
 
@@ -680,7 +682,7 @@ cudaError_t launch_gqa_attn(const GqaAttnCall& c, cudaStream_t stream) {
     p.cuts = reinterpret_cast<GqaCut*>(ws + kWsHeader);
     p.ws_ml = reinterpret_cast<float2*>(ws + kWsHeader + kGqaCutBytes);
     p.ws_o = reinterpret_cast<float*>(p.ws_ml + 2 * kGqaMaxCtas * 16);
-    if (gqa_tc_supported(c.head_dim, c.dtype) && p.max_tok * p.group > kTensorVectors * (int64_t)p.n_seq)
+    if (gqa_tc_supported(c.head_dim, c.dtype) && p.max_tok * p.group > tensor_vectors(c.dtype) * p.n_seq)
         return launch_gqa_tc(p, c.head_dim, c.dtype, p.ws_ml, stream);
     switch (c.head_dim) {
         case 64: return launch_type<64>(p, c.dtype, stream);

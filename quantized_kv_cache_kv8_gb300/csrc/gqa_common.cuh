@@ -74,7 +74,9 @@ struct GqaSegment {
 // A CTA's walk over its segments, by one warp (the others read the segment from shared memory: the
 // walk would cost every thread 40 registers, and each line of its code may have to be fetched).
 // What only batches with several tiles a head need stands in functions of its own.
-template <int M, int N, int OV>
+// LEAST: numbers a CTA takes at least, so that few long tiles are not cut into more states than
+// their joining is worth.
+template <int M, int N, int OV, int LEAST>
 struct GqaWalk {
     static_assert(N % M == 0, "closed form");
     static constexpr int kScratch = 2;   // int64s a warp of start_many
@@ -144,7 +146,7 @@ struct GqaWalk {
     __device__ __forceinline__ bool deal(int64_t sum, int32_t k, int32_t n_cta) {
         c = k;
         total = sum;
-        ctas = (int32_t)min((int64_t)n_cta, sum);
+        ctas = (int32_t)min((int64_t)n_cta, (sum + LEAST - 1) / LEAST);
         if (c >= ctas) return false;
         per = quot(sum, ctas);
         extra = (int32_t)(sum - per * ctas);

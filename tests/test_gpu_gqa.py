@@ -46,7 +46,7 @@ def attend(kvq, pool, q, lens, new, causal=True, sm=None, ws=None, extra=0, stre
 
 def check(out, q, pool, lens, new, sm, causal, what=""):
     """Against 64 bits; bf16 queries with many vectors of a kv head go the tensor cores' way, with weights in f16."""
-    wide = q.dtype == torch.bfloat16 and len(q) * (q.shape[1] // pool.heads) > 32 * len(lens)
+    wide = q.dtype == torch.bfloat16 and len(q) * (q.shape[1] // pool.heads) > 24 * len(lens)
     mass = attention(q, pool, lens, new, sm, causal, absolute=True) if wide else None
     close(out, attention(q, pool, lens, new, sm, causal), what, mass)
 
