@@ -18,7 +18,8 @@
 // more go to a list in shared memory; when it has grown by 16 their elements find their ranks by
 // counting, the best `keep` stay and the last of them is the new bound.  Should a list overflow (ascending or equal logits), the slice's best are found
 // one after another by maxima over the slice, `keep` passes in L2: slower, the same answer.
-// The slice lists of a request are merged by the CTA that comes last, a head a lane.
+// The slice lists of a request are merged by the CTA that comes last: their elements' scores, those
+// out that the best full list's last beats, ranks among the rest.
 #include "gqa.cuh"
 #include "tc_common.cuh"
 
@@ -195,7 +196,7 @@ __device__ __forceinline__ Wide wide_log(float s) {
 
 struct Shared {
     union alignas(16) {
-        uint64_t list[kList];
+        uint64_t list[kList + 2];   // read in pairs
         uint64_t cand[kMaxCand];
     };
     Mass warp_mass[kWarps];
@@ -204,68 +205,54 @@ struct Shared {
     Wide base[kMaxBeams];    // cum - log of the mass against the largest logit
     float cum[kMaxBeams], top[kMaxBeams];
     int32_t count[kMaxLists];
-    uint64_t best_key[kWarps][kMaxKeep];
-    uint64_t best_score[kWarps][kMaxKeep];
-    uint8_t best_beam[kWarps][kMaxKeep];
-    int32_t best_count[kWarps];
+    float2 mass[kMaxLists];
+    uint64_t floor;
+    int n_best, warp_count[kWarps];
+    alignas(16) uint64_t best[kMaxCand + 2];
+    uint16_t best_at[kMaxCand];
     uint4 vec[kVec];
     uint32_t vec_id[kVec];
     int n_vec, n_list, last;
 };
 
 __device__ __forceinline__ uint64_t ordered64(Wide x) { return ((uint64_t)ordered(x.hi) << 32) | ordered(x.lo); }
-// The lane among `who` with the largest v (uniform); those that share it.
-__device__ __forceinline__ unsigned warp_best(unsigned who, uint64_t v, int lane) {
-    const bool in = (who >> lane) & 1u;
-    const uint32_t hi = __reduce_max_sync(kFull, in ? (uint32_t)(v >> 32) : 0u);
-    who = __ballot_sync(kFull, in && (uint32_t)(v >> 32) == hi);
-    if ((who & (who - 1)) == 0u) return who;
-    const bool in2 = (who >> lane) & 1u;
-    const uint32_t lo = __reduce_max_sync(kFull, in2 ? (uint32_t)v : 0u);
-    return __ballot_sync(kFull, in2 && (uint32_t)v == lo);
-}
-
-// `keep` best of sorted lists, one a lane: score(i) the ordered score of element i of the
-// lane's list (0: none), key(i) its key.  take(k, lane, i) is called by the lane that holds the k-th.
-template <class Score, class Key, class Take>
-__device__ __forceinline__ int merge_lists(int keep, int n, int beam, int lane, Score score, Key key, Take take) {
-    int i = 0;
-    uint64_t s = n > 0 ? score(0) : 0ull;
-    uint64_t k = s ? key(0) : 0ull;
-    int found = 0;
-    for (; found < keep; ++found) {
-        unsigned who = __ballot_sync(kFull, s != 0ull);
-        if (who == 0u) break;
-        who = warp_best(who, s, lane);
-        if (who & (who - 1)) {   // the same score: the lower beam, then the better key
-            const uint32_t b = __reduce_min_sync(kFull, (who >> lane) & 1u ? (uint32_t)beam : 0xffffffffu);
-            who = __ballot_sync(kFull, ((who >> lane) & 1u) && (uint32_t)beam == b);
-            if (who & (who - 1)) who = warp_best(who, k, lane);
-        }
-        if (lane == __ffs(who) - 1) {
-            take(found, i, s, k);
-            ++i;
-            s = i < n ? score(i) : 0ull;
-            k = s ? key(i) : 0ull;
-        }
-    }
-    return found;
-}
-
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
     return r;
 }
-// How many of the first n keys are better than k.
-__device__ __forceinline__ int rank_of(const uint64_t* list, int n, uint64_t k) {
-    int rank = 0, j = 0;
+// take(i, rank) for each of the first n keys: rank, how many are larger or, being equal, before(j, i)
+// (a list of one slice has no equal keys: they hold the token).
+// By the whole CTA; as many threads share a key as there are for one.
+template <bool EQUALS, class Before, class Take>
+__device__ __forceinline__ void rank_all(const uint64_t* list, int n, Before before, Take take) {
+    int share = 1;
+    while (share < 8 && 2 * share * n <= kNT) share *= 2;
+    const int part = threadIdx.x & (share - 1);
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kNT / share) {
+        const int i = i0 + (int)threadIdx.x / share;
+        const uint64_t k = i < n ? list[i] : ~0ull;
+        int rank = 0, same = 0;
 #pragma unroll 4
-    for (; j + 1 < n; j += 2) {
-        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(list + j);
-        rank += (x.x > k) + (x.y > k);
+        for (int j = 2 * part; j < n; j += 2 * share) {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(list + j);
+            rank += x.x > k;
+            rank += j + 1 < n && x.y > k;
+            if (EQUALS) same += (x.x == k) + (j + 1 < n && x.y == k);
+        }
+        for (int o = 1; o < share; o <<= 1) {
+            rank += __shfl_xor_sync(kFull, rank, o);
+            if (EQUALS) same += __shfl_xor_sync(kFull, same, o);
+        }
+        if (part != 0 || i >= n) continue;
+        if constexpr (EQUALS)
+            if (same > 1) {
+#pragma unroll 1
+                for (int j = 0; j < n; ++j) rank += list[j] == k && j != i && before(j, i);
+            }
+        take(i, rank);
     }
-    return j < n ? rank + (list[j] > k) : rank;
 }
 // Elements of the listed vectors that reach the bound, to the list of keys.  By the whole CTA; the
 // vectors are stored, the keys need a barrier.
@@ -385,19 +372,23 @@ __global__ void __launch_bounds__(kNT, 4) beam_select_kernel(const __grid_consta
                 }
         }
         // once some more than `keep` are listed, the best `keep` stay and the last of them is the bound
-        if (t0 + kTrip * kNT < v1 && (trip < 2 || (trip & 3) == 0) &&
-            __syncthreads_or(tid == 0 && sm.n_vec + sm.n_list >= keep + 16)) {
+        if (t0 + kTrip * kNT < v1 && (trip == 0 || trip == 2 || (trip & 15) == 15)) {
+            __syncthreads();
             const int n_vec = sm.n_vec, listed = sm.n_list;
             __syncthreads();   // read by all before it grows
-            if (n_vec <= kVec && listed <= kList) {
+            if (n_vec + listed >= keep + 16 && n_vec <= kVec && listed <= kList) {
                 expand<T>(sm, n_vec, bound);
                 __syncthreads();
                 const int n = sm.n_list;
                 if (n <= kNT) {   // else the list waits
-                    const uint64_t k = tid < n ? sm.list[tid] : 0ull;
-                    const int rank = 32 * warp < n ? rank_of(sm.list, n, k) : 0;
+                    uint64_t k = 0ull;
+                    int place = keep;
+                    rank_all<false>(sm.list, n, 0, [&](int i, int rank) {
+                        k = sm.list[i];
+                        place = rank;
+                    });
                     __syncthreads();
-                    if (tid < n && rank < keep) sm.list[rank] = k;
+                    if (place < keep) sm.list[place] = k;
                     if (tid == 0) sm.n_list = min(n, keep);
                 }
                 if (tid == 0) sm.n_vec = 0;
@@ -437,11 +428,9 @@ __global__ void __launch_bounds__(kNT, 4) beam_select_kernel(const __grid_consta
     }
     uint64_t* keys = p.keys + out * keep;
     if (n <= kList) {
-        for (int i = tid; i < n; i += kNT) {
-            const uint64_t k = sm.list[i];
-            const int rank = rank_of(sm.list, n, k);
-            if (rank < keep) keys[rank] = k;
-        }
+        rank_all<false>(sm.list, n, 0, [&](int i, int rank) {
+            if (rank < keep) keys[rank] = sm.list[i];
+        });
         if (tid == 0) p.counts[out] = min(n, keep);
     } else {
         uint64_t before = ~0ull;   // the key found last
@@ -483,15 +472,17 @@ __global__ void __launch_bounds__(kNT, 4) beam_select_kernel(const __grid_consta
     if (tid == 0) p.tickets[seq] = 0u;
     const int64_t list0 = seq * lists;
     for (int i = tid; i < lists * keep; i += kNT) sm.cand[i] = __ldcg(p.keys + list0 * keep + i);
-    if (tid < lists) sm.count[tid] = __ldcg(p.counts + list0 + tid);
+    if (tid < lists) {
+        sm.count[tid] = __ldcg(p.counts + list0 + tid);
+        sm.mass[tid] = __ldcg(p.sums + list0 + tid);
+    }
+    __syncthreads();
     if (tid < p.n_beams) {
         Mass mass{-INFINITY, 0.0f};
         float top = -INFINITY;
-        for (int i = 0; i < p.splits; ++i) {
-            const int64_t l = list0 + tid * p.splits + i;
-            const float2 o = __ldcg(p.sums + l);
-            mass = join(mass, Mass{o.x, o.y});
-            if (__ldcg(p.counts + l) > 0) top = fmaxf(top, key_value(__ldcg(p.keys + l * keep)));
+        for (int l = tid * p.splits; l < (tid + 1) * p.splits; ++l) {
+            mass = join(mass, Mass{sm.mass[l].x, sm.mass[l].y});
+            if (sm.count[l] > 0) top = fmaxf(top, key_value(sm.cand[l * keep]));
         }
         const float cum = p.scores[seq * p.n_beams + tid];
         sm.top[tid] = top;
@@ -501,77 +492,76 @@ __global__ void __launch_bounds__(kNT, 4) beam_select_kernel(const __grid_consta
         sm.base[tid] = add(Wide{cum, 0.0f}, add(away, Wide{-l.hi, -l.lo}));
     }
     __syncthreads();
-    const int beam = tid < lists ? tid / p.splits : 0;
-    const float cum = sm.cum[beam];
-    const float top = sm.top[beam];
-    const bool alive = fabsf(cum) <= 3.402823466e38f;
-    const Wide base = sm.base[beam];
-    const uint64_t* mine = sm.cand + tid * keep;
-    // cum + (v - top) - log mass; what lies past f32 counts as its end
-    auto score = [&](int i) -> uint64_t {
-        const float v = key_value(mine[i]);
-        if (v == top) return ordered64(base);
-        if (top == INFINITY) return 0ull;   // beside an infinite logit
-        Wide d = two_sum(v, -top);
-        if (!(d.hi >= -3.4e38f)) d = Wide{-3.4e38f, 0.0f};
-        return ordered64(add(base, d));
-    };
-    const int n_mine = tid < lists && alive ? sm.count[tid] : 0;
-    const int warps = (lists + 31) / 32;
+    if (tid == 0) {
+        sm.floor = 0ull;
+        sm.n_best = 0;
+    }
+    __syncthreads();
+    // scores of all slices' elements.  The last of a full list has `keep` elements no worse than it: what
+    // is worse than the best such is out
+    const int n_cand = lists * keep;
+    uint64_t floor = 0ull;
+#pragma unroll 1
+    for (int i = tid; i < n_cand; i += kNT) {
+        const int list = i / keep, place = i - list * keep, beam = list / p.splits;
+        uint64_t sc = 0ull;
+        if (place < sm.count[list] && fabsf(sm.cum[beam]) <= 3.402823466e38f) {
+            const float v = key_value(sm.cand[i]), top = sm.top[beam];
+            // cum + (v - top) - log mass; what lies past f32 counts as its end; nothing beside an
+            // infinite logit
+            Wide d = v == top ? Wide{0.0f, 0.0f} : two_sum(v, -top);
+            if (!(d.hi >= -3.4e38f)) d = Wide{-3.4e38f, 0.0f};
+            if (v == top || top < INFINITY) sc = ordered64(add(sm.base[beam], d));
+            if (place == keep - 1) floor = max(floor, sc);
+        }
+        sm.cand[i] = sc;   // its key is needed again by the few that stay: from global memory
+    }
+    if (floor) atomicMax(reinterpret_cast<unsigned long long*>(&sm.floor), (unsigned long long)floor);
+    __syncthreads();
+    floor = sm.floor;
+    // what stays, in the lists' order
+#pragma unroll 1
+    for (int i0 = 0; i0 < n_cand; i0 += kNT) {
+        const int i = i0 + tid;
+        const uint64_t sc = i < n_cand ? sm.cand[i] : 0ull;
+        const bool stays = sc != 0ull && sc >= floor;
+        const unsigned who = __ballot_sync(kFull, stays);
+        if (lane == 0) sm.warp_count[warp] = __popc(who);
+        __syncthreads();
+        int at = sm.n_best;
+        for (int w = 0; w < warp; ++w) at += sm.warp_count[w];
+        at += __popc(who & ((1u << lane) - 1u));
+        if (stays) {
+            sm.best[at] = sc;
+            sm.best_at[at] = (uint16_t)i;
+        }
+        __syncthreads();
+        if (tid == kNT - 1) sm.n_best = at + (stays ? 1 : 0);
+        __syncthreads();
+    }
+    // by score, then the lower beam, then the key (a beam's score may be too large to tell its tokens apart)
+    const int m = sm.n_best;
     float* os = p.out_scores + seq * keep;
     int32_t* op = p.parents + seq * keep;
     int32_t* ot = p.tokens + seq * keep;
-    auto emit = [&](int k, uint64_t sc, uint64_t key, int bm) {
-        os[k] = from_ordered((uint32_t)(sc >> 32));
-        op[k] = (int32_t)(seq * p.n_beams + bm);
-        ot[k] = (int32_t)key_index(key);
+    const uint64_t* all = p.keys + list0 * keep;
+    const auto before = [&](int a, int b) {
+        const int at_a = sm.best_at[a], at_b = sm.best_at[b];
+        const int beam_a = at_a / keep / p.splits, beam_b = at_b / keep / p.splits;
+        return beam_a != beam_b ? beam_a < beam_b : __ldcg(all + at_a) > __ldcg(all + at_b);
     };
-    int found = 0;
-    if (warps == 1) {
-        if (warp == 0)
-            found = merge_lists(keep, n_mine, beam, lane, score, [&](int i) { return mine[i]; },
-                                [&](int k, int, uint64_t sc, uint64_t key) { emit(k, sc, key, beam); });
-    } else {
-        if (warp < warps) {
-            const int f = merge_lists(keep, n_mine, beam, lane, score, [&](int i) { return mine[i]; },
-                                      [&](int k, int, uint64_t sc, uint64_t key) {
-                                          sm.best_score[warp][k] = sc;
-                                          sm.best_key[warp][k] = key;
-                                          sm.best_beam[warp][k] = (uint8_t)beam;
-                                      });
-            if (lane == 0) sm.best_count[warp] = f;
-        }
-        __syncthreads();
-        if (warp == 0) {
-            // lists of several beams: a head's beam is its element's
-            const int l = min(lane, kWarps - 1), nl = lane < warps ? sm.best_count[l] : 0;
-            int i = 0;
-            uint64_t s_ = nl > 0 ? sm.best_score[l][0] : 0ull;
-            for (; found < keep; ++found) {
-                unsigned who = __ballot_sync(kFull, s_ != 0ull);
-                if (who == 0u) break;
-                who = warp_best(who, s_, lane);
-                if (who & (who - 1)) {
-                    const bool in = (who >> lane) & 1u;
-                    const uint32_t bm = in ? sm.best_beam[l][i] : 0xffffffffu;
-                    const uint32_t b = __reduce_min_sync(kFull, bm);
-                    who = __ballot_sync(kFull, in && bm == b);
-                    if (who & (who - 1)) who = warp_best(who, (who >> lane) & 1u ? sm.best_key[l][i] : 0ull, lane);
-                }
-                if (lane == __ffs(who) - 1) {
-                    emit(found, s_, sm.best_key[l][i], sm.best_beam[l][i]);
-                    ++i;
-                    s_ = i < nl ? sm.best_score[l][i] : 0ull;
-                }
-            }
-        }
+    rank_all<true>(sm.best, m, before, [&](int i, int rank) {
+        if (rank >= keep) return;
+        const int at = sm.best_at[i];
+        os[rank] = from_ordered((uint32_t)(sm.best[i] >> 32));
+        op[rank] = (int32_t)(seq * p.n_beams + at / keep / p.splits);
+        ot[rank] = (int32_t)key_index(__ldcg(all + at));
+    });
+    for (int k = m + tid; k < keep; k += kNT) {   // fewer continuations than asked for
+        os[k] = -INFINITY;
+        op[k] = -1;
+        ot[k] = -1;
     }
-    if (warp == 0)
-        for (int k = found + lane; k < keep; k += 32) {   // fewer continuations than asked for
-            os[k] = -INFINITY;
-            op[k] = -1;
-            ot[k] = -1;
-        }
 }
 
 // Slices of a row: 3 CTAs a SM at least, slices of at least 16 KB, lists within a request's limits.

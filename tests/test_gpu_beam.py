@@ -107,6 +107,13 @@ def test_sizes_of_logits(kvq):
         check_select(kvq, x + scale, s, 8)
 
 
+def test_scores_that_cannot_tell_logits_apart(kvq):
+    # one beam: whatever the sums round to, the larger logit is better
+    x, _ = random_logits(3, 1, 150001, torch.float32)
+    for scores in (0.0, -1e6, 1e30, -3e38):
+        check_select(kvq, x * 1e-9, torch.full((3, 1), scores, device="cuda"), 64)
+
+
 def test_rows_at_a_distance_and_unaligned(kvq):
     x, s = random_logits(2, 3, 5001, torch.bfloat16)
     wide = torch.full((2, 3, 6007), 50.0, dtype=torch.bfloat16, device="cuda")
