@@ -468,11 +468,11 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                 const uint64_t dq = umma_desc(smem_u32(raw + C::kOffQ), 16, 1024);
                 const uint64_t dk = umma_desc(smem_u32(raw + C::kOffK), 16, 1024);
 #pragma unroll
-                for (int q = 0; q < QP; ++q)
+                for (int q = QP - 1; q >= 0; --q)   // the small halves first: each product rounds the sum so far
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
                         const uint32_t at = (i / 4) * kStep + 2 * (i % 4);
-                        umma_f16(tmem, dq + q * C::kChunks * kStep + at, dk + at, kIdescS, q > 0 || i > 0);
+                        umma_f16(tmem, dq + q * C::kChunks * kStep + at, dk + at, kIdescS, q < QP - 1 || i > 0);
                     }
                 umma_commit(&sm.bars[kBarS]);
             };
@@ -480,11 +480,11 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                 tc_after();
                 const uint64_t dv = umma_desc(smem_u32(raw + C::kOffV), C::kChunk, 1024);
 #pragma unroll
-                for (int i = 0; i < kN / 16; ++i) {
-                    const uint32_t a = tmem + weight_col<QP>(i);
-                    umma_f16_ts(tmem + C::kColO, a, dv + 128 * i, kIdescO, s % C::kFlush != 0 || i > 0);
-                    if constexpr (QP == 2) umma_f16_ts(tmem + C::kColO, a + 8, dv + 128 * i, kIdescO, 1u);
-                }
+                for (int q = QP - 1; q >= 0; --q)
+#pragma unroll
+                    for (int i = 0; i < kN / 16; ++i)
+                        umma_f16_ts(tmem + C::kColO, tmem + weight_col<QP>(i) + 8 * q, dv + 128 * i, kIdescO,
+                                    s % C::kFlush != 0 || q < QP - 1 || i > 0);
                 umma_commit(&sm.bars[kBarO]);
             };
             if (tid == 0 && n_steps > 0 && mbar_spin(&sm.bars[kBarK], it & 1u, abort_flag, p.wait_limit)) issue_scores(0);
