@@ -5,25 +5,30 @@
 //   S = Q C_k^T (128 vectors x 128 rows), P = 2^(z - R) s_v, O += P C_v
 // with z = S s_k sm log2(e), the codes in f16 (exact), f32 accumulators in tensor memory.
 //
-// What bounds it: shared memory (256 vectors x 128 rows x D = 128 read 192 KB of operands
-// and move 192 KB of converted codes, at 128 bytes a cycle 3,000 cycles, for 2,048 of
-// products) and the softmax (about 4.5 instructions a score).  So two CTAs share an SM, one's
-// softmax beside the other's products, and the weights go into the second product from
-// tensor memory, over the scores they came from, instead of through shared memory.
-//   * warps 0-3: softmax, a vector a thread, so maxima and sums need no exchange; 16 scores at
-//     a time are loaded, turned into weights and stored over the first half of their
+// What bounds it: the chain of a step (scores, softmax, weights into tensor memory, products), which
+// one tile can't overlap with itself: tensor memory holds two tiles' scores and contexts and no more.
+// So two CTAs share an SM, one's softmax beside the other's products, and the weights go
+// into the second product from tensor memory, over the scores they came from, instead of
+// through shared memory.  512 bf16 tokens of 32 heads (8 of keys) of 128 on 8704 rows: 133 us, 533
+// TFLOP/s; tensor pipe 24% busy, shared memory 43%, issue slots 33%.
+// Slower: scores of 64 rows in two buffers (157 us); the next scores loaded ahead, with more
+// registers for the softmax and fewer for the converters (154).
+//   * warps 0-3: softmax, a vector a thread, so maxima and sums need no exchange; 32 scores at
+//     a time are loaded, turned into weights and stored over the first half of the scores'
 //     place (f32 queries: two f16 halves, over the whole place);
 //   * warps 4-7: codes to f16, in the layout of 128-byte swizzled rows, which the first
 //     product reads with dims along K and the second with rows along K; keys and values are asked
 //     for in turn, each as soon as the other is stored;
 //   * a lane of warp 0 issues the products: between its weights and the next scores the
-//     softmax has nothing to do (with a ninth warp for it, 96 registers a thread spilled).
+//     softmax has nothing to do (a ninth warp for it left 96 registers a thread, which
+//     spilled, and one of the converters' was missed there: 155 us).
 //
 // Numbers.  Queries as in gqa_attn.cu (bf16 exactly, f32 in two f16 halves).  R is an
 // integer per vector, max(z + log2 s_v) - 8 when it is set (f32 queries: 12); it rises
 // when a weight passes 60000, and then what has been summed is brought to it by a power of two.  bf16
 // queries: weights in one f16 (2^-11 of themselves, down to 2^-22 of the largest).
-// f32 queries: in two (2^-22).  Every 256 steps (f32 queries: 8) the accumulators, which round
+// f32 queries: in two (2^-22); products of the small halves come first, since each rounds the sum
+// so far.  Every 256 steps (f32 queries: 8) the accumulators, which round
 // towards zero, go to totals in the workspace.  Rows that are no numbers as in gqa_attn.cu.
 #include "gqa_common.cuh"
 #include "tc_common.cuh"
@@ -497,40 +502,40 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                 // waited for here: the next keys' arrival could be the phase after, seen as not yet)
                 ok = __all_sync(kFull, mbar_wait(&sm.bars[kBarS], ph, abort_flag, p.wait_limit));
                 if (ok) {
-                tc_after();
-                if (s > 0 && s % C::kFlush == 0) flush(s == C::kFlush);
-                const int32_t row0 = (u0 + s) * kN;
-                const bool partly = row0 + kN > all, context = s % C::kFlush != 0;
-                // a reference that had to rise takes its scores again (kept in registers meanwhile, they
-                // would be spilled every time)
+                    tc_after();
+                    if (s > 0 && s % C::kFlush == 0) flush(s == C::kFlush);
+                    const int32_t row0 = (u0 + s) * kN;
+                    const bool partly = row0 + kN > all, context = s % C::kFlush != 0;
+                    // a reference that had to rise takes its scores again (kept in registers meanwhile, they
+                    // would be spilled every time)
 #pragma unroll 1
-                for (int j = 0, pass = 0; j < kN / kC;) {
-                    const int32_t visible = partly ? min(max(lim - row0 - kC * j, 0), kC) : kC;
-                    uint32_t now[kC], pk[kWords<QP>];
-                    tmem_ld32(tm + kC * j, now);
-                    const float svt = sm.sv_top[st][j];
-                    tmem_wait_ld();
-                    float sum, most = 0.0f;
-                    if (partly) sum = weights<QP, true>(sm, now, j, st, qs, R, visible, pk, &most);
-                    else sum = weights<QP, false>(sm, now, j, st, qs, R, kC, pk, &most);
-                    // one half: the sum and the scales bound the weights (references leave the room, a false
-                    // alarm only costs time); two: the weights themselves
-                    if (QP == 1) most = sum * svt;
-                    const bool lift = (R == kNone && visible > 0) || !(most <= 60000.0f) || !(sum <= 0x1p110f);
-                    if (pass == 0 && __any_sync(kFull, lift)) {
-                        const float2 up = raise<D, QP>(sm, tm, tm + C::kColO, j, st, qs, R, lift, visible, context);
-                        R = up.x;
-                        l *= up.y;
-                        pass = 1;
-                        continue;
+                    for (int j = 0, pass = 0; j < kN / kC;) {
+                        const int32_t visible = partly ? min(max(lim - row0 - kC * j, 0), kC) : kC;
+                        uint32_t now[kC], pk[kWords<QP>];
+                        tmem_ld32(tm + kC * j, now);
+                        const float svt = sm.sv_top[st][j];
+                        tmem_wait_ld();
+                        float sum, most = 0.0f;
+                        if (partly) sum = weights<QP, true>(sm, now, j, st, qs, R, visible, pk, &most);
+                        else sum = weights<QP, false>(sm, now, j, st, qs, R, kC, pk, &most);
+                        // one half: the sum and the scales bound the weights (references leave the room, a false
+                        // alarm only costs time); two: the weights themselves
+                        if (QP == 1) most = sum * svt;
+                        const bool lift = (R == kNone && visible > 0) || !(most <= 60000.0f) || !(sum <= 0x1p110f);
+                        if (pass == 0 && __any_sync(kFull, lift)) {
+                            const float2 up = raise<D, QP>(sm, tm, tm + C::kColO, j, st, qs, R, lift, visible, context);
+                            R = up.x;
+                            l *= up.y;
+                            pass = 1;
+                            continue;
+                        }
+                        l += sum;
+                        store_weights(tm + weight_col<QP>(j * (kC / 16)), pk);
+                        pass = 0;
+                        ++j;
                     }
-                    l += sum;
-                    store_weights(tm + weight_col<QP>(j * (kC / 16)), pk);
-                    pass = 0;
-                    ++j;
-                }
-                tmem_wait_st();
-                tc_before();
+                    tmem_wait_st();
+                    tc_before();
                 }
                 // this step's values and the next keys, there for long: waited for before the others are
                 if (tid == 0 && ok) {
