@@ -11,8 +11,10 @@
 // into the second product from tensor memory, over the scores they came from, instead of
 // through shared memory.  512 bf16 tokens of 32 heads (8 of keys) of 128 on 8704 rows: 133 us, 533
 // TFLOP/s; tensor pipe 24% busy, shared memory 43%, issue slots 33%.
-// Slower: scores of 64 rows in two buffers (157 us); the next scores loaded ahead, with more
-// registers for the softmax and fewer for the converters (154).
+// A step takes one CTA 6,600 cycles: 3,400 the softmax, 2,400 the products (issuing, waiting for the
+// weights' product and for the scores), 700 until values and next keys are there.  Slower: scores of
+// 64 rows in two buffers (157 us); the next scores loaded ahead, with more registers for the softmax and
+// fewer for the converters (154); eight softmax warps, half of the rows each (215: 80 registers).
 //   * warps 0-3: softmax, a vector a thread, so maxima and sums need no exchange; 32 scores at
 //     a time are loaded, turned into weights and stored over the first half of the scores'
 //     place (f32 queries: two f16 halves, over the whole place);
