@@ -387,7 +387,8 @@ kvq_status kv_attn_prefill(kvq_format fmt, const kvq_mla_layout* layout,
  * KVQ_TQ4 (pools with grouped query heads: below).  block_table is int32 [n_seq][table_stride].  A sequence appears once
  * in a batch.  Attention only reads, so sequences may list the same page there (a
  * shared prefix); the stack of free pages knows no counts, so such a page is given
- * back by one of them alone, and no new row goes into it.  A workspace serves one
+ * back by one of them alone, and no new row goes into it (kv_pages_fork, below, shares
+ * pages among all of a batch's sequences and gives them back).  A workspace serves one
  * call at a time. */
 
 /* Bytes of workspace kv_pages_reserve and kv_pages_trim need: the error word
@@ -595,7 +596,8 @@ kvq_status kv_gqa_attn_paged(const void* q, kvq_dtype q_dtype, int64_t n_tokens,
  * and the next step's kv_pages_reserve appends as usual.  The tables serve any pool
  * (latent rows or grouped heads). */
 
-/* Bytes of workspace kv_beam_select needs; 0 for what it would refuse. */
+/* Bytes of workspace kv_beam_select needs, for n_seq requests or fewer; 0 for what it would
+ * refuse. */
 size_t kv_beam_workspace_size(int32_t n_seq, int32_t n_beams, int64_t vocab, int32_t keep);
 
 /* For every request the `keep` best pairs of a beam b and a token v by
@@ -610,14 +612,15 @@ size_t kv_beam_workspace_size(int32_t n_seq, int32_t n_beams, int64_t vocab, int
  *   parents     [n_seq][keep] int32: s * n_beams + b
  *   tokens      [n_seq][keep] int32
  * Where a request has fewer continuations the rest are -inf, -1, -1.  n_beams 1 .. 32,
- * keep 1 .. 64, vocab 1 .. 2^31 - 1.  The workspace starts zeroed; calls leave it ready for
- * the next.  No output may overlap an input. */
+ * keep 1 .. 64, vocab 1 .. 2^31 - 1, n_seq up to 65535.  The workspace starts zeroed; calls leave
+ * it ready for the next, of whatever sizes it is large enough for.  No output may overlap an input. */
 kvq_status kv_beam_select(const void* logits, kvq_dtype dtype, int64_t row_stride, int32_t n_seq, int32_t n_beams,
                           int64_t vocab, const float* scores, int32_t keep, float* out_scores, int32_t* parents,
                           int32_t* tokens, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace kv_pages_fork needs: the error word, a mark per page (zero
- * before the first call; each call leaves them so) and the new table. */
+ * before the first call; each call leaves them so) and the new table.  It serves batches of
+ * any size up to its own over one pool; for another n_pages it has to be zeroed again. */
 size_t kv_pages_fork_workspace_size(int32_t n_seq, int32_t table_stride, int32_t n_pages);
 
 /* Sequence i continues the rows of sequence parents[i]; -1 ends it (length 0).
@@ -651,7 +654,7 @@ typedef struct kvq_pool {
 /* Copies page copies[i][0] to page copies[i][1] in every pool, for i < n; entries with a
  * negative page are skipped, pages outside [0, n_pages) skipped and KVQ_ERR_ARG set in
  * err_word (NULL or a device int32 error word).  `pools` is read on the host, any number of
- * them.  No page may be both copied from and copied to.  16-byte aligned pages move fastest. */
+ * them.  No page may be both copied from and copied to, or copied to twice.  16-byte aligned pages move fastest. */
 kvq_status kv_pages_copy(int32_t n, const int32_t* copies, int32_t n_pages, int32_t n_pools, const kvq_pool* pools,
                          int32_t* err_word, void* stream);
 
@@ -694,7 +697,7 @@ int32_t kvq_read_device_error(void* workspace, int32_t clear, void* stream);
 int64_t kvq_read_exact_rescales(void* workspace, int32_t clear, void* stream);
 
 /* Testing hook for the timeout path of the tensor-core attention kernels (the
- * KV8, KV8 f32-query and TQ4 decode/prefill kernels, and the paged kernel).  Process-wide, not
+ * KV8, KV8 f32-query and TQ4 decode/prefill kernels, and the paged and grouped ones).  Process-wide, not
  * thread-safe, off by default.  With polls > 0, every later launch of those
  * kernels first waits, for at most `polls` polls, on a barrier that nothing
  * arrives on, and its other tile-loop waits give up after `polls` polls too:

@@ -640,7 +640,7 @@ kvq_status kv_gqa_attn_paged(const void* q, kvq_dtype q_dtype, int64_t n_tokens,
 
 static kvq_status check_beam(int32_t n_seq, int32_t n_beams, int64_t vocab, int32_t keep) {
     if (n_seq < 0 || n_beams < 1 || vocab < 1 || keep < 1) return KVQ_ERR_ARG;
-    if (n_beams > 32 || keep > 64 || vocab > 0x7fffffff || n_seq > 65535) return KVQ_ERR_UNSUPPORTED;
+    if (n_beams > 32 || keep > 64 || vocab > 0x7fffffff || n_seq > kBeamMaxSeq) return KVQ_ERR_UNSUPPORTED;
     return KVQ_OK;
 }
 

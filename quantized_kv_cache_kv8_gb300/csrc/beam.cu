@@ -570,21 +570,24 @@ __global__ void __launch_bounds__(kNT, 4) beam_select_kernel(const __grid_consta
 }
 
 // Slices of a row: 3 CTAs a SM at least, slices of at least 16 KB, lists within a request's limits.
+constexpr int64_t kCtas = 152 * 3;
+int64_t most_splits(int32_t n_beams, int64_t vocab, int32_t keep, int size) {
+    const int64_t lists = std::min(kMaxLists / n_beams, kMaxCand / (n_beams * keep));
+    return std::max<int64_t>(1, std::min(vocab * size / 16384, lists));
+}
 int splits_for(int64_t rows, int32_t n_beams, int64_t vocab, int32_t keep, int size) {
-    int64_t s = (152 * 3 + rows - 1) / std::max<int64_t>(1, rows);
-    s = std::min<int64_t>(s, vocab * size / 16384);
-    s = std::min<int64_t>(s, std::min(kMaxLists / n_beams, kMaxCand / (n_beams * keep)));
-    return (int)std::max<int64_t>(1, s);
+    return (int)std::min((kCtas + rows - 1) / std::max<int64_t>(1, rows), most_splits(n_beams, vocab, keep, size));
 }
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-// Sized for the slices of either type (f32 rows have the most).
+// Tickets are zero between calls, so they have a place of their own whatever the sizes of the call.  Sized
+// for either type (f32 rows have the most slices) and for fewer requests, of more slices each.
 size_t beam_workspace_bytes(int32_t n_seq, int32_t n_beams, int64_t vocab, int32_t keep) {
     const int64_t rows = (int64_t)n_seq * n_beams;
-    const size_t lists = (size_t)rows * splits_for(rows, n_beams, vocab, keep, 4);
-    return kWsHeader + round_up((size_t)n_seq * 4) + lists * (sizeof(float2) + 8 * (size_t)keep + 4);
+    const int64_t lists = std::max(rows, std::min(rows + kCtas - 1, rows * most_splits(n_beams, vocab, keep, 4)));
+    return kWsHeader + round_up(sizeof(uint32_t) * kBeamMaxSeq) + (size_t)lists * (sizeof(float2) + 8 * (size_t)keep + 4);
 }
 
 cudaError_t launch_beam_select(const void* logits, kvq_dtype dt, int64_t row_stride, int32_t n_seq, int32_t n_beams,
@@ -607,7 +610,7 @@ cudaError_t launch_beam_select(const void* logits, kvq_dtype dt, int64_t row_str
     p.tokens = tokens;
     char* ws = static_cast<char*>(workspace) + kWsHeader;
     p.tickets = reinterpret_cast<uint32_t*>(ws);
-    ws += round_up((size_t)n_seq * 4);
+    ws += round_up(sizeof(uint32_t) * kBeamMaxSeq);
     p.sums = reinterpret_cast<float2*>(ws);
     p.keys = reinterpret_cast<uint64_t*>(p.sums + rows * p.splits);
     p.counts = reinterpret_cast<int32_t*>(p.keys + rows * p.splits * keep);

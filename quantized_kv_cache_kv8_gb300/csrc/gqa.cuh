@@ -52,6 +52,7 @@ struct GqaAppendCall {
 };
 cudaError_t launch_gqa_append(const GqaAppendCall& c, cudaStream_t stream);
 
+constexpr int kBeamMaxSeq = 65535;   // requests of a selection
 size_t beam_workspace_bytes(int32_t n_seq, int32_t n_beams, int64_t vocab, int32_t keep);
 cudaError_t launch_beam_select(const void* logits, kvq_dtype dt, int64_t row_stride, int32_t n_seq, int32_t n_beams,
                                int64_t vocab, const float* scores, int32_t keep, float* out_scores, int32_t* parents,

@@ -16,6 +16,9 @@ def kvq():
     return kvq_module()
 
 
+DTYPES = [torch.bfloat16, torch.float32]
+
+
 def run_select(kvq, logits, scores, keep, ws=None):
     n, b, v = logits.shape
     ws = torch.zeros(kvq.kv_beam_workspace_size(n, b, v, keep), dtype=torch.uint8, device="cuda") if ws is None else ws
@@ -136,6 +139,14 @@ def test_the_workspace_is_left_ready_and_graphs_replay(kvq):
         x.copy_(x.roll(k, -1))
         graph.replay()
         assert all(torch.equal(i, j) for i, j in zip((o, p, t), run_select(kvq, x, s, 8)))
+
+
+def test_one_workspace_for_calls_of_different_sizes(kvq):
+    sizes = [(40, 4, 30000, 8), (2, 4, 30000, 8), (40, 4, 100, 8), (1, 4, 30000, 8), (33, 2, 9000, 3)]
+    ws = torch.zeros(kvq.kv_beam_workspace_size(*sizes[0]), dtype=torch.uint8, device="cuda")
+    for i, (n, b, v, keep) in enumerate(sizes + sizes):
+        x, s = random_logits(n, b, v, DTYPES[i % 2], seed=i)
+        assert all(torch.equal(i, j) for i, j in zip(run_select(kvq, x, s, keep, ws), run_select(kvq, x, s, keep)))
 
 
 # -- page sharing ------------------------------------------------------------------

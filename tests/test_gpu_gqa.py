@@ -187,6 +187,91 @@ def test_many_vectors_long_sums(kvq):
     assert kvq.read_device_error(ws) == 0
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("most", [3, 60])
+def test_many_sequences(kvq, causal, most):
+    """More sequences than one warp deals out; `most` tokens each: with few and with many vectors."""
+    g = torch.Generator().manual_seed(most)
+    new = torch.randint(0, most + 1, (700,), generator=g).tolist()
+    lens = [max(0, int(t) + (n if causal else 0) - 2) for t, n in zip(torch.randint(0, 300, (700,), generator=g), new)]
+    pool = Pool(2, 64, 32, lens, seed=most)
+    for dtype in DT:
+        q = queries(sum(new), 6, 64, dtype)
+        out, ws = attend(kvq, pool, q, lens, new, causal)
+        check(out, q, pool, lens, new, 0.125, causal, f"{dtype}")
+        assert kvq.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("heads", [128, 200, 300])
+def test_groups_wider_than_a_tile(kvq, heads):
+    """A token's vectors fill a tile, or more than one."""
+    lens, new = [700, 33, 5], [3, 1, 7]
+    pool = Pool(1, 64, 16, lens, seed=heads)
+    for dtype in DT:
+        q = queries(11, heads, 64, dtype)
+        out, ws = attend(kvq, pool, q, lens, new)
+        check(out, q, pool, lens, new, 0.125, True, f"{dtype}")
+        assert kvq.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("new", [1, 70])
+def test_scales_of_scores_and_queries_that_are_no_numbers(kvq, dtype, new):
+    pool = Pool(2, 128, 32, [500])
+    q = queries(new, 8, 128, dtype)
+    for sm in (0.0, -0.3):
+        out, _ = attend(kvq, pool, q, [500], [new], sm=sm)
+        check(out, q, pool, [500], [new], sm, True, f"sm {sm}")
+    ref = attention(q, pool, [500], [new], 0.1, True)
+    mass = attention(q, pool, [500], [new], 0.1, True, absolute=True) if new > 1 and dtype == torch.bfloat16 else None
+    bad = q.clone()
+    bad[0, 1, 5], bad[-1, 7, 100] = math.nan, math.inf
+    out, _ = attend(kvq, pool, bad, [500], [new], sm=0.1)
+    rest = torch.ones(new, 8, dtype=torch.bool, device="cuda")
+    rest[0, 1] = rest[-1, 7] = False
+    assert bool(torch.isnan(out[~rest]).any(-1).all())
+    close(out[rest], ref[rest], "the other vectors", None if mass is None else mass[rest])
+
+
+def test_tensors_and_calls_on_a_stream(kvq):
+    """The stream that is given takes the call, whichever is current."""
+    pool = Pool(2, 128, 32, [900])
+    q = queries(40, 8, 128, torch.bfloat16)
+    st = torch.cuda.Stream()
+    turned = torch.zeros_like(q)
+    rope = kvq.rope_layout([100.0 ** (-i / 64) for i in range(64)])
+    pos = torch.arange(40, device="cuda")
+    ref = torch.zeros_like(q)
+    kvq.kv_gqa_append(rope, None, None, pos, None, q, ref, None, None, None)
+    want, _ = attend(kvq, pool, ref, [900], [40])
+    ws, out, lens, cu = workspace(kvq, 8, 2, 128, True), torch.zeros_like(q), torch.tensor([900], device="cuda"), offsets([40])
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(20_000_000)
+    kvq.kv_gqa_append(rope, None, None, pos, None, q, turned, None, None, None, stream=st)
+    kvq.kv_gqa_attn_paged(turned, cu, pool.k, pool.v, pool.scales, pool.table, lens, out, ws, 1 / math.sqrt(128), stream=st)
+    assert not st.query()
+    st.synchronize()
+    assert torch.equal(turned, ref) and torch.equal(out, want)
+
+
+def test_more_than_2_to_31_elements_of_queries(kvq):
+    n, heads, dim = 70001, 128, 256
+    pool = Pool(4, dim, 16, [20], seed=4)
+    q = torch.zeros(n, heads, dim, dtype=torch.bfloat16, device="cuda")
+    q[-9:] = queries(9, heads, dim, torch.bfloat16)
+    out, ws = attend(kvq, pool, q, [20], [n], causal=False)
+    ref, mass = (attention(q[-9:], pool, [20], [9], 1 / 16, False, absolute=a) for a in (False, True))
+    close(out[-9:], ref, "the last", mass)
+    assert torch.equal(out[0], out[-10]) and kvq.read_device_error(ws) == 0
+    last = q[-9:].clone()
+    rope, pos = kvq.rope_layout([0.5 ** i for i in range(64)]), torch.arange(n, device="cuda")
+    kvq.kv_gqa_append(rope, None, None, pos, None, q, q, None, None, None)
+    few = torch.empty_like(last)
+    kvq.kv_gqa_append(rope, None, None, pos[-9:].contiguous(), None, last, few, None, None, None)
+    assert torch.equal(q[-9:], few) and not bool(q[:-9].any())
+
+
 def test_wait_that_runs_out(kvq):
     pool = Pool(2, 128, 64, [300])
     q = queries(64, 4, 128, torch.bfloat16)

@@ -64,7 +64,11 @@ def test_beam_refusals(kvq):
     assert select(beams=0) == 1 and select(beams=33) == 5 and select(keep=0) == 1 and select(keep=65) == 5
     assert select(vocab=0) == 1 and select(stride=99) == 1 and select(dt=2) == 1 and select(x=None) == 1
     assert select(x=C.c_void_p(4097)) == 1 and select(ws=None) == 3 and select(ws_bytes=100) == 3 and select(n=0) == 0
-    assert kvq.kv_beam_workspace_size(2, 40, 100, 8) == 0
+    assert kvq.kv_beam_workspace_size(2, 40, 100, 8) == 0 and select(n=65536) == 5
+    for v in (100, 30000, 200000):   # fewer requests have more slices each, and no larger a workspace
+        for b in (1, 4, 32):
+            sizes = [kvq.kv_beam_workspace_size(n, b, v, 8) for n in range(1, 600)]
+            assert sizes == sorted(sizes)
 
 
 def test_fork_and_copy_refusals(kvq):
