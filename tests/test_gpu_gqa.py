@@ -521,3 +521,76 @@ def test_append_reports_what_is_no_number_and_what_is_no_slot(kvq):
     err.zero_()
     kvq.kv_gqa_append(None, v, v, None, torch.tensor([16, -1, 99], device="cuda"), None, None, pool.k, pool.v, pool.scales, err)
     assert int(err) == 1
+
+
+# -- the binding -------------------------------------------------------------------
+
+def test_refusals_of_the_binding(kvq):
+    pool = Pool(2, 64, 16, [20, 30])
+    q = queries(2, 4, 64, torch.bfloat16)
+    ws = workspace(kvq, 4, 2, 64, True)
+    good = dict(q=q, cu_q=offsets([1, 1]), k_codes=pool.k, v_codes=pool.v, scales=pool.scales, block_table=pool.table,
+                kv_lens=pool.lens, out=torch.zeros_like(q), workspace=ws, sm_scale=0.1)
+    kvq.kv_gqa_attn_paged(**good)
+    for bad in (dict(q=q.half()), dict(q=q.cpu()), dict(q=q[:, :, :32]), dict(q=q[:, :3]), dict(q=None), dict(out=good["out"].float()),
+                dict(cu_q=good["cu_q"].int()), dict(cu_q=good["cu_q"][:2]), dict(k_codes=pool.k.int()), dict(v_codes=pool.v[1:]),
+                dict(scales=pool.scales[..., :1]), dict(block_table=pool.table.long()), dict(block_table=pool.table[:1]),
+                dict(kv_lens=pool.lens.int()), dict(kv_lens=pool.lens.cpu()), dict(workspace=ws[:1024]), dict(workspace=ws.int()),
+                dict(sm_scale=math.nan), dict(sm_scale="x"), dict(q=q.transpose(0, 1).contiguous().transpose(0, 1))):
+        with pytest.raises((ValueError, TypeError, kvq.KvqError)):
+            kvq.kv_gqa_attn_paged(**{**good, **bad})
+    rope, pos, slots = kvq.rope_layout([1.0] * 32), torch.arange(2, device="cuda"), torch.arange(2, device="cuda")
+    k = queries(2, 2, 64, torch.bfloat16)
+    good = dict(rope=rope, k_new=k, v_new=k.clone(), positions=pos, slot_map=slots, q_in=q, q_out=torch.zeros_like(q),
+                k_codes=pool.k, v_codes=pool.v, scales=pool.scales)
+    kvq.kv_gqa_append(**good)
+    for bad in (dict(v_new=None), dict(k_new=None, v_new=None, q_in=None), dict(k_new=k.float()), dict(k_new=k[:, :1]), dict(k_new=k[:1]),
+                dict(q_out=None), dict(q_out=good["q_out"].float()), dict(q_out=q[:1]), dict(positions=None), dict(positions=pos.int()),
+                dict(positions=pos[:1]), dict(slot_map=None), dict(slot_map=slots[:1]), dict(slot_map=slots.int()),
+                dict(rope=kvq.rope_layout([1.0] * 33)), dict(rope=kvq.mla_layout()), dict(k_codes=None), dict(q_in=q[:, :3]),
+                dict(err_word=torch.zeros(1, device="cuda")), dict(q_in=q.permute(0, 2, 1))):
+        with pytest.raises((ValueError, TypeError, kvq.KvqError)):
+            kvq.kv_gqa_append(**{**good, **bad})
+    x, s = torch.zeros(2, 3, 100, device="cuda"), torch.zeros(2, 3, device="cuda")
+    o, i = torch.zeros(2, 4, device="cuda"), torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    good = dict(logits=x, scores=s, out_scores=o, parents=i, tokens=i.clone(),
+                workspace=torch.zeros(kvq.kv_beam_workspace_size(2, 3, 100, 4), dtype=torch.uint8, device="cuda"))
+    kvq.kv_beam_select(**good)
+    for bad in (dict(logits=x.half()), dict(logits=x[:, :, ::2]), dict(logits=x[0]), dict(logits=x.expand(2, 3, 100)[:, :1].expand(2, 3, 100)),
+                dict(logits=torch.zeros(2, 5, 100, device="cuda")[:, :3]), dict(scores=s[:1]), dict(scores=s.double()), dict(parents=i.long()),
+                dict(tokens=i[:, :3]), dict(out_scores=o.cpu()), dict(workspace=good["workspace"][:4096])):
+        with pytest.raises((ValueError, TypeError, kvq.KvqError)):
+            kvq.kv_beam_select(**{**good, **bad})
+    free, n_free = torch.arange(pool.n_pages, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    good = dict(parents=torch.arange(2, dtype=torch.int32, device="cuda"), kv_lens=pool.lens, block_table=pool.table, free_pages=free,
+                n_free=n_free, page_rows=16, copies=torch.zeros(2, 2, dtype=torch.int32, device="cuda"),
+                workspace=torch.zeros(kvq.kv_pages_fork_workspace_size(2, pool.width, pool.n_pages), dtype=torch.uint8, device="cuda"))
+    kvq.kv_pages_fork(**good)
+    for bad in (dict(parents=good["parents"].long()), dict(parents=good["parents"][:1]), dict(kv_lens=pool.lens.int()),
+                dict(block_table=pool.table[:, :1]), dict(n_free=free), dict(page_rows=24), dict(page_rows=0),
+                dict(copies=good["copies"].view(-1)), dict(workspace=good["workspace"][:256])):
+        with pytest.raises((ValueError, TypeError, kvq.KvqError)):
+            kvq.kv_pages_fork(**{**good, **bad})
+    copies = torch.full((2, 2), -1, dtype=torch.int32, device="cuda")
+    kvq.kv_pages_copy(copies, [pool.k, pool.v, pool.scales])
+    for bad in (dict(copies=copies.long()), dict(copies=copies[:, :1]), dict(pools=[pool.k, pool.v[1:]]), dict(pools=[pool.k.cpu()]),
+                dict(pools=[pool.k.transpose(1, 2)]), dict(pools=7), dict(pools=[None])):
+        with pytest.raises((ValueError, TypeError, kvq.KvqError)):
+            kvq.kv_pages_copy(**{**dict(copies=copies, pools=[pool.k]), **bad})
+
+
+def test_calls_side_by_side(kvq):
+    """Two streams, a workspace each."""
+    jobs = []
+    for i, (new, dtype) in enumerate(((1, torch.bfloat16), (300, torch.bfloat16), (90, torch.float32))):
+        pool = Pool(4, 128, 64, [6000 + i], seed=i)
+        q = queries(new, 16, 128, dtype, seed=i)
+        jobs.append((pool, q, offsets([new]), torch.zeros_like(q), workspace(kvq, 16, 4, 128, dtype == torch.bfloat16), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for pool, q, cu, out, ws, st in jobs:
+            kvq.kv_gqa_attn_paged(q, cu, pool.k, pool.v, pool.scales, pool.table, pool.lens, out, ws, 0.1, stream=st)
+    torch.cuda.synchronize()
+    for i, (pool, q, cu, out, ws, st) in enumerate(jobs):
+        check(out, q, pool, [6000 + i], [len(q)], 0.1, True, f"job {i}")
+        assert kvq.read_device_error(ws) == 0
