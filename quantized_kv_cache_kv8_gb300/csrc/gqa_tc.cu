@@ -9,12 +9,12 @@
 // one tile can't overlap with itself: tensor memory holds two tiles' scores and contexts and no more.
 // So two CTAs share an SM, one's softmax beside the other's products, and the weights go
 // into the second product from tensor memory, over the scores they came from, instead of
-// through shared memory.  512 bf16 tokens of 32 heads (8 of keys) of 128 on 8704 rows: 133 us, 533
+// through shared memory.  512 bf16 tokens of 32 heads (8 of keys) of 128 on 8704 rows: 127 us, 555
 // TFLOP/s; tensor pipe 24% busy, shared memory 43%, issue slots 33%.
-// A step takes one CTA 6,600 cycles: 3,400 the softmax, 2,400 the products (issuing, waiting for the
-// weights' product and for the scores), 700 until values and next keys are there.  Slower: scores of
-// 64 rows in two buffers (157 us); the next scores loaded ahead, with more registers for the softmax and
-// fewer for the converters (154); eight softmax warps, half of the rows each (215: 80 registers).
+// A step takes one CTA some 6,200 cycles: 3,200 the softmax, 2,400 the products (issuing, waiting for the
+// weights' product and for the scores).  Slower (of 133 us then): scores of 64 rows in two buffers (157);
+// the next scores loaded ahead, with more registers for the softmax and fewer for the converters
+// (154); eight softmax warps, half of the rows each (215: 80 registers).
 //   * warps 0-3: softmax, a vector a thread, so maxima and sums need no exchange; 32 scores at
 //     a time are loaded, turned into weights and stored over the first half of the scores'
 //     place (f32 queries: two f16 halves, over the whole place);
@@ -134,10 +134,28 @@ __device__ __forceinline__ void load_weights(uint32_t t, uint32_t (&v)[32]) { tm
 __device__ __forceinline__ void store_weights(uint32_t t, const uint32_t (&v)[16]) { tmem_st16(t, v); }
 __device__ __forceinline__ void store_weights(uint32_t t, const uint32_t (&v)[32]) { tmem_st32(t, v); }
 
-// The issuing lane's waits: polls without suspending (a suspended lane woke some 800 cycles
-// late, with every product of the CTA behind it).
+// The softmax's waits, for a phase of each of two barriers at once: polls without suspending (a suspended
+// lane woke some 800 cycles late, with every product of the CTA behind it), and looks at the abort
+// flag only when the first fails: with the converters' stores in the queue a read of shared memory
+// takes some 150 cycles.
+__device__ __forceinline__ bool mbar_spin(uint64_t* x, uint32_t px, uint64_t* y, uint32_t py, volatile int* abort_flag,
+                                          long long limit) {
+    const uint32_t a = smem_u32(x), b = smem_u32(y);
+    for (long long i = 0; i < 16 * limit; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p, q;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            " mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n and.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(a), "r"(px), "r"(b), "r"(py)
+            : "memory");
+        if (ok) return true;
+        if ((i & 63) == 0 && *abort_flag) return false;
+    }
+    *abort_flag = 1;
+    return false;
+}
 __device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
-    if (*abort_flag) return false;
     const uint32_t a = smem_u32(bar);
     for (long long i = 0; i < 16 * limit; ++i) {
         uint32_t ok;
@@ -147,7 +165,7 @@ __device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volati
             : "r"(a), "r"(parity)
             : "memory");
         if (ok) return true;
-        if ((i & 63) == 63 && *abort_flag) return false;
+        if ((i & 63) == 0 && *abort_flag) return false;
     }
     *abort_flag = 1;
     return false;
@@ -502,7 +520,7 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                 const int st = (int)ph;
                 // (the scales too: their writers arrived on kBarK, which the issuing lane waited for.  Not
                 // waited for here: the next keys' arrival could be the phase after, seen as not yet)
-                ok = __all_sync(kFull, mbar_wait(&sm.bars[kBarS], ph, abort_flag, p.wait_limit));
+                ok = __all_sync(kFull, mbar_spin(&sm.bars[kBarS], ph, abort_flag, p.wait_limit));
                 if (ok) {
                     tc_after();
                     if (s > 0 && s % C::kFlush == 0) flush(s == C::kFlush);
@@ -541,12 +559,12 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                 }
                 // this step's values and the next keys, there for long: waited for before the others are
                 if (tid == 0 && ok) {
-                    ok = mbar_spin(&sm.bars[kBarV], ph, abort_flag, p.wait_limit) &&
-                         (s + 1 == n_steps || mbar_spin(&sm.bars[kBarK], ph ^ 1u, abort_flag, p.wait_limit));
+                    const bool next = s + 1 < n_steps;   // else the values' again
+                    ok = mbar_spin(&sm.bars[kBarV], ph, &sm.bars[next ? kBarK : kBarV], next ? ph ^ 1u : ph, abort_flag, p.wait_limit);
                 }
                 __syncwarp();
                 // every softmax warp comes here at every step, and all leave together
-                ok = !worker_any<kSoft>(!ok || *abort_flag != 0);
+                ok = !worker_any<kSoft>(!ok);
                 if (!ok) break;
                 if (tid == 0) {
                     issue_context(s);
