@@ -187,6 +187,30 @@ def test_many_vectors_long_sums(kvq):
     assert kvq.read_device_error(ws) == 0
 
 
+@pytest.mark.parametrize("binades", [12, 20, 26])
+def test_many_vectors_small_weights_add_up(kvq, binades):
+    """131,072 rows that far below one row, by score and by scale, in tiles of 128 vectors."""
+    n = 131073
+    pool = Pool(1, 64, 256, [n])
+    one = torch.zeros(1, 64)
+    one[0, 0] = 1.0
+    codes, _ = encode_rows(one)
+    pool.k[:] = codes.cuda()[0]
+    pool.v[:] = 0
+    pool.v[..., 1] = codes.cuda()[0, 0]
+    pg = int(pool.table[0, 0])
+    for by_scale in (False, True):
+        pool.scales[..., 0] = 0.0 if by_scale else -binades * math.log(2) / 448
+        pool.scales[..., 1] = 2.0 ** -binades / 448 if by_scale else 1 / 448
+        pool.scales[pg, 0, 0, 0] = 0.0
+        pool.scales[pg, 0, 0, 1] = 1 / 448
+        for dtype in DT:
+            q = torch.zeros(64, 1, 64, dtype=dtype, device="cuda")
+            q[..., 0] = 1.0
+            out, _ = attend(kvq, pool, q, [n], [64], causal=False, sm=1.0)
+            check(out, q, pool, [n], [64], 1.0, False, f"{dtype} by_scale={by_scale}")
+
+
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("most", [3, 60])
 def test_many_sequences(kvq, causal, most):
