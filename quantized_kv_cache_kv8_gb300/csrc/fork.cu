@@ -19,7 +19,7 @@
 // What bounds it: the latency of these dependent passes; the tables of a batch are a few
 // hundred KB.  One cluster of 8 CTAs does it in one launch, with a cluster barrier
 // between passes; its 256 warps take pieces of 128 pages of a sequence in turn.  512 sequences of 53
-// pages on average take 23 us, 64 of 36 14 (by a CTA that takes one sequence after another: 79 for the
+// pages on average take 22 us, 64 of 36 12 (by a CTA that takes one sequence after another: 79 for the
 // 512).
 #include "gqa.cuh"
 
@@ -328,7 +328,8 @@ struct CopyParams {
 
 // Unit: the type that pages are moved in.  A page's units in all pools are numbered through; a
 // CTA moves 1024 of them, so small arrays (scales) share one.  What bounds it: memory; 8 layers'
-// pages of 16 rows, 2 heads of 256, for about 250 children: 15 us, 4.5 TB/s.
+// pages of 16 rows, 2 heads of 256, for 270 of 512 children: 15 us, 4.8 TB/s (as much with the
+// copies picked out first and taken in turn by 608 CTAs).
 template <typename Unit>
 __global__ void __launch_bounds__(kCopyNT) pages_copy_kernel(const __grid_constant__ CopyParams p) {
     launch_dependents();
