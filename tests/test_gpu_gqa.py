@@ -449,6 +449,64 @@ def test_captured_on_another_stream_and_replayed(kvq):
             close(out, ref)
 
 
+def test_a_captured_chunk_with_other_lengths(kvq):
+    """Many vectors: offsets and lengths may change between replays, rows behind the last sequence stay."""
+    pool = Pool(2, 128, 32, [900, 1200, 500], seed=2)
+    q = queries(220, 8, 128, torch.bfloat16)
+    cu, lens = offsets([100, 20, 100]), torch.tensor([900, 1200, 500], device="cuda")
+    ws, out = workspace(kvq, 8, 2, 128, True), torch.zeros_like(q)
+    graph, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=st):
+        kvq.kv_gqa_attn_paged(q, cu, pool.k, pool.v, pool.scales, pool.table, lens, out, ws, 0.1)
+    for new, rows in (([100, 20, 100], [900, 1200, 500]), ([1, 0, 200], [20, 0, 400]), ([220, 0, 0], [300, 5, 5]), ([0, 0, 0], [1, 1, 1])):
+        cu.copy_(offsets(new))
+        lens.copy_(torch.tensor(rows, device="cuda"))
+        out.fill_(7.0)
+        graph.replay()
+        n = sum(new)
+        mass = attention(q[:n], pool, rows, new, 0.1, True, absolute=True)
+        close(out[:n], attention(q[:n], pool, rows, new, 0.1, True), f"{new}", mass)
+        assert bool((out[n:] == 7.0).all()) and kvq.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_entries_behind_a_sequence_are_not_read(kvq, new):
+    lens = [33, 0, 500, 16]
+    pool = Pool(2, 64, 16, lens, seed=3)
+    for b, t in enumerate(lens):
+        pool.table[b, -(-t // 16):] = -7
+    q = queries(4 * new, 4, 64, torch.bfloat16)
+    for causal in (True, False):
+        out, ws = attend(kvq, pool, q, lens, [new] * 4, causal)
+        check(out, q, pool, lens, [new] * 4, 0.125, causal)
+        assert kvq.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_a_pool_without_pages(kvq, new):
+    q = queries(2 * new, 4, 64, torch.bfloat16)
+    codes = torch.empty(0, 2, 16, 64, dtype=torch.uint8, device="cuda")
+    for width in (0, 3):
+        ws, out = workspace(kvq, 4, 2, 64, True), torch.full_like(q, 7.0)
+        kvq.kv_gqa_attn_paged(q, offsets([new, new]), codes, codes, torch.empty(0, 2, 16, 2, device="cuda"),
+                              torch.zeros(2, width, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int64, device="cuda"),
+                              out, ws, 0.1)
+        assert not bool(out.any()) and kvq.read_device_error(ws) == 0
+
+
+def test_timed_calls(kvq):
+    pool = Pool(2, 128, 32, [900])
+    kvq.timing_enable(4)
+    try:
+        for new in (1, 100):
+            attend(kvq, pool, queries(new, 8, 128, torch.bfloat16), [900], [new])
+        partial, merge, calls = kvq.timing_read()
+        assert calls == 2 and 0 < partial < 100 and 0 < merge < 100
+    finally:
+        kvq.timing_enable(0)
+
+
 # -- append ----------------------------------------------------------------------
 
 def turn(x, positions, inv, axis, adjacent):
