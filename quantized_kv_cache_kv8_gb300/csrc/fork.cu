@@ -19,8 +19,8 @@
 // What bounds it: the latency of these dependent passes; the tables of a batch are a few
 // hundred KB.  One cluster of 8 CTAs does it in one launch, with a cluster barrier
 // between passes; its 256 warps take pieces of 128 pages of a sequence in turn.  512 sequences of 53
-// pages on average take 22 us, 64 of 36 12 (by a CTA that takes one sequence after another: 79 for the
-// 512).
+// pages on average take 17.5 us, 64 of 36 10.9 (with each piece's sequence found by bisection 20.1 and
+// 11.4; by a CTA that takes one sequence after another 79 for the 512).
 #include "gqa.cuh"
 
 #include <algorithm>
@@ -58,6 +58,9 @@ struct ForkShared {
     int32_t pages[kMaxSeq];       // pages of it
     int32_t piece0[kMaxSeq + 1];  // pieces of the sequences before it
     int32_t rank[kMaxSeq];        // of sequence i: copies before it, or -1
+    int32_t parent[kMaxSeq];
+    int2 gone[kNT];               // of the first kNT pieces: owned pages, of the pieces before
+    uint16_t of[kNT];             // and their sequences
     int64_t part[kWarps];
     int bad;
     int32_t flag;                 // this CTA met a page outside the pool
@@ -100,7 +103,7 @@ __device__ __forceinline__ int find_last(const int32_t* off, int n, int32_t x) {
 struct Piece {
     int s, w0, pages;
     __device__ __forceinline__ Piece(const ForkShared& sm, int n, int32_t k)
-        : s(find_last(sm.piece0, n, k)), w0((k - sm.piece0[s]) * kPiece), pages(sm.pages[s]) {}
+        : s(k < kNT ? sm.of[k] : find_last(sm.piece0, n, k)), w0((k - sm.piece0[s]) * kPiece), pages(sm.pages[s]) {}
     __device__ __forceinline__ void load(const int32_t* table, int32_t stride, int lane, int32_t (&id)[kPer]) const {
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
@@ -129,6 +132,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kNT, 1) pages
     __syncthreads();
     int32_t parent[kMaxSeq / kNT];
     bool whole[kMaxSeq / kNT];
+    int64_t len[kMaxSeq / kNT];   // of the parents: the new lengths
 #pragma unroll
     for (int k = 0; k < kMaxSeq / kNT; ++k) {
         const int i = k * kNT + tid;
@@ -143,13 +147,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kNT, 1) pages
                 sm.pages[i] = (int32_t)pages;
                 if (f >= 0) atomicMin(&sm.first[f], i);
             }
+            sm.parent[i] = parent[k];
             sm.rank[i] = (len & (P - 1)) != 0;   // until the ranks are known: a page in progress
         }
     }
     __syncthreads();
     const bool bad = sm.bad != 0;
 #pragma unroll
-    for (int k = 0; k < kMaxSeq / kNT; ++k) whole[k] = parent[k] < 0 || sm.rank[parent[k]] == 0;
+    for (int k = 0; k < kMaxSeq / kNT; ++k) {
+        whole[k] = parent[k] < 0 || sm.rank[parent[k]] == 0;
+        len[k] = cta == 0 && parent[k] >= 0 ? __ldcg(p.lens + parent[k]) : 0;
+    }
     __syncthreads();
     int32_t pieces = 0, copies = 0;
     if (!bad) {
@@ -163,7 +171,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kNT, 1) pages
             const int64_t at =
                 scan(((int64_t)(i < n ? (sm.pages[i] + kPiece - 1) / kPiece : 0) << 32) + copy, sm.part, &sum);
             if (i < n) {
-                sm.piece0[i] = pieces + (int32_t)(at >> 32);
+                const int32_t k0 = pieces + (int32_t)(at >> 32), k1 = min(k0 + (sm.pages[i] + kPiece - 1) / kPiece, kNT);
+                sm.piece0[i] = k0;
+                for (int32_t j = k0; j < k1; ++j) sm.of[j] = (uint16_t)i;
                 sm.rank[i] = copy ? copies + (int32_t)(uint32_t)at : -1;
             }
             pieces += (int32_t)(sum >> 32);
@@ -220,16 +230,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kNT, 1) pages
         }
         // new rows, a piece of the parent's a warp at a time
         for (int i = gw; i < n; i += stride_w) {
-            const int32_t f = __ldcg(p.parents + i);
+            const int32_t f = sm.parent[i];
             if (f < 0) continue;
             const int32_t pages = sm.pages[f], rank = sm.rank[i];
+            const int32_t to = rank >= 0 ? __ldcg(p.free_pages + n_free - 1 - rank) : 0;
             const int32_t* src = p.table + (int64_t)f * p.stride;
             int32_t* dst = p.rows + (int64_t)i * p.stride;
 #pragma unroll 4
             for (int32_t w = lane; w < pages; w += 32) {
                 int32_t id = __ldcg(src + w);
                 if (rank >= 0 && w == pages - 1) {
-                    const int32_t to = __ldcg(p.free_pages + n_free - 1 - rank);
                     *reinterpret_cast<int2*>(p.copies + 2 * i) = make_int2(id, to);
                     id = to;
                 }
@@ -239,11 +249,19 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kNT, 1) pages
     }
     cluster.sync();
     // every CTA adds up what the pieces let go
+    const bool few = pieces <= kNT;
     int64_t total = 0;
     if (!broken) {
-        int64_t freed = 0;
-        for (int32_t k0 = 0; k0 < pieces; k0 += kNT) freed += k0 + tid < pieces ? __ldcg(p.counts + k0 + tid) : 0;
-        scan(freed, sm.part, &total);
+        if (few) {
+            const int32_t c = tid < pieces ? __ldcg(p.counts + tid) : 0;
+            const int64_t at = scan(c, sm.part, &total);
+            sm.gone[tid] = make_int2(c, (int32_t)at);
+            __syncthreads();
+        } else {
+            int64_t freed = 0;
+            for (int32_t k0 = 0; k0 < pieces; k0 += kNT) freed += k0 + tid < pieces ? __ldcg(p.counts + k0 + tid) : 0;
+            scan(freed, sm.part, &total);
+        }
     }
     const int64_t top = (int64_t)n_free - copies + total;
     broken |= top > p.n_pages;   // a page listed twice by a sequence
@@ -263,25 +281,27 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kNT, 1) pages
         return;
     }
     // owned pages onto the stack, a piece a warp, from the place its counts before it give
-    int64_t base = 0;
-    for (int32_t k0 = 0; k0 < pieces; k0 += kNT) {
-        const int32_t k = k0 + tid;
-        int64_t sum;
-        const int64_t at = base + scan(k < pieces ? __ldcg(p.counts + k) : 0, sm.part, &sum);
-        base += sum;
-        if (k < pieces && k % kCluster == cta) p.places[k] = (int32_t)at;   // this CTA's warps'
+    if (!few) {
+        int64_t base = 0;
+        for (int32_t k0 = 0; k0 < pieces; k0 += kNT) {
+            const int32_t k = k0 + tid;
+            int64_t sum;
+            const int64_t at = base + scan(k < pieces ? __ldcg(p.counts + k) : 0, sm.part, &sum);
+            base += sum;
+            if (k < pieces && k % kCluster == cta) p.places[k] = (int32_t)at;   // this CTA's warps'
+        }
+        __syncthreads();
     }
-    __syncthreads();
     for (int32_t k = gw; k < pieces; k += stride_w) {
-        const int32_t c = __ldcg(p.counts + k);
-        if (c == 0) continue;
+        const int2 c = few ? sm.gone[k] : make_int2(__ldcg(p.counts + k), __ldcg(p.places + k));
+        if (c.x == 0) continue;
         const Piece q(sm, n, k);
         const int32_t* src = p.gone + (int64_t)q.s * p.stride + q.w0;
-        const int64_t last = top - 1 - __ldcg(p.places + k);
+        const int64_t last = top - 1 - c.y;
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
             const int j = 32 * u + lane;
-            if (j < c) {
+            if (j < c.x) {
                 const int32_t id = __ldcg(src + j);
                 p.marks[id] = 0;
                 p.free_pages[last - j] = id;
@@ -289,11 +309,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kNT, 1) pages
         }
     }
     if (cta == 0 && tid == 0) *p.n_free = (int32_t)top;
-    int64_t len[kMaxSeq / kNT];
-    if (cta == 0) {   // read by all before it is written: the other CTAs are past their reads
-#pragma unroll
-        for (int k = 0; k < kMaxSeq / kNT; ++k) len[k] = parent[k] >= 0 ? __ldcg(p.lens + parent[k]) : 0;
-        __syncthreads();
+    if (cta == 0) {   // the other CTAs are past their reads
 #pragma unroll
         for (int k = 0; k < kMaxSeq / kNT; ++k) {
             const int i = k * kNT + tid;
@@ -301,7 +317,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kNT, 1) pages
         }
     }
     for (int i = gw; i < n; i += stride_w) {
-        const int32_t f = __ldcg(p.parents + i);
+        const int32_t f = sm.parent[i];
         if (lane == 0 && sm.rank[i] < 0) *reinterpret_cast<int2*>(p.copies + 2 * i) = make_int2(-1, -1);
         if (f < 0) continue;
         const int32_t pages = sm.pages[f];
@@ -328,7 +344,7 @@ struct CopyParams {
 
 // Unit: the type that pages are moved in.  A page's units in all pools are numbered through; a
 // CTA moves 1024 of them, so small arrays (scales) share one.  What bounds it: memory; 8 layers'
-// pages of 16 rows, 2 heads of 256, for 270 of 512 children: 15 us, 4.8 TB/s (as much with the
+// pages of 16 rows, 2 heads of 256, for 270 of 512 children: 14 us, 5.1 TB/s (as much with the
 // copies picked out first and taken in turn by 608 CTAs).
 template <typename Unit>
 __global__ void __launch_bounds__(kCopyNT) pages_copy_kernel(const __grid_constant__ CopyParams p) {
