@@ -130,8 +130,10 @@ __global__ void __launch_bounds__(kNT, sizeof(T) == 4 ? 4 : 5) gqa_append_kernel
             const int64_t pos = a.positions[p.axis[k] * a.pos_stride + t0 + tok];
             const int64_t phase = (int64_t)((uint64_t)pos * p.inc[k]);
             float2 cs;
-            sincospif(__ll2float_rn(phase) * 0x1p-63f, &cs.y, &cs.x);
-            table[tok][k] = cs;
+            // half turns in f32 are off by up to 2^-25, which the next term of the angle's sum takes back
+            const float h = __ll2float_rn(phase), r = __ll2float_rn(phase - __float2ll_rn(h)) * (float)(M_PI * 0x1p-63);
+            sincospif(h * 0x1p-63f, &cs.y, &cs.x);
+            table[tok][k] = make_float2(__fmaf_rn(-r, cs.y, cs.x), __fmaf_rn(r, cs.x, cs.y));
         }
         __syncthreads();
     }
