@@ -331,36 +331,26 @@ __device__ __forceinline__ void load_queries(const GqaParams& p, const GqaSegmen
     const bool live = r < g.vecs;
     const QT* src = static_cast<const QT*>(p.q) + (live ? gqa_vector<D>(p, g, g.vec0 + r) : 0) + half * E;
     constexpr int V = 16 / sizeof(QT);
+    struct alignas(16) Piece {
+        QT e[V];
+    } v[E / V];   // all asked for at once
+#pragma unroll
+    for (int i = 0; i < E / V; ++i)
+        *reinterpret_cast<uint4*>(&v[i]) = live ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
     float amax = 0.0f;
-    auto load8 = [&](int i, float (&x)[8]) {
 #pragma unroll
-        for (int k = 0; k < 8; k += V) {
-            struct alignas(16) { QT e[V]; } v;
-            *reinterpret_cast<uint4*>(&v) =
-                live ? __ldg(reinterpret_cast<const uint4*>(src + 8 * i + k)) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int e = 0; e < V; ++e) x[k + e] = (float)v.e[e];
-        }
-    };
-#pragma unroll 4
-    for (int i = 0; i < E / 8; ++i) {
-        float x[8];
-        load8(i, x);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(x[k]));
-    }
+    for (int i = 0; i < E; ++i) amax = fmaxf(amax, fabsf((float)v[i / V].e[i % V]));
     amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
     const int e = max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -110);
     const float up = __uint_as_float((uint32_t)(127 - e) << 23);
     if (half == 0) sm.qs[r] = p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll 4
+#pragma unroll
     for (int i = 0; i < E / 8; ++i) {
-        float x[8];
-        load8(i, x);   // from L1
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float a = x[2 * k] * up, b = x[2 * k + 1] * up;
+            const int e0 = 8 * i + 2 * k;
+            const float a = (float)v[e0 / V].e[e0 % V] * up, b = (float)v[e0 / V].e[e0 % V + 1] * up;
             hi[k] = half2_of(a, b);
             const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
             lo[k] = half2_of(a - h.x, b - h.y);
