@@ -323,43 +323,51 @@ struct Codes {
     }
 };
 
-// Queries of the tile to f16, two threads a vector; threads 0 .. 255.
+// Queries of the tile to f16: a warp takes 16 vectors, a lane 16 bytes of one at a time, all asked for at
+// once.
 template <int D, int QP, typename QT>
 __device__ __forceinline__ void load_queries(const GqaParams& p, const GqaSegment& g, Misc& sm, unsigned char* sq) {
-    constexpr int E = D / 2;
-    const int r = threadIdx.x / 2, half = threadIdx.x % 2;
-    const bool live = r < g.vecs;
-    const QT* src = static_cast<const QT*>(p.q) + (live ? gqa_vector<D>(p, g, g.vec0 + r) : 0) + half * E;
-    constexpr int V = 16 / sizeof(QT);
+    constexpr int V = 16 / sizeof(QT), kLanes = D / V, kAt = 32 / kLanes;   // elements a lane, lanes a vector, vectors a load
+    constexpr int kVecs = kM / (kNT / 32), kLoads = kVecs / kAt;
+    const int lane = threadIdx.x & 31, r0 = (threadIdx.x >> 5) * kVecs + lane / kLanes, d = lane % kLanes * V;
     struct alignas(16) Piece {
         QT e[V];
-    } v[E / V];   // all asked for at once
+    } v[kLoads];
+    int32_t tok = (int32_t)((uint32_t)(g.vec0 + r0) / (uint32_t)p.group), rem = g.vec0 + r0 - tok * p.group;
+    const QT* src = static_cast<const QT*>(p.q) + (g.q0 * p.n_heads + g.h * p.group) * (int64_t)D + d;
 #pragma unroll
-    for (int i = 0; i < E / V; ++i)
-        *reinterpret_cast<uint4*>(&v[i]) = live ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
-    float amax = 0.0f;
+    for (int i = 0; i < kLoads; ++i) {
+        *reinterpret_cast<uint4*>(&v[i]) =
+            r0 + i * kAt < g.vecs ? __ldg(reinterpret_cast<const uint4*>(src + ((int64_t)tok * p.n_heads + rem) * D))
+                                  : make_uint4(0u, 0u, 0u, 0u);
+        for (rem += kAt; rem >= p.group; rem -= p.group) ++tok;
+    }
 #pragma unroll
-    for (int i = 0; i < E; ++i) amax = fmaxf(amax, fabsf((float)v[i / V].e[i % V]));
-    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
-    const int e = max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -110);
-    const float up = __uint_as_float((uint32_t)(127 - e) << 23);
-    if (half == 0) sm.qs[r] = p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 + e) << 23);
+    for (int i = 0; i < kLoads; ++i) {
+        const int r = r0 + i * kAt;
+        float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E / 8; ++i) {
-        uint32_t hi[4], lo[4];
+        for (int k = 0; k < V; ++k) amax = fmaxf(amax, fabsf((float)v[i].e[k]));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int e0 = 8 * i + 2 * k;
-            const float a = (float)v[e0 / V].e[e0 % V] * up, b = (float)v[e0 / V].e[e0 % V + 1] * up;
+        for (int o = kLanes / 2; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+        const int e = max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -110);
+        const float up = __uint_as_float((uint32_t)(127 - e) << 23);
+        if (d == 0) sm.qs[r] = p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 + e) << 23);
+        uint32_t hi[V / 2], lo[V / 2];
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) {
+            const float a = (float)v[i].e[2 * k] * up, b = (float)v[i].e[2 * k + 1] * up;
             hi[k] = half2_of(a, b);
             const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
             lo[k] = half2_of(a - h.x, b - h.y);
         }
-        const int d = half * E + 8 * i;
         unsigned char* at = sq + (d / 64) * (128 * 128) + sw128(r, 2 * (d % 64));
-        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if constexpr (QP == 2)
-            *reinterpret_cast<uint4*>(at + (D / 64) * (128 * 128)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if constexpr (QP == 1) {
+            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        } else {
+            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(at + (D / 64) * (128 * 128)) = make_uint2(lo[0], lo[1]);
+        }
     }
 }
 
