@@ -153,16 +153,19 @@ struct GqaWalk {
         v_end = start_of(c + 1);
         return true;
     }
-    // The place of number v in sequence b (its shape in s, first number in seq_v).
+    // The place of number v in sequence b (its shape in s, first number in seq_v), by whole warps: 32 tiles are
+    // tried at a time.
     __device__ __forceinline__ void place(const GqaParams& p, int64_t v) {
         int64_t x = v - seq_v;
         h = x < s.per_head ? 0 : (int32_t)quot(x, s.per_head);
         x -= h * s.per_head;
         int32_t lo = 0, hi = s.tiles;
         while (hi - lo > 1) {
-            const int32_t mid = lo + (hi - lo) / 2;
-            if (prefix_many(p, s, mid) <= x) lo = mid;
-            else hi = mid;
+            const int32_t step = (hi - lo + 31) / 32;
+            const int64_t mid = lo + (int64_t)step * (1 + (int32_t)(threadIdx.x & 31));
+            const bool before = mid < hi && prefix_many(p, s, mid) <= x;
+            lo += step * __popc(__ballot_sync(kFull, before));
+            hi = (int32_t)min((int64_t)hi, (int64_t)lo + step);
         }
         j = lo;
         u0 = max((int64_t)0, x - prefix(p, s, lo) - OV);
@@ -196,11 +199,19 @@ struct GqaWalk {
                 const int l = __ffs(who) - 1;
                 b = k0 + l;
                 seq_v = __shfl_sync(kFull, first + incl - n, l);
+                s.n = __shfl_sync(kFull, y.n, l);
+                s.rows = __shfl_sync(kFull, y.rows, l);
+                s.base = __shfl_sync(kFull, y.base, l);
+                s.tiles = __shfl_sync(kFull, y.tiles, l);
+                s.q0 = __shfl_sync(kFull, y.q0, l);
+                s.D = __shfl_sync(kFull, y.D, l);
+                s.before = __shfl_sync(kFull, y.before, l);
+                s.per_head = __shfl_sync(kFull, y.per_head, l);
+                s.j0 = __shfl_sync(kFull, y.j0, l);
                 break;
             }
             first += __shfl_sync(kFull, incl, 31);
         }
-        s = shape(p, b);
         place(p, v0);
         return true;
     }

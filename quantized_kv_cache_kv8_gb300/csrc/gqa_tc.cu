@@ -9,12 +9,14 @@
 // one tile can't overlap with itself: tensor memory holds two tiles' scores and contexts and no more.
 // So two CTAs share an SM, one's softmax beside the other's products, and the weights go
 // into the second product from tensor memory, over the scores they came from, instead of
-// through shared memory.  512 bf16 tokens of 32 heads (8 of keys) of 128 on 8704 rows: 127 us, 555
-// TFLOP/s; tensor pipe 24% busy, shared memory 43%, issue slots 33%.
+// through shared memory.  512 bf16 tokens of 32 heads (8 of keys) of 128 on 8704 rows: 117 us, 606
+// TFLOP/s; at 133 us the tensor pipe was 24% busy, shared memory 43%, issue slots 33%.
 // A step takes one CTA some 6,200 cycles: 3,200 the softmax, 2,400 the products (issuing, waiting for the
 // weights' product and for the scores).  Slower (of 133 us then): scores of 64 rows in two buffers (157);
 // the next scores loaded ahead, with more registers for the softmax and fewer for the converters
-// (154); eight softmax warps, half of the rows each (215: 80 registers).
+// (154); eight softmax warps, half of the rows each (215: 80 registers).  Beside the steps a CTA spends
+// some 10,000 cycles on finding its place (by bisection over the tiles 17,000), 4,000 on the first queries
+// and as many on each tile's outputs.
 //   * warps 0-3: softmax, a vector a thread, so maxima and sums need no exchange; 32 scores at
 //     a time are loaded, turned into weights and stored over the first half of the scores'
 //     place (f32 queries: two f16 halves, over the whole place);
