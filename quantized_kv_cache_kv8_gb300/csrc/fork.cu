@@ -66,6 +66,11 @@ struct ForkShared {
     int32_t flag;                 // this CTA met a page outside the pool
 };
 
+__device__ __forceinline__ void set_copy(const ForkParams& p, int i, int32_t from, int32_t to) {
+    p.copies[2 * i] = from;   // aligned to its elements only
+    p.copies[2 * i + 1] = to;
+}
+
 // Exclusive scan over the CTA of one value a thread; the total in *sum.
 __device__ __forceinline__ int64_t scan(int64_t v, int64_t* part, int64_t* sum) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -240,7 +245,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kNT, 1) pages
             for (int32_t w = lane; w < pages; w += 32) {
                 int32_t id = __ldcg(src + w);
                 if (rank >= 0 && w == pages - 1) {
-                    *reinterpret_cast<int2*>(p.copies + 2 * i) = make_int2(id, to);
+                    set_copy(p, i, id, to);
                     id = to;
                 }
                 dst[w] = id;
@@ -277,7 +282,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kNT, 1) pages
             }
         if (cta == 0 && tid == 0 && p.err) atomicCAS(p.err, 0, status != KVQ_OK ? status : (int32_t)KVQ_ERR_ARG);
         for (int i = cta * kNT + tid; i < n; i += kCluster * kNT)
-            *reinterpret_cast<int2*>(p.copies + 2 * i) = make_int2(-1, -1);
+            set_copy(p, i, -1, -1);
         return;
     }
     // owned pages onto the stack, a piece a warp, from the place its counts before it give
@@ -318,7 +323,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kNT, 1) pages
     }
     for (int i = gw; i < n; i += stride_w) {
         const int32_t f = sm.parent[i];
-        if (lane == 0 && sm.rank[i] < 0) *reinterpret_cast<int2*>(p.copies + 2 * i) = make_int2(-1, -1);
+        if (lane == 0 && sm.rank[i] < 0) set_copy(p, i, -1, -1);
         if (f < 0) continue;
         const int32_t pages = sm.pages[f];
         const int32_t* src = p.rows + (int64_t)i * p.stride;

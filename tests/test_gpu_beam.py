@@ -268,6 +268,28 @@ def test_fork_refuses_all_or_nothing(kvq):
         assert kvq.read_device_error(ws) == 0
 
 
+def test_operands_aligned_to_their_elements_only(kvq):
+    def odd(t):   # the same values, one element behind a 16-byte boundary
+        return torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)
+
+    batch = Batch([33, 40, 5, 64], 16, 5, 30, seed=4)
+    d = {k: odd(v) for k, v in batch.device().items()}
+    assert all(v.data_ptr() % 16 for v in d.values())
+    for parents in ([0, 0, 1, 3], [2, 2, 2, -1]):
+        copies = batch.step(parents)
+        ws = torch.zeros(kvq.kv_pages_fork_workspace_size(4, 5, 30), dtype=torch.uint8, device="cuda")
+        kvq.kv_pages_fork(odd(torch.tensor(parents, dtype=torch.int32, device="cuda")), d["lens"], d["table"], d["free"], d["n_free"], 16,
+                          d["copies"], ws)
+        same(d, batch, copies)
+    pool = torch.arange(30 * 7, dtype=torch.int32, device="cuda").view(30, 7)
+    kvq.kv_pages_copy(odd(torch.tensor([[3, 9]], dtype=torch.int32, device="cuda")), [odd(pool)])
+    x, s = random_logits(3, 4, 5000, torch.float32)
+    want = run_select(kvq, x, s, 8)
+    got = [odd(torch.zeros_like(w)) for w in want]
+    kvq.kv_beam_select(odd(x), odd(s), *got, torch.zeros(kvq.kv_beam_workspace_size(3, 4, 5000, 8), dtype=torch.uint8, device="cuda"))
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
 def test_copy(kvq):
     g = torch.Generator().manual_seed(0)
     pools = [torch.randint(0, 255, (12, 2, 16, 64), generator=g, dtype=torch.uint8).cuda(),

@@ -589,6 +589,28 @@ def test_append_in_place_without_rotation_and_parts(kvq):
     assert torch.equal(pool.k[0, :, :n].transpose(0, 1), c) and torch.equal(pool.scales[0, :, :n, 0].T, s)
 
 
+@pytest.mark.parametrize("dtype", DT)
+def test_operands_aligned_to_their_elements_only(kvq, dtype):
+    def odd(t):
+        return torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)
+
+    pool, twin = Pool(2, 128, 16, [40, 60]), Pool(2, 128, 16, [40, 60])
+    k, v, q = (queries(5, h, 128, dtype, seed=h + i) for i, h in enumerate((2, 2, 6)))
+    rope = kvq.rope_layout([0.7 ** i for i in range(20)], [i % 2 for i in range(20)], n_axes=2)
+    pos, slots = torch.arange(10, device="cuda").view(2, 5), torch.tensor([3, 50, 17, 0, 64], device="cuda")
+    outs, errs = [torch.zeros_like(q), odd(torch.zeros_like(q))], [torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2)]
+    kvq.kv_gqa_append(rope, k, v, pos, slots, q, outs[0], pool.k, pool.v, pool.scales, errs[0])
+    kvq.kv_gqa_append(rope, odd(k), odd(v), odd(pos), odd(slots), odd(q), outs[1], twin.k, twin.v, twin.scales, odd(errs[1]))
+    assert torch.equal(*outs) and all(torch.equal(getattr(pool, a), getattr(twin, a)) for a in ("k", "v", "scales"))
+    for new in (1, 40):
+        q = queries(2 * new, 6, 128, dtype)
+        want, ws = attend(kvq, pool, q, [40, 60], [new, new])
+        out = torch.zeros_like(q)
+        kvq.kv_gqa_attn_paged(q, odd(offsets([new, new])), pool.k, pool.v, pool.scales, odd(pool.table), odd(pool.lens), out, ws,
+                              1 / math.sqrt(128))
+        assert torch.equal(out, want)
+
+
 def test_append_reports_what_is_no_number_and_what_is_no_slot(kvq):
     pool = Pool(2, 64, 16, [16], spare=0)
     x = queries(3, 2, 64, torch.float32)
