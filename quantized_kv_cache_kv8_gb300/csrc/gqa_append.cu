@@ -10,9 +10,9 @@
 // D / 8 threads holds one head's row, 8 elements a thread.  The rows of all tokens are
 // numbered through and a CTA takes a run of them; the cos and sin of its tokens are shared
 // by their heads, so it tabulates them, while the rows it has asked for are on their way.
-// Measured: 13.1 us for 1999 tokens of 16 query and 2 + 2 rows of 256 in bf16 (39 MB: 3.0
-// TB/s; a plain copy of the queries alone takes 7.9), the rest index arithmetic and the
-// correctly rounded divisions of the codes; 64 tokens of 32 + 8 + 8 heads 4.9 us, the launch's
+// Measured: 12.5 us a call (13 to 14.5 in a replayed graph) for 1999 tokens of 16 query and 2 + 2
+// rows of 256 in bf16 (39 MB: 3 TB/s; a plain copy of the queries alone takes 7.9), issue slots 74%
+// busy with angles, index arithmetic and the correctly rounded divisions of the codes; 64 tokens of 32 + 8 + 8 heads 4.9 us, the launch's
 // latency.
 #include "gqa.cuh"
 
