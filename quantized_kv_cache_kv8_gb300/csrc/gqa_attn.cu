@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kNT, sm_ctas<D, NV>()) gqa_attn_kernel(const _
                     const float x = z[b][i] - m[b][i & 1];
                     over = fmaxf(over, x);
                     pr[b][i] = ex2(x);
-                    w[b][i] = pr[b][i] * (sv[i >> 1] * f[b][i & 1]);
+                    w[b][i] = pr[b][i] * sv[i >> 1] * f[b][i & 1];   // s_v f may pass f32 where p is 0
                 }
             if (partly) {
 #pragma unroll
