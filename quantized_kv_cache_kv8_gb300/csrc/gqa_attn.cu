@@ -420,7 +420,9 @@ __global__ void __launch_bounds__(kNT, sm_ctas<D, NV>()) gqa_attn_kernel(const _
                         const float d = ex2(m[b][i] - n), f0 = f[b][i];
                         // the largest weight so far, at most 2^14 / f, against the step's
                         const float large = fmaxf(top, f0 > 0.0f ? d * 0x1p14f / f0 : 0.0f);
-                        const float f1 = large > 0.0f ? fminf(0x1p14f / large, 0x1p100f) : f0;
+                        // (rows of zero values weigh nothing yet: the largest factor, with which the first
+                        // weight passes 60000 and lifts; a factor of 0 would hide all that follow)
+                        const float f1 = fminf(0x1p14f / large, 0x1p100f);
                         k[i] = f0 > 0.0f ? d * (f1 / f0) : 0.0f;
                         l[b][i] *= d;
                         tl[b][i] *= d;

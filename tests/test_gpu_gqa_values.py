@@ -1,4 +1,4 @@
-"""Grouped-query attention over value rows of extreme sizes."""
+"""Grouped-query attention over value rows of zeros and of extreme sizes."""
 import math
 
 import pytest
@@ -24,6 +24,15 @@ def place(pool, b, t):
     return pool.table[b].long()[t // pool.page], t % pool.page
 
 
+def blank(pool, b, t, heads=slice(None)):
+    """Rows t of sequence b as kv_gqa_append stores values of zero."""
+    pg, at = place(pool, b, t)
+    v, s = pool.v[pg, :, at], pool.scales[pg, :, at]   # [rows][heads][..]
+    v[:, heads] = 0
+    s[:, heads, 1] = 0.0
+    pool.v[pg, :, at], pool.scales[pg, :, at] = v, s
+
+
 # So many sequences over the same pages that a CTA takes several steps of each.
 MANY = 300
 
@@ -32,6 +41,68 @@ def shared(pool):
     """The table and lengths of MANY sequences with the pages of sequence 0."""
     pool.table = pool.table[:1].expand(MANY, pool.width).contiguous()
     return [int(pool.lens[0])] * MANY
+
+
+def check_shared(out, q, pool, new, sm, causal, what=""):
+    """As check, for sequences that share their rows: token i of all of them at once."""
+    n, ref = int(pool.lens[0]), {}
+    wide = q.dtype == torch.bfloat16 and new * (q.shape[1] // pool.heads) > 24
+    for absolute in (False, True)[:1 + wide]:
+        r = ref[absolute] = torch.empty(q.shape, dtype=torch.float64, device="cuda")
+        for i in range(new):
+            rows = n - new + 1 + i if causal else n
+            r[i::new] = attention(q[i::new], pool, [rows], [len(q) // new], sm, False, absolute)
+    close(out, ref[False], what, ref.get(True))
+
+
+# a sequence's new tokens, and the vectors of a tile: 8, 16, 128
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim,heads,kv", [(64, 8, 2), (128, 8, 2), (256, 4, 1)])
+@pytest.mark.parametrize("new", [1, 4, 20])
+def test_zero_values_in_front(kvq, dtype, causal, dim, heads, kv, new):
+    for front in (15, 16, 64, 200):
+        pool = Pool(kv, dim, 16, [330], seed=front)
+        blank(pool, 0, range(front))
+        lens, news = shared(pool), [new] * MANY
+        q = queries(new * MANY, heads, dim, dtype)
+        out, ws = attend(kvq, pool, q, lens, news, causal)
+        check_shared(out, q, pool, new, 1 / math.sqrt(dim), causal, f"{front} rows")
+        assert kvq.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("odd", [0, 1])
+@pytest.mark.parametrize("run", [16, 64, 256])
+def test_zero_values_where_a_share_of_the_rows_begins(kvq, dtype, odd, run):
+    """Long sequences are cut among the CTAs at multiples of 64 rows: every other run is zero."""
+    lens = [30000, 9001]
+    for dim in (64, 128, 256):
+        pool = Pool(2, dim, 64, lens, seed=run)
+        for b, n in enumerate(lens):
+            t = torch.arange(n)
+            blank(pool, b, t[t // run % 2 == odd], heads=slice(0, 1))
+        for causal, new in ((True, [1, 1]), (True, [3, 4]), (False, [2, 1])):
+            q = queries(sum(new), 8, dim, dtype)
+            out, _ = attend(kvq, pool, q, lens, new, causal)
+            check(out, q, pool, lens, new, 1 / math.sqrt(dim), causal, f"dim {dim} {new}")
+
+
+def test_appended_zero_values(kvq):
+    """As an encoder's padding gets there: rows of zero values through the append, then decode steps and cross attention."""
+    n, kv, dim = 200, 2, 128
+    for front in (16, 64):
+        pool = Pool(kv, dim, 16, [n], seed=3)
+        pool.k.zero_(), pool.v.zero_(), pool.scales.zero_()
+        k, v = queries(n, kv, dim, torch.bfloat16, seed=4), queries(n, kv, dim, torch.bfloat16, seed=5)
+        v[:front] = 0
+        pg, at = place(pool, 0, range(n))
+        kvq.kv_gqa_append(None, k, v, None, pg * pool.page + at, None, None, pool.k, pool.v, pool.scales)
+        assert bool((pool.scales[pg[:front], :, at[:front], 1] == 0).all())
+        lens, q = shared(pool), queries(2 * MANY, 8, dim, torch.bfloat16)
+        for causal in (True, False):
+            out, _ = attend(kvq, pool, q, lens, [2] * MANY, causal)
+            check_shared(out, q, pool, 2, 1 / math.sqrt(dim), causal, f"{front} causal={causal}")
 
 
 @pytest.mark.parametrize("dtype", DT)
@@ -48,7 +119,7 @@ def test_sizes_of_values(kvq, dtype, gain):
 
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("new", [1, 3, 20])
-@pytest.mark.parametrize("small", [1e-25])
+@pytest.mark.parametrize("small", [0.0, 1e-25])
 def test_large_values_of_no_weight_behind_small_ones(kvq, dtype, new, small):
     """The last rows' values are 1e13, at scores so low that their weights vanish from f32."""
     n, dim = 640, 128
@@ -64,4 +135,4 @@ def test_large_values_of_no_weight_behind_small_ones(kvq, dtype, new, small):
     lens, news = shared(pool), [new] * MANY
     q = q.repeat(MANY, 1, 1)
     out, _ = attend(kvq, pool, q, lens, news, causal=False, sm=1.0)
-    check(out, q, pool, lens, news, 1.0, False)
+    check_shared(out, q, pool, new, 1.0, False)
