@@ -333,12 +333,13 @@ __global__ void __launch_bounds__(kNT, sm_ctas<D, NV>()) gqa_attn_kernel(const _
                         }
                 }
                 if (more) load_keys<D>(rows, p.k_codes + at * D, g, c);
+                const float sk[2] = {key_scale(rows.s[0].x), key_scale(rows.s[1].x)};
 #pragma unroll
                 for (int b = 0; b < NV; ++b) {
-                    z[b][0] = s4[b].x * rows.s[0].x * qs[b][0];
-                    z[b][1] = s4[b].y * rows.s[0].x * qs[b][1];
-                    z[b][2] = s4[b].z * rows.s[1].x * qs[b][0];
-                    z[b][3] = s4[b].w * rows.s[1].x * qs[b][1];
+                    z[b][0] = s4[b].x * sk[0] * qs[b][0];
+                    z[b][1] = s4[b].y * sk[0] * qs[b][1];
+                    z[b][2] = s4[b].z * sk[1] * qs[b][0];
+                    z[b][3] = s4[b].w * sk[1] * qs[b][1];
                 }
             }
             float sv[2] = {rows.s[0].y, rows.s[1].y};

@@ -319,6 +319,10 @@ __device__ __forceinline__ int32_t gqa_page(const GqaParams& p, int32_t b, int32
     return id;
 }
 
+// A key's scale as its scores take it: NaN for an infinite one (0 times it is NaN), whose row a negative
+// product would hide.
+__device__ __forceinline__ float key_scale(float s) { return __fmaf_rn(s, 0.0f, s); }
+
 // The tensor-core kernel (gqa_tc.cu): f32 queries up to 128 dims.
 size_t gqa_tc_state_bytes(int32_t head_dim);
 bool gqa_tc_supported(int32_t head_dim, kvq_dtype dt);

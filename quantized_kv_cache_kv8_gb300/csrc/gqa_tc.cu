@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                 codes.store(raw + C::kOffK + w0 * 128, lane);
                 codes.load(p.v_codes, at, lane);
                 if ((u0 + s) * kN + kN > all && codes.mend(lane)) sc.y = __uint_as_float(0x7fffffffu);
-                sm.sk[ph][w0 + lane] = sc.x;
+                sm.sk[ph][w0 + lane] = key_scale(sc.x);
                 sm.sv[ph][w0 + lane] = sc.y;
                 const float top = warp_max(fabsf(sc.y));
                 if (lane == 0) sm.sv_top[ph][warp - 4] = top;

@@ -1,4 +1,4 @@
-"""Grouped-query attention over value rows of zeros and of extreme sizes."""
+"""Grouped-query attention over value rows of zeros and of extreme sizes, and rows that are no numbers."""
 import math
 
 import pytest
@@ -136,3 +136,35 @@ def test_large_values_of_no_weight_behind_small_ones(kvq, dtype, new, small):
     q = q.repeat(MANY, 1, 1)
     out, _ = attend(kvq, pool, q, lens, news, causal=False, sm=1.0)
     check_shared(out, q, pool, new, 1.0, False)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [6, 70])
+def test_every_dim_of_a_token_that_sees_no_number(kvq, dtype, causal, dim, new):
+    """A key's NaN code or either scale that is no finite number makes every dim NaN, whatever the sign of the product;
+    a value's NaN code its own dim; tokens that don't see the row are as without it."""
+    lens, news, sm = [330 + new, 150], [new, 20 if new > 6 else 2], 0.1
+    row = 330 + new // 2
+    for bad in ("k", "v", "sk", "sv"):
+        for x in (math.nan, math.inf, -math.inf) if bad in ("sk", "sv") else (None,):
+            pool, clean = Pool(2, dim, 16, lens, seed=9), Pool(2, dim, 16, lens, seed=9)
+            q = queries(sum(news), 8, dim, dtype)
+            pg, at = place(pool, 0, [row])
+            pg1 = int(pool.table[1, 150 // 16])   # behind sequence 1's end
+            for p_, a in ((int(pg), slice(int(at), int(at) + 1)), (pg1, slice(150 % 16, 16))):
+                if x is None:
+                    (pool.k if bad == "k" else pool.v)[p_, :, a, 5] = 0x7f
+                else:
+                    pool.scales[p_, :, a, 0 if bad == "sk" else 1] = x
+            out, ws = attend(kvq, pool, q, lens, news, causal, sm=sm)
+            sees = [i for i in range(new) if not causal or 330 + i >= row]
+            rest = [i for i in range(len(q)) if i not in sees]
+            hit = torch.isnan(out[sees])
+            assert bool(hit[..., 5].all() if bad == "v" else hit.all()), (bad, x)
+            ref = attention(q, clean, lens, news, sm, causal)
+            wide = dtype == torch.bfloat16 and new > 6
+            mass = attention(q, clean, lens, news, sm, causal, absolute=True)[rest] if wide else None
+            close(out[rest], ref[rest], f"{bad} {x}", mass)
+            assert kvq.read_device_error(ws) == 0
