@@ -195,16 +195,26 @@ __device__ __forceinline__ float2 raise(const Misc& sm, uint32_t tm, uint32_t to
     if (lift) n = fmaxf(R, ceilf(fmaxf(y - (QP == 1 ? 8.0f : 12.0f), zm - 100.0f)));
     if (!(n >= kNone)) n = kNone;   // no score but -inf
     const float a = n == R ? 1.0f : ex2(R - n);
-    const __half2 a2 = __float2half2_rn(a);
+    // in f32: the factor may lie below f16's range where the weights, up to 2^16 of the old reference, stay in it
 #pragma unroll 1
     for (int k = 0; k < j; ++k) {
         uint32_t w[kWords<QP>];
         load_weights(tm + weight_col<QP>(k * (kC / 16)), w);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < kWords<QP>; ++i) {
-            __half2 h = __hmul2(*reinterpret_cast<__half2*>(&w[i]), a2);
-            w[i] = *reinterpret_cast<uint32_t*>(&h);
+        for (int c = 0; c < kC; c += 2) {
+            const int at = QP * 8 * (c / 16) + c % 16 / 2;
+            float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[at]));
+            if constexpr (QP == 2) {   // the halves' sum is exact: 22 bits
+                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[8 + at]));
+                x = make_float2(x.x + y.x, x.y + y.y);
+            }
+            x = make_float2(x.x * a, x.y * a);
+            w[at] = half2_of(x.x, x.y);
+            if constexpr (QP == 2) {
+                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[at]));
+                w[8 + at] = half2_of(x.x - y.x, x.y - y.y);
+            }
         }
         store_weights(tm + weight_col<QP>(k * (kC / 16)), w);
     }

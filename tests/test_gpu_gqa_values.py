@@ -1,4 +1,5 @@
-"""Grouped-query attention over value rows of zeros and of extreme sizes, and rows that are no numbers."""
+"""Grouped-query attention over value rows of zeros and of extreme sizes, rows that are no numbers,
+and weights that a later row dwarfs."""
 import math
 
 import pytest
@@ -168,3 +169,29 @@ def test_every_dim_of_a_token_that_sees_no_number(kvq, dtype, causal, dim, new):
             mass = attention(q, clean, lens, news, sm, causal, absolute=True)[rest] if wide else None
             close(out[rest], ref[rest], f"{bad} {x}", mass)
             assert kvq.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("ahead", [20.0, 24.5, 25.5, 30.0])
+def test_weights_of_a_step_whose_last_row_dwarfs_them(kvq, dtype, dim, ahead):
+    """Rows 128 .. 223 score some binades above the first 128, the next row `ahead` binades: 448 as the values' second
+    dim of the 96 makes their share of the output visible."""
+    one, most = 0x38, 0x7e   # 1.0, 448
+    pool = Pool(1, dim, 64, [256])
+    pool.k[:], pool.v[:] = 0, 0
+    pool.k[..., 0] = one
+    pool.v[..., 0] = one
+    pool.scales[..., 0], pool.scales[..., 1] = 0.0, 1.0
+    pg, at = place(pool, 0, range(128, 224))
+    pool.scales[pg, :, at, 0] = 2.5 if dtype == torch.bfloat16 else 3.5
+    v = pool.v[pg, :, at]
+    v[..., 1] = most
+    pool.v[pg, :, at] = v
+    pg, at = place(pool, 0, [224])
+    pool.scales[pg, :, at, 0] = ahead
+    q = torch.zeros(2, 64, dim, device="cuda", dtype=dtype)
+    q[..., 0] = 1.0
+    sm = float(torch.tensor(math.log(2.0)))   # scores are binades
+    out, _ = attend(kvq, pool, q, [256], [2], causal=False, sm=sm)
+    check(out, q, pool, [256], [2], sm, False)
