@@ -350,8 +350,7 @@ __device__ __forceinline__ void load_queries(const GqaParams& p, const GqaSegmen
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
         *reinterpret_cast<uint4*>(&v[i]) =
-            r0 + i * kAt < g.vecs ? __ldg(reinterpret_cast<const uint4*>(src + ((int64_t)tok * p.n_heads + rem) * D))
-                                  : make_uint4(0u, 0u, 0u, 0u);
+            r0 + i * kAt < g.vecs ? ldg16(src + ((int64_t)tok * p.n_heads + rem) * D) : make_uint4(0u, 0u, 0u, 0u);
         for (rem += kAt; rem >= p.group; rem -= p.group) ++tok;
     }
 #pragma unroll
