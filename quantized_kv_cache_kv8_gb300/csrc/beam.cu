@@ -86,20 +86,13 @@ struct Row {
     __device__ __forceinline__ Row(const T* p, int64_t vocab)
         : x(reinterpret_cast<const char*>(p)), shift((uint32_t)((uintptr_t)p & 15u)), n((uint32_t)vocab), whole(n / V) {}
     __device__ __forceinline__ uint32_t vectors() const { return (n + V - 1) / V; }
-    static __device__ __forceinline__ uint4 ldg(const char* p) {
-        uint4 r;
-        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                     : "l"(p));
-        return r;
-    }
     // The vectors from, from + step, ...: `none` from `end` on.
     template <int N>
     __device__ __forceinline__ void load(uint4 (&r)[N], uint32_t from, uint32_t step, uint32_t end) const {
         if (shift == 0 && from + (N - 1) * step < min(end, whole)) {
             const char* at = x + (uint64_t)from * 16u;
 #pragma unroll
-            for (int u = 0; u < N; ++u) r[u] = ldg(at + u * step * 16u);
+            for (int u = 0; u < N; ++u) r[u] = ldg16(at + u * step * 16u);
         } else {
 #pragma unroll
             for (int u = 0; u < N; ++u) r[u] = from + u * step < end ? load(from + u * step) : none();
@@ -108,7 +101,7 @@ struct Row {
     __device__ __noinline__ uint4 load(uint32_t v) const {
         const char* at = x + (uint64_t)v * 16u;
         if (v < whole) {
-            if (shift == 0) return ldg(at);
+            if (shift == 0) return ldg16(at);
             // both aligned pieces hold elements of the vector
             const uint4 lo = *reinterpret_cast<const uint4*>(at - shift), hi = *reinterpret_cast<const uint4*>(at - shift + 16);
             uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};

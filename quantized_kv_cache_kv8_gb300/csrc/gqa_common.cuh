@@ -52,10 +52,9 @@ struct GqaSeq {
     int64_t j0;
 };
 // The tile that a CTA begins and does not end: how many CTAs share it (0: there is none), where its outputs go.
-struct GqaCut {
+struct alignas(16) GqaCut {
     int32_t count, h, vec0, vecs;
     int64_t q0;
-    int64_t pad;
 };
 // Part of a tile, as its CTA works on it (row counts fit 32 bits: a pool has fewer rows).
 struct GqaSegment {
@@ -79,8 +78,7 @@ struct GqaSegment {
 template <int M, int N, int OV, int LEAST>
 struct GqaWalk {
     static_assert(N % M == 0, "closed form");
-    static constexpr int kScratch = 2;   // int64s a warp of start_many
-    int64_t v_end, per, total;   // the CTA's last number + 1; numbers a CTA, in all
+    int64_t v_end, per;          // the CTA's last number + 1; numbers a CTA
     int32_t extra, ctas, c;      // CTAs with one number more; CTAs that hold any; this one
     int32_t b, h, j;             // sequence, kv head, tile
     int64_t seq_v;               // the sequence's first number
@@ -145,7 +143,6 @@ struct GqaWalk {
     // The numbers dealt out, this CTA's share; false when it has none.
     __device__ __forceinline__ bool deal(int64_t sum, int32_t k, int32_t n_cta) {
         c = k;
-        total = sum;
         ctas = (int32_t)min((int64_t)n_cta, (sum + LEAST - 1) / LEAST);
         if (c >= ctas) return false;
         per = quot(sum, ctas);
@@ -322,6 +319,12 @@ __device__ __forceinline__ int32_t gqa_page(const GqaParams& p, int32_t b, int32
 // A key's scale as its scores take it: NaN for an infinite one (0 times it is NaN), whose row a negative
 // product would hide.
 __device__ __forceinline__ float key_scale(float s) { return __fmaf_rn(s, 0.0f, s); }
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
 
 // The tensor-core kernel (gqa_tc.cu): f32 queries up to 128 dims.
 size_t gqa_tc_state_bytes(int32_t head_dim);

@@ -83,45 +83,6 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, 
         " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 un2(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ uint32_t half2_of(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint4 ldg16(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
 
 // Columns of weights of scores 16 i ..: over the first half of the scores' place, or (two halves)
 // over all of it.
@@ -204,16 +165,16 @@ __device__ __forceinline__ float2 raise(const Misc& sm, uint32_t tm, uint32_t to
 #pragma unroll
         for (int c = 0; c < kC; c += 2) {
             const int at = QP * 8 * (c / 16) + c % 16 / 2;
-            float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[at]));
+            float2 x = unpack_half2(w[at]);
             if constexpr (QP == 2) {   // the halves' sum is exact: 22 bits
-                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[8 + at]));
+                const float2 y = unpack_half2(w[8 + at]);
                 x = make_float2(x.x + y.x, x.y + y.y);
             }
             x = make_float2(x.x * a, x.y * a);
-            w[at] = half2_of(x.x, x.y);
+            w[at] = pack_half2(x.x, x.y);
             if constexpr (QP == 2) {
-                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[at]));
-                w[8 + at] = half2_of(x.x - y.x, x.y - y.y);
+                const float2 y = unpack_half2(w[at]);
+                w[8 + at] = pack_half2(x.x - y.x, x.y - y.y);
             }
         }
         store_weights(tm + weight_col<QP>(k * (kC / 16)), w);
@@ -248,7 +209,7 @@ __device__ __forceinline__ float weights(const Misc& sm, const uint32_t (&s)[kC]
         for (int h = 0; h < 2; ++h) {
             const int c = 4 * q + 2 * h, at = QP * 8 * (c / 16) + c % 16 / 2;
             const F2 b = mul2(h == 0 ? f2(k4.x, k4.y) : f2(k4.z, k4.w), qs2);
-            const float2 t = un2(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), b, r2));
+            const float2 t = unpack(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), b, r2));
             float2 p = make_float2(ex2(t.x), ex2(t.y));
             if (PART) {
                 if (c >= visible) p.x = 0.0f;
@@ -256,21 +217,21 @@ __device__ __forceinline__ float weights(const Misc& sm, const uint32_t (&s)[kC]
             }
             const F2 pp = f2(p.x, p.y);
             sum[h] = add2(sum[h], pp);
-            float2 w = un2(mul2(pp, h == 0 ? f2(v4.x, v4.y) : f2(v4.z, v4.w)));
+            float2 w = unpack(mul2(pp, h == 0 ? f2(v4.x, v4.y) : f2(v4.z, v4.w)));
             if (PART) {   // a hidden row's scale may be no number
                 if (c >= visible) w.x = 0.0f;
                 if (c + 1 >= visible) w.y = 0.0f;
             }
-            const uint32_t hi = half2_of(w.x, w.y);
+            const uint32_t hi = pack_half2(w.x, w.y);
             pk[at] = hi;
             if constexpr (QP == 2) {
                 *most = fmaxf(*most, fmaxf(fabsf(w.x), fabsf(w.y)));
-                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-                pk[8 + at] = half2_of(w.x - x.x, w.y - x.y);
+                const float2 x = unpack_half2(hi);
+                pk[8 + at] = pack_half2(w.x - x.x, w.y - x.y);
             }
         }
     }
-    const float2 u = un2(add2(sum[0], sum[1]));
+    const float2 u = unpack(add2(sum[0], sum[1]));
     return u.x + u.y;
 }
 
@@ -368,9 +329,9 @@ __device__ __forceinline__ void load_queries(const GqaParams& p, const GqaSegmen
 #pragma unroll
         for (int k = 0; k < V / 2; ++k) {
             const float a = (float)v[i].e[2 * k] * up, b = (float)v[i].e[2 * k + 1] * up;
-            hi[k] = half2_of(a, b);
-            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
-            lo[k] = half2_of(a - h.x, b - h.y);
+            hi[k] = pack_half2(a, b);
+            const float2 h = unpack_half2(hi[k]);
+            lo[k] = pack_half2(a - h.x, b - h.y);
         }
         unsigned char* at = sq + (d / 64) * (128 * 128) + sw128(r, 2 * (d % 64));
         if constexpr (QP == 1) {
@@ -631,7 +592,7 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                 if (seg.slot >= 0)
                     p.ws_ml[seg.slot * kM + tid] = make_float2(sum == 0.0f ? kNone : ref + log2f(sum), 0.0f);
                 if (tid == 0 && seg.slot >= 0 && seg.u0 == 0)
-                    p.cuts[blockIdx.x] = GqaCut{seg.count, seg.h, seg.vec0, seg.vecs, seg.q0, 0};
+                    p.cuts[blockIdx.x] = GqaCut{seg.count, seg.h, seg.vec0, seg.vecs, seg.q0};
             }
         } else {
             // ---- codes to f16: rows 32 (warp - 4) .. of each step ---------------------
