@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kNT, 1) paged_exact_kernel(const __grid_consta
             for (int w = tid; w < kN * kWords; w += kNT) {
                 const int r = w / kWords, c = w - r * kWords;
                 uint32_t x = 0u;
-                if (r < nt) x = __ldg(reinterpret_cast<const uint32_t*>(p.codes + (int64_t)prow[r] * (kWords * 4)) + c);
+                if (r < nt) x = reinterpret_cast<const uint32_t*>(p.codes + (int64_t)prow[r] * (kWords * 4))[c];
                 if (TQ4) {
                     float f[8];
 #pragma unroll

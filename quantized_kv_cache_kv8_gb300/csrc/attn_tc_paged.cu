@@ -452,7 +452,7 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, int64_t row0,
         const bool ok = r0 + 4 * g < rows;
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
-            raw[i] = ok ? __ldg(src + g * kMlaD + 8 * i) : make_uint2(0u, 0u);   // 4 vectors on: 4 * 144 units
+            raw[i] = ok ? src[g * kMlaD + 8 * i] : make_uint2(0u, 0u);   // 4 vectors on: 4 * 144 units
     };
     fetch(0, raw);
     fetch(1, ahead);
@@ -519,7 +519,7 @@ __device__ __forceinline__ void rotate_queries(const PagedParams& p, int64_t row
     auto fetch = [&](int g) {
         const bool ok = r0 + 4 * g < rows;
 #pragma unroll
-        for (int j = 0; j < 9; ++j) raw[j] = ok ? __ldg(src + g * 4 * (kMlaD / 8) + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < 9; ++j) raw[j] = ok ? src[g * 4 * (kMlaD / 8) + 8 * j] : make_uint4(0u, 0u, 0u, 0u);
     };
     // two elements with their signs (the lowest two bits) applied
     auto pair = [](uint32_t w, uint32_t bits) {
@@ -920,7 +920,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int32_t row0 = w.first + kHalf * rank + j * box;
                     auto page = [&](int t) {
                         const int32_t r = row0 + t * kRows;
-                        return mine && t < w.steps && r < w.end ? __ldg(table + (r >> p.shift)) : 0;
+                        return mine && t < w.steps && r < w.end ? table[r >> p.shift] : 0;
                     };
                     int32_t id = page(0);
                     for (int t = 0; t < w.steps; ++t, ++it) {
@@ -965,7 +965,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int32_t* table = p.table + (int64_t)w.b * p.table_stride;
                 auto page = [&](int t) {
                     const int32_t x = w.first + t * kRows + 4 * lane;
-                    return t < w.steps && x < w.end ? __ldg(table + (x >> p.shift)) : 0;
+                    return t < w.steps && x < w.end ? table[x >> p.shift] : 0;
                 };
                 int32_t id = page(0);
                 for (int t = 0; t < w.steps; ++t, ++it) {
@@ -977,7 +977,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         v[i] = make_float2(0.f, 0.f);
-                        if (x + i < w.end) v[i] = make_float2(__ldg(s + i * p.n_blocks), __ldg(s + (i + 1) * p.n_blocks - 1));
+                        if (x + i < w.end) v[i] = make_float2(s[i * p.n_blocks], s[(i + 1) * p.n_blocks - 1]);
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[i] = row_scales(v[i].x, v[i].y);
@@ -1009,7 +1009,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             warp_arrive(&bars[kBarWorkFree0 + (n & 1)], lane);
             if (steps == 0) break;
             // pages are asked for a step before the codes, the codes a step before their use
-            auto page = [&](int32_t r) { return r < end ? __ldg(table + (r >> p.shift)) : 0; };
+            auto page = [&](int32_t r) { return r < end ? table[r >> p.shift] : 0; };
             auto code_rows = [&](int32_t r, int32_t id) {
                 if (id < 0 || id >= p.n_pages) {
                     if (lane == 0 && r < end) set_err(p.err, KVQ_ERR_ARG);
@@ -1061,7 +1061,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 auto request_k = [&](int g) {   // chunks 3 g ..
 #pragma unroll
                     for (int c = 3 * g; c < 3 * g + 3; ++c)
-                        k[c] = there_k ? __ldg(reinterpret_cast<const uint2*>(from_k + 32 * c)) : make_uint2(0u, 0u);
+                        k[c] = there_k ? *reinterpret_cast<const uint2*>(from_k + 32 * c) : make_uint2(0u, 0u);
                 };
                 auto request_v = [&](int t, int h) {   // rows 64 h ..
                     const int32_t r = row_v + t * kRows + kHalf * h;
@@ -1069,7 +1069,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         v[h][i] = t < steps && r + 4 * i + v_row < end
-                                      ? __ldg(reinterpret_cast<const uint4*>(a + 4 * i * kRowBytes))
+                                      ? *reinterpret_cast<const uint4*>(a + 4 * i * kRowBytes)
                                       : make_uint4(0u, 0u, 0u, 0u);
                     id_v[h] = t + 1 < steps ? page(r + kRows) : 0;
                 };
@@ -1143,8 +1143,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const int last = end - r0 - up;   // rows 2 i up to here exist
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            ctx[h][i] = 2 * i < last ? __ldg(reinterpret_cast<const uint4*>(a + 2 * i * kMlaD))
-                                                     : make_uint4(0u, 0u, 0u, 0u);
+                            ctx[h][i] = 2 * i < last ? ldg16(a + 2 * i * kMlaD) : make_uint4(0u, 0u, 0u, 0u);
                         if (t + 1 < steps) id_v[h] = page(r0 + kRows);
                     }
                 };

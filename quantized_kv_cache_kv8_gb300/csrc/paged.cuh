@@ -12,7 +12,9 @@ namespace kvq {
 // The kernels of a serving step follow one another, each a few microseconds, so each
 // is launched while the one before it runs (a launch gap less, about 1.5 us).  Every
 // kernel lets its successor come at once and, before it touches global memory, waits
-// for its predecessor to have completed, which had waited for its own.
+// for its predecessor to have completed, which had waited for its own.  What a
+// predecessor may have written it reads by ordinary loads: one through the non-coherent
+// path (__ldg) is for what nobody writes while the kernel lives.
 template <class K, class... A>
 cudaError_t launch_chained(K* kernel, dim3 grid, unsigned block, size_t smem, cudaStream_t stream, A&&... args) {
     cudaLaunchConfig_t cfg = {};
