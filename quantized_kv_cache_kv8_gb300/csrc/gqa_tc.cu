@@ -134,12 +134,18 @@ __device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volati
     return false;
 }
 
+// x 2^d, d whole and at most 0: 2^d alone may lie below f32 where the product does not (sums of weights before
+// the values' scales, under a reference that a large scale raised).
+__device__ __forceinline__ float times_2(float x, float d) {
+    const float h = truncf(0.5f * d);
+    return x * ex2(h) * ex2(d - h);
+}
+
 // A vector's reference raised for chunk j of a step (see the file's head), by a whole warp: its weights of
-// the chunks before (tm: its scores), its context (to) and its sums are brought to the new one.  Returns it
-// and the factor.
+// the chunks before (tm: its scores) and its context (to) are brought to the new one, which is returned.
 template <int D, int QP>
-__device__ __forceinline__ float2 raise(const Misc& sm, uint32_t tm, uint32_t to, int j, int st, float qs, float R, bool lift,
-                                     int32_t visible, bool context) {
+__device__ __forceinline__ float raise(const Misc& sm, uint32_t tm, uint32_t to, int j, int st, float qs, float R, bool lift,
+                                       int32_t visible, bool context) {
     uint32_t s[kC];
     tmem_ld32(tm + kC * j, s);
     tmem_wait_ld();
@@ -191,7 +197,7 @@ __device__ __forceinline__ float2 raise(const Misc& sm, uint32_t tm, uint32_t to
         }
     }
     tmem_wait_st();
-    return make_float2(n, a);
+    return n;
 }
 
 // Scores kC j .. of a step to weights; their sum before the values' scales.  PART: some are hidden from
@@ -449,7 +455,7 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                         tot[(8 * k + i) * kM] = v;
                     }
                 }
-                sm.sum_tot[tid] = lt * a + l * b;
+                sm.sum_tot[tid] = times_2(lt, Rt - n) + times_2(l, R - n);
                 sm.ref_tot[tid] = n;
                 l = 0.0f;
             };
@@ -513,9 +519,9 @@ __global__ void __launch_bounds__(kNT, (Cfg<D, QP>::kCtas)) gqa_tc_kernel(const 
                         if (QP == 1) most = sum * svt;
                         const bool lift = (R == kNone && visible > 0) || !(most <= 60000.0f) || !(sum <= 0x1p110f);
                         if (pass == 0 && __any_sync(kFull, lift)) {
-                            const float2 up = raise<D, QP>(sm, tm, tm + C::kColO, j, st, qs, R, lift, visible, context);
-                            R = up.x;
-                            l *= up.y;
+                            const float n = raise<D, QP>(sm, tm, tm + C::kColO, j, st, qs, R, lift, visible, context);
+                            l = times_2(l, R - n);
+                            R = n;
                             pass = 1;
                             continue;
                         }

@@ -195,3 +195,19 @@ def test_weights_of_a_step_whose_last_row_dwarfs_them(kvq, dtype, dim, ahead):
     sm = float(torch.tensor(math.log(2.0)))   # scores are binades
     out, _ = attend(kvq, pool, q, [256], [2], causal=False, sm=sm)
     check(out, q, pool, [256], [2], sm, False)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("gain", [1e10, 1e18, 1e25])
+def test_large_values_behind_zero_ones(kvq, dtype, dim, gain):
+    """The rows of zero values count in the softmax's sum, whatever the size of the values behind them."""
+    for new, n in ((1, 330), (20, 330), (20, 2600)):
+        for front in (16, 32, 128, n - 70):
+            pool = Pool(1, dim, 64, [n], seed=front)
+            pool.scales[..., 1] *= gain
+            blank(pool, 0, range(front))
+            lens, news = shared(pool), [new] * MANY
+            q = queries(new * MANY, 4, dim, dtype)
+            out, _ = attend(kvq, pool, q, lens, news, causal=False)
+            check_shared(out, q, pool, new, 1 / math.sqrt(dim), False, f"{front} of {n} rows, {new} tokens")
