@@ -43,6 +43,7 @@ constexpr int kMaxKeep = 64, kMaxBeams = 32;
 constexpr int kMaxLists = kNT;       // slice lists of a request
 constexpr int kMaxCand = 2048;       // their elements
 constexpr float kL = tc::kLog2e;
+constexpr float kMaxF = 3.402823466e38f;   // f32's largest
 
 struct BeamParams {
     const void* logits;
@@ -503,13 +504,13 @@ __global__ void __launch_bounds__(kNT, 4) beam_select_kernel(const __grid_consta
     for (int i = tid; i < n_cand; i += kNT) {
         const int list = i / keep, place = i - list * keep, beam = list / p.splits;
         uint64_t sc = 0ull;
-        if (place < sm.count[list] && fabsf(sm.cum[beam]) <= 3.402823466e38f) {
+        if (place < sm.count[list] && fabsf(sm.cum[beam]) <= kMaxF) {
             const float v = key_value(sm.cand[i]), top = sm.top[beam];
-            // cum + (v - top) - log mass; what lies past f32 counts as its end; nothing beside an
-            // infinite logit
-            Wide d = v == top ? Wide{0.0f, 0.0f} : two_sum(v, -top);
-            if (!(d.hi >= -3.4e38f)) d = Wide{-3.4e38f, 0.0f};
-            if (v == top || top < INFINITY) sc = ordered64(add(sm.base[beam], d));
+            // cum + (v - top) - log mass; what lies past f32 counts as its end (a mask's lowest value is
+            // that, and goes on being told apart by the rest); nothing beside an infinite logit
+            const auto end = [](Wide x) { return x.hi >= -kMaxF ? x : Wide{-kMaxF, 0.0f}; };
+            const Wide d = v == top ? Wide{0.0f, 0.0f} : end(two_sum(v, -top));
+            if (v == top || top < INFINITY) sc = ordered64(end(add(sm.base[beam], d)));
             if (place == keep - 1) floor = max(floor, sc);
         }
         sm.cand[i] = sc;   // its key is needed again by the few that stay: from global memory

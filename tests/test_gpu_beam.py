@@ -103,6 +103,30 @@ def test_masks(kvq, dtype):
         check_select(kvq, x, d, 8)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fill", ["lowest", -1e30, -1e4])
+def test_masks_of_the_lowest_value_with_few_tokens_left(kvq, dtype, fill):
+    """Masked tokens of a finite logit come once the others have: of the beam with the largest cum - lse, in order."""
+    fill = torch.finfo(dtype).min if fill == "lowest" else float(torch.tensor(fill, dtype=dtype))
+    for v, keep in ((40, 12), (1000, 16), (30011, 20)):
+        x, s = torch.full((2, 3, v), fill, dtype=dtype, device="cuda"), torch.tensor([[-3.0, -1.0, -2.0], [0.0, -9.0, 1.0]], device="cuda")
+        g = torch.Generator().manual_seed(v)
+        free = torch.tensor([5, 17])
+        x[:, :, free] = torch.randn(2, 3, 2, generator=g).to(dtype).cuda()
+        o, p, t = (a.cpu().numpy() for a in run_select(kvq, x, s, keep))
+        z = x[:, :, free].double().cpu().numpy()
+        lse = np.logaddexp(z[..., 0], z[..., 1])
+        base = s.double().cpu().numpy() - lse
+        for i in range(2):
+            order = sorted((-(base[i, b] + z[i, b, k]), b, int(free[k])) for b in range(3) for k in range(2))
+            b = int(base[i].argmax())
+            rest = [t_ for t_ in range(v) if t_ not in free.tolist()][:keep - 6]
+            assert p[i].tolist() == [3 * i + c[1] for c in order] + [3 * i + b] * (keep - 6)
+            assert t[i].tolist() == [c[2] for c in order] + rest
+            ref = np.array([-c[0] for c in order] + [fill + base[i, b]] * (keep - 6))
+            assert np.all(np.abs(o[i] - ref) <= 1e-5 + 2.0 ** -24 * np.abs(ref))   # as check_select
+
+
 def test_sizes_of_logits(kvq):
     x, s = random_logits(1, 3, 5000, torch.float32)
     for scale in (1e-20, 1e3, 1e10, 1e30, 1e38 / 12):
