@@ -531,7 +531,8 @@ kvq_status kv_attn_paged(kvq_format fmt, const kvq_mla_layout* layout, const voi
 /* One step's producer, one launch: rotates the leading rope->dim dims of every
  * query and key head (rotation and angles as kv_rope_append; there the trailing dims
  * of a latent row), encodes the rotated keys and the values and stores them.
- *   rope         NULL: no rotation (an encoder's states); dim at most head_dim
+ *   rope         NULL: no rotation (an encoder's states); dim at most head_dim, and at
+ *                most 128 (kvq_rope's 64 pairs) of 256
  *   k_new, v_new [n][n_kv_heads][head_dim] in dtype, strides in elements; both NULL:
  *                only queries
  *   positions    [n_axes][n] int64, axis stride pos_stride; unused without rope
@@ -570,10 +571,11 @@ size_t kv_gqa_attn_paged_workspace_size(kvq_dtype q_dtype, int32_t n_seq, int32_
  *                behind cu_q[n_seq] are left as they are
  *   kv_lens      [n_seq] int64, at most min(table_stride, n_pages) * page_rows
  * Products take 16-bit operands, sums are f32: outputs are within 1e-5 of a vector's largest
- * before the rounding to q_dtype, but for what f32 scores of some hundreds lose and, where a
- * sequence brings more than 24 query vectors to a kv head on average and queries are bf16 (tensor
- * cores), a rounding of each row's weight to f16 (2^-11 of it).  A row with a NaN code, or a scale that
- * is no finite number, makes NaN the tokens that see it and leaves the others as they are.  Invalid
+ * before the rounding to q_dtype, but for what f32 loses in large scores (3e-5 at scores of 100) and,
+ * where a sequence brings more than 24 query vectors to a kv head on average and queries are bf16
+ * (tensor cores), a rounding of each row's weight to f16 (2^-11 of it).  That holds for rows of values
+ * whose largest is 0 or lies between 1e-25 and 1e25.  A row with a NaN code, or a scale that is no
+ * finite number, makes NaN the tokens that see it and leaves the others as they are.  Invalid
  * lengths or offsets and pages outside [0, n_pages) set KVQ_ERR_ARG in the workspace's
  * device word; nothing outside the pool is read.  q, out, pools and workspace are 16-byte
  * aligned.  The workspace starts zeroed; calls leave it ready for the next. */
@@ -606,7 +608,8 @@ size_t kv_beam_workspace_size(int32_t n_seq, int32_t n_beams, int64_t vocab, int
  * lower token.
  *   logits      [n_seq * n_beams][vocab] f32 or bf16, rows row_stride elements apart.  A
  *               logit of -inf, or NaN, is a token that may not come; the mass of a row with
- *               infinite logits is shared among those
+ *               infinite logits is shared among those.  (A mask of -inf costs nothing; with
+ *               the type's lowest value in most places a row is read `keep` times)
  *   scores      [n_seq][n_beams] f32; a beam whose score is not finite has no continuation
  *   out_scores  [n_seq][keep] f32
  *   parents     [n_seq][keep] int32: s * n_beams + b

@@ -20,7 +20,7 @@
 // A warp takes 16 rows at a time (a page holds at least 16, so they have one page
 // entry) and keeps its own running maximum, sum and context; the 4 warps of a CTA
 // take turns over the rows and are joined at the tile's end.  32 bf16 sequences of 1k to 65k rows,
-// 8 kv heads of 128: 437 us, 5.6 TB/s; 4 of 32768 rows, 2 of 256: 40 us in a row of calls, of which
+// 8 kv heads of 128: 424 us, 5.8 TB/s; 4 of 32768 rows, 2 of 256: 40 us in a row of calls, of which
 // 25 are the rows and the rest the walk's start (4,500 cycles), the first loads and the join;
 // one of 300 rows 9.7 us, latencies alone.  With vectors on the 16 side of the product, half of
 // it empty at 8 vectors, a step took 750 instructions a warp at D = 256 and 255 registers.
@@ -31,7 +31,8 @@
 // passes it by 2^8.  A context weight is w = p s_v f, p = 2^(z - m), with f per vector so
 // that the largest w so far lies in [2^14, 2^16), and goes in two f16 halves: to 2^-22
 // of itself or 2^-25 absolute, 2^-39 of the largest, whatever the spread of scales and scores; a million
-// such roundings add up to 2^-19.  The products' f32 accumulators lose up to
+// such roundings add up to 2^-19.  (f is at most 2^100, also while only rows of zero values have weighed:
+// it serves value scales from some 2^-86 on.)  The products' f32 accumulators lose up to
 // 2^-23 a step towards zero, so every 32 steps they are added to totals in shared
 // memory, and sums of p likewise.
 //

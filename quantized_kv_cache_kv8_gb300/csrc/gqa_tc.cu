@@ -9,7 +9,7 @@
 // one tile can't overlap with itself: tensor memory holds two tiles' scores and contexts and no more.
 // So two CTAs share an SM, one's softmax beside the other's products, and the weights go
 // into the second product from tensor memory, over the scores they came from, instead of
-// through shared memory.  512 bf16 tokens of 32 heads (8 of keys) of 128 on 8704 rows: 117 us, 606
+// through shared memory.  512 bf16 tokens of 32 heads (8 of keys) of 128 on 8704 rows: 116 us, 611
 // TFLOP/s; at 133 us the tensor pipe was 24% busy, shared memory 43%, issue slots 33%.
 // A step takes one CTA some 6,200 cycles: 3,200 the softmax, 2,400 the products (issuing, waiting for the
 // weights' product and for the scores).  Slower (of 133 us then): scores of 64 rows in two buffers (157);
@@ -28,8 +28,9 @@
 //     spilled, and one of the converters' was missed there: 155 us).
 //
 // Numbers.  Queries as in gqa_attn.cu (bf16 exactly, f32 in two f16 halves).  R is an
-// integer per vector, max(z + log2 s_v) - 8 when it is set (f32 queries: 12); it rises
-// when a weight passes 60000, and then what has been summed is brought to it by a power of two.  bf16
+// integer per vector, max(z + log2 s_v) - 8 when it is set (f32 queries: 12), and at least max(z) - 100,
+// which rows of zero values leave it at; it rises when a weight passes 60000, and then what has been
+// summed is brought to it by a power of two.  bf16
 // queries: weights in one f16 (2^-11 of themselves, down to 2^-22 of the largest).
 // f32 queries: in two (2^-22); products of the small halves come first, since each rounds the sum
 // so far.  Every 256 steps (f32 queries: 8) the accumulators, which round
