@@ -571,14 +571,15 @@ size_t kv_gqa_attn_paged_workspace_size(kvq_dtype q_dtype, int32_t n_seq, int32_
  *                behind cu_q[n_seq] are left as they are
  *   kv_lens      [n_seq] int64, at most min(table_stride, n_pages) * page_rows
  * Products take 16-bit operands, sums are f32: outputs are within 1e-5 of a vector's largest
- * before the rounding to q_dtype, but for what f32 loses in large scores (3e-5 at scores of 100) and,
- * where a sequence brings more than 24 query vectors to a kv head on average and queries are bf16
- * (tensor cores), a rounding of each row's weight to f16 (2^-11 of it).  That holds for rows of values
+ * before the rounding to q_dtype, but for what f32 loses in large scores (some 3e-5 from scores of 40
+ * on) and, where a sequence brings more than 24 query vectors to a kv head on average and queries
+ * are bf16 (tensor cores), a rounding of each row's weight to f16 (2^-11 of it).  That holds for rows of values
  * whose largest is 0 or lies between 1e-25 and 1e25.  A row with a NaN code, or a scale that is no
- * finite number, makes NaN the tokens that see it and leaves the others as they are.  Invalid
- * lengths or offsets and pages outside [0, n_pages) set KVQ_ERR_ARG in the workspace's
- * device word; nothing outside the pool is read.  q, out, pools and workspace are 16-byte
- * aligned.  The workspace starts zeroed; calls leave it ready for the next. */
+ * finite number, makes NaN the tokens that see it and leaves the others as they are; a query vector
+ * with a NaN or an infinity yields NaN where it sees a row.  Invalid lengths or offsets and pages outside
+ * [0, n_pages) set KVQ_ERR_ARG in the workspace's device word; nothing outside the pool is read.
+ * q, out, pools and workspace are 16-byte aligned.  The workspace starts zeroed; calls leave it ready
+ * for the next. */
 kvq_status kv_gqa_attn_paged(const void* q, kvq_dtype q_dtype, int64_t n_tokens, int32_t n_heads, int32_t n_kv_heads,
                              int32_t head_dim, int32_t n_seq, const int64_t* cu_q, const uint8_t* k_codes,
                              const uint8_t* v_codes, const float* scales, const int32_t* block_table,

@@ -40,7 +40,6 @@
 // see it and no other: in steps that some vector sees only in part, values' NaN codes
 // are replaced and flagged, and hidden weights are set to zero rather than multiplied.
 #include "gqa_common.cuh"
-#include "tc_common.cuh"
 
 #include <algorithm>
 
@@ -48,7 +47,6 @@ namespace kvq {
 namespace {
 
 using tc::ex2;
-using tc::kLog2e;
 
 constexpr int kNT = 128, kWarps = kNT / 32, kN = 16 * kWarps;
 constexpr int kFlush = 32;          // steps between additions to the totals
@@ -164,7 +162,7 @@ __device__ __forceinline__ void load_queries(const GqaParams& p, const GqaSegmen
     for (int o = kT / 2; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
     const int e = max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -110);
     const float up = __uint_as_float((uint32_t)(127 - e) << 23);
-    if (t == 0) sm.qs[r] = p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 + e) << 23);
+    if (t == 0) sm.qs[r] = query_scale(p.sm_scale, e, amax);
 #pragma unroll
     for (int i = 0; i < E; i += 2) {
         // word (d % 4) / 2 of product s = 4 (d / 64) + (d % 16) / 4, lane (r % 8, (d % 64) / 16)

@@ -22,6 +22,7 @@
 
 #include "gqa.cuh"
 #include "paged_common.cuh"
+#include "tc_common.cuh"
 
 namespace kvq {
 
@@ -319,6 +320,12 @@ __device__ __forceinline__ int32_t gqa_page(const GqaParams& p, int32_t b, int32
 // A key's scale as its scores take it: NaN for an infinite one (0 times it is NaN), whose row a negative
 // product would hide.
 __device__ __forceinline__ float key_scale(float s) { return __fmaf_rn(s, 0.0f, s); }
+
+// What the scores of a vector held as 2^-e of itself are multiplied by: binades.  NaN for a vector with an infinity,
+// whose scores of -inf would hide rows.
+__device__ __forceinline__ float query_scale(float sm_scale, int e, float amax) {
+    return sm_scale * tc::kLog2e * __uint_as_float((uint32_t)(127 + e) << 23) * __fmaf_rn(amax, 0.0f, 1.0f);
+}
 
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);

@@ -36,7 +36,6 @@
 // so far.  Every 256 steps (f32 queries: 8) the accumulators, which round
 // towards zero, go to totals in the workspace.  Rows that are no numbers as in gqa_attn.cu.
 #include "gqa_common.cuh"
-#include "tc_common.cuh"
 
 #include <algorithm>
 
@@ -331,7 +330,7 @@ __device__ __forceinline__ void load_queries(const GqaParams& p, const GqaSegmen
         for (int o = kLanes / 2; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
         const int e = max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -110);
         const float up = __uint_as_float((uint32_t)(127 - e) << 23);
-        if (d == 0) sm.qs[r] = p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 + e) << 23);
+        if (d == 0) sm.qs[r] = query_scale(p.sm_scale, e, amax);
         uint32_t hi[V / 2], lo[V / 2];
 #pragma unroll
         for (int k = 0; k < V / 2; ++k) {

@@ -211,3 +211,21 @@ def test_large_values_behind_zero_ones(kvq, dtype, dim, gain):
             q = queries(new * MANY, 4, dim, dtype)
             out, _ = attend(kvq, pool, q, lens, news, causal=False)
             check_shared(out, q, pool, new, 1 / math.sqrt(dim), False, f"{front} of {n} rows, {new} tokens")
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 40])
+def test_queries_that_are_no_numbers(kvq, dtype, dim, new):
+    """Every dim of their outputs is NaN, on one row too, whose score may be -inf; zeros where no row is seen."""
+    lens, news = [1, 3, 0, 200], [new] * 4
+    pool = Pool(2, dim, 16, lens, seed=1)
+    q = queries(4 * new, 8, dim, dtype)
+    ref = attention(q, pool, lens, news, 0.1, False)
+    mass = attention(q, pool, lens, news, 0.1, False, absolute=True) if new * 4 > 24 and dtype == torch.bfloat16 else None
+    q[:, 1, 5], q[:, 2, 5], q[:, 6, 40] = math.inf, -math.inf, math.nan
+    out, _ = attend(kvq, pool, q, lens, news, False, sm=0.1)
+    rest = [0, 3, 4, 5, 7]
+    some = torch.tensor([n > 0 for n in lens for _ in range(new)], device="cuda")
+    assert bool(torch.isnan(out[some][:, [1, 2, 6]]).all()) and bool((out[~some] == 0).all())
+    close(out[:, rest], ref[:, rest], "the other heads", None if mass is None else mass[:, rest])
