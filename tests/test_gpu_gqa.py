@@ -698,3 +698,25 @@ def test_calls_side_by_side(kvq):
     for i, (pool, q, cu, out, ws, st) in enumerate(jobs):
         check(out, q, pool, [6000 + i], [len(q)], 0.1, True, f"job {i}")
         assert kvq.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("page", [1024, 65536])
+def test_large_pages(kvq, page):
+    """Rows appended into pages larger than a tile's steps and attended; the second sequence's page is partly filled."""
+    kv, dim, lens, new = 2, 64, [page + 3, 100], [70, 1]
+    for dtype in DT:
+        pool = Pool(kv, dim, page, lens, seed=2)
+        t = torch.cat([torch.arange(n - m, n, device="cuda") for n, m in zip(lens, new)])
+        b = torch.repeat_interleave(torch.arange(2, device="cuda"), torch.tensor(new, device="cuda"))
+        slots = pool.table[b, t // page].long() * page + t % page
+        k, v = queries(71, kv, dim, dtype, seed=3), queries(71, kv, dim, dtype, seed=4)
+        kvq.kv_gqa_append(None, k, v, None, slots, None, None, pool.k, pool.v, pool.scales)
+        (kc, ks), (vc, vs) = encode_rows(k.float()), encode_rows(v.float())
+        pg, at = slots // page, slots % page
+        assert torch.equal(pool.k[pg, :, at], kc) and torch.equal(pool.v[pg, :, at], vc)
+        assert torch.allclose(pool.scales[pg, :, at], torch.stack([ks, vs], -1), rtol=2.0 ** -23, atol=0.0)
+        q = queries(71, 8, dim, dtype)
+        for causal in (True, False):
+            out, ws = attend(kvq, pool, q, lens, new, causal)
+            check(out, q, pool, lens, new, 1 / math.sqrt(dim), causal, f"{dtype} {causal}")
+            assert kvq.read_device_error(ws) == 0

@@ -88,3 +88,12 @@ def test_fork_and_copy_refusals(kvq):
     assert copy(1, D, 4, 1, C.byref(pool), None, None) == 1
     assert copy(-1, D, 4, 1, C.byref(pool), None, None) == 1 and copy(1, None, 4, 1, C.byref(pool), None, None) == 1
     assert copy(0, D, 4, 1, C.byref(pool), None, None) == 0
+
+
+def test_wide_heads_turn_128_dims_at_most(kvq):
+    rope = kvq.rope_layout([1.0] * 64)
+    assert append(kvq, rope, dim=256, n=0) == 0
+    rope.dim = 130
+    assert append(kvq, rope, dim=256, n=0) == 5
+    with pytest.raises(ValueError):
+        kvq.rope_layout([1.0] * 65)
